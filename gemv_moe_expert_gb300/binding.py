@@ -35,6 +35,8 @@ ACT_SPLIT, ACT_BF16 = 0, 1
 IDS_DISTINCT_PER_TOKEN, IDS_MAY_REPEAT = 0, 1
 ROUTE_DIRECT, ROUTE_GROUPED_PREFILL = 0, 1
 MATMUL_ID_SCHEMA_VERSION = 3
+SOFTMAX_ALL, SOFTMAX_SELECTED = 0, 1
+MOE_MAX_TOP_K = 32
 GROUPED_MAX_EXPERTS = 1024
 
 # every symbol include/gbmm.h declares
@@ -44,6 +46,9 @@ EXPORTS = (
     "gbmm_device_error", "gbmm_test_inject_kernel_failure", "gbmm_test_launch_count",
     "gbmm_test_reset_launch_count", "gbmm_test_last_kernel", "gbmm_test_bounded_wait",
     "gbmm_matmul_id_static_scratch", "gbmm_test_static_scratch_copy",
+    "gbmm_moe_route", "gbmm_moe_route_backward", "gbmm_moe_sort_scratch_bytes", "gbmm_moe_sort",
+    "gbmm_moe_dispatch", "gbmm_moe_dispatch_backward", "gbmm_moe_combine",
+    "gbmm_moe_combine_backward", "gbmm_gemv_q4", "gbmm_matmul_id_q4",
 )
 
 # n_experts * m * 4 bytes of routed rows fit the fixed scratch of
@@ -136,6 +141,24 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.gbmm_matmul_id_static_scratch.restype = i32
         lib.gbmm_test_static_scratch_copy.argtypes = [vp, u64, vp]
         lib.gbmm_test_static_scratch_copy.restype = i32
+        rows_args = [i32, u32, u32, u32, i64]
+        for name, args in (
+                ("gbmm_moe_route", [i32, u32, u32, u32, u32, vp, i64, vp, vp, vp, vp]),
+                ("gbmm_moe_route_backward",
+                 [i32, u32, u32, u32, u32, vp, i64, vp, vp, vp, vp, vp, i64, vp]),
+                ("gbmm_moe_sort_scratch_bytes", [u32, u32, u32, ctypes.POINTER(u64)]),
+                ("gbmm_moe_sort", [u32, u32, u32, vp, vp, vp, vp, vp, u64, vp]),
+                ("gbmm_moe_dispatch", [*rows_args, vp, i64, vp, vp, vp, i64, vp]),
+                ("gbmm_moe_dispatch_backward", [*rows_args, vp, i64, vp, vp, vp, i64, vp]),
+                ("gbmm_moe_combine", [*rows_args, vp, i64, vp, vp, vp, vp, i64, vp]),
+                ("gbmm_moe_combine_backward",
+                 [*rows_args, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp]),
+                ("gbmm_gemv_q4",
+                 [i32, u32, i64, i64, u32, vp, i64, vp, i32, vp, vp, i64, vp, i64, vp]),
+                ("gbmm_matmul_id_q4",
+                 [i32, u32, i64, i64, u32, u32, u32, u32, vp, i64, i64, vp, i32, vp, vp, vp, vp, vp])):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = i32
         _lib = lib
         return lib
 
@@ -242,6 +265,77 @@ def gbmm_matmul_id_static_scratch(params: MatmulIdParams, weight_dtype, weights,
                                               input_bytes, _ptr(ids), ids_bytes, _ptr(out),
                                               out_bytes, _stream(stream), ctypes.byref(rec))
     return st, rec
+
+
+def gbmm_moe_route(dtype, m, n_experts, top_k, softmax, logits, ld_logits, select_bias, ids,
+                   weights, stream=None) -> int:
+    return load().gbmm_moe_route(_dt(dtype), m, n_experts, top_k, softmax, _ptr(logits), ld_logits,
+                                 _ptr(select_bias), _ptr(ids), _ptr(weights), _stream(stream))
+
+
+def gbmm_moe_route_backward(dtype, m, n_experts, top_k, softmax, logits, ld_logits, select_bias,
+                            ids, weights, d_weights, d_logits, ld_d_logits, stream=None) -> int:
+    return load().gbmm_moe_route_backward(_dt(dtype), m, n_experts, top_k, softmax, _ptr(logits),
+                                          ld_logits, _ptr(select_bias), _ptr(ids), _ptr(weights),
+                                          _ptr(d_weights), _ptr(d_logits), ld_d_logits,
+                                          _stream(stream))
+
+
+def gbmm_moe_sort_scratch_bytes(m: int, top_k: int, n_experts: int):
+    """Returns (status, bytes)."""
+    b = ctypes.c_uint64(0)
+    st = load().gbmm_moe_sort_scratch_bytes(m, top_k, n_experts, ctypes.byref(b))
+    return st, b.value
+
+
+def gbmm_moe_sort(m, top_k, n_experts, ids, offsets, order, position, scratch, scratch_bytes,
+                  stream=None) -> int:
+    return load().gbmm_moe_sort(m, top_k, n_experts, _ptr(ids), _ptr(offsets), _ptr(order),
+                                _ptr(position), _ptr(scratch), scratch_bytes, _stream(stream))
+
+
+def gbmm_moe_dispatch(dtype, m, top_k, n_experts, n, x, ldx, position, offsets, xs, ldxs,
+                      stream=None) -> int:
+    return load().gbmm_moe_dispatch(_dt(dtype), m, top_k, n_experts, n, _ptr(x), ldx,
+                                    _ptr(position), _ptr(offsets), _ptr(xs), ldxs, _stream(stream))
+
+
+def gbmm_moe_dispatch_backward(dtype, m, top_k, n_experts, n, d_xs, ld_dxs, position, offsets, d_x,
+                               ld_dx, stream=None) -> int:
+    return load().gbmm_moe_dispatch_backward(_dt(dtype), m, top_k, n_experts, n, _ptr(d_xs), ld_dxs,
+                                             _ptr(position), _ptr(offsets), _ptr(d_x), ld_dx,
+                                             _stream(stream))
+
+
+def gbmm_moe_combine(dtype, m, top_k, n_experts, n, ys, ldys, weights, position, offsets, y, ldy,
+                     stream=None) -> int:
+    return load().gbmm_moe_combine(_dt(dtype), m, top_k, n_experts, n, _ptr(ys), ldys,
+                                   _ptr(weights), _ptr(position), _ptr(offsets), _ptr(y), ldy,
+                                   _stream(stream))
+
+
+def gbmm_moe_combine_backward(dtype, m, top_k, n_experts, n, ys, ldys, weights, position, offsets,
+                              d_y, ld_dy, d_ys, ld_dys, d_weights, stream=None) -> int:
+    return load().gbmm_moe_combine_backward(_dt(dtype), m, top_k, n_experts, n, _ptr(ys), ldys,
+                                            _ptr(weights), _ptr(position), _ptr(offsets),
+                                            _ptr(d_y), ld_dy, _ptr(d_ys), ld_dys, _ptr(d_weights),
+                                            _stream(stream))
+
+
+def gbmm_gemv_q4(dtype, m, n, k, group, q, ldq_bytes, scales, scale_dtype, zeros, x, ldx, y, ldy,
+                 stream=None) -> int:
+    return load().gbmm_gemv_q4(_dt(dtype), m, n, k, group, _ptr(q), ldq_bytes, _ptr(scales),
+                               _dt(scale_dtype), _ptr(zeros), _ptr(x), ldx, _ptr(y), ldy,
+                               _stream(stream))
+
+
+def gbmm_matmul_id_q4(dtype, m, n, k, top_k, n_experts, input_layout, group, q, ldq_bytes,
+                      expert_stride_bytes, scales, scale_dtype, zeros, x, ids, out,
+                      stream=None) -> int:
+    return load().gbmm_matmul_id_q4(_dt(dtype), m, n, k, top_k, n_experts, input_layout, group,
+                                    _ptr(q), ldq_bytes, expert_stride_bytes, _ptr(scales),
+                                    _dt(scale_dtype), _ptr(zeros), _ptr(x), _ptr(ids), _ptr(out),
+                                    _stream(stream))
 
 
 def gbmm_last_error() -> str:

@@ -19,6 +19,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/gbmm.h"
+#include "api_internal.h"
 #include "kernel_params.h"
 
 using namespace gbmm;
@@ -503,11 +504,14 @@ Range range_of(const void *p, uint64_t bytes) {
 }  // namespace
 
 namespace gbmm {
-// Lets other translation units of the library set gbmm_last_error().
+// Let other translation units of the library set gbmm_last_error(), ask for a
+// kernel and account for a launch as the entry points here do (api_internal.h).
 int record_error(int status, const char *message) {
     t_last_error = message ? message : "";
     return status;
 }
+bool resolve_kernel(const char *name) { return resolve(name); }
+gbmm_status finish_launch(cudaError_t e, const char *name, cudaStream_t s) { return after_launch(e, name, s); }
 }  // namespace gbmm
 
 extern "C" {

@@ -106,6 +106,64 @@ struct GemvTcParams {
     uint64_t wait_limit_ns;
 };
 
+// Top-k softmax router (moe_route.cu).  logits [m, n_experts], rows
+// ld_logits elements apart; ids, weights, d_weights [m, top_k] tight.
+struct MoeRouteParams {
+    const void *logits;
+    const float *bias;       // added for the selection only; may be null
+    uint32_t *ids;           // written forward, read backward
+    float *weights;          // written forward, read backward
+    const float *d_weights;  // backward
+    void *d_logits;          // backward
+    int64_t ld_logits, ld_d_logits;
+    uint32_t m, n_experts, top_k;
+    int32_t selected;        // softmax over the chosen experts (1) or over every live one (0)
+};
+
+// Stable sort of routed rows by expert (moe_sort.cu).
+struct MoeSortParams {
+    const uint32_t *ids;  // [rows]
+    uint32_t *offsets;    // [n_experts + 1]
+    uint32_t *order;      // [rows]
+    uint32_t *position;   // [rows]
+    uint32_t *scratch;    // moe_sort_scratch_words() words
+    uint32_t rows, n_experts;
+};
+
+// Rows of n elements in token order (tok, m rows) and in expert order (row,
+// m * top_k rows); moe_rows.cu.  position / offsets null: routed row r is row r.
+struct MoeRowsParams {
+    const void *tok_in;    // dispatch: x; combine backward: d_y
+    void *tok_out;         // combine: y; dispatch backward: d_x
+    const void *row_in;    // combine, its backward: ys; dispatch backward: d_xs
+    void *row_out;         // dispatch: xs; combine backward: d_ys
+    const float *weights;  // [m, top_k]; null = 1 (dispatch backward)
+    float *d_weights;      // combine backward
+    const uint32_t *position;
+    const uint32_t *valid;  // offsets + n_experts: rows that have an expert
+    int64_t ld_tok_in, ld_tok_out, ld_row_in, ld_row_out;
+    int64_t n;
+    uint32_t m, top_k;
+};
+
+// Matrix-vector products with 4-bit weights (q4.cu), dense (ids null: every
+// row of x through the one matrix) or per expert id (routed row r through
+// matrix ids[r]).
+struct Q4Params {
+    const uint8_t *q;
+    const void *scales;
+    const uint8_t *zeros;  // null: 8
+    const void *x;
+    void *out;
+    const uint32_t *ids;
+    int64_t ldq, expert_stride;  // bytes
+    int64_t ldx, x_slot_stride;  // elements; x row of routed row r: (r / top_k) ldx + (r % top_k) x_slot_stride
+    int64_t ldo;
+    int64_t n, k, groups;        // groups = ceil(k / group)
+    int32_t group, scale_dtype;
+    uint32_t rows, top_k, n_experts;
+};
+
 // ---- launchers (each returns the launch's cudaError_t) --------------------
 
 cudaError_t launch_fill_zero(int dt, void *c, int64_t batch, int64_t m, int64_t n, int64_t ldc,
@@ -158,6 +216,16 @@ int direct_tc_max_experts();
 int direct_tc_block_rows();
 int direct_tc_block_k();
 int grouped_tc_block_k();
+
+cudaError_t launch_moe_route(int dt, const MoeRouteParams &p, cudaStream_t s);
+cudaError_t launch_moe_route_backward(int dt, const MoeRouteParams &p, cudaStream_t s);
+uint64_t moe_sort_scratch_words(uint64_t rows, uint32_t n_experts);
+int moe_sort_launches(uint64_t rows, uint32_t n_experts);
+cudaError_t launch_moe_sort(int step, const MoeSortParams &p, cudaStream_t s);
+cudaError_t launch_moe_dispatch(int dt, const MoeRowsParams &p, cudaStream_t s);
+cudaError_t launch_moe_combine(int dt, const MoeRowsParams &p, cudaStream_t s);
+cudaError_t launch_moe_combine_backward(int dt, const MoeRowsParams &p, cudaStream_t s);
+cudaError_t launch_q4(int dt, const Q4Params &p, cudaStream_t s);
 
 int gemm_tc_block_m();
 int gemm_tc_wide_block_m();

@@ -1,6 +1,7 @@
 /*
  * gbmm.h -- C ABI of the GB300 (sm_103a) dense GEMM / GEMV / expert-ID matmul
- * library (libgbmm.so).
+ * library (libgbmm.so), with the router, token order and gradients of a
+ * mixture-of-experts layer and 4-bit matrix-vector products.
  *
  * Conventions shared by every entry point
  *   - Pointers named a, b, c, weights, input, ids, out, expert_counts and
@@ -350,6 +351,163 @@ GBMM_API gbmm_status gbmm_matmul_id_static_scratch(const gbmm_matmul_id_params *
                                                    gbmm_matmul_id_receipt *receipt);
 
 /* ------------------------------------------------------------------------ */
+/* Mixture-of-experts layer: router, expert order, combine                     */
+/* ------------------------------------------------------------------------ */
+/*
+ * What surrounds the expert products, with the gradients that training needs.
+ * (The pages have no counterpart: their callers bring ids.)  Shared rules:
+ *   - m tokens, top_k expert slots per token; routed row r = t*top_k + s, as in
+ *     gbmm_matmul_id.  An id >= n_experts means "no expert"; all of these calls
+ *     and gbmm_matmul_id agree on that.  m * top_k < 2^31; n_experts <=
+ *     GBMM_GROUPED_MAX_EXPERTS.
+ *   - ids, weights and d_weights are tight [m, top_k] (u32 and f32).  Other
+ *     matrices have rows ld* elements apart (ld* >= their row length).
+ *   - dt (f32, f16, bf16) is the type of the logits, or of every matrix of rows
+ *     in the call.  All arithmetic is f32, sums run in a fixed order (results do
+ *     not change from call to call), and each output is rounded once.
+ *   - Pointers must be aligned to their elements, outputs must not overlap
+ *     inputs or each other (GBMM_ERR_OVERLAP), and m == 0 is a no-op (except
+ *     that gbmm_moe_sort writes its offsets).  No call allocates or synchronises.
+ */
+
+enum { GBMM_SOFTMAX_ALL = 0, GBMM_SOFTMAX_SELECTED = 1 };
+/* Most expert slots per token of the router. */
+#define GBMM_MOE_MAX_TOP_K 32u
+
+/*
+ * gbmm_moe_route -- top-k softmax gate over logits [m, n_experts].
+ *
+ * score[t,e] = logit[t,e], plus select_bias[e] rounded to f32 when select_bias
+ *   (f32 [n_experts]) is not NULL.  An expert is live for a token when its
+ *   score is greater than -inf (so a logit or bias of -inf or NaN masks it).
+ * ids[t,:] = the live experts of largest score, in descending order, the lowest
+ *   index first among equals.  If fewer than top_k are live the remaining slots
+ *   get id n_experts and weight 0; every slot of a row without a live expert does.
+ * weights[t,s], with e = ids[t,s] and l the logits (without the bias):
+ *   GBMM_SOFTMAX_ALL       exp(l_e) / sum of exp(l) over the live experts
+ *   GBMM_SOFTMAX_SELECTED  exp(l_e) / sum of exp(l) over the chosen experts
+ *   computed with the maximum subtracted.  A live logit of +inf gives NaN weights.
+ * n_experts >= 1, 1 <= top_k <= min(n_experts, GBMM_MOE_MAX_TOP_K).
+ */
+GBMM_API gbmm_status gbmm_moe_route(gbmm_dtype dt, uint32_t m, uint32_t n_experts, uint32_t top_k,
+                                    uint32_t softmax, const void *logits, int64_t ld_logits,
+                                    const float *select_bias, uint32_t *ids, float *weights,
+                                    gbmm_stream stream);
+
+/*
+ * gbmm_moe_route_backward -- d_logits [m, n_experts] from d_weights, given the
+ * forward call's arguments and its ids and weights (w):
+ *   GBMM_SOFTMAX_ALL       d_l[e] = p[e] * (g[e] - c) for live e, p the softmax
+ *     over the live experts, g[e] = d_weights[s] where ids[s] == e, else 0
+ *   GBMM_SOFTMAX_SELECTED  d_l[ids[s]] = w[s] * (d_weights[s] - c)
+ *   with c = sum_s w[s] * d_weights[s] over the slots that have an expert; every
+ *   other entry 0.  The selection itself has no gradient.
+ * GBMM_SOFTMAX_SELECTED reads neither logits nor select_bias (both may be NULL).
+ * ids must be distinct within a token (those of gbmm_moe_route are) or n_experts.
+ */
+GBMM_API gbmm_status gbmm_moe_route_backward(gbmm_dtype dt, uint32_t m, uint32_t n_experts, uint32_t top_k,
+                                             uint32_t softmax, const void *logits, int64_t ld_logits,
+                                             const float *select_bias, const uint32_t *ids,
+                                             const float *weights, const float *d_weights, void *d_logits,
+                                             int64_t ld_d_logits, gbmm_stream stream);
+
+/* gbmm_moe_sort_scratch_bytes -- bytes of scratch that gbmm_moe_sort needs for
+ * these sizes (0 is possible); grows with m.  Host-only. */
+GBMM_API gbmm_status gbmm_moe_sort_scratch_bytes(uint32_t m, uint32_t top_k, uint32_t n_experts,
+                                                 uint64_t *bytes);
+
+/*
+ * gbmm_moe_sort -- stable order of the routed rows by expert.
+ *   position[r]  the place of routed row r: rows of expert 0 first, in increasing
+ *                r, then those of expert 1, ..., last the rows without an expert
+ *   order[p]     the routed row at place p (order[position[r]] == r)
+ *   offsets[e]   the first place of expert e; offsets[n_experts] (n_experts + 1
+ *                entries) = the number of rows that have an expert
+ * ids may repeat within a token.  scratch (4-byte aligned; NULL when 0 bytes are
+ * needed) of at least gbmm_moe_sort_scratch_bytes(), else GBMM_ERR_SCRATCH; its
+ * contents need no preparation, and calls in flight must not share it.
+ */
+GBMM_API gbmm_status gbmm_moe_sort(uint32_t m, uint32_t top_k, uint32_t n_experts, const uint32_t *ids,
+                                   uint32_t *offsets, uint32_t *order, uint32_t *position, void *scratch,
+                                   uint64_t scratch_bytes, gbmm_stream stream);
+
+/*
+ * Rows to expert order and back.  position and offsets are gbmm_moe_sort's; with
+ * both NULL the rows stay in routed order and all count as having an expert
+ * (the layout that gbmm_matmul_id writes).  "has an expert": position[r] <
+ * offsets[n_experts].  Rows of m tokens (x, y and their gradients, [m, n]) and of
+ * m * top_k places (xs, ys and their gradients, [m * top_k, n]).
+ *
+ * gbmm_moe_dispatch            xs[position[r]] = x[t]; zeros where r has no expert
+ * gbmm_moe_dispatch_backward   d_x[t] = sum over s of d_xs[position[r]]
+ * gbmm_moe_combine             y[t] = sum over s of weights[r] * ys[position[r]]
+ * gbmm_moe_combine_backward    d_ys[position[r]] = weights[r] * d_y[t],
+ *                              d_weights[r] = <d_y[t], ys[position[r]]>; both zero
+ *                              where r has no expert
+ * The sums run over the slots that have an expert (rows of xs or ys without one
+ * are not read), in increasing s.  n == 0 is a no-op, except that
+ * gbmm_moe_combine_backward then writes zeros to d_weights.
+ */
+GBMM_API gbmm_status gbmm_moe_dispatch(gbmm_dtype dt, uint32_t m, uint32_t top_k, uint32_t n_experts,
+                                       int64_t n, const void *x, int64_t ldx, const uint32_t *position,
+                                       const uint32_t *offsets, void *xs, int64_t ldxs, gbmm_stream stream);
+GBMM_API gbmm_status gbmm_moe_dispatch_backward(gbmm_dtype dt, uint32_t m, uint32_t top_k,
+                                                uint32_t n_experts, int64_t n, const void *d_xs,
+                                                int64_t ld_dxs, const uint32_t *position,
+                                                const uint32_t *offsets, void *d_x, int64_t ld_dx,
+                                                gbmm_stream stream);
+GBMM_API gbmm_status gbmm_moe_combine(gbmm_dtype dt, uint32_t m, uint32_t top_k, uint32_t n_experts,
+                                      int64_t n, const void *ys, int64_t ldys, const float *weights,
+                                      const uint32_t *position, const uint32_t *offsets, void *y,
+                                      int64_t ldy, gbmm_stream stream);
+GBMM_API gbmm_status gbmm_moe_combine_backward(gbmm_dtype dt, uint32_t m, uint32_t top_k,
+                                               uint32_t n_experts, int64_t n, const void *ys, int64_t ldys,
+                                               const float *weights, const uint32_t *position,
+                                               const uint32_t *offsets, const void *d_y, int64_t ld_dy,
+                                               void *d_ys, int64_t ld_dys, float *d_weights,
+                                               gbmm_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* Matrix-vector products with 4-bit weights                                  */
+/* ------------------------------------------------------------------------ */
+/*
+ * The decode counterpart of gbmm_gemm (few rows, transpose_b) and of
+ * gbmm_matmul_id's Direct route for weights of 4 bits.
+ *   W[j,x] = (q[j,x] - z[j,g]) * scale[j,g],  g = x / group,  j < n, x < k
+ * q: row j starts at byte j*ldq_bytes; byte i of a row holds column 2i in its low
+ *   and column 2i+1 in its high four bits (ldq_bytes >= (k+1)/2; the unused half
+ *   of the last byte of an odd k is ignored).  Rows 16 bytes apart in a 16-byte
+ *   aligned matrix are read fastest; every other alignment works.
+ * group: 32, 64 or 128 columns; the last one may be ragged.  G = ceil(k/group).
+ * scales: [n, G] tight, scale_dt f32, f16 or bf16.  zeros: u8 [n, G] tight, values
+ *   0..255, or NULL for 8 everywhere.
+ * Every weight value enters the product exactly, x in its own precision (f32
+ * included); products accumulate in f32, and each result is rounded once.
+ */
+
+/* gbmm_gemv_q4 -- y[i,j] = sum_x x[i,x] * W[j,x] for i < m.  x [m, k] and y
+ * [m, n] of type dt, rows ldx / ldy elements apart.  Any m: the weights are read
+ * once for each block of up to 8 rows, so it is meant for few of them.  m or
+ * n == 0 is a no-op, k == 0 writes zeros. */
+GBMM_API gbmm_status gbmm_gemv_q4(gbmm_dtype dt, uint32_t m, int64_t n, int64_t k, uint32_t group,
+                                  const void *q, int64_t ldq_bytes, const void *scales,
+                                  gbmm_dtype scale_dt, const uint8_t *zeros, const void *x, int64_t ldx,
+                                  void *y, int64_t ldy, gbmm_stream stream);
+
+/* gbmm_matmul_id_q4 -- out[r,:] = x row of r times matrix ids[r], transposed, for
+ * the routed rows r = t*top_k + s; ids >= n_experts give zero rows.  Expert e's q
+ * starts at byte e*expert_stride_bytes, its scales and zeros at element e*n*G.
+ * input_layout GBMM_INPUT_*: x is [m, k] or [m, top_k, k], out [m, top_k, n], both
+ * tight and of type dt.  Each distinct expert among 1024 consecutive routed rows
+ * is read once for each block of up to 8 of its rows.  m or n == 0 is a no-op,
+ * k == 0 writes zeros. */
+GBMM_API gbmm_status gbmm_matmul_id_q4(gbmm_dtype dt, uint32_t m, int64_t n, int64_t k, uint32_t top_k,
+                                       uint32_t n_experts, uint32_t input_layout, uint32_t group,
+                                       const void *q, int64_t ldq_bytes, int64_t expert_stride_bytes,
+                                       const void *scales, gbmm_dtype scale_dt, const uint8_t *zeros,
+                                       const void *x, const uint32_t *ids, void *out, gbmm_stream stream);
+
+/* ------------------------------------------------------------------------ */
 /* Errors, diagnostics                                                        */
 /* ------------------------------------------------------------------------ */
 
@@ -385,7 +543,8 @@ GBMM_API gbmm_status gbmm_device_error(gbmm_stream stream, uint32_t *code);
  * (tests that hand the library addresses no kernel may touch use it).
  * Kernel names: "gbmm_gemv_rowdot", "gbmm_gemv_coldot", "gbmm_gemv_tc", "gbmm_gemm_simt",
  * "gbmm_gemm_tc", "gbmm_fill_zero", "gbmm_matmul_id_direct",
- * "gbmm_matmul_id_map", "gbmm_matmul_id_grouped". */
+ * "gbmm_matmul_id_map", "gbmm_matmul_id_grouped", and the names of the gbmm_moe_*
+ * and *_q4 entry points for theirs. */
 GBMM_API void gbmm_test_inject_kernel_failure(const char *name);
 
 /* Kernels launched by this library since load / the last reset. */
@@ -396,7 +555,8 @@ GBMM_API void gbmm_test_reset_launch_count(void);
  * "gbmm_gemm_tc", "gbmm_gemm_simt", "gbmm_gemm_small", "gbmm_gemv_stream",
  * "gbmm_gemv_rowdot", "gbmm_gemv_coldot", "gbmm_gemv_tc", "gbmm_fill_zero",
  * "gbmm_matmul_id_direct", "gbmm_matmul_id_direct_tc", "gbmm_matmul_id_map",
- * "gbmm_matmul_id_grouped_tc", "gbmm_matmul_id_grouped_simt", and "gbmm_bounded_wait_test" for the wait test below. */
+ * "gbmm_matmul_id_grouped_tc", "gbmm_matmul_id_grouped_simt", "gbmm_bounded_wait_test" for the wait test below, and
+ * the names of the gbmm_moe_* and *_q4 entry points for theirs. */
 GBMM_API const char *gbmm_test_last_kernel(void);
 
 /*
