@@ -22,9 +22,9 @@ LIB = os.path.join(PKG, "libgbmm.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.cu", "direct_tc.cu", "gemv.cu", "gemv_tc.cu", "gemm_simt.cu", "gemm_tc.cu", "grouped_tc.cu", "matmul_id.cu",
-           "misc.cu", "moe_api.cu", "moe_route.cu", "moe_rows.cu", "moe_sort.cu", "q4.cu", "static_scratch.cu",
-           "stream.cu"]
-HEADERS = ["api_internal.h", "device_common.cuh", "kernel_params.h"]
+           "misc.cu", "moe_api.cu", "moe_route.cu", "moe_rows.cu", "moe_sort.cu", "q4_bf16.cu", "q4_f16.cu", "q4_f32.cu",
+           "static_scratch.cu", "stream.cu"]
+HEADERS = ["api_internal.h", "device_common.cuh", "kernel_params.h", "q4.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",

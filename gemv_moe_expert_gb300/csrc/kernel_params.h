@@ -118,6 +118,7 @@ struct MoeRouteParams {
     int64_t ld_logits, ld_d_logits;
     uint32_t m, n_experts, top_k;
     int32_t selected;        // softmax over the chosen experts (1) or over every live one (0)
+    int32_t logits_vec, bias_vec, d_logits_vec;  // rows divide into aligned runs (set by the launcher)
 };
 
 // Stable sort of routed rows by expert (moe_sort.cu).
@@ -146,7 +147,7 @@ struct MoeRowsParams {
     uint32_t m, top_k;
 };
 
-// Matrix-vector products with 4-bit weights (q4.cu), dense (ids null: every
+// Matrix-vector products with 4-bit weights (q4.cuh), dense (ids null: every
 // row of x through the one matrix) or per expert id (routed row r through
 // matrix ids[r]).
 struct Q4Params {
@@ -220,12 +221,14 @@ int grouped_tc_block_k();
 cudaError_t launch_moe_route(int dt, const MoeRouteParams &p, cudaStream_t s);
 cudaError_t launch_moe_route_backward(int dt, const MoeRouteParams &p, cudaStream_t s);
 uint64_t moe_sort_scratch_words(uint64_t rows, uint32_t n_experts);
-int moe_sort_launches(uint64_t rows, uint32_t n_experts);
+int moe_sort_launches(uint64_t rows);
 cudaError_t launch_moe_sort(int step, const MoeSortParams &p, cudaStream_t s);
 cudaError_t launch_moe_dispatch(int dt, const MoeRowsParams &p, cudaStream_t s);
 cudaError_t launch_moe_combine(int dt, const MoeRowsParams &p, cudaStream_t s);
 cudaError_t launch_moe_combine_backward(int dt, const MoeRowsParams &p, cudaStream_t s);
-cudaError_t launch_q4(int dt, const Q4Params &p, cudaStream_t s);
+cudaError_t launch_q4_f32(const Q4Params &p, cudaStream_t s);
+cudaError_t launch_q4_f16(const Q4Params &p, cudaStream_t s);
+cudaError_t launch_q4_bf16(const Q4Params &p, cudaStream_t s);
 
 int gemm_tc_block_m();
 int gemm_tc_wide_block_m();

@@ -188,6 +188,10 @@ gbmm_status check_q4(const char *fn, gbmm_dtype dt, int64_t n, int64_t k, uint32
     return GBMM_OK;
 }
 
+cudaError_t launch_q4(gbmm_dtype dt, const Q4Params &p, cudaStream_t s) {
+    return dt == GBMM_F32 ? launch_q4_f32(p, s) : dt == GBMM_F16 ? launch_q4_f16(p, s) : launch_q4_bf16(p, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -309,7 +313,7 @@ gbmm_status gbmm_moe_sort(uint32_t m, uint32_t top_k, uint32_t n_experts, const 
     p.scratch = static_cast<uint32_t *>(scratch);
     p.rows = static_cast<uint32_t>(rows);
     p.n_experts = n_experts;
-    const int launches = moe_sort_launches(rows, n_experts);
+    const int launches = moe_sort_launches(rows);
     for (int step = 0; step < launches; ++step) {
         st = finish_launch(launch_moe_sort(step, p, cuda_stream(stream)), fn, cuda_stream(stream));
         if (st != GBMM_OK) return st;
