@@ -10,8 +10,10 @@
 // at or past *valid have no expert.
 //
 // A block is a grid of tx x ty threads: tx along the row (one access of VB bytes
-// a thread and step), ty tokens.  Slots are taken in batches of kBatch, all of a
-// batch's loads issued before the first is used.
+// a thread and step), ty tokens.  Slots are taken in batches of B (4, or 8 for more
+// than 4 slots), all of a batch's loads issued before the first is used.  Blocks
+// stay and walk over the tokens: the places of the next token's slots are loaded
+// while the current token's rows are in flight.
 #include "device_common.cuh"
 
 namespace gbmm {
@@ -19,7 +21,16 @@ namespace gbmm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 8;
+constexpr int B = 4;
+// Blocks an SM (the registers they may use follow).  4-byte elements need fewer
+// registers for the same bytes in flight.  Measured on 4096 tokens x 8 slots of
+// 4096 elements: combine f32 95 us with 4 and 97 us with 5, bf16 52 and 51 us; its
+// gradient f32 177 us with 3 and 190 us with 4, bf16 97 and 92 us.
+template <typename T> struct Resident {
+    static constexpr int kCombine = sizeof(T) == 4 ? 4 : 5;
+    static constexpr int kBackward = sizeof(T) == 4 ? 3 : 4;
+};
+constexpr int kDispatchBlocks = 4;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kNowhere = 0xffffffffu;
 
@@ -28,32 +39,13 @@ template <> struct Raw<16> { using type = uint4; };
 template <> struct Raw<4> { using type = uint32_t; };
 template <> struct Raw<2> { using type = uint16_t; };
 
-// V elements of a row starting at element i, zeros past its end
 template <typename T, int VB>
-__device__ __forceinline__ typename Raw<VB>::type load_raw(const T *row, int64_t i, int64_t n) {
-    using R = typename Raw<VB>::type;
-    constexpr int V = VB / static_cast<int>(sizeof(T));
-    if (V == 1 || i + V <= n) return __ldg(reinterpret_cast<const R *>(row + i));
-    R r{};
-    T *e = reinterpret_cast<T *>(&r);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (i + j < n) e[j] = row[i + j];
-    return r;
+__device__ __forceinline__ typename Raw<VB>::type load_raw(const T *p) {
+    return __ldg(reinterpret_cast<const typename Raw<VB>::type *>(p));
 }
-
 template <typename T, int VB>
-__device__ __forceinline__ void store_raw(T *row, int64_t i, int64_t n, const typename Raw<VB>::type &r) {
-    using R = typename Raw<VB>::type;
-    constexpr int V = VB / static_cast<int>(sizeof(T));
-    if (V == 1 || i + V <= n) {
-        *reinterpret_cast<R *>(row + i) = r;
-        return;
-    }
-    const T *e = reinterpret_cast<const T *>(&r);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (i + j < n) row[i + j] = e[j];
+__device__ __forceinline__ void store_raw(T *p, const typename Raw<VB>::type &r) {
+    *reinterpret_cast<typename Raw<VB>::type *>(p) = r;
 }
 
 template <typename T, int V, typename R>
@@ -76,165 +68,249 @@ __device__ __forceinline__ uint32_t valid_rows(const MoeRowsParams &p) {
     const uint32_t rows = p.m * p.top_k;
     return p.valid != nullptr ? min(__ldg(p.valid), rows) : rows;
 }
-// place of slot s of token t, kNowhere past the token's slots
-__device__ __forceinline__ uint32_t place_of(const MoeRowsParams &p, uint32_t t, uint32_t s) {
-    if (s >= p.top_k) return kNowhere;
-    const uint32_t r = t * p.top_k + s;
-    return p.position != nullptr ? __ldg(p.position + r) : r;
+
+// Places and weights of a batch of slots of token t: slot s0 + b in lane b of the
+// token's warps; kNowhere past the token's slots and past the last token, weight 0
+// where there is no expert.  One load for the batch, handed out by shuffles, so
+// that the rows' loads wait for one latency and not for eight.
+struct Slots {
+    uint32_t at;
+    float w;
+    __device__ __forceinline__ void load(const MoeRowsParams &p, uint32_t valid, uint64_t t, uint32_t s0) {
+        const uint32_t s = s0 + (threadIdx.x & 31);
+        at = kNowhere;
+        w = 0.f;
+        if (t < p.m && s < s0 + B && s < p.top_k) {
+            const uint32_t r = static_cast<uint32_t>(t) * p.top_k + s;
+            w = p.weights != nullptr ? __ldg(p.weights + r) : 1.f;
+            at = p.position != nullptr ? __ldg(p.position + r) : r;
+            if (at >= valid) w = 0.f;
+        }
+    }
+    __device__ __forceinline__ uint32_t place(int b) const { return __shfl_sync(kFull, at, b); }
+    __device__ __forceinline__ float weight(int b) const { return __shfl_sync(kFull, w, b); }
+};
+
+// Columns of a row are dealt to threads in steps that all threads of a warp take
+// together (the shuffles need the whole warp; a thread past the end idles): first
+// the columns that divide into accesses of VB bytes, then the rest one by one.  The
+// two are separate calls so that every access in them is one predicated instruction
+// (with the choice inside the loop each load sat behind its own branch and the
+// loads of a batch no longer overlapped).
+
+struct Columns {
+    int64_t from, to, step;  // elements
+};
+template <int V>
+__device__ __forceinline__ Columns whole_columns(const MoeRowsParams &p) {
+    return Columns{(static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * V, p.n / V * V,
+                   static_cast<int64_t>(gridDim.y) * blockDim.x * V};
+}
+template <int V>
+__device__ __forceinline__ Columns rest_columns(const MoeRowsParams &p) {
+    return Columns{p.n / V * V + threadIdx.x, blockIdx.y == 0 ? p.n : 0, static_cast<int64_t>(blockDim.x)};
 }
 
 template <typename T, int VB>
-__global__ void __launch_bounds__(kThreads) moe_dispatch_kernel(MoeRowsParams p) {
+__device__ __forceinline__ void dispatch_columns(const MoeRowsParams &p, const Slots &slots, uint32_t valid,
+                                                 const T *x, const Columns &c) {
     using R = typename Raw<VB>::type;
     constexpr int V = VB / static_cast<int>(sizeof(T));
-    const uint32_t t = blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= p.m) return;
-    const uint32_t rows = p.m * p.top_k, valid = valid_rows(p);
-    const int64_t step = static_cast<int64_t>(gridDim.y) * blockDim.x * V;
-    const T *x = static_cast<const T *>(p.tok_in) + static_cast<int64_t>(t) * p.ld_tok_in;
+    const uint32_t rows = p.m * p.top_k;
+    const int lane = threadIdx.x & 31;
     T *out = static_cast<T *>(p.row_out);
-    for (uint32_t s0 = 0; s0 < p.top_k; s0 += kBatch) {
-        uint32_t at[kBatch];
+    for (int64_t i = c.from; i - lane * V < c.to; i += c.step) {
+        const bool in = i < c.to;
+        R v{};
+        if (in) v = load_raw<T, VB>(x + i);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) at[b] = place_of(p, t, s0 + b);
-        for (int64_t i = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * V; i < p.n; i += step) {
-            const R v = load_raw<T, VB>(x, i, p.n);
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-                if (at[b] < rows)
-                    store_raw<T, VB>(out + static_cast<int64_t>(at[b]) * p.ld_row_out, i, p.n, at[b] < valid ? v : R{});
+        for (int b = 0; b < B; ++b) {
+            const uint32_t at = slots.place(b);
+            if (in && at < rows) store_raw<T, VB>(out + static_cast<int64_t>(at) * p.ld_row_out + i, at < valid ? v : R{});
         }
     }
 }
 
 template <typename T, int VB>
-__global__ void __launch_bounds__(kThreads) moe_combine_kernel(MoeRowsParams p) {
+__global__ void __launch_bounds__(kThreads, kDispatchBlocks) moe_dispatch_kernel(const __grid_constant__ MoeRowsParams p) {
+    constexpr int V = VB / static_cast<int>(sizeof(T));
+    const uint32_t valid = valid_rows(p);
+    const uint64_t step = static_cast<uint64_t>(gridDim.x) * blockDim.y;
+    uint64_t t = static_cast<uint64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    Slots slots, next;
+    slots.load(p, valid, t, 0);
+    for (; t < p.m; t += step) {
+        next.load(p, valid, t + step, 0);
+        const T *x = static_cast<const T *>(p.tok_in) + static_cast<int64_t>(t) * p.ld_tok_in;
+        for (uint32_t s0 = 0; s0 < p.top_k; s0 += B) {
+            if (s0 != 0) slots.load(p, valid, t, s0);
+            dispatch_columns<T, VB>(p, slots, valid, x, whole_columns<V>(p));
+            if (V > 1) dispatch_columns<T, sizeof(T)>(p, slots, valid, x, rest_columns<V>(p));
+        }
+        slots = next;
+    }
+}
+
+// A slot without an expert adds 0 * 0.
+template <typename T, int VB>
+__device__ __forceinline__ void combine_columns(const MoeRowsParams &p, uint32_t t, Slots slots, uint32_t valid,
+                                                const Columns &c) {
     using R = typename Raw<VB>::type;
     constexpr int V = VB / static_cast<int>(sizeof(T));
-    const uint32_t t = blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= p.m) return;
-    const uint32_t valid = valid_rows(p);
-    const int64_t step = static_cast<int64_t>(gridDim.y) * blockDim.x * V;
-    const T *in = static_cast<const T *>(p.row_in);
+    const int lane = threadIdx.x & 31;
+    const T *in_rows = static_cast<const T *>(p.row_in);
     T *y = static_cast<T *>(p.tok_out) + static_cast<int64_t>(t) * p.ld_tok_out;
-    for (int64_t i = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * V; i < p.n; i += step) {
+    for (int64_t i = c.from; i - lane * V < c.to; i += c.step) {
+        const bool in = i < c.to;
         float acc[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] = 0.f;
-        for (uint32_t s0 = 0; s0 < p.top_k; s0 += kBatch) {
-            R v[kBatch];
-            float w[kBatch];
-            bool has[kBatch];
+        for (uint32_t s0 = 0; s0 < p.top_k; s0 += B) {
+            if (p.top_k > B) slots.load(p, valid, t, s0);
+            R v[B];
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                const uint32_t at = place_of(p, t, s0 + b);
-                has[b] = at < valid;
-                if (has[b]) {
-                    v[b] = load_raw<T, VB>(in + static_cast<int64_t>(at) * p.ld_row_in, i, p.n);
-                    w[b] = p.weights != nullptr ? __ldg(p.weights + t * p.top_k + s0 + b) : 1.f;
-                }
+            for (int b = 0; b < B; ++b) {
+                const uint32_t at = slots.place(b);
+                v[b] = R{};
+                if (in && at < valid) v[b] = load_raw<T, VB>(in_rows + static_cast<int64_t>(at) * p.ld_row_in + i);
             }
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                if (has[b]) {
-                    float f[V];
-                    unpack<T, V>(v[b], f);
+            for (int b = 0; b < B; ++b) {
+                const float w = slots.weight(b);
+                float f[V];
+                unpack<T, V>(v[b], f);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) acc[j] = fmaf(w[b], f[j], acc[j]);
-                }
+                for (int j = 0; j < V; ++j) acc[j] = fmaf(w, f[j], acc[j]);
             }
         }
-        store_raw<T, VB>(y, i, p.n, pack<T, V, R>(acc));
+        if (in) store_raw<T, VB>(y + i, pack<T, V, R>(acc));
     }
 }
 
-// Sums v[b] over the warp; lane l returns the sum of v[l / 4] (8 values, 9
-// shuffles: each of the first three steps halves the values a lane carries).
-__device__ __forceinline__ float warp_sum8(const float (&v)[kBatch], int lane) {
-    static_assert(kBatch == 8, "written for batches of 8");
-    float a[4], b[2], c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool up = lane & 16;
-        const float keep = up ? v[i + 4] : v[i], give = up ? v[i] : v[i + 4];
-        a[i] = keep + __shfl_xor_sync(kFull, give, 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool up = lane & 8;
-        const float keep = up ? a[i + 2] : a[i], give = up ? a[i] : a[i + 2];
-        b[i] = keep + __shfl_xor_sync(kFull, give, 8);
-    }
-    {
-        const bool up = lane & 4;
-        const float keep = up ? b[1] : b[0], give = up ? b[0] : b[1];
-        c = keep + __shfl_xor_sync(kFull, give, 4);
-    }
-    c += __shfl_xor_sync(kFull, c, 2);
-    c += __shfl_xor_sync(kFull, c, 1);
-    return c;
-}
-
-// blockDim.x is a multiple of 32, so a warp belongs to one token; the grid's y
-// extent is 1 (a block sees a token's whole row, for the dot products).
 template <typename T, int VB>
-__global__ void __launch_bounds__(kThreads) moe_combine_backward_kernel(MoeRowsParams p) {
+__global__ void __launch_bounds__(kThreads, Resident<T>::kCombine) moe_combine_kernel(const __grid_constant__ MoeRowsParams p) {
+    constexpr int V = VB / static_cast<int>(sizeof(T));
+    const uint32_t valid = valid_rows(p);
+    const uint64_t step = static_cast<uint64_t>(gridDim.x) * blockDim.y;
+    uint64_t t = static_cast<uint64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    Slots slots, next;
+    slots.load(p, valid, t, 0);
+    for (; t < p.m; t += step) {
+        next.load(p, valid, t + step, 0);
+        combine_columns<T, VB>(p, static_cast<uint32_t>(t), slots, valid, whole_columns<V>(p));
+        if (V > 1) combine_columns<T, sizeof(T)>(p, static_cast<uint32_t>(t), slots, valid, rest_columns<V>(p));
+        slots = next;
+    }
+}
+
+// Sums each v[b] over the warp; lane l returns the sum of v[l / (32 / B)]: each of
+// the first log2 B steps halves the values a lane carries, so 8 sums take 9
+// shuffles instead of 40.
+__device__ __forceinline__ float warp_sums(float (&v)[B]) {
+    const int lane = threadIdx.x & 31;
+    int o = 16;
+#pragma unroll
+    for (int half = B / 2; half > 0; half /= 2, o /= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float keep = up ? v[i + half] : v[i], give = up ? v[i] : v[i + half];
+            v[i] = keep + __shfl_xor_sync(kFull, give, o);
+        }
+    }
+#pragma unroll
+    for (; o > 0; o /= 2) v[0] += __shfl_xor_sync(kFull, v[0], o);
+    return v[0];
+}
+
+template <typename T, int VB>
+__device__ __forceinline__ void combine_backward_columns(const MoeRowsParams &p, const Slots &slots, uint32_t valid,
+                                                         const T *dy, const Columns &c, float (&dot)[B]) {
     using R = typename Raw<VB>::type;
     constexpr int V = VB / static_cast<int>(sizeof(T));
-    __shared__ float part[kThreads / 32][kBatch];
+    const uint32_t rows = p.m * p.top_k;
     const int lane = threadIdx.x & 31;
-    const uint32_t t = blockIdx.x * blockDim.y + threadIdx.y;
-    const bool live = t < p.m;
-    const uint32_t rows = p.m * p.top_k, valid = valid_rows(p);
-    const T *in = static_cast<const T *>(p.row_in);
+    const T *in_rows = static_cast<const T *>(p.row_in);
     T *out = static_cast<T *>(p.row_out);
-    const T *dy = static_cast<const T *>(p.tok_in) + static_cast<int64_t>(live ? t : 0) * p.ld_tok_in;
-    for (uint32_t s0 = 0; s0 < p.top_k; s0 += kBatch) {
-        uint32_t at[kBatch];
-        float w[kBatch], dot[kBatch];
+    for (int64_t i = c.from; i - lane * V < c.to; i += c.step) {
+        const bool in = i < c.to;
+        R v[B], graw{};
+        if (in) graw = load_raw<T, VB>(dy + i);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            at[b] = live ? place_of(p, t, s0 + b) : kNowhere;
-            w[b] = at[b] < valid ? __ldg(p.weights + t * p.top_k + s0 + b) : 0.f;
-            dot[b] = 0.f;
+        for (int b = 0; b < B; ++b) {
+            const uint32_t at = slots.place(b);
+            v[b] = R{};
+            if (in && at < valid) v[b] = load_raw<T, VB>(in_rows + static_cast<int64_t>(at) * p.ld_row_in + i);
         }
-        for (int64_t i = static_cast<int64_t>(threadIdx.x) * V; i < p.n; i += static_cast<int64_t>(blockDim.x) * V) {
-            if (!live) break;
-            R v[kBatch];
-            const R graw = load_raw<T, VB>(dy, i, p.n);
+        float g[V];
+        unpack<T, V>(graw, g);
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-                if (at[b] < valid) v[b] = load_raw<T, VB>(in + static_cast<int64_t>(at[b]) * p.ld_row_in, i, p.n);
-            float g[V];
-            unpack<T, V>(graw, g);
+        for (int b = 0; b < B; ++b) {
+            const uint32_t at = slots.place(b);
+            const float w = slots.weight(b);
+            float f[V], wg[V];
+            unpack<T, V>(v[b], f);
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                if (at[b] >= rows) continue;
-                R d{};
-                if (at[b] < valid) {
-                    float f[V], wg[V];
-                    unpack<T, V>(v[b], f);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        dot[b] = fmaf(g[j], f[j], dot[b]);
-                        wg[j] = w[b] * g[j];
-                    }
-                    d = pack<T, V, R>(wg);
-                }
-                store_raw<T, VB>(out + static_cast<int64_t>(at[b]) * p.ld_row_out, i, p.n, d);
+            for (int j = 0; j < V; ++j) {
+                dot[b] = fmaf(g[j], f[j], dot[b]);
+                wg[j] = w * g[j];
             }
+            const R d = pack<T, V, R>(wg);
+            if (in && at < rows) store_raw<T, VB>(out + static_cast<int64_t>(at) * p.ld_row_out + i, at < valid ? d : R{});
         }
-        // the warps of a token add up in order of their number
-        const float sum = warp_sum8(dot, lane);
-        const int warp = (threadIdx.y * blockDim.x + threadIdx.x) >> 5;
-        if ((lane & 3) == 0) part[warp][lane >> 2] = sum;
-        __syncthreads();
-        if (threadIdx.x < kBatch && live && s0 + threadIdx.x < p.top_k) {
-            float total = 0.f;
-            for (int q = 0; q < static_cast<int>(blockDim.x) / 32; ++q) total += part[warp + q][threadIdx.x];
-            p.d_weights[t * p.top_k + s0 + threadIdx.x] = total;
+    }
+}
+
+// The grid's y extent is 1: a block sees a token's whole row, for the dot products.
+template <typename T, int VB>
+__global__ void __launch_bounds__(kThreads, Resident<T>::kBackward)
+    moe_combine_backward_kernel(const __grid_constant__ MoeRowsParams p) {
+    constexpr int V = VB / static_cast<int>(sizeof(T));
+    __shared__ float part[2][kThreads / 32][B];
+    const int lane = threadIdx.x & 31;
+    const uint32_t valid = valid_rows(p);
+    const uint64_t step = static_cast<uint64_t>(gridDim.x) * blockDim.y;
+    const int warps = blockDim.x / 32, first_warp = threadIdx.y * warps, warp = first_warp + threadIdx.x / 32;
+    int turn = 0;
+    uint64_t t = static_cast<uint64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    Slots slots, next;
+    slots.load(p, valid, t, 0);
+    // every thread of the block takes the same number of turns (they meet at barriers)
+    for (uint64_t t_block = static_cast<uint64_t>(blockIdx.x) * blockDim.y; t_block < p.m; t_block += step, t += step) {
+        next.load(p, valid, t + step, 0);
+        const bool live = t < p.m;
+        const T *dy = static_cast<const T *>(p.tok_in) + static_cast<int64_t>(live ? t : 0) * p.ld_tok_in;
+        for (uint32_t s0 = 0; s0 < p.top_k; s0 += B) {
+            if (s0 != 0) slots.load(p, valid, t, s0);
+            float dot[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) dot[b] = 0.f;
+            if (live) {
+                combine_backward_columns<T, VB>(p, slots, valid, dy, whole_columns<V>(p), dot);
+                if (V > 1) combine_backward_columns<T, sizeof(T)>(p, slots, valid, dy, rest_columns<V>(p), dot);
+            }
+            // a slot without an expert has met zeros only, unless d_y is not finite
+            const float sum = warp_sums(dot);
+            constexpr int kLanes = 32 / B;  // that hold the same sum
+            if (warps == 1) {
+                const uint32_t s = s0 + lane / kLanes;
+                const uint32_t at = __shfl_sync(kFull, slots.at, lane / kLanes);
+                if (lane % kLanes == 0 && live && s < p.top_k)
+                    p.d_weights[t * p.top_k + s] = at < valid ? sum : 0.f;
+                continue;
+            }
+            // the warps of a token add up in order of their number; two buffers, so that
+            // one barrier a turn keeps the sums of the turn before from being overwritten
+            if (lane % kLanes == 0) part[turn][warp][lane / kLanes] = sum;
+            __syncthreads();
+            if (threadIdx.x < B && live && s0 + threadIdx.x < p.top_k) {
+                float total = 0.f;
+                for (int q = 0; q < warps; ++q) total += part[turn][first_warp + q][threadIdx.x];
+                p.d_weights[t * p.top_k + s0 + threadIdx.x] = slots.at < valid ? total : 0.f;
+            }
+            turn ^= 1;
         }
-        __syncthreads();
+        slots = next;
     }
 }
 
@@ -254,30 +330,42 @@ struct Shape {
     dim3 grid, block;
 };
 
-// tx covers a row of nvec accesses if it can; rows_whole: a block must see the
-// whole row.
-Shape shape_of(const MoeRowsParams &p, int V, bool rows_whole) {
+// tx covers a row of nvec accesses if it can, or half of it where that still gives
+// every SM its `resident` blocks (two steps a thread: 8192 tokens x 8 slots of 2048
+// bf16, gradient of combine, 91 us against 97 us).  `stays`: no more blocks than
+// that; they walk over the tokens (combine of the same rows 51 us, 54 us with a
+// block for each token).  A dispatch is mostly stores and is faster with a block for
+// each token (49 us against 56 us).  Along the row there are further blocks when there
+// are few tokens and a block need not see a whole row.
+Shape shape_of(const MoeRowsParams &p, int V, int resident, bool stays, bool rows_whole) {
     const int64_t nvec = (p.n + V - 1) / V;
+    const int64_t most = static_cast<int64_t>(resident) * device_sm_count();
     unsigned tx = 32;
-    while (tx < static_cast<unsigned>(kThreads) && tx < nvec) tx *= 2;
+    while (tx < static_cast<unsigned>(kThreads) &&
+           tx * (static_cast<int64_t>(p.m) * tx * 2 >= most * kThreads ? 2 : 1) < nvec)
+        tx *= 2;
     const unsigned ty = kThreads / tx;
-    int64_t gy = rows_whole ? 1 : (nvec + tx - 1) / tx;
-    if (gy > 65535) gy = 65535;
-    if (gy < 1) gy = 1;
-    return Shape{dim3((p.m + ty - 1) / ty, static_cast<unsigned>(gy)), dim3(tx, ty)};
+    int64_t gx = (static_cast<int64_t>(p.m) + ty - 1) / ty, gy = 1;
+    if (stays && gx > most) gx = most;
+    while (!rows_whole && gx * gy * 2 <= most && gy * tx < nvec) gy *= 2;
+    return Shape{dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(tx, ty)};
 }
 
 enum Which { kDispatch, kCombine, kCombineBackward };
 
 template <typename T, int VB>
 cudaError_t launch_vb(Which which, const MoeRowsParams &p, cudaStream_t s) {
-    const Shape h = shape_of(p, VB / static_cast<int>(sizeof(T)), which == kCombineBackward);
-    if (which == kDispatch)
+    constexpr int V = VB / static_cast<int>(sizeof(T));
+    if (which == kDispatch) {
+        const Shape h = shape_of(p, V, kDispatchBlocks, false, false);
         moe_dispatch_kernel<T, VB><<<h.grid, h.block, 0, s>>>(p);
-    else if (which == kCombine)
+    } else if (which == kCombine) {
+        const Shape h = shape_of(p, V, Resident<T>::kCombine, true, false);
         moe_combine_kernel<T, VB><<<h.grid, h.block, 0, s>>>(p);
-    else
+    } else {
+        const Shape h = shape_of(p, V, Resident<T>::kBackward, true, true);
         moe_combine_backward_kernel<T, VB><<<h.grid, h.block, 0, s>>>(p);
+    }
     return cudaGetLastError();
 }
 

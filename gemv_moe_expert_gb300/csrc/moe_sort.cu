@@ -57,18 +57,21 @@ struct Tile {
         row = static_cast<int64_t>(index) * kTile + warp * (32 * kPerThread) + lane;
 #pragma unroll
         for (int j = 0; j < kPerThread; ++j)
-            key[j] = row + 32 * j < p.rows ? min(p.ids[row + 32 * j], p.n_experts) : kFull;
-        for (uint32_t i = threadIdx.x; i < keys * kPitch; i += kThreads) counts[i] = 0;
+            key[j] = row + 32 * j < p.rows ? min(__ldg(p.ids + row + 32 * j), p.n_experts) : kFull;
+        uint32_t *words = reinterpret_cast<uint32_t *>(counts);
+        for (uint32_t i = threadIdx.x; i < (keys * kPitch + 1) / 2; i += kThreads) words[i] = 0u;
+        unsigned same[kPerThread];
+#pragma unroll
+        for (int j = 0; j < kPerThread; ++j) same[j] = __match_any_sync(kFull, key[j]);
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kPerThread; ++j) {
-            const unsigned same = __match_any_sync(kFull, key[j]);
             uint16_t *mine = counts + key[j] * kPitch + warp;
             const bool has = key[j] != kFull;
             const uint32_t before = has ? *mine : 0u;
-            rank[j] = before + __popc(same & ((1u << lane) - 1u));
+            rank[j] = before + __popc(same[j] & ((1u << lane) - 1u));
             __syncwarp();
-            if (has && lane == __ffs(same) - 1) *mine = static_cast<uint16_t>(before + __popc(same));
+            if (has && lane == __ffs(same[j]) - 1) *mine = static_cast<uint16_t>(before + __popc(same[j]));
             __syncwarp();
         }
         __syncthreads();
@@ -111,24 +114,35 @@ __device__ __forceinline__ uint32_t scan_keys(uint32_t c0, uint32_t c1, uint32_t
 }
 
 // ---- one launch: a cluster whose CTA c owns tile c ----
-
-__global__ void __launch_bounds__(kThreads, 1) moe_sort_cluster_kernel(MoeSortParams p) {
-    extern __shared__ uint16_t counts[];  // [keys][kPitch]
-    __shared__ uint32_t total[kMaxKeys], first[kMaxKeys], warp_sums[kWarps];
+//
+// Each CTA writes its totals into every CTA's shared memory (stores need no answer;
+// reading the others' totals would wait for each of them in turn), and one cluster
+// barrier makes them visible.
+__global__ void __launch_bounds__(kThreads, 1) moe_sort_cluster_kernel(const __grid_constant__ MoeSortParams p) {
+    extern __shared__ __align__(16) uint16_t counts[];  // [keys][kPitch]
+    __shared__ uint32_t total[kMaxKeys], first[kMaxKeys], all[kClusterTiles][kMaxKeys], warp_sums[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t keys = p.n_experts + 1, rank = cluster.block_rank(), tiles = cluster.num_blocks();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     Tile tile;
     tile.load(p, rank, counts);
     scan_warps(keys, counts, total);
-    cluster.sync();  // every tile's totals can be read
+    __syncthreads();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA runs: its shared memory can be written
+    for (uint32_t e = threadIdx.x; e < keys; e += kThreads) {
+        const uint32_t n = total[e];
+        for (uint32_t b = 0; b < tiles; ++b) *cluster.map_shared_rank(&all[rank][e], b) = n;
+    }
+    cluster.sync();  // every tile's totals have arrived
     uint32_t c[2], below[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t e = 2 * threadIdx.x + i;
         c[i] = below[i] = 0;
         if (e < keys) {
-            for (uint32_t b = 0; b < tiles; ++b) {
-                const uint32_t n = cluster.map_shared_rank(total, b)[e];
+#pragma unroll
+            for (uint32_t b = 0; b < kClusterTiles; ++b) {
+                const uint32_t n = b < tiles ? all[b][e] : 0u;
                 c[i] += n;
                 if (b < rank) below[i] += n;
             }
@@ -144,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_sort_cluster_kernel(MoeSortPa
         }
         start += c[i];
     }
-    cluster.sync();  // first[] is written, and nobody reads another CTA's totals any more
+    __syncthreads();
     tile.place(p, counts, first);
 }
 
@@ -183,7 +197,7 @@ __global__ void __launch_bounds__(256) moe_sort_scan_kernel(MoeSortParams p, uin
 }
 
 __global__ void __launch_bounds__(kThreads, 1) moe_sort_place_kernel(MoeSortParams p) {
-    extern __shared__ uint16_t counts[];  // [keys][kPitch]
+    extern __shared__ __align__(16) uint16_t counts[];  // [keys][kPitch]
     __shared__ uint32_t total[kMaxKeys], first[kMaxKeys], warp_sums[kWarps];
     const uint32_t keys = p.n_experts + 1, tiles = gridDim.x;
     Tile tile;
@@ -214,7 +228,7 @@ cudaError_t allow_smem(K *kernel, unsigned long long *done) {
     const unsigned long long bit = 1ull << (dev & 63);
     if (*done & bit) return cudaSuccess;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(kMaxKeys * kPitch * sizeof(uint16_t)));
+                                               static_cast<int>((kMaxKeys * kPitch + 1) / 2 * 4));
     if (e == cudaSuccess) *done |= bit;
     return e;
 }
@@ -231,7 +245,7 @@ int moe_sort_launches(uint64_t rows) { return tiles_of(rows) <= kClusterTiles ? 
 cudaError_t launch_moe_sort(int step, const MoeSortParams &p, cudaStream_t s) {
     static unsigned long long cluster_done = 0, place_done = 0;
     const uint32_t keys = p.n_experts + 1, tiles = tiles_of(p.rows);
-    const size_t smem = static_cast<size_t>(keys) * kPitch * sizeof(uint16_t);
+    const size_t smem = (static_cast<size_t>(keys) * kPitch + 1) / 2 * 4;
     if (tiles <= kClusterTiles) {
         const cudaError_t e = allow_smem(moe_sort_cluster_kernel, &cluster_done);
         if (e != cudaSuccess) return e;
