@@ -94,17 +94,21 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t z, uint32_t (&ou
     }
 }
 
+// d = A * B + (first ? 0 : d)
 template <Kind K>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
+__device__ __forceinline__ void mma(float (&d)[4], bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+    const float c0 = first ? 0.f : d[0], c1 = first ? 0.f : d[1], c2 = first ? 0.f : d[2], c3 = first ? 0.f : d[3];
     if (K == kHalf)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // The last bytes of a row, zeros past them.
@@ -115,28 +119,19 @@ static __device__ __noinline__ uint4 load_tail(const uint8_t *p, int64_t len) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 16 bytes of a packed row at byte `at` (a multiple of 16) of its `len` bytes.
-// VEC: rows start 16-byte aligned, 16 bytes can be read where `at` < `whole`
-// (the codes past the row's end meet zeros of x).  Otherwise pieces inside the row
-// are put together from the aligned words that cover them.
+// 16 bytes at p, inside a row.  Without VEC they are put together from the aligned
+// words that cover them (which may reach 3 bytes before p and 4 past them).
 template <bool VEC>
-__device__ __forceinline__ uint4 load_codes(const uint8_t *row, int32_t at, int32_t whole, int32_t len) {
-    const uint8_t *p = row + at;
-    if (VEC) {
-        if (at < whole) return ld_stream16(p);
-    } else {
-        const int32_t off = static_cast<int32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
-        if (at >= off && at + 20 <= len) {
-            const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
-            uint32_t w[5];
+__device__ __forceinline__ uint4 load_codes(const uint8_t *p) {
+    if (VEC) return ld_stream16(p);
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
+    uint32_t w[5];
 #pragma unroll
-            for (int i = 0; i < 5; ++i) w[i] = __ldg(q + i);
-            const uint32_t s = 8 * off;
-            return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s),
-                              __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
-        }
-    }
-    return at < len ? load_tail(p, len - at) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 5; ++i) w[i] = __ldg(q + i);
+    const uint32_t s = 8 * off;
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
 }
 
 // A chunk of a warp: rows g and g + 8 of its 16, 128 columns; scale and zero
@@ -147,9 +142,8 @@ struct Chunk {
 };
 
 __device__ __forceinline__ float scale_value(uint32_t raw, int dtype) {
-    if (dtype == kF32) return __uint_as_float(raw);
-    if (dtype == kBF16) return __uint_as_float(raw << 16);
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(raw)));
+    const float h = __half2float(__ushort_as_half(static_cast<unsigned short>(raw)));
+    return dtype == kF16 ? h : __uint_as_float(raw << (dtype == kBF16 ? 16 : 0));
 }
 
 // lane c of a quad holds words v.x .. v.w of columns 32 c .. 32 c + 31; after
@@ -362,41 +356,61 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
     const uint32_t base_row = blockIdx.z * kWindow;
     if (by_id && !find_expert<T>(p, base_row, blockIdx.y, j0, tile_rows, s_ids, s_bits, expert)) return;
 
-    // this thread's two rows (rows past the end repeat the last one and are not stored)
+    // This thread's two rows (rows past the end repeat the last one and are not
+    // stored), at this lane's 16 bytes of the warp's next chunk, and the cells of its
+    // group's scales and zero points.
     const int32_t row_len = static_cast<int32_t>((p.k + 1) / 2);
     const int32_t chunks = static_cast<int32_t>((p.k + 127) / 128), groups = static_cast<int32_t>(p.groups);
+    // chunks that can be read without a look at the row's end: whole ones, and without
+    // VEC neither the row's first nor its last words
+    const int32_t lo = VEC ? 0 : 1, hi = static_cast<int32_t>(VEC ? p.k / 128 : (p.k - 8) / 128);
     const int lane_group = NG == 4 ? c : NG == 2 ? c >> 1 : 0;  // of the chunk's, whose scale this lane loads
-    const uint8_t *row[2];
-    const uint8_t *zrow[2];
-    const char *srow[2];
-    int32_t whole[2];
     const int ssize = p.scale_dtype == kF32 ? 4 : 2;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        int64_t j = j0 + wr * 16 + g + 8 * h;
-        if (j >= p.n) j = p.n - 1;
-        row[h] = p.q + static_cast<int64_t>(expert) * p.expert_stride + j * p.ldq;
-        const int64_t cell = (static_cast<int64_t>(expert) * p.n + j) * p.groups;
-        srow[h] = static_cast<const char *>(p.scales) + cell * ssize;
-        zrow[h] = ZEROS ? p.zeros + cell : nullptr;
-        // the bytes after a row belong to the matrix too, except after the last row of all
-        whole[h] = j == p.n - 1 && expert == p.n_experts - 1 ? row_len - 15 : row_len;
-    }
-    auto fetch = [&](int32_t chunk, Chunk &b) {
-        if (chunk >= chunks) return;
-        const int32_t group = chunk * NG + lane_group;
+    const uint8_t *qat[2], *zat[2];
+    const char *sat[2];
+    auto rewind = [&] {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            b.q[h] = load_codes<VEC>(row[h], chunk * 64 + 16 * c, whole[h], row_len);
-            b.s[h] = b.z[h] = 0u;
-            if (group < groups) {
-                b.s[h] = ssize == 4 ? __ldg(reinterpret_cast<const uint32_t *>(srow[h]) + group)
-                                    : __ldg(reinterpret_cast<const uint16_t *>(srow[h]) + group);
-                if (ZEROS) b.z[h] = __ldg(zrow[h] + group);
+            int64_t j = j0 + wr * 16 + g + 8 * h;
+            if (j >= p.n) j = p.n - 1;
+            qat[h] = p.q + static_cast<int64_t>(expert) * p.expert_stride + j * p.ldq + wk * 64 + 16 * c;
+            const int64_t cell = (static_cast<int64_t>(expert) * p.n + j) * p.groups + wk * NG + lane_group;
+            sat[h] = static_cast<const char *>(p.scales) + cell * ssize;
+            zat[h] = ZEROS ? p.zeros + cell : nullptr;
+        }
+    };
+    // the warp's next chunk
+    auto fetch = [&](int32_t chunk, Chunk &b) {
+        if (chunk < hi && chunk >= lo) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                b.q[h] = load_codes<VEC>(qat[h]);
+                b.s[h] = ssize == 4 ? __ldg(reinterpret_cast<const uint32_t *>(sat[h]))
+                                    : __ldg(reinterpret_cast<const uint16_t *>(sat[h]));
+                b.z[h] = ZEROS ? __ldg(zat[h]) : 0u;
             }
+        } else if (chunk < chunks) {
+            const bool inside = chunk * NG + lane_group < groups;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                b.q[h] = load_tail(qat[h], row_len - (chunk * 64 + 16 * c));
+                b.s[h] = b.z[h] = 0u;
+                if (inside) {
+                    b.s[h] = ssize == 4 ? __ldg(reinterpret_cast<const uint32_t *>(sat[h]))
+                                        : __ldg(reinterpret_cast<const uint16_t *>(sat[h]));
+                    if (ZEROS) b.z[h] = __ldg(zat[h]);
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            qat[h] += cfg.wk * 64;
+            sat[h] += cfg.wk * NG * ssize;
+            if (ZEROS) zat[h] += cfg.wk * NG;
         }
     };
     Chunk buf[kDepth];
+    rewind();
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) fetch(wk + d * cfg.wk, buf[d]);
 
@@ -415,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
         slab = slab >= total ? total : slab / kDepth * kDepth;
         const uint32_t pitch = static_cast<uint32_t>(slab * cfg.wk) * 256 + 64;
         if (t0 != first) {
+            rewind();
 #pragma unroll
             for (int d = 0; d < kDepth; ++d) fetch(wk + d * cfg.wk, buf[d]);
         }
@@ -431,13 +446,21 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
                            static_cast<uint32_t>(slab * cfg.wk) * 16, pitch, stage);
             __syncthreads();
             const int32_t s1 = s0 + slab < total ? s0 + slab : total;
-            uint32_t xat = static_cast<uint32_t>(wk) * 256 + 16 * c + g * pitch;  // column g, this lane's first word
+            // this lane's first word of its column in each tile; lanes past the last column
+            // repeat it, and what they compute is not stored
+            const uint8_t *xat[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const uint32_t col = 8 * t + g;
+                xat[t] = stage + (col < cols ? col : cols - 1) * pitch + wk * 256 + 16 * c;
+            }
             int32_t chunk = wk + s0 * cfg.wk;
+            const int32_t end = s1 * cfg.wk < chunks ? s1 * cfg.wk : chunks;
 #pragma unroll 1
-            for (int32_t i0 = s0; i0 < s1; i0 += kDepth) {
+            while (chunk < end) {
 #pragma unroll
                 for (int d = 0; d < kDepth; ++d) {
-                    if (i0 + d < s1 && chunk < chunks) {
+                    if (chunk < end) {
                         uint32_t codes[2][4];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) exchange<NG>(buf[d].q[h], c, codes[h]);
@@ -464,15 +487,9 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
                                 if (t < tiles) {
-                                    if (opens) {
-#pragma unroll
-                                        for (int q = 0; q < 4; ++q) part[t][q] = 0.f;
-                                    }
-                                    uint4 b = make_uint4(0u, 0u, 0u, 0u);
-                                    if (8 * t + g < cols)
-                                        b = *reinterpret_cast<const uint4 *>(stage + (xat + 8 * t * pitch + 64 * w));
-                                    mma<K>(part[t], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
-                                    mma<K>(part[t], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+                                    const uint4 b = *reinterpret_cast<const uint4 *>(xat[t] + 64 * w);
+                                    mma<K>(part[t], opens, a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+                                    mma<K>(part[t], false, a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
                                     if (closes) {
 #pragma unroll
                                         for (int q = 0; q < 4; ++q)
@@ -481,10 +498,11 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
                                 }
                             }
                         }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) xat[t] += cfg.wk * 256;
+                        fetch(chunk + kDepth * cfg.wk, buf[d]);
+                        chunk += cfg.wk;
                     }
-                    xat += static_cast<uint32_t>(cfg.wk) * 256;
-                    fetch(chunk + kDepth * cfg.wk, buf[d]);
-                    chunk += cfg.wk;
                 }
             }
         }
@@ -543,7 +561,12 @@ cudaError_t launch(const Q4Params &p, int num_sms, cudaStream_t s) {
     const bool vec = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 16 == 0 && p.expert_stride % 16 == 0;
     // rows of x that one matrix can meet; past those of one column tile, the wide kernel
     const uint32_t most = p.ids != nullptr && p.rows > static_cast<uint32_t>(kWindow) ? kWindow : p.rows;
-    const bool wide = !vec || most * kTerms > 8;
+    // Per expert id the rows spread over the experts: on average there are `share` rows
+    // for each one that occurs, and a second pass over the few with more finds the
+    // weights in L2.
+    const uint32_t distinct = most < p.n_experts ? most : p.n_experts;
+    const uint32_t share = p.ids != nullptr ? (most + distinct - 1) / distinct : most;
+    const bool wide = !vec || share * kTerms > 8;
     const uint32_t pass = 8u * (wide ? (K == kFloat ? 3 : 2) : 1) / kTerms;
     const int64_t tiles = (p.n + 15) / 16;
     const int64_t chunks = (p.k + 127) / 128;
