@@ -185,11 +185,18 @@ gbmm_status check_q4(const char *fn, gbmm_dtype dt, int64_t n, int64_t k, uint32
     p->groups = (k + group - 1) / group;
     p->ldq = ldq;
     p->scale_dtype = scale_dt;
+    p->wait_limit_ns = kWaitLimitNs;
     return GBMM_OK;
 }
 
-cudaError_t launch_q4(gbmm_dtype dt, const Q4Params &p, cudaStream_t s) {
-    return dt == GBMM_F32 ? launch_q4_f32(p, s) : dt == GBMM_F16 ? launch_q4_f16(p, s) : launch_q4_bf16(p, s);
+gbmm_status launch_q4(const char *fn, gbmm_dtype dt, Q4Params &p, cudaStream_t s) {
+    if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
+    p.err = device_error_word();
+    if (p.err == nullptr) return fail(GBMM_ERR_CUDA, "%s: device error word unavailable", fn);
+    return finish_launch(dt == GBMM_F32   ? launch_q4_f32(p, s)
+                         : dt == GBMM_F16 ? launch_q4_f16(p, s)
+                                          : launch_q4_bf16(p, s),
+                         fn, s);
 }
 
 }  // namespace
@@ -452,7 +459,6 @@ gbmm_status gbmm_gemv_q4(gbmm_dtype dt, uint32_t m, int64_t n, int64_t k, uint32
                            {"y", y, y_bytes, size, true}};
     st = check_operands(fn, ops, 5);
     if (st != GBMM_OK) return st;
-    if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
     p.q = static_cast<const uint8_t *>(q);
     p.scales = scales;
     p.zeros = zeros;
@@ -463,7 +469,7 @@ gbmm_status gbmm_gemv_q4(gbmm_dtype dt, uint32_t m, int64_t n, int64_t k, uint32
     p.rows = m;
     p.top_k = 1;
     p.n_experts = 1;
-    return finish_launch(launch_q4(dt, p, cuda_stream(stream)), fn, cuda_stream(stream));
+    return launch_q4(fn, dt, p, cuda_stream(stream));
 }
 
 gbmm_status gbmm_matmul_id_q4(gbmm_dtype dt, uint32_t m, int64_t n, int64_t k, uint32_t top_k, uint32_t n_experts,
@@ -501,7 +507,6 @@ gbmm_status gbmm_matmul_id_q4(gbmm_dtype dt, uint32_t m, int64_t n, int64_t k, u
                            {"output", out, out_bytes, size, true}};
     st = check_operands(fn, ops, 6);
     if (st != GBMM_OK) return st;
-    if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
     p.q = static_cast<const uint8_t *>(q);
     p.expert_stride = expert_stride_bytes;
     p.scales = scales;
@@ -515,7 +520,7 @@ gbmm_status gbmm_matmul_id_q4(gbmm_dtype dt, uint32_t m, int64_t n, int64_t k, u
     p.rows = static_cast<uint32_t>(rows);
     p.top_k = top_k;
     p.n_experts = n_experts;
-    return finish_launch(launch_q4(dt, p, cuda_stream(stream)), fn, cuda_stream(stream));
+    return launch_q4(fn, dt, p, cuda_stream(stream));
 }
 
 }  // extern "C"

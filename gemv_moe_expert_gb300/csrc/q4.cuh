@@ -4,28 +4,43 @@
 //   y[i, j] = sum over groups g of s[j,g] * sum over x in g of (q[j,x] - z[j,g]) x[i,x]
 //
 // The weights are read once from HBM and have to become multiplier operands: the
-// kernel is bound by that stream, and next by the instructions that unpack it.
-// So the products run on the tensor cores straight from registers (mma m16n8k16:
-// 16 weight rows x 16 columns against 8 columns of x): a thread masks two codes
-// at a time into 16-bit floats whose mantissa holds the code, subtracts the zero
-// point (exactly: the codes are small integers) and has half an A register; a
-// product in f32 registers would also have to widen every code and multiply it
-// once per row of x.  The sum of a group is an f32 accumulator, scaled into the
-// result by one f32 multiply-add a group.
+// kernel is bound by that stream, and next to it by the instructions that unpack
+// the codes.  So the products run on the tensor cores straight from registers (mma
+// m16n8k16: 16 weight rows x 16 columns against 8 columns of x), and a pair of
+// codes becomes half an operand register with a single AND: a code c in the lowest
+// four mantissa bits of an f16 is the subnormal number c 2^-24, one in the next four
+// is 16 c 2^-24, and subnormal operands multiply exactly.  (An f32 product would have
+// to widen every code and multiply it once for each row of x; subtracting the zero
+// point from each code in f16 takes 9 instead of 5 instructions for 8 codes.)  With S
+// = sum of x over the group, the group's part of the result is s (sum of q x - z S).
 //
-// The order of a contraction is free, so a thread keeps the 16 bytes it loads
-// (32 neighbouring codes of a row) and x is stored in shared memory in the order
-// in which those codes come out of the words: with groups of 128 columns a quad of
-// lanes covers one group; for groups of 64 and 32 the lanes of a quad first
-// exchange words, so that one mma never mixes two groups.
+// x is staged in shared memory as f16, the columns that meet 16 c divided by 16,
+// after each group of columns of a row has been scaled by a power of two that puts
+// its largest magnitude into [2^14, 2^15): f16 and bf16 values keep all their bits
+// unless they lie 2^36 below that, where they round to a multiple of 2^-39 of it.
+// f32 values become three f16 terms in three of the mma's eight columns (33 bits
+// from the largest down).  A group that holds an infinity, a NaN or a value from
+// 2^117 up is left out and its row computed in plain f32 at the end.
 //
-// x in f32 is split exactly into three bf16 terms (8 significant bits each) that
-// take three columns of the mma's eight; the f32 sum of the three products is
-// exact up to the accumulator's rounding.
+// The order of a contraction is free, so a thread keeps the 32 bytes it loads (64
+// neighbouring codes of a row; the quad of lanes of a row covers a block of 256
+// columns, eight rows of whole 128-byte lines an access) and x is stored in the order
+// in which those codes come out of the words.  The mma must not add up different
+// groups: each row of x (each term of it) takes kParts of the mma's columns, and the
+// lanes of a quad that hold another group's codes read zeros there.  With groups of 128
+// lanes 0, 1 and 2, 3 hold one group each, with 64 every lane one, with 32 two, which
+// are closed one after the other.  The tensor pipe has the room, and nothing is
+// exchanged between lanes.
 //
-// A CTA has kWarps warps: wk of them split the columns (chunks of 128, one after
-// the other) of the same 16 rows, and kWarps / wk take different rows.  Each warp
-// keeps kDepth chunks of weights in flight in registers.
+// A warp takes 32 rows, so that what it reads of x serves two mma rows of tiles.  A CTA
+// has kWarps warps: wk of them split the columns (blocks, one after the other) of the
+// same rows, and kWarps / wk take different rows.  A warp's next block is loaded when
+// the one before has been used; twenty warps an SM hide the latency.
+//
+// What was measured on the way (16 bf16 tokens x 8 of 128 experts, 4096 x 1536, groups
+// of 32): 16 rows a warp and 16-byte loads of half lines 151 us, bound by the L1 data
+// path (95 of its cycles a KB of weights, 43 are there at the rate of HBM); a ring of
+// shared-memory slots filled by bulk copies of 256-byte row pieces 206 us; TIMING_NOW now.
 #pragma once
 
 #include "device_common.cuh"
@@ -38,107 +53,51 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kWindow = 1024;  // routed rows that a CTA searches for its expert's
 constexpr uint32_t kFull = 0xffffffffu;
 
-enum Kind { kHalf, kBfloat, kFloat };  // type of x
+constexpr int kTile = 32;      // rows of a warp
 
-// NT column tiles of 8: chunks in flight a warp, CTAs an SM, and the shared
-// memory for a slab of x, which holds kDepth chunks of every column for each of 4
-// warps at least.
+// NT column tiles of 8: CTAs an SM, and the shared memory for a slab of x, which holds
+// a block for each of kWarps warps at least.
 template <int NT> struct Budget {
-    static constexpr int kDepth = NT == 1 ? 4 : 2;
-    static constexpr int kCtas = NT == 1 ? 5 : 4;
-    static constexpr int kStageBytes = NT == 1 ? 34 * 1024 : NT == 2 ? 36 * 1024 : 56 * 1024;
-    static_assert((kStageBytes / (8 * NT) - 64) / 256 >= kWarps * kDepth, "a slab holds kDepth chunks a warp");
+    static constexpr int kCtas = NT == 1 ? 5 : NT == 2 ? 4 : 3;
+    static constexpr int kStageBytes = NT == 1 ? 32 * 1024 : NT == 2 ? 44 * 1024 : 60 * 1024;
 };
+// mma columns that a row of x takes; how often a block's sums are closed
+template <int G> struct Group {
+    static constexpr int kParts = G == 128 ? 2 : 4;
+    static constexpr int kCloses = G == 32 ? 2 : 1;
+    static constexpr int kInBlock = 256 / G;
+    static constexpr int kCells = G == 32 ? 4 : 2;  // neighbouring groups whose scales a lane needs
+};
+
+enum Kind { kHalf, kBfloat, kFloat };  // type of x
 
 template <Kind K> struct XType;
 template <> struct XType<kHalf> { using type = __half; };
 template <> struct XType<kBfloat> { using type = __nv_bfloat16; };
 template <> struct XType<kFloat> { using type = float; };
 
-__device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t mask, uint32_t bits) { return (w & mask) | bits; }
-
-__device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
-__device__ __forceinline__ uint32_t bits_of(__nv_bfloat162 h) { return *reinterpret_cast<uint32_t *>(&h); }
-
-// The four pairs (q[i] - z, q[i + 4] - z), i < 4, of a word's eight codes, as
-// 16-bit floats.  f16: 0x6400 | c is 1024 + c, and 0x6400 | 16 c is 1024 + 16 c,
-// whose sixteenth part is 64 + c.
-template <bool ZEROS>
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t z, uint32_t (&out)[4]) {
-    const __half2 low = __half2half2(__ushort_as_half(static_cast<unsigned short>(0xe400u + (ZEROS ? z : 8u))));
-    // 64 + z, negative: exact for every z <= 255
-    const __half2 high = ZEROS ? __half2half2(__uint2half_rn(64u + z)) : __half2half2(__ushort_as_half(0x5480));
-    const __half2 sixteenth = __half2half2(__ushort_as_half(0x2c00));
-    const uint32_t h = w >> 8;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t v = i ? h : w;
-        const uint32_t even = mask_or(v, 0x000f000fu, 0x64006400u), odd = mask_or(v, 0x00f000f0u, 0x64006400u);
-        out[2 * i] = bits_of(__hadd2(*reinterpret_cast<const __half2 *>(&even), low));
-        out[2 * i + 1] = bits_of(__hfma2(*reinterpret_cast<const __half2 *>(&odd), sixteenth, __hneg2(high)));
-    }
-}
-
-// bf16: 0x4300 | c is 128 + c.  128 + z is exact for z = 8; other zero points
-// are subtracted after 128 (both steps exact).
-template <bool ZEROS>
-__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t z, uint32_t (&out)[4]) {
-    const __nv_bfloat162 base = __bfloat162bfloat162(__ushort_as_bfloat16(ZEROS ? 0xc300 : 0xc308));
-    const __nv_bfloat162 zero = __bfloat162bfloat162(__float2bfloat16_rn(-static_cast<float>(z)));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t v = mask_or(w >> (4 * i), 0x000f000fu, 0x43004300u);
-        __nv_bfloat162 c = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&v), base);
-        if (ZEROS) c = __hadd2(c, zero);
-        out[i] = bits_of(c);
-    }
-}
+constexpr int kPitchPad = 64;                    // spreads the lines of x over the banks
+constexpr int kZeroBytes = 512;  // a block: what lanes of another group read
+// shared memory of one block of x: `lines` rows (terms of rows), and {factor, sum} of each column
+constexpr int block_bytes(int lines, int NT, int closes) { return lines * 512 + 64 * NT * closes; }
 
 // d = A * B + (first ? 0 : d)
-template <Kind K>
 __device__ __forceinline__ void mma(float (&d)[4], bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                     uint32_t b0, uint32_t b1) {
     const float c0 = first ? 0.f : d[0], c1 = first ? 0.f : d[1], c2 = first ? 0.f : d[2], c3 = first ? 0.f : d[3];
-    if (K == kHalf)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-            "{%10,%11,%12,%13};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-            "{%10,%11,%12,%13};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// The last bytes of a row, zeros past them.
-static __device__ __noinline__ uint4 load_tail(const uint8_t *p, int64_t len) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    for (int i = 0; i < 16; ++i)
-        if (i < len) w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// 16 bytes at p, inside a row.  Without VEC they are put together from the aligned
-// words that cover them (which may reach 3 bytes before p and 4 past them).
-template <bool VEC>
-__device__ __forceinline__ uint4 load_codes(const uint8_t *p) {
-    if (VEC) return ld_stream16(p);
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
-    const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
-    uint32_t w[5];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = __ldg(q + i);
-    const uint32_t s = 8 * off;
-    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
-                      __funnelshift_r(w[3], w[4], s));
-}
-
-// A chunk of a warp: rows g and g + 8 of its 16, 128 columns; scale and zero
-// point of the group that this lane loads for its quad, as loaded.
-struct Chunk {
-    uint4 q[2];
-    uint32_t s[2], z[2];
+struct Launch {
+    int wk_log;   // log2 of the warps that split the columns
+    int x_vec;    // rows of x start 16-byte aligned
+    int wide_q;   // packed rows start 32-byte aligned
+    int cells;    // scales are 16-bit, and they and the zero points of a lane can be read at once
+    int tails;    // the codes of the last blocks go through shared memory
+    int slab;     // blocks of x a warp in shared memory
+    int info_at, tails_at;  // byte offsets in shared memory
 };
 
 __device__ __forceinline__ float scale_value(uint32_t raw, int dtype) {
@@ -146,99 +105,36 @@ __device__ __forceinline__ float scale_value(uint32_t raw, int dtype) {
     return dtype == kF16 ? h : __uint_as_float(raw << (dtype == kBF16 ? 16 : 0));
 }
 
-// lane c of a quad holds words v.x .. v.w of columns 32 c .. 32 c + 31; after
-// this, word i of every lane lies in group i * NG / 4 of the chunk
-template <int NG>
-__device__ __forceinline__ void exchange(uint4 &q, int c, uint32_t (&v)[4]) {
-    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-    if (NG == 2) {
-        const bool up = c & 2;
-        const uint32_t r0 = __shfl_xor_sync(kFull, up ? v[0] : v[2], 2);
-        const uint32_t r1 = __shfl_xor_sync(kFull, up ? v[1] : v[3], 2);
-        if (up) {
-            v[0] = r0, v[1] = r1;
-        } else {
-            v[2] = r0, v[3] = r1;
-        }
-    } else if (NG == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            const uint32_t r = __shfl_xor_sync(kFull, (c & 1) ? v[i] : v[i + 1], 1);
-            if (c & 1) v[i] = r;
-            else v[i + 1] = r;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t r = __shfl_xor_sync(kFull, (c & 2) ? v[i] : v[i + 2], 2);
-            if (c & 2) v[i] = r;
-            else v[i + 2] = r;
-        }
-    }
-}
-
-// Byte offset, within its chunk's 256 bytes, of the eight columns 8 w .. 8 w + 7
-// of x (lane c reads word i at 64 i + 16 c): the inverse of exchange().
-template <int NG>
-__device__ __forceinline__ uint32_t word_offset(uint32_t w) {
-    uint32_t c, i;
-    if (NG == 1) {
-        c = w >> 2, i = w & 3;
-    } else if (NG == 2) {
-        c = ((w >> 2) & 1) + (w & 2), i = ((w >> 3) << 1) + (w & 1);
-    } else {
-        c = w & 3, i = w >> 2;
-    }
-    return 64 * i + 16 * c;
-}
-
-struct Launch {
-    int wk;           // warps that split the columns: 1, 2 or 4
-    int x_vec;        // rows of x start 16-byte aligned
-    int stage_bytes;  // shared memory for x
-};
-
 template <typename T>
-__device__ __forceinline__ void load8(const T *row, int64_t k0, int64_t k, bool vec, T (&v)[8]) {
+__device__ __forceinline__ void load8(const T *row, int64_t k0, int64_t k, bool vec, float (&f)[8]) {
     if (vec && k0 + 8 <= k) {
         constexpr int N = 8 * static_cast<int>(sizeof(T)) / 16;
-        uint4 raw[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) raw[i] = __ldg(reinterpret_cast<const uint4 *>(row + k0) + i);
-        const T *e = reinterpret_cast<const T *>(raw);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = e[j];
+        for (int i = 0; i < N; ++i)
+            unpack16<T>(__ldg(reinterpret_cast<const uint4 *>(row + k0) + i),
+                        f + i * (16 / static_cast<int>(sizeof(T))));
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = k0 + j < k ? row[k0 + j] : Elem<T>::from_f(0.f);
+        for (int j = 0; j < 8; ++j) f[j] = k0 + j < k ? Elem<T>::to_f(row[k0 + j]) : 0.f;
     }
 }
 
-__device__ __forceinline__ uint32_t pair_bits(uint32_t lo, uint32_t hi) { return lo | (hi << 16); }
+__device__ __forceinline__ float power_of_two(uint32_t exponent_field) { return __uint_as_float(exponent_field << 23); }
 
-// the 16-bit patterns of v in the order in which codes come out of a word
-__device__ __forceinline__ uint4 interleave(const uint32_t (&b)[8]) {
-    return make_uint4(pair_bits(b[0], b[4]), pair_bits(b[1], b[5]), pair_bits(b[2], b[6]), pair_bits(b[3], b[7]));
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// hi + mid + lo == v exactly, each with the 8 significant bits of a bf16 (cut off,
-// not rounded, so nothing overflows); an infinity or NaN is all in hi
-__device__ __forceinline__ void split3(float v, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    const uint32_t u = __float_as_uint(v);
-    hi = u >> 16;
-    mid = lo = 0u;
-    if ((u & 0x7f800000u) == 0x7f800000u) {
-        if (u & 0x007fffffu) hi |= 0x40u;
-        return;
-    }
-    const float r = v - __uint_as_float(u & 0xffff0000u);
-    const uint32_t ur = __float_as_uint(r);
-    mid = ur >> 16;
-    lo = __float_as_uint(r - __uint_as_float(ur & 0xffff0000u)) >> 16;
+// Byte offset, within its block's 512 bytes, of columns 8 w .. 8 w + 7 of x: word i =
+// w % 4 of half v = w / 4 % 2 of lane c = w / 8, which reads it at 256 v + 64 i + 16 c.
+__device__ __forceinline__ uint32_t word_offset(uint32_t w) {
+    return 256 * (w >> 2 & 1) + 64 * (w & 3) + 16 * (w >> 3);
 }
 
-// The routed rows of the window that starts at base_row and the expert that this
-// CTA serves: the d-th distinct one.  Returns false if there are fewer.  Leaves the
-// window's ids in s_ids; also zeroes the CTA's outputs of rows without an expert.
+// The window's expert that this CTA serves: the d-th distinct one of its ids.
+// Returns false if there are fewer.  Leaves the window's ids in s_ids; zeroes the CTA's
+// outputs of rows without an expert.
 template <typename T>
 __device__ __forceinline__ bool find_expert(const Q4Params &p, uint32_t base_row, uint32_t d, int64_t j0, int tile_rows,
                                             uint32_t *s_ids, uint32_t *s_bits, uint32_t &expert) {
@@ -299,120 +195,281 @@ __device__ __forceinline__ uint32_t list_rows(const Q4Params &p, uint32_t base_r
 }
 
 // x of `tokens` rows (routed rows list[t0 ..], or rows t0 .. without a list),
-// columns k0 .. k0 + 8 words - 1, into shared memory
-template <Kind K, int NG>
+// columns k0 .. k0 + 8 words - 1, into shared memory: f16 terms at stage + line *
+// pitch, and for each block (half a block with groups of 32) and mma column {factor, sum}: what undoes the scalings, and
+// the group's sum of x (of its first term's column only).  Rows with a group that
+// cannot be scaled are marked in *bad.
+template <Kind K, int G, int NT>
 __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, const uint32_t *list, uint32_t t0,
-                                        uint32_t tokens, int32_t k0, uint32_t words, uint32_t pitch, uint8_t *stage) {
+                                        uint32_t tokens, int32_t k0, uint32_t words, uint32_t pitch, uint8_t *stage,
+                                        float2 *info, uint32_t *bad) {
     using T = typename XType<K>::type;
     constexpr int kTerms = K == kFloat ? 3 : 1;
+    constexpr int kLanes = G / 8;  // that share a group
+    const int lane = threadIdx.x & 31;
 #pragma unroll 1
     for (uint32_t tok = 0; tok < tokens; ++tok) {
-        const uint32_t r = list != nullptr ? list[t0 + tok] : t0 + tok;
-        const T *x = static_cast<const T *>(p.x) + static_cast<int64_t>(r / p.top_k) * p.ldx +
-                     static_cast<int64_t>(r % p.top_k) * p.x_slot_stride;
-        uint8_t *col = stage + tok * kTerms * pitch;
+        uint32_t r = t0 + tok, slot = 0;
+        if (list != nullptr) {
+            slot = list[r] % p.top_k;
+            r = list[r] / p.top_k;
+        }
+        const T *x = static_cast<const T *>(p.x) + static_cast<int64_t>(r) * p.ldx + slot * p.x_slot_stride;
+        uint8_t *line = stage + tok * kTerms * pitch + word_offset(lane);
 #pragma unroll 1
         for (uint32_t w = threadIdx.x; w < words; w += kThreads) {
-            T v[8];
-            load8<T>(x, k0 + 8 * w, p.k, cfg.x_vec != 0, v);
-            uint8_t *dst = col + (w >> 4) * 256 + word_offset<NG>(w & 15);
-            if constexpr (K == kFloat) {
-                uint32_t b[3][8];
+            float f[8];  // words is a multiple of 32: a warp is all in or all out
+            load8<T>(x, static_cast<int64_t>(k0) + 8 * w, p.k, cfg.x_vec != 0, f);
+            float most = 0.f, sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) split3(v[j], b[0][j], b[1][j], b[2][j]);
+            for (int j = 0; j < 8; ++j) {
+                most = fmaxf(most, fabsf(f[j]));  // passes over NaN; the sum does not
+                sum += f[j];
+            }
 #pragma unroll
-                for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4 *>(dst + q * pitch) = interleave(b[q]);
-            } else {
-                uint32_t b[8];
+            for (int o = 1; o < kLanes; o <<= 1) {
+                most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
+                sum += __shfl_xor_sync(kFull, sum, o);
+            }
+            if (!(most < 1.6615349947311448e35f) || sum != sum) {  // 2^117
+                atomicOr(bad, 1u << tok);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) b[j] = *reinterpret_cast<const uint16_t *>(&v[j]);
-                *reinterpret_cast<uint4 *>(dst) = interleave(b);
+                for (int j = 0; j < 8; ++j) f[j] = 0.f;
+                most = sum = 0.f;
+            }
+            const uint32_t e = max(__float_as_uint(most) >> 23, 14u);
+            const float even = power_of_two(268u - e);   // 2^14 over the largest value's power of two
+            const float odd = power_of_two(264u - e);    // a sixteenth: codes 1, 3, 5, 7 of a word come as 16 c
+            const float factor = power_of_two(e + 10u);  // 2^24 (the codes come as c 2^-24) / even
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= j & 1 ? odd : even;
+            const uint32_t block = w >> 5, group = lane / kLanes;
+            // column of the row's (term's) first, and the close it belongs to
+            const uint32_t part = G == 32 ? group >> 1 : group, close = G == 32 ? group & 1 : 0;
+#pragma unroll
+            for (int q = 0; q < kTerms; ++q) {
+                uint32_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[i] = half2_bits(f[i], f[i + 4]);
+                    if (q + 1 < kTerms) {
+                        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                        f[i] -= v.x;
+                        f[i + 4] -= v.y;
+                    }
+                }
+                *reinterpret_cast<uint4 *>(line + block * 512 + q * pitch) = make_uint4(h[0], h[1], h[2], h[3]);
+                if (lane % kLanes == 0)
+                    info[(block * Group<G>::kCloses + close) * (8 * NT) + (tok * kTerms + q) * Group<G>::kParts + part] =
+                        make_float2(factor, q == 0 ? sum : 0.f);
             }
         }
     }
 }
 
-// NG: groups in a chunk of 128 columns.  NT: mma column tiles, 8 NT / terms rows
-// of x a pass.
-template <Kind K, int NG, bool ZEROS, bool VEC, int NT>
+// One output in plain f32, for a row of x that cannot be scaled.
+template <typename T>
+__device__ __noinline__ float plain_output(const Q4Params &p, uint32_t expert, int64_t j, uint32_t r) {
+    const uint8_t *q = p.q + static_cast<int64_t>(expert) * p.expert_stride + j * p.ldq;
+    const int64_t cell = (static_cast<int64_t>(expert) * p.n + j) * p.groups;
+    const T *x = static_cast<const T *>(p.x) + static_cast<int64_t>(r / p.top_k) * p.ldx +
+                 static_cast<int64_t>(r % p.top_k) * p.x_slot_stride;
+    float acc = 0.f;
+    for (int64_t g = 0; g < p.groups; ++g) {
+        const float s = scale_value(p.scale_dtype == kF32 ? static_cast<const uint32_t *>(p.scales)[cell + g]
+                                                          : static_cast<const uint16_t *>(p.scales)[cell + g],
+                                    p.scale_dtype);
+        const float z = p.zeros != nullptr ? static_cast<float>(p.zeros[cell + g]) : 8.f;
+        const int64_t end = (g + 1) * p.group < p.k ? (g + 1) * p.group : p.k;
+        float part = 0.f;
+        for (int64_t i = g * p.group; i < end; ++i)
+            part = fmaf(static_cast<float>((q[i >> 1] >> (4 * (i & 1))) & 15) - z, Elem<T>::to_f(x[i]), part);
+        acc = fmaf(s, part, acc);
+    }
+    return acc;
+}
+
+// 16 bytes at p, inside a row, put together from the aligned words that cover them,
+// which may reach 4 bytes past them, and 3 before: there, only the first word of the first
+// row of all would lie partly before the matrix.
+__device__ __forceinline__ uint4 load_unaligned(const uint8_t *p, const uint8_t *matrices) {
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
+    uint32_t w[5] = {0u, 0u, 0u, 0u, 0u};
+    if (p - off >= matrices) {
+        w[0] = __ldg(q);
+    } else {
+        for (uint32_t i = off; i < 4; ++i) w[0] |= static_cast<uint32_t>(__ldg(p + (i - off))) << (8 * i);
+    }
+#pragma unroll
+    for (int i = 1; i < 5; ++i) w[i] = __ldg(q + i);
+    const uint32_t s = 8 * off;
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
+}
+
+// 32 bytes, streamed once from HBM
+__device__ __forceinline__ void load_stream32(const void *p, uint4 &a, uint4 &b) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
+}
+
+// G: columns of a group.  VEC: packed rows start 16-byte aligned.  NT: mma column tiles,
+// 8 NT / (terms kParts) rows of x a pass.
+template <Kind K, int G, bool VEC, int NT>
 __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
     q4_kernel(const __grid_constant__ Q4Params p, const __grid_constant__ Launch cfg) {
     using T = typename XType<K>::type;
     constexpr int kTerms = K == kFloat ? 3 : 1;
-    constexpr int kDepth = Budget<NT>::kDepth;
-    constexpr uint32_t kPass = 8 * NT / kTerms;  // rows of x a pass
+    constexpr int kParts = Group<G>::kParts, kCloses = Group<G>::kCloses, kCells = Group<G>::kCells;
+    constexpr uint32_t kPass = 8 * NT / (kTerms * kParts);
+    static_assert(kPass > 0, "a row of x takes kTerms * kParts columns");
     constexpr int kRedPitch = 8 * NT + 1;
-    extern __shared__ __align__(16) uint8_t stage[];
-    __shared__ float red[kWarps][16][kRedPitch];
+    extern __shared__ __align__(16) uint8_t smem[];  // zeros, x, info, tails
+    __shared__ float red[kWarps][kTile][kRedPitch];
     __shared__ uint32_t s_ids[kWindow];
     __shared__ uint32_t s_bits[32];
-    __shared__ uint32_t s_count;
+    __shared__ uint32_t s_count, s_bad;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const int wk = warp & (cfg.wk - 1), wr = warp / cfg.wk, tile_rows = 16 * (kWarps / cfg.wk);
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * tile_rows;  // the CTA's first row
+    const int wk_count = 1 << cfg.wk_log, wk = warp & (wk_count - 1), wr = warp >> cfg.wk_log;
+    const int tile_rows_log = 7 - cfg.wk_log, tile_rows = 1 << tile_rows_log;  // kTile kWarps / wk
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x) << tile_rows_log;      // the CTA's first row
     const bool by_id = p.ids != nullptr;
 
     uint32_t expert = 0;
     const uint32_t base_row = blockIdx.z * kWindow;
     if (by_id && !find_expert<T>(p, base_row, blockIdx.y, j0, tile_rows, s_ids, s_bits, expert)) return;
 
-    // This thread's two rows (rows past the end repeat the last one and are not
-    // stored), at this lane's 16 bytes of the warp's next chunk, and the cells of its
-    // group's scales and zero points.
     const int32_t row_len = static_cast<int32_t>((p.k + 1) / 2);
-    const int32_t chunks = static_cast<int32_t>((p.k + 127) / 128), groups = static_cast<int32_t>(p.groups);
-    // chunks that can be read without a look at the row's end: whole ones, and without
-    // VEC neither the row's first nor its last words
-    const int32_t lo = VEC ? 0 : 1, hi = static_cast<int32_t>(VEC ? p.k / 128 : (p.k - 8) / 128);
-    const int lane_group = NG == 4 ? c : NG == 2 ? c >> 1 : 0;  // of the chunk's, whose scale this lane loads
-    const int ssize = p.scale_dtype == kF32 ? 4 : 2;
-    const uint8_t *qat[2], *zat[2];
-    const char *sat[2];
-    auto rewind = [&] {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            int64_t j = j0 + wr * 16 + g + 8 * h;
-            if (j >= p.n) j = p.n - 1;
-            qat[h] = p.q + static_cast<int64_t>(expert) * p.expert_stride + j * p.ldq + wk * 64 + 16 * c;
-            const int64_t cell = (static_cast<int64_t>(expert) * p.n + j) * p.groups + wk * NG + lane_group;
-            sat[h] = static_cast<const char *>(p.scales) + cell * ssize;
-            zat[h] = ZEROS ? p.zeros + cell : nullptr;
+    const int32_t blocks = static_cast<int32_t>((p.k + 255) / 256);
+    // Blocks that can be read without a look at the row's end: whole ones (without VEC
+    // up to 4 bytes more).  The codes of the others, one or two, go to shared memory byte by
+    // byte, unless rows end on a multiple of 16 bytes (what is read past a row's end, or
+    // stands there, meets zeros of x).
+    const int32_t hi = static_cast<int32_t>(VEC ? p.k / 256 : (p.k - 8) / 256);
+    uint8_t *tails = smem + cfg.tails_at;  // [tile_rows][VEC ? 128 : 256]
+    constexpr int kTailPitch = VEC ? 128 : 256;
+    if (cfg.tails) {
+        const int32_t len = row_len - hi * 128;
+        for (int32_t u = tid; u < len << tile_rows_log; u += kThreads) {
+            const int32_t r = u & (tile_rows - 1), b = u >> tile_rows_log;
+            if (j0 + r < p.n)
+                tails[r * kTailPitch + b] =
+                    __ldg(p.q + static_cast<int64_t>(expert) * p.expert_stride + (j0 + r) * p.ldq + hi * 128 + b);
         }
+        __syncthreads();
+    }
+    // The warp's rows are row + 8 h, h < 4; those past the end are not read (their
+    // registers hold whatever they do) and not stored.
+    const int64_t row = j0 + wr * kTile + g;
+    const int left = row >= p.n ? 0 : static_cast<int>(min((p.n - row + 7) / 8, static_cast<int64_t>(4)));
+    const int lane_cell = G == 128 ? 0 : kCells * (c & 1);
+    const uint8_t *qat;  // this lane's 32 bytes of row `row` in the block that is fetched next
+    int64_t cell;        // its first scale there
+    int32_t ahead;       // that block
+    auto rewind = [&] {
+        ahead = wk;
+        qat = p.q + static_cast<int64_t>(expert) * p.expert_stride + row * p.ldq + wk * 128 + 32 * c;
+        cell = (static_cast<int64_t>(expert) * p.n + row) * p.groups + wk * Group<G>::kInBlock + lane_cell;
     };
-    // the warp's next chunk
-    auto fetch = [&](int32_t chunk, Chunk &b) {
-        if (chunk < hi && chunk >= lo) {
+    uint4 q[4][2];
+    uint2 s_raw[4];
+    uint32_t z_raw[4];
+    auto fetch_codes = [&] {
+        if (ahead < hi) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                b.q[h] = load_codes<VEC>(qat[h]);
-                b.s[h] = ssize == 4 ? __ldg(reinterpret_cast<const uint32_t *>(sat[h]))
-                                    : __ldg(reinterpret_cast<const uint16_t *>(sat[h]));
-                b.z[h] = ZEROS ? __ldg(zat[h]) : 0u;
+            for (int h = 0; h < 4; ++h) {
+                const uint8_t *at = qat + h * (8 * p.ldq);
+                if (h < left) {
+                    if (!VEC) {
+                        q[h][0] = load_unaligned(at, p.q);
+                        q[h][1] = load_unaligned(at + 16, p.q);
+                    } else if (cfg.wide_q) {
+                        load_stream32(at, q[h][0], q[h][1]);
+                    } else {
+                        q[h][0] = ld_stream16(at);
+                        q[h][1] = ld_stream16(at + 16);
+                    }
+                }
             }
-        } else if (chunk < chunks) {
-            const bool inside = chunk * NG + lane_group < groups;
+        } else if (ahead < blocks) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                b.q[h] = load_tail(qat[h], row_len - (chunk * 64 + 16 * c));
-                b.s[h] = b.z[h] = 0u;
-                if (inside) {
-                    b.s[h] = ssize == 4 ? __ldg(reinterpret_cast<const uint32_t *>(sat[h]))
-                                        : __ldg(reinterpret_cast<const uint16_t *>(sat[h]));
-                    if (ZEROS) b.z[h] = __ldg(zat[h]);
+            for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    if (cfg.tails)
+                        q[h][v] = *reinterpret_cast<const uint4 *>(tails + (wr * kTile + g + 8 * h) * kTailPitch +
+                                                                   (ahead - hi) * 128 + 32 * c + 16 * v);
+                    else if (h < left && ahead * 128 + 32 * c + 16 * v < row_len)
+                        q[h][v] = ld_stream16(qat + h * (8 * p.ldq) + 16 * v);
                 }
             }
         }
+    };
+    auto fetch_cells = [&] {
+        if (ahead >= hi || !cfg.cells) return;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            qat[h] += cfg.wk * 64;
-            sat[h] += cfg.wk * NG * ssize;
-            if (ZEROS) zat[h] += cfg.wk * NG;
+        for (int h = 0; h < 4; ++h) {
+            const int64_t at = cell + h * (8 * p.groups);
+            if (h < left) {
+                const uint16_t *s = static_cast<const uint16_t *>(p.scales) + at;
+                if (kCells == 4) s_raw[h] = __ldg(reinterpret_cast<const uint2 *>(s));
+                else s_raw[h].x = __ldg(reinterpret_cast<const uint32_t *>(s));
+                if (p.zeros != nullptr) {
+                    if (kCells == 4) z_raw[h] = __ldg(reinterpret_cast<const uint32_t *>(p.zeros + at));
+                    else z_raw[h] = __ldg(reinterpret_cast<const uint16_t *>(p.zeros + at));
+                }
+            }
         }
     };
-    Chunk buf[kDepth];
-    rewind();
+    // scales and negative zero points times scales of row h's groups `close` and `close` +
+    // kCloses of the block `block` that was fetched last
+    auto cells_of = [&](int32_t block, int h, int close, float (&s)[2], float (&sz)[2]) {
+        float z[2] = {-8.f, -8.f};
+        if (block < hi && cfg.cells) {
+            // 16-bit cells 0, 1 | 2, 3; with groups of 32 close 0 takes 0 and 2, close 1 takes 1 and 3
+            const uint32_t a = kCells == 4 ? (close ? s_raw[h].x >> 16 : s_raw[h].x & 0xffffu) : s_raw[h].x & 0xffffu;
+            const uint32_t b = kCells == 4 ? (close ? s_raw[h].y >> 16 : s_raw[h].y & 0xffffu) : s_raw[h].x >> 16;
+            s[0] = scale_value(a, p.scale_dtype);
+            s[1] = scale_value(b, p.scale_dtype);
+            if (p.zeros != nullptr) {
+                z[0] = -static_cast<float>(z_raw[h] >> (8 * close) & 255u);
+                z[1] = -static_cast<float>(z_raw[h] >> (8 * (close + kCloses)) & 255u);
+            }
+        } else {
+            const int64_t at = (static_cast<int64_t>(expert) * p.n + row + 8 * h) * p.groups;
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) fetch(wk + d * cfg.wk, buf[d]);
+            for (int i = 0; i < 2; ++i) {
+                const int64_t group = static_cast<int64_t>(block) * Group<G>::kInBlock + lane_cell + close + kCloses * i;
+                s[i] = 0.f;
+                if (h < left && group < p.groups) {
+                    s[i] = scale_value(p.scale_dtype == kF32
+                                           ? __ldg(static_cast<const uint32_t *>(p.scales) + at + group)
+                                           : __ldg(static_cast<const uint16_t *>(p.scales) + at + group),
+                                       p.scale_dtype);
+                    if (p.zeros != nullptr) z[i] = -static_cast<float>(__ldg(p.zeros + at + group));
+                }
+            }
+        }
+        sz[0] = s[0] * z[0];
+        sz[1] = s[1] * z[1];
+    };
+    auto advance = [&] {
+        ahead += wk_count;
+        qat += 128 << cfg.wk_log;
+        cell += Group<G>::kInBlock << cfg.wk_log;
+    };
+    rewind();
+    fetch_codes();
+    fetch_cells();
+    advance();
+    // the zeros that lanes of another group read
+    if (tid < kZeroBytes / 16) reinterpret_cast<uint4 *>(smem)[tid] = make_uint4(0u, 0u, 0u, 0u);
+    uint8_t *stage = smem + kZeroBytes;
+    float2 *info = reinterpret_cast<float2 *>(smem + cfg.info_at);
+    const int32_t slab_blocks = cfg.slab << cfg.wk_log;
+    const uint32_t pitch = (static_cast<uint32_t>(slab_blocks) << 9) + kPitchPad;
 
     const uint32_t first = by_id ? 0u : blockIdx.y * kPass;
     const uint32_t stride = by_id ? kPass : gridDim.y * kPass;
@@ -421,184 +478,210 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
 #pragma unroll 1
     for (uint32_t t0 = first; t0 < count; t0 += stride) {
         const uint32_t tokens = min(count - t0, kPass);
-        const uint32_t cols = tokens * kTerms;
-        const int tiles = static_cast<int>((cols + 7) / 8);
-        const int32_t total = (chunks + cfg.wk - 1) / cfg.wk;  // chunks a warp
-        // chunks a warp of x that fit, a multiple of kDepth or all of them
-        int32_t slab = static_cast<int32_t>((cfg.stage_bytes / cols - 64) / 256) / cfg.wk;
-        slab = slab >= total ? total : slab / kDepth * kDepth;
-        const uint32_t pitch = static_cast<uint32_t>(slab * cfg.wk) * 256 + 64;
+        const uint32_t cols = tokens * kTerms * kParts;
         if (t0 != first) {
             rewind();
-#pragma unroll
-            for (int d = 0; d < kDepth; ++d) fetch(wk + d * cfg.wk, buf[d]);
+            fetch_codes();
+            fetch_cells();
+            advance();
         }
-        float acc[NT][4];
+        float acc[2][NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][t][i] = 0.f;
 
 #pragma unroll 1
-        for (int32_t s0 = 0; s0 < total; s0 += slab) {
+        for (int32_t b0 = 0; b0 < blocks; b0 += slab_blocks) {
             __syncthreads();  // the slab before, or the pass before, is done with
-            stage_x<K, NG>(p, cfg, by_id ? s_ids : nullptr, t0, tokens, s0 * cfg.wk * 128,
-                           static_cast<uint32_t>(slab * cfg.wk) * 16, pitch, stage);
+            if (b0 == 0) {
+                if (tid == 0) s_bad = 0u;
+                __syncthreads();
+            }
+            const int32_t b1 = min(b0 + slab_blocks, blocks);
+            stage_x<K, G, NT>(p, cfg, by_id ? s_ids : nullptr, t0, tokens, b0 * 256,
+                              static_cast<uint32_t>(b1 - b0) * 32, pitch, stage, info, &s_bad);
             __syncthreads();
-            const int32_t s1 = s0 + slab < total ? s0 + slab : total;
-            // this lane's first word of its column in each tile; lanes past the last column
-            // repeat it, and what they compute is not stored
+            // This lane's first word of the line of mma column 8 t + g, if its codes are of
+            // that column's group.  Lanes past the last column repeat it; what they compute
+            // is not stored.
             const uint8_t *xat[NT];
+            uint32_t xstep[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const uint32_t col = 8 * t + g;
-                xat[t] = stage + (col < cols ? col : cols - 1) * pitch + wk * 256 + 16 * c;
+                const uint32_t col = 8 * t + g < cols ? 8 * t + g : cols - 1;
+                const bool own = (kParts == 2 ? c >> 1 : c) == static_cast<int>(col % kParts);
+                xat[t] = own ? stage + (col / kParts) * pitch + wk * 512 + 16 * c : smem;
+                xstep[t] = own ? 512 << cfg.wk_log : 0;
             }
-            int32_t chunk = wk + s0 * cfg.wk;
-            const int32_t end = s1 * cfg.wk < chunks ? s1 * cfg.wk : chunks;
+            // {factor, sum} of columns 2 c and 2 c + 1
+            const float4 *iat = reinterpret_cast<const float4 *>(info + wk * (kCloses * 8 * NT)) + c;
 #pragma unroll 1
-            while (chunk < end) {
+            for (int32_t block = wk + b0; block < b1; block += wk_count) {
+                float part[2][NT][4];
 #pragma unroll
-                for (int d = 0; d < kDepth; ++d) {
-                    if (chunk < end) {
-                        uint32_t codes[2][4];
+                for (int v = 0; v < 2; ++v) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) exchange<NG>(buf[d].q[h], c, codes[h]);
-                        float part[NT][4];
+                    for (int i = 0; i < 4; ++i) {
+                        constexpr uint32_t kEven = 0x000f000fu, kOdd = 0x00f000f0u;
+                        uint32_t u[4];
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const int from = (lane & 28) + (NG == 2 ? w & 2 : w);
-                            uint32_t a[2][4];
+                        for (int h = 0; h < 4; ++h)
+                            u[h] = i == 0 ? q[h][v].x : i == 1 ? q[h][v].y : i == 2 ? q[h][v].z : q[h][v].w;
+                        const bool opens = i == 0 && (v == 0 || kCloses == 2);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t z = 0u;
-                                if (ZEROS) z = NG == 1 ? buf[d].z[h] : __shfl_sync(kFull, buf[d].z[h], from);
-                                if (K == kHalf) codes_f16<ZEROS>(codes[h][w], z, a[h]);
-                                else codes_bf16<ZEROS>(codes[h][w], z, a[h]);
+                        for (int t = 0; t < NT; ++t) {
+                            {
+                                const uint4 b = *reinterpret_cast<const uint4 *>(xat[t] + 256 * v + 64 * i);
+#pragma unroll
+                                for (int m = 0; m < 2; ++m) {
+                                    const uint32_t v0 = u[2 * m], v1 = u[2 * m + 1];
+                                    mma(part[m][t], opens, v0 & kEven, v1 & kEven, v0 & kOdd, v1 & kOdd, b.x, b.y);
+                                    mma(part[m][t], false, v0 >> 8 & kEven, v1 >> 8 & kEven, v0 >> 8 & kOdd,
+                                        v1 >> 8 & kOdd, b.z, b.w);
+                                }
                             }
-                            const bool opens = w % (4 / NG) == 0, closes = w % (4 / NG) == 4 / NG - 1;
-                            float s[2];
-                            if (closes) {
+                        }
+                    }
+                    if (v == 1) fetch_codes();
+                    if (v == 1 || kCloses == 2) {
+                        const int close = kCloses == 2 ? v : 0;
 #pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    s[h] = scale_value(
-                                        NG == 1 ? buf[d].s[h] : __shfl_sync(kFull, buf[d].s[h], from), p.scale_dtype);
-                            }
+                        for (int m = 0; m < 2; ++m) {
+                            float s[2][2], sz[2][2];  // [row][column's group]
+                            cells_of(block, 2 * m, close, s[0], sz[0]);
+                            cells_of(block, 2 * m + 1, close, s[1], sz[1]);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                if (t < tiles) {
-                                    const uint4 b = *reinterpret_cast<const uint4 *>(xat[t] + 64 * w);
-                                    mma<K>(part[t], opens, a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
-                                    mma<K>(part[t], false, a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
-                                    if (closes) {
+                                {
+                                    const float4 f = iat[close * (4 * NT) + 4 * t];
 #pragma unroll
-                                        for (int q = 0; q < 4; ++q)
-                                            acc[t][q] = fmaf(s[q >> 1], part[t][q], acc[t][q]);
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float factor = i & 1 ? f.z : f.x, sum = i & 1 ? f.w : f.y;
+                                        float &a = acc[m][t][i];
+                                        a = fmaf(s[i >> 1][i & 1] * factor, part[m][t][i], a);
+                                        a = fmaf(sz[i >> 1][i & 1], sum, a);
                                     }
                                 }
                             }
                         }
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) xat[t] += cfg.wk * 256;
-                        fetch(chunk + kDepth * cfg.wk, buf[d]);
-                        chunk += cfg.wk;
                     }
                 }
+                fetch_cells();
+                advance();
+#pragma unroll
+                for (int t = 0; t < NT; ++t) xat[t] += xstep[t];
+                iat += (kCloses * 4 * NT) << cfg.wk_log;
             }
         }
 
-        // the warps that split the columns, and the terms of an f32 row, add up in order
-        if (t0 != first) __syncthreads();  // the pass before has read red
+        // the warps that split the columns, and the terms and groups of a row, add up in order
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) red[warp][g + 8 * (q >> 1)][8 * t + 2 * c + (q & 1)] = acc[t][q];
-        }
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    red[warp][16 * m + g + 8 * (i >> 1)][8 * t + 2 * c + (i & 1)] = acc[m][t][i];
         __syncthreads();
-        for (uint32_t u = tid; u < tile_rows * tokens; u += kThreads) {
-            const uint32_t jj = u & (tile_rows - 1), tok = u / tile_rows;
+        const uint32_t bad = s_bad;
+        for (uint32_t u = tid; u < tokens << tile_rows_log; u += kThreads) {
+            const uint32_t jj = u & (tile_rows - 1), tok = u >> tile_rows_log;
             if (j0 + jj >= p.n) continue;
-            float sum = 0.f;
-            for (int w = 0; w < cfg.wk; ++w) {
-#pragma unroll
-                for (int q = 0; q < kTerms; ++q) sum += red[(jj >> 4) * cfg.wk + w][jj & 15][tok * kTerms + q];
-            }
             const uint32_t r = by_id ? s_ids[t0 + tok] : t0 + tok;
+            float sum = 0.f;
+            if (bad >> tok & 1u) {
+                sum = plain_output<T>(p, expert, j0 + jj, r);
+            } else {
+                for (int w = 0; w < wk_count; ++w) {
+#pragma unroll
+                    for (int i = 0; i < kTerms * kParts; ++i)
+                        sum += red[((jj / kTile) << cfg.wk_log) + w][jj % kTile][tok * (kTerms * kParts) + i];
+                }
+            }
             static_cast<T *>(p.out)[static_cast<int64_t>(r) * p.ldo + j0 + jj] = Elem<T>::from_f(sum);
         }
     }
 }
 
-template <Kind K, int NG, bool ZEROS, bool VEC, int NT>
-cudaError_t launch_one(const Q4Params &p, const Launch &cfg, dim3 grid, cudaStream_t s) {
+template <Kind K, int G, bool VEC, int NT>
+cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
+    using T = typename XType<K>::type;
+    constexpr int kTerms = K == kFloat ? 3 : 1;
+    constexpr uint32_t kPass = 8 * NT / (kTerms * Group<G>::kParts);
+    constexpr int kCells = Group<G>::kCells;
+    const int64_t tiles = (p.n + kTile - 1) / kTile;
+    const int64_t blocks = (p.k + 255) / 256;
+    uint32_t gy, gz = 1;
+    if (p.ids != nullptr) {
+        gz = (p.rows + kWindow - 1) / kWindow;
+        gy = p.rows < kWindow ? p.rows : kWindow;  // distinct experts of a window at most
+        if (gy > p.n_experts) gy = p.n_experts;
+    } else {
+        gy = (p.rows + kPass - 1) / kPass;
+        if (gy > 65535u) gy = 65535u;
+    }
+    if (gz > 65535u) return cudaErrorInvalidConfiguration;
+    Launch cfg{};
+    int wk = 1;
+    while (wk < kWarps && wk < blocks && tiles * gy * wk < 16LL * num_sms) wk *= 2, ++cfg.wk_log;
+    auto multiple = [](const void *ptr, int64_t a) { return reinterpret_cast<uintptr_t>(ptr) % a == 0; };
+    cfg.x_vec = multiple(p.x, 16) && p.ldx * sizeof(T) % 16 == 0 && p.x_slot_stride * sizeof(T) % 16 == 0;
+    cfg.wide_q = multiple(p.q, 32) && p.ldq % 32 == 0 && p.expert_stride % 32 == 0;
+    cfg.cells = p.scale_dtype != kF32 && p.groups % kCells == 0 && multiple(p.scales, 2 * kCells) &&
+                multiple(p.zeros, kCells);
+    cfg.tails = VEC ? (p.k + 1) / 2 % 16 != 0 : 1;
+    const int lines = static_cast<int>(p.rows < kPass ? p.rows : kPass) * kTerms;
+    const int64_t all = (blocks + wk - 1) / wk;
+    const int per_block = wk * block_bytes(lines, NT, Group<G>::kCloses);
+    cfg.slab = (Budget<NT>::kStageBytes - lines * kPitchPad) / per_block;
+    if (cfg.slab > all) cfg.slab = static_cast<int>(all);
+    cfg.info_at = kZeroBytes + lines * (cfg.slab * wk * 512 + kPitchPad);
+    cfg.tails_at = kZeroBytes + lines * kPitchPad + cfg.slab * per_block;
+    const int64_t wr = kWarps / wk;
+    const int bytes = cfg.tails_at + (cfg.tails ? static_cast<int>(wr) * kTile * (VEC ? 128 : 256) : 0);
+
     static unsigned long long done = 0;  // devices on which the kernel may use its shared memory
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(done & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(q4_kernel<K, NG, ZEROS, VEC, NT>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   Budget<NT>::kStageBytes);
+        const cudaError_t e = cudaFuncSetAttribute(q4_kernel<K, G, VEC, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   Budget<NT>::kStageBytes + kZeroBytes + kWarps * kTile * 256);
         if (e != cudaSuccess) return e;
         done |= bit;
     }
-    q4_kernel<K, NG, ZEROS, VEC, NT><<<grid, kThreads, cfg.stage_bytes, s>>>(p, cfg);
+    q4_kernel<K, G, VEC, NT><<<dim3(static_cast<unsigned>((tiles + wr - 1) / wr), gy, gz), kThreads, bytes, s>>>(p, cfg);
     return cudaGetLastError();
 }
 
-template <Kind K, int NG, bool ZEROS>
-cudaError_t launch_vec(const Q4Params &p, const Launch &cfg, bool vec, bool wide, dim3 grid, cudaStream_t s) {
-    constexpr int kWide = K == kFloat ? 3 : 2;
-    if (!vec) return launch_one<K, NG, ZEROS, false, kWide>(p, cfg, grid, s);
-    return wide ? launch_one<K, NG, ZEROS, true, kWide>(p, cfg, grid, s)
-                : launch_one<K, NG, ZEROS, true, 1>(p, cfg, grid, s);
+// Column tiles: kNarrow for a few rows of x a matrix, kWide for more.  A pass takes 8
+// NT / (terms kParts) rows; more tiles cost registers and shared memory, so that fewer
+// warps are there to hide latency.  Per expert id the rows spread over the experts: on
+// average there are `share` rows for each one that occurs, and a second pass over the
+// few with more finds the weights in L2.
+template <Kind K, int G>
+cudaError_t launch_g(const Q4Params &p, int num_sms, cudaStream_t s) {
+    constexpr int kTerms = K == kFloat ? 3 : 1;
+    constexpr int kColumns = kTerms * Group<G>::kParts;
+    constexpr int kNarrow = (kColumns + 7) / 8;
+    constexpr int kWide = K == kFloat ? 3 : G == 128 ? 2 : 4;
+    const bool vec = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 16 == 0 && p.expert_stride % 16 == 0;
+    const uint32_t distinct = p.rows < p.n_experts ? p.rows : p.n_experts;
+    const uint32_t share = p.ids != nullptr ? (p.rows + distinct - 1) / distinct : p.rows;
+    if (!vec) return launch_nt<K, G, false, kWide>(p, num_sms, s);
+    return share * kColumns > 8 * kNarrow ? launch_nt<K, G, true, kWide>(p, num_sms, s)
+                                          : launch_nt<K, G, true, kNarrow>(p, num_sms, s);
 }
 
 template <Kind K>
 cudaError_t launch(const Q4Params &p, int num_sms, cudaStream_t s) {
-    using T = typename XType<K>::type;
-    constexpr int kTerms = K == kFloat ? 3 : 1;
-    const bool vec = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 16 == 0 && p.expert_stride % 16 == 0;
-    // rows of x that one matrix can meet; past those of one column tile, the wide kernel
-    const uint32_t most = p.ids != nullptr && p.rows > static_cast<uint32_t>(kWindow) ? kWindow : p.rows;
-    // Per expert id the rows spread over the experts: on average there are `share` rows
-    // for each one that occurs, and a second pass over the few with more finds the
-    // weights in L2.
-    const uint32_t distinct = most < p.n_experts ? most : p.n_experts;
-    const uint32_t share = p.ids != nullptr ? (most + distinct - 1) / distinct : most;
-    const bool wide = !vec || share * kTerms > 8;
-    const uint32_t pass = 8u * (wide ? (K == kFloat ? 3 : 2) : 1) / kTerms;
-    const int64_t tiles = (p.n + 15) / 16;
-    const int64_t chunks = (p.k + 127) / 128;
-    uint32_t gy, gz = 1;
-    if (p.ids != nullptr) {
-        gz = (p.rows + kWindow - 1) / kWindow;
-        gy = most < p.n_experts ? most : p.n_experts;
-    } else {
-        gy = (p.rows + pass - 1) / pass;
-        if (gy > 65535u) gy = 65535u;
-    }
-    if (gz > 65535u) return cudaErrorInvalidConfiguration;
-    Launch cfg{};
-    cfg.wk = 1;
-    while (cfg.wk < kWarps && cfg.wk < chunks && tiles * gy * cfg.wk < 16LL * num_sms) cfg.wk *= 2;
-    cfg.x_vec = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx * sizeof(T) % 16 == 0 &&
-                p.x_slot_stride * sizeof(T) % 16 == 0;
-    const int64_t cols = static_cast<int64_t>(most < pass ? most : pass) * kTerms;
-    const int64_t want = cols * ((chunks + cfg.wk - 1) / cfg.wk * cfg.wk * 256 + 64);
-    const int64_t cap = wide ? Budget<K == kFloat ? 3 : 2>::kStageBytes : Budget<1>::kStageBytes;
-    cfg.stage_bytes = static_cast<int>(want < cap ? want : cap);
-    const int64_t wr = kWarps / cfg.wk;
-    const dim3 grid(static_cast<unsigned>((tiles + wr - 1) / wr), gy, gz);
-    const int ng = 128 / p.group;
-    if (p.zeros != nullptr) {
-        if (ng == 1) return launch_vec<K, 1, true>(p, cfg, vec, wide, grid, s);
-        if (ng == 2) return launch_vec<K, 2, true>(p, cfg, vec, wide, grid, s);
-        return launch_vec<K, 4, true>(p, cfg, vec, wide, grid, s);
-    }
-    if (ng == 1) return launch_vec<K, 1, false>(p, cfg, vec, wide, grid, s);
-    if (ng == 2) return launch_vec<K, 2, false>(p, cfg, vec, wide, grid, s);
-    return launch_vec<K, 4, false>(p, cfg, vec, wide, grid, s);
+    if (p.k == 0) return launch_fill_zero(K == kFloat ? kF32 : K == kHalf ? kF16 : kBF16, p.out, 1, p.rows, p.n, p.ldo, 0, s);
+    if (p.group == 128) return launch_g<K, 128>(p, num_sms, s);
+    if (p.group == 64) return launch_g<K, 64>(p, num_sms, s);
+    return launch_g<K, 32>(p, num_sms, s);
 }
 
 }  // namespace q4
