@@ -26,7 +26,6 @@ enum KernelId : uint32_t {
     kKidGemvTc = 5,
     kKidDirectTc = 6,
     kKidGemvColdotStream = 7,
-    kKidQ4 = 8,
 };
 
 // default limit of a bounded device wait (1 s)
@@ -164,8 +163,6 @@ struct Q4Params {
     int64_t n, k, groups;        // groups = ceil(k / group)
     int32_t group, scale_dtype;
     uint32_t rows, top_k, n_experts;
-    uint32_t *err;
-    uint64_t wait_limit_ns;
 };
 
 // ---- launchers (each returns the launch's cudaError_t) --------------------

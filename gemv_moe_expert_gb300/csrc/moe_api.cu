@@ -185,14 +185,11 @@ gbmm_status check_q4(const char *fn, gbmm_dtype dt, int64_t n, int64_t k, uint32
     p->groups = (k + group - 1) / group;
     p->ldq = ldq;
     p->scale_dtype = scale_dt;
-    p->wait_limit_ns = kWaitLimitNs;
     return GBMM_OK;
 }
 
-gbmm_status launch_q4(const char *fn, gbmm_dtype dt, Q4Params &p, cudaStream_t s) {
+gbmm_status launch_q4(const char *fn, gbmm_dtype dt, const Q4Params &p, cudaStream_t s) {
     if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
-    p.err = device_error_word();
-    if (p.err == nullptr) return fail(GBMM_ERR_CUDA, "%s: device error word unavailable", fn);
     return finish_launch(dt == GBMM_F32   ? launch_q4_f32(p, s)
                          : dt == GBMM_F16 ? launch_q4_f16(p, s)
                                           : launch_q4_bf16(p, s),

@@ -16,11 +16,12 @@
 //
 // x is staged in shared memory as f16, the columns that meet 16 c divided by 16,
 // after each group of columns of a row has been scaled by a power of two that puts
-// its largest magnitude into [2^14, 2^15): f16 and bf16 values keep all their bits
-// unless they lie 2^36 below that, where they round to a multiple of 2^-39 of it.
-// f32 values become three f16 terms in three of the mma's eight columns (33 bits
-// from the largest down).  A group that holds an infinity, a NaN or a value from
-// 2^117 up is left out and its row computed in plain f32 at the end.
+// its largest magnitude into [2^14, 2^15).  A value keeps all its bits unless it lies
+// 2^25 (f16) or 2^28 (bf16) below the largest of its group; then it is off by 2^-35 of that
+// at most, far less than what rounding does to an f32 sum with the largest in it.  f32
+// values become the sum of three f16 terms, in three of the mma's eight columns, with the
+// same bound.  A group that holds an infinity, a NaN or a value from 2^117 up is left out and
+// its row computed in plain f32 at the end.
 //
 // The order of a contraction is free, so a thread keeps the 32 bytes it loads (64
 // neighbouring codes of a row; the quad of lanes of a row covers a block of 256
@@ -32,15 +33,26 @@
 // are closed one after the other.  The tensor pipe has the room, and nothing is
 // exchanged between lanes.
 //
-// A warp takes 32 rows, so that what it reads of x serves two mma rows of tiles.  A CTA
+// A warp takes 32 rows, so that what it reads of x serves two mma row tiles.  A CTA
 // has kWarps warps: wk of them split the columns (blocks, one after the other) of the
-// same rows, and kWarps / wk take different rows.  A warp's next block is loaded when
-// the one before has been used; twenty warps an SM hide the latency.
+// same rows, and kWarps / wk take different rows.  A warp's first block is loaded before x
+// is staged, each next one as soon as the one before has been used: sixteen to twenty
+// warps an SM hide the latency.  Loads are predicated, not branched around, and the
+// alignment they need is settled at the launch (Access).
 //
-// What was measured on the way (16 bf16 tokens x 8 of 128 experts, 4096 x 1536, groups
-// of 32): 16 rows a warp and 16-byte loads of half lines 151 us, bound by the L1 data
-// path (95 of its cycles a KB of weights, 43 are there at the rate of HBM); a ring of
-// shared-memory slots filled by bulk copies of 256-byte row pieces 206 us; TIMING_NOW now.
+// Measured (us, and GB/s of codes, scales, zeros, x and y; inputs rotate past L2):
+//   dense 11008 x 4096, groups of 128, 1 row     f16 9.6 (2410)   f32 10.5 (2220)
+//   the same, 4 f16 rows 16.1, 16 f16 rows 28.4, 8 f32 rows 28.7
+//   4 bf16 tokens x 8 of 64 experts, 1408 x 2048     14.5 (2880)
+//   16 tokens x 8 of 128 experts, 1536 x 4096: bf16, groups of 32 with zeros 84 (3660);
+//   bf16, groups of 128 70.9 (3850); f32, groups of 128 100 (2730)
+// The large ones issue in 53 % of the cycles, half of it the ANDs and shifts that unpack the
+// codes, and wait as often for HBM as for results of the instructions before; the small
+// ones are over before HBM is at its rate.  On the way (the case with groups of 32): 16
+// rows a warp and 16-byte loads of half lines 151, bound by the L1 data path; a ring of
+// shared-memory slots filled by bulk copies of 256-byte row pieces 206; the next block held
+// in a second set of registers 91, as it leaves room for fewer instructions in flight; CTAs that
+// walk over several row tiles 172.
 #pragma once
 
 #include "device_common.cuh"
@@ -53,12 +65,13 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kWindow = 1024;  // routed rows that a CTA searches for its expert's
 constexpr uint32_t kFull = 0xffffffffu;
 
-constexpr int kTile = 32;      // rows of a warp
-
-// NT column tiles of 8: CTAs an SM, and the shared memory for a slab of x, which holds
-// a block for each of kWarps warps at least.
-template <int NT> struct Budget {
-    static constexpr int kCtas = NT == 1 ? 5 : NT == 2 ? 4 : 3;
+// NT column tiles of 8, MT row tiles of 16 a warp: CTAs an SM, and the shared memory for
+// a slab of x, which holds two blocks for each of kWarps warps at least.  One row tile with
+// four CTAs in place of five: 13.1 us for 9.6 (dense, 1 row); two tiles with five in place
+// of four: 22.1 for 18.8 (4 f32 tokens x 8 of 64 experts); three and more column tiles with
+// two in place of three: 42 for 29 (dense, 8 bf16 rows, groups of 64).
+template <int NT, int MT> struct Budget {
+    static constexpr int kCtas = MT == 1 ? (NT == 1 ? 5 : 4) : NT == 1 ? 4 : 3;
     static constexpr int kStageBytes = NT == 1 ? 32 * 1024 : NT == 2 ? 44 * 1024 : 60 * 1024;
 };
 // mma columns that a row of x takes; how often a block's sums are closed
@@ -76,7 +89,7 @@ template <> struct XType<kHalf> { using type = __half; };
 template <> struct XType<kBfloat> { using type = __nv_bfloat16; };
 template <> struct XType<kFloat> { using type = float; };
 
-constexpr int kPitchPad = 64;                    // spreads the lines of x over the banks
+constexpr int kPitchPad = 64;    // spreads the lines of x over the banks
 constexpr int kZeroBytes = 512;  // a block: what lanes of another group read
 // shared memory of one block of x: `lines` rows (terms of rows), and {factor, sum} of each column
 constexpr int block_bytes(int lines, int NT, int closes) { return lines * 512 + 64 * NT * closes; }
@@ -93,9 +106,7 @@ __device__ __forceinline__ void mma(float (&d)[4], bool first, uint32_t a0, uint
 struct Launch {
     int wk_log;   // log2 of the warps that split the columns
     int x_vec;    // rows of x start 16-byte aligned
-    int wide_q;   // packed rows start 32-byte aligned
-    int cells;    // scales are 16-bit, and they and the zero points of a lane can be read at once
-    int tails;    // the codes of the last blocks go through shared memory
+    int aligned;  // packed rows start 16-byte aligned
     int slab;     // blocks of x a warp in shared memory
     int info_at, tails_at;  // byte offsets in shared memory
 };
@@ -105,19 +116,27 @@ __device__ __forceinline__ float scale_value(uint32_t raw, int dtype) {
     return dtype == kF16 ? h : __uint_as_float(raw << (dtype == kBF16 ? 16 : 0));
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T *row, int64_t k0, int64_t k, bool vec, float (&f)[8]) {
-    if (vec && k0 + 8 <= k) {
-        constexpr int N = 8 * static_cast<int>(sizeof(T)) / 16;
+// Eight neighbouring values of x as loaded, zeros past the row's k columns.
+template <typename T> struct Eight {
+    static constexpr int N = 8 * static_cast<int>(sizeof(T)) / 16;
+    uint4 raw[N];
+    __device__ __forceinline__ void load(const T *row, int64_t k0, int64_t k, bool vec) {
+        if (vec && k0 + 8 <= k) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            unpack16<T>(__ldg(reinterpret_cast<const uint4 *>(row + k0) + i),
-                        f + i * (16 / static_cast<int>(sizeof(T))));
-    } else {
+            for (int i = 0; i < N; ++i) raw[i] = __ldg(reinterpret_cast<const uint4 *>(row + k0) + i);
+        } else {
+            T v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = k0 + j < k ? Elem<T>::to_f(row[k0 + j]) : 0.f;
+            for (int j = 0; j < 8; ++j) v[j] = k0 + j < k ? row[k0 + j] : Elem<T>::from_f(0.f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) raw[i] = reinterpret_cast<const uint4 *>(v)[i];
+        }
     }
-}
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) unpack16<T>(raw[i], f + i * (8 / N));
+    }
+};
 
 __device__ __forceinline__ float power_of_two(uint32_t exponent_field) { return __uint_as_float(exponent_field << 23); }
 
@@ -196,9 +215,9 @@ __device__ __forceinline__ uint32_t list_rows(const Q4Params &p, uint32_t base_r
 
 // x of `tokens` rows (routed rows list[t0 ..], or rows t0 .. without a list),
 // columns k0 .. k0 + 8 words - 1, into shared memory: f16 terms at stage + line *
-// pitch, and for each block (half a block with groups of 32) and mma column {factor, sum}: what undoes the scalings, and
-// the group's sum of x (of its first term's column only).  Rows with a group that
-// cannot be scaled are marked in *bad.
+// pitch, and for each block (half a block with groups of 32) and mma column {factor, sum}:
+// what undoes the scalings, and the group's sum of x (of its first term's column only).
+// Rows with a group that cannot be scaled are marked in *bad.
 template <Kind K, int G, int NT>
 __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, const uint32_t *list, uint32_t t0,
                                         uint32_t tokens, int32_t k0, uint32_t words, uint32_t pitch, uint8_t *stage,
@@ -206,20 +225,37 @@ __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, co
     using T = typename XType<K>::type;
     constexpr int kTerms = K == kFloat ? 3 : 1;
     constexpr int kLanes = G / 8;  // that share a group
+    constexpr int kAhead = 3;  // loads in flight a thread (1: 16 f16 rows 53 us for 41; 4: no faster)
     const int lane = threadIdx.x & 31;
-#pragma unroll 1
-    for (uint32_t tok = 0; tok < tokens; ++tok) {
-        uint32_t r = t0 + tok, slot = 0;
-        if (list != nullptr) {
-            slot = list[r] % p.top_k;
-            r = list[r] / p.top_k;
+    // a warp takes 32 words, of one row (words is a multiple of 32), and goes on kThreads further
+    uint32_t tok = 0, w = threadIdx.x;
+    while (tok < tokens) {
+        Eight<T> x8[kAhead];
+        uint32_t toks[kAhead], ws[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            while (w >= words && tok < tokens) {
+                w -= words;
+                ++tok;
+            }
+            toks[a] = tok;
+            ws[a] = w;
+            if (tok < tokens) {
+                uint32_t r = t0 + tok, slot = 0;
+                if (list != nullptr) {
+                    slot = list[r] % p.top_k;
+                    r = list[r] / p.top_k;
+                }
+                const T *x = static_cast<const T *>(p.x) + static_cast<int64_t>(r) * p.ldx + slot * p.x_slot_stride;
+                x8[a].load(x, static_cast<int64_t>(k0) + 8 * w, p.k, cfg.x_vec != 0);
+            }
+            w += kThreads;
         }
-        const T *x = static_cast<const T *>(p.x) + static_cast<int64_t>(r) * p.ldx + slot * p.x_slot_stride;
-        uint8_t *line = stage + tok * kTerms * pitch + word_offset(lane);
-#pragma unroll 1
-        for (uint32_t w = threadIdx.x; w < words; w += kThreads) {
-            float f[8];  // words is a multiple of 32: a warp is all in or all out
-            load8<T>(x, static_cast<int64_t>(k0) + 8 * w, p.k, cfg.x_vec != 0, f);
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            if (toks[a] >= tokens) break;
+            float f[8];
+            x8[a].get(f);
             float most = 0.f, sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -232,7 +268,7 @@ __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, co
                 sum += __shfl_xor_sync(kFull, sum, o);
             }
             if (!(most < 1.6615349947311448e35f) || sum != sum) {  // 2^117
-                atomicOr(bad, 1u << tok);
+                atomicOr(bad, 1u << toks[a]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] = 0.f;
                 most = sum = 0.f;
@@ -243,9 +279,12 @@ __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, co
             const float factor = power_of_two(e + 10u);  // 2^24 (the codes come as c 2^-24) / even
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] *= j & 1 ? odd : even;
-            const uint32_t block = w >> 5, group = lane / kLanes;
+            const uint32_t block = ws[a] >> 5, group = lane / kLanes;
             // column of the row's (term's) first, and the close it belongs to
             const uint32_t part = G == 32 ? group >> 1 : group, close = G == 32 ? group & 1 : 0;
+            uint8_t *line = stage + toks[a] * kTerms * pitch + block * 512 + word_offset(lane);
+            float2 *column = info + (block * Group<G>::kCloses + close) * (8 * NT) +
+                             toks[a] * kTerms * Group<G>::kParts + part;
 #pragma unroll
             for (int q = 0; q < kTerms; ++q) {
                 uint32_t h[4];
@@ -258,10 +297,8 @@ __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, co
                         f[i + 4] -= v.y;
                     }
                 }
-                *reinterpret_cast<uint4 *>(line + block * 512 + q * pitch) = make_uint4(h[0], h[1], h[2], h[3]);
-                if (lane % kLanes == 0)
-                    info[(block * Group<G>::kCloses + close) * (8 * NT) + (tok * kTerms + q) * Group<G>::kParts + part] =
-                        make_float2(factor, q == 0 ? sum : 0.f);
+                *reinterpret_cast<uint4 *>(line + q * pitch) = make_uint4(h[0], h[1], h[2], h[3]);
+                if (lane % kLanes == 0) column[q * Group<G>::kParts] = make_float2(factor, q == 0 ? sum : 0.f);
             }
         }
     }
@@ -308,17 +345,59 @@ __device__ __forceinline__ uint4 load_unaligned(const uint8_t *p, const uint8_t 
                       __funnelshift_r(w[3], w[4], s));
 }
 
-// 32 bytes, streamed once from HBM
-__device__ __forceinline__ void load_stream32(const void *p, uint4 &a, uint4 &b) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-                 : "l"(p));
+// Loads under a predicate, without a branch: a branch around each would end a basic
+// block, and nothing would be scheduled across it.
+__device__ __forceinline__ void load_stream32(bool pred, const void *p, uint4 (&v)[2]) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %9, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t}"
+        : "+r"(v[0].x), "+r"(v[0].y), "+r"(v[0].z), "+r"(v[0].w), "+r"(v[1].x), "+r"(v[1].y), "+r"(v[1].z),
+          "+r"(v[1].w)
+        : "l"(p), "r"(static_cast<uint32_t>(pred)));
+}
+// zero where the predicate is false
+__device__ __forceinline__ uint2 load_cells64(bool pred, const void *p) {
+    uint2 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+        "@p ld.global.nc.v2.b32 {%0, %1}, [%2];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y)
+        : "l"(p), "r"(static_cast<uint32_t>(pred)));
+    return v;
+}
+__device__ __forceinline__ uint32_t load_cells32(bool pred, const void *p) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
+                 : "=&r"(v)
+                 : "l"(p), "r"(static_cast<uint32_t>(pred)));
+    return v;
+}
+__device__ __forceinline__ uint32_t load_cells16(bool pred, const void *p) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
+                 : "=&r"(v)
+                 : "l"(p), "r"(static_cast<uint32_t>(pred)));
+    return v;
+}
+__device__ __forceinline__ uint32_t load_cells8(bool pred, const void *p) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.u8 %0, [%1];\n\t}"
+                 : "=&r"(v)
+                 : "l"(p), "r"(static_cast<uint32_t>(pred)));
+    return v;
 }
 
-// G: columns of a group.  VEC: packed rows start 16-byte aligned.  NT: mma column tiles,
-// 8 NT / (terms kParts) rows of x a pass.
-template <Kind K, int G, bool VEC, int NT>
-__global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
+// How a kernel reads codes, scales and zero points.
+//   kAnyhow  any alignment and scale type; a look at every access
+//   kApart   packed rows start and end on multiples of 32 bytes, 16-bit scales; the
+//            scales of a lane one by one (groups of 32: two by two)
+//   kAtOnce  and the scales of a lane, and its zero points, can be read at once
+enum Access { kAnyhow, kApart, kAtOnce };
+
+// G: columns of a group.  NT: mma column tiles, 8 NT / (terms kParts) rows of x a pass.
+// MT: mma row tiles of a warp.
+template <Kind K, int G, Access A, int NT, int MT>
+__global__ void __launch_bounds__(kThreads, Budget<NT, MT>::kCtas)
     q4_kernel(const __grid_constant__ Q4Params p, const __grid_constant__ Launch cfg) {
     using T = typename XType<K>::type;
     constexpr int kTerms = K == kFloat ? 3 : 1;
@@ -326,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
     constexpr uint32_t kPass = 8 * NT / (kTerms * kParts);
     static_assert(kPass > 0, "a row of x takes kTerms * kParts columns");
     constexpr int kRedPitch = 8 * NT + 1;
+    constexpr int kTile = 16 * MT, kRows = 2 * MT;  // rows of a warp, of a lane
     extern __shared__ __align__(16) uint8_t smem[];  // zeros, x, info, tails
     __shared__ float red[kWarps][kTile][kRedPitch];
     __shared__ uint32_t s_ids[kWindow];
@@ -333,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
     __shared__ uint32_t s_count, s_bad;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int wk_count = 1 << cfg.wk_log, wk = warp & (wk_count - 1), wr = warp >> cfg.wk_log;
-    const int tile_rows_log = 7 - cfg.wk_log, tile_rows = 1 << tile_rows_log;  // kTile kWarps / wk
+    const int tile_rows_log = (MT == 2 ? 7 : 6) - cfg.wk_log, tile_rows = 1 << tile_rows_log;  // kTile kWarps / wk
     const int64_t j0 = static_cast<int64_t>(blockIdx.x) << tile_rows_log;      // the CTA's first row
     const bool by_id = p.ids != nullptr;
 
@@ -343,127 +423,128 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
 
     const int32_t row_len = static_cast<int32_t>((p.k + 1) / 2);
     const int32_t blocks = static_cast<int32_t>((p.k + 255) / 256);
-    // Blocks that can be read without a look at the row's end: whole ones (without VEC
-    // up to 4 bytes more).  The codes of the others, one or two, go to shared memory byte by
-    // byte, unless rows end on a multiple of 16 bytes (what is read past a row's end, or
-    // stands there, meets zeros of x).
-    const int32_t hi = static_cast<int32_t>(VEC ? p.k / 256 : (p.k - 8) / 256);
-    uint8_t *tails = smem + cfg.tails_at;  // [tile_rows][VEC ? 128 : 256]
-    constexpr int kTailPitch = VEC ? 128 : 256;
-    if (cfg.tails) {
+    const int32_t groups = static_cast<int32_t>(p.groups);
+    // The lane's rows are row + 8 h, h < kRows; those past the end are not read (their
+    // registers hold whatever they do) and not stored.
+    const int64_t row = j0 + wr * kTile + g;
+    const int left = row >= p.n ? 0 : static_cast<int>(min((p.n - row + 7) / 8, static_cast<int64_t>(kRows)));
+    const uint8_t *const codes = p.q + static_cast<int64_t>(expert) * p.expert_stride + row * p.ldq + 32 * c;
+    const int64_t cell = (static_cast<int64_t>(expert) * p.n + row) * p.groups;
+    const int lane_cell = G == 128 ? 0 : kCells * (c & 1);  // the lane's first group of a block
+
+    // kAnyhow: blocks that can be read without a look at the row's end are whole ones (and
+    // 4 bytes more where rows are not aligned).  The codes of the others, one or two, go to
+    // shared memory byte by byte (what stands there past a row's end meets zeros of x).
+    const int32_t hi = static_cast<int32_t>(cfg.aligned ? p.k / 256 : (p.k - 8) / 256);
+    uint8_t *tails = smem + cfg.tails_at;  // [tile_rows][256]
+    if (A == kAnyhow) {
         const int32_t len = row_len - hi * 128;
         for (int32_t u = tid; u < len << tile_rows_log; u += kThreads) {
             const int32_t r = u & (tile_rows - 1), b = u >> tile_rows_log;
             if (j0 + r < p.n)
-                tails[r * kTailPitch + b] =
+                tails[r * 256 + b] =
                     __ldg(p.q + static_cast<int64_t>(expert) * p.expert_stride + (j0 + r) * p.ldq + hi * 128 + b);
         }
         __syncthreads();
     }
-    // The warp's rows are row + 8 h, h < 4; those past the end are not read (their
-    // registers hold whatever they do) and not stored.
-    const int64_t row = j0 + wr * kTile + g;
-    const int left = row >= p.n ? 0 : static_cast<int>(min((p.n - row + 7) / 8, static_cast<int64_t>(4)));
-    const int lane_cell = G == 128 ? 0 : kCells * (c & 1);
-    const uint8_t *qat;  // this lane's 32 bytes of row `row` in the block that is fetched next
-    int64_t cell;        // its first scale there
-    int32_t ahead;       // that block
-    auto rewind = [&] {
-        ahead = wk;
-        qat = p.q + static_cast<int64_t>(expert) * p.expert_stride + row * p.ldq + wk * 128 + 32 * c;
-        cell = (static_cast<int64_t>(expert) * p.n + row) * p.groups + wk * Group<G>::kInBlock + lane_cell;
-    };
-    uint4 q[4][2];
-    uint2 s_raw[4];
-    uint32_t z_raw[4];
-    auto fetch_codes = [&] {
-        if (ahead < hi) {
+    int32_t b1 = 0;  // end of the slab: what lies past it is not fetched
+    auto fetch_codes = [&](int32_t block, uint4 (&q)[kRows][2]) {
+        if (A != kAnyhow) {
+            const bool in = block < b1 && block * 128 + 32 * c < row_len;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const uint8_t *at = qat + h * (8 * p.ldq);
+            for (int h = 0; h < kRows; ++h) load_stream32(in && h < left, codes + block * 128 + h * (8 * p.ldq), q[h]);
+        } else if (block < hi && block < b1) {
+#pragma unroll
+            for (int h = 0; h < kRows; ++h) {
+                const uint8_t *at = codes + static_cast<int64_t>(block) * 128 + h * (8 * p.ldq);
                 if (h < left) {
-                    if (!VEC) {
-                        q[h][0] = load_unaligned(at, p.q);
-                        q[h][1] = load_unaligned(at + 16, p.q);
-                    } else if (cfg.wide_q) {
-                        load_stream32(at, q[h][0], q[h][1]);
-                    } else {
-                        q[h][0] = ld_stream16(at);
-                        q[h][1] = ld_stream16(at + 16);
-                    }
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+                        q[h][v] = cfg.aligned ? ld_stream16(at + 16 * v) : load_unaligned(at + 16 * v, p.q);
                 }
             }
-        } else if (ahead < blocks) {
+        } else if (block < b1) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 0; h < kRows; ++h)
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    if (cfg.tails)
-                        q[h][v] = *reinterpret_cast<const uint4 *>(tails + (wr * kTile + g + 8 * h) * kTailPitch +
-                                                                   (ahead - hi) * 128 + 32 * c + 16 * v);
-                    else if (h < left && ahead * 128 + 32 * c + 16 * v < row_len)
-                        q[h][v] = ld_stream16(qat + h * (8 * p.ldq) + 16 * v);
-                }
+                for (int v = 0; v < 2; ++v)
+                    q[h][v] = *reinterpret_cast<const uint4 *>(tails + (wr * kTile + g + 8 * h) * 256 +
+                                                               (block - hi) * 128 + 32 * c + 16 * v);
+        }
+    };
+    // Raw scales and zero points of the lane's kCells groups of a block.  kAtOnce: s.x, s.y
+    // pairs of scales, z.x bytes.  kApart: s.x, s.y one scale each, z.x, z.y one byte each;
+    // with groups of 32, pairs.
+    uint2 s_raw[kRows], z_raw[kRows];
+    auto fetch_cells = [&](int32_t block) {
+        if (A == kAnyhow) return;
+        const int32_t group = block * Group<G>::kInBlock + lane_cell;
+        const bool have = group < groups, more = group + kCells / 2 < groups;
+#pragma unroll
+        for (int h = 0; h < kRows; ++h) {
+            const int64_t at = cell + group + h * (8 * p.groups);
+            const uint16_t *s = static_cast<const uint16_t *>(p.scales) + at;
+            const uint8_t *z = p.zeros + at;
+            const bool in = have && h < left, in2 = more && h < left, zin = in && p.zeros != nullptr,
+                       zin2 = in2 && p.zeros != nullptr;
+            if (A == kAtOnce && kCells == 4) {
+                s_raw[h] = load_cells64(in, s);
+                z_raw[h].x = load_cells32(zin, z);
+            } else if (A == kAtOnce) {
+                s_raw[h].x = load_cells32(in, s);
+                z_raw[h].x = load_cells16(zin, z);
+            } else if (kCells == 4) {
+                s_raw[h] = make_uint2(load_cells32(in, s), load_cells32(in2, s + 2));
+                z_raw[h] = make_uint2(load_cells16(zin, z), load_cells16(zin2, z + 2));
+            } else {
+                s_raw[h] = make_uint2(load_cells16(in, s), load_cells16(in2, s + 1));
+                z_raw[h] = make_uint2(load_cells8(zin, z), load_cells8(zin2, z + 1));
             }
         }
     };
-    auto fetch_cells = [&] {
-        if (ahead >= hi || !cfg.cells) return;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const int64_t at = cell + h * (8 * p.groups);
-            if (h < left) {
-                const uint16_t *s = static_cast<const uint16_t *>(p.scales) + at;
-                if (kCells == 4) s_raw[h] = __ldg(reinterpret_cast<const uint2 *>(s));
-                else s_raw[h].x = __ldg(reinterpret_cast<const uint32_t *>(s));
-                if (p.zeros != nullptr) {
-                    if (kCells == 4) z_raw[h] = __ldg(reinterpret_cast<const uint32_t *>(p.zeros + at));
-                    else z_raw[h] = __ldg(reinterpret_cast<const uint16_t *>(p.zeros + at));
-                }
-            }
-        }
-    };
-    // scales and negative zero points times scales of row h's groups `close` and `close` +
-    // kCloses of the block `block` that was fetched last
+    // scales, and scales times negative zero points, of row h's groups `close` and `close` +
+    // kCloses among the lane's of a block
     auto cells_of = [&](int32_t block, int h, int close, float (&s)[2], float (&sz)[2]) {
         float z[2] = {-8.f, -8.f};
-        if (block < hi && cfg.cells) {
-            // 16-bit cells 0, 1 | 2, 3; with groups of 32 close 0 takes 0 and 2, close 1 takes 1 and 3
-            const uint32_t a = kCells == 4 ? (close ? s_raw[h].x >> 16 : s_raw[h].x & 0xffffu) : s_raw[h].x & 0xffffu;
-            const uint32_t b = kCells == 4 ? (close ? s_raw[h].y >> 16 : s_raw[h].y & 0xffffu) : s_raw[h].x >> 16;
+        if (A != kAnyhow) {
+            uint32_t a, b, y, z1;
+            if (kCells == 4) {  // close 0 takes groups 0 and 2, close 1 takes 1 and 3
+                a = s_raw[h].x >> (16 * close) & 0xffffu;
+                b = s_raw[h].y >> (16 * close) & 0xffffu;
+                y = z_raw[h].x >> (8 * close) & 255u;
+                z1 = (A == kAtOnce ? z_raw[h].x >> (16 + 8 * close) : z_raw[h].y >> (8 * close)) & 255u;
+            } else {
+                a = A == kAtOnce ? s_raw[h].x & 0xffffu : s_raw[h].x;
+                b = A == kAtOnce ? s_raw[h].x >> 16 : s_raw[h].y;
+                y = A == kAtOnce ? z_raw[h].x & 255u : z_raw[h].x;
+                z1 = A == kAtOnce ? z_raw[h].x >> 8 : z_raw[h].y;
+            }
             s[0] = scale_value(a, p.scale_dtype);
             s[1] = scale_value(b, p.scale_dtype);
-            if (p.zeros != nullptr) {
-                z[0] = -static_cast<float>(z_raw[h] >> (8 * close) & 255u);
-                z[1] = -static_cast<float>(z_raw[h] >> (8 * (close + kCloses)) & 255u);
-            }
+            // 2^23 + byte, as f32
+            z[0] = p.zeros != nullptr ? 8388608.f - __uint_as_float(0x4b000000u | y) : -8.f;
+            z[1] = p.zeros != nullptr ? 8388608.f - __uint_as_float(0x4b000000u | z1) : -8.f;
         } else {
-            const int64_t at = (static_cast<int64_t>(expert) * p.n + row + 8 * h) * p.groups;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int64_t group = static_cast<int64_t>(block) * Group<G>::kInBlock + lane_cell + close + kCloses * i;
+                const int32_t group = block * Group<G>::kInBlock + lane_cell + close + kCloses * i;
+                const int64_t at = cell + group + h * (8 * p.groups);
                 s[i] = 0.f;
-                if (h < left && group < p.groups) {
-                    s[i] = scale_value(p.scale_dtype == kF32
-                                           ? __ldg(static_cast<const uint32_t *>(p.scales) + at + group)
-                                           : __ldg(static_cast<const uint16_t *>(p.scales) + at + group),
+                if (h < left && group < groups) {
+                    s[i] = scale_value(p.scale_dtype == kF32 ? __ldg(static_cast<const uint32_t *>(p.scales) + at)
+                                                             : __ldg(static_cast<const uint16_t *>(p.scales) + at),
                                        p.scale_dtype);
-                    if (p.zeros != nullptr) z[i] = -static_cast<float>(__ldg(p.zeros + at + group));
+                    if (p.zeros != nullptr) z[i] = -static_cast<float>(__ldg(p.zeros + at));
                 }
             }
         }
         sz[0] = s[0] * z[0];
         sz[1] = s[1] * z[1];
     };
-    auto advance = [&] {
-        ahead += wk_count;
-        qat += 128 << cfg.wk_log;
-        cell += Group<G>::kInBlock << cfg.wk_log;
-    };
-    rewind();
-    fetch_codes();
-    fetch_cells();
-    advance();
+    uint4 q[kRows][2];
+    b1 = min(cfg.slab << cfg.wk_log, blocks);
+    fetch_codes(wk, q);
+    fetch_cells(wk);
     // the zeros that lanes of another group read
     if (tid < kZeroBytes / 16) reinterpret_cast<uint4 *>(smem)[tid] = make_uint4(0u, 0u, 0u, 0u);
     uint8_t *stage = smem + kZeroBytes;
@@ -479,15 +560,9 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
     for (uint32_t t0 = first; t0 < count; t0 += stride) {
         const uint32_t tokens = min(count - t0, kPass);
         const uint32_t cols = tokens * kTerms * kParts;
-        if (t0 != first) {
-            rewind();
-            fetch_codes();
-            fetch_cells();
-            advance();
-        }
-        float acc[2][NT][4];
+        float acc[MT][NT][4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -500,10 +575,14 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
                 if (tid == 0) s_bad = 0u;
                 __syncthreads();
             }
-            const int32_t b1 = min(b0 + slab_blocks, blocks);
+            b1 = min(b0 + slab_blocks, blocks);
             stage_x<K, G, NT>(p, cfg, by_id ? s_ids : nullptr, t0, tokens, b0 * 256,
                               static_cast<uint32_t>(b1 - b0) * 32, pitch, stage, info, &s_bad);
             __syncthreads();
+            if (b0 != 0 || t0 != first) {
+                fetch_codes(wk + b0, q);
+                fetch_cells(wk + b0);
+            }
             // This lane's first word of the line of mma column 8 t + g, if its codes are of
             // that column's group.  Lanes past the last column repeat it; what they compute
             // is not stored.
@@ -520,57 +599,55 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
             const float4 *iat = reinterpret_cast<const float4 *>(info + wk * (kCloses * 8 * NT)) + c;
 #pragma unroll 1
             for (int32_t block = wk + b0; block < b1; block += wk_count) {
-                float part[2][NT][4];
+                float part[MT][NT][4];
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         constexpr uint32_t kEven = 0x000f000fu, kOdd = 0x00f000f0u;
-                        uint32_t u[4];
+                        uint32_t u[kRows];
 #pragma unroll
-                        for (int h = 0; h < 4; ++h)
-                            u[h] = i == 0 ? q[h][v].x : i == 1 ? q[h][v].y : i == 2 ? q[h][v].z : q[h][v].w;
+                        for (int h = 0; h < kRows; ++h)
+                            u[h] = i == 0   ? q[h][v].x
+                                   : i == 1 ? q[h][v].y
+                                   : i == 2 ? q[h][v].z
+                                            : q[h][v].w;
                         const bool opens = i == 0 && (v == 0 || kCloses == 2);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            {
-                                const uint4 b = *reinterpret_cast<const uint4 *>(xat[t] + 256 * v + 64 * i);
+                            const uint4 b = *reinterpret_cast<const uint4 *>(xat[t] + 256 * v + 64 * i);
 #pragma unroll
-                                for (int m = 0; m < 2; ++m) {
-                                    const uint32_t v0 = u[2 * m], v1 = u[2 * m + 1];
-                                    mma(part[m][t], opens, v0 & kEven, v1 & kEven, v0 & kOdd, v1 & kOdd, b.x, b.y);
-                                    mma(part[m][t], false, v0 >> 8 & kEven, v1 >> 8 & kEven, v0 >> 8 & kOdd,
-                                        v1 >> 8 & kOdd, b.z, b.w);
-                                }
+                            for (int m = 0; m < MT; ++m) {
+                                const uint32_t v0 = u[2 * m], v1 = u[2 * m + 1];
+                                mma(part[m][t], opens, v0 & kEven, v1 & kEven, v0 & kOdd, v1 & kOdd, b.x, b.y);
+                                mma(part[m][t], false, v0 >> 8 & kEven, v1 >> 8 & kEven, v0 >> 8 & kOdd,
+                                    v1 >> 8 & kOdd, b.z, b.w);
                             }
                         }
                     }
-                    if (v == 1) fetch_codes();
+                    if (v == 1) fetch_codes(block + wk_count, q);
                     if (v == 1 || kCloses == 2) {
                         const int close = kCloses == 2 ? v : 0;
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
+                        for (int m = 0; m < MT; ++m) {
                             float s[2][2], sz[2][2];  // [row][column's group]
                             cells_of(block, 2 * m, close, s[0], sz[0]);
                             cells_of(block, 2 * m + 1, close, s[1], sz[1]);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                {
-                                    const float4 f = iat[close * (4 * NT) + 4 * t];
+                                const float4 f = iat[close * (4 * NT) + 4 * t];
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const float factor = i & 1 ? f.z : f.x, sum = i & 1 ? f.w : f.y;
-                                        float &a = acc[m][t][i];
-                                        a = fmaf(s[i >> 1][i & 1] * factor, part[m][t][i], a);
-                                        a = fmaf(sz[i >> 1][i & 1], sum, a);
-                                    }
+                                for (int i = 0; i < 4; ++i) {
+                                    const float factor = i & 1 ? f.z : f.x, sum = i & 1 ? f.w : f.y;
+                                    float &a = acc[m][t][i];
+                                    a = fmaf(s[i >> 1][i & 1] * factor, part[m][t][i], a);
+                                    a = fmaf(sz[i >> 1][i & 1], sum, a);
                                 }
                             }
                         }
                     }
                 }
-                fetch_cells();
-                advance();
+                fetch_cells(block + wk_count);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) xat[t] += xstep[t];
                 iat += (kCloses * 4 * NT) << cfg.wk_log;
@@ -579,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
 
         // the warps that split the columns, and the terms and groups of a row, add up in order
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -606,12 +683,12 @@ __global__ void __launch_bounds__(kThreads, Budget<NT>::kCtas)
     }
 }
 
-template <Kind K, int G, bool VEC, int NT>
+template <Kind K, int G, Access A, int NT, int MT>
 cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     using T = typename XType<K>::type;
     constexpr int kTerms = K == kFloat ? 3 : 1;
     constexpr uint32_t kPass = 8 * NT / (kTerms * Group<G>::kParts);
-    constexpr int kCells = Group<G>::kCells;
+    constexpr int kTile = 16 * MT;
     const int64_t tiles = (p.n + kTile - 1) / kTile;
     const int64_t blocks = (p.k + 255) / 256;
     uint32_t gy, gz = 1;
@@ -625,60 +702,85 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     }
     if (gz > 65535u) return cudaErrorInvalidConfiguration;
     Launch cfg{};
+    // Warps that split the columns: enough for 16 warps an SM (8 where a pass takes more than
+    // one column tile, as the staging of its rows is repeated for each CTA), and no warp
+    // with more than 16 blocks, so that the last CTAs are short.  Measured: 8 a SM 11.4 us for
+    // 9.6 (dense, 1 row) and 23.7 for 18.8 (4 f32 tokens x 8 of 64 experts); 16 a SM with three
+    // column tiles 35 for 28.7 (8 f32 rows); without the second rule 111 for 100 (16 f32
+    // tokens x 8 of 128 experts, 16 blocks), with at most 8 blocks a warp 113.
     int wk = 1;
-    while (wk < kWarps && wk < blocks && tiles * gy * wk < 16LL * num_sms) wk *= 2, ++cfg.wk_log;
-    auto multiple = [](const void *ptr, int64_t a) { return reinterpret_cast<uintptr_t>(ptr) % a == 0; };
-    cfg.x_vec = multiple(p.x, 16) && p.ldx * sizeof(T) % 16 == 0 && p.x_slot_stride * sizeof(T) % 16 == 0;
-    cfg.wide_q = multiple(p.q, 32) && p.ldq % 32 == 0 && p.expert_stride % 32 == 0;
-    cfg.cells = p.scale_dtype != kF32 && p.groups % kCells == 0 && multiple(p.scales, 2 * kCells) &&
-                multiple(p.zeros, kCells);
-    cfg.tails = VEC ? (p.k + 1) / 2 % 16 != 0 : 1;
+    while (wk < kWarps && wk < blocks && (tiles * gy * wk < (NT == 1 ? 16LL : 8LL) * num_sms || blocks >= 16 * wk)) wk *= 2, ++cfg.wk_log;
+    cfg.x_vec = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx * sizeof(T) % 16 == 0 &&
+                p.x_slot_stride * sizeof(T) % 16 == 0;
+    cfg.aligned = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 16 == 0 && p.expert_stride % 16 == 0;
     const int lines = static_cast<int>(p.rows < kPass ? p.rows : kPass) * kTerms;
     const int64_t all = (blocks + wk - 1) / wk;
     const int per_block = wk * block_bytes(lines, NT, Group<G>::kCloses);
-    cfg.slab = (Budget<NT>::kStageBytes - lines * kPitchPad) / per_block;
+    cfg.slab = (Budget<NT, MT>::kStageBytes - lines * kPitchPad) / per_block;
     if (cfg.slab > all) cfg.slab = static_cast<int>(all);
     cfg.info_at = kZeroBytes + lines * (cfg.slab * wk * 512 + kPitchPad);
     cfg.tails_at = kZeroBytes + lines * kPitchPad + cfg.slab * per_block;
     const int64_t wr = kWarps / wk;
-    const int bytes = cfg.tails_at + (cfg.tails ? static_cast<int>(wr) * kTile * (VEC ? 128 : 256) : 0);
+    const int bytes = cfg.tails_at + (A == kAnyhow ? static_cast<int>(wr) * kTile * 256 : 0);
 
     static unsigned long long done = 0;  // devices on which the kernel may use its shared memory
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(done & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(q4_kernel<K, G, VEC, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   Budget<NT>::kStageBytes + kZeroBytes + kWarps * kTile * 256);
+        const cudaError_t e =
+            cudaFuncSetAttribute(q4_kernel<K, G, A, NT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Budget<NT, MT>::kStageBytes + kZeroBytes + kWarps * kTile * 256);
         if (e != cudaSuccess) return e;
         done |= bit;
     }
-    q4_kernel<K, G, VEC, NT><<<dim3(static_cast<unsigned>((tiles + wr - 1) / wr), gy, gz), kThreads, bytes, s>>>(p, cfg);
+    const dim3 grid(static_cast<unsigned>((tiles + wr - 1) / wr), gy, gz);
+    q4_kernel<K, G, A, NT, MT><<<grid, kThreads, bytes, s>>>(p, cfg);
     return cudaGetLastError();
 }
 
-// Column tiles: kNarrow for a few rows of x a matrix, kWide for more.  A pass takes 8
-// NT / (terms kParts) rows; more tiles cost registers and shared memory, so that fewer
-// warps are there to hide latency.  Per expert id the rows spread over the experts: on
-// average there are `share` rows for each one that occurs, and a second pass over the
-// few with more finds the weights in L2.
+template <Kind K, int G, int NT, int MT>
+cudaError_t launch_access(const Q4Params &p, int num_sms, cudaStream_t s) {
+    constexpr int kCells = Group<G>::kCells;
+    auto multiple = [](const void *ptr, int64_t a) { return reinterpret_cast<uintptr_t>(ptr) % a == 0; };
+    const bool even = multiple(p.q, 32) && p.ldq % 32 == 0 && p.expert_stride % 32 == 0 && p.k % 64 == 0 &&
+                      p.scale_dtype != kF32 && multiple(p.scales, kCells) && multiple(p.zeros, kCells / 2);
+    if (!even) return launch_nt<K, G, kAnyhow, NT, MT>(p, num_sms, s);
+    if (p.groups % kCells == 0 && multiple(p.scales, 2 * kCells) && multiple(p.zeros, kCells))
+        return launch_nt<K, G, kAtOnce, NT, MT>(p, num_sms, s);
+    return launch_nt<K, G, kApart, NT, MT>(p, num_sms, s);
+}
+
+// Column tiles: as few as hold the rows of x that a matrix meets, up to kWide.  A pass
+// takes 8 NT / (terms kParts) rows; more tiles cost registers and shared memory, so that
+// fewer warps are there to hide latency.  Per expert id the rows spread over the experts:
+// on average there are `share` rows for each one that occurs, and a second pass over the
+// few with more finds the weights in L2 (16 tokens x 8 of 128 experts with groups of 32:
+// 84 us with one tile, 91 with two).  A matrix of few rows of f16 or bf16 is cut into row
+// tiles of 16, so that every SM has several warps a scheduler (4096 x 11008, 1 row: 17.1 us
+// for 18.9; 64 experts' worth of rows and more: 94 for 84, hence the limit).  f32 has three
+// times the staging for each row tile and always takes 32 (11008 x 4096: 10.5 for 11.2).
 template <Kind K, int G>
 cudaError_t launch_g(const Q4Params &p, int num_sms, cudaStream_t s) {
-    constexpr int kTerms = K == kFloat ? 3 : 1;
-    constexpr int kColumns = kTerms * Group<G>::kParts;
+    constexpr int kColumns = (K == kFloat ? 3 : 1) * Group<G>::kParts;
     constexpr int kNarrow = (kColumns + 7) / 8;
     constexpr int kWide = K == kFloat ? 3 : G == 128 ? 2 : 4;
-    const bool vec = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 16 == 0 && p.expert_stride % 16 == 0;
     const uint32_t distinct = p.rows < p.n_experts ? p.rows : p.n_experts;
     const uint32_t share = p.ids != nullptr ? (p.rows + distinct - 1) / distinct : p.rows;
-    if (!vec) return launch_nt<K, G, false, kWide>(p, num_sms, s);
-    return share * kColumns > 8 * kNarrow ? launch_nt<K, G, true, kWide>(p, num_sms, s)
-                                          : launch_nt<K, G, true, kNarrow>(p, num_sms, s);
+    if (share * kColumns <= 8 * kNarrow) {
+        if constexpr (K != kFloat) {
+            if ((p.n + 31) / 32 * (p.ids != nullptr ? distinct : 1) < 4LL * num_sms) return launch_access<K, G, kNarrow, 1>(p, num_sms, s);
+        }
+        return launch_access<K, G, kNarrow, 2>(p, num_sms, s);
+    }
+    if (share * kColumns <= 8 * (kNarrow + 1)) return launch_access<K, G, kNarrow + 1, 2>(p, num_sms, s);
+    return launch_access<K, G, kWide, 2>(p, num_sms, s);
 }
 
 template <Kind K>
 cudaError_t launch(const Q4Params &p, int num_sms, cudaStream_t s) {
-    if (p.k == 0) return launch_fill_zero(K == kFloat ? kF32 : K == kHalf ? kF16 : kBF16, p.out, 1, p.rows, p.n, p.ldo, 0, s);
+    constexpr int dt = K == kFloat ? kF32 : K == kHalf ? kF16 : kBF16;
+    if (p.k == 0) return launch_fill_zero(dt, p.out, 1, p.rows, p.n, p.ldo, 0, s);
     if (p.group == 128) return launch_g<K, 128>(p, num_sms, s);
     if (p.group == 64) return launch_g<K, 64>(p, num_sms, s);
     return launch_g<K, 32>(p, num_sms, s);

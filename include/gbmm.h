@@ -476,18 +476,23 @@ GBMM_API gbmm_status gbmm_moe_combine_backward(gbmm_dtype dt, uint32_t m, uint32
  *   W[j,x] = (q[j,x] - z[j,g]) * scale[j,g],  g = x / group,  j < n, x < k
  * q: row j starts at byte j*ldq_bytes; byte i of a row holds column 2i in its low
  *   and column 2i+1 in its high four bits (ldq_bytes >= (k+1)/2; the unused half
- *   of the last byte of an odd k is ignored).  Rows 16 bytes apart in a 16-byte
- *   aligned matrix are read fastest; every other alignment works.
+ *   of the last byte of an odd k is ignored).  Read fastest: a k that is a multiple
+ *   of 64, matrices and rows that start on multiples of 32 bytes, and 16-bit scales;
+ *   every other alignment works.
  * group: 32, 64 or 128 columns; the last one may be ragged.  G = ceil(k/group).
  * scales: [n, G] tight, scale_dt f32, f16 or bf16.  zeros: u8 [n, G] tight, values
  *   0..255, or NULL for 8 everywhere.
- * Every weight value enters the product exactly, x in its own precision (f32
- * included); products accumulate in f32, and each result is rounded once.
+ * Codes and zero points enter exactly.  The values of x do too, f32 included, except
+ * that one far below the largest magnitude of its group of columns (2^25 for f16, 2^28
+ * for bf16, 2^12 for f32) may be off by up to 2^-35 of that magnitude.  A row with an
+ * infinity, a NaN or a magnitude from 2^117 up is computed in plain f32, slower.
+ * Products accumulate in f32, and each result is rounded once.
  */
 
 /* gbmm_gemv_q4 -- y[i,j] = sum_x x[i,x] * W[j,x] for i < m.  x [m, k] and y
  * [m, n] of type dt, rows ldx / ldy elements apart.  Any m: the weights are read
- * once for each block of up to 8 rows, so it is meant for few of them.  m or
+ * once for each block of up to 8 rows (f32: 4 with groups of 128, else 2), so it is
+ * meant for few of them.  m or
  * n == 0 is a no-op, k == 0 writes zeros. */
 GBMM_API gbmm_status gbmm_gemv_q4(gbmm_dtype dt, uint32_t m, int64_t n, int64_t k, uint32_t group,
                                   const void *q, int64_t ldq_bytes, const void *scales,
@@ -499,7 +504,8 @@ GBMM_API gbmm_status gbmm_gemv_q4(gbmm_dtype dt, uint32_t m, int64_t n, int64_t 
  * starts at byte e*expert_stride_bytes, its scales and zeros at element e*n*G.
  * input_layout GBMM_INPUT_*: x is [m, k] or [m, top_k, k], out [m, top_k, n], both
  * tight and of type dt.  Each distinct expert among 1024 consecutive routed rows
- * is read once for each block of up to 8 of its rows.  m or n == 0 is a no-op,
+ * is read once for each block of up to 8 of its rows (fewer where a row more
+ * would cost the rest more; the second block finds the weights in L2).  m or n == 0 is a no-op,
  * k == 0 writes zeros. */
 GBMM_API gbmm_status gbmm_matmul_id_q4(gbmm_dtype dt, uint32_t m, int64_t n, int64_t k, uint32_t top_k,
                                        uint32_t n_experts, uint32_t input_layout, uint32_t group,
