@@ -195,6 +195,23 @@ def test_route_masked_experts_and_empty_rows(dtype, selected):
     check_route(logits, dtype, 5, selected, bias=bias)
 
 
+@pytest.mark.parametrize("dtype,E,top_k,selected", [("f32", 128, 8, False), ("f32", 6, 3, True), ("bf16", 64, 1, False),
+                                                    ("f16", 101, 7, True), ("bf16", 200, 8, False)])
+def test_route_many_tokens(dtype, E, top_k, selected):
+    """A batch from which a warp takes several tokens, the last warp fewer; equal,
+    masked and empty rows lie among the others."""
+    rng = np.random.default_rng(E)
+    m = 64 * torch.cuda.get_device_properties(0).multi_processor_count + 3
+    logits = rng.standard_normal((m, E))
+    logits[1::9] = rng.integers(-1, 2, logits[1::9].shape)
+    logits[2::9] = -np.inf
+    logits[3::9, top_k // 2:] = -np.inf
+    logits[4::9, ::2] = np.nan
+    bias = rng.standard_normal(E).astype(np.float32)
+    bias[E // 2] = -np.inf
+    check_route(logits, dtype, top_k, selected, bias=bias if E != 128 else None, ld=E + E % 4)
+
+
 def test_route_infinite_live_logit_gives_nan_weights():
     logits = np.zeros((1, 8))
     logits[0, 3] = np.inf
