@@ -41,11 +41,11 @@
 // alignment they need is settled at the launch (Access).
 //
 // Measured (us, and GB/s of codes, scales, zeros, x and y; inputs rotate past L2):
-//   dense 11008 x 4096, groups of 128, 1 row     f16 9.6 (2410)   f32 10.5 (2220)
-//   the same, 4 f16 rows 16.1, 16 f16 rows 28.4, 8 f32 rows 28.7
-//   4 bf16 tokens x 8 of 64 experts, 1408 x 2048     14.5 (2880)
-//   16 tokens x 8 of 128 experts, 1536 x 4096: bf16, groups of 32 with zeros 84 (3660);
-//   bf16, groups of 128 70.9 (3850); f32, groups of 128 100 (2730)
+//   dense 11008 x 4096, groups of 128, 1 row     f16 9.5 (2440)   f32 10.4 (2250)
+//   the same, 4 f16 rows 13.0, 16 f16 rows 25.7, 8 f32 rows 28.2
+//   4 bf16 tokens x 8 of 64 experts, 1408 x 2048     14.1 (2960)
+//   16 tokens x 8 of 128 experts, 1536 x 4096: bf16, groups of 32 with zeros 79.3 (3870);
+//   bf16, groups of 128 63.5 (4300); f32, groups of 128 98.4 (2780)
 // The large ones issue in 53 % of the cycles, half of it the ANDs and shifts that unpack the
 // codes, and wait as often for HBM as for results of the instructions before; the small
 // ones are over before HBM is at its rate.  On the way (the case with groups of 32): 16
@@ -60,20 +60,9 @@
 namespace gbmm {
 namespace q4 {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kWindow = 1024;  // routed rows that a CTA searches for its expert's
 constexpr uint32_t kFull = 0xffffffffu;
 
-// NT column tiles of 8, MT row tiles of 16 a warp: CTAs an SM, and the shared memory for
-// a slab of x, which holds two blocks for each of kWarps warps at least.  One row tile with
-// four CTAs in place of five: 13.1 us for 9.6 (dense, 1 row); two tiles with five in place
-// of four: 22.1 for 18.8 (4 f32 tokens x 8 of 64 experts); three and more column tiles with
-// two in place of three: 42 for 29 (dense, 8 bf16 rows, groups of 64).
-template <int NT, int MT> struct Budget {
-    static constexpr int kCtas = MT == 1 ? (NT == 1 ? 5 : 4) : NT == 1 ? 4 : 3;
-    static constexpr int kStageBytes = NT == 1 ? 32 * 1024 : NT == 2 ? 44 * 1024 : 60 * 1024;
-};
 // mma columns that a row of x takes; how often a block's sums are closed
 template <int G> struct Group {
     static constexpr int kParts = G == 128 ? 2 : 4;
@@ -83,6 +72,19 @@ template <int G> struct Group {
 };
 
 enum Kind { kHalf, kBfloat, kFloat };  // type of x
+
+// NT column tiles of 8, MT row tiles of 16 a warp: warps a CTA, CTAs an SM, and the shared
+// memory for a slab of x, which holds two blocks for each warp at least.
+// Eight warps share the staging of x: 4 f16 rows x 11008 x 4096 13.3 us for 16.0 with four,
+// 1 row x 4096 x 11008 12.2 for 16.2.  f32, which needs the registers, and three and more column tiles
+// take four (8 f32 rows 28.7 for 44.3 with eight, 8 bf16 rows with groups of 64 27.3 for 29.3).
+template <Kind K, int NT, int MT> struct Budget {
+    static constexpr int kWarps = K != kFloat && NT <= 2 ? 8 : 4;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kCtas = kWarps == 8 ? (MT == 1 && NT == 1 ? 3 : 2) : NT == 1 ? 4 : 3;
+    static constexpr int kStageBytes =
+        kWarps == 8 ? (NT == 1 ? 48 * 1024 : 80 * 1024) : NT == 1 ? 32 * 1024 : NT == 2 ? 44 * 1024 : 60 * 1024;
+};
 
 template <Kind K> struct XType;
 template <> struct XType<kHalf> { using type = __half; };
@@ -154,7 +156,7 @@ __device__ __forceinline__ uint32_t word_offset(uint32_t w) {
 // The window's expert that this CTA serves: the d-th distinct one of its ids.
 // Returns false if there are fewer.  Leaves the window's ids in s_ids; zeroes the CTA's
 // outputs of rows without an expert.
-template <typename T>
+template <typename T, int kThreads>
 __device__ __forceinline__ bool find_expert(const Q4Params &p, uint32_t base_row, uint32_t d, int64_t j0, int tile_rows,
                                             uint32_t *s_ids, uint32_t *s_bits, uint32_t &expert) {
     const int tid = threadIdx.x, lane = tid & 31;
@@ -218,7 +220,7 @@ __device__ __forceinline__ uint32_t list_rows(const Q4Params &p, uint32_t base_r
 // pitch, and for each block (half a block with groups of 32) and mma column {factor, sum}:
 // what undoes the scalings, and the group's sum of x (of its first term's column only).
 // Rows with a group that cannot be scaled are marked in *bad.
-template <Kind K, int G, int NT>
+template <Kind K, int G, int NT, int kThreads>
 __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, const uint32_t *list, uint32_t t0,
                                         uint32_t tokens, int32_t k0, uint32_t words, uint32_t pitch, uint8_t *stage,
                                         float2 *info, uint32_t *bad) {
@@ -389,16 +391,17 @@ __device__ __forceinline__ uint32_t load_cells8(bool pred, const void *p) {
 
 // How a kernel reads codes, scales and zero points.
 //   kAnyhow  any alignment and scale type; a look at every access
-//   kApart   packed rows start and end on multiples of 32 bytes, 16-bit scales; the
-//            scales of a lane one by one (groups of 32: two by two)
+//   kApart   packed rows start and end on multiples of 32 bytes, 16-bit scales, enough rows for
+//            a warp; the scales of a lane one by one (groups of 32: two by two)
 //   kAtOnce  and the scales of a lane, and its zero points, can be read at once
 enum Access { kAnyhow, kApart, kAtOnce };
 
 // G: columns of a group.  NT: mma column tiles, 8 NT / (terms kParts) rows of x a pass.
 // MT: mma row tiles of a warp.
 template <Kind K, int G, Access A, int NT, int MT>
-__global__ void __launch_bounds__(kThreads, Budget<NT, MT>::kCtas)
+__global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>::kCtas)
     q4_kernel(const __grid_constant__ Q4Params p, const __grid_constant__ Launch cfg) {
+    constexpr int kWarps = Budget<K, NT, MT>::kWarps, kThreads = Budget<K, NT, MT>::kThreads;
     using T = typename XType<K>::type;
     constexpr int kTerms = K == kFloat ? 3 : 1;
     constexpr int kParts = Group<G>::kParts, kCloses = Group<G>::kCloses, kCells = Group<G>::kCells;
@@ -413,21 +416,24 @@ __global__ void __launch_bounds__(kThreads, Budget<NT, MT>::kCtas)
     __shared__ uint32_t s_count, s_bad;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int wk_count = 1 << cfg.wk_log, wk = warp & (wk_count - 1), wr = warp >> cfg.wk_log;
-    const int tile_rows_log = (MT == 2 ? 7 : 6) - cfg.wk_log, tile_rows = 1 << tile_rows_log;  // kTile kWarps / wk
+    const int tile_rows_log = (MT == 2 ? 5 : 4) + (kWarps == 8 ? 3 : 2) - cfg.wk_log;
+    const int tile_rows = 1 << tile_rows_log;  // kTile kWarps / wk
     const int64_t j0 = static_cast<int64_t>(blockIdx.x) << tile_rows_log;      // the CTA's first row
     const bool by_id = p.ids != nullptr;
 
     uint32_t expert = 0;
     const uint32_t base_row = blockIdx.z * kWindow;
-    if (by_id && !find_expert<T>(p, base_row, blockIdx.y, j0, tile_rows, s_ids, s_bits, expert)) return;
+    if (by_id && !find_expert<T, kThreads>(p, base_row, blockIdx.y, j0, tile_rows, s_ids, s_bits, expert)) return;
 
     const int32_t row_len = static_cast<int32_t>((p.k + 1) / 2);
     const int32_t blocks = static_cast<int32_t>((p.k + 255) / 256);
     const int32_t groups = static_cast<int32_t>(p.groups);
-    // The lane's rows are row + 8 h, h < kRows; those past the end are not read (their
+    // The lane's rows are row + 8 h, h < kRows.  A tile that would pass the end starts earlier
+    // and computes some rows of the one before again; kAnyhow: rows past the end are not read (their
     // registers hold whatever they do) and not stored.
-    const int64_t row = j0 + wr * kTile + g;
-    const int left = row >= p.n ? 0 : static_cast<int>(min((p.n - row + 7) / 8, static_cast<int64_t>(kRows)));
+    const int64_t start = j0 + wr * kTile, row = (A == kAnyhow ? start : min(start, p.n - kTile)) + g;
+    const int left =
+        A != kAnyhow ? kRows : row >= p.n ? 0 : static_cast<int>(min((p.n - row + 7) / 8, static_cast<int64_t>(kRows)));
     const uint8_t *const codes = p.q + static_cast<int64_t>(expert) * p.expert_stride + row * p.ldq + 32 * c;
     const int64_t cell = (static_cast<int64_t>(expert) * p.n + row) * p.groups;
     const int lane_cell = G == 128 ? 0 : kCells * (c & 1);  // the lane's first group of a block
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, Budget<NT, MT>::kCtas)
         if (A != kAnyhow) {
             const bool in = block < b1 && block * 128 + 32 * c < row_len;
 #pragma unroll
-            for (int h = 0; h < kRows; ++h) load_stream32(in && h < left, codes + block * 128 + h * (8 * p.ldq), q[h]);
+            for (int h = 0; h < kRows; ++h) load_stream32(in, codes + block * 128 + h * (8 * p.ldq), q[h]);
         } else if (block < hi && block < b1) {
 #pragma unroll
             for (int h = 0; h < kRows; ++h) {
@@ -480,25 +486,24 @@ __global__ void __launch_bounds__(kThreads, Budget<NT, MT>::kCtas)
         if (A == kAnyhow) return;
         const int32_t group = block * Group<G>::kInBlock + lane_cell;
         const bool have = group < groups, more = group + kCells / 2 < groups;
+        const bool zhave = have && p.zeros != nullptr, zmore = more && p.zeros != nullptr;
 #pragma unroll
         for (int h = 0; h < kRows; ++h) {
             const int64_t at = cell + group + h * (8 * p.groups);
             const uint16_t *s = static_cast<const uint16_t *>(p.scales) + at;
             const uint8_t *z = p.zeros + at;
-            const bool in = have && h < left, in2 = more && h < left, zin = in && p.zeros != nullptr,
-                       zin2 = in2 && p.zeros != nullptr;
             if (A == kAtOnce && kCells == 4) {
-                s_raw[h] = load_cells64(in, s);
-                z_raw[h].x = load_cells32(zin, z);
+                s_raw[h] = load_cells64(have, s);
+                z_raw[h].x = load_cells32(zhave, z);
             } else if (A == kAtOnce) {
-                s_raw[h].x = load_cells32(in, s);
-                z_raw[h].x = load_cells16(zin, z);
+                s_raw[h].x = load_cells32(have, s);
+                z_raw[h].x = load_cells16(zhave, z);
             } else if (kCells == 4) {
-                s_raw[h] = make_uint2(load_cells32(in, s), load_cells32(in2, s + 2));
-                z_raw[h] = make_uint2(load_cells16(zin, z), load_cells16(zin2, z + 2));
+                s_raw[h] = make_uint2(load_cells32(have, s), load_cells32(more, s + 2));
+                z_raw[h] = make_uint2(load_cells16(zhave, z), load_cells16(zmore, z + 2));
             } else {
-                s_raw[h] = make_uint2(load_cells16(in, s), load_cells16(in2, s + 1));
-                z_raw[h] = make_uint2(load_cells8(zin, z), load_cells8(zin2, z + 1));
+                s_raw[h] = make_uint2(load_cells16(have, s), load_cells16(more, s + 1));
+                z_raw[h] = make_uint2(load_cells8(zhave, z), load_cells8(zmore, z + 1));
             }
         }
     };
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, Budget<NT, MT>::kCtas)
                 __syncthreads();
             }
             b1 = min(b0 + slab_blocks, blocks);
-            stage_x<K, G, NT>(p, cfg, by_id ? s_ids : nullptr, t0, tokens, b0 * 256,
+            stage_x<K, G, NT, kThreads>(p, cfg, by_id ? s_ids : nullptr, t0, tokens, b0 * 256,
                               static_cast<uint32_t>(b1 - b0) * 32, pitch, stage, info, &s_bad);
             __syncthreads();
             if (b0 != 0 || t0 != first) {
@@ -666,11 +671,15 @@ __global__ void __launch_bounds__(kThreads, Budget<NT, MT>::kCtas)
         const uint32_t bad = s_bad;
         for (uint32_t u = tid; u < tokens << tile_rows_log; u += kThreads) {
             const uint32_t jj = u & (tile_rows - 1), tok = u >> tile_rows_log;
-            if (j0 + jj >= p.n) continue;
+            int64_t j = j0 + jj;
+            if (A != kAnyhow)
+                j = min(j0 + jj / kTile * kTile, p.n - kTile) + jj % kTile;
+            else if (j >= p.n)
+                continue;
             const uint32_t r = by_id ? s_ids[t0 + tok] : t0 + tok;
             float sum = 0.f;
             if (bad >> tok & 1u) {
-                sum = plain_output<T>(p, expert, j0 + jj, r);
+                sum = plain_output<T>(p, expert, j, r);
             } else {
                 for (int w = 0; w < wk_count; ++w) {
 #pragma unroll
@@ -678,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, Budget<NT, MT>::kCtas)
                         sum += red[((jj / kTile) << cfg.wk_log) + w][jj % kTile][tok * (kTerms * kParts) + i];
                 }
             }
-            static_cast<T *>(p.out)[static_cast<int64_t>(r) * p.ldo + j0 + jj] = Elem<T>::from_f(sum);
+            static_cast<T *>(p.out)[static_cast<int64_t>(r) * p.ldo + j] = Elem<T>::from_f(sum);
         }
     }
 }
@@ -688,7 +697,8 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     using T = typename XType<K>::type;
     constexpr int kTerms = K == kFloat ? 3 : 1;
     constexpr uint32_t kPass = 8 * NT / (kTerms * Group<G>::kParts);
-    constexpr int kTile = 16 * MT;
+    using B = Budget<K, NT, MT>;
+    constexpr int kTile = 16 * MT, kWarps = B::kWarps;
     const int64_t tiles = (p.n + kTile - 1) / kTile;
     const int64_t blocks = (p.k + 255) / 256;
     uint32_t gy, gz = 1;
@@ -716,7 +726,7 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     const int lines = static_cast<int>(p.rows < kPass ? p.rows : kPass) * kTerms;
     const int64_t all = (blocks + wk - 1) / wk;
     const int per_block = wk * block_bytes(lines, NT, Group<G>::kCloses);
-    cfg.slab = (Budget<NT, MT>::kStageBytes - lines * kPitchPad) / per_block;
+    cfg.slab = (B::kStageBytes - lines * kPitchPad) / per_block;
     if (cfg.slab > all) cfg.slab = static_cast<int>(all);
     cfg.info_at = kZeroBytes + lines * (cfg.slab * wk * 512 + kPitchPad);
     cfg.tails_at = kZeroBytes + lines * kPitchPad + cfg.slab * per_block;
@@ -730,12 +740,12 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     if (!(done & bit)) {
         const cudaError_t e =
             cudaFuncSetAttribute(q4_kernel<K, G, A, NT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Budget<NT, MT>::kStageBytes + kZeroBytes + kWarps * kTile * 256);
+                                 B::kStageBytes + kZeroBytes + kWarps * kTile * 256);
         if (e != cudaSuccess) return e;
         done |= bit;
     }
     const dim3 grid(static_cast<unsigned>((tiles + wr - 1) / wr), gy, gz);
-    q4_kernel<K, G, A, NT, MT><<<grid, kThreads, bytes, s>>>(p, cfg);
+    q4_kernel<K, G, A, NT, MT><<<grid, B::kThreads, bytes, s>>>(p, cfg);
     return cudaGetLastError();
 }
 
@@ -744,7 +754,8 @@ cudaError_t launch_access(const Q4Params &p, int num_sms, cudaStream_t s) {
     constexpr int kCells = Group<G>::kCells;
     auto multiple = [](const void *ptr, int64_t a) { return reinterpret_cast<uintptr_t>(ptr) % a == 0; };
     const bool even = multiple(p.q, 32) && p.ldq % 32 == 0 && p.expert_stride % 32 == 0 && p.k % 64 == 0 &&
-                      p.scale_dtype != kF32 && multiple(p.scales, kCells) && multiple(p.zeros, kCells / 2);
+                      p.scale_dtype != kF32 && multiple(p.scales, kCells) && multiple(p.zeros, kCells / 2) &&
+                      p.n >= 16 * MT;
     if (!even) return launch_nt<K, G, kAnyhow, NT, MT>(p, num_sms, s);
     if (p.groups % kCells == 0 && multiple(p.scales, 2 * kCells) && multiple(p.zeros, kCells))
         return launch_nt<K, G, kAtOnce, NT, MT>(p, num_sms, s);
