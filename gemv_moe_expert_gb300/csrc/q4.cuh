@@ -43,16 +43,18 @@
 // Measured (us, and GB/s of codes, scales, zeros, x and y; inputs rotate past L2):
 //   dense 11008 x 4096, groups of 128, 1 row     f16 9.5 (2440)   f32 10.4 (2250)
 //   the same, 4 f16 rows 13.0, 16 f16 rows 25.7, 8 f32 rows 28.2
-//   4 bf16 tokens x 8 of 64 experts, 1408 x 2048     14.1 (2960)
+//   4 tokens x 8 of 64 experts, 1408 x 2048      bf16 14.0 (2970)   f32 18.3 (2290)
 //   16 tokens x 8 of 128 experts, 1536 x 4096: bf16, groups of 32 with zeros 79.3 (3870);
-//   bf16, groups of 128 63.5 (4300); f32, groups of 128 98.4 (2780)
-// The large ones issue in 53 % of the cycles, half of it the ANDs and shifts that unpack the
-// codes, and wait as often for HBM as for results of the instructions before; the small
+//   bf16, groups of 128 62.6 (4360); f32, groups of 128 96.8 (2830)
+// The large ones issue in more than half of the cycles, half of it the ANDs and shifts that
+// unpack the codes, and a warp waits as often for HBM as for the instructions before; the
+// last case but one takes 56.6 when x is not staged, 53.7 when nothing is multiplied.  The small
 // ones are over before HBM is at its rate.  On the way (the case with groups of 32): 16
 // rows a warp and 16-byte loads of half lines 151, bound by the L1 data path; a ring of
 // shared-memory slots filled by bulk copies of 256-byte row pieces 206; the next block held
 // in a second set of registers 91, as it leaves room for fewer instructions in flight; CTAs that
-// walk over several row tiles 172.
+// walk over several row tiles 172; lines fetched to L2 three blocks ahead 88 for 84; a cluster of
+// four CTAs that stage a quarter of x each and copy the rest from each other 89 for 79.
 #pragma once
 
 #include "device_common.cuh"
@@ -215,15 +217,14 @@ __device__ __forceinline__ uint32_t list_rows(const Q4Params &p, uint32_t base_r
     return *s_count;
 }
 
-// x of `tokens` rows (routed rows list[t0 ..], or rows t0 .. without a list),
-// columns k0 .. k0 + 8 words - 1, into shared memory: f16 terms at stage + line *
-// pitch, and for each block (half a block with groups of 32) and mma column {factor, sum}:
+// x of `tokens` rows, which start at offsets[] (in elements), columns k0 .. k0 + 8
+// words - 1, into shared memory: f16 terms at stage + line * pitch, and for each block (half a block with groups of 32) and mma column {factor, sum}:
 // what undoes the scalings, and the group's sum of x (of its first term's column only).
 // Rows with a group that cannot be scaled are marked in *bad.
 template <Kind K, int G, int NT, int kThreads>
-__device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, const uint32_t *list, uint32_t t0,
-                                        uint32_t tokens, int32_t k0, uint32_t words, uint32_t pitch, uint8_t *stage,
-                                        float2 *info, uint32_t *bad) {
+__device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, const int64_t *offsets, uint32_t tokens,
+                                        int32_t k0, uint32_t words, uint32_t pitch, uint8_t *stage, float2 *info,
+                                        uint32_t *bad) {
     using T = typename XType<K>::type;
     constexpr int kTerms = K == kFloat ? 3 : 1;
     constexpr int kLanes = G / 8;  // that share a group
@@ -242,15 +243,9 @@ __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, co
             }
             toks[a] = tok;
             ws[a] = w;
-            if (tok < tokens) {
-                uint32_t r = t0 + tok, slot = 0;
-                if (list != nullptr) {
-                    slot = list[r] % p.top_k;
-                    r = list[r] / p.top_k;
-                }
-                const T *x = static_cast<const T *>(p.x) + static_cast<int64_t>(r) * p.ldx + slot * p.x_slot_stride;
-                x8[a].load(x, static_cast<int64_t>(k0) + 8 * w, p.k, cfg.x_vec != 0);
-            }
+            if (tok < tokens)
+                x8[a].load(static_cast<const T *>(p.x) + offsets[tok], k0 + 8 * static_cast<int64_t>(w), p.k,
+                           cfg.x_vec != 0);
             w += kThreads;
         }
 #pragma unroll
@@ -414,6 +409,7 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
     __shared__ uint32_t s_ids[kWindow];
     __shared__ uint32_t s_bits[32];
     __shared__ uint32_t s_count, s_bad;
+    __shared__ int64_t s_x[kPass];  // where the rows of x of a pass start
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int wk_count = 1 << cfg.wk_log, wk = warp & (wk_count - 1), wr = warp >> cfg.wk_log;
     const int tile_rows_log = (MT == 2 ? 5 : 4) + (kWarps == 8 ? 3 : 2) - cfg.wk_log;
@@ -578,10 +574,14 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
             __syncthreads();  // the slab before, or the pass before, is done with
             if (b0 == 0) {
                 if (tid == 0) s_bad = 0u;
+                if (tid < tokens) {
+                    const uint32_t r = by_id ? s_ids[t0 + tid] : t0 + tid, t = r / p.top_k;
+                    s_x[tid] = t * p.ldx + (r - t * p.top_k) * p.x_slot_stride;
+                }
                 __syncthreads();
             }
             b1 = min(b0 + slab_blocks, blocks);
-            stage_x<K, G, NT, kThreads>(p, cfg, by_id ? s_ids : nullptr, t0, tokens, b0 * 256,
+            stage_x<K, G, NT, kThreads>(p, cfg, s_x, tokens, b0 * 256,
                               static_cast<uint32_t>(b1 - b0) * 32, pitch, stage, info, &s_bad);
             __syncthreads();
             if (b0 != 0 || t0 != first) {
