@@ -36,7 +36,7 @@
 // A warp takes 32 rows, so that what it reads of x serves two mma row tiles.  A CTA
 // has kWarps warps: wk of them split the columns (blocks, one after the other) of the
 // same rows, and kWarps / wk take different rows.  A warp's first block is loaded before x
-// is staged, each next one as soon as the one before has been used: sixteen to twenty
+// is staged, each next one as soon as the one before has been used: twelve to twenty-four
 // warps an SM hide the latency.  Loads are predicated, not branched around, and the
 // alignment they need is settled at the launch (Access).
 //
@@ -77,9 +77,11 @@ enum Kind { kHalf, kBfloat, kFloat };  // type of x
 
 // NT column tiles of 8, MT row tiles of 16 a warp: warps a CTA, CTAs an SM, and the shared
 // memory for a slab of x, which holds two blocks for each warp at least.
-// Eight warps share the staging of x: 4 f16 rows x 11008 x 4096 13.3 us for 16.0 with four,
-// 1 row x 4096 x 11008 12.2 for 16.2.  f32, which needs the registers, and three and more column tiles
-// take four (8 f32 rows 28.7 for 44.3 with eight, 8 bf16 rows with groups of 64 27.3 for 29.3).
+// Eight warps share the staging of x: 4 f16 rows x 11008 x 4096 13.0 us for 15.7 with four,
+// 1 row x 4096 x 11008 11.9 for 16.2, 16 bf16 tokens x 8 of 128 experts 62.5 for 67.9 (groups of
+// 32 with zeros the same, dense 1 row 11.4 for 10.9).  f32, which needs the registers, and three
+// and more column tiles take four (8 f32 rows 28.4 for 44.3 with eight, 8 bf16 rows with
+// groups of 64 26.8 for 29.3).
 template <Kind K, int NT, int MT> struct Budget {
     static constexpr int kWarps = K != kFloat && NT <= 2 ? 8 : 4;
     static constexpr int kThreads = 32 * kWarps;
@@ -217,10 +219,11 @@ __device__ __forceinline__ uint32_t list_rows(const Q4Params &p, uint32_t base_r
     return *s_count;
 }
 
-// x of `tokens` rows, which start at offsets[] (in elements), columns k0 .. k0 + 8
-// words - 1, into shared memory: f16 terms at stage + line * pitch, and for each block (half a block with groups of 32) and mma column {factor, sum}:
-// what undoes the scalings, and the group's sum of x (of its first term's column only).
-// Rows with a group that cannot be scaled are marked in *bad.
+// x of `tokens` rows, which start at offsets[] (in elements), columns k0 .. k0 + 8 words
+// - 1, into shared memory: f16 terms at stage + line * pitch, and for each block (half a
+// block with groups of 32) and mma column {factor, sum}: what undoes the scalings, and the
+// group's sum of x (of its first term's column only).  Rows with a group that cannot be
+// scaled are marked in *bad.
 template <Kind K, int G, int NT, int kThreads>
 __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, const int64_t *offsets, uint32_t tokens,
                                         int32_t k0, uint32_t words, uint32_t pitch, uint8_t *stage, float2 *info,
@@ -228,7 +231,7 @@ __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, co
     using T = typename XType<K>::type;
     constexpr int kTerms = K == kFloat ? 3 : 1;
     constexpr int kLanes = G / 8;  // that share a group
-    constexpr int kAhead = 3;  // loads in flight a thread (1: 16 f16 rows 53 us for 41; 4: no faster)
+    constexpr int kAhead = 3;  // loads in flight a thread (1: 8 bf16 rows 33 us for 26.8; 4: no faster)
     const int lane = threadIdx.x & 31;
     // a warp takes 32 words, of one row (words is a multiple of 32), and goes on kThreads further
     uint32_t tok = 0, w = threadIdx.x;
@@ -714,12 +717,16 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     Launch cfg{};
     // Warps that split the columns: enough for 16 warps an SM (8 where a pass takes more than
     // one column tile, as the staging of its rows is repeated for each CTA), and no warp
-    // with more than 16 blocks, so that the last CTAs are short.  Measured: 8 a SM 11.4 us for
-    // 9.6 (dense, 1 row) and 23.7 for 18.8 (4 f32 tokens x 8 of 64 experts); 16 a SM with three
-    // column tiles 35 for 28.7 (8 f32 rows); without the second rule 111 for 100 (16 f32
-    // tokens x 8 of 128 experts, 16 blocks), with at most 8 blocks a warp 113.
+    // with 16 blocks or more, so that the last CTAs are short.  Measured: 8 an SM 11.4 us for
+    // 9.5 (dense, 1 f16 row) and 23.0 for 18.3 (4 f32 tokens x 8 of 64 experts); 16 an SM with
+    // more column tiles 34.6 for 28.4 (8 f32 rows); without the second rule 111 for 96 (16 f32
+    // tokens x 8 of 128 experts, 16 blocks) and 90.5 for 79.5 (bf16, groups of 32), with at most
+    // 7 blocks a warp 108 and 83.4.
     int wk = 1;
-    while (wk < kWarps && wk < blocks && (tiles * gy * wk < (NT == 1 ? 16LL : 8LL) * num_sms || blocks >= 16 * wk)) wk *= 2, ++cfg.wk_log;
+    while (wk < kWarps && wk < blocks && (tiles * gy * wk < (NT == 1 ? 16LL : 8LL) * num_sms || blocks >= 16 * wk)) {
+        wk *= 2;
+        ++cfg.wk_log;
+    }
     cfg.x_vec = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx * sizeof(T) % 16 == 0 &&
                 p.x_slot_stride * sizeof(T) % 16 == 0;
     cfg.aligned = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 16 == 0 && p.expert_stride % 16 == 0;
@@ -767,10 +774,11 @@ cudaError_t launch_access(const Q4Params &p, int num_sms, cudaStream_t s) {
 // fewer warps are there to hide latency.  Per expert id the rows spread over the experts:
 // on average there are `share` rows for each one that occurs, and a second pass over the
 // few with more finds the weights in L2 (16 tokens x 8 of 128 experts with groups of 32:
-// 84 us with one tile, 91 with two).  A matrix of few rows of f16 or bf16 is cut into row
-// tiles of 16, so that every SM has several warps a scheduler (4096 x 11008, 1 row: 17.1 us
-// for 18.9; 64 experts' worth of rows and more: 94 for 84, hence the limit).  f32 has three
-// times the staging for each row tile and always takes 32 (11008 x 4096: 10.5 for 11.2).
+// 79.5 us with one tile, 85.8 with two).  A matrix of few rows and 16-bit x is cut into row
+// tiles of 16, so that every SM has several warps a scheduler (dense, 1 row, 11008 x 4096
+// 9.5 us for 11.4, 4096 x 11008 11.9 for 12.9; with many rows 16 tokens x 8 of 128 experts 68.0 for
+// 62.5, hence the limit).  f32 has three times the staging for each row tile and always
+// takes 32 (11008 x 4096: 10.4 for 11.2).
 template <Kind K, int G>
 cudaError_t launch_g(const Q4Params &p, int num_sms, cudaStream_t s) {
     constexpr int kColumns = (K == kFloat ? 3 : 1) * Group<G>::kParts;
@@ -780,7 +788,8 @@ cudaError_t launch_g(const Q4Params &p, int num_sms, cudaStream_t s) {
     const uint32_t share = p.ids != nullptr ? (p.rows + distinct - 1) / distinct : p.rows;
     if (share * kColumns <= 8 * kNarrow) {
         if constexpr (K != kFloat) {
-            if ((p.n + 31) / 32 * (p.ids != nullptr ? distinct : 1) < 4LL * num_sms) return launch_access<K, G, kNarrow, 1>(p, num_sms, s);
+            const int64_t tiles = (p.n + 31) / 32 * (p.ids != nullptr ? distinct : 1);
+            if (tiles < 4LL * num_sms) return launch_access<K, G, kNarrow, 1>(p, num_sms, s);
         }
         return launch_access<K, G, kNarrow, 2>(p, num_sms, s);
     }
