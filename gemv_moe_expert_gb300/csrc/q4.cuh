@@ -112,9 +112,8 @@ __device__ __forceinline__ void mma(float (&d)[4], bool first, uint32_t a0, uint
 struct Launch {
     int wk_log;   // log2 of the warps that split the columns
     int x_vec;    // rows of x start 16-byte aligned
-    int aligned;  // packed rows start 16-byte aligned
     int slab;     // blocks of x a warp in shared memory
-    int info_at, tails_at;  // byte offsets in shared memory
+    int info_at;  // byte offset in shared memory
 };
 
 __device__ __forceinline__ float scale_value(uint32_t raw, int dtype) {
@@ -326,23 +325,13 @@ __device__ __noinline__ float plain_output(const Q4Params &p, uint32_t expert, i
     return acc;
 }
 
-// 16 bytes at p, inside a row, put together from the aligned words that cover them,
-// which may reach 4 bytes past them, and 3 before: there, only the first word of the first
-// row of all would lie partly before the matrix.
-__device__ __forceinline__ uint4 load_unaligned(const uint8_t *p, const uint8_t *matrices) {
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
-    const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
-    uint32_t w[5] = {0u, 0u, 0u, 0u, 0u};
-    if (p - off >= matrices) {
-        w[0] = __ldg(q);
-    } else {
-        for (uint32_t i = off; i < 4; ++i) w[0] |= static_cast<uint32_t>(__ldg(p + (i - off))) << (8 * i);
-    }
+// The first n of 16 bytes at p, one by one.
+static __device__ __noinline__ uint4 load_bytes(const uint8_t *p, int n) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 1; i < 5; ++i) w[i] = __ldg(q + i);
-    const uint32_t s = 8 * off;
-    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
-                      __funnelshift_r(w[3], w[4], s));
+    for (int i = 0; i < 16; ++i)
+        if (i < n) w[i / 4] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Loads under a predicate, without a branch: a branch around each would end a basic
@@ -353,6 +342,13 @@ __device__ __forceinline__ void load_stream32(bool pred, const void *p, uint4 (&
         "@p ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t}"
         : "+r"(v[0].x), "+r"(v[0].y), "+r"(v[0].z), "+r"(v[0].w), "+r"(v[1].x), "+r"(v[1].y), "+r"(v[1].z),
           "+r"(v[1].w)
+        : "l"(p), "r"(static_cast<uint32_t>(pred)));
+}
+__device__ __forceinline__ void load_stream16(bool pred, const void *p, uint4 &v) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
         : "l"(p), "r"(static_cast<uint32_t>(pred)));
 }
 // zero where the predicate is false
@@ -387,12 +383,29 @@ __device__ __forceinline__ uint32_t load_cells8(bool pred, const void *p) {
     return v;
 }
 
-// How a kernel reads codes, scales and zero points.
-//   kAnyhow  any alignment and scale type; a look at every access
-//   kApart   packed rows start and end on multiples of 32 bytes, 16-bit scales, enough rows for
-//            a warp; the scales of a lane one by one (groups of 32: two by two)
+// 16 bytes at any p, put together from the five aligned words that cover them.
+__device__ __forceinline__ uint4 load_unaligned(bool pred, const uint8_t *p) {
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u), s = 8 * off;
+    uint32_t w[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = load_cells32(pred, p - off + 4 * i);
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
+}
+
+// How a kernel reads codes, scales and zero points.  What lies between a row's end and
+// the end of an access meets zeros of x; only where the memory ends there, after the last
+// row, single bytes are read.
+//   kAnyhow  any alignment, scale type and number of rows
+//   kLoose   packed rows start on multiples of 16 bytes, 16-bit scales, enough rows for a warp
+//   kApart   they start and end on multiples of 32 bytes; the scales of a lane one by one
+//            (groups of 32: two by two)
 //   kAtOnce  and the scales of a lane, and its zero points, can be read at once
-enum Access { kAnyhow, kApart, kAtOnce };
+// Measured, 16 bf16 tokens x 8 of 128 experts, groups of 128 (of 32, with zeros): 1536 x 4096,
+// kAtOnce, 62.3 us (79.5); 1537 x 4090 with rows 2048 bytes apart, kLoose, 84.5 (149); with rows
+// 2045 bytes apart, kAnyhow, 177 (243).  Dense 1 f16 row, groups of 128: 11008 x 4224 (33 groups),
+// kApart, 11.0; 11009 x 4098 kLoose 12.3, kAnyhow 19.0.
+enum Access { kAnyhow, kLoose, kApart, kAtOnce };
 
 // G: columns of a group.  NT: mma column tiles, 8 NT / (terms kParts) rows of x a pass.
 // MT: mma row tiles of a warp.
@@ -407,7 +420,7 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
     static_assert(kPass > 0, "a row of x takes kTerms * kParts columns");
     constexpr int kRedPitch = 8 * NT + 1;
     constexpr int kTile = 16 * MT, kRows = 2 * MT;  // rows of a warp, of a lane
-    extern __shared__ __align__(16) uint8_t smem[];  // zeros, x, info, tails
+    extern __shared__ __align__(16) uint8_t smem[];  // zeros, x, info
     __shared__ float red[kWarps][kTile][kRedPitch];
     __shared__ uint32_t s_ids[kWindow];
     __shared__ uint32_t s_bits[32];
@@ -428,67 +441,68 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
     const int32_t blocks = static_cast<int32_t>((p.k + 255) / 256);
     const int32_t groups = static_cast<int32_t>(p.groups);
     // The lane's rows are row + 8 h, h < kRows.  A tile that would pass the end starts earlier
-    // and computes some rows of the one before again; kAnyhow: rows past the end are not read (their
-    // registers hold whatever they do) and not stored.
+    // and computes some rows of the one before again; kAnyhow: the last row is read in place
+    // of those past the end, which are not stored.
     const int64_t start = j0 + wr * kTile, row = (A == kAnyhow ? start : min(start, p.n - kTile)) + g;
-    const int left =
-        A != kAnyhow ? kRows : row >= p.n ? 0 : static_cast<int>(min((p.n - row + 7) / 8, static_cast<int64_t>(kRows)));
-    const uint8_t *const codes = p.q + static_cast<int64_t>(expert) * p.expert_stride + row * p.ldq + 32 * c;
-    const int64_t cell = (static_cast<int64_t>(expert) * p.n + row) * p.groups;
+    const uint8_t *const matrix = p.q + static_cast<int64_t>(expert) * p.expert_stride;
+    const uint8_t *const codes = matrix + row * p.ldq + 32 * c;
+    const int64_t cells = static_cast<int64_t>(expert) * p.n * p.groups, cell = cells + row * p.groups;
+    auto row_of = [&](int h) { return min(row + 8 * h, p.n - 1); };
     const int lane_cell = G == 128 ? 0 : kCells * (c & 1);  // the lane's first group of a block
 
-    // kAnyhow: blocks that can be read without a look at the row's end are whole ones (and
-    // 4 bytes more where rows are not aligned).  The codes of the others, one or two, go to
-    // shared memory byte by byte (what stands there past a row's end meets zeros of x).
-    const int32_t hi = static_cast<int32_t>(cfg.aligned ? p.k / 256 : (p.k - 8) / 256);
-    uint8_t *tails = smem + cfg.tails_at;  // [tile_rows][256]
-    if (A == kAnyhow) {
-        const int32_t len = row_len - hi * 128;
-        for (int32_t u = tid; u < len << tile_rows_log; u += kThreads) {
-            const int32_t r = u & (tile_rows - 1), b = u >> tile_rows_log;
-            if (j0 + r < p.n)
-                tails[r * 256 + b] =
-                    __ldg(p.q + static_cast<int64_t>(expert) * p.expert_stride + (j0 + r) * p.ldq + hi * 128 + b);
-        }
-        __syncthreads();
-    }
     int32_t b1 = 0;  // end of the slab: what lies past it is not fetched
     auto fetch_codes = [&](int32_t block, uint4 (&q)[kRows][2]) {
-        if (A != kAnyhow) {
-            const bool in = block < b1 && block * 128 + 32 * c < row_len;
+        const int32_t at = block * 128 + 32 * c;  // in the row
+        const bool in = block < b1 && at < row_len;
+        if (A >= kApart) {
 #pragma unroll
             for (int h = 0; h < kRows; ++h) load_stream32(in, codes + block * 128 + h * (8 * p.ldq), q[h]);
-        } else if (block < hi && block < b1) {
+        } else if (A == kLoose) {
+            const bool in2 = block < b1 && at + 16 < row_len;
+            const bool ends = in && at + 32 > row_len;  // the row's end lies in these bytes
 #pragma unroll
             for (int h = 0; h < kRows; ++h) {
-                const uint8_t *at = codes + static_cast<int64_t>(block) * 128 + h * (8 * p.ldq);
-                if (h < left) {
+                const bool last = ends && row + 8 * h == p.n - 1;
+                const uint8_t *from = codes + block * 128 + h * (8 * p.ldq);
+                load_stream16(in && !last, from, q[h][0]);
+                load_stream16(in2 && !last, from + 16, q[h][1]);
+            }
+            if (ends && row <= p.n - 1 && row + 8 * kRows > p.n - 1) {
 #pragma unroll
-                    for (int v = 0; v < 2; ++v)
-                        q[h][v] = cfg.aligned ? ld_stream16(at + 16 * v) : load_unaligned(at + 16 * v, p.q);
+                for (int h = 0; h < kRows; ++h) {
+                    if (row + 8 * h != p.n - 1) continue;
+                    const uint8_t *from = codes + block * 128 + h * (8 * p.ldq);
+                    q[h][0] = load_bytes(from, row_len - at);
+                    q[h][1] = load_bytes(from + 16, row_len - at - 16);
                 }
             }
-        } else if (block < b1) {
+        } else {
+            const uint8_t *const first_byte = p.q, *const end = matrix + (p.n - 1) * p.ldq + row_len;
 #pragma unroll
-            for (int h = 0; h < kRows; ++h)
+            for (int h = 0; h < kRows; ++h) {
 #pragma unroll
-                for (int v = 0; v < 2; ++v)
-                    q[h][v] = *reinterpret_cast<const uint4 *>(tails + (wr * kTile + g + 8 * h) * 256 +
-                                                               (block - hi) * 128 + 32 * c + 16 * v);
+                for (int v = 0; v < 2; ++v) {
+                    const uint8_t *from = matrix + row_of(h) * p.ldq + at + 16 * v;
+                    const bool some = in && at + 16 * v < row_len;
+                    const bool whole = from - 3 >= first_byte && from + 20 <= end;  // the words that cover them
+                    q[h][v] = load_unaligned(some && whole, from);
+                    if (some && !whole) q[h][v] = load_bytes(from, row_len - at - 16 * v);
+                }
+            }
         }
     };
     // Raw scales and zero points of the lane's kCells groups of a block.  kAtOnce: s.x, s.y
-    // pairs of scales, z.x bytes.  kApart: s.x, s.y one scale each, z.x, z.y one byte each;
-    // with groups of 32, pairs.
+    // pairs of scales, z.x bytes.  Else: s.x, s.y one scale each, z.x, z.y one byte each;
+    // with groups of 32, pairs.  (32-bit scales are read where they are used.)
     uint2 s_raw[kRows], z_raw[kRows];
     auto fetch_cells = [&](int32_t block) {
-        if (A == kAnyhow) return;
+        if (A == kAnyhow && p.scale_dtype == kF32) return;
         const int32_t group = block * Group<G>::kInBlock + lane_cell;
         const bool have = group < groups, more = group + kCells / 2 < groups;
         const bool zhave = have && p.zeros != nullptr, zmore = more && p.zeros != nullptr;
 #pragma unroll
         for (int h = 0; h < kRows; ++h) {
-            const int64_t at = cell + group + h * (8 * p.groups);
+            const int64_t at = (A == kAnyhow ? cells + row_of(h) * p.groups : cell + h * (8 * p.groups)) + group;
             const uint16_t *s = static_cast<const uint16_t *>(p.scales) + at;
             const uint8_t *z = p.zeros + at;
             if (A == kAtOnce && kCells == 4) {
@@ -497,9 +511,15 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
             } else if (A == kAtOnce) {
                 s_raw[h].x = load_cells32(have, s);
                 z_raw[h].x = load_cells16(zhave, z);
-            } else if (kCells == 4) {
+            } else if (A == kApart && kCells == 4) {
                 s_raw[h] = make_uint2(load_cells32(have, s), load_cells32(more, s + 2));
                 z_raw[h] = make_uint2(load_cells16(zhave, z), load_cells16(zmore, z + 2));
+            } else if (kCells == 4) {
+                const bool second = group + 1 < groups, fourth = group + 3 < groups;
+                s_raw[h].x = load_cells16(have, s) | load_cells16(second, s + 1) << 16;
+                s_raw[h].y = load_cells16(more, s + 2) | load_cells16(fourth, s + 3) << 16;
+                z_raw[h].x = load_cells8(zhave, z) | load_cells8(zhave && second, z + 1) << 8;
+                z_raw[h].y = load_cells8(zmore, z + 2) | load_cells8(zmore && fourth, z + 3) << 8;
             } else {
                 s_raw[h] = make_uint2(load_cells16(have, s), load_cells16(more, s + 1));
                 z_raw[h] = make_uint2(load_cells8(zhave, z), load_cells8(zmore, z + 1));
@@ -510,7 +530,7 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
     // kCloses among the lane's of a block
     auto cells_of = [&](int32_t block, int h, int close, float (&s)[2], float (&sz)[2]) {
         float z[2] = {-8.f, -8.f};
-        if (A != kAnyhow) {
+        if (A != kAnyhow || p.scale_dtype != kF32) {
             uint32_t a, b, y, z1;
             if (kCells == 4) {  // close 0 takes groups 0 and 2, close 1 takes 1 and 3
                 a = s_raw[h].x >> (16 * close) & 0xffffu;
@@ -532,12 +552,10 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int32_t group = block * Group<G>::kInBlock + lane_cell + close + kCloses * i;
-                const int64_t at = cell + group + h * (8 * p.groups);
+                const int64_t at = cells + row_of(h) * p.groups + group;
                 s[i] = 0.f;
-                if (h < left && group < groups) {
-                    s[i] = scale_value(p.scale_dtype == kF32 ? __ldg(static_cast<const uint32_t *>(p.scales) + at)
-                                                             : __ldg(static_cast<const uint16_t *>(p.scales) + at),
-                                       p.scale_dtype);
+                if (group < groups) {
+                    s[i] = __ldg(static_cast<const float *>(p.scales) + at);
                     if (p.zeros != nullptr) z[i] = -static_cast<float>(__ldg(p.zeros + at));
                 }
             }
@@ -729,16 +747,14 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     }
     cfg.x_vec = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx * sizeof(T) % 16 == 0 &&
                 p.x_slot_stride * sizeof(T) % 16 == 0;
-    cfg.aligned = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.ldq % 16 == 0 && p.expert_stride % 16 == 0;
     const int lines = static_cast<int>(p.rows < kPass ? p.rows : kPass) * kTerms;
     const int64_t all = (blocks + wk - 1) / wk;
     const int per_block = wk * block_bytes(lines, NT, Group<G>::kCloses);
     cfg.slab = (B::kStageBytes - lines * kPitchPad) / per_block;
     if (cfg.slab > all) cfg.slab = static_cast<int>(all);
     cfg.info_at = kZeroBytes + lines * (cfg.slab * wk * 512 + kPitchPad);
-    cfg.tails_at = kZeroBytes + lines * kPitchPad + cfg.slab * per_block;
     const int64_t wr = kWarps / wk;
-    const int bytes = cfg.tails_at + (A == kAnyhow ? static_cast<int>(wr) * kTile * 256 : 0);
+    const int bytes = kZeroBytes + lines * kPitchPad + cfg.slab * per_block;
 
     static unsigned long long done = 0;  // devices on which the kernel may use its shared memory
     int dev = 0;
@@ -747,7 +763,7 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     if (!(done & bit)) {
         const cudaError_t e =
             cudaFuncSetAttribute(q4_kernel<K, G, A, NT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 B::kStageBytes + kZeroBytes + kWarps * kTile * 256);
+                                 B::kStageBytes + kZeroBytes);
         if (e != cudaSuccess) return e;
         done |= bit;
     }
@@ -760,10 +776,11 @@ template <Kind K, int G, int NT, int MT>
 cudaError_t launch_access(const Q4Params &p, int num_sms, cudaStream_t s) {
     constexpr int kCells = Group<G>::kCells;
     auto multiple = [](const void *ptr, int64_t a) { return reinterpret_cast<uintptr_t>(ptr) % a == 0; };
-    const bool even = multiple(p.q, 32) && p.ldq % 32 == 0 && p.expert_stride % 32 == 0 && p.k % 64 == 0 &&
-                      p.scale_dtype != kF32 && multiple(p.scales, kCells) && multiple(p.zeros, kCells / 2) &&
-                      p.n >= 16 * MT;
-    if (!even) return launch_nt<K, G, kAnyhow, NT, MT>(p, num_sms, s);
+    if (p.scale_dtype == kF32 || p.n < 16 * MT || !multiple(p.q, 16) || p.ldq % 16 != 0 || p.expert_stride % 16 != 0)
+        return launch_nt<K, G, kAnyhow, NT, MT>(p, num_sms, s);
+    if (!multiple(p.q, 32) || p.ldq % 32 != 0 || p.expert_stride % 32 != 0 || p.k % 64 != 0 ||
+        !multiple(p.scales, kCells) || !multiple(p.zeros, kCells / 2))
+        return launch_nt<K, G, kLoose, NT, MT>(p, num_sms, s);
     if (p.groups % kCells == 0 && multiple(p.scales, 2 * kCells) && multiple(p.zeros, kCells))
         return launch_nt<K, G, kAtOnce, NT, MT>(p, num_sms, s);
     return launch_nt<K, G, kApart, NT, MT>(p, num_sms, s);

@@ -478,7 +478,7 @@ GBMM_API gbmm_status gbmm_moe_combine_backward(gbmm_dtype dt, uint32_t m, uint32
  *   and column 2i+1 in its high four bits (ldq_bytes >= (k+1)/2; the unused half
  *   of the last byte of an odd k is ignored).  Read fastest: a k that is a multiple
  *   of 64, matrices and rows that start on multiples of 32 bytes, and 16-bit scales;
- *   every other alignment works.
+ *   next, multiples of 16 bytes and any k; every other alignment works.
  * group: 32, 64 or 128 columns; the last one may be ragged.  G = ceil(k/group).
  * scales: [n, G] tight, scale_dt f32, f16 or bf16.  zeros: u8 [n, G] tight, values
  *   0..255, or NULL for 8 everywhere.

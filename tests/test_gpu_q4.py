@@ -201,6 +201,14 @@ def test_matmul_id_q4_strides(dtype):
     experts(dtype, 3, 18, 300, 2, 5, 64, ldq=151, stride_pad=5, offset=3, zeros=True, scale_dt="f32")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("ldq,offset,stride_pad", [(2064, 0, 0), (2048, 16, 16), (2045, 3, 1)])
+def test_matmul_id_q4_odd_sizes(dtype, group, ldq, offset, stride_pad):
+    """Rows that end inside an access, the last one at the end of the memory."""
+    experts(dtype, 6, 161, 4090, 2, 3, group, ldq=ldq, offset=offset, stride_pad=stride_pad, zeros=True)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_matmul_id_q4_more_rows_than_a_window(dtype):
     experts(dtype, 400, 17, 96, 6, 9, 32)
