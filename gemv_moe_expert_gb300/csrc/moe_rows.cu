@@ -28,12 +28,14 @@ constexpr int B = 4;
 // Blocks an SM (the registers they may use follow).  4-byte elements need fewer
 // registers for the same bytes in flight.  Measured on 4096 tokens x 8 slots of
 // 4096 elements: combine f32 95 us with 4 and 97 us with 5, bf16 52 and 51 us; its
-// gradient f32 177 us with 3 and 190 us with 4, bf16 97 and 92 us.
-template <typename T> struct Resident {
-    static constexpr int kCombine = sizeof(T) == 4 ? 4 : 5;
-    static constexpr int kBackward = sizeof(T) == 4 ? 3 : 4;
+// gradient f32 177 us with 3 and 190 us with 4, bf16 97 and 92 us.  Shifted rows need
+// twice the registers for a piece: bf16 combine 83 us with 3 and 113 with 4; its gradient 172
+// with 4, 195 with 3 and 200 with 5.
+template <typename T, bool SHIFT> struct Resident {
+    static constexpr int kDispatch = 4;
+    static constexpr int kCombine = SHIFT ? 3 : sizeof(T) == 4 ? 4 : 5;
+    static constexpr int kBackward = SHIFT ? 4 : sizeof(T) == 4 ? 3 : 4;
 };
-constexpr int kDispatchBlocks = 4;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kNowhere = 0xffffffffu;
 
@@ -49,6 +51,30 @@ __device__ __forceinline__ typename Raw<VB>::type load_raw(const T *p) {
 template <typename T, int VB>
 __device__ __forceinline__ void store_raw(T *p, const typename Raw<VB>::type &r) {
     *reinterpret_cast<typename Raw<VB>::type *>(p) = r;
+}
+
+// 16 bytes at any element: the two aligned chunks that cover them, and how many bytes of
+// the first come before.
+struct Chunks {
+    uint4 a, b;
+    uint32_t off;
+};
+template <typename T> __device__ __forceinline__ Chunks load_chunks(const T *p) {
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+    const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - off);
+    return Chunks{__ldg(q), __ldg(q + 1), off};
+}
+__device__ __forceinline__ uint4 shifted(const Chunks &c) {
+    const bool two = c.off & 8u, one = c.off & 4u;
+    const uint32_t bits = 8 * (c.off & 3u);
+    uint32_t w[8] = {c.a.x, c.a.y, c.a.z, c.a.w, c.b.x, c.b.y, c.b.z, c.b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = two ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = one ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <typename T, int V, typename R>
@@ -94,6 +120,20 @@ struct Slots {
     __device__ __forceinline__ float weight(int b) const { return __shfl_sync(kFull, w, b); }
 };
 
+// V elements as loaded: with one access, or (SHIFT) as the two chunks that cover them.
+template <typename R, bool SHIFT> struct Piece {
+    R r;
+    __device__ __forceinline__ void clear() { r = R{}; }
+    template <typename T> __device__ __forceinline__ void load(const T *p) { r = load_raw<T, sizeof(R)>(p); }
+    __device__ __forceinline__ R get() const { return r; }
+};
+template <typename R> struct Piece<R, true> {
+    Chunks c;
+    __device__ __forceinline__ void clear() { c = Chunks{}; }
+    template <typename T> __device__ __forceinline__ void load(const T *p) { c = load_chunks<T>(p); }
+    __device__ __forceinline__ R get() const { return shifted(c); }
+};
+
 // Columns of a row are dealt to threads in steps that all threads of a warp take
 // together (the shuffles need the whole warp; a thread past the end idles): first
 // the columns that divide into accesses of VB bytes, then the rest one by one.  The
@@ -101,20 +141,47 @@ struct Slots {
 // (with the choice inside the loop each load sat behind its own branch and the
 // loads of a batch no longer overlapped).
 
+//
+// Rows that do not all start on multiples of 16 bytes (SHIFT) are still written 16 bytes
+// at a time: every row that is written has its own first whole access, `head` elements
+// in and one access further (so that what covers a piece of a row that is read never
+// starts before that row), its last one ends an access before the row does, and the
+// elements before and behind them are the rest.  4096 tokens x 8 slots x 4097 (in brackets
+// one element an access): dispatch bf16 59 us (102), f32 104 (162); combine 83 (177), 130
+// (214); its gradient 172 (285), 274 (424).
+
 struct Columns {
     int64_t from, to, step;  // elements
 };
 template <int V>
-__device__ __forceinline__ Columns whole_columns(const MoeRowsParams &p) {
-    return Columns{(static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * V, p.n / V * V,
+__device__ __forceinline__ Columns whole_columns(const MoeRowsParams &p, bool shift) {
+    return Columns{(static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * V, shift ? p.n : p.n / V * V,
                    static_cast<int64_t>(gridDim.y) * blockDim.x * V};
 }
 template <int V>
-__device__ __forceinline__ Columns rest_columns(const MoeRowsParams &p) {
-    return Columns{p.n / V * V + threadIdx.x, blockIdx.y == 0 ? p.n : 0, static_cast<int64_t>(blockDim.x)};
+__device__ __forceinline__ Columns rest_columns(const MoeRowsParams &p, bool shift) {
+    return Columns{(shift ? 0 : p.n / V * V) + threadIdx.x,
+                   blockIdx.y != 0 ? 0 : shift ? min(p.n, static_cast<int64_t>(5 * V)) : p.n,
+                   static_cast<int64_t>(blockDim.x)};
 }
 
-template <typename T, int VB>
+// Element of a row, written at `row`, that column i means, and whether there is one.
+struct Place {
+    int64_t i;
+    bool in;
+};
+template <typename T, int VB, bool SHIFT>
+__device__ __forceinline__ Place place_of(const MoeRowsParams &p, const Columns &c, int64_t i, const T *row) {
+    if (!SHIFT) return Place{i, i < c.to};
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    const int64_t first =
+        V + ((16u - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u)) & 15u) / static_cast<int>(sizeof(T));
+    if (VB == 16) return Place{first + i, first + i + 2 * V <= p.n};
+    const int64_t whole = p.n - 2 * V >= first ? (p.n - 2 * V - first) / V * V + V : 0;
+    return Place{i < first ? i : i + whole, i < p.n - whole};
+}
+
+template <typename T, int VB, bool SHIFT>
 __device__ __forceinline__ void dispatch_columns(const MoeRowsParams &p, const Slots &slots, uint32_t valid,
                                                  const T *x, const Columns &c) {
     using R = typename Raw<VB>::type;
@@ -123,20 +190,37 @@ __device__ __forceinline__ void dispatch_columns(const MoeRowsParams &p, const S
     const int lane = threadIdx.x & 31;
     T *out = static_cast<T *>(p.row_out);
     for (int64_t i = c.from; i - lane * V < c.to; i += c.step) {
-        const bool in = i < c.to;
-        R v{};
-        if (in) v = load_raw<T, VB>(x + i);
+        if constexpr (SHIFT) {
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const uint32_t at = slots.place(b);
-            if (in && at < rows)
-                store_raw<T, VB>(out + static_cast<int64_t>(at) * p.ld_row_out + i, at < valid ? v : R{});
+            for (int b = 0; b < B; ++b) {
+                const uint32_t at = slots.place(b);
+                T *row = out + static_cast<int64_t>(at) * p.ld_row_out;
+                const Place to = place_of<T, VB, SHIFT>(p, c, i, row);
+                if (to.in && at < rows) {
+                    R v;
+                    if constexpr (VB == 16)
+                        v = shifted(load_chunks<T>(x + to.i));
+                    else
+                        v = load_raw<T, VB>(x + to.i);
+                    store_raw<T, VB>(row + to.i, at < valid ? v : R{});
+                }
+            }
+        } else {
+            const bool in = i < c.to;
+            R v{};
+            if (in) v = load_raw<T, VB>(x + i);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const uint32_t at = slots.place(b);
+                if (in && at < rows)
+                    store_raw<T, VB>(out + static_cast<int64_t>(at) * p.ld_row_out + i, at < valid ? v : R{});
+            }
         }
     }
 }
 
-template <typename T, int VB>
-__global__ void __launch_bounds__(kThreads, kDispatchBlocks)
+template <typename T, int VB, bool SHIFT>
+__global__ void __launch_bounds__(kThreads, Resident<T, SHIFT>::kDispatch)
     moe_dispatch_kernel(const __grid_constant__ MoeRowsParams p) {
     constexpr int V = VB / static_cast<int>(sizeof(T));
     const uint32_t valid = valid_rows(p);
@@ -149,15 +233,15 @@ __global__ void __launch_bounds__(kThreads, kDispatchBlocks)
         const T *x = static_cast<const T *>(p.tok_in) + static_cast<int64_t>(t) * p.ld_tok_in;
         for (uint32_t s0 = 0; s0 < p.top_k; s0 += B) {
             if (s0 != 0) slots.load(p, valid, t, s0);
-            dispatch_columns<T, VB>(p, slots, valid, x, whole_columns<V>(p));
-            if (V > 1) dispatch_columns<T, sizeof(T)>(p, slots, valid, x, rest_columns<V>(p));
+            dispatch_columns<T, VB, SHIFT>(p, slots, valid, x, whole_columns<V>(p, SHIFT));
+            if (V > 1) dispatch_columns<T, sizeof(T), SHIFT>(p, slots, valid, x, rest_columns<V>(p, SHIFT));
         }
         slots = next;
     }
 }
 
 // A slot without an expert adds 0 * 0.
-template <typename T, int VB>
+template <typename T, int VB, bool SHIFT>
 __device__ __forceinline__ void combine_columns(const MoeRowsParams &p, uint32_t t, Slots slots, uint32_t valid,
                                                 const Columns &c) {
     using R = typename Raw<VB>::type;
@@ -165,25 +249,25 @@ __device__ __forceinline__ void combine_columns(const MoeRowsParams &p, uint32_t
     const int lane = threadIdx.x & 31;
     const T *in_rows = static_cast<const T *>(p.row_in);
     T *y = static_cast<T *>(p.tok_out) + static_cast<int64_t>(t) * p.ld_tok_out;
-    for (int64_t i = c.from; i - lane * V < c.to; i += c.step) {
-        const bool in = i < c.to;
+    for (int64_t step = c.from; step - lane * V < c.to; step += c.step) {
+        const auto [i, in] = place_of<T, VB, SHIFT>(p, c, step, y);
         float acc[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] = 0.f;
         for (uint32_t s0 = 0; s0 < p.top_k; s0 += B) {
             if (p.top_k > B) slots.load(p, valid, t, s0);
-            R v[B];
+            Piece<R, SHIFT && VB == 16> v[B];
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 const uint32_t at = slots.place(b);
-                v[b] = R{};
-                if (in && at < valid) v[b] = load_raw<T, VB>(in_rows + static_cast<int64_t>(at) * p.ld_row_in + i);
+                v[b].clear();
+                if (in && at < valid) v[b].load(in_rows + static_cast<int64_t>(at) * p.ld_row_in + i);
             }
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 const float w = slots.weight(b);
                 float f[V];
-                unpack<T, V>(v[b], f);
+                unpack<T, V>(v[b].get(), f);
 #pragma unroll
                 for (int j = 0; j < V; ++j) acc[j] = fmaf(w, f[j], acc[j]);
             }
@@ -192,8 +276,8 @@ __device__ __forceinline__ void combine_columns(const MoeRowsParams &p, uint32_t
     }
 }
 
-template <typename T, int VB>
-__global__ void __launch_bounds__(kThreads, Resident<T>::kCombine)
+template <typename T, int VB, bool SHIFT>
+__global__ void __launch_bounds__(kThreads, Resident<T, SHIFT>::kCombine)
     moe_combine_kernel(const __grid_constant__ MoeRowsParams p) {
     constexpr int V = VB / static_cast<int>(sizeof(T));
     const uint32_t valid = valid_rows(p);
@@ -203,8 +287,9 @@ __global__ void __launch_bounds__(kThreads, Resident<T>::kCombine)
     slots.load(p, valid, t, 0);
     for (; t < p.m; t += step) {
         next.load(p, valid, t + step, 0);
-        combine_columns<T, VB>(p, static_cast<uint32_t>(t), slots, valid, whole_columns<V>(p));
-        if (V > 1) combine_columns<T, sizeof(T)>(p, static_cast<uint32_t>(t), slots, valid, rest_columns<V>(p));
+        const uint32_t token = static_cast<uint32_t>(t);
+        combine_columns<T, VB, SHIFT>(p, token, slots, valid, whole_columns<V>(p, SHIFT));
+        if (V > 1) combine_columns<T, sizeof(T), SHIFT>(p, token, slots, valid, rest_columns<V>(p, SHIFT));
         slots = next;
     }
 }
@@ -229,7 +314,20 @@ __device__ __forceinline__ float warp_sums(float (&v)[B]) {
     return v[0];
 }
 
-template <typename T, int VB>
+// one slot's part of combine_backward_columns: d_ys, and the dot product's terms
+template <typename T, int V, typename R>
+__device__ __forceinline__ R backward_piece(const R &y, const float (&g)[V], float w, float &dot) {
+    float f[V], wg[V];
+    unpack<T, V>(y, f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        dot = fmaf(g[j], f[j], dot);
+        wg[j] = w * g[j];
+    }
+    return pack<T, V, R>(wg);
+}
+
+template <typename T, int VB, bool SHIFT>
 __device__ __forceinline__ void combine_backward_columns(const MoeRowsParams &p, const Slots &slots, uint32_t valid,
                                                          const T *dy, const Columns &c, float (&dot)[B]) {
     using R = typename Raw<VB>::type;
@@ -238,39 +336,61 @@ __device__ __forceinline__ void combine_backward_columns(const MoeRowsParams &p,
     const int lane = threadIdx.x & 31;
     const T *in_rows = static_cast<const T *>(p.row_in);
     T *out = static_cast<T *>(p.row_out);
-    for (int64_t i = c.from; i - lane * V < c.to; i += c.step) {
-        const bool in = i < c.to;
-        R v[B], graw{};
-        if (in) graw = load_raw<T, VB>(dy + i);
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const uint32_t at = slots.place(b);
-            v[b] = R{};
-            if (in && at < valid) v[b] = load_raw<T, VB>(in_rows + static_cast<int64_t>(at) * p.ld_row_in + i);
-        }
+    for (int64_t step = c.from; step - lane * V < c.to; step += c.step) {
         float g[V];
-        unpack<T, V>(graw, g);
+        if constexpr (SHIFT) {
+            // each slot has its own piece of dy: two slots at once, and more blocks an SM
+            constexpr int kBatch = 2;
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const uint32_t at = slots.place(b);
-            const float w = slots.weight(b);
-            float f[V], wg[V];
-            unpack<T, V>(v[b], f);
+            for (int b0 = 0; b0 < B; b0 += kBatch) {
+                Piece<R, VB == 16> v[kBatch], graw[kBatch];
+                Place place[kBatch];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                dot[b] = fmaf(g[j], f[j], dot[b]);
-                wg[j] = w * g[j];
+                for (int u = 0; u < kBatch; ++u) {
+                    const uint32_t at = slots.place(b0 + u);
+                    place[u] = place_of<T, VB, SHIFT>(p, c, step, out + static_cast<int64_t>(at) * p.ld_row_out);
+                    v[u].clear();
+                    graw[u].clear();
+                    if (place[u].in && at < valid) {
+                        v[u].load(in_rows + static_cast<int64_t>(at) * p.ld_row_in + place[u].i);
+                        graw[u].load(dy + place[u].i);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const uint32_t at = slots.place(b0 + u);
+                    unpack<T, V>(graw[u].get(), g);
+                    const R d = backward_piece<T, V>(v[u].get(), g, slots.weight(b0 + u), dot[b0 + u]);
+                    if (place[u].in && at < rows)
+                        store_raw<T, VB>(out + static_cast<int64_t>(at) * p.ld_row_out + place[u].i,
+                                         at < valid ? d : R{});
+                }
             }
-            const R d = pack<T, V, R>(wg);
-            if (in && at < rows)
-                store_raw<T, VB>(out + static_cast<int64_t>(at) * p.ld_row_out + i, at < valid ? d : R{});
+        } else {
+            const bool in = step < c.to;
+            R v[B], graw{};
+            if (in) graw = load_raw<T, VB>(dy + step);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const uint32_t at = slots.place(b);
+                v[b] = R{};
+                if (in && at < valid) v[b] = load_raw<T, VB>(in_rows + static_cast<int64_t>(at) * p.ld_row_in + step);
+            }
+            unpack<T, V>(graw, g);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const uint32_t at = slots.place(b);
+                const R d = backward_piece<T, V>(v[b], g, slots.weight(b), dot[b]);
+                if (in && at < rows)
+                    store_raw<T, VB>(out + static_cast<int64_t>(at) * p.ld_row_out + step, at < valid ? d : R{});
+            }
         }
     }
 }
 
 // The grid's y extent is 1: a block sees a token's whole row, for the dot products.
-template <typename T, int VB>
-__global__ void __launch_bounds__(kThreads, Resident<T>::kBackward)
+template <typename T, int VB, bool SHIFT>
+__global__ void __launch_bounds__(kThreads, Resident<T, SHIFT>::kBackward)
     moe_combine_backward_kernel(const __grid_constant__ MoeRowsParams p) {
     constexpr int V = VB / static_cast<int>(sizeof(T));
     __shared__ float part[2][kThreads / 32][B];
@@ -293,8 +413,9 @@ __global__ void __launch_bounds__(kThreads, Resident<T>::kBackward)
 #pragma unroll
             for (int b = 0; b < B; ++b) dot[b] = 0.f;
             if (live) {
-                combine_backward_columns<T, VB>(p, slots, valid, dy, whole_columns<V>(p), dot);
-                if (V > 1) combine_backward_columns<T, sizeof(T)>(p, slots, valid, dy, rest_columns<V>(p), dot);
+                combine_backward_columns<T, VB, SHIFT>(p, slots, valid, dy, whole_columns<V>(p, SHIFT), dot);
+                if (V > 1)
+                    combine_backward_columns<T, sizeof(T), SHIFT>(p, slots, valid, dy, rest_columns<V>(p, SHIFT), dot);
             }
             // a slot without an expert has met zeros only, unless d_y is not finite
             const float sum = warp_sums(dot);
@@ -321,16 +442,15 @@ __global__ void __launch_bounds__(kThreads, Resident<T>::kBackward)
     }
 }
 
-// Bytes of an access that every row start allows: 16, else 4, else one element.
-template <typename T>
-int access_bytes(const MoeRowsParams &p) {
+// whether every row starts on a multiple of 16 bytes
+template <typename T> bool aligned_rows(const MoeRowsParams &p) {
     const void *ptrs[4] = {p.tok_in, p.tok_out, p.row_in, p.row_out};
     const int64_t lds[4] = {p.ld_tok_in, p.ld_tok_out, p.ld_row_in, p.ld_row_out};
     uint64_t bits = 0;
     for (int i = 0; i < 4; ++i)
         if (ptrs[i] != nullptr)
             bits |= reinterpret_cast<uintptr_t>(ptrs[i]) | static_cast<uint64_t>(lds[i]) * sizeof(T);
-    return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : static_cast<int>(sizeof(T));
+    return bits % 16 == 0;
 }
 
 struct Shape {
@@ -360,29 +480,31 @@ Shape shape_of(const MoeRowsParams &p, int V, int resident, bool stays, bool row
 
 enum Which { kDispatch, kCombine, kCombineBackward };
 
-template <typename T, int VB>
+template <typename T, int VB, bool SHIFT>
 cudaError_t launch_vb(Which which, const MoeRowsParams &p, cudaStream_t s) {
     constexpr int V = VB / static_cast<int>(sizeof(T));
+    using Blocks = Resident<T, SHIFT>;
     if (which == kDispatch) {
-        const Shape h = shape_of(p, V, kDispatchBlocks, false, false);
-        moe_dispatch_kernel<T, VB><<<h.grid, h.block, 0, s>>>(p);
+        const Shape h = shape_of(p, V, Blocks::kDispatch, false, false);
+        moe_dispatch_kernel<T, VB, SHIFT><<<h.grid, h.block, 0, s>>>(p);
     } else if (which == kCombine) {
-        const Shape h = shape_of(p, V, Resident<T>::kCombine, true, false);
-        moe_combine_kernel<T, VB><<<h.grid, h.block, 0, s>>>(p);
+        const Shape h = shape_of(p, V, Blocks::kCombine, true, false);
+        moe_combine_kernel<T, VB, SHIFT><<<h.grid, h.block, 0, s>>>(p);
     } else {
-        const Shape h = shape_of(p, V, Resident<T>::kBackward, true, true);
-        moe_combine_backward_kernel<T, VB><<<h.grid, h.block, 0, s>>>(p);
+        const Shape h = shape_of(p, V, Blocks::kBackward, true, true);
+        moe_combine_backward_kernel<T, VB, SHIFT><<<h.grid, h.block, 0, s>>>(p);
     }
     return cudaGetLastError();
 }
 
+// 16 bytes an access; rows that start anywhere are shifted into place, as long as they are
+// long enough for whole accesses between their ends.
 template <typename T>
 cudaError_t launch_t(Which which, const MoeRowsParams &p, cudaStream_t s) {
-    switch (access_bytes<T>(p)) {
-    case 16: return launch_vb<T, 16>(which, p, s);
-    case 4: return launch_vb<T, 4>(which, p, s);
-    default: return launch_vb<T, static_cast<int>(sizeof(T))>(which, p, s);
-    }
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    if (aligned_rows<T>(p)) return launch_vb<T, 16, false>(which, p, s);
+    if (p.n >= 8 * V) return launch_vb<T, 16, true>(which, p, s);
+    return launch_vb<T, static_cast<int>(sizeof(T)), false>(which, p, s);
 }
 
 cudaError_t launch_dt(int dt, Which which, const MoeRowsParams &p, cudaStream_t s) {

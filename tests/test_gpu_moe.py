@@ -367,6 +367,15 @@ def test_rows_in_routed_order(dtype, m, top_k, n):
     assert np.array_equal(fetch(out, b.rows, n, n, dtype), np.repeat(x, top_k, axis=0))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,top_k,E,n,pad,offset", [(9, 5, 7, 64, 1, 1), (6, 8, 8, 71, 0, 3), (5, 3, 4, 257, 2, 0),
+                                                    (3, 4, 4, 4097, 0, 0), (40, 2, 9, 333, 5, 2)])
+def test_rows_that_start_anywhere(dtype, m, top_k, E, n, pad, offset):
+    """Row starts of every alignment in one call, with whole accesses between the rows' ends."""
+    test_dispatch_and_its_gradient(dtype, m, top_k, E, n, pad, offset, 0.2)
+    check_combine(Rows(m, top_k, E, 0.2, n + 1), dtype, n, n + pad, offset)
+
+
 def check_combine(b, dtype, n, ld, offset):
     m, top_k, E = b.m, b.top_k, b.E
     ys = b.rng.standard_normal((b.rows, n))
