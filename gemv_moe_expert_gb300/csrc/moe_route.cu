@@ -373,11 +373,12 @@ cudaError_t launch_v(bool backward, MoeRouteParams p, cudaStream_t s) {
     // Several tokens a warp, as long as their slots fit into its lanes and there are 64 tokens an
     // SM: 8 of 128 experts, four a warp and one, forward: 2048 tokens 3.6 and 2.4 us, 8192
     // 5.0 and 4.3, 16384 6.8 and 6.8 (backward 5.7 and 7.0), 65536 20.5 and 23.0.  8 of 256
-    // experts, 32768 tokens: two a warp 17.1, one 19.7, four 17.8.
+    // experts, 32768 tokens: two a warp 17.1, one 19.7, four 17.8; 16 of 128 experts, 65536 tokens, two
+    // 26.5 (backward 17.1), one 28.3 (21.5).
     if constexpr (V <= 8) {
-        constexpr int N = V <= 4 ? 4 : 2;
         const bool many = p.m >= 64u * static_cast<uint32_t>(device_sm_count());
-        if (p.top_k <= 8 && many) return launch_n<T, V, N>(backward, p, s);
+        if (V <= 4 && p.top_k <= 8 && many) return launch_n<T, V, 4>(backward, p, s);
+        if (p.top_k <= 16 && many) return launch_n<T, V, 2>(backward, p, s);
     }
     return launch_n<T, V, 1>(backward, p, s);
 }

@@ -13,10 +13,10 @@
 // 4 tokens x 8 slots of 2048 5.1 to 6.4 each, a launch and two trips to memory.
 //
 // A block is a grid of tx x ty threads: tx along the row (one access of VB bytes
-// a thread and step), ty tokens.  Slots are taken in batches of B (4, or 8 for more
-// than 4 slots), all of a batch's loads issued before the first is used.  Blocks
-// stay and walk over the tokens: the places of the next token's slots are loaded
-// while the current token's rows are in flight.
+// a thread and step), ty tokens.  Slots are taken in batches of B, all of a batch's
+// loads issued before the first is used.  Blocks stay and walk over the tokens: the
+// places of the next token's slots are loaded while the current token's rows are in
+// flight.
 #include "device_common.cuh"
 
 namespace gbmm {
@@ -174,8 +174,8 @@ template <typename T, int VB, bool SHIFT>
 __device__ __forceinline__ Place place_of(const MoeRowsParams &p, const Columns &c, int64_t i, const T *row) {
     if (!SHIFT) return Place{i, i < c.to};
     constexpr int V = 16 / static_cast<int>(sizeof(T));
-    const int64_t first =
-        V + ((16u - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u)) & 15u) / static_cast<int>(sizeof(T));
+    const uint32_t past = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u;
+    const int64_t first = V + (16u - past) % 16u / static_cast<uint32_t>(sizeof(T));
     if (VB == 16) return Place{first + i, first + i + 2 * V <= p.n};
     const int64_t whole = p.n - 2 * V >= first ? (p.n - 2 * V - first) / V * V + V : 0;
     return Place{i < first ? i : i + whole, i < p.n - whole};
