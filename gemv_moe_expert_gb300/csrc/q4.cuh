@@ -218,6 +218,34 @@ __device__ __forceinline__ uint32_t list_rows(const Q4Params &p, uint32_t base_r
     return *s_count;
 }
 
+// Both for a window of at most 32 rows, which every warp sees at once: the distinct
+// experts in the order of their first rows, without a barrier (8 of 64 experts: 1 f32 token
+// 7.3 us for 7.5, 4 bf16 tokens 13.7 for 14.0).  `list` is valid after the next barrier.
+template <typename T>
+__device__ __forceinline__ bool find_in_warp(const Q4Params &p, uint32_t base_row, uint32_t d, int64_t j0, int tile_rows,
+                                             uint32_t *list, uint32_t &expert, uint32_t &count) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const uint32_t rows = p.rows - base_row;
+    const uint32_t id = lane < rows ? __ldg(p.ids + base_row + lane) : p.n_experts;
+    const bool has = id < p.n_experts;
+    const uint32_t same = __match_any_sync(kFull, id);
+    uint32_t firsts = __ballot_sync(kFull, has && (same & ((1u << lane) - 1u)) == 0u);
+    if (d == 0) {
+        for (uint32_t none = __ballot_sync(kFull, lane < rows && !has); none != 0u; none &= none - 1)
+            if (tid < tile_rows && j0 + tid < p.n)
+                static_cast<T *>(p.out)[static_cast<int64_t>(base_row + __ffs(none) - 1) * p.ldo + j0 + tid] =
+                    Elem<T>::from_f(0.f);
+    }
+    if (d >= __popc(firsts)) return false;
+    for (uint32_t skip = d; skip > 0; --skip) firsts &= firsts - 1;
+    const int src = __ffs(firsts) - 1;
+    expert = __shfl_sync(kFull, id, src);
+    const uint32_t mine = __shfl_sync(kFull, same, src);
+    count = __popc(mine);
+    if (tid < 32 && mine >> lane & 1u) list[__popc(mine & ((1u << lane) - 1u))] = base_row + lane;
+    return true;
+}
+
 // x of `tokens` rows, which start at offsets[] (in elements), columns k0 .. k0 + 8 words
 // - 1, into shared memory: f16 terms at stage + line * pitch, and for each block (half a
 // block with groups of 32) and mma column {factor, sum}: what undoes the scalings, and the
@@ -435,7 +463,13 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
 
     uint32_t expert = 0;
     const uint32_t base_row = blockIdx.z * kWindow;
-    if (by_id && !find_expert<T, kThreads>(p, base_row, blockIdx.y, j0, tile_rows, s_ids, s_bits, expert)) return;
+    const bool small = by_id && p.rows <= 32;
+    uint32_t listed = 0;
+    if (small) {
+        if (!find_in_warp<T>(p, base_row, blockIdx.y, j0, tile_rows, s_ids, expert, listed)) return;
+    } else if (by_id && !find_expert<T, kThreads>(p, base_row, blockIdx.y, j0, tile_rows, s_ids, s_bits, expert)) {
+        return;
+    }
 
     const int32_t row_len = static_cast<int32_t>((p.k + 1) / 2);
     const int32_t blocks = static_cast<int32_t>((p.k + 255) / 256);
@@ -576,7 +610,7 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
 
     const uint32_t first = by_id ? 0u : blockIdx.y * kPass;
     const uint32_t stride = by_id ? kPass : gridDim.y * kPass;
-    const uint32_t count = by_id ? list_rows(p, base_row, expert, s_ids, &s_count) : p.rows;
+    const uint32_t count = !by_id ? p.rows : small ? listed : list_rows(p, base_row, expert, s_ids, &s_count);
 
 #pragma unroll 1
     for (uint32_t t0 = first; t0 < count; t0 += stride) {
