@@ -198,6 +198,30 @@ __device__ __forceinline__ void grid_dep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A launch with programmatic stream serialisation: its blocks take the places that the
+// kernel before it leaves, in place of waiting for its last block.  The kernel begins with
+// grid_dep_begin().
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                         const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+// before the first access to global memory
+__device__ __forceinline__ void grid_dep_begin() {
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+}
+
 // Bring the 128-byte line holding p into L2, marked evict-last.
 __device__ __forceinline__ void prefetch_l2_evict_last(const void *p) {
     asm volatile("prefetch.global.L2::evict_last [%0];" ::"l"(p));

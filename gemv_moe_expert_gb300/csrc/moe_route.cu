@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(MoeRouteParams p) {
     __shared__ uint32_t slots[kWarps][N][kGroup];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, own = lane / kGroup;
     const uint32_t t0 = (blockIdx.x * kWarps + warp) * N;
+    grid_dep_begin();
     if (t0 >= p.m) return;
     float l[N][V], b[V], sums[N];
 #pragma unroll
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 2048 / kThreads : 0) moe_ro
     __shared__ __align__(16) float rows[kWarps][N][32 * V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, own = lane / kGroup;
     const uint32_t t0 = (blockIdx.x * kWarps + warp) * N;
+    grid_dep_begin();
     if (t0 >= p.m) return;
     // slot s of the n-th token in lane s of the n-th group
     const uint32_t slot = lane % kGroup;
@@ -357,6 +359,9 @@ bool runs_fit(const void *ptr, int64_t ld, uint32_t E, int W, int size) {
 template <typename T, int V, int N>
 cudaError_t launch_n(bool backward, const MoeRouteParams &p, cudaStream_t s) {
     const unsigned grid = (p.m + kWarps * N - 1) / (kWarps * N);
+    // early for many tokens (65536 tokens, both ways: 31.6 us, 32.6 otherwise; 4096: 6.3 and 5.5)
+    if (N > 1 && backward) return launch_early(moe_route_backward_kernel<T, V, N>, grid, kThreads, 0, s, p);
+    if (N > 1) return launch_early(moe_route_kernel<T, V, N>, grid, kThreads, 0, s, p);
     if (backward)
         moe_route_backward_kernel<T, V, N><<<grid, kThreads, 0, s>>>(p);
     else

@@ -223,6 +223,7 @@ template <typename T, int VB, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, Resident<T, SHIFT>::kDispatch)
     moe_dispatch_kernel(const __grid_constant__ MoeRowsParams p) {
     constexpr int V = VB / static_cast<int>(sizeof(T));
+    grid_dep_begin();
     const uint32_t valid = valid_rows(p);
     const uint64_t step = static_cast<uint64_t>(gridDim.x) * blockDim.y;
     uint64_t t = static_cast<uint64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -280,6 +281,7 @@ template <typename T, int VB, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, Resident<T, SHIFT>::kCombine)
     moe_combine_kernel(const __grid_constant__ MoeRowsParams p) {
     constexpr int V = VB / static_cast<int>(sizeof(T));
+    grid_dep_begin();
     const uint32_t valid = valid_rows(p);
     const uint64_t step = static_cast<uint64_t>(gridDim.x) * blockDim.y;
     uint64_t t = static_cast<uint64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -395,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, Resident<T, SHIFT>::kBackward)
     constexpr int V = VB / static_cast<int>(sizeof(T));
     __shared__ float part[2][kThreads / 32][B];
     const int lane = threadIdx.x & 31;
+    grid_dep_begin();
     const uint32_t valid = valid_rows(p);
     const uint64_t step = static_cast<uint64_t>(gridDim.x) * blockDim.y;
     const int warps = blockDim.x / 32, first_warp = threadIdx.y * warps, warp = first_warp + threadIdx.x / 32;
@@ -480,21 +483,22 @@ Shape shape_of(const MoeRowsParams &p, int V, int resident, bool stays, bool row
 
 enum Which { kDispatch, kCombine, kCombineBackward };
 
+// Started early: dispatch after the sort 52.6 us a pair for 54.8 (4096 tokens x 8 slots x 4096
+// bf16), the gradients of combine and dispatch 143.6 for 146.1 (8192 tokens x 8 slots x 2048 bf16).
 template <typename T, int VB, bool SHIFT>
 cudaError_t launch_vb(Which which, const MoeRowsParams &p, cudaStream_t s) {
     constexpr int V = VB / static_cast<int>(sizeof(T));
     using Blocks = Resident<T, SHIFT>;
     if (which == kDispatch) {
         const Shape h = shape_of(p, V, Blocks::kDispatch, false, false);
-        moe_dispatch_kernel<T, VB, SHIFT><<<h.grid, h.block, 0, s>>>(p);
+        return launch_early(moe_dispatch_kernel<T, VB, SHIFT>, h.grid, h.block, 0, s, p);
     } else if (which == kCombine) {
         const Shape h = shape_of(p, V, Blocks::kCombine, true, false);
-        moe_combine_kernel<T, VB, SHIFT><<<h.grid, h.block, 0, s>>>(p);
+        return launch_early(moe_combine_kernel<T, VB, SHIFT>, h.grid, h.block, 0, s, p);
     } else {
         const Shape h = shape_of(p, V, Blocks::kBackward, true, true);
-        moe_combine_backward_kernel<T, VB, SHIFT><<<h.grid, h.block, 0, s>>>(p);
+        return launch_early(moe_combine_backward_kernel<T, VB, SHIFT>, h.grid, h.block, 0, s, p);
     }
-    return cudaGetLastError();
 }
 
 // 16 bytes an access; rows that start anywhere are shifted into place, as long as they are

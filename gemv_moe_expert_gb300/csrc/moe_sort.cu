@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_sort_cluster_kernel(const __g
     const uint32_t keys = p.n_experts + 1, rank = cluster.block_rank(), tiles = cluster.num_blocks();
     uint32_t *total = smem, *first = smem + keys;  // over the masks, which are done with by then
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    grid_dep_begin();
     Tile<kClusterP> tile;
     tile.load(p, rank, smem, total);
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA runs: its shared memory can be written
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_sort_place_kernel(MoeSortPara
     __shared__ uint32_t warp_sums[kWarps];
     const uint32_t keys = p.n_experts + 1, tiles = gridDim.x;
     uint32_t *total = smem, *first = smem + keys;  // over the masks, which are done with by then
+    grid_dep_launch_dependents();
     Tile<kLargeP> tile;
     tile.load(p, blockIdx.x, smem, total);
     grid_dep_wait();
@@ -284,38 +286,27 @@ cudaError_t launch_moe_sort(int step, const MoeSortParams &p, cudaStream_t s) {
         cfg.blockDim = dim3(kThreads, 1, 1);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = s;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = tiles;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         return cudaLaunchKernelEx(&cfg, moe_sort_cluster_kernel, p);
     }
     const unsigned tiles = static_cast<unsigned>(tiles_of(p.rows, kLargeP));
     if (step == 0) {
+        // not early: the kernel two launches on reads the ids before it waits
         moe_sort_count_kernel<<<tiles, kThreads, 0, s>>>(p);
         return cudaGetLastError();
     }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = s;
-    if (step == 1) {
-        cfg.gridDim = dim3((keys + 7) / 8, 1, 1);
-        cfg.blockDim = dim3(256, 1, 1);
-        return cudaLaunchKernelEx(&cfg, moe_sort_scan_kernel, p, static_cast<uint32_t>(tiles));
-    }
+    if (step == 1) return launch_early(moe_sort_scan_kernel, (keys + 7) / 8, 256, 0, s, p, tiles);
     const cudaError_t e = allow(moe_sort_place_kernel, false, &place_done);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(tiles, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    return cudaLaunchKernelEx(&cfg, moe_sort_place_kernel, p);
+    return launch_early(moe_sort_place_kernel, tiles, kThreads, smem, s, p);
 }
 
 }  // namespace gbmm

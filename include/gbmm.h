@@ -24,7 +24,8 @@
  *     modules, which a capture does not allow); replays read whatever
  *     the captured buffers hold.  GroupedPrefill's grouped kernel is launched
  *     with programmatic stream serialisation behind the map kernel and waits
- *     for it before touching global memory, which a capture keeps.  Not with
+ *     for it before touching global memory, which a capture keeps; the kernels
+ *     of gbmm_moe_* are behind whatever precedes them.  Not with
  *     GBMM_DEBUG_SYNC=1 (it synchronises the stream).
  *   - Debugging: with the environment variable GBMM_DEBUG_SYNC=1 (read once
  *     per process) every launch is followed by a stream synchronisation, so a

@@ -517,3 +517,42 @@ def test_another_stream_and_graph_capture():
         graph.replay()
         torch.cuda.synchronize()
         verify()
+
+
+@pytest.mark.parametrize("m,n", [(40, 96), (2500, 1024)])
+def test_calls_back_to_back_on_the_same_buffers(m, n):
+    """Router to combine and back again and again without a wait in between, every
+    buffer overwritten by the next turn: the results are those of turns on their own."""
+    E, k, turns = 16, 4, 12
+    g = torch.Generator(device="cuda").manual_seed(m)
+    xs_in = torch.randn(turns, m, n, generator=g, device="cuda")
+    logits_in = torch.randn(turns, m, E, generator=g, device="cuda")
+    new = lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device="cuda")  # noqa: E731
+    x, logits, y, d_x = new(m, n), new(m, E), new(m, n), new(m, n)
+    ids, w, d_w = new(m, k, dtype=torch.int32), new(m, k), new(m, k)
+    offsets, order, position = (new(c, dtype=torch.int32) for c in (E + 1, m * k, m * k))
+    xs, d_xs = new(m * k, n), new(m * k, n)
+    st, nbytes = gb.gbmm_moe_sort_scratch_bytes(m, k, E)
+    gb.check(st)
+    scratch = new(max(nbytes, 1), dtype=torch.uint8)
+
+    def turn(i):
+        x.copy_(xs_in[i])
+        logits.copy_(logits_in[i])
+        gb.check(gb.gbmm_moe_route("f32", m, E, k, gb.SOFTMAX_ALL, logits, E, None, ids, w))
+        gb.check(gb.gbmm_moe_sort(m, k, E, ids, offsets, order, position, scratch, nbytes))
+        gb.check(gb.gbmm_moe_dispatch("f32", m, k, E, n, x, n, position, offsets, xs, n))
+        gb.check(gb.gbmm_moe_combine("f32", m, k, E, n, xs, n, w, position, offsets, y, n))
+        gb.check(gb.gbmm_moe_combine_backward("f32", m, k, E, n, xs, n, w, position, offsets, y, n, d_xs, n, d_w))
+        gb.check(gb.gbmm_moe_dispatch_backward("f32", m, k, E, n, d_xs, n, position, offsets, d_x, n))
+        return y.clone(), d_x.clone(), d_w.clone()
+    alone = []
+    for i in range(turns):
+        alone.append(turn(i))
+        torch.cuda.synchronize()
+    together = [turn(i) for i in range(turns)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, together):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+    total = torch.softmax(logits_in[-1].double(), 1).topk(k).values.sum(1, keepdim=True)
+    assert ((together[-1][0].double() - total * xs_in[-1].double()).abs() <= 1e-5 * xs_in[-1].abs() + 1e-30).all()
