@@ -14,10 +14,11 @@
 // a warp takes several of them, so that what concerns the slots is done for all at once.
 //
 // Measured (us forward / backward): 65536 tokens, 8 of 128 experts, f32, softmax over all
-// 20.5 (288 instructions a token) / 15.2 (155); one token a warp 23.0 / 21.2; and with
+// 20.0 (288 instructions a token) / 14.9 (155); one token a warp 23.0 / 21.2; and with
 // registers moved up in place of lists, two reductions a step and the logits read again
-// 27 / 20.5.  The same with bf16, a bias and softmax over the chosen 18.5 / 7.0; 2 of 64 experts
-// 10.1 / 10.0; 32768 tokens, 8 of 256 experts, bf16 17.1 / 9.1; 2048 tokens, 8 of 64 2.4 / 1.9.
+// 27 / 20.5.  The same with bf16, a bias and softmax over the chosen 18.2 / 7.3; 2 of 64 experts
+// 9.8 / 9.5; 32768 tokens, 8 of 256 experts, bf16 16.8 / 7.3; 15762 tokens, 15 of 512 23.9 / 15.4;
+// 2048 tokens, 8 of 64 2.4 / 1.9.
 #include "device_common.cuh"
 
 namespace gbmm {
@@ -45,12 +46,13 @@ __device__ __forceinline__ float warp_max(float v) {
     return m;
 }
 
-// Lane `lane` holds experts expert_of(lane, 0..V-1), increasing: V neighbours, or
-// with more than 8 runs of W neighbours, 32 W apart.
-template <int V> struct Lanes {
+// Lane `lane` holds experts expert_of(lane, 0..V-1), increasing: V neighbours where lists
+// of sorted keys are made (an earlier lane's experts lie before a later one's), else runs
+// of W neighbours, 32 W apart.
+template <int V, bool LISTS> struct Lanes {
     static constexpr int W = V < 4 ? V : 4;
     __device__ static __forceinline__ uint32_t expert_of(int lane, int j) {
-        return static_cast<uint32_t>(V <= 8 ? lane * V + j : j / W * 32 * W + lane * W + j % W);
+        return static_cast<uint32_t>(LISTS ? lane * V + j : j / W * 32 * W + lane * W + j % W);
     }
 };
 
@@ -59,12 +61,12 @@ template <typename T, int W> struct alignas(sizeof(T) * W) Run {
 };
 
 // row[expert_of(lane, j)] for every j, `fill` past the row's E elements; vec: whole runs can be read
-template <typename T, int V>
+template <bool LISTS, typename T, int V>
 __device__ __forceinline__ void load_lanes(const T *row, uint32_t E, int lane, bool vec, float fill, float (&out)[V]) {
-    constexpr int W = Lanes<V>::W;
+    constexpr int W = Lanes<V, false>::W;
 #pragma unroll
     for (int c = 0; c < V / W; ++c) {
-        const uint32_t e = Lanes<V>::expert_of(lane, c * W);
+        const uint32_t e = Lanes<V, LISTS>::expert_of(lane, c * W);
         if (vec) {
             Run<T, W> r;
             if (e < E) r = *reinterpret_cast<const Run<T, W> *>(row + e);
@@ -78,14 +80,14 @@ __device__ __forceinline__ void load_lanes(const T *row, uint32_t E, int lane, b
 }
 
 // row[expert_of(lane, j)] = v[j], in shared memory
-template <int V> __device__ __forceinline__ void store_lanes(float *row, int lane, const float (&v)[V]) {
-    constexpr int W = Lanes<V>::W;
+template <bool LISTS, int V> __device__ __forceinline__ void store_lanes(float *row, int lane, const float (&v)[V]) {
+    constexpr int W = Lanes<V, false>::W;
 #pragma unroll
     for (int c = 0; c < V / W; ++c) {
         Run<float, W> r;
 #pragma unroll
         for (int i = 0; i < W; ++i) r.v[i] = v[c * W + i];
-        *reinterpret_cast<Run<float, W> *>(row + Lanes<V>::expert_of(lane, c * W)) = r;
+        *reinterpret_cast<Run<float, W> *>(row + Lanes<V, LISTS>::expert_of(lane, c * W)) = r;
     }
 }
 
@@ -161,7 +163,7 @@ __device__ __forceinline__ void select(const uint32_t (&key)[V], uint2 (*list)[3
         }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) list[rank[j]][lane] = make_uint2(key[j], Lanes<V>::expert_of(lane, j));
+    for (int j = 0; j < V; ++j) list[rank[j]][lane] = make_uint2(key[j], Lanes<V, true>::expert_of(lane, j));
     // one step: the largest head wins, and its lane moves on
     const uint32_t before = (1u << lane) - 1u;
     const uint2 *head = &list[0][lane];
@@ -180,8 +182,8 @@ __device__ __forceinline__ void select(const uint32_t (&key)[V], uint2 (*list)[3
     __syncwarp();
 }
 
-// The same with more than 8 experts a lane, where sorting them costs more than a look at all
-// of them in each step (with 8 a look costs more: 29.7 us for 19.7 for 32768 tokens).
+// The same by a look at all of a lane's experts in each step (with 8 experts a lane 29.7 us for
+// 19.7 for 32768 tokens).
 template <int V>
 __device__ __forceinline__ void select_scan(uint32_t (&key)[V], uint32_t top_k, int lane, uint32_t *slot) {
     for (uint32_t s = 0; s < top_k; ++s) {
@@ -195,24 +197,23 @@ __device__ __forceinline__ void select_scan(uint32_t (&key)[V], uint32_t top_k, 
         }
         const uint32_t most = __reduce_max_sync(kFull, best);
         if (most == 0u) break;
-        const uint32_t own = static_cast<uint32_t>(Lanes<V>::expert_of(lane, 0)) + at / 4 * 128 + at % 4;
+        const uint32_t own = static_cast<uint32_t>(Lanes<V, false>::expert_of(lane, 0)) + at / 4 * 128 + at % 4;
         const uint32_t e = __reduce_min_sync(kFull, best == most ? own : kFull);
         if (lane == 0) slot[s] = e;
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (Lanes<V>::expert_of(lane, j) == e) key[j] = 0u;
+            if (Lanes<V, false>::expert_of(lane, j) == e) key[j] = 0u;
     }
     __syncwarp();
 }
 
 // A warp takes N tokens; what is done for each slot is done for all of them at once,
 // slot s of the n-th token in lane s of the n-th group of 32 / N lanes.
-template <typename T, int V, int N>
+template <typename T, int V, int N, bool LISTS>
 __global__ void __launch_bounds__(kThreads) moe_route_kernel(MoeRouteParams p) {
     constexpr int kGroup = 32 / N;
-    constexpr bool kLists = V <= 8;
     __shared__ __align__(16) float rows[kWarps][N][32 * V];  // what the weights are made of
-    __shared__ uint2 lists[kLists ? kWarps : 1][kLists ? V + 1 : 1][32];
+    __shared__ uint2 lists[LISTS ? kWarps : 1][LISTS ? V + 1 : 1][32];
     __shared__ uint32_t slots[kWarps][N][kGroup];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, own = lane / kGroup;
     const uint32_t t0 = (blockIdx.x * kWarps + warp) * N;
@@ -222,22 +223,22 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(MoeRouteParams p) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const uint32_t t = min(t0 + n, p.m - 1);
-        load_lanes<T, V>(static_cast<const T *>(p.logits) + static_cast<int64_t>(t) * p.ld_logits, p.n_experts, lane,
+        load_lanes<LISTS, T, V>(static_cast<const T *>(p.logits) + static_cast<int64_t>(t) * p.ld_logits, p.n_experts, lane,
                          p.logits_vec != 0, neg_inf(), l[n]);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) b[j] = 0.f;
-    if (p.bias != nullptr) load_lanes<float, V>(p.bias, p.n_experts, lane, p.bias_vec != 0, 0.f, b);
+    if (p.bias != nullptr) load_lanes<LISTS, float, V>(p.bias, p.n_experts, lane, p.bias_vec != 0, 0.f, b);
     slots[warp][own][lane % kGroup] = p.n_experts;
-    if (kLists) lists[warp][V][lane] = make_uint2(0u, 0u);
+    if (LISTS) lists[warp][V][lane] = make_uint2(0u, 0u);
     __syncwarp();
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         uint32_t key[V];
         keys_of<V>(l[n], b, key);
         if (!p.selected) sums[n] = softmax_terms<V>(l[n]);
-        store_lanes<V>(rows[warp][n], lane, l[n]);
-        if constexpr (kLists)
+        store_lanes<LISTS, V>(rows[warp][n], lane, l[n]);
+        if constexpr (LISTS)
             select<V>(key, lists[warp], p.top_k, lane, slots[warp][n]);
         else
             select_scan<V>(key, p.top_k, lane, slots[warp][n]);
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(MoeRouteParams p) {
 // (32 registers with up to 4 experts a lane: 8.1 us for 7.0 with more; 65536 tokens of bf16)
 template <typename T, int V, int N>
 __global__ void __launch_bounds__(kThreads, V <= 4 ? 2048 / kThreads : 0) moe_route_backward_kernel(MoeRouteParams p) {
-    constexpr int W = Lanes<V>::W, kGroup = 32 / N;
+    constexpr int W = Lanes<V, false>::W, kGroup = 32 / N;
     __shared__ __align__(16) float rows[kWarps][N][32 * V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, own = lane / kGroup;
     const uint32_t t0 = (blockIdx.x * kWarps + warp) * N;
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 2048 / kThreads : 0) moe_ro
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const uint32_t t = min(t0 + n, p.m - 1);
-            load_lanes<T, V>(static_cast<const T *>(p.logits) + static_cast<int64_t>(t) * p.ld_logits, p.n_experts,
+            load_lanes<false, T, V>(static_cast<const T *>(p.logits) + static_cast<int64_t>(t) * p.ld_logits, p.n_experts,
                              lane, p.logits_vec != 0, neg_inf(), l[n]);
         }
     }
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 2048 / kThreads : 0) moe_ro
 #pragma unroll
     for (int j = 0; j < V; ++j) zeros[j] = 0.f;
 #pragma unroll
-    for (int n = 0; n < N; ++n) store_lanes<V>(rows[warp][n], lane, zeros);
+    for (int n = 0; n < N; ++n) store_lanes<false, V>(rows[warp][n], lane, zeros);
     const float dot = group_sum<N>(w * d);
     __syncwarp();
     if (id < p.n_experts) rows[warp][own][id] = p.selected ? w * (d - dot) : d;
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 2048 / kThreads : 0) moe_ro
         float b[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) b[j] = 0.f;
-        if (p.bias != nullptr) load_lanes<float, V>(p.bias, p.n_experts, lane, p.bias_vec != 0, 0.f, b);
+        if (p.bias != nullptr) load_lanes<false, float, V>(p.bias, p.n_experts, lane, p.bias_vec != 0, 0.f, b);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             uint32_t key[V];
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 2048 / kThreads : 0) moe_ro
         T *row = static_cast<T *>(p.d_logits) + static_cast<int64_t>(t0 + n) * p.ld_d_logits;
 #pragma unroll
         for (int c = 0; c < V / W; ++c) {
-            const uint32_t e = Lanes<V>::expert_of(lane, c * W);
+            const uint32_t e = Lanes<V, false>::expert_of(lane, c * W);
             const Run<float, W> r = *reinterpret_cast<const Run<float, W> *>(rows[warp][n] + e);
             float g[W];
 #pragma unroll
@@ -359,19 +360,28 @@ bool runs_fit(const void *ptr, int64_t ld, uint32_t E, int W, int size) {
 template <typename T, int V, int N>
 cudaError_t launch_n(bool backward, const MoeRouteParams &p, cudaStream_t s) {
     const unsigned grid = (p.m + kWarps * N - 1) / (kWarps * N);
-    // early for many tokens (65536 tokens, both ways: 31.6 us, 32.6 otherwise; 4096: 6.3 and 5.5)
-    if (N > 1 && backward) return launch_early(moe_route_backward_kernel<T, V, N>, grid, kThreads, 0, s, p);
-    if (N > 1) return launch_early(moe_route_kernel<T, V, N>, grid, kThreads, 0, s, p);
-    if (backward)
-        moe_route_backward_kernel<T, V, N><<<grid, kThreads, 0, s>>>(p);
-    else
-        moe_route_kernel<T, V, N><<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    // Started early when there are many waves of blocks (128 experts, both ways, early and not: 65536
+    // tokens 31.7 us and 32.6; 16384 16.0 and 12.5, as blocks that come early crowd a few SMs).
+    const bool early = p.m >= 256u * static_cast<uint32_t>(device_sm_count());
+    auto start = [&](void (*kernel)(MoeRouteParams)) {
+        if (early) return launch_early(kernel, grid, kThreads, 0, s, p);
+        kernel<<<grid, kThreads, 0, s>>>(p);
+        return cudaGetLastError();
+    };
+    if (backward) return start(moe_route_backward_kernel<T, V, N>);
+    // Sorted lists with up to 8 experts a lane; with 16 they cost more than a look at all of them
+    // in each step does until there are some steps (15762 tokens, 512 experts: 2 slots 20.7 us
+    // and 13.8, 8 slots 21.9 and 26.8, 15 slots 23.8 and 42.4).
+    if constexpr (V <= 8) return start(moe_route_kernel<T, V, N, true>);
+    if constexpr (V == 16) {
+        if (p.top_k > 5) return start(moe_route_kernel<T, V, N, true>);
+    }
+    if constexpr (V > 8) return start(moe_route_kernel<T, V, N, false>);
 }
 
 template <typename T, int V>
 cudaError_t launch_v(bool backward, MoeRouteParams p, cudaStream_t s) {
-    constexpr int W = Lanes<V>::W;
+    constexpr int W = Lanes<V, false>::W;
     p.logits_vec = runs_fit(p.logits, p.ld_logits, p.n_experts, W, sizeof(T));
     p.bias_vec = runs_fit(p.bias, W, p.n_experts, W, sizeof(float));
     p.d_logits_vec = runs_fit(p.d_logits, p.ld_d_logits, p.n_experts, W, sizeof(T));

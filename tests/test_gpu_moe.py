@@ -196,7 +196,7 @@ def test_route_masked_experts_and_empty_rows(dtype, selected):
 
 
 @pytest.mark.parametrize("dtype,E,top_k,selected", [("f32", 128, 8, False), ("f32", 6, 3, True), ("bf16", 64, 1, False),
-                                                    ("f16", 101, 7, True), ("bf16", 200, 8, False), ("f32", 40, 16, True), ("f16", 256, 13, False)])
+                                                    ("f16", 101, 7, True), ("bf16", 200, 8, False), ("f32", 40, 16, True), ("f16", 256, 13, False), ("f32", 300, 6, True)])
 def test_route_many_tokens(dtype, E, top_k, selected):
     """A batch from which a warp takes several tokens, the last warp fewer; equal,
     masked and empty rows lie among the others."""
