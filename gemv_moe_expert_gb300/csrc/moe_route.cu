@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(MoeRouteParams p) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const uint32_t t = min(t0 + n, p.m - 1);
-        load_lanes<LISTS, T, V>(static_cast<const T *>(p.logits) + static_cast<int64_t>(t) * p.ld_logits, p.n_experts, lane,
-                         p.logits_vec != 0, neg_inf(), l[n]);
+        load_lanes<LISTS, T, V>(static_cast<const T *>(p.logits) + static_cast<int64_t>(t) * p.ld_logits, p.n_experts,
+                                lane, p.logits_vec != 0, neg_inf(), l[n]);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) b[j] = 0.f;
@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 2048 / kThreads : 0) moe_ro
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const uint32_t t = min(t0 + n, p.m - 1);
-            load_lanes<false, T, V>(static_cast<const T *>(p.logits) + static_cast<int64_t>(t) * p.ld_logits, p.n_experts,
-                             lane, p.logits_vec != 0, neg_inf(), l[n]);
+            const T *row = static_cast<const T *>(p.logits) + static_cast<int64_t>(t) * p.ld_logits;
+            load_lanes<false, T, V>(row, p.n_experts, lane, p.logits_vec != 0, neg_inf(), l[n]);
         }
     }
     float zeros[V];

@@ -43,9 +43,9 @@
 // Measured (us, and GB/s of codes, scales, zeros, x and y; inputs rotate past L2):
 //   dense 11008 x 4096, groups of 128, 1 row     f16 9.5 (2440)   f32 10.4 (2250)
 //   the same, 4 f16 rows 13.0, 16 f16 rows 25.7, 8 f32 rows 28.2
-//   4 tokens x 8 of 64 experts, 1408 x 2048      bf16 14.0 (2970)   f32 18.3 (2290)
-//   16 tokens x 8 of 128 experts, 1536 x 4096: bf16, groups of 32 with zeros 79.3 (3870);
-//   bf16, groups of 128 62.6 (4360); f32, groups of 128 96.8 (2830)
+//   4 tokens x 8 of 64 experts, 1408 x 2048      bf16 13.7 (3040)   f32 18.0 (2320)
+//   16 tokens x 8 of 128 experts, 1536 x 4096: bf16, groups of 32 with zeros 77.4 (3970);
+//   bf16, groups of 128 62.2 (4390); f32, groups of 128 96.7 (2830)
 // The large ones issue in more than half of the cycles, half of it the ANDs and shifts that
 // unpack the codes, and a warp waits as often for HBM as for the instructions before; the
 // last case but one takes 56.6 when x is not staged, 53.7 when nothing is multiplied.  The small
@@ -222,8 +222,8 @@ __device__ __forceinline__ uint32_t list_rows(const Q4Params &p, uint32_t base_r
 // experts in the order of their first rows, without a barrier (8 of 64 experts: 1 f32 token
 // 7.3 us for 7.5, 4 bf16 tokens 13.7 for 14.0).  `list` is valid after the next barrier.
 template <typename T>
-__device__ __forceinline__ bool find_in_warp(const Q4Params &p, uint32_t base_row, uint32_t d, int64_t j0, int tile_rows,
-                                             uint32_t *list, uint32_t &expert, uint32_t &count) {
+__device__ __forceinline__ bool find_in_warp(const Q4Params &p, uint32_t base_row, uint32_t d, int64_t j0,
+                                             int tile_rows, uint32_t *list, uint32_t &expert, uint32_t &count) {
     const int tid = threadIdx.x, lane = tid & 31;
     const uint32_t rows = p.rows - base_row;
     const uint32_t id = lane < rows ? __ldg(p.ids + base_row + lane) : p.n_experts;
@@ -430,7 +430,7 @@ __device__ __forceinline__ uint4 load_unaligned(bool pred, const uint8_t *p) {
 //            (groups of 32: two by two)
 //   kAtOnce  and the scales of a lane, and its zero points, can be read at once
 // Measured, 16 bf16 tokens x 8 of 128 experts, groups of 128 (of 32, with zeros): 1536 x 4096,
-// kAtOnce, 62.3 us (79.5); 1537 x 4090 with rows 2048 bytes apart, kLoose, 84.5 (149); with rows
+// kAtOnce, 62.2 us (77.4); 1537 x 4090 with rows 2048 bytes apart, kLoose, 84.5 (149); with rows
 // 2045 bytes apart, kAnyhow, 177 (243).  Dense 1 f16 row, groups of 128: 11008 x 4224 (33 groups),
 // kApart, 11.0; 11009 x 4098 kLoose 12.3, kAnyhow 19.0.
 enum Access { kAnyhow, kLoose, kApart, kAtOnce };
@@ -767,15 +767,17 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     }
     if (gz > 65535u) return cudaErrorInvalidConfiguration;
     Launch cfg{};
-    // Warps that split the columns: enough for 16 warps an SM (8 where a pass takes more than
-    // one column tile, as the staging of its rows is repeated for each CTA), and no warp
-    // with 16 blocks or more, so that the last CTAs are short.  Measured: 8 an SM 11.4 us for
-    // 9.5 (dense, 1 f16 row) and 23.0 for 18.3 (4 f32 tokens x 8 of 64 experts); 16 an SM with
-    // more column tiles 34.6 for 28.4 (8 f32 rows); without the second rule 111 for 96 (16 f32
-    // tokens x 8 of 128 experts, 16 blocks) and 90.5 for 79.5 (bf16, groups of 32), with at most
-    // 7 blocks a warp 108 and 83.4.
+    // Warps that split the columns: enough for 16 warps an SM (8, and 4 with f32, where a pass
+    // takes more than one column tile, as the staging of its rows is repeated for each CTA),
+    // and no warp with 16 blocks or more, so that the last CTAs are short.  Measured: 8 an SM
+    // 11.4 us for 9.5 (dense, 1 f16 row) and 23.0 for 18.3 (4 f32 tokens x 8 of 64 experts); 16
+    // an SM with more column tiles 34.6 for 28.4 (8 f32 rows), 8 and 2 with f32 61.8 and 67.2
+    // for 51.2 (6 tokens x 8 of 13 experts, 1472 x 3200, groups of 32); without the second rule
+    // 111 for 96 (16 f32 tokens x 8 of 128 experts, 16 blocks) and 90.5 for 79.5 (bf16, groups
+    // of 32), with at most 7 blocks a warp 108 and 83.4.
     int wk = 1;
-    while (wk < kWarps && wk < blocks && (tiles * gy * wk < (NT == 1 ? 16LL : 8LL) * num_sms || blocks >= 16 * wk)) {
+    constexpr int64_t kEnough = NT == 1 ? 16 : K == kFloat ? 4 : 8;
+    while (wk < kWarps && wk < blocks && (tiles * gy * wk < kEnough * num_sms || blocks >= 16 * wk)) {
         wk *= 2;
         ++cfg.wk_log;
     }
