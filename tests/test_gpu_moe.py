@@ -212,6 +212,12 @@ def test_route_many_tokens(dtype, E, top_k, selected):
     check_route(logits, dtype, top_k, selected, bias=bias if E != 128 else None, ld=E + E % 4)
 
 
+def test_route_many_waves_of_tokens():
+    rng = np.random.default_rng(8)
+    m = 256 * torch.cuda.get_device_properties(0).multi_processor_count + 5
+    check_route(rng.standard_normal((m, 12)), "f16", 2, False)
+
+
 def test_route_infinite_live_logit_gives_nan_weights():
     logits = np.zeros((1, 8))
     logits[0, 3] = np.inf
@@ -519,7 +525,7 @@ def test_another_stream_and_graph_capture():
         verify()
 
 
-@pytest.mark.parametrize("m,n", [(40, 96), (2500, 1024)])
+@pytest.mark.parametrize("m,n", [(40, 96), (2500, 1024), (40000, 24)])
 def test_calls_back_to_back_on_the_same_buffers(m, n):
     """Router to combine and back again and again without a wait in between, every
     buffer overwritten by the next turn: the results are those of turns on their own."""
