@@ -700,7 +700,8 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
                                 for (int i = 0; i < 4; ++i) {
                                     const float factor = i & 1 ? f.z : f.x, sum = i & 1 ? f.w : f.y;
                                     float &a = acc[m][t][i];
-                                    a = fmaf(s[i >> 1][i & 1] * factor, part[m][t][i], a);
+                                    // (the scale times the factor could pass the range of f32)
+                                    a = fmaf(s[i >> 1][i & 1], factor * part[m][t][i], a);
                                     a = fmaf(sz[i >> 1][i & 1], sum, a);
                                 }
                             }

@@ -1,0 +1,83 @@
+"""GPU parity of the 4-bit matrix-vector products where values are very large or
+small, and where the weights are zero or x has one sign, against the dequantised product
+in 64 bits.
+
+Tolerances are those of test_gpu_q4.py, relative to sum |w x|.
+"""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from gemv_moe_expert_gb300 import binding as gb  # noqa: E402
+from gemv_moe_expert_gb300 import synth  # noqa: E402
+from tests import moe_ref  # noqa: E402
+from tests.gpu_util import DevBuf, to_f64  # noqa: E402
+from tests.test_gpu_moe import TINY, UO, empty, fetch, ints, near, strided  # noqa: E402
+from tests.test_gpu_q4 import tau  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from gemv_moe_expert_gb300 import build
+    build.build()
+    gb.load()
+    torch.cuda.init()
+
+
+def signed(rng, shape, low, high):
+    """Magnitudes between low and high, of either sign."""
+    return rng.choice([-1.0, 1.0], shape) * rng.uniform(low, high, shape)
+
+
+def product(dtype, x, codes, scales, scale_dt, group, zeros=None, by_id=False):
+    """The library's result, x and the matrix in 64 bits; codes [n, k], scales and zeros [n, G].
+    by_id: through the per-expert call, as the second of two experts."""
+    m, (n, k) = x.shape[0], codes.shape
+    xb, xp, xv = strided(x, k, dtype)
+    packed = moe_ref.pack_q4(codes)
+    stored = synth._store(scales.astype(np.float32), scale_dt)
+    w = moe_ref.q4_matrix(packed, to_f64(stored, scale_dt), zeros, k, group)
+    copies = 2 if by_id else 1
+    qb = DevBuf(packed.nbytes * copies, host=np.stack([packed] * copies))
+    sb = DevBuf(stored.nbytes * copies, host=np.stack([stored] * copies))
+    zb = None if zeros is None else DevBuf(zeros.nbytes * copies, host=np.stack([zeros] * copies))
+    out, outp = empty(m, n, dtype)
+    ldq, z = (k + 1) // 2, None if zb is None else zb.ptr
+    if by_id:
+        ib = ints(np.ones((m, 1)))
+        gb.check(gb.gbmm_matmul_id_q4(dtype, m, n, k, 1, 2, gb.INPUT_SHARED_PER_TOKEN, group, qb.ptr, ldq, n * ldq,
+                                      sb.ptr, scale_dt, z, xp, ib.ptr, outp))
+    else:
+        gb.check(gb.gbmm_gemv_q4(dtype, m, n, k, group, qb.ptr, ldq, sb.ptr, scale_dt, z, xp, k, outp, n))
+    return fetch(out, m, n, n, dtype), xv, w
+
+
+def agree(got, x, w, dtype, relative, what, extra=0.0):
+    ref, mag = x @ w.T, np.abs(x) @ np.abs(w).T
+    near(got, ref, relative * mag + UO[dtype] * np.abs(ref) + TINY[dtype] * (mag > 0) + extra, what)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale_dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("by_id", [False, True])
+def test_large_values_times_large_scales(dtype, scale_dt, group, by_id):
+    """Eight values of x a row up to 2^116, scales from 4 up, up to 2^119 together: every sum of terms stays
+    below 2^127.1 whatever the signs, so the results are finite."""
+    rng = np.random.default_rng(11)
+    n, k = 40, 512
+    for e, t in ((116, 2), (112, 6), (104, 15), (116, 3)):
+        x = np.zeros((3, k))
+        for row in x:
+            row[rng.choice(k, 8, replace=False)] = signed(rng, 8, 1.0, 1.5) * 2.0 ** e
+        codes = rng.integers(0, 16, (n, k)).astype(np.uint8)
+        codes[0], codes[1] = 0, 15
+        scales = rng.uniform(1.0, 1.5, (n, k // group)) * 2.0 ** t
+        got, xv, w = product(dtype, x, codes, scales, scale_dt, group, by_id=by_id)
+        agree(got, xv, w, dtype, tau(dtype, k, group), (e, t))
