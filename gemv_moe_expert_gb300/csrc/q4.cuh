@@ -331,7 +331,8 @@ __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, co
     }
 }
 
-// One output in plain f32, for a row of x that cannot be scaled.
+// One output in plain f32, for a row of x that cannot be scaled: each weight first, as a group's
+// sum of codes times x could pass the range of f32 where the result does not.
 template <typename T>
 __device__ __noinline__ float plain_output(const Q4Params &p, uint32_t expert, int64_t j, uint32_t r) {
     const uint8_t *q = p.q + static_cast<int64_t>(expert) * p.expert_stride + j * p.ldq;
@@ -347,8 +348,8 @@ __device__ __noinline__ float plain_output(const Q4Params &p, uint32_t expert, i
         const int64_t end = (g + 1) * p.group < p.k ? (g + 1) * p.group : p.k;
         float part = 0.f;
         for (int64_t i = g * p.group; i < end; ++i)
-            part = fmaf(static_cast<float>((q[i >> 1] >> (4 * (i & 1))) & 15) - z, Elem<T>::to_f(x[i]), part);
-        acc = fmaf(s, part, acc);
+            part = fmaf((static_cast<float>((q[i >> 1] >> (4 * (i & 1))) & 15) - z) * s, Elem<T>::to_f(x[i]), part);
+        acc += part;
     }
     return acc;
 }

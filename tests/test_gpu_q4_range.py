@@ -2,7 +2,10 @@
 small, and where the weights are zero or x has one sign, against the dequantised product
 in 64 bits.
 
-Tolerances are those of test_gpu_q4.py, relative to sum |w x|.
+Tolerances are those of test_gpu_q4.py, relative to sum |w x|.  A row of x that is
+computed in plain f32 (an infinity, a NaN or a magnitude of 2^117 and more) rounds each
+weight and each product once and adds up within the groups of g columns, then the
+groups: (g + ceil(k / g) + 2) 2^-24 of sum |w x|.
 """
 
 import numpy as np
@@ -81,3 +84,23 @@ def test_large_values_times_large_scales(dtype, scale_dt, group, by_id):
         scales = rng.uniform(1.0, 1.5, (n, k // group)) * 2.0 ** t
         got, xv, w = product(dtype, x, codes, scales, scale_dt, group, by_id=by_id)
         agree(got, xv, w, dtype, tau(dtype, k, group), (e, t))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale_dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_values_near_the_largest_of_f32(dtype, scale_dt, group):
+    """Up to 2^126.6 times scales of 2^-14: a group's sum of codes times x passes the range of
+    f32, the results do not."""
+    rng = np.random.default_rng(12)
+    n, k = 37, 300
+    x = signed(rng, (3, k), 1.0, 1.5) * 2.0 ** 126
+    x[1] *= 2.0 ** -8
+    x[2] = rng.standard_normal(k)
+    codes = rng.integers(0, 16, (n, k)).astype(np.uint8)
+    scales = rng.uniform(1.0, 1.5, (n, -(-k // group))) * 2.0 ** -14
+    zeros = rng.integers(0, 256, scales.shape).astype(np.uint8)
+    for z in (None, zeros):
+        got, xv, w = product(dtype, x, codes, scales, scale_dt, group, z)
+        agree(got[:2], xv[:2], w, dtype, (group + -(-k // group) + 2) * 2.0 ** -24, "plain")
+        agree(got[2:], xv[2:], w, dtype, tau(dtype, k, group), "another row")
