@@ -7,21 +7,24 @@
 // kernel is bound by that stream, and next to it by the instructions that unpack
 // the codes.  So the products run on the tensor cores straight from registers (mma
 // m16n8k16: 16 weight rows x 16 columns against 8 columns of x), and a pair of
-// codes becomes half an operand register with a single AND: a code c in the lowest
-// four mantissa bits of an f16 is the subnormal number c 2^-24, one in the next four
-// is 16 c 2^-24, and subnormal operands multiply exactly.  (An f32 product would have
-// to widen every code and multiply it once for each row of x; subtracting the zero
-// point from each code in f16 takes 9 instead of 5 instructions for 8 codes.)  With S
-// = sum of x over the group, the group's part of the result is s (sum of q x - z S).
+// codes becomes half an operand register, less its zero point, with two instructions: a code
+// c put under the exponent of 1024 is the f16 number 1024 + c in the lowest four mantissa bits and
+// 1024 + 16 c in the next four, from where one subtraction, or one multiply-add with 1/16,
+// makes q - z, exactly.  (An f32 product would have to widen every code and multiply it
+// once for each row of x.)  A group's sum then takes its scale.
 //
-// x is staged in shared memory as f16, the columns that meet 16 c divided by 16,
-// after each group of columns of a row has been scaled by a power of two that puts
-// its largest magnitude into [2^14, 2^15).  A value keeps all its bits unless it lies
-// 2^25 (f16) or 2^28 (bf16) below the largest of its group; then it is off by 2^-35 of that
-// at most, far less than what rounding does to an f32 sum with the largest in it.  f32
-// values become the sum of three f16 terms, in three of the mma's eight columns, with the
-// same bound.  A group that holds an infinity, a NaN or a value from 2^117 up is left out and
-// its row computed in plain f32 at the end.
+// The zero point goes before the product and not after the sum (sum of q x less z times
+// sum of x, which needs one instruction for a pair of codes and 4 to 8 % less time where there
+// are many weights): the difference of two sums of which each is rounded is off by parts of z sum
+// |x|, however small the weights are, and weights of 0 would not give 0.
+//
+// x is staged in shared memory as f16, after each group of columns of a row has been scaled
+// by a power of two that puts its largest magnitude into [2^14, 2^15).  A value keeps all its
+// bits unless it lies 2^28 (f16) or 2^31 (bf16) below the largest of its group; then it is off by
+// 2^-39 of that at most.  f32 values become the sum of three f16 terms, in three of the mma's eight
+// columns, each with what the terms before have left, scaled up by 2^11: 2^37, and 2^-61.  A
+// group that holds an infinity, a NaN or a value from 2^112 up is left out and its row computed in
+// plain f32 at the end.
 //
 // The order of a contraction is free, so a thread keeps the 32 bytes it loads (64
 // neighbouring codes of a row; the quad of lanes of a row covers a block of 256
@@ -41,11 +44,11 @@
 // alignment they need is settled at the launch (Access).
 //
 // Measured (us, and GB/s of codes, scales, zeros, x and y; inputs rotate past L2):
-//   dense 11008 x 4096, groups of 128, 1 row     f16 9.5 (2440)   f32 10.4 (2250)
-//   the same, 4 f16 rows 13.0, 16 f16 rows 25.7, 8 f32 rows 28.2
-//   4 tokens x 8 of 64 experts, 1408 x 2048      bf16 13.7 (3040)   f32 18.0 (2320)
-//   16 tokens x 8 of 128 experts, 1536 x 4096: bf16, groups of 32 with zeros 77.4 (3970);
-//   bf16, groups of 128 62.2 (4390); f32, groups of 128 96.7 (2830)
+//   dense 11008 x 4096, groups of 128, 1 row     f16 10.2 (2270)   f32 11.3 (2060)
+//   the same, 4 f16 rows 13.1, 16 f16 rows 27.9, 8 f32 rows 28.9
+//   4 tokens x 8 of 64 experts, 1408 x 2048      bf16 14.6 (2860)   f32 18.9 (2210)
+//   16 tokens x 8 of 128 experts, 1536 x 4096: bf16, groups of 32 with zeros 82.7 (3710);
+//   bf16, groups of 128 66.0 (4140); f32, groups of 128 104 (2630)
 // The large ones issue in more than half of the cycles, half of it the ANDs and shifts that
 // unpack the codes, and a warp waits as often for HBM as for the instructions before; the
 // last case but one takes 56.6 when x is not staged, 53.7 when nothing is multiplied.  The small
@@ -97,8 +100,15 @@ template <> struct XType<kFloat> { using type = float; };
 
 constexpr int kPitchPad = 64;    // spreads the lines of x over the banks
 constexpr int kZeroBytes = 512;  // a block: what lanes of another group read
-// shared memory of one block of x: `lines` rows (terms of rows), and {factor, sum} of each column
-constexpr int block_bytes(int lines, int NT, int closes) { return lines * 512 + 64 * NT * closes; }
+// shared memory of one block of x: `lines` rows (terms of rows), and what undoes each column's scaling
+constexpr int block_bytes(int lines, int NT, int closes) { return lines * 512 + 32 * NT * closes; }
+
+// Exponent field of 2^112: 128 values below it times a code less a zero point (255 at most) add
+// up to less than 2^127.
+constexpr uint32_t kPlainFrom = 239;
+// An f16 keeps 11 bits: what the first term of an f32 value leaves is scaled up by 2^11 before it
+// becomes the next.
+constexpr uint32_t kTermBits = 11;
 
 // d = A * B + (first ? 0 : d)
 __device__ __forceinline__ void mma(float (&d)[4], bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -107,6 +117,25 @@ __device__ __forceinline__ void mma(float (&d)[4], bool first, uint32_t a0, uint
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+// Two codes less their row's zero point z, exactly, as f16: the codes in the lowest four bits of w's
+// halves, made 1024 + c by the exponent's bits, less 1024 + z; and those in the next four, made 1024 +
+// 16 c, a sixteenth of that less 64 + z.
+__device__ __forceinline__ uint32_t half2_word(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+__device__ __forceinline__ __half2 word_half2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
+// `exponents` is 0x64006400, in a register that the compiler does not see through: of two constants it
+// makes two instructions.
+template <uint32_t MASK> __device__ __forceinline__ __half2 pick(uint32_t w, uint32_t exponents) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "n"(MASK), "r"(exponents));  // (w & MASK) | exponents
+    return word_half2(r);
+}
+__device__ __forceinline__ uint32_t low_codes(uint32_t w, uint32_t exponents, __half2 z) {
+    return half2_word(__hsub2(pick<0x000f000fu>(w, exponents), z));
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w, uint32_t exponents, __half2 minus_z) {
+    return half2_word(__hfma2(pick<0x00f000f0u>(w, exponents), word_half2(0x2c002c00u), minus_z));
 }
 
 struct Launch {
@@ -248,12 +277,11 @@ __device__ __forceinline__ bool find_in_warp(const Q4Params &p, uint32_t base_ro
 
 // x of `tokens` rows, which start at offsets[] (in elements), columns k0 .. k0 + 8 words
 // - 1, into shared memory: f16 terms at stage + line * pitch, and for each block (half a
-// block with groups of 32) and mma column {factor, sum}: what undoes the scalings, and the
-// group's sum of x (of its first term's column only).  Rows with a group that cannot be
-// scaled are marked in *bad.
+// block with groups of 32) and mma column what undoes the scaling.  Rows with a group that
+// cannot be scaled are marked in *bad.
 template <Kind K, int G, int NT, int kThreads>
 __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, const int64_t *offsets, uint32_t tokens,
-                                        int32_t k0, uint32_t words, uint32_t pitch, uint8_t *stage, float2 *info,
+                                        int32_t k0, uint32_t words, uint32_t pitch, uint8_t *stage, float *info,
                                         uint32_t *bad) {
     using T = typename XType<K>::type;
     constexpr int kTerms = K == kFloat ? 3 : 1;
@@ -283,35 +311,27 @@ __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, co
             if (toks[a] >= tokens) break;
             float f[8];
             x8[a].get(f);
-            float most = 0.f, sum = 0.f;
+            uint32_t most = 0u;  // of the magnitudes' bits: infinities and NaN are the largest
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                most = fmaxf(most, fabsf(f[j]));  // passes over NaN; the sum does not
-                sum += f[j];
-            }
+            for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(f[j]) & 0x7fffffffu);
 #pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) {
-                most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
-                sum += __shfl_xor_sync(kFull, sum, o);
-            }
-            if (!(most < 1.6615349947311448e35f) || sum != sum) {  // 2^117
+            for (int o = 1; o < kLanes; o <<= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
+            if (most >= kPlainFrom << 23) {
                 atomicOr(bad, 1u << toks[a]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] = 0.f;
-                most = sum = 0.f;
+                most = 0u;
             }
-            const uint32_t e = max(__float_as_uint(most) >> 23, 14u);
-            const float even = power_of_two(268u - e);   // 2^14 over the largest value's power of two
-            const float odd = power_of_two(264u - e);    // a sixteenth: codes 1, 3, 5, 7 of a word come as 16 c
-            const float factor = power_of_two(e + 10u);  // 2^24 (the codes come as c 2^-24) / even
+            const uint32_t e = max(most >> 23, 15u + kTermBits * (kTerms - 1));
+            const float up = power_of_two(268u - e);  // 2^14 over the largest value's power of two
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] *= j & 1 ? odd : even;
+            for (int j = 0; j < 8; ++j) f[j] *= up;
             const uint32_t block = ws[a] >> 5, group = lane / kLanes;
             // column of the row's (term's) first, and the close it belongs to
             const uint32_t part = G == 32 ? group >> 1 : group, close = G == 32 ? group & 1 : 0;
             uint8_t *line = stage + toks[a] * kTerms * pitch + block * 512 + word_offset(lane);
-            float2 *column = info + (block * Group<G>::kCloses + close) * (8 * NT) +
-                             toks[a] * kTerms * Group<G>::kParts + part;
+            float *column = info + (block * Group<G>::kCloses + close) * (8 * NT) +
+                            toks[a] * kTerms * Group<G>::kParts + part;
 #pragma unroll
             for (int q = 0; q < kTerms; ++q) {
                 uint32_t h[4];
@@ -320,12 +340,12 @@ __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, co
                     h[i] = half2_bits(f[i], f[i + 4]);
                     if (q + 1 < kTerms) {
                         const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-                        f[i] -= v.x;
-                        f[i + 4] -= v.y;
+                        f[i] = (f[i] - v.x) * static_cast<float>(1 << kTermBits);
+                        f[i + 4] = (f[i + 4] - v.y) * static_cast<float>(1 << kTermBits);
                     }
                 }
                 *reinterpret_cast<uint4 *>(line + q * pitch) = make_uint4(h[0], h[1], h[2], h[3]);
-                if (lane % kLanes == 0) column[q * Group<G>::kParts] = make_float2(factor, q == 0 ? sum : 0.f);
+                if (lane % kLanes == 0) column[q * Group<G>::kParts] = power_of_two(e - 14u - kTermBits * q);
             }
         }
     }
@@ -485,6 +505,15 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
     auto row_of = [&](int h) { return min(row + 8 * h, p.n - 1); };
     const int lane_cell = G == 128 ? 0 : kCells * (c & 1);  // the lane's first group of a block
 
+    uint32_t exponents;
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(exponents));
+    auto z_of = [&](uint32_t raw, int byte, __half2 &z, __half2 &minus_z) {
+        z = word_half2(__byte_perm(raw, exponents, byte == 0 ? 0x5050 : 0x5151));
+        minus_z = __hsub2(word_half2(0x63806380u), z);
+    };
+    __half2 z[kRows], minus_z[kRows];  // 1024 + z and -(64 + z)
+#pragma unroll
+    for (int h = 0; h < kRows; ++h) z_of(0x0808u, 0, z[h], minus_z[h]);
     int32_t b1 = 0;  // end of the slab: what lies past it is not fetched
     auto fetch_codes = [&](int32_t block, uint4 (&q)[kRows][2]) {
         const int32_t at = block * 128 + 32 * c;  // in the row
@@ -526,86 +555,82 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
             }
         }
     };
-    // Raw scales and zero points of the lane's kCells groups of a block.  kAtOnce: s.x, s.y
-    // pairs of scales, z.x bytes.  Else: s.x, s.y one scale each, z.x, z.y one byte each;
-    // with groups of 32, pairs.  (32-bit scales are read where they are used.)
-    uint2 s_raw[kRows], z_raw[kRows];
-    auto fetch_cells = [&](int32_t block) {
+    // Zero points of the lane's rows for its own codes of a block: one byte, with groups of 32 two.
+    uint32_t z_raw[kRows];
+#pragma unroll
+    for (int h = 0; h < kRows; ++h) z_raw[h] = 0x0808u;
+    auto fetch_zeros = [&](int32_t block) {
+        const int32_t group = block * Group<G>::kInBlock + (G == 128 ? c >> 1 : G == 64 ? c : 2 * c);
+        const bool have = group < groups;
+#pragma unroll
+        for (int h = 0; h < kRows; ++h) {
+            const uint8_t *z =
+                p.zeros + (A == kAnyhow ? cells + row_of(h) * p.groups : cell + h * (8 * p.groups)) + group;
+            if (G == 32 && A >= kApart)
+                z_raw[h] = load_cells16(have, z);
+            else
+                z_raw[h] = load_cells8(have, z);
+            if (G == 32 && A < kApart) z_raw[h] |= load_cells8(group + 1 < groups, z + 1) << 8;
+        }
+    };
+    // Raw scales of the lane's kCells groups of a block.  kAtOnce: s.x, s.y pairs of scales.
+    // Else: s.x, s.y one scale each; with groups of 32, pairs.  (32-bit scales are read where they
+    // are used.)
+    uint2 s_raw[kRows];
+    auto fetch_scales = [&](int32_t block) {
         if (A == kAnyhow && p.scale_dtype == kF32) return;
         const int32_t group = block * Group<G>::kInBlock + lane_cell;
         const bool have = group < groups, more = group + kCells / 2 < groups;
-        const bool zhave = have && p.zeros != nullptr, zmore = more && p.zeros != nullptr;
 #pragma unroll
         for (int h = 0; h < kRows; ++h) {
             const int64_t at = (A == kAnyhow ? cells + row_of(h) * p.groups : cell + h * (8 * p.groups)) + group;
             const uint16_t *s = static_cast<const uint16_t *>(p.scales) + at;
-            const uint8_t *z = p.zeros + at;
             if (A == kAtOnce && kCells == 4) {
                 s_raw[h] = load_cells64(have, s);
-                z_raw[h].x = load_cells32(zhave, z);
             } else if (A == kAtOnce) {
                 s_raw[h].x = load_cells32(have, s);
-                z_raw[h].x = load_cells16(zhave, z);
             } else if (A == kApart && kCells == 4) {
                 s_raw[h] = make_uint2(load_cells32(have, s), load_cells32(more, s + 2));
-                z_raw[h] = make_uint2(load_cells16(zhave, z), load_cells16(zmore, z + 2));
             } else if (kCells == 4) {
                 const bool second = group + 1 < groups, fourth = group + 3 < groups;
                 s_raw[h].x = load_cells16(have, s) | load_cells16(second, s + 1) << 16;
                 s_raw[h].y = load_cells16(more, s + 2) | load_cells16(fourth, s + 3) << 16;
-                z_raw[h].x = load_cells8(zhave, z) | load_cells8(zhave && second, z + 1) << 8;
-                z_raw[h].y = load_cells8(zmore, z + 2) | load_cells8(zmore && fourth, z + 3) << 8;
             } else {
                 s_raw[h] = make_uint2(load_cells16(have, s), load_cells16(more, s + 1));
-                z_raw[h] = make_uint2(load_cells8(zhave, z), load_cells8(zmore, z + 1));
             }
         }
     };
-    // scales, and scales times negative zero points, of row h's groups `close` and `close` +
-    // kCloses among the lane's of a block
-    auto cells_of = [&](int32_t block, int h, int close, float (&s)[2], float (&sz)[2]) {
-        float z[2] = {-8.f, -8.f};
+    // scales of row h's groups `close` and `close` + kCloses among the lane's of a block
+    auto scales_of = [&](int32_t block, int h, int close, float (&s)[2]) {
         if (A != kAnyhow || p.scale_dtype != kF32) {
-            uint32_t a, b, y, z1;
+            uint32_t a, b;
             if (kCells == 4) {  // close 0 takes groups 0 and 2, close 1 takes 1 and 3
                 a = s_raw[h].x >> (16 * close) & 0xffffu;
                 b = s_raw[h].y >> (16 * close) & 0xffffu;
-                y = z_raw[h].x >> (8 * close) & 255u;
-                z1 = (A == kAtOnce ? z_raw[h].x >> (16 + 8 * close) : z_raw[h].y >> (8 * close)) & 255u;
             } else {
                 a = A == kAtOnce ? s_raw[h].x & 0xffffu : s_raw[h].x;
                 b = A == kAtOnce ? s_raw[h].x >> 16 : s_raw[h].y;
-                y = A == kAtOnce ? z_raw[h].x & 255u : z_raw[h].x;
-                z1 = A == kAtOnce ? z_raw[h].x >> 8 : z_raw[h].y;
             }
             s[0] = scale_value(a, p.scale_dtype);
             s[1] = scale_value(b, p.scale_dtype);
-            // 2^23 + byte, as f32
-            z[0] = p.zeros != nullptr ? 8388608.f - __uint_as_float(0x4b000000u | y) : -8.f;
-            z[1] = p.zeros != nullptr ? 8388608.f - __uint_as_float(0x4b000000u | z1) : -8.f;
         } else {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int32_t group = block * Group<G>::kInBlock + lane_cell + close + kCloses * i;
-                const int64_t at = cells + row_of(h) * p.groups + group;
-                s[i] = 0.f;
-                if (group < groups) {
-                    s[i] = __ldg(static_cast<const float *>(p.scales) + at);
-                    if (p.zeros != nullptr) z[i] = -static_cast<float>(__ldg(p.zeros + at));
-                }
+                s[i] = group < groups ? __ldg(static_cast<const float *>(p.scales) + cells + row_of(h) * p.groups + group)
+                                      : 0.f;
             }
         }
-        sz[0] = s[0] * z[0];
-        sz[1] = s[1] * z[1];
     };
     uint4 q[kRows][2];
     b1 = min(cfg.slab << cfg.wk_log, blocks);
     fetch_codes(wk, q);
-    fetch_cells(wk);
+    if (p.zeros != nullptr) fetch_zeros(wk);
+    fetch_scales(wk);
     // the zeros that lanes of another group read
     if (tid < kZeroBytes / 16) reinterpret_cast<uint4 *>(smem)[tid] = make_uint4(0u, 0u, 0u, 0u);
     uint8_t *stage = smem + kZeroBytes;
-    float2 *info = reinterpret_cast<float2 *>(smem + cfg.info_at);
+    float *info = reinterpret_cast<float *>(smem + cfg.info_at);
     const int32_t slab_blocks = cfg.slab << cfg.wk_log;
     const uint32_t pitch = (static_cast<uint32_t>(slab_blocks) << 9) + kPitchPad;
 
@@ -642,7 +667,8 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
             __syncthreads();
             if (b0 != 0 || t0 != first) {
                 fetch_codes(wk + b0, q);
-                fetch_cells(wk + b0);
+                if (p.zeros != nullptr) fetch_zeros(wk + b0);
+                fetch_scales(wk + b0);
             }
             // This lane's first word of the line of mma column 8 t + g, if its codes are of
             // that column's group.  Lanes past the last column repeat it; what they compute
@@ -656,60 +682,77 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
                 xat[t] = own ? stage + (col / kParts) * pitch + wk * 512 + 16 * c : smem;
                 xstep[t] = own ? 512 << cfg.wk_log : 0;
             }
-            // {factor, sum} of columns 2 c and 2 c + 1
-            const float4 *iat = reinterpret_cast<const float4 *>(info + wk * (kCloses * 8 * NT)) + c;
+            // what undoes the scalings of columns 2 c and 2 c + 1
+            const float2 *iat = reinterpret_cast<const float2 *>(info + wk * (kCloses * 8 * NT)) + c;
 #pragma unroll 1
             for (int32_t block = wk + b0; block < b1; block += wk_count) {
                 float part[MT][NT][4];
+                uint32_t z_now[kRows];
+#pragma unroll
+                for (int h = 0; h < kRows; ++h) z_now[h] = z_raw[h];
+                if (p.zeros != nullptr) {
+                    if (G != 32) {
+#pragma unroll
+                        for (int h = 0; h < kRows; ++h) z_of(z_now[h], 0, z[h], minus_z[h]);
+                    }
+                    fetch_zeros(block + wk_count);
+                }
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
+                    if (G == 32) {
+#pragma unroll
+                        for (int h = 0; h < kRows; ++h) z_of(z_now[h], v, z[h], minus_z[h]);
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        constexpr uint32_t kEven = 0x000f000fu, kOdd = 0x00f000f0u;
-                        uint32_t u[kRows];
+                        uint32_t a[kRows][4];  // columns 0 and 4, 1 and 5, 2 and 6, 3 and 7 of a word
 #pragma unroll
-                        for (int h = 0; h < kRows; ++h)
-                            u[h] = i == 0   ? q[h][v].x
-                                   : i == 1 ? q[h][v].y
-                                   : i == 2 ? q[h][v].z
-                                            : q[h][v].w;
+                        for (int h = 0; h < kRows; ++h) {
+                            const uint32_t u = i == 0   ? q[h][v].x
+                                               : i == 1 ? q[h][v].y
+                                               : i == 2 ? q[h][v].z
+                                                        : q[h][v].w;
+                            a[h][0] = low_codes(u, exponents, z[h]);
+                            a[h][1] = high_codes(u, exponents, minus_z[h]);
+                            a[h][2] = low_codes(u >> 8, exponents, z[h]);
+                            a[h][3] = high_codes(u >> 8, exponents, minus_z[h]);
+                        }
                         const bool opens = i == 0 && (v == 0 || kCloses == 2);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             const uint4 b = *reinterpret_cast<const uint4 *>(xat[t] + 256 * v + 64 * i);
 #pragma unroll
                             for (int m = 0; m < MT; ++m) {
-                                const uint32_t v0 = u[2 * m], v1 = u[2 * m + 1];
-                                mma(part[m][t], opens, v0 & kEven, v1 & kEven, v0 & kOdd, v1 & kOdd, b.x, b.y);
-                                mma(part[m][t], false, v0 >> 8 & kEven, v1 >> 8 & kEven, v0 >> 8 & kOdd,
-                                    v1 >> 8 & kOdd, b.z, b.w);
+                                const uint32_t(&a0)[4] = a[2 * m], (&a1)[4] = a[2 * m + 1];
+                                mma(part[m][t], opens, a0[0], a1[0], a0[1], a1[1], b.x, b.y);
+                                mma(part[m][t], false, a0[2], a1[2], a0[3], a1[3], b.z, b.w);
                             }
                         }
                     }
-                    if (v == 1) fetch_codes(block + wk_count, q);
+                    if (v == 1) {
+                        fetch_codes(block + wk_count, q);
+                    }
                     if (v == 1 || kCloses == 2) {
                         const int close = kCloses == 2 ? v : 0;
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
-                            float s[2][2], sz[2][2];  // [row][column's group]
-                            cells_of(block, 2 * m, close, s[0], sz[0]);
-                            cells_of(block, 2 * m + 1, close, s[1], sz[1]);
+                            float s[2][2];  // [row][column's group]
+                            scales_of(block, 2 * m, close, s[0]);
+                            scales_of(block, 2 * m + 1, close, s[1]);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                const float4 f = iat[close * (4 * NT) + 4 * t];
+                                const float2 f = iat[close * (4 * NT) + 4 * t];
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
-                                    const float factor = i & 1 ? f.z : f.x, sum = i & 1 ? f.w : f.y;
-                                    float &a = acc[m][t][i];
                                     // (the scale times the factor could pass the range of f32)
-                                    a = fmaf(s[i >> 1][i & 1], factor * part[m][t][i], a);
-                                    a = fmaf(sz[i >> 1][i & 1], sum, a);
+                                    float &sum = acc[m][t][i];
+                                    sum = fmaf(s[i >> 1][i & 1], (i & 1 ? f.y : f.x) * part[m][t][i], sum);
                                 }
                             }
                         }
                     }
                 }
-                fetch_cells(block + wk_count);
+                fetch_scales(block + wk_count);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) xat[t] += xstep[t];
                 iat += (kCloses * 4 * NT) << cfg.wk_log;
@@ -819,9 +862,9 @@ cudaError_t launch_access(const Q4Params &p, int num_sms, cudaStream_t s) {
     if (p.scale_dtype == kF32 || p.n < 16 * MT || !multiple(p.q, 16) || p.ldq % 16 != 0 || p.expert_stride % 16 != 0)
         return launch_nt<K, G, kAnyhow, NT, MT>(p, num_sms, s);
     if (!multiple(p.q, 32) || p.ldq % 32 != 0 || p.expert_stride % 32 != 0 || p.k % 64 != 0 ||
-        !multiple(p.scales, kCells) || !multiple(p.zeros, kCells / 2))
+        !multiple(p.scales, kCells) || !multiple(p.zeros, G == 32 ? 2 : 1))
         return launch_nt<K, G, kLoose, NT, MT>(p, num_sms, s);
-    if (p.groups % kCells == 0 && multiple(p.scales, 2 * kCells) && multiple(p.zeros, kCells))
+    if (p.groups % kCells == 0 && multiple(p.scales, 2 * kCells))
         return launch_nt<K, G, kAtOnce, NT, MT>(p, num_sms, s);
     return launch_nt<K, G, kApart, NT, MT>(p, num_sms, s);
 }

@@ -483,11 +483,14 @@ GBMM_API gbmm_status gbmm_moe_combine_backward(gbmm_dtype dt, uint32_t m, uint32
  * group: 32, 64 or 128 columns; the last one may be ragged.  G = ceil(k/group).
  * scales: [n, G] tight, scale_dt f32, f16 or bf16.  zeros: u8 [n, G] tight, values
  *   0..255, or NULL for 8 everywhere.
- * Codes and zero points enter exactly.  The values of x do too, f32 included, except
- * that one far below the largest magnitude of its group of columns (2^25 for f16, 2^28
- * for bf16, 2^12 for f32) may be off by up to 2^-35 of that magnitude.  A row with an
- * infinity, a NaN or a magnitude from 2^117 up is computed in plain f32, slower.
- * Products accumulate in f32, and each result is rounded once.
+ * Codes and zero points enter exactly, and are subtracted before the product: a weight
+ * of 0 adds exactly 0.  The values of x enter exactly too, f32 included, except that one far below
+ * the largest magnitude of its group of columns (2^28 for f16, 2^31 for bf16, 2^37 for f32)
+ * may be off by up to 2^-39 (f32: 2^-61) of that magnitude.  Products accumulate in f32, group by
+ * group; a group's sum is multiplied by its scale, and each result is rounded once to its type.
+ * The sums' error is below (t ceil(group/16) 2^-22 + (k/32 + 16) 2^-24) * sum |x W|, t = 3 for f32
+ * and 1 otherwise.  A row with an infinity, a NaN or a magnitude from 2^112 up is computed in
+ * plain f32, each W[j,x] rounded first, and much slower.
  */
 
 /* gbmm_gemv_q4 -- y[i,j] = sum_x x[i,x] * W[j,x] for i < m.  x [m, k] and y

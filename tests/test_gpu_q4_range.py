@@ -2,8 +2,9 @@
 small, and where the weights are zero or x has one sign, against the dequantised product
 in 64 bits.
 
-Tolerances are those of test_gpu_q4.py, relative to sum |w x|.  A row of x that is
-computed in plain f32 (an infinity, a NaN or a magnitude of 2^117 and more) rounds each
+Tolerances are those of test_gpu_q4.py, relative to sum |w x| (so a result is exactly 0 where
+every weight is 0).  A row of x that is
+computed in plain f32 (an infinity, a NaN or a magnitude of 2^112 and more) rounds each
 weight and each product once and adds up within the groups of g columns, then the
 groups: (g + ceil(k / g) + 2) 2^-24 of sum |w x|.
 """
@@ -104,3 +105,88 @@ def test_values_near_the_largest_of_f32(dtype, scale_dt, group):
         got, xv, w = product(dtype, x, codes, scales, scale_dt, group, z)
         agree(got[:2], xv[:2], w, dtype, (group + -(-k // group) + 2) * 2.0 ** -24, "plain")
         agree(got[2:], xv[2:], w, dtype, tau(dtype, k, group), "another row")
+
+
+ALIGNED = [(512, 48), (500, 33), (517, 5)]  # packed rows on 32 bytes; anywhere, a ragged last group
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("by_id", [False, True])
+@pytest.mark.parametrize("k,n", ALIGNED)
+def test_weights_of_zero_give_zero(dtype, group, by_id, k, n):
+    """Codes that equal their zero point are weights of exactly 0."""
+    rng = np.random.default_rng(13)
+    scales, zeros = rng.uniform(0.5, 1.5, (n, -(-k // group))), rng.integers(0, 16, (n, -(-k // group))).astype(np.uint8)
+    for x in (rng.uniform(0.5, 1.5, (9, k)), rng.standard_normal((1, k)) * 1000, rng.uniform(1.0, 2.0, (2, k))):
+        for scale_dt in ("f16", "f32"):
+            got, _, w = product(dtype, x, np.full((n, k), 8, np.uint8), scales, scale_dt, group, by_id=by_id)
+            assert (w == 0).all() and (got == 0).all()
+            codes = np.repeat(zeros, group, axis=1)[:, :k]
+            got, _, w = product(dtype, x, codes, scales, scale_dt, group, zeros, by_id=by_id)
+            assert (w == 0).all() and (got == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("k,n", ALIGNED)
+def test_few_weights_that_are_not_zero(dtype, group, k, n):
+    """x of one sign everywhere; a row of the matrix has three weights that are not zero."""
+    rng = np.random.default_rng(14)
+    scales, zeros = rng.uniform(0.5, 1.5, (n, -(-k // group))), rng.integers(1, 15, (n, -(-k // group))).astype(np.uint8)
+    x = rng.uniform(0.5, 1.5, (4, k))
+    for z in (None, zeros):
+        codes = np.full((n, k), 8, np.uint8) if z is None else np.repeat(z, group, axis=1)[:, :k].copy()
+        for row in codes:
+            at = rng.choice(k, 3, replace=False)
+            row[at] += rng.choice([-1, 1], 3).astype(np.int8).view(np.uint8)
+        got, xv, w = product(dtype, x, codes, scales, "f16", group, z)
+        assert ((w != 0).sum(axis=1) == 3).all()
+        agree(got, xv, w, dtype, tau(dtype, k, group), z is None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("k,n", ALIGNED)
+def test_rows_of_one_sign(dtype, group, k, n):
+    rng = np.random.default_rng(15)
+    codes = rng.integers(0, 16, (n, k)).astype(np.uint8)
+    scales = rng.uniform(0.005, 0.015, (n, -(-k // group)))
+    x = rng.uniform(0.5, 1.5, (5, k)) * np.array([1.0, -1.0, 1.0, -30.0, 0.01])[:, None]
+    far = rng.integers(0, 256, scales.shape).astype(np.uint8)
+    for z in (None, rng.integers(0, 16, scales.shape).astype(np.uint8), far):
+        got, xv, w = product(dtype, x, codes, scales, "f16", group, z)
+        agree(got, xv, w, dtype, tau(dtype, k, group), "one sign")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("factor", [2.0 ** 6, 2.0 ** 12])
+def test_one_outlier_a_group(dtype, group, factor):
+    """One value of x a group is `factor` times the others'; every other row of the matrix
+    has a weight of 0 there.  (x keeps all its bits next to it.)"""
+    rng = np.random.default_rng(16)
+    n, k = 40, 640
+    codes = rng.integers(0, 16, (n, k)).astype(np.uint8)
+    scales = rng.uniform(0.005, 0.015, (n, k // group))
+    x = signed(rng, (3, k), 0.5, 1.0)
+    at = np.arange(0, k, group) + rng.integers(0, group, k // group)
+    x[:, at] *= factor
+    codes[::2, at] = 8
+    got, xv, w = product(dtype, x, codes, scales, "f16", group)
+    agree(got, xv, w, dtype, tau(dtype, k, group), factor)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("exponent", [-149, -140, -133, -126, -110])
+def test_subnormal_values(dtype, group, exponent):
+    """x from the smallest subnormals on, times scales that bring the results back."""
+    rng = np.random.default_rng(17)
+    n, k = 20, 256
+    codes = rng.integers(0, 16, (n, k)).astype(np.uint8)
+    scales = rng.uniform(1.0, 2.0, (n, k // group)) * 2.0 ** 100
+    x = signed(rng, (2, k), 1.0, 8.0) * 2.0 ** exponent
+    got, xv, w = product(dtype, x, codes, scales, "f32", group)
+    # a group's sum of (q - z) x, before its scale, is held in f32: 2^-150 is half its last bit there
+    agree(got, xv, w, dtype, tau(dtype, k, group), exponent, extra=k // group * 2.0 ** (101 - 150))
