@@ -163,7 +163,10 @@ struct Q4Params {
     int64_t n, k, groups;        // groups = ceil(k / group)
     int32_t group, scale_dtype;
     uint32_t rows, top_k, n_experts;
+    uint32_t first_row;  // per expert id: the launch's first routed row; it takes kQ4LaunchRows at most
 };
+constexpr uint32_t kQ4Window = 1024;  // routed rows that a CTA searches for its expert's
+constexpr uint32_t kQ4LaunchRows = 65535u * kQ4Window;
 
 // ---- launchers (each returns the launch's cudaError_t) --------------------
 

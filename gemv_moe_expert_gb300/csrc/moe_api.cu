@@ -188,12 +188,17 @@ gbmm_status check_q4(const char *fn, gbmm_dtype dt, int64_t n, int64_t k, uint32
     return GBMM_OK;
 }
 
-gbmm_status launch_q4(const char *fn, gbmm_dtype dt, const Q4Params &p, cudaStream_t s) {
+// Per expert id, a launch for each kQ4LaunchRows routed rows.
+gbmm_status launch_q4(const char *fn, gbmm_dtype dt, Q4Params p, cudaStream_t s) {
     if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
-    return finish_launch(dt == GBMM_F32   ? launch_q4_f32(p, s)
-                         : dt == GBMM_F16 ? launch_q4_f16(p, s)
-                                          : launch_q4_bf16(p, s),
-                         fn, s);
+    for (;;) {
+        const gbmm_status st = finish_launch(dt == GBMM_F32   ? launch_q4_f32(p, s)
+                                             : dt == GBMM_F16 ? launch_q4_f16(p, s)
+                                                              : launch_q4_bf16(p, s),
+                                             fn, s);
+        if (st != GBMM_OK || p.ids == nullptr || p.k == 0 || p.rows - p.first_row <= kQ4LaunchRows) return st;
+        p.first_row += kQ4LaunchRows;
+    }
 }
 
 }  // namespace

@@ -60,12 +60,14 @@
 // four CTAs that stage a quarter of x each and copy the rest from each other 89 for 79.
 #pragma once
 
+#include <algorithm>
+
 #include "device_common.cuh"
 
 namespace gbmm {
 namespace q4 {
 
-constexpr int kWindow = 1024;  // routed rows that a CTA searches for its expert's
+constexpr uint32_t kWindow = kQ4Window;
 constexpr uint32_t kFull = 0xffffffffu;
 
 // mma columns that a row of x takes; how often a block's sums are closed
@@ -192,7 +194,7 @@ template <typename T, int kThreads>
 __device__ __forceinline__ bool find_expert(const Q4Params &p, uint32_t base_row, uint32_t d, int64_t j0, int tile_rows,
                                             uint32_t *s_ids, uint32_t *s_bits, uint32_t &expert) {
     const int tid = threadIdx.x, lane = tid & 31;
-    const uint32_t rows = min(p.rows - base_row, static_cast<uint32_t>(kWindow));
+    const uint32_t rows = min(p.rows - base_row, kWindow);
     if (tid < 32) s_bits[tid] = 0u;
     __syncthreads();
     bool none = false;
@@ -230,7 +232,7 @@ __device__ __forceinline__ bool find_expert(const Q4Params &p, uint32_t base_row
 __device__ __forceinline__ uint32_t list_rows(const Q4Params &p, uint32_t base_row, uint32_t expert, uint32_t *s_ids,
                                               uint32_t *s_count) {
     const int lane = threadIdx.x & 31;
-    const uint32_t rows = min(p.rows - base_row, static_cast<uint32_t>(kWindow));
+    const uint32_t rows = min(p.rows - base_row, kWindow);
     __syncthreads();
     if (threadIdx.x < 32) {
         uint32_t n = 0;
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(Budget<K, NT, MT>::kThreads, Budget<K, NT, MT>
     const bool by_id = p.ids != nullptr;
 
     uint32_t expert = 0;
-    const uint32_t base_row = blockIdx.z * kWindow;
+    const uint32_t base_row = p.first_row + blockIdx.z * kWindow;
     const bool small = by_id && p.rows <= 32;
     uint32_t listed = 0;
     if (small) {
@@ -803,14 +805,13 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     const int64_t blocks = (p.k + 255) / 256;
     uint32_t gy, gz = 1;
     if (p.ids != nullptr) {
-        gz = (p.rows + kWindow - 1) / kWindow;
+        gz = (std::min(p.rows - p.first_row, kQ4LaunchRows) + kWindow - 1) / kWindow;
         gy = p.rows < kWindow ? p.rows : kWindow;  // distinct experts of a window at most
         if (gy > p.n_experts) gy = p.n_experts;
     } else {
         gy = (p.rows + kPass - 1) / kPass;
         if (gy > 65535u) gy = 65535u;
     }
-    if (gz > 65535u) return cudaErrorInvalidConfiguration;
     Launch cfg{};
     // Warps that split the columns: enough for 16 warps an SM (8, and 4 with f32, where a pass
     // takes more than one column tile, as the staging of its rows is repeated for each CTA),

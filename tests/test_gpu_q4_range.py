@@ -190,3 +190,21 @@ def test_subnormal_values(dtype, group, exponent):
     got, xv, w = product(dtype, x, codes, scales, "f32", group)
     # a group's sum of (q - z) x, before its scale, is held in f32: 2^-150 is half its last bit there
     agree(got, xv, w, dtype, tau(dtype, k, group), exponent, extra=k // group * 2.0 ** (101 - 150))
+
+
+def test_matmul_id_q4_more_windows_than_a_grid_has():
+    """67 million routed rows: more windows of 1024 than one launch takes."""
+    m, E, tail = 65535 * 1024 + 1500, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randint(-8, 9, (m, 1), generator=g, device="cuda", dtype=torch.int8).half()
+    ids = torch.randint(0, E + 1, (m, 1), generator=g, device="cuda", dtype=torch.int32)
+    q = torch.tensor([11, 2], dtype=torch.uint8, device="cuda")  # 3 and -6
+    scales = torch.ones(E, 1, 1, dtype=torch.float16, device="cuda")
+    out = torch.full((m + tail,), 77.0, dtype=torch.float16, device="cuda")
+    torch.cuda.synchronize()
+    gb.check(gb.gbmm_matmul_id_q4("f16", m, 1, 1, 1, E, gb.INPUT_SHARED_PER_TOKEN, 128, q, 1, 1, scales, "f16", None, x,
+                                  ids, out))
+    torch.cuda.synchronize()
+    w = torch.tensor([3.0, -6.0, 0.0], dtype=torch.float16, device="cuda")
+    assert torch.equal(out[:m], (x * w[ids.long()])[:, 0])
+    assert (out[m:] == 77.0).all()
