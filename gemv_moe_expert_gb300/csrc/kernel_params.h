@@ -225,6 +225,7 @@ cudaError_t launch_moe_route(int dt, const MoeRouteParams &p, cudaStream_t s);
 cudaError_t launch_moe_route_backward(int dt, const MoeRouteParams &p, cudaStream_t s);
 uint64_t moe_sort_scratch_words(uint64_t rows, uint32_t n_experts);
 int moe_sort_launches(uint64_t rows);
+cudaError_t prepare_moe_sort(uint64_t rows);  // before the first of its launches
 cudaError_t launch_moe_sort(int step, const MoeSortParams &p, cudaStream_t s);
 cudaError_t launch_moe_dispatch(int dt, const MoeRowsParams &p, cudaStream_t s);
 cudaError_t launch_moe_combine(int dt, const MoeRowsParams &p, cudaStream_t s);

@@ -323,6 +323,10 @@ gbmm_status gbmm_moe_sort(uint32_t m, uint32_t top_k, uint32_t n_experts, const 
     p.rows = static_cast<uint32_t>(rows);
     p.n_experts = n_experts;
     const int launches = moe_sort_launches(rows);
+    // whatever can fail ahead of the last launch does so ahead of the first
+    if (launches > 1 && !resolve_kernel("gbmm_moe_sort_place")) return GBMM_ERR_KERNEL_UNAVAILABLE;
+    const cudaError_t prepared = prepare_moe_sort(rows);
+    if (prepared != cudaSuccess) return finish_launch(prepared, fn, cuda_stream(stream));
     for (int step = 0; step < launches; ++step) {
         st = finish_launch(launch_moe_sort(step, p, cuda_stream(stream)), fn, cuda_stream(stream));
         if (st != GBMM_OK) return st;

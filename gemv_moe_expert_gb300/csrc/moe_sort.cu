@@ -273,13 +273,16 @@ uint64_t moe_sort_scratch_words(uint64_t rows, uint32_t n_experts) {
 
 int moe_sort_launches(uint64_t rows) { return tiles_of(rows, kClusterP) <= kClusterTiles ? 1 : 3; }
 
-cudaError_t launch_moe_sort(int step, const MoeSortParams &p, cudaStream_t s) {
+cudaError_t prepare_moe_sort(uint64_t rows) {
     static unsigned long long cluster_done = 0, place_done = 0;
+    if (moe_sort_launches(rows) == 1) return allow(moe_sort_cluster_kernel, true, &cluster_done);
+    return allow(moe_sort_place_kernel, false, &place_done);
+}
+
+cudaError_t launch_moe_sort(int step, const MoeSortParams &p, cudaStream_t s) {
     const uint32_t keys = p.n_experts + 1;
     const size_t smem = tile_bytes(keys);
     if (moe_sort_launches(p.rows) == 1) {
-        const cudaError_t e = allow(moe_sort_cluster_kernel, true, &cluster_done);
-        if (e != cudaSuccess) return e;
         const unsigned tiles = static_cast<unsigned>(tiles_of(p.rows, kClusterP));
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(tiles, 1, 1);
@@ -304,8 +307,6 @@ cudaError_t launch_moe_sort(int step, const MoeSortParams &p, cudaStream_t s) {
         return cudaGetLastError();
     }
     if (step == 1) return launch_early(moe_sort_scan_kernel, (keys + 7) / 8, 256, 0, s, p, tiles);
-    const cudaError_t e = allow(moe_sort_place_kernel, false, &place_done);
-    if (e != cudaSuccess) return e;
     return launch_early(moe_sort_place_kernel, tiles, kThreads, smem, s, p);
 }
 

@@ -554,7 +554,7 @@ GBMM_API gbmm_status gbmm_device_error(gbmm_stream stream, uint32_t *code);
  * Kernel names: "gbmm_gemv_rowdot", "gbmm_gemv_coldot", "gbmm_gemv_tc", "gbmm_gemm_simt",
  * "gbmm_gemm_tc", "gbmm_fill_zero", "gbmm_matmul_id_direct",
  * "gbmm_matmul_id_map", "gbmm_matmul_id_grouped", and the names of the gbmm_moe_*
- * and *_q4 entry points for theirs. */
+ * and *_q4 entry points for theirs; "gbmm_moe_sort_place" is the last of gbmm_moe_sort's three. */
 GBMM_API void gbmm_test_inject_kernel_failure(const char *name);
 
 /* Kernels launched by this library since load / the last reset. */
