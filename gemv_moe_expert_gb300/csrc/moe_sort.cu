@@ -27,7 +27,9 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kClusterP = 2, kLargeP = 4;  // rows a thread
-constexpr int kClusterTiles = 16;          // the largest cluster
+// The largest cluster; a GB300 has room for one with the shared memory that 1024 experts take (226 KB
+// a CTA, one CTA an SM).
+constexpr int kClusterTiles = 16;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kMaxKeys = 1025;
 constexpr uint32_t kPitch = kWarps + 1;  // counts[key][warp]: an odd pitch spreads the keys over the banks

@@ -8,7 +8,7 @@ torch = pytest.importorskip("torch")
 
 from gemv_moe_expert_gb300 import binding as gb  # noqa: E402
 from tests.gpu_util import SENTINEL, DevBuf  # noqa: E402
-from tests.test_gpu_moe import ints  # noqa: E402
+from tests.test_gpu_moe import check_sort, ints  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,10 @@ def test_a_sort_that_cannot_finish_launches_nothing():
         assert (b.read(np.uint8) == SENTINEL).all()
     gb.check(gb.gbmm_moe_sort(*args))
     assert gb.gbmm_test_launch_count() == 3
+
+
+@pytest.mark.parametrize("m,top_k,E", [(4096, 8, 1024), (2341, 7, 1024), (32768, 1, 1023), (3750, 8, 1000)])
+def test_clusters_of_the_most_ctas_with_the_most_experts(m, top_k, E):
+    """9 to 16 CTAs, each with nearly all of an SM's shared memory."""
+    rng = np.random.default_rng(m + E)
+    check_sort(rng.integers(0, E + 1, (m, top_k)).astype(np.uint32), E)
