@@ -7,16 +7,17 @@
 // is one maximum over the warp and one ballot for the first lane that has it.  The
 // softmax subtracts the maximum and sums in f32.
 //
-// Bound by instruction issue (80 % of the cycles forward, 72 % backward), so the layout
-// saves instructions: a lane's keys are sorted once, into a list in shared memory from which
+// In this layout the selection serves one token at a time with a whole warp, and with many tokens the
+// kernel is bound by instruction issue (80 % of the cycles in which an SM has work forward, 68 %
+// backward), so it saves instructions: a lane's keys are sorted once, into a list in shared memory from which
 // the lane of a step's maximum alone takes its next; the weights come from the terms
 // of the softmax, left in shared memory, in place of the logits again; and with many tokens
 // a warp takes several of them, so that what concerns the slots is done for all at once.
 //
 // Measured (us forward / backward): 65536 tokens, 8 of 128 experts, f32, softmax over all
-// 20.0 (288 instructions a token) / 14.9 (155); one token a warp 23.0 / 21.2; and with
-// registers moved up in place of lists, two reductions a step and the logits read again
-// 27 / 20.5.  The same with bf16, a bias and softmax over the chosen 18.2 / 7.3; 2 of 64 experts
+// 20.0 (288 instructions a token; the bytes take 5.6) / 14.8 (155; 10.8); one token a warp 23.0 /
+// 21.2; and with registers moved up in place of lists, two reductions a step and the logits read
+// again 27 / 20.5.  The same with bf16, a bias and softmax over the chosen 18.2 / 7.3; 2 of 64 experts
 // 9.8 / 9.5; 32768 tokens, 8 of 256 experts, bf16 16.8 / 7.3; 15762 tokens, 15 of 512 23.9 / 15.4;
 // 2048 tokens, 8 of 64 2.4 / 1.9.
 #include "device_common.cuh"

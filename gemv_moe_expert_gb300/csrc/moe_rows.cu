@@ -14,9 +14,9 @@
 //
 // A block is a grid of tx x ty threads: tx along the row (one access of VB bytes
 // a thread and step), ty tokens.  Slots are taken in batches of B, all of a batch's
-// loads issued before the first is used.  Blocks stay and walk over the tokens: the
-// places of the next token's slots are loaded while the current token's rows are in
-// flight.
+// loads issued before the first is used.  The blocks of combine and of its gradient stay
+// and walk over the tokens: the places of the next token's slots are loaded while the
+// current token's rows are in flight.  A dispatch has a block for every ty tokens.
 #include "device_common.cuh"
 
 namespace gbmm {
@@ -30,7 +30,7 @@ constexpr int B = 4;
 // 4096 elements: combine f32 95 us with 4 and 97 us with 5, bf16 52 and 51 us; its
 // gradient f32 177 us with 3 and 190 us with 4, bf16 97 and 92 us.  Shifted rows need
 // twice the registers for a piece: bf16 combine 83 us with 3 and 113 with 4; its gradient 172
-// with 4, 195 with 3 and 200 with 5.
+// with 4, 195 with 3 and 200 with 5 (with 4 it spills 112 to 120 bytes a thread).
 template <typename T, bool SHIFT> struct Resident {
     static constexpr int kDispatch = 4;
     static constexpr int kCombine = SHIFT ? 3 : sizeof(T) == 4 ? 4 : 5;
@@ -101,7 +101,7 @@ __device__ __forceinline__ uint32_t valid_rows(const MoeRowsParams &p) {
 // Places and weights of a batch of slots of token t: slot s0 + b in lane b of the
 // token's warps; kNowhere past the token's slots and past the last token, weight 0
 // where there is no expert.  One load for the batch, handed out by shuffles, so
-// that the rows' loads wait for one latency and not for eight.
+// that the rows' loads wait for one latency and not for one a slot.
 struct Slots {
     uint32_t at;
     float w;
@@ -140,7 +140,6 @@ template <typename R> struct Piece<R, true> {
 // two are separate calls so that every access in them is one predicated instruction
 // (with the choice inside the loop each load sat behind its own branch and the
 // loads of a batch no longer overlapped).
-
 //
 // Rows that do not all start on multiples of 16 bytes (SHIFT) are still written 16 bytes
 // at a time: every row that is written has its own first whole access, `head` elements
@@ -225,6 +224,8 @@ __global__ void __launch_bounds__(kThreads, Resident<T, SHIFT>::kDispatch)
     constexpr int V = VB / static_cast<int>(sizeof(T));
     grid_dep_begin();
     const uint32_t valid = valid_rows(p);
+    // One turn, as there is a block for every ty tokens (written without the loop, rows that start
+    // anywhere took 5 % longer: 59.8 us for 57.0, bf16, 4096 tokens x 8 slots x 4097).
     const uint64_t step = static_cast<uint64_t>(gridDim.x) * blockDim.y;
     uint64_t t = static_cast<uint64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     Slots slots, next;
@@ -297,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, Resident<T, SHIFT>::kCombine)
 }
 
 // Sums each v[b] over the warp; lane l returns the sum of v[l / (32 / B)]: each of
-// the first log2 B steps halves the values a lane carries, so 8 sums take 9
-// shuffles instead of 40.
+// the first log2 B steps halves the values a lane carries, so 4 sums take 6
+// shuffles instead of 20.
 __device__ __forceinline__ float warp_sums(float (&v)[B]) {
     const int lane = threadIdx.x & 31;
     int o = 16;

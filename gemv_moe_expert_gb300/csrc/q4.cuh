@@ -46,13 +46,14 @@
 // Measured (us, and GB/s of codes, scales, zeros, x and y; inputs rotate past L2):
 //   dense 11008 x 4096, groups of 128, 1 row     f16 10.2 (2270)   f32 11.3 (2060)
 //   the same, 4 f16 rows 13.1, 16 f16 rows 27.9, 8 f32 rows 28.9
-//   4 tokens x 8 of 64 experts, 1408 x 2048      bf16 14.6 (2860)   f32 18.9 (2210)
+//   4 tokens x 8 of 64 experts, 1408 x 2048      bf16 14.5 (2880)   f32 19.0 (2200)
 //   16 tokens x 8 of 128 experts, 1536 x 4096: bf16, groups of 32 with zeros 82.7 (3710);
 //   bf16, groups of 128 66.0 (4140); f32, groups of 128 104 (2630)
-// The large ones issue in more than half of the cycles, half of it the ANDs and shifts that
-// unpack the codes, and a warp waits as often for HBM as for the instructions before; the
-// last case but one takes 56.6 when x is not staged, 53.7 when nothing is multiplied.  The small
-// ones are over before HBM is at its rate.  On the way (the case with groups of 32): 16
+// No pipe is full in the large ones (an SM that has work issues in 53 % of its cycles, the ALU is
+// busy in 45 % of them, the tensor pipe in 24 %): a warp's next block is on its way only while the
+// warps beside it compute, and the last wave is short.  The last case but one takes 60.1 when x is
+// not staged and 61.0 when no zero points are subtracted.  The small ones are over before HBM is at
+// its rate.  Tried on the way (the case with groups of 32, which took 77 to 84 then): 16
 // rows a warp and 16-byte loads of half lines 151, bound by the L1 data path; a ring of
 // shared-memory slots filled by bulk copies of 256-byte row pieces 206; the next block held
 // in a second set of registers 91, as it leaves room for fewer instructions in flight; CTAs that
@@ -82,11 +83,11 @@ enum Kind { kHalf, kBfloat, kFloat };  // type of x
 
 // NT column tiles of 8, MT row tiles of 16 a warp: warps a CTA, CTAs an SM, and the shared
 // memory for a slab of x, which holds two blocks for each warp at least.
-// Eight warps share the staging of x: 4 f16 rows x 11008 x 4096 13.0 us for 15.7 with four,
-// 1 row x 4096 x 11008 11.9 for 16.2, 16 bf16 tokens x 8 of 128 experts 62.5 for 67.9 (groups of
-// 32 with zeros the same, dense 1 row 11.4 for 10.9).  f32, which needs the registers, and three
-// and more column tiles take four (8 f32 rows 28.4 for 44.3 with eight, 8 bf16 rows with
-// groups of 64 26.8 for 29.3).
+// Eight warps share the staging of x: 4 f16 rows x 11008 x 4096 13.2 us for 23.3 with four,
+// 1 row x 4096 x 11008 12.3 for 15.5, 16 bf16 tokens x 8 of 128 experts 66.1 for 71.8 (groups of
+// 32 with zeros 82.9 for 82.3).  f32, which needs the registers, and three and more column
+// tiles take four (8 f32 rows 28.9 for 38.9 with eight, 8 bf16 rows with groups of 64 27.8 for
+// 30.4).
 template <Kind K, int NT, int MT> struct Budget {
     static constexpr int kWarps = K != kFloat && NT <= 2 ? 8 : 4;
     static constexpr int kThreads = 32 * kWarps;
@@ -251,7 +252,7 @@ __device__ __forceinline__ uint32_t list_rows(const Q4Params &p, uint32_t base_r
 
 // Both for a window of at most 32 rows, which every warp sees at once: the distinct
 // experts in the order of their first rows, without a barrier (8 of 64 experts: 1 f32 token
-// 7.3 us for 7.5, 4 bf16 tokens 13.7 for 14.0).  `list` is valid after the next barrier.
+// 7.2 us for 7.5, 4 bf16 tokens 14.6 for 14.8).  `list` is valid after the next barrier.
 template <typename T>
 __device__ __forceinline__ bool find_in_warp(const Q4Params &p, uint32_t base_row, uint32_t d, int64_t j0,
                                              int tile_rows, uint32_t *list, uint32_t &expert, uint32_t &count) {
@@ -288,7 +289,9 @@ __device__ __forceinline__ void stage_x(const Q4Params &p, const Launch &cfg, co
     using T = typename XType<K>::type;
     constexpr int kTerms = K == kFloat ? 3 : 1;
     constexpr int kLanes = G / 8;  // that share a group
-    constexpr int kAhead = 3;  // loads in flight a thread (1: 8 bf16 rows 33 us for 26.8; 4: no faster)
+    // Loads in flight a thread (1: 8 bf16 rows 33.8 us for 27.8, 1 f32 row x 4096 x 11008 21.4 for 20.1,
+    // but 4 f32 tokens x 8 of 64 experts 18.4 for 19.2).
+    constexpr int kAhead = 3;
     const int lane = threadIdx.x & 31;
     // a warp takes 32 words, of one row (words is a multiple of 32), and goes on kThreads further
     uint32_t tok = 0, w = threadIdx.x;
@@ -453,9 +456,9 @@ __device__ __forceinline__ uint4 load_unaligned(bool pred, const uint8_t *p) {
 //            (groups of 32: two by two)
 //   kAtOnce  and the scales of a lane, and its zero points, can be read at once
 // Measured, 16 bf16 tokens x 8 of 128 experts, groups of 128 (of 32, with zeros): 1536 x 4096,
-// kAtOnce, 62.2 us (77.4); 1537 x 4090 with rows 2048 bytes apart, kLoose, 84.5 (149); with rows
-// 2045 bytes apart, kAnyhow, 177 (243).  Dense 1 f16 row, groups of 128: 11008 x 4224 (33 groups),
-// kApart, 11.0; 11009 x 4098 kLoose 12.3, kAnyhow 19.0.
+// kAtOnce, 66 us (83); 1537 x 4090 with rows 2048 bytes apart, kLoose, 82 (134); with rows
+// 2045 bytes apart, kAnyhow, 183 (226).  Dense 1 f16 row, groups of 128: 11008 x 4224 (33 groups),
+// kApart, 11.2; 11009 x 4098 kLoose 12.6, kAnyhow 19.4.
 enum Access { kAnyhow, kLoose, kApart, kAtOnce };
 
 // G: columns of a group.  NT: mma column tiles, 8 NT / (terms kParts) rows of x a pass.
@@ -816,11 +819,11 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     // Warps that split the columns: enough for 16 warps an SM (8, and 4 with f32, where a pass
     // takes more than one column tile, as the staging of its rows is repeated for each CTA),
     // and no warp with 16 blocks or more, so that the last CTAs are short.  Measured: 8 an SM
-    // 11.4 us for 9.5 (dense, 1 f16 row) and 23.0 for 18.3 (4 f32 tokens x 8 of 64 experts); 16
-    // an SM with more column tiles 34.6 for 28.4 (8 f32 rows), 8 and 2 with f32 61.8 and 67.2
-    // for 51.2 (6 tokens x 8 of 13 experts, 1472 x 3200, groups of 32); without the second rule
-    // 111 for 96 (16 f32 tokens x 8 of 128 experts, 16 blocks) and 90.5 for 79.5 (bf16, groups
-    // of 32), with at most 7 blocks a warp 108 and 83.4.
+    // 11.8 us for 10.0 (dense, 1 f16 row) and 24.2 for 19.3 (4 f32 tokens x 8 of 64 experts); 16
+    // an SM with more column tiles 35.0 for 28.9 (8 f32 rows), 8 and 2 with f32 60.2 and 69.2
+    // for 48.4 (6 tokens x 8 of 13 experts, 1472 x 3200, groups of 32); without the second rule
+    // 118 for 105 (16 f32 tokens x 8 of 128 experts, 16 blocks) and 95.0 for 82.9 (bf16, groups
+    // of 32), with at most 7 blocks a warp 116 and 87.5.
     int wk = 1;
     constexpr int64_t kEnough = NT == 1 ? 16 : K == kFloat ? 4 : 8;
     while (wk < kWarps && wk < blocks && (tiles * gy * wk < kEnough * num_sms || blocks >= 16 * wk)) {
@@ -851,7 +854,7 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     }
     const dim3 grid(static_cast<unsigned>((tiles + wr - 1) / wr), gy, gz);
     // (Launched early, as the MoE layer's kernels are, this one gains 0.2 us with 1 f16 row and
-    // loses 1.3 with 1 f32 row: its blocks, one wave, are spread over the SMs as places come free.)
+    // loses 1.4 with 1 f32 row: its blocks, one wave, are spread over the SMs as places come free.)
     q4_kernel<K, G, A, NT, MT><<<grid, B::kThreads, bytes, s>>>(p, cfg);
     return cudaGetLastError();
 }
@@ -875,11 +878,11 @@ cudaError_t launch_access(const Q4Params &p, int num_sms, cudaStream_t s) {
 // fewer warps are there to hide latency.  Per expert id the rows spread over the experts:
 // on average there are `share` rows for each one that occurs, and a second pass over the
 // few with more finds the weights in L2 (16 tokens x 8 of 128 experts with groups of 32:
-// 79.5 us with one tile, 85.8 with two).  A matrix of few rows and 16-bit x is cut into row
+// 82.9 us with one tile, 91.2 with two).  A matrix of few rows and 16-bit x is cut into row
 // tiles of 16, so that every SM has several warps a scheduler (dense, 1 row, 11008 x 4096
-// 9.5 us for 11.4, 4096 x 11008 11.9 for 12.9; with many rows 16 tokens x 8 of 128 experts 68.0 for
-// 62.5, hence the limit).  f32 has three times the staging for each row tile and always
-// takes 32 (11008 x 4096: 10.4 for 11.2).
+// 10.0 us for 12.0, 4096 x 11008 12.3 for 13.4; with many rows 16 tokens x 8 of 128 experts 71.1
+// for 66.1, hence the limit).  f32 has three times the staging for each row tile and always
+// takes 32 (11008 x 4096: 10.9 for 14.8; 4096 x 11008, with fewer tiles, 20.1 for 17.4).
 template <Kind K, int G>
 cudaError_t launch_g(const Q4Params &p, int num_sms, cudaStream_t s) {
     constexpr int kColumns = (K == kFloat ? 3 : 1) * Group<G>::kParts;
