@@ -37,6 +37,8 @@ ROUTE_DIRECT, ROUTE_GROUPED_PREFILL = 0, 1
 MATMUL_ID_SCHEMA_VERSION = 3
 SOFTMAX_ALL, SOFTMAX_SELECTED = 0, 1
 MOE_MAX_TOP_K = 32
+GATE_SILU, GATE_GELU, GATE_GELU_TANH, GATE_RELU = 0, 1, 2, 3
+I8_MAX_K = 131071
 GROUPED_MAX_EXPERTS = 1024
 
 # every symbol include/gbmm.h declares
@@ -49,6 +51,8 @@ EXPORTS = (
     "gbmm_moe_route", "gbmm_moe_route_backward", "gbmm_moe_sort_scratch_bytes", "gbmm_moe_sort",
     "gbmm_moe_dispatch", "gbmm_moe_dispatch_backward", "gbmm_moe_combine",
     "gbmm_moe_combine_backward", "gbmm_gemv_q4", "gbmm_matmul_id_q4",
+    "gbmm_gated", "gbmm_gated_scratch_bytes", "gbmm_gated_backward", "gbmm_gated_backward_scratch_bytes",
+    "gbmm_quantize_i8", "gbmm_gemm_i8", "gbmm_gemm_i8_scratch_bytes",
 )
 
 # n_experts * m * 4 bytes of routed rows fit the fixed scratch of
@@ -156,7 +160,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
                 ("gbmm_gemv_q4",
                  [i32, u32, i64, i64, u32, vp, i64, vp, i32, vp, vp, i64, vp, i64, vp]),
                 ("gbmm_matmul_id_q4",
-                 [i32, u32, i64, i64, u32, u32, u32, u32, vp, i64, i64, vp, i32, vp, vp, vp, vp, vp])):
+                 [i32, u32, i64, i64, u32, u32, u32, u32, vp, i64, i64, vp, i32, vp, vp, vp, vp, vp]),
+                ("gbmm_gated_scratch_bytes", [i32, i64, i64, i64, ctypes.POINTER(u64)]),
+                ("gbmm_gated",
+                 [i32, u32, i64, i64, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, u64, vp]),
+                ("gbmm_gated_backward_scratch_bytes", [i32, i64, i64, i64, ctypes.POINTER(u64)]),
+                ("gbmm_gated_backward",
+                 [i32, u32, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, u64,
+                  vp]),
+                ("gbmm_quantize_i8", [i32, i64, i64, vp, i64, vp, i64, vp, vp]),
+                ("gbmm_gemm_i8_scratch_bytes", [i64, i64, i64, ctypes.POINTER(u64)]),
+                ("gbmm_gemm_i8", [i32, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, u64, vp])):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = i32
         _lib = lib
@@ -336,6 +350,51 @@ def gbmm_matmul_id_q4(dtype, m, n, k, top_k, n_experts, input_layout, group, q, 
                                     _ptr(q), ldq_bytes, expert_stride_bytes, _ptr(scales),
                                     _dt(scale_dtype), _ptr(zeros), _ptr(x), _ptr(ids), _ptr(out),
                                     _stream(stream))
+
+
+def gbmm_gated_scratch_bytes(dtype, m: int, n: int, k: int):
+    """Returns (status, bytes)."""
+    need = ctypes.c_uint64(0)
+    st = load().gbmm_gated_scratch_bytes(_dt(dtype), m, n, k, ctypes.byref(need))
+    return st, need.value
+
+
+def gbmm_gated(dtype, activation, m, n, k, x, ldx, w_gate, w_up, ldw, h, ldh, gate, up, ld_saved, scratch,
+               scratch_bytes, stream=None) -> int:
+    return load().gbmm_gated(_dt(dtype), activation, m, n, k, _ptr(x), ldx, _ptr(w_gate), _ptr(w_up), ldw, _ptr(h),
+                             ldh, _ptr(gate), _ptr(up), ld_saved, _ptr(scratch), scratch_bytes, _stream(stream))
+
+
+def gbmm_gated_backward_scratch_bytes(dtype, m: int, n: int, k: int):
+    """Returns (status, bytes)."""
+    need = ctypes.c_uint64(0)
+    st = load().gbmm_gated_backward_scratch_bytes(_dt(dtype), m, n, k, ctypes.byref(need))
+    return st, need.value
+
+
+def gbmm_gated_backward(dtype, activation, m, n, k, x, ldx, w_gate, w_up, ldw, gate, up, ld_saved, d_h, ld_dh, d_x,
+                        ld_dx, d_w_gate, d_w_up, ld_dw, scratch, scratch_bytes, stream=None) -> int:
+    return load().gbmm_gated_backward(_dt(dtype), activation, m, n, k, _ptr(x), ldx, _ptr(w_gate), _ptr(w_up), ldw,
+                                      _ptr(gate), _ptr(up), ld_saved, _ptr(d_h), ld_dh, _ptr(d_x), ld_dx,
+                                      _ptr(d_w_gate), _ptr(d_w_up), ld_dw, _ptr(scratch), scratch_bytes,
+                                      _stream(stream))
+
+
+def gbmm_quantize_i8(dtype, m, k, x, ldx, q, ldq, scale, stream=None) -> int:
+    return load().gbmm_quantize_i8(_dt(dtype), m, k, _ptr(x), ldx, _ptr(q), ldq, _ptr(scale), _stream(stream))
+
+
+def gbmm_gemm_i8_scratch_bytes(m: int, n: int, k: int):
+    """Returns (status, bytes)."""
+    need = ctypes.c_uint64(0)
+    st = load().gbmm_gemm_i8_scratch_bytes(m, n, k, ctypes.byref(need))
+    return st, need.value
+
+
+def gbmm_gemm_i8(dtype, m, n, k, a, lda, scale_a, b, ldb, scale_b, c, ldc, scratch, scratch_bytes,
+                 stream=None) -> int:
+    return load().gbmm_gemm_i8(_dt(dtype), m, n, k, _ptr(a), lda, _ptr(scale_a), _ptr(b), ldb, _ptr(scale_b), _ptr(c),
+                               ldc, _ptr(scratch), scratch_bytes, _stream(stream))
 
 
 def gbmm_last_error() -> str:

@@ -1,0 +1,277 @@
+// ffn_api.cu -- the extern "C" entry points of the gated projection
+// (gbmm_gated*) and of the 8-bit integer product (gbmm_quantize_i8,
+// gbmm_gemm_i8): argument checks, all of them before the first launch, then
+// the choice of kernels.
+#include "api_checks.h"
+#include "kernel_params.h"
+
+using namespace gbmm;
+
+namespace {
+
+constexpr int64_t kAlign = 256;  // of each part of a scratch buffer
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+bool in_range(int64_t v) { return v >= 0 && v <= INT32_MAX; }
+
+// The parts that a call takes from its scratch, one behind the other, each on a multiple of
+// kAlign bytes from a base that is rounded up to one.
+struct Parts {
+    uint64_t bytes = kAlign;
+    uint64_t add(int64_t rows, int64_t ld, int size) {
+        const uint64_t at = bytes;
+        bytes += static_cast<uint64_t>(round_up(rows * ld * size, kAlign));
+        return at;
+    }
+    static char *base(void *scratch) {
+        return reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(scratch) + kAlign - 1) / kAlign * kAlign) - kAlign;
+    }
+};
+
+Operand matrix(const char *label, const void *p, uint64_t bytes, int64_t cols, int64_t ld, uint32_t size, bool output) {
+    return {label, p, bytes, size, output, static_cast<uint64_t>(cols) * size, static_cast<uint64_t>(ld) * size};
+}
+
+gbmm_status check_gated(const char *fn, gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n, int64_t k) {
+    if (!known_dtype(dt))
+        return fail(GBMM_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d is not f32, f16 or bf16", fn, (int)dt);
+    if (activation > GBMM_GATE_RELU)
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: unknown activation %u", fn, activation);
+    if (!in_range(m) || !in_range(n) || !in_range(k))
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: m, n and k must lie in [0, 2^31)", fn);
+    return GBMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gbmm_status gbmm_gated_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, uint64_t *bytes) {
+    record_error(GBMM_OK, "");
+    const char *fn = "gbmm_gated_scratch_bytes";
+    const gbmm_status st = check_gated(fn, dt, 0, m, n, k);
+    if (st != GBMM_OK) return st;
+    if (bytes == nullptr) return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: bytes is null", fn);
+    *bytes = 0;
+    return GBMM_OK;
+}
+
+gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx,
+                       const void *w_gate, const void *w_up, int64_t ldw, void *h, int64_t ldh, void *gate, void *up,
+                       int64_t ld_saved, void *scratch, uint64_t scratch_bytes, gbmm_stream stream) {
+    record_error(GBMM_OK, "");
+    const char *fn = "gbmm_gated";
+    gbmm_status st = check_gated(fn, dt, activation, m, n, k);
+    if (st != GBMM_OK) return st;
+    if ((gate == nullptr) != (up == nullptr))
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: gate and up come together or not at all", fn);
+    if (ldx < k || ldw < k || ldh < n || (gate != nullptr && ld_saved < n))
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: a leading dimension is smaller than its row", fn);
+    if (m == 0 || n == 0) return GBMM_OK;
+    const uint32_t size = static_cast<uint32_t>(dtype_size(dt));
+    uint64_t xb, wb, hb, sb = 0;
+    if (!span(m, k, ldx, size, &xb) || !span(n, k, ldw, size, &wb) || !span(m, n, ldh, size, &hb) ||
+        (gate != nullptr && !span(m, n, ld_saved, size, &sb)))
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: operand extent overflows", fn);
+    const Operand ops[] = {matrix("x", x, xb, k, ldx, size, false),       matrix("w_gate", w_gate, wb, k, ldw, size, false),
+                           matrix("w_up", w_up, wb, k, ldw, size, false), matrix("h", h, hb, n, ldh, size, true),
+                           matrix("gate", gate, sb, n, ld_saved, size, true), matrix("up", up, sb, n, ld_saved, size, true),
+                           {"scratch", scratch, scratch ? scratch_bytes : 0, 1, true}};
+    st = check_operands(fn, ops, 7);
+    if (st != GBMM_OK) return st;
+    if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
+    GatedParams p{};
+    p.x = x;
+    p.w[0] = w_gate;
+    p.w[1] = w_up;
+    p.h = h;
+    p.saved[0] = gate;
+    p.saved[1] = up;
+    p.m = m;
+    p.n = n;
+    p.k = k;
+    p.ldx = ldx;
+    p.ldw = ldw;
+    p.ldh = ldh;
+    p.ld_saved = ld_saved;
+    p.act = static_cast<int32_t>(activation);
+    cudaStream_t s = cuda_stream(stream);
+    return finish_launch(m <= 8 ? launch_gated_rowdot(dt, p, s) : launch_gated_simt(dt, p, s), fn, s);
+}
+
+gbmm_status gbmm_gated_backward_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, uint64_t *bytes) {
+    record_error(GBMM_OK, "");
+    const char *fn = "gbmm_gated_backward_scratch_bytes";
+    const gbmm_status st = check_gated(fn, dt, 0, m, n, k);
+    if (st != GBMM_OK) return st;
+    if (bytes == nullptr) return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: bytes is null", fn);
+    const int size = dtype_size(dt);
+    Parts parts;
+    const int64_t ldd = round_up(n, 16 / size);
+    parts.add(m, ldd, size);
+    parts.add(m, ldd, size);
+    *bytes = parts.bytes;
+    return GBMM_OK;
+}
+
+gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n, int64_t k, const void *x,
+                                int64_t ldx, const void *w_gate, const void *w_up, int64_t ldw, const void *gate,
+                                const void *up, int64_t ld_saved, const void *d_h, int64_t ld_dh, void *d_x,
+                                int64_t ld_dx, void *d_w_gate, void *d_w_up, int64_t ld_dw, void *scratch,
+                                uint64_t scratch_bytes, gbmm_stream stream) {
+    record_error(GBMM_OK, "");
+    const char *fn = "gbmm_gated_backward";
+    gbmm_status st = check_gated(fn, dt, activation, m, n, k);
+    if (st != GBMM_OK) return st;
+    if ((d_w_gate == nullptr) != (d_w_up == nullptr))
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: d_w_gate and d_w_up come together or not at all", fn);
+    const bool need_x = d_x != nullptr, need_w = d_w_gate != nullptr;
+    if ((need_w && ldx < k) || (need_x && ldw < k) || ld_saved < n || ld_dh < n || (need_x && ld_dx < k) ||
+        (need_w && ld_dw < k))
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: a leading dimension is smaller than its row", fn);
+    if (k == 0 || (!need_x && !need_w) || (m == 0 && !need_w) || (n == 0 && !need_x) || (m == 0 && n == 0))
+        return GBMM_OK;
+    const uint32_t size = static_cast<uint32_t>(dtype_size(dt));
+    uint64_t xb, wb, sb, hb, dxb = 0, dwb = 0;
+    if (!span(m, k, ldx, size, &xb) || !span(n, k, ldw, size, &wb) || !span(m, n, ld_saved, size, &sb) ||
+        !span(m, n, ld_dh, size, &hb) || (need_x && !span(m, k, ld_dx, size, &dxb)) ||
+        (need_w && !span(n, k, ld_dw, size, &dwb)))
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: operand extent overflows", fn);
+    const bool empty = m == 0 || n == 0;  // what is left to do is writing zeros
+    if (empty || !need_w) xb = 0;
+    if (empty || !need_x) wb = 0;
+    uint64_t need;
+    st = gbmm_gated_backward_scratch_bytes(dt, m, n, k, &need);
+    if (st != GBMM_OK) return st;
+    const Operand ops[] = {matrix("x", x, xb, k, ldx, size, false),
+                           matrix("w_gate", w_gate, wb, k, ldw, size, false),
+                           matrix("w_up", w_up, wb, k, ldw, size, false),
+                           matrix("gate", gate, sb, n, ld_saved, size, false),
+                           matrix("up", up, sb, n, ld_saved, size, false),
+                           matrix("d_h", d_h, hb, n, ld_dh, size, false),
+                           matrix("d_x", d_x, dxb, k, ld_dx, size, true),
+                           matrix("d_w_gate", d_w_gate, dwb, k, ld_dw, size, true),
+                           matrix("d_w_up", d_w_up, dwb, k, ld_dw, size, true),
+                           {"scratch", scratch, scratch ? scratch_bytes : 0, 1, true}};
+    st = check_operands(fn, ops, 10);
+    if (st != GBMM_OK) return st;
+    if (!empty && (scratch == nullptr || scratch_bytes < need))
+        return fail(GBMM_ERR_SCRATCH, "%s: needs %llu bytes of scratch (got %llu)", fn, (unsigned long long)need,
+                    (unsigned long long)(scratch ? scratch_bytes : 0));
+    // the products' kernels are asked for before the first launch, so that nothing runs where one is missing
+    static const char *const kProducts[] = {"gbmm_fill_zero",     "gbmm_gemm_tc", "gbmm_gemm_simt", "gbmm_gemv_rowdot",
+                                            "gbmm_gemv_coldot", "gbmm_gemv_tc"};
+    if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
+    for (const char *name : kProducts)
+        if (!resolve_kernel(name)) return GBMM_ERR_KERNEL_UNAVAILABLE;
+    cudaStream_t s = cuda_stream(stream);
+    if (empty) {
+        if (m == 0) {
+            st = finish_launch(launch_fill_zero(dt, d_w_gate, 1, n, k, ld_dw, 0, s), fn, s);
+            if (st == GBMM_OK) st = finish_launch(launch_fill_zero(dt, d_w_up, 1, n, k, ld_dw, 0, s), fn, s);
+        } else {
+            st = finish_launch(launch_fill_zero(dt, d_x, 1, m, k, ld_dx, 0, s), fn, s);
+        }
+        return st;
+    }
+    Parts parts;
+    const int64_t ldd = round_up(n, 16 / size);
+    GatedGradParams g{};
+    g.gate = gate;
+    g.up = up;
+    g.d_h = d_h;
+    g.d[0] = Parts::base(scratch) + parts.add(m, ldd, size);
+    g.d[1] = Parts::base(scratch) + parts.add(m, ldd, size);
+    g.m = m;
+    g.n = n;
+    g.ld_saved = ld_saved;
+    g.ld_dh = ld_dh;
+    g.ldd = ldd;
+    g.act = static_cast<int32_t>(activation);
+    st = finish_launch(launch_gated_grad(dt, g, s), fn, s);
+    if (st != GBMM_OK) return st;
+    if (need_x) {
+        SumGemmParams q{{g.d[0], g.d[1]}, {w_gate, w_up}, d_x, m, k, n, ldd, ldw, ld_dx};
+        st = finish_launch(launch_sum_gemm_simt(dt, q, s), fn, s);
+        if (st != GBMM_OK) return st;
+    }
+    if (need_w) {
+        void *const dw[2] = {d_w_gate, d_w_up};
+        for (int i = 0; i < 2 && st == GBMM_OK; ++i)
+            st = gbmm_gemm(dt, 1, n, k, m, 1, 0, g.d[i], 0, ldd, 0, x, 0, ldx, 0, dw[i], 0, ld_dw, 0, stream);
+    }
+    return st;
+}
+
+gbmm_status gbmm_quantize_i8(gbmm_dtype dt, int64_t m, int64_t k, const void *x, int64_t ldx, int8_t *q, int64_t ldq,
+                             float *scale, gbmm_stream stream) {
+    record_error(GBMM_OK, "");
+    const char *fn = "gbmm_quantize_i8";
+    if (!known_dtype(dt))
+        return fail(GBMM_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d is not f32, f16 or bf16", fn, (int)dt);
+    if (!in_range(m) || !in_range(k))
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: m and k must lie in [0, 2^31)", fn);
+    if (ldx < k || ldq < k)
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: a leading dimension is smaller than the row length %lld", fn,
+                    (long long)k);
+    if (m == 0) return GBMM_OK;
+    const uint32_t size = static_cast<uint32_t>(dtype_size(dt));
+    uint64_t xb, qb;
+    if (!span(m, k, ldx, size, &xb) || !span(m, k, ldq, 1, &qb))
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: operand extent overflows", fn);
+    const Operand ops[] = {matrix("x", x, xb, k, ldx, size, false), matrix("q", q, qb, k, ldq, 1, true),
+                           {"scale", scale, static_cast<uint64_t>(m) * 4, 4, true}};
+    const gbmm_status st = check_operands(fn, ops, 3);
+    if (st != GBMM_OK) return st;
+    if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
+    const QuantizeParams p{x, q, scale, m, k, ldx, ldq};
+    return finish_launch(launch_quantize_i8(dt, p, cuda_stream(stream)), fn, cuda_stream(stream));
+}
+
+gbmm_status gbmm_gemm_i8_scratch_bytes(int64_t m, int64_t n, int64_t k, uint64_t *bytes) {
+    record_error(GBMM_OK, "");
+    const char *fn = "gbmm_gemm_i8_scratch_bytes";
+    if (!in_range(m) || !in_range(n) || k < 0 || k > GBMM_I8_MAX_K)
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: m and n must lie in [0, 2^31), k in [0, %d]", fn, GBMM_I8_MAX_K);
+    if (bytes == nullptr) return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: bytes is null", fn);
+    *bytes = 0;
+    return GBMM_OK;
+}
+
+gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const int8_t *a, int64_t lda,
+                         const float *scale_a, const int8_t *b, int64_t ldb, const float *scale_b, void *c, int64_t ldc,
+                         void *scratch, uint64_t scratch_bytes, gbmm_stream stream) {
+    record_error(GBMM_OK, "");
+    const char *fn = "gbmm_gemm_i8";
+    if (!known_dtype(dt))
+        return fail(GBMM_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d is not f32, f16 or bf16", fn, (int)dt);
+    uint64_t need;
+    if (!in_range(m) || !in_range(n) || k < 0 || k > GBMM_I8_MAX_K)
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: m and n must lie in [0, 2^31), k in [0, %d]", fn, GBMM_I8_MAX_K);
+    if (lda < k || ldb < k || ldc < n)
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: a leading dimension is smaller than its row", fn);
+    if (m == 0 || n == 0) return GBMM_OK;
+    const uint32_t size = static_cast<uint32_t>(dtype_size(dt));
+    uint64_t ab, bb, cb;
+    if (!span(m, k, lda, 1, &ab) || !span(n, k, ldb, 1, &bb) || !span(m, n, ldc, size, &cb))
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: operand extent overflows", fn);
+    gbmm_status st = gbmm_gemm_i8_scratch_bytes(m, n, k, &need);
+    if (st != GBMM_OK) return st;
+    const Operand ops[] = {matrix("a", a, ab, k, lda, 1, false),
+                           {"scale_a", scale_a, scale_a ? static_cast<uint64_t>(m) * 4 : 0, 4, false},
+                           matrix("b", b, bb, k, ldb, 1, false),
+                           {"scale_b", scale_b, scale_b ? static_cast<uint64_t>(n) * 4 : 0, 4, false},
+                           matrix("c", c, cb, n, ldc, size, true),
+                           {"scratch", scratch, scratch ? scratch_bytes : 0, 1, true}};
+    st = check_operands(fn, ops, 6);
+    if (st != GBMM_OK) return st;
+    if (need > 0 && (scratch == nullptr || scratch_bytes < need))
+        return fail(GBMM_ERR_SCRATCH, "%s: needs %llu bytes of scratch (got %llu)", fn, (unsigned long long)need,
+                    (unsigned long long)(scratch ? scratch_bytes : 0));
+    if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
+    const GemmI8Params p{a, b, scale_a, scale_b, c, m, n, k, lda, ldb, ldc};
+    return finish_launch(launch_gemm_i8_dot(dt, p, cuda_stream(stream)), fn, cuda_stream(stream));
+}
+
+}  // extern "C"

@@ -168,6 +168,54 @@ struct Q4Params {
 constexpr uint32_t kQ4Window = 1024;  // routed rows that a CTA searches for its expert's
 constexpr uint32_t kQ4LaunchRows = 65535u * kQ4Window;
 
+// Gated projection h = act(x Wg^T) * (x Wu^T) (gated.cu): index 0 is the gate, 1 the up projection.
+struct GatedParams {
+    const void *x;
+    const void *w[2];  // [n, k]
+    void *h;
+    void *saved[2];    // both projections, or null
+    int64_t m, n, k;
+    int64_t ldx, ldw, ldh, ld_saved;
+    int32_t act;       // GBMM_GATE_*
+};
+
+// d_gate and d_up from d_h and the saved projections (gated.cu).
+struct GatedGradParams {
+    const void *gate, *up, *d_h;
+    void *d[2];
+    int64_t m, n, ld_saved, ld_dh, ldd;
+    int32_t act;
+};
+
+// c [m, n] = a[0] b[0] + a[1] b[1], a [m, k] and b [k, n] (gated.cu).
+struct SumGemmParams {
+    const void *a[2], *b[2];
+    void *c;
+    int64_t m, n, k, lda, ldb, ldc;
+};
+
+// Rows laid out again: src [rows, cols] (16-bit values, or 8-bit codes that become f16) into
+// dst [rows, ldd] (gated.cu).
+struct RepackParams {
+    const void *src;
+    void *dst;
+    int64_t rows, cols, lds, ldd;
+};
+
+// Rows to 8-bit codes with a scale each, and the product of such codes (i8.cu).
+struct QuantizeParams {
+    const void *x;
+    int8_t *q;
+    float *scale;
+    int64_t m, k, ldx, ldq;
+};
+struct GemmI8Params {
+    const int8_t *a, *b;
+    const float *scale_a, *scale_b;  // null: 1
+    void *c;
+    int64_t m, n, k, lda, ldb, ldc;
+};
+
 // ---- launchers (each returns the launch's cudaError_t) --------------------
 
 cudaError_t launch_fill_zero(int dt, void *c, int64_t batch, int64_t m, int64_t n, int64_t ldc,
@@ -233,6 +281,16 @@ cudaError_t launch_moe_combine_backward(int dt, const MoeRowsParams &p, cudaStre
 cudaError_t launch_q4_f32(const Q4Params &p, cudaStream_t s);
 cudaError_t launch_q4_f16(const Q4Params &p, cudaStream_t s);
 cudaError_t launch_q4_bf16(const Q4Params &p, cudaStream_t s);
+
+// gated projection: one warp a column for few rows, FFMA tiles for any number
+cudaError_t launch_gated_rowdot(int dt, const GatedParams &p, cudaStream_t s);
+cudaError_t launch_gated_simt(int dt, const GatedParams &p, cudaStream_t s);
+cudaError_t launch_gated_grad(int dt, const GatedGradParams &p, cudaStream_t s);
+cudaError_t launch_sum_gemm_simt(int dt, const SumGemmParams &p, cudaStream_t s);
+cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s);
+cudaError_t launch_codes_to_f16(const RepackParams &p, cudaStream_t s);
+cudaError_t launch_quantize_i8(int dt, const QuantizeParams &p, cudaStream_t s);
+cudaError_t launch_gemm_i8_dot(int dt, const GemmI8Params &p, cudaStream_t s);
 
 int gemm_tc_block_m();
 int gemm_tc_wide_block_m();

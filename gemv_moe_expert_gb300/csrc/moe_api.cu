@@ -2,72 +2,13 @@
 // around the expert products (gbmm_moe_*) and of the 4-bit matrix-vector
 // products (gbmm_gemv_q4, gbmm_matmul_id_q4): argument checks, all of them
 // before the first launch, then the launchers.
-#include <cstdarg>
-#include <cstdio>
-
+#include "api_checks.h"
 #include "api_internal.h"
 #include "kernel_params.h"
 
 using namespace gbmm;
 
 namespace {
-
-gbmm_status fail(gbmm_status s, const char *fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    return static_cast<gbmm_status>(record_error(s, buf));
-}
-
-// one operand of a call: the bytes it spans, its alignment and whether the call writes it
-struct Operand {
-    const char *label;
-    const void *ptr;
-    uint64_t bytes;
-    uint32_t align;
-    bool output;
-};
-
-// bytes from the first to the last element of [rows, cols] with rows ld elements apart
-bool span(uint64_t rows, int64_t cols, int64_t ld, uint64_t size, uint64_t *out) {
-    if (rows == 0 || cols == 0) {
-        *out = 0;
-        return true;
-    }
-    const unsigned __int128 last =
-        static_cast<unsigned __int128>(rows - 1) * static_cast<uint64_t>(ld) + static_cast<uint64_t>(cols);
-    if (last > INT64_MAX / size) return false;
-    *out = static_cast<uint64_t>(last) * size;
-    return true;
-}
-
-// Non-null, aligned, and no output on top of another operand.  Operands of 0
-// bytes are not looked at.
-gbmm_status check_operands(const char *fn, const Operand *ops, int count) {
-    for (int i = 0; i < count; ++i) {
-        if (ops[i].bytes == 0) continue;
-        if (ops[i].ptr == nullptr) return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: %s is null", fn, ops[i].label);
-        if (reinterpret_cast<uintptr_t>(ops[i].ptr) % ops[i].align != 0)
-            return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: %s is not aligned to its element", fn, ops[i].label);
-        if (ops[i].bytes > UINTPTR_MAX - reinterpret_cast<uintptr_t>(ops[i].ptr))
-            return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: %s runs past the address space", fn, ops[i].label);
-    }
-    for (int i = 0; i < count; ++i) {
-        if (!ops[i].output || ops[i].bytes == 0) continue;
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(ops[i].ptr), hi = lo + ops[i].bytes;
-        for (int j = 0; j < count; ++j) {
-            if (j == i || ops[j].bytes == 0) continue;
-            const uintptr_t l = reinterpret_cast<uintptr_t>(ops[j].ptr), h = l + ops[j].bytes;
-            if (lo < h && l < hi)
-                return fail(GBMM_ERR_OVERLAP, "%s: %s overlaps %s", fn, ops[i].label, ops[j].label);
-        }
-    }
-    return GBMM_OK;
-}
-
-bool known_dtype(gbmm_dtype dt) { return dt == GBMM_F32 || dt == GBMM_F16 || dt == GBMM_BF16; }
 
 // m, top_k and n_experts of every gbmm_moe_* call and of gbmm_matmul_id_q4
 gbmm_status check_slots(const char *fn, uint32_t m, uint32_t top_k, uint32_t n_experts) {
@@ -160,8 +101,6 @@ MoeRowsParams rows_params(const RowsCall &c) {
     p.valid = c.offsets ? c.offsets + c.n_experts : nullptr;
     return p;
 }
-
-cudaStream_t cuda_stream(gbmm_stream s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Checks shared by the two 4-bit calls, and the parameter block.
 gbmm_status check_q4(const char *fn, gbmm_dtype dt, int64_t n, int64_t k, uint32_t group, int64_t ldq,

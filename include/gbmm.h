@@ -1,7 +1,8 @@
 /*
  * gbmm.h -- C ABI of the GB300 (sm_103a) dense GEMM / GEMV / expert-ID matmul
  * library (libgbmm.so), with the router, token order and gradients of a
- * mixture-of-experts layer and 4-bit matrix-vector products.
+ * mixture-of-experts layer, 4-bit matrix-vector products, the gated
+ * feed-forward projection with its gradients and products of 8-bit integers.
  *
  * Conventions shared by every entry point
  *   - Pointers named a, b, c, weights, input, ids, out, expert_counts and
@@ -518,6 +519,99 @@ GBMM_API gbmm_status gbmm_matmul_id_q4(gbmm_dtype dt, uint32_t m, int64_t n, int
                                        const void *x, const uint32_t *ids, void *out, gbmm_stream stream);
 
 /* ------------------------------------------------------------------------ */
+/* Gated feed-forward projection                                              */
+/* ------------------------------------------------------------------------ */
+/*
+ * The first half of a gated feed-forward block, forward and backward; its second
+ * half, the product with the down projection, is gbmm_gemm's (or gbmm_gemm_i8's).
+ * dt (f32, f16, bf16) is the type of every matrix of a call.  x [m, k], both weights
+ * [n, k], h, gate, up and d_h [m, n], rows ld* elements apart (both weights with the
+ * same ldw, both saved projections with the same ld_saved, both weights' gradients
+ * with the same ld_dw; two of them may lie side by side in rows of that pitch).
+ * m, n and k below 2^31.  Sums are f32 in a fixed order, and each output is rounded
+ * once.  Pointers must be aligned to their elements, and outputs must not overlap
+ * inputs, scratch or each other (GBMM_ERR_OVERLAP).
+ */
+enum {
+    GBMM_GATE_SILU = 0,      /* v / (1 + e^-v) */
+    GBMM_GATE_GELU = 1,      /* v (1 + erf(v / sqrt 2)) / 2 */
+    GBMM_GATE_GELU_TANH = 2, /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+    GBMM_GATE_RELU = 3       /* max(v, 0); slope 0 at 0 */
+};
+
+/* gbmm_gated_scratch_bytes -- bytes of scratch with which gbmm_gated runs these sizes at
+ * full speed whatever the layout of its operands.  Host-only. */
+GBMM_API gbmm_status gbmm_gated_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, uint64_t *bytes);
+
+/*
+ * gbmm_gated -- h = act(x w_gate^T) * (x w_up^T), both projections, the activation and
+ * the product in one kernel.
+ * gate, up: both NULL, or both projections are written too (for gbmm_gated_backward).
+ * h is computed from the unrounded projections.
+ * scratch: may be NULL.  Calls in flight must not share it.
+ * m or n == 0 is a no-op; k == 0 writes zeros.
+ */
+GBMM_API gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n, int64_t k, const void *x,
+                                int64_t ldx, const void *w_gate, const void *w_up, int64_t ldw, void *h, int64_t ldh,
+                                void *gate, void *up, int64_t ld_saved, void *scratch, uint64_t scratch_bytes,
+                                gbmm_stream stream);
+
+/* gbmm_gated_backward_scratch_bytes -- bytes of scratch that gbmm_gated_backward needs. Host-only. */
+GBMM_API gbmm_status gbmm_gated_backward_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k,
+                                                       uint64_t *bytes);
+
+/*
+ * gbmm_gated_backward -- from d_h, x, the weights and the saved projections:
+ *   d_gate = d_h * up * act'(gate)      d_up = d_h * act(gate)     (rounded to dt)
+ *   d_x [m, k] = d_gate w_gate + d_up w_up
+ *   d_w_gate [n, k] = d_gate^T x        d_w_up [n, k] = d_up^T x
+ * d_x may be NULL (the weights are not read then), and d_w_gate and d_w_up may both be (x is
+ * not read).  Gradients are written, not added.  An m of 0 writes zeros to the weights'
+ * gradients, an n of 0 zeros to d_x.
+ * scratch: at least gbmm_gated_backward_scratch_bytes(), else GBMM_ERR_SCRATCH; its contents
+ * need no preparation, and calls in flight must not share it.
+ */
+GBMM_API gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n, int64_t k,
+                                         const void *x, int64_t ldx, const void *w_gate, const void *w_up, int64_t ldw,
+                                         const void *gate, const void *up, int64_t ld_saved, const void *d_h,
+                                         int64_t ld_dh, void *d_x, int64_t ld_dx, void *d_w_gate, void *d_w_up,
+                                         int64_t ld_dw, void *scratch, uint64_t scratch_bytes, gbmm_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* Matrix product in 8-bit integers                                           */
+/* ------------------------------------------------------------------------ */
+
+/* Longest contraction of gbmm_gemm_i8: its sums stay inside 32-bit integers. */
+#define GBMM_I8_MAX_K 131071
+
+/*
+ * gbmm_quantize_i8 -- rows of x [m, k] to codes q [m, k] and a scale for each row:
+ *   scale[i] = max |x[i,:]| * (1.0f / 127.0f) in f32;  q[i,x] = the integer nearest to
+ *   x[i,x] / scale[i] (the real quotient, ties to even), within -127..127
+ * so that x is about q * scale.  A row of zeros (or one whose scale is 0 in f32) gets scale 0
+ * and codes 0, a row that holds a NaN or an infinity scale NaN and codes 0.  It serves tokens
+ * (rows of activations) and channels (rows of a weight [n, k]) alike.  x of type dt.  m == 0 is
+ * a no-op; k == 0 writes scales of 0.
+ */
+GBMM_API gbmm_status gbmm_quantize_i8(gbmm_dtype dt, int64_t m, int64_t k, const void *x, int64_t ldx, int8_t *q,
+                                      int64_t ldq, float *scale, gbmm_stream stream);
+
+/* gbmm_gemm_i8_scratch_bytes -- bytes of scratch that gbmm_gemm_i8 needs (0 is possible).  Host-only. */
+GBMM_API gbmm_status gbmm_gemm_i8_scratch_bytes(int64_t m, int64_t n, int64_t k, uint64_t *bytes);
+
+/*
+ * gbmm_gemm_i8 -- c[i,j] = (sum_x a[i,x] b[j,x]) * scale_a[i] * scale_b[j]
+ * a [m, k] and b [n, k]: codes from -128 to 127, rows lda / ldb bytes apart, any alignment.
+ * The sum is that of integers, exactly; it is rounded to f32, multiplied by scale_a and then by
+ * scale_b (f32; NULL for 1), and rounded to dt, the type of c.  k <= GBMM_I8_MAX_K.
+ * scratch: at least gbmm_gemm_i8_scratch_bytes(), else GBMM_ERR_SCRATCH; its contents need no
+ * preparation, and calls in flight must not share it.  m or n == 0 is a no-op.
+ */
+GBMM_API gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const int8_t *a, int64_t lda,
+                                  const float *scale_a, const int8_t *b, int64_t ldb, const float *scale_b, void *c,
+                                  int64_t ldc, void *scratch, uint64_t scratch_bytes, gbmm_stream stream);
+
+/* ------------------------------------------------------------------------ */
 /* Errors, diagnostics                                                        */
 /* ------------------------------------------------------------------------ */
 
@@ -553,8 +647,8 @@ GBMM_API gbmm_status gbmm_device_error(gbmm_stream stream, uint32_t *code);
  * (tests that hand the library addresses no kernel may touch use it).
  * Kernel names: "gbmm_gemv_rowdot", "gbmm_gemv_coldot", "gbmm_gemv_tc", "gbmm_gemm_simt",
  * "gbmm_gemm_tc", "gbmm_fill_zero", "gbmm_matmul_id_direct",
- * "gbmm_matmul_id_map", "gbmm_matmul_id_grouped", and the names of the gbmm_moe_*
- * and *_q4 entry points for theirs; "gbmm_moe_sort_place" is the last of gbmm_moe_sort's three. */
+ * "gbmm_matmul_id_map", "gbmm_matmul_id_grouped", and the names of the gbmm_moe_*,
+ * *_q4, gbmm_gated* and *_i8 entry points for theirs; "gbmm_moe_sort_place" is the last of gbmm_moe_sort's three. */
 GBMM_API void gbmm_test_inject_kernel_failure(const char *name);
 
 /* Kernels launched by this library since load / the last reset. */
@@ -566,7 +660,7 @@ GBMM_API void gbmm_test_reset_launch_count(void);
  * "gbmm_gemv_rowdot", "gbmm_gemv_coldot", "gbmm_gemv_tc", "gbmm_fill_zero",
  * "gbmm_matmul_id_direct", "gbmm_matmul_id_direct_tc", "gbmm_matmul_id_map",
  * "gbmm_matmul_id_grouped_tc", "gbmm_matmul_id_grouped_simt", "gbmm_bounded_wait_test" for the wait test below, and
- * the names of the gbmm_moe_* and *_q4 entry points for theirs. */
+ * the names of the gbmm_moe_*, *_q4, gbmm_gated* and *_i8 entry points for theirs. */
 GBMM_API const char *gbmm_test_last_kernel(void);
 
 /*

@@ -1,0 +1,146 @@
+"""Host-only refusals of the gated projection, the quantisation and the 8-bit
+product: every rule of include/gbmm.h is checked before the first launch.  The
+pointers are fake, aligned addresses, and every kernel is made unavailable, so a
+call that passes its checks answers GBMM_ERR_KERNEL_UNAVAILABLE."""
+
+import pytest
+
+from gemv_moe_expert_gb300 import binding as gb
+from gemv_moe_expert_gb300 import build as gbuild
+
+BAD, OVERLAP, DTYPE, SCRATCH = (gb.GBMM_ERR_INVALID_ARGUMENT, gb.GBMM_ERR_OVERLAP, gb.GBMM_ERR_UNSUPPORTED_DTYPE,
+                                gb.GBMM_ERR_SCRATCH)
+PASSES = gb.GBMM_ERR_KERNEL_UNAVAILABLE
+BASE, STEP = 1 << 40, 1 << 24
+A, B, C, D, E, F, G, H, I, J, K = (BASE + i * STEP for i in range(11))
+
+
+@pytest.fixture(autouse=True)
+def _no_kernel_may_launch():
+    gbuild.build()
+    gb.load()
+    gb.gbmm_test_inject_kernel_failure("*")
+    gb.gbmm_test_reset_launch_count()
+    yield
+    assert gb.gbmm_test_launch_count() == 0
+    gb.gbmm_test_inject_kernel_failure(None)
+
+
+def call(fn, defaults, over):
+    args = dict(defaults)
+    assert set(over) <= set(args), over
+    args.update(over)
+    return fn(*args.values(), stream=0)
+
+
+GATED = dict(dt="bf16", act=0, m=4, n=32, k=64, x=A, ldx=64, wg=B, wu=C, ldw=64, h=D, ldh=32, gate=E, up=F, lds=32,
+             scratch=G, nbytes=1 << 20)
+BACK = dict(dt="bf16", act=0, m=4, n=32, k=64, x=A, ldx=64, wg=B, wu=C, ldw=64, gate=D, up=E, lds=32, dh=F, lddh=32,
+            dx=G, lddx=64, dwg=H, dwu=I, lddw=64, scratch=J, nbytes=1 << 20)
+QUANT = dict(dt="f16", m=4, k=64, x=A, ldx=64, q=B, ldq=64, scale=C)
+GEMM = dict(dt="f16", m=4, n=32, k=64, a=A, lda=64, sa=B, b=C, ldb=64, sb=D, c=E, ldc=32, scratch=F, nbytes=1 << 20)
+CALLS = {"gated": (gb.gbmm_gated, GATED), "back": (gb.gbmm_gated_backward, BACK),
+         "quant": (gb.gbmm_quantize_i8, QUANT), "gemm": (gb.gbmm_gemm_i8, GEMM)}
+NAMES = {"gated": "gbmm_gated", "back": "gbmm_gated_backward", "quant": "gbmm_quantize_i8", "gemm": "gbmm_gemm_i8"}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_accepts_and_names_the_kernel(name):
+    assert call(*CALLS[name], {}) == PASSES
+    assert NAMES[name] in gb.gbmm_last_error()
+
+
+REFUSED = [
+    ("gated", dict(dt=3), DTYPE), ("gated", dict(act=4), BAD), ("gated", dict(m=-1), BAD), ("gated", dict(n=-1), BAD),
+    ("gated", dict(k=-1), BAD), ("gated", dict(m=1 << 31), BAD), ("gated", dict(k=1 << 31, ldx=1 << 31, ldw=1 << 31), BAD),
+    ("gated", dict(ldx=63), BAD), ("gated", dict(ldw=63), BAD), ("gated", dict(ldh=31), BAD),
+    ("gated", dict(lds=31), BAD), ("gated", dict(gate=0), BAD), ("gated", dict(up=0), BAD), ("gated", dict(x=0), BAD),
+    ("gated", dict(wg=0), BAD), ("gated", dict(wu=0), BAD), ("gated", dict(h=0), BAD), ("gated", dict(x=A + 1), BAD),
+    ("gated", dict(wu=C + 1), BAD), ("gated", dict(h=D + 1), BAD), ("gated", dict(ldx=1 << 62), BAD),
+    ("gated", dict(h=A), OVERLAP), ("gated", dict(h=B + 4094), OVERLAP), ("gated", dict(h=E), OVERLAP),
+    ("gated", dict(gate=F), OVERLAP), ("gated", dict(gate=F + 32), OVERLAP), ("gated", dict(up=C), OVERLAP),
+    ("gated", dict(scratch=A), OVERLAP), ("gated", dict(scratch=D - 8), OVERLAP),
+    ("gated", dict(lds=64, up=E + 62), OVERLAP), ("gated", dict(lds=64, up=E + 66), OVERLAP),
+    ("back", dict(dt=9), DTYPE), ("back", dict(act=9), BAD), ("back", dict(m=-1), BAD), ("back", dict(n=1 << 31), BAD),
+    ("back", dict(ldx=63), BAD), ("back", dict(ldw=63), BAD), ("back", dict(lds=31), BAD), ("back", dict(lddh=31), BAD),
+    ("back", dict(lddx=63), BAD), ("back", dict(lddw=63), BAD), ("back", dict(dwg=0), BAD), ("back", dict(dwu=0), BAD),
+    ("back", dict(x=0), BAD), ("back", dict(wg=0), BAD), ("back", dict(wu=0), BAD), ("back", dict(gate=0), BAD),
+    ("back", dict(up=0), BAD), ("back", dict(dh=0), BAD), ("back", dict(dh=F + 1), BAD), ("back", dict(dx=G + 1), BAD),
+    ("back", dict(dx=A), OVERLAP), ("back", dict(dwg=B), OVERLAP), ("back", dict(dwg=I + 2), OVERLAP),
+    ("back", dict(dwu=J + 100), OVERLAP), ("back", dict(dx=F), OVERLAP), ("back", dict(scratch=C), OVERLAP),
+    ("back", dict(scratch=0), SCRATCH), ("back", dict(nbytes=100), SCRATCH), ("back", dict(lddw=1 << 62), BAD),
+    ("quant", dict(dt=3), DTYPE), ("quant", dict(m=-1), BAD), ("quant", dict(k=-1), BAD), ("quant", dict(ldx=63), BAD),
+    ("quant", dict(ldq=63), BAD), ("quant", dict(x=0), BAD), ("quant", dict(q=0), BAD), ("quant", dict(scale=0), BAD),
+    ("quant", dict(scale=C + 2), BAD), ("quant", dict(x=A + 1), BAD), ("quant", dict(q=A), OVERLAP),
+    ("quant", dict(scale=A), OVERLAP), ("quant", dict(scale=B + 252), OVERLAP), ("quant", dict(m=1 << 31), BAD),
+    ("gemm", dict(dt=3), DTYPE), ("gemm", dict(m=-1), BAD), ("gemm", dict(n=-1), BAD), ("gemm", dict(k=-1), BAD),
+    ("gemm", dict(k=131072, lda=131072, ldb=131072), BAD), ("gemm", dict(lda=63), BAD), ("gemm", dict(ldb=63), BAD),
+    ("gemm", dict(ldc=31), BAD), ("gemm", dict(a=0), BAD), ("gemm", dict(b=0), BAD), ("gemm", dict(c=0), BAD),
+    ("gemm", dict(c=E + 1), BAD), ("gemm", dict(sa=B + 2), BAD), ("gemm", dict(sb=D + 1), BAD),
+    ("gemm", dict(c=A), OVERLAP), ("gemm", dict(c=B), OVERLAP), ("gemm", dict(c=C + 2046), OVERLAP),
+    ("gemm", dict(c=D + 124), OVERLAP), ("gemm", dict(scratch=C), OVERLAP), ("gemm", dict(lda=1 << 62), BAD),
+]
+
+
+@pytest.mark.parametrize("name,over,status", REFUSED, ids=[f"{n}-{o}" for n, o, _ in REFUSED])
+def test_refuses(name, over, status):
+    assert call(*CALLS[name], over) == status, gb.gbmm_last_error()
+    assert gb.gbmm_last_error() != ""
+
+
+@pytest.mark.parametrize("name,over", [
+    ("gated", dict(gate=0, up=0)), ("gated", dict(gate=0, up=0, lds=0)), ("gated", dict(scratch=0, nbytes=0)),
+    ("gated", dict(k=0, x=0, wg=0, wu=0, ldx=0, ldw=0)),
+    ("gated", dict(lds=64, up=E + 64)),            # both projections in one [m, 2 n] matrix
+    ("gated", dict(lds=64, gate=E + 64, up=E)),
+    ("gated", dict(ldh=96, lds=96, h=D, gate=D + 64, up=D + 128)),
+    ("gated", dict(wu=B + 64 * 64 * 2)), ("gated", dict(ldw=128, wu=B + 128)),
+    ("back", dict(dx=0, lddx=0)), ("back", dict(dx=0, wg=0, wu=0, ldw=0)), ("back", dict(dwg=0, dwu=0, lddw=0)),
+    ("back", dict(dwg=0, dwu=0, x=0, ldx=0)), ("back", dict(lddw=128, dwu=H + 128)),
+    ("back", dict(m=0, x=0, gate=0, up=0, dh=0, scratch=0, nbytes=0)),
+    ("back", dict(n=0, wg=0, wu=0, gate=0, up=0, dh=0, scratch=0, nbytes=0)),
+    ("quant", dict(k=0, x=0, q=0, ldx=0, ldq=0)), ("quant", dict(q=B + 1, ldq=67)),
+    ("gemm", dict(sa=0, sb=0)), ("gemm", dict(a=A + 1, lda=65, b=C + 3, ldb=71)), ("gemm", dict(k=131071, lda=131071, ldb=131071)),
+    ("gemm", dict(k=0, a=0, b=0, lda=0, ldb=0)),
+])
+def test_optional_operands(name, over):
+    assert call(*CALLS[name], over) == PASSES, gb.gbmm_last_error()
+
+
+@pytest.mark.parametrize("name,over", [
+    ("gated", dict(m=0)), ("gated", dict(n=0)), ("back", dict(k=0)), ("back", dict(dx=0, dwg=0, dwu=0)),
+    ("back", dict(m=0, dwg=0, dwu=0)), ("back", dict(n=0, dx=0)), ("back", dict(m=0, n=0)), ("quant", dict(m=0)),
+    ("gemm", dict(m=0)), ("gemm", dict(n=0)),
+])
+def test_nothing_to_do_is_a_no_op(name, over):
+    assert call(*CALLS[name], over) == gb.GBMM_OK, gb.gbmm_last_error()
+
+
+def test_scratch_sizes():
+    for fn in (gb.gbmm_gated_scratch_bytes, gb.gbmm_gated_backward_scratch_bytes):
+        assert fn(5, 4, 4, 4)[0] == DTYPE
+        assert fn("bf16", -1, 4, 4)[0] == BAD
+        assert fn("bf16", 4, 1 << 31, 4)[0] == BAD
+        sizes = [fn("bf16", m, 1000, 1000) for m in (0, 1, 1000, 100000)]
+        assert all(st == gb.GBMM_OK for st, _ in sizes) and [v for _, v in sizes] == sorted(v for _, v in sizes)
+    assert gb.gbmm_gemm_i8_scratch_bytes(1, 1, gb.I8_MAX_K + 1)[0] == BAD
+    assert gb.gbmm_gemm_i8_scratch_bytes(-1, 1, 1)[0] == BAD
+    assert gb.gbmm_gemm_i8_scratch_bytes(1 << 31, 1, 1)[0] == BAD
+    for m, n, k in ((4, 32, 64), (1000, 1001, 1003), (100000, 7, 131071)):
+        st, need = gb.gbmm_gemm_i8_scratch_bytes(m, n, k)
+        assert st == gb.GBMM_OK
+        far = dict(m=m, n=n, k=k, lda=k, ldb=k, ldc=n, a=BASE, b=BASE << 1, c=BASE << 2, scratch=BASE << 3, sa=0, sb=0)
+        assert call(*CALLS["gemm"], dict(far, nbytes=need)) == PASSES
+        if need:
+            assert call(*CALLS["gemm"], dict(far, nbytes=need - 1)) == SCRATCH
+            assert call(*CALLS["gemm"], dict(far, nbytes=need, scratch=0)) == SCRATCH
+    st, need = gb.gbmm_gated_backward_scratch_bytes("bf16", 4, 32, 64)
+    assert call(*CALLS["back"], dict(nbytes=need)) == PASSES
+    assert call(*CALLS["back"], dict(nbytes=need - 1)) == SCRATCH
+
+
+@pytest.mark.parametrize("kernel", ["gbmm_gated_backward", "gbmm_gemm_tc", "gbmm_gemm_simt", "gbmm_gemv_rowdot"])
+def test_backward_asks_for_its_products_first(kernel):
+    gb.gbmm_test_inject_kernel_failure(kernel)
+    assert call(*CALLS["back"], {}) == PASSES and kernel in gb.gbmm_last_error()
+    gb.gbmm_test_inject_kernel_failure("*")

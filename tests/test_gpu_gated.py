@@ -1,0 +1,347 @@
+"""GPU parity of the gated projection and its gradients against plain 64-bit
+definitions.
+
+Tolerances, from the arithmetic (u = 2^-24; uo = half a step of the type relative to
+its value; A the sum of a product's magnitudes):
+  projections  (k + 16) u A.  A sum of k products in f32 in any order is off by k u A at
+               most; a tensor-core step adds 16 of them and may truncate (2^-22 of the
+               partial sum a step: k / 16 * 2^-22 = k u / 4); a few partial sums are added
+  h            1.2 e_g |up| + |act| e_u + 1.2 e_g e_u + 16 u |gate up|, e_g and e_u the
+               projections' bounds, 1.2 above every activation's slope (1.13 at most), 16 u
+               |gate| above what evaluating the activation in f32 costs
+  d_gate       16 u |d_h up| (the slope, below 1.2, in f32) + uo |d_gate|, rounded to the type
+  d_up         16 u |d_h gate| + uo |d_up|, rounded to the type
+  d_x, d_w     the errors of d_gate and d_up through the products' magnitudes, plus
+               (length + 16) u A, the length of the contraction (2 n for d_x, m for d_w)
+Each stored result adds uo |value| and the absolute half spacing below the type's normal range.
+"""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from gemv_moe_expert_gb300 import binding as gb  # noqa: E402
+from tests import ffn_ref  # noqa: E402
+from tests.gpu_util import DevBuf  # noqa: E402
+from tests.test_gpu_moe import TINY, U, UO, empty, fetch, near, strided  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+CODE = {name: i for i, name in enumerate(ffn_ref.ACTS)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from gemv_moe_expert_gb300 import build
+    build.build()
+    gb.load()
+    torch.cuda.init()
+
+
+def scratch_for(fn, dtype, m, n, k):
+    st, need = fn(dtype, m, n, k)
+    gb.check(st)
+    return DevBuf(max(need, 1)), need
+
+
+class Block:
+    """Operands of one block; `pad` elements between rows hold NaN, `off` elements before them."""
+
+    def __init__(self, dtype, m, n, k, seed=0, pad=0, off=0, scale=1.0):
+        rng = np.random.default_rng(seed + 31 * m + 7 * n + k)
+        self.dtype, self.m, self.n, self.k, self.pad, self.off = dtype, m, n, k, pad, off
+        self.ldk, self.ldn = max(k, 1) + pad, max(n, 1) + pad
+        w = scale / max(k, 1) ** 0.5
+        self.xb, self.xp, self.x = strided(rng.standard_normal((m, k)), self.ldk, dtype, offset=off)
+        self.gb, self.gp, self.wg = strided(w * rng.standard_normal((n, k)), self.ldk, dtype, offset=off)
+        self.ub, self.up, self.wu = strided(w * rng.standard_normal((n, k)), self.ldk, dtype, offset=off)
+        self.rng = rng
+
+    def forward(self, act, save=False, scratch=True, stream=None):
+        m, n, k = self.m, self.n, self.k
+        outs = [empty(m, self.ldn, self.dtype, self.off) for _ in range(3 if save else 1)]
+        sb, need = scratch_for(gb.gbmm_gated_scratch_bytes, self.dtype, m, n, k) if scratch else (None, 0)
+        ptr = [o[1] for o in outs] + [None] * (3 - len(outs))
+        gb.check(gb.gbmm_gated(self.dtype, CODE[act], m, n, k, self.xp, self.ldk, self.gp, self.up, self.ldk, ptr[0],
+                               self.ldn, ptr[1], ptr[2], self.ldn, sb and sb.ptr, need, stream))
+        got = [fetch(o[0], m, n, self.ldn, self.dtype, self.off) for o in outs]
+        assert sb is None or sb.guards_intact()
+        assert gb.gbmm_device_error()[0] == gb.GBMM_OK
+        return got
+
+    def check_forward(self, act, got):
+        h, g, u = ffn_ref.forward(act, self.x, self.wg, self.wu)
+        e = (self.k + 16) * U
+        eg, eu = (e * np.abs(self.x) @ np.abs(w).T for w in (self.wg, self.wu))
+        uo, tiny = UO[self.dtype], TINY[self.dtype]
+        tol = 1.2 * eg * np.abs(u) + np.abs(ffn_ref.act(act, g)) * eu + 1.2 * eg * eu + 16 * U * np.abs(g * u)
+        near(got[0], h, tol * (1 + uo) + uo * np.abs(h) + tiny, "h")
+        if len(got) > 1:
+            near(got[1], g, eg * (1 + uo) + uo * np.abs(g) + tiny, "gate")
+            near(got[2], u, eu * (1 + uo) + uo * np.abs(u) + tiny, "up")
+
+    def backward(self, act, d_x=True, d_w=True):
+        m, n, k, dt = self.m, self.n, self.k, self.dtype
+        self.saved = [strided(self.rng.standard_normal((m, n)), self.ldn, dt, offset=self.off) for _ in range(3)]
+        (_, gp, self.g), (_, up, self.u), (_, hp, self.d_h) = self.saved
+        dx = empty(m, self.ldk, dt, self.off) if d_x else (None, None)
+        dg, du = (empty(n, self.ldk, dt, self.off) if d_w else (None, None) for _ in range(2))
+        sb, need = scratch_for(gb.gbmm_gated_backward_scratch_bytes, dt, m, n, k)
+        gb.check(gb.gbmm_gated_backward(dt, CODE[act], m, n, k, self.xp if d_w else None, self.ldk,
+                                        self.gp if d_x else None, self.up if d_x else None, self.ldk, gp, up, self.ldn,
+                                        hp, self.ldn, dx[1], self.ldk, dg[1], du[1], self.ldk, sb.ptr, need))
+        got = [o[0] and fetch(o[0], rows, k, self.ldk, dt, self.off) for o, rows in ((dx, m), (dg, n), (du, n))]
+        assert sb.guards_intact() and gb.gbmm_device_error()[0] == gb.GBMM_OK
+        return got
+
+    def check_backward(self, act, got):
+        dt = self.dtype
+        uo, tiny = UO[dt], TINY[dt]
+        dx, dwg, dwu, dg, du = ffn_ref.backward(act, self.x, self.wg, self.wu, self.g, self.u, self.d_h)
+        eg = 16 * U * np.abs(self.d_h * self.u) * (1 + uo) + uo * np.abs(dg) + tiny
+        eu = 16 * U * np.abs(self.d_h * self.g) * (1 + uo) + uo * np.abs(du) + tiny
+        ag, au = np.abs(dg) + eg, np.abs(du) + eu  # what is multiplied is at most this
+        wg, wu, x = np.abs(self.wg), np.abs(self.wu), np.abs(self.x)
+        if got[0] is not None:
+            tol = eg @ wg + eu @ wu + (2 * self.n + 16) * U * (ag @ wg + au @ wu)
+            near(got[0], dx, tol * (1 + uo) + uo * np.abs(dx) + tiny, "d_x")
+        for name, out, ref, e, a in (("d_w_gate", got[1], dwg, eg, ag), ("d_w_up", got[2], dwu, eu, au)):
+            if out is not None:
+                tol = e.T @ x + (self.m + 16) * U * (a.T @ x)
+                near(out, ref, tol * (1 + uo) + uo * np.abs(ref) + tiny, name)
+
+
+SIZES = [(1, 1, 1), (1, 5, 8), (1, 64, 512), (1, 131, 4097), (2, 33, 130), (3, 128, 1024), (5, 7, 200), (7, 257, 264),
+         (8, 40, 40), (9, 65, 33), (15, 300, 512), (16, 128, 64), (17, 129, 72), (33, 200, 640), (64, 256, 128),
+         (65, 130, 1000), (100, 64, 2056), (128, 300, 256), (129, 127, 65), (147, 513, 520), (260, 264, 192)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_forward_sizes(dtype, m, n, k):
+    act = ffn_ref.ACTS[(m + n + k) % 4]
+    b = Block(dtype, m, n, k)
+    b.check_forward(act, b.forward(act, save=(m + n) % 2 == 0))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m", [1, 12, 80, 300])
+@pytest.mark.parametrize("pad,off", [(0, 1), (3, 0), (8, 0), (8, 8), (4, 4)])
+def test_forward_layouts(dtype, m, pad, off):
+    b = Block(dtype, m, 136, 328, pad=pad, off=off)
+    b.check_forward("silu", b.forward("silu", save=True))
+
+
+@pytest.mark.parametrize("m", [12, 300])
+def test_forward_rows_that_start_anywhere_without_scratch(m):
+    b = Block("bf16", m, 70, 130, pad=1, off=1)
+    b.check_forward("gelu", b.forward("gelu", save=True, scratch=False))
+
+
+@pytest.mark.parametrize("act", ffn_ref.ACTS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [3, 40, 300])
+def test_forward_activations_over_their_range(act, dtype, m):
+    b = Block(dtype, m, 72, 64, scale=12.0)  # gates of both signs up to about 50
+    b.check_forward(act, b.forward(act, save=True))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(512, 2000, 576), (1000, 1300, 1032), (700, 5504, 64), (2049, 264, 520)])
+def test_forward_many_tiles(dtype, m, n, k):
+    b = Block(dtype, m, n, k)
+    b.check_forward("gelu_tanh", b.forward("gelu_tanh", save=True))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("m", [1, 20, 300])
+def test_forward_of_nothing_writes_zeros(dtype, m):
+    b = Block(dtype, m, 40, 0)
+    for out in b.forward("silu", save=True):
+        assert (out == 0).all()
+
+
+@pytest.mark.parametrize("m", [1, 30, 200])
+def test_forward_carries_nan_and_infinity(m):
+    """A NaN in one row of x reaches that row of h and no other; so does an infinite gate."""
+    n, k = 40, 128
+    x, w = torch.ones(m, k, device="cuda").bfloat16(), torch.full((n, k), 0.125, device="cuda").bfloat16()
+    x[m // 2, 5] = float("nan")
+    h = torch.empty(m, n, device="cuda", dtype=torch.bfloat16)
+    for act in range(4):
+        gb.check(gb.gbmm_gated("bf16", act, m, n, k, x, k, w, w, k, h, n, None, None, 0, None, 0))
+        bad = torch.isnan(h).all(dim=1)
+        assert bad[m // 2] and bad.sum() == 1 and not torch.isnan(h[~bad]).any()
+    x.fill_(1.0)
+    x[m // 2, 5] = float("inf")
+    gb.check(gb.gbmm_gated("bf16", 0, m, n, k, x, k, w, w, k, h, n, None, None, 0, None, 0))
+    assert torch.isinf(h[m // 2]).all() and torch.isinf(h).sum() == n
+
+
+@pytest.mark.parametrize("m", [6, 40, 300])
+def test_projections_side_by_side(m):
+    """w_gate and w_up as the halves of one [2 n, k] matrix, gate and up as those of one [m, 2 n]."""
+    n, k = 264, 320
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(m, k, generator=g, device="cuda").half()
+    w = (torch.randn(2 * n, k, generator=g, device="cuda") / k ** 0.5).half()
+    both, h = torch.empty(m, 2 * n, device="cuda").half(), torch.empty(m, n, device="cuda").half()
+    apart, h2 = [torch.empty(m, n, device="cuda").half() for _ in range(2)], torch.empty_like(h)
+    gb.check(gb.gbmm_gated("f16", 0, m, n, k, x, k, w, w[n:], k, h, n, both, both[:, n:], 2 * n, None, 0))
+    gb.check(gb.gbmm_gated("f16", 0, m, n, k, x, k, w, w[n:].clone(), k, h2, n, *apart, n, None, 0))
+    assert torch.equal(h, h2) and torch.equal(both, torch.cat(apart, dim=1))
+
+
+BACK_SIZES = [(1, 1, 1), (1, 64, 128), (3, 5, 7), (7, 40, 264), (16, 64, 64), (33, 129, 65), (64, 128, 256),
+              (100, 72, 520), (147, 257, 129), (128, 512, 1000), (300, 264, 328)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", BACK_SIZES)
+def test_backward_sizes(dtype, m, n, k):
+    act = ffn_ref.ACTS[(m + n + k) % 4]
+    b = Block(dtype, m, n, k)
+    b.check_backward(act, b.backward(act))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("pad,off", [(0, 1), (3, 0), (8, 0), (8, 8), (4, 4)])
+def test_backward_layouts(dtype, pad, off):
+    b = Block(dtype, 90, 136, 200, pad=pad, off=off)
+    b.check_backward("silu", b.backward("silu"))
+
+
+@pytest.mark.parametrize("act", ffn_ref.ACTS)
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_backward_activations(act, dtype):
+    b = Block(dtype, 40, 48, 56)
+    b.check_backward(act, b.backward(act))
+
+
+@pytest.mark.parametrize("d_x,d_w", [(True, False), (False, True)])
+def test_backward_of_one_side(d_x, d_w):
+    b = Block("bf16", 70, 96, 104)
+    got = b.backward("gelu", d_x, d_w)
+    assert (got[0] is None) != d_x and (got[1] is None) != d_w
+    b.check_backward("gelu", got)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(1100, 1000, 840), (512, 2056, 1032), (2500, 520, 264)])
+def test_backward_many_tiles(dtype, m, n, k):
+    b = Block(dtype, m, n, k)
+    b.check_backward("silu", b.backward("silu"))
+
+
+def test_backward_of_nothing_writes_zeros():
+    t = torch.full((3, 8, 16), 7.0, device="cuda")
+    gb.check(gb.gbmm_gated_backward("f32", 0, 0, 8, 16, None, 16, t, t, 16, None, None, 8, None, 8, None, 16, t[0],
+                                    t[1], 16, None, 0))
+    assert (t[:2] == 0).all() and (t[2] == 7).all()
+    t.fill_(7.0)
+    gb.check(gb.gbmm_gated_backward("f32", 0, 8, 0, 16, None, 16, None, None, 16, None, None, 0, None, 0, t[0], 16,
+                                    None, None, 16, None, 0))
+    assert (t[0] == 0).all() and (t[1:] == 7).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_gradient_against_differences(act):
+    """<gradient, v> against central differences of the definition in 64 bits along v, through forward and
+    backward calls in f32.  The differences are off by 1e-10 of the sum of magnitudes at a step of 1e-5 (its square
+    times a third derivative of order 1, and 2^-53 / 1e-5); the f32 gradients and saved projections by less
+    than (2 n + m + k + 100) 2^-24 of the magnitudes."""
+    m, n, k = 12, 24, 40
+    b = Block("f32", m, n, k, seed=5)
+    _, gate, up = b.forward(act, save=True)
+    d_h = b.rng.standard_normal((m, n)).astype(np.float32).astype(np.float64)
+
+    def up_(v):
+        return torch.from_numpy(np.ascontiguousarray(v, np.float32)).cuda()
+    x, wg, wu, g, u, dh = (up_(v) for v in (b.x, b.wg, b.wu, gate, up, d_h))
+    out = [torch.empty_like(v) for v in (x, wg, wu)]
+    st, need = gb.gbmm_gated_backward_scratch_bytes("f32", m, n, k)
+    scratch = torch.empty(need, dtype=torch.uint8, device="cuda")
+    gb.check(gb.gbmm_gated_backward("f32", CODE[act], m, n, k, x, k, wg, wu, k, g, u, n, dh, n, out[0], k, out[1],
+                                    out[2], k, scratch, need))
+    torch.cuda.synchronize()
+    grads, at, eps = [o.double().cpu().numpy() for o in out], (b.x, b.wg, b.wu), 1e-5
+    for i in range(3):
+        v = b.rng.standard_normal(at[i].shape)
+        far = [(d_h * ffn_ref.forward(act, *[a + (s * eps * v if j == i else 0) for j, a in enumerate(at)])[0]).sum()
+               for s in (1, -1)]
+        got, ref = (grads[i] * v).sum(), (far[0] - far[1]) / (2 * eps)
+        # magnitudes of what the gradient's entry sums
+        mag = np.abs(v) * (np.abs(d_h * up) @ np.abs(b.wg) + np.abs(d_h * gate) @ np.abs(b.wu)) if i == 0 else \
+            np.abs(v) * (1.2 * np.abs(d_h * (up if i == 1 else gate)).T @ np.abs(b.x))
+        assert abs(got - ref) <= (2 * n + m + k + 100) * U * 1.2 * mag.sum() + 1e-9 * mag.sum(), (i, got, ref)
+
+
+def make(dtype, m, n, k, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    dt = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dt)  # noqa: E731
+    t = {"x": new(m, k), "wg": new(n, k) / k ** 0.5, "wu": new(n, k) / k ** 0.5, "dh": new(m, n)}
+    t |= {name: torch.zeros(m, n, dtype=dt, device="cuda") for name in ("h", "gate", "up")}
+    t |= {"dx": torch.zeros_like(t["x"]), "dwg": torch.zeros_like(t["wg"]), "dwu": torch.zeros_like(t["wu"])}
+    t["need"] = max(gb.gbmm_gated_backward_scratch_bytes(dtype, m, n, k)[1], gb.gbmm_gated_scratch_bytes(dtype, m, n, k)[1])
+    t["scratch"] = torch.empty(t["need"] + 1, dtype=torch.uint8, device="cuda")
+    return t
+
+
+def step(dtype, m, n, k, t, stream=None):
+    """Forward and backward as a training step makes them, one workspace for both."""
+    gb.check(gb.gbmm_gated(dtype, 0, m, n, k, t["x"], k, t["wg"], t["wu"], k, t["h"], n, t["gate"], t["up"], n,
+                           t["scratch"], t["need"], stream))
+    gb.check(gb.gbmm_gated_backward(dtype, 0, m, n, k, t["x"], k, t["wg"], t["wu"], k, t["gate"], t["up"], n, t["dh"],
+                                    n, t["dx"], k, t["dwg"], t["dwu"], k, t["scratch"], t["need"], stream))
+    return [t[name].clone() for name in ("h", "gate", "up", "dx", "dwg", "dwu")]
+
+
+STEPS = [("f32", 20, 72, 136), ("f16", 12, 264, 520), ("bf16", 100, 200, 320), ("bf16", 600, 1032, 520),
+         ("f16", 130, 77, 33)]
+
+
+@pytest.mark.parametrize("dtype,m,n,k", STEPS)
+def test_steps_do_not_change_from_call_to_call(dtype, m, n, k):
+    t = make(dtype, m, n, k, 3)
+    first = step(dtype, m, n, k, t)
+    for _ in range(3):
+        t["scratch"].fill_(255)
+        assert all(torch.equal(a, b) for a, b in zip(first, step(dtype, m, n, k, t)))
+
+
+@pytest.mark.parametrize("dtype,m,n,k", STEPS)
+def test_steps_replay_from_a_graph(dtype, m, n, k):
+    t, other = make(dtype, m, n, k, 4), make(dtype, m, n, k, 5)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(dtype, m, n, k, t)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        outs = step(dtype, m, n, k, t)
+    want = step(dtype, m, n, k, other)
+    for name in ("x", "wg", "wu", "dh"):
+        t[name].copy_(other[name])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, outs))
+
+
+def test_two_streams_at_once():
+    cases = [("bf16", 600, 1032, 520), ("f16", 12, 264, 520)]
+    sets = [make(*c, seed) for seed, c in enumerate(cases)]
+    want = [step(*c, t) for c, t in zip(cases, sets)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(4):
+        got = []
+        for c, t, s in zip(cases, sets, streams):
+            with torch.cuda.stream(s):
+                got.append(step(*c, t, s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g))
