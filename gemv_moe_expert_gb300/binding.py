@@ -161,10 +161,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
                  [i32, u32, i64, i64, u32, vp, i64, vp, i32, vp, vp, i64, vp, i64, vp]),
                 ("gbmm_matmul_id_q4",
                  [i32, u32, i64, i64, u32, u32, u32, u32, vp, i64, i64, vp, i32, vp, vp, vp, vp, vp]),
-                ("gbmm_gated_scratch_bytes", [i32, i64, i64, i64, ctypes.POINTER(u64)]),
+                ("gbmm_gated_scratch_bytes", [i32, i64, i64, i64, i32, ctypes.POINTER(u64)]),
                 ("gbmm_gated",
                  [i32, u32, i64, i64, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, u64, vp]),
-                ("gbmm_gated_backward_scratch_bytes", [i32, i64, i64, i64, ctypes.POINTER(u64)]),
+                ("gbmm_gated_backward_scratch_bytes", [i32, i64, i64, i64, i32, ctypes.POINTER(u64)]),
                 ("gbmm_gated_backward",
                  [i32, u32, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, u64,
                   vp]),
@@ -352,10 +352,10 @@ def gbmm_matmul_id_q4(dtype, m, n, k, top_k, n_experts, input_layout, group, q, 
                                     _stream(stream))
 
 
-def gbmm_gated_scratch_bytes(dtype, m: int, n: int, k: int):
+def gbmm_gated_scratch_bytes(dtype, m: int, n: int, k: int, aligned: bool):
     """Returns (status, bytes)."""
     need = ctypes.c_uint64(0)
-    st = load().gbmm_gated_scratch_bytes(_dt(dtype), m, n, k, ctypes.byref(need))
+    st = load().gbmm_gated_scratch_bytes(_dt(dtype), m, n, k, int(bool(aligned)), ctypes.byref(need))
     return st, need.value
 
 
@@ -365,10 +365,10 @@ def gbmm_gated(dtype, activation, m, n, k, x, ldx, w_gate, w_up, ldw, h, ldh, ga
                              ldh, _ptr(gate), _ptr(up), ld_saved, _ptr(scratch), scratch_bytes, _stream(stream))
 
 
-def gbmm_gated_backward_scratch_bytes(dtype, m: int, n: int, k: int):
+def gbmm_gated_backward_scratch_bytes(dtype, m: int, n: int, k: int, aligned: bool):
     """Returns (status, bytes)."""
     need = ctypes.c_uint64(0)
-    st = load().gbmm_gated_backward_scratch_bytes(_dt(dtype), m, n, k, ctypes.byref(need))
+    st = load().gbmm_gated_backward_scratch_bytes(_dt(dtype), m, n, k, int(bool(aligned)), ctypes.byref(need))
     return st, need.value
 
 

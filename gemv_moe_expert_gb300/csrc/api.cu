@@ -512,6 +512,10 @@ int record_error(int status, const char *message) {
 }
 bool resolve_kernel(const char *name) { return resolve(name); }
 gbmm_status finish_launch(cudaError_t e, const char *name, cudaStream_t s) { return after_launch(e, name, s); }
+bool encode_matrix16(CUtensorMap *map, int dt, const void *base, int64_t inner, int64_t outer, int64_t ld,
+                     uint32_t box_outer) {
+    return encode_operand(map, dt, base, inner, outer, 1, ld, 0, true, box_outer);
+}
 }  // namespace gbmm
 
 extern "C" {

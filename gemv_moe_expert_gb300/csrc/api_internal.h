@@ -3,6 +3,7 @@
 // that every kernel is asked through, and the launch accounting.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/gbmm.h"
@@ -15,5 +16,10 @@ int record_error(int status, const char *message);
 bool resolve_kernel(const char *name);
 // status of a launch that returned `e`; counts it, and synchronises under GBMM_DEBUG_SYNC=1
 gbmm_status finish_launch(cudaError_t e, const char *name, cudaStream_t s);
+
+// Tensor map of a 16-bit matrix [outer][inner], rows ld elements apart, boxes of box_outer x 64, 128-byte
+// swizzle.  False where TMA cannot read it (16-byte aligned base and rows).
+bool encode_matrix16(CUtensorMap *map, int dt, const void *base, int64_t inner, int64_t outer, int64_t ld,
+                     uint32_t box_outer);
 
 }  // namespace gbmm

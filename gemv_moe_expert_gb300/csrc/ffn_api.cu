@@ -33,6 +33,50 @@ Operand matrix(const char *label, const void *p, uint64_t bytes, int64_t cols, i
     return {label, p, bytes, size, output, static_cast<uint64_t>(cols) * size, static_cast<uint64_t>(ld) * size};
 }
 
+bool rows16(const void *p, int64_t ld_bytes) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld_bytes % 16 == 0;
+}
+int32_t rows32(const void *p, int64_t ld_bytes) {
+    return reinterpret_cast<uintptr_t>(p) % 32 == 0 && ld_bytes % 32 == 0;
+}
+
+// Few rows run as dot products, a warp for each column or two; more run as tiles.
+constexpr int64_t kDotRows = 8;
+
+// A 16-bit matrix as TMA reads it: in place, or laid out again in a part of the scratch.
+struct Laid {
+    const void *p;
+    int64_t ld;
+    uint64_t at;
+    bool again;
+};
+Laid lay(const void *p, int64_t rows, int64_t cols, int64_t ld, Parts *parts) {
+    if (rows16(p, ld * 2)) return {p, ld, 0, false};
+    const int64_t to = round_up(cols, 8);
+    return {p, to, parts->add(rows, to, 2), true};
+}
+// launches what lay() put off; the matrix is read from its new place then
+gbmm_status lay_again(const char *fn, Laid *l, int64_t rows, int64_t cols, int64_t ld, void *scratch, cudaStream_t s) {
+    if (!l->again) return GBMM_OK;
+    const RepackParams r{l->p, Parts::base(scratch) + l->at, rows, cols, ld, l->ld};
+    l->p = r.dst;
+    return finish_launch(launch_repack16(r, s), fn, s);
+}
+
+// what the tensor-core products share
+bool pair_params(PairTcParams *p, void *c, int64_t ldc, int size, int64_t m, int64_t n, int64_t k) {
+    *p = PairTcParams{};
+    p->c = c;
+    p->ldc = ldc;
+    p->m = static_cast<int32_t>(m);
+    p->n = static_cast<int32_t>(n);
+    p->k = static_cast<int32_t>(k);
+    p->c_vec = rows32(c, ldc * size);
+    p->err = device_error_word();
+    p->wait_limit_ns = kWaitLimitNs;
+    return p->err != nullptr;
+}
+
 gbmm_status check_gated(const char *fn, gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n, int64_t k) {
     if (!known_dtype(dt))
         return fail(GBMM_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d is not f32, f16 or bf16", fn, (int)dt);
@@ -47,13 +91,19 @@ gbmm_status check_gated(const char *fn, gbmm_dtype dt, uint32_t activation, int6
 
 extern "C" {
 
-gbmm_status gbmm_gated_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, uint64_t *bytes) {
+gbmm_status gbmm_gated_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, int aligned, uint64_t *bytes) {
     record_error(GBMM_OK, "");
     const char *fn = "gbmm_gated_scratch_bytes";
     const gbmm_status st = check_gated(fn, dt, 0, m, n, k);
     if (st != GBMM_OK) return st;
     if (bytes == nullptr) return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: bytes is null", fn);
     *bytes = 0;
+    if (dt == GBMM_F32 || aligned || m <= kDotRows || n == 0 || k == 0) return GBMM_OK;
+    Parts parts;
+    parts.add(m, round_up(k, 8), 2);
+    parts.add(n, round_up(k, 8), 2);
+    parts.add(n, round_up(k, 8), 2);
+    *bytes = parts.bytes;
     return GBMM_OK;
 }
 
@@ -80,7 +130,40 @@ gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n,
                            {"scratch", scratch, scratch ? scratch_bytes : 0, 1, true}};
     st = check_operands(fn, ops, 7);
     if (st != GBMM_OK) return st;
+    const bool tiles16 = dt != GBMM_F32 && m > kDotRows && k > 0;
+    Parts parts;
+    Laid lx{}, lg{}, lu{};
+    if (tiles16) {
+        lx = lay(x, m, k, ldx, &parts);
+        lg = lay(w_gate, n, k, ldw, &parts);
+        lu = lay(w_up, n, k, ldw, &parts);
+    }
+    const bool again = lx.again || lg.again || lu.again;
+    if (again && scratch != nullptr && scratch_bytes < parts.bytes)
+        return fail(GBMM_ERR_SCRATCH, "%s: needs %llu bytes of scratch for this layout (got %llu)", fn,
+                    (unsigned long long)parts.bytes, (unsigned long long)scratch_bytes);
     if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
+    cudaStream_t s = cuda_stream(stream);
+    if (tiles16 && (!again || scratch != nullptr)) {
+        st = lay_again(fn, &lx, m, k, ldx, scratch, s);
+        if (st == GBMM_OK) st = lay_again(fn, &lg, n, k, ldw, scratch, s);
+        if (st == GBMM_OK) st = lay_again(fn, &lu, n, k, ldw, scratch, s);
+        if (st != GBMM_OK) return st;
+        PairTcMaps maps;
+        PairTcParams q;
+        const uint32_t rows = static_cast<uint32_t>(pair_tc_rows());
+        if (!pair_params(&q, h, ldh, 2, m, n, k) || !encode_matrix16(&maps.a[0], dt, lx.p, k, m, lx.ld, rows) ||
+            !encode_matrix16(&maps.b[0], dt, lg.p, k, n, lg.ld, rows) ||
+            !encode_matrix16(&maps.b[1], dt, lu.p, k, n, lu.ld, rows))
+            return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
+        maps.a[1] = maps.a[0];
+        q.saved[0] = gate;
+        q.saved[1] = up;
+        q.ld_saved = ld_saved;
+        q.saved_vec = rows32(gate, ld_saved * 2) && rows32(up, ld_saved * 2);
+        q.act = static_cast<int32_t>(activation);
+        return finish_launch(launch_gated_tc(dt, maps, q, device_sm_count(), s), fn, s);
+    }
     GatedParams p{};
     p.x = x;
     p.w[0] = w_gate;
@@ -96,11 +179,11 @@ gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n,
     p.ldh = ldh;
     p.ld_saved = ld_saved;
     p.act = static_cast<int32_t>(activation);
-    cudaStream_t s = cuda_stream(stream);
-    return finish_launch(m <= 8 ? launch_gated_rowdot(dt, p, s) : launch_gated_simt(dt, p, s), fn, s);
+    return finish_launch(m <= kDotRows ? launch_gated_rowdot(dt, p, s) : launch_gated_simt(dt, p, s), fn, s);
 }
 
-gbmm_status gbmm_gated_backward_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, uint64_t *bytes) {
+gbmm_status gbmm_gated_backward_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, int aligned,
+                                              uint64_t *bytes) {
     record_error(GBMM_OK, "");
     const char *fn = "gbmm_gated_backward_scratch_bytes";
     const gbmm_status st = check_gated(fn, dt, 0, m, n, k);
@@ -108,9 +191,13 @@ gbmm_status gbmm_gated_backward_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t 
     if (bytes == nullptr) return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: bytes is null", fn);
     const int size = dtype_size(dt);
     Parts parts;
-    const int64_t ldd = round_up(n, 16 / size);
-    parts.add(m, ldd, size);
-    parts.add(m, ldd, size);
+    parts.add(m, round_up(n, 16 / size), size);
+    parts.add(m, round_up(n, 16 / size), size);
+    if (dt != GBMM_F32 && !aligned) {
+        parts.add(m, round_up(k, 8), 2);
+        parts.add(n, round_up(k, 8), 2);
+        parts.add(n, round_up(k, 8), 2);
+    }
     *bytes = parts.bytes;
     return GBMM_OK;
 }
@@ -141,9 +228,17 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     const bool empty = m == 0 || n == 0;  // what is left to do is writing zeros
     if (empty || !need_w) xb = 0;
     if (empty || !need_x) wb = 0;
-    uint64_t need;
-    st = gbmm_gated_backward_scratch_bytes(dt, m, n, k, &need);
-    if (st != GBMM_OK) return st;
+    Parts parts;
+    const int64_t ldd = round_up(n, 16 / static_cast<int>(size));
+    const uint64_t d_at[2] = {parts.add(m, ldd, static_cast<int>(size)), parts.add(m, ldd, static_cast<int>(size))};
+    Laid lx{x, ldx, 0, false}, lw[2] = {{w_gate, ldw, 0, false}, {w_up, ldw, 0, false}};
+    if (dt != GBMM_F32 && !empty) {
+        if (need_w) lx = lay(x, m, k, ldx, &parts);
+        if (need_x) {
+            lw[0] = lay(w_gate, n, k, ldw, &parts);
+            lw[1] = lay(w_up, n, k, ldw, &parts);
+        }
+    }
     const Operand ops[] = {matrix("x", x, xb, k, ldx, size, false),
                            matrix("w_gate", w_gate, wb, k, ldw, size, false),
                            matrix("w_up", w_up, wb, k, ldw, size, false),
@@ -156,8 +251,8 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
                            {"scratch", scratch, scratch ? scratch_bytes : 0, 1, true}};
     st = check_operands(fn, ops, 10);
     if (st != GBMM_OK) return st;
-    if (!empty && (scratch == nullptr || scratch_bytes < need))
-        return fail(GBMM_ERR_SCRATCH, "%s: needs %llu bytes of scratch (got %llu)", fn, (unsigned long long)need,
+    if (!empty && (scratch == nullptr || scratch_bytes < parts.bytes))
+        return fail(GBMM_ERR_SCRATCH, "%s: needs %llu bytes of scratch (got %llu)", fn, (unsigned long long)parts.bytes,
                     (unsigned long long)(scratch ? scratch_bytes : 0));
     // the products' kernels are asked for before the first launch, so that nothing runs where one is missing
     static const char *const kProducts[] = {"gbmm_fill_zero",     "gbmm_gemm_tc", "gbmm_gemm_simt", "gbmm_gemv_rowdot",
@@ -175,31 +270,40 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
         }
         return st;
     }
-    Parts parts;
-    const int64_t ldd = round_up(n, 16 / size);
+    char *const base = Parts::base(scratch);
     GatedGradParams g{};
     g.gate = gate;
     g.up = up;
     g.d_h = d_h;
-    g.d[0] = Parts::base(scratch) + parts.add(m, ldd, size);
-    g.d[1] = Parts::base(scratch) + parts.add(m, ldd, size);
+    g.d[0] = base + d_at[0];
+    g.d[1] = base + d_at[1];
     g.m = m;
     g.n = n;
     g.ld_saved = ld_saved;
     g.ld_dh = ld_dh;
     g.ldd = ldd;
     g.act = static_cast<int32_t>(activation);
-    st = finish_launch(launch_gated_grad(dt, g, s), fn, s);
+    st = lay_again(fn, &lx, m, k, ldx, scratch, s);
+    for (int i = 0; i < 2 && st == GBMM_OK; ++i) st = lay_again(fn, &lw[i], n, k, ldw, scratch, s);
+    if (st == GBMM_OK) st = finish_launch(launch_gated_grad(dt, g, s), fn, s);
     if (st != GBMM_OK) return st;
-    if (need_x) {
-        SumGemmParams q{{g.d[0], g.d[1]}, {w_gate, w_up}, d_x, m, k, n, ldd, ldw, ld_dx};
+    if (need_x && dt != GBMM_F32) {
+        PairTcMaps maps;
+        PairTcParams q;
+        bool ok = pair_params(&q, d_x, ld_dx, 2, m, k, n);
+        for (int i = 0; i < 2 && ok; ++i)
+            ok = encode_matrix16(&maps.a[i], dt, g.d[i], n, m, ldd, static_cast<uint32_t>(pair_tc_rows())) &&
+                 encode_matrix16(&maps.b[i], dt, lw[i].p, k, n, lw[i].ld, static_cast<uint32_t>(pair_tc_block_k()));
+        if (!ok) return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
+        st = finish_launch(launch_sum_gemm_tc(dt, maps, q, device_sm_count(), s), fn, s);
+    } else if (need_x) {
+        const SumGemmParams q{{g.d[0], g.d[1]}, {w_gate, w_up}, d_x, m, k, n, ldd, ldw, ld_dx};
         st = finish_launch(launch_sum_gemm_simt(dt, q, s), fn, s);
-        if (st != GBMM_OK) return st;
     }
     if (need_w) {
         void *const dw[2] = {d_w_gate, d_w_up};
         for (int i = 0; i < 2 && st == GBMM_OK; ++i)
-            st = gbmm_gemm(dt, 1, n, k, m, 1, 0, g.d[i], 0, ldd, 0, x, 0, ldx, 0, dw[i], 0, ld_dw, 0, stream);
+            st = gbmm_gemm(dt, 1, n, k, m, 1, 0, g.d[i], 0, ldd, 0, lx.p, 0, lx.ld, 0, dw[i], 0, ld_dw, 0, stream);
     }
     return st;
 }
@@ -236,6 +340,11 @@ gbmm_status gbmm_gemm_i8_scratch_bytes(int64_t m, int64_t n, int64_t k, uint64_t
         return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: m and n must lie in [0, 2^31), k in [0, %d]", fn, GBMM_I8_MAX_K);
     if (bytes == nullptr) return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: bytes is null", fn);
     *bytes = 0;
+    if (m <= kDotRows || n == 0 || k == 0) return GBMM_OK;
+    Parts parts;
+    parts.add(m, round_up(k, 8), 2);
+    parts.add(n, round_up(k, 8), 2);
+    *bytes = parts.bytes;
     return GBMM_OK;
 }
 
@@ -270,8 +379,30 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
         return fail(GBMM_ERR_SCRATCH, "%s: needs %llu bytes of scratch (got %llu)", fn, (unsigned long long)need,
                     (unsigned long long)(scratch ? scratch_bytes : 0));
     if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
-    const GemmI8Params p{a, b, scale_a, scale_b, c, m, n, k, lda, ldb, ldc};
-    return finish_launch(launch_gemm_i8_dot(dt, p, cuda_stream(stream)), fn, cuda_stream(stream));
+    cudaStream_t s = cuda_stream(stream);
+    if (m <= kDotRows || k == 0) {
+        const GemmI8Params p{a, b, scale_a, scale_b, c, m, n, k, lda, ldb, ldc};
+        return finish_launch(launch_gemm_i8_dot(dt, p, s), fn, s);
+    }
+    Parts parts;
+    const int64_t ld = round_up(k, 8);
+    char *const base = Parts::base(scratch);
+    const RepackParams ra{a, base + parts.add(m, ld, 2), m, k, lda, ld}, rb{b, base + parts.add(n, ld, 2), n, k, ldb, ld};
+    PairTcMaps maps;
+    PairTcParams q;
+    const uint32_t rows = static_cast<uint32_t>(pair_tc_rows());
+    if (!pair_params(&q, c, ldc, static_cast<int>(size), m, n, k) ||
+        !encode_matrix16(&maps.a[0], GBMM_F16, ra.dst, k, m, ld, rows) ||
+        !encode_matrix16(&maps.b[0], GBMM_F16, rb.dst, k, n, ld, rows))
+        return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
+    maps.a[1] = maps.a[0];
+    maps.b[1] = maps.b[0];
+    q.scale_a = scale_a;
+    q.scale_b = scale_b;
+    st = finish_launch(launch_codes_to_f16(ra, s), fn, s);
+    if (st == GBMM_OK) st = finish_launch(launch_codes_to_f16(rb, s), fn, s);
+    if (st != GBMM_OK) return st;
+    return finish_launch(launch_gemm_i8_tc(dt, maps, q, device_sm_count(), s), fn, s);
 }
 
 }  // extern "C"

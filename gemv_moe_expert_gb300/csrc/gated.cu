@@ -393,6 +393,7 @@ cudaError_t sum_gemm_t(const SumGemmParams &p, cudaStream_t s) {
 template <typename T>
 __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p, int vec) {
     constexpr int kN = Elem<T>::kVec;
+    grid_dep_begin();
     const int64_t pieces = (p.n + kN - 1) / kN, total = pieces * p.m;
     for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < total;
          at += static_cast<int64_t>(gridDim.x) * 256) {
@@ -420,8 +421,8 @@ cudaError_t gated_grad_t(const GatedGradParams &p, cudaStream_t s) {
                     rows16(p.d_h, p.ld_dh, sizeof(T));
     const int64_t blocks = (p.m * ((p.n + Elem<T>::kVec - 1) / Elem<T>::kVec) + 255) / 256;
     const int64_t most = 16LL * device_sm_count();
-    gated_grad_kernel<T><<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, s>>>(p, vec);
-    return cudaGetLastError();
+    return launch_early(gated_grad_kernel<T>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s,
+                        p, vec);
 }
 
 // ---------------------------------------------------------------------------
@@ -438,6 +439,7 @@ __device__ __forceinline__ uint16_t as_bits(int8_t v) { return __half_as_ushort(
 
 template <typename S>
 __global__ void __launch_bounds__(256) repack_kernel(const RepackParams p) {
+    grid_dep_begin();
     const int64_t pieces = p.ldd / 8, total = pieces * p.rows;
     for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < total;
          at += static_cast<int64_t>(gridDim.x) * 256) {
@@ -454,8 +456,7 @@ template <typename S>
 cudaError_t repack_t(const RepackParams &p, cudaStream_t s) {
     const int64_t blocks = (p.rows * (p.ldd / 8) + 255) / 256, most = 16LL * device_sm_count();
     if (blocks == 0) return cudaSuccess;
-    repack_kernel<S><<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(repack_kernel<S>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, p);
 }
 
 }  // namespace

@@ -26,6 +26,8 @@ enum KernelId : uint32_t {
     kKidGemvTc = 5,
     kKidDirectTc = 6,
     kKidGemvColdotStream = 7,
+    kKidPairTc = 8,
+    kKidFewTc = 9,
 };
 
 // default limit of a bounded device wait (1 s)
@@ -216,6 +218,23 @@ struct GemmI8Params {
     int64_t m, n, k, lda, ldb, ldc;
 };
 
+// Products of the feed-forward block on CTA pairs (pair_tc.cu): what the tensor maps do not say.
+struct PairTcParams {
+    void *c;
+    void *saved[2];                  // gated: both projections, or null
+    const float *scale_a, *scale_b;  // codes; null: 1
+    int64_t ldc, ld_saved;
+    int32_t m, n, k;                 // k: of one source
+    int32_t c_vec, saved_vec;        // rows allow 32-byte stores
+    int32_t act;
+    int32_t tiles_m, tiles_n, num_tiles;  // set by the launcher
+    uint32_t *err;
+    uint64_t wait_limit_ns;
+};
+struct PairTcMaps {
+    CUtensorMap a[2], b[2];
+};
+
 // ---- launchers (each returns the launch's cudaError_t) --------------------
 
 cudaError_t launch_fill_zero(int dt, void *c, int64_t batch, int64_t m, int64_t n, int64_t ldc,
@@ -289,6 +308,13 @@ cudaError_t launch_gated_grad(int dt, const GatedGradParams &p, cudaStream_t s);
 cudaError_t launch_sum_gemm_simt(int dt, const SumGemmParams &p, cudaStream_t s);
 cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s);
 cudaError_t launch_codes_to_f16(const RepackParams &p, cudaStream_t s);
+// on the tensor cores: gated a[0] = x, b = both weights, all K-contiguous in boxes of pair_tc_rows()
+// rows; sum a and b as in SumGemmParams, b in 64 x 64 boxes; codes a[0] and b[0] (f16) as gated
+cudaError_t launch_gated_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_sum_gemm_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_gemm_i8_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s);
+int pair_tc_rows();
+int pair_tc_block_k();
 cudaError_t launch_quantize_i8(int dt, const QuantizeParams &p, cudaStream_t s);
 cudaError_t launch_gemm_i8_dot(int dt, const GemmI8Params &p, cudaStream_t s);
 

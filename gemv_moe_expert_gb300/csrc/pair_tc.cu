@@ -1,0 +1,466 @@
+// pair_tc.cu -- products of the feed-forward block on the tensor cores, 256 x 256
+// accumulators on CTA pairs (tcgen05.mma.cta_group::2, M = 256, N = 256, K = 16):
+//   kGated  h = act(x Wg^T) * (x Wu^T): the pair's even CTA loads 128 rows of Wg, its odd CTA
+//           the same 128 rows of Wu, so columns 0..127 of each CTA's accumulator hold the gate
+//           and 128..255 the up projection of the same outputs; one thread has both
+//   kSum    c = a0 b0 + a1 b1 (the gradient of x from those of both projections): one
+//           accumulator, the contraction runs over the first source and then the second
+//   kCodes  c = (a b^T) scale_a scale_b for 8-bit codes held as f16: a product of two codes, and
+//           any sum of them below 2^24, is exact in the f32 accumulator; after each 1024 of k (at
+//           most 2^24) the epilogue adds the accumulator to 32-bit integers in registers
+// The tensor core has no fast 8-bit integer form on sm_103a, so codes run at the 16-bit rate.
+//
+// Roles and buffers are those of the CTA-pair GEMM (gemm_tc.cu): per CTA and k-block of 64 a 128 x
+// 64 piece of A and of B in a six-deep ring, two accumulators in tensor memory, so that a tile's
+// epilogue runs under the next tile's MMAs, a grouped raster of tiles, and the last round's tiles
+// as two halves where it would leave half of the pairs idle.  Eight epilogue warps a CTA: a lane
+// quarter and half of the columns each, since both projections' activation (or the integer
+// conversion) costs more than rounding.
+//   warp 0      TMA (both CTAs), completion counted on the even CTA's barrier
+//   warp 1      tensor memory; in the even CTA one thread issues the pair's MMAs
+//   warps 2..9  epilogue (both CTAs)
+// Every wait is bounded; a timeout raises both CTAs' abort flags and the device error word.
+#include "gated.cuh"
+
+namespace gbmm {
+
+namespace {
+
+constexpr int kBM = 128;  // rows of A and of B in one CTA
+constexpr int kBN = 256;  // accumulator columns
+constexpr int kBK = 64;
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kGroupM = 8;
+constexpr uint32_t kABytes = kBM * kBK * 2;
+constexpr uint32_t kStageBytes = 2 * kABytes;
+constexpr uint32_t kMNBox = 64 * kBK * 2;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSmemBytes = kStages * kStageBytes + 256 + 1024;
+constexpr int kExactBlocks = 1024 / kBK;  // k-blocks whose sum of products of two codes stays within 2^24
+
+enum Mode { kGated, kSum, kCodes };
+
+template <int kMode>
+struct Shape {
+    static constexpr int kTileN = kMode == kGated ? kBN / 2 : kBN;  // outputs across a tile
+};
+
+struct Unit {
+    int mb, nb;
+    int h;       // half of the tile's columns that a half unit computes
+    int halves;  // 2: whole tile, 1: half unit h, 0: nothing (half past n)
+};
+
+// Units [0, split_from) are whole tiles; every tile from there on is two half units.
+__device__ __forceinline__ Unit decode(int u, int split_from, int tile_n, const PairTcParams &p) {
+    Unit t;
+    const bool half = u >= split_from;
+    const int tile = half ? split_from + (u - split_from) / 2 : u;
+    const int first_m = tile / (kGroupM * p.tiles_n) * kGroupM;
+    const int gm = min(kGroupM, p.tiles_m - first_m);
+    const int local = tile % (kGroupM * p.tiles_n);
+    t.mb = first_m + local % gm;
+    t.nb = local / gm;
+    t.h = half ? (u - split_from) & 1 : 0;
+    t.halves = !half ? 2 : (static_cast<int64_t>(t.nb) * tile_n + t.h * (tile_n / 2) < p.n ? 1 : 0);
+    return t;
+}
+
+template <typename TC>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 32 consecutive outputs of a row (32-byte stores where `vec`, else the first `left`)
+template <typename TC>
+__device__ __forceinline__ void store32(TC *dst, const float (&v)[32], bool vec, int64_t left) {
+    if (vec && left >= 32) {
+        constexpr int kWords = 32 * sizeof(TC) / 4;
+        uint32_t o[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (sizeof(TC) == 4) o[i] = __float_as_uint(v[i]);
+            else o[i] = pack2<TC>(v[2 * i], v[2 * i + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; i += 8)
+            asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             reinterpret_cast<uint32_t *>(dst) + i),
+                         "r"(o[i]), "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]),
+                         "r"(o[i + 6]), "r"(o[i + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < left) dst[i] = Elem<TC>::from_f(v[i]);
+    }
+}
+
+template <int kAct>
+__device__ __forceinline__ void gate32(const uint32_t (&g)[32], const uint32_t (&u)[32], float (&h)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) h[i] = gate_act(kAct, __uint_as_float(g[i])) * __uint_as_float(u[i]);
+}
+
+template <typename TC, uint32_t kFmt, int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+pair_tc_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ CUtensorMap map_a1,
+               const __grid_constant__ CUtensorMap map_b0, const __grid_constant__ CUtensorMap map_b1,
+               const PairTcParams p) {
+    constexpr int kTileN = Shape<kMode>::kTileN;
+    constexpr bool kBMN = kMode == kSum;  // B stored [k, n]
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t s0 = raw_addr + pad;  // stage s: A at s0 + s * kStageBytes, B kABytes after it
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes);
+    const uint32_t bar0 = smem_addr(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kStages + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kStages + 2 + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kStages + 5);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();  // 0 issues the MMAs
+    const bool leader = rank == 0;
+    const uint64_t lim = p.wait_limit_ns;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full_bar(s), 1);   // the even CTA's producer arrive + both CTAs' bytes
+            mbar_init(empty_bar(s), 1);  // the pair MMAs' commit
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull_bar(a), 1);
+            mbar_init(tempty_bar(a), 2 * kEpiWarps);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&map_a0);
+        tma_prefetch_desc(&map_b0);
+        if (kMode != kCodes) tma_prefetch_desc(&map_b1);
+        if (kMode == kSum) tma_prefetch_desc(&map_a1);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_addr(tmem_slot), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    // both CTAs' barriers exist before any copy, commit or arrival can reach them
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    grid_dep_begin();
+    const int blocks1 = (p.k + kBK - 1) / kBK;  // k-blocks of a source
+    const int kblocks = kMode == kSum ? 2 * blocks1 : blocks1;
+    const int chunk = kMode == kCodes ? kExactBlocks : kblocks;  // k-blocks that go into one accumulator
+    const int cl = static_cast<int>(blockIdx.x) >> 1;
+    const int ncl = static_cast<int>(gridDim.x) >> 1;
+    int tail = p.num_tiles > ncl ? p.num_tiles % ncl : (2 * p.num_tiles <= ncl ? p.num_tiles : 0);
+    if (2 * tail > ncl) tail = 0;
+    const int split_from = p.num_tiles - tail;
+    const int num_units = split_from + 2 * tail;
+    // a timeout stops both CTAs of the pair
+    const uint32_t peer_abort = mapa_shared(smem_addr(const_cast<int *>(abort_flag)), rank ^ 1u);
+    auto raise_abort = [&]() {
+        *abort_flag = 1;
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_abort), "r"(1) : "memory");
+        report_device_error(p.err, kKidPairTc);
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer (both CTAs) ----------------
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = cl; u < num_units && ok; u += ncl) {
+                const Unit t = decode(u, split_from, kTileN, p);
+                if (t.halves == 0) continue;
+                const int arow = t.mb * 2 * kBM + static_cast<int>(rank) * kBM;
+                // a half unit uses the first 64 of the 128 B rows that each CTA loads
+                const int brow = kMode == kGated ? t.nb * kTileN + t.h * (kTileN / 2)
+                                 : t.halves == 2 ? t.nb * kTileN + static_cast<int>(rank) * kBM
+                                                 : t.nb * kTileN + t.h * (kTileN / 2) + static_cast<int>(rank) * (kBM / 2);
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!mbar_wait_bounded_cluster(empty_bar(stage), phase ^ 1u, lim, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) mbar_arrive_expect_tx(full_bar(stage), 2 * kStageBytes);
+                    const uint32_t sa = s0 + stage * kStageBytes, sb = sa + kABytes;
+                    const uint32_t fb = mapa_shared(full_bar(stage), 0);
+                    const bool second = kMode == kSum && kb >= blocks1;
+                    const int k0 = (second ? kb - blocks1 : kb) * kBK;
+                    tma_load_3d_pair(sa, second ? &map_a1 : &map_a0, fb, k0, arow, 0);
+                    if (kBMN) {
+                        const CUtensorMap *mb = second ? &map_b1 : &map_b0;
+                        tma_load_3d_pair(sb, mb, fb, brow, k0, 0);
+                        tma_load_3d_pair(sb + kMNBox, mb, fb, brow + 64, k0, 0);
+                    } else {
+                        tma_load_3d_pair(sb, kMode == kGated && !leader ? &map_b1 : &map_b0, fb, k0, brow, 0);
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                raise_abort();
+                // copies still in flight land within microseconds; give them 200 us
+                const uint64_t t0 = global_ns();
+                while (global_ns() - t0 < 200000ull) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ---------------- pair MMA issuer (even CTA) ----------------
+            constexpr uint32_t kIdesc = idesc_f16(kFmt, 2 * kBM, kBN, 0u, kBMN ? 1u : 0u);
+            constexpr uint32_t kIdescHalf = idesc_f16(kFmt, 2 * kBM, kBN / 2, 0u, kBMN ? 1u : 0u);
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t acc_phase[2] = {0u, 0u};
+            bool ok = true;
+            int local = 0;
+            for (int u = cl; u < num_units && ok; u += ncl) {
+                const Unit t = decode(u, split_from, kTileN, p);
+                if (t.halves == 0) continue;
+                const uint32_t idesc = t.halves == 2 ? kIdesc : kIdescHalf;
+                for (int c0 = 0; c0 < kblocks && ok; c0 += chunk) {
+                    const int a = local++ & 1;
+                    // both CTAs' epilogues have read what this accumulator held
+                    if (!mbar_wait_bounded_cluster(tempty_bar(a), acc_phase[a] ^ 1u, lim, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(a * kBN);
+                    const int c1 = min(c0 + chunk, kblocks);
+                    for (int kb = c0; kb < c1; ++kb) {
+                        if (!mbar_wait_bounded_cluster(full_bar(stage), phase, lim, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = s0 + stage * kStageBytes, sb = sa + kABytes;
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 16; ++kk) {
+                            const uint64_t da = sdesc_kmajor_sw128(sa + kk * 32);
+                            const uint64_t db = kBMN ? sdesc_mnmajor_sw128(sb + kk * 2048, kMNBox)
+                                                     : sdesc_kmajor_sw128(sb + kk * 32);
+                            umma_f16_ss_pair(d_tmem, da, db, idesc, kb != c0 || kk != 0 ? 1u : 0u);
+                        }
+                        umma_commit_pair_mc(empty_bar(stage), 0x3);  // the stage is free in both CTAs
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    umma_commit_pair_mc(tfull_bar(a), 0x3);
+                    acc_phase[a] ^= 1u;
+                }
+            }
+            if (!ok) raise_abort();
+            umma_commit_pair_mc(drain_bar, 0x1);
+            mbar_wait_bounded(drain_bar, 0, lim, nullptr);
+        }
+    } else {
+        // ---------------- epilogue (warps 2..9, both CTAs) ----------------
+        const int quarter = warp & 3;        // TMEM lanes 32 * quarter .. + 31
+        const int side = (warp - 2) >> 2;    // which half of a unit's outputs
+        uint32_t tphase[2] = {0u, 0u};
+        int local = 0;
+        bool ok = true;
+        for (int u = cl; u < num_units && ok; u += ncl) {
+            const Unit t = decode(u, split_from, kTileN, p);
+            if (t.halves == 0) continue;
+            const int64_t row = static_cast<int64_t>(t.mb) * 2 * kBM + static_cast<int64_t>(rank) * kBM + quarter * 32 +
+                                lane;
+            const int width = t.halves * (kTileN / 2);  // outputs across this unit
+            const int mine = width / 2;                 // and this warp's share of them
+            const int64_t col0 = static_cast<int64_t>(t.nb) * kTileN + t.h * (kTileN / 2) + side * mine;
+            TC *crow = static_cast<TC *>(p.c) + row * p.ldc;
+            int sum[kMode == kCodes ? kBN / 2 : 1];
+            if constexpr (kMode == kCodes) {
+#pragma unroll
+                for (int i = 0; i < kBN / 2; ++i) sum[i] = 0;
+            }
+            for (int c0 = 0; c0 < kblocks; c0 += chunk) {
+                const int a = local++ & 1;
+                int ready = 0;
+                if (lane == 0) ready = mbar_wait_bounded_cluster(tfull_bar(a), tphase[a], lim, abort_flag);
+                ready = __shfl_sync(0xffffffffu, ready, 0);
+                if (!ready) {
+                    if (lane == 0) raise_abort();
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                        static_cast<uint32_t>(a * kBN + side * mine);
+                if constexpr (kMode == kCodes) {
+#pragma unroll
+                    for (int i = 0; i < kBN / 2; i += 16) {
+                        if (i >= mine) break;
+                        uint32_t r[16];
+                        tmem_ld16(t_addr + i, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) sum[i + e] += __float2int_rn(__uint_as_float(r[e]));
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < mine; i += 32) {
+                        uint32_t r[32];
+                        float v[32];
+                        tmem_ld32(t_addr + i, r);
+                        const int64_t col = col0 + i;
+                        const bool live = row < p.m && col < p.n;
+                        if constexpr (kMode == kGated) {
+                            uint32_t q[32];
+                            tmem_ld32(t_addr + width + i, q);
+                            tmem_ld_wait();
+                            switch (p.act) {
+                            case GBMM_GATE_SILU: gate32<GBMM_GATE_SILU>(r, q, v); break;
+                            case GBMM_GATE_GELU: gate32<GBMM_GATE_GELU>(r, q, v); break;
+                            case GBMM_GATE_GELU_TANH: gate32<GBMM_GATE_GELU_TANH>(r, q, v); break;
+                            default: gate32<GBMM_GATE_RELU>(r, q, v);
+                            }
+                            if (live) store32<TC>(crow + col, v, p.c_vec, p.n - col);
+                            if (p.saved[0] != nullptr && live) {
+                                const int64_t at = row * p.ld_saved + col;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+                                store32<TC>(static_cast<TC *>(p.saved[0]) + at, v, p.saved_vec, p.n - col);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(q[e]);
+                                store32<TC>(static_cast<TC *>(p.saved[1]) + at, v, p.saved_vec, p.n - col);
+                            }
+                        } else {
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+                            if (live) store32<TC>(crow + col, v, p.c_vec, p.n - col);
+                        }
+                    }
+                }
+                // this CTA's rows of the accumulator are read: hand it back to the even CTA's issuer
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(a), 0));
+                tphase[a] ^= 1u;
+            }
+            if constexpr (kMode == kCodes) {
+                if (ok && row < p.m) {
+                    const float sa = p.scale_a != nullptr ? p.scale_a[row] : 1.f;
+#pragma unroll
+                    for (int i = 0; i < kBN / 2; i += 32) {
+                        const int64_t col = col0 + i;
+                        if (i >= mine || col >= p.n) break;
+                        float v[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float sb = p.scale_b != nullptr ? __ldg(p.scale_b + min(col + e, p.n - int64_t{1})) : 1.f;
+                            v[e] = static_cast<float>(sum[i + e]) * sa * sb;
+                        }
+                        store32<TC>(crow + col, v, p.c_vec, p.n - col);
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // every pair MMA has completed (the even CTA waited for its drain) and both CTAs' epilogues are
+    // done before either CTA releases the columns
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, kTmemCols);
+    }
+}
+
+template <typename TC, uint32_t kFmt, int kMode>
+cudaError_t pair_t(const PairTcMaps &maps, PairTcParams p, int num_sms, cudaStream_t s) {
+    constexpr int kTileN = Shape<kMode>::kTileN;
+    static unsigned long long attr_set = 0;  // one bit per device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(attr_set & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(pair_tc_kernel<TC, kFmt, kMode>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        attr_set |= bit;
+    }
+    const int64_t tm = (static_cast<int64_t>(p.m) + 2 * kBM - 1) / (2 * kBM), tn = (p.n + kTileN - 1) / kTileN;
+    if (tm * tn > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
+    p.tiles_m = static_cast<int32_t>(tm);
+    p.tiles_n = static_cast<int32_t>(tn);
+    p.num_tiles = static_cast<int32_t>(tm * tn);
+    const int pairs = num_sms / 2;
+    const int clusters = 2 * p.num_tiles <= pairs ? 2 * p.num_tiles : (p.num_tiles < pairs ? p.num_tiles : pairs);
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, pair_tc_kernel<TC, kFmt, kMode>, maps.a[0], maps.a[1], maps.b[0], maps.b[1], p);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s) {
+    return dt == kF16 ? pair_t<__half, 0, kGated>(maps, p, num_sms, s)
+                      : pair_t<__nv_bfloat16, 1, kGated>(maps, p, num_sms, s);
+}
+cudaError_t launch_sum_gemm_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s) {
+    return dt == kF16 ? pair_t<__half, 0, kSum>(maps, p, num_sms, s) : pair_t<__nv_bfloat16, 1, kSum>(maps, p, num_sms, s);
+}
+cudaError_t launch_gemm_i8_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s) {
+    switch (dt) {
+    case kF32: return pair_t<float, 0, kCodes>(maps, p, num_sms, s);
+    case kF16: return pair_t<__half, 0, kCodes>(maps, p, num_sms, s);
+    case kBF16: return pair_t<__nv_bfloat16, 0, kCodes>(maps, p, num_sms, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+int pair_tc_rows() { return kBM; }
+int pair_tc_block_k() { return kBK; }
+
+}  // namespace gbmm

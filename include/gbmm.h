@@ -540,15 +540,20 @@ enum {
 };
 
 /* gbmm_gated_scratch_bytes -- bytes of scratch with which gbmm_gated runs these sizes at
- * full speed whatever the layout of its operands.  Host-only. */
-GBMM_API gbmm_status gbmm_gated_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, uint64_t *bytes);
+ * full speed.  aligned: nonzero if x and both weights start on multiples of 16 bytes and ldx
+ * and ldw are multiples of 16 bytes (0 is returned then); 0 for any layout.  Host-only. */
+GBMM_API gbmm_status gbmm_gated_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, int aligned,
+                                              uint64_t *bytes);
 
 /*
  * gbmm_gated -- h = act(x w_gate^T) * (x w_up^T), both projections, the activation and
  * the product in one kernel.
  * gate, up: both NULL, or both projections are written too (for gbmm_gated_backward).
  * h is computed from the unrounded projections.
- * scratch: may be NULL.  Calls in flight must not share it.
+ * scratch: 16-bit operands whose rows do not start on multiples of 16 bytes are laid out
+ * again in it; where it is NULL such a call runs on the FFMA pipe, many times slower for large
+ * m, and where it is smaller than the layout needs the call fails with GBMM_ERR_SCRATCH.  Its
+ * contents need no preparation, and calls in flight must not share it.
  * m or n == 0 is a no-op; k == 0 writes zeros.
  */
 GBMM_API gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n, int64_t k, const void *x,
@@ -556,8 +561,10 @@ GBMM_API gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, i
                                 void *gate, void *up, int64_t ld_saved, void *scratch, uint64_t scratch_bytes,
                                 gbmm_stream stream);
 
-/* gbmm_gated_backward_scratch_bytes -- bytes of scratch that gbmm_gated_backward needs. Host-only. */
-GBMM_API gbmm_status gbmm_gated_backward_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k,
+/* gbmm_gated_backward_scratch_bytes -- bytes of scratch that gbmm_gated_backward needs (both
+ * projections' gradients, and, where x or the weights are not `aligned` as above, 16-bit rows
+ * laid out again).  Host-only. */
+GBMM_API gbmm_status gbmm_gated_backward_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, int aligned,
                                                        uint64_t *bytes);
 
 /*

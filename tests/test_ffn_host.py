@@ -118,11 +118,24 @@ def test_nothing_to_do_is_a_no_op(name, over):
 
 def test_scratch_sizes():
     for fn in (gb.gbmm_gated_scratch_bytes, gb.gbmm_gated_backward_scratch_bytes):
-        assert fn(5, 4, 4, 4)[0] == DTYPE
-        assert fn("bf16", -1, 4, 4)[0] == BAD
-        assert fn("bf16", 4, 1 << 31, 4)[0] == BAD
-        sizes = [fn("bf16", m, 1000, 1000) for m in (0, 1, 1000, 100000)]
-        assert all(st == gb.GBMM_OK for st, _ in sizes) and [v for _, v in sizes] == sorted(v for _, v in sizes)
+        assert fn(5, 4, 4, 4, True)[0] == DTYPE
+        assert fn("bf16", -1, 4, 4, True)[0] == BAD
+        assert fn("bf16", 4, 1 << 31, 4, True)[0] == BAD
+        for aligned in (False, True):
+            sizes = [fn("bf16", m, 1000, 1000, aligned) for m in (0, 1, 1000, 100000)]
+            assert all(st == gb.GBMM_OK for st, _ in sizes) and [v for _, v in sizes] == sorted(v for _, v in sizes)
+        assert fn("bf16", 1000, 1000, 1000, True)[1] < fn("bf16", 1000, 1000, 1000, False)[1]
+        assert fn("f32", 1000, 1000, 1000, True)[1] == fn("f32", 1000, 1000, 1000, False)[1]
+    # rows that do not start on multiples of 16 bytes
+    need = gb.gbmm_gated_scratch_bytes("bf16", 40, 32, 64, False)[1]
+    over = dict(m=40, ldx=65, ldw=65)
+    assert call(*CALLS["gated"], dict(over, nbytes=need)) == PASSES
+    assert call(*CALLS["gated"], dict(over, nbytes=need - 1)) == SCRATCH
+    assert call(*CALLS["gated"], dict(over, scratch=0, nbytes=0)) == PASSES
+    need = gb.gbmm_gated_backward_scratch_bytes("bf16", 4, 32, 64, False)[1]
+    over = dict(ldx=65, ldw=65)
+    assert call(*CALLS["back"], dict(over, nbytes=need)) == PASSES
+    assert call(*CALLS["back"], dict(over, nbytes=need - 1)) == SCRATCH
     assert gb.gbmm_gemm_i8_scratch_bytes(1, 1, gb.I8_MAX_K + 1)[0] == BAD
     assert gb.gbmm_gemm_i8_scratch_bytes(-1, 1, 1)[0] == BAD
     assert gb.gbmm_gemm_i8_scratch_bytes(1 << 31, 1, 1)[0] == BAD
@@ -134,7 +147,7 @@ def test_scratch_sizes():
         if need:
             assert call(*CALLS["gemm"], dict(far, nbytes=need - 1)) == SCRATCH
             assert call(*CALLS["gemm"], dict(far, nbytes=need, scratch=0)) == SCRATCH
-    st, need = gb.gbmm_gated_backward_scratch_bytes("bf16", 4, 32, 64)
+    st, need = gb.gbmm_gated_backward_scratch_bytes("bf16", 4, 32, 64, True)
     assert call(*CALLS["back"], dict(nbytes=need)) == PASSES
     assert call(*CALLS["back"], dict(nbytes=need - 1)) == SCRATCH
 

@@ -42,7 +42,7 @@ def _lib():
 
 
 def scratch_for(fn, dtype, m, n, k):
-    st, need = fn(dtype, m, n, k)
+    st, need = fn(dtype, m, n, k, False)
     gb.check(st)
     return DevBuf(max(need, 1)), need
 
@@ -262,7 +262,7 @@ def test_gradient_against_differences(act):
         return torch.from_numpy(np.ascontiguousarray(v, np.float32)).cuda()
     x, wg, wu, g, u, dh = (up_(v) for v in (b.x, b.wg, b.wu, gate, up, d_h))
     out = [torch.empty_like(v) for v in (x, wg, wu)]
-    st, need = gb.gbmm_gated_backward_scratch_bytes("f32", m, n, k)
+    st, need = gb.gbmm_gated_backward_scratch_bytes("f32", m, n, k, True)
     scratch = torch.empty(need, dtype=torch.uint8, device="cuda")
     gb.check(gb.gbmm_gated_backward("f32", CODE[act], m, n, k, x, k, wg, wu, k, g, u, n, dh, n, out[0], k, out[1],
                                     out[2], k, scratch, need))
@@ -286,7 +286,7 @@ def make(dtype, m, n, k, seed):
     t = {"x": new(m, k), "wg": new(n, k) / k ** 0.5, "wu": new(n, k) / k ** 0.5, "dh": new(m, n)}
     t |= {name: torch.zeros(m, n, dtype=dt, device="cuda") for name in ("h", "gate", "up")}
     t |= {"dx": torch.zeros_like(t["x"]), "dwg": torch.zeros_like(t["wg"]), "dwu": torch.zeros_like(t["wu"])}
-    t["need"] = max(gb.gbmm_gated_backward_scratch_bytes(dtype, m, n, k)[1], gb.gbmm_gated_scratch_bytes(dtype, m, n, k)[1])
+    t["need"] = max(fn(dtype, m, n, k, False)[1] for fn in (gb.gbmm_gated_scratch_bytes, gb.gbmm_gated_backward_scratch_bytes))
     t["scratch"] = torch.empty(t["need"] + 1, dtype=torch.uint8, device="cuda")
     return t
 
