@@ -97,6 +97,8 @@ _lock = threading.Lock()
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load libgbmm.so (once).  Raises OSError if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -182,9 +184,10 @@ def _ptr(x) -> int:
         return 0
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return int(x.data_ptr())
-    raise TypeError(f"expected a device pointer, got {type(x)!r}")
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        raise TypeError(f"expected a device pointer, got {type(x)!r}") from None
 
 
 def _stream(stream) -> int:

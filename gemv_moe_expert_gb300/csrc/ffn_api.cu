@@ -2,6 +2,8 @@
 // (gbmm_gated*) and of the 8-bit integer product (gbmm_quantize_i8,
 // gbmm_gemm_i8): argument checks, all of them before the first launch, then
 // the choice of kernels.
+#include <algorithm>
+
 #include "api_checks.h"
 #include "kernel_params.h"
 
@@ -36,8 +38,9 @@ Operand matrix(const char *label, const void *p, uint64_t bytes, int64_t cols, i
 bool rows16(const void *p, int64_t ld_bytes) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld_bytes % 16 == 0;
 }
-int32_t rows32(const void *p, int64_t ld_bytes) {
-    return reinterpret_cast<uintptr_t>(p) % 32 == 0 && ld_bytes % 32 == 0;
+// widest stores that rows allow: 2: 32 bytes, 1: 16
+int32_t row_stores(const void *p, int64_t ld_bytes) {
+    return reinterpret_cast<uintptr_t>(p) % 32 == 0 && ld_bytes % 32 == 0 ? 2 : rows16(p, ld_bytes) ? 1 : 0;
 }
 
 // Few rows run as dot products, a warp for each column or two; more run as tiles.
@@ -71,7 +74,7 @@ bool pair_params(PairTcParams *p, void *c, int64_t ldc, int size, int64_t m, int
     p->m = static_cast<int32_t>(m);
     p->n = static_cast<int32_t>(n);
     p->k = static_cast<int32_t>(k);
-    p->c_vec = rows32(c, ldc * size);
+    p->c_vec = row_stores(c, ldc * size);
     p->err = device_error_word();
     p->wait_limit_ns = kWaitLimitNs;
     return p->err != nullptr;
@@ -160,7 +163,7 @@ gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n,
         q.saved[0] = gate;
         q.saved[1] = up;
         q.ld_saved = ld_saved;
-        q.saved_vec = rows32(gate, ld_saved * 2) && rows32(up, ld_saved * 2);
+        q.saved_vec = std::min(row_stores(gate, ld_saved * 2), row_stores(up, ld_saved * 2));
         q.act = static_cast<int32_t>(activation);
         return finish_launch(launch_gated_tc(dt, maps, q, device_sm_count(), s), fn, s);
     }

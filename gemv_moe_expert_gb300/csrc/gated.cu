@@ -42,65 +42,90 @@ __device__ __forceinline__ void store_f(T *p, bool whole, int64_t left, const fl
 }
 
 // ---------------------------------------------------------------------------
-// few rows: one warp computes column j of both projections for kM rows of x
+// few rows: one warp computes column j of both projections for kM rows of x.  Bound by reading the weights: a lane
+// asks for kU units of both weight rows before it uses the first.  A unit is the widest access (16 to 2 bytes) that
+// every row allows.
 // ---------------------------------------------------------------------------
 
 constexpr int kDotWarps = 4;
 
-template <typename T, int kM, bool kVec>
+template <int kBytes>
+struct Raw;
+template <> struct Raw<16> { using type = uint4; };
+template <> struct Raw<8> { using type = uint2; };
+template <> struct Raw<4> { using type = uint32_t; };
+template <> struct Raw<2> { using type = uint16_t; };
+
+template <typename T, typename R>
+__device__ __forceinline__ void unpack(const R &raw, float (&v)[sizeof(R) / sizeof(T)]) {
+    if constexpr (sizeof(R) == 16) {
+        unpack16<T>(raw, v);
+    } else {
+        T t[sizeof(R) / sizeof(T)];
+        memcpy(t, &raw, sizeof(R));
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(R) / sizeof(T)); ++i) v[i] = Elem<T>::to_f(t[i]);
+    }
+}
+template <typename R>
+__device__ __forceinline__ R load_weights(const void *p) {
+    if constexpr (sizeof(R) == 16) return ld_stream16(p);
+    else return __ldg(static_cast<const R *>(p));
+}
+
+template <typename T, int kM, int kBytes>
 __global__ void __launch_bounds__(32 * kDotWarps) gated_rowdot_kernel(const GatedParams p) {
+    using R = typename Raw<kBytes>::type;
+    constexpr int kN = kBytes / sizeof(T);
+    constexpr int kU = kBytes == 16 && kM > 2 ? 4 : 8;
+    grid_dep_begin();
     const int lane = threadIdx.x & 31;
     const int64_t j = static_cast<int64_t>(blockIdx.x) * kDotWarps + (threadIdx.x >> 5);
     if (j >= p.n) return;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kM;
-    const T *x = static_cast<const T *>(p.x) + i0 * p.ldx;
+    const T *x = static_cast<const T *>(p.x);
     const T *w0 = static_cast<const T *>(p.w[0]) + j * p.ldw;
     const T *w1 = static_cast<const T *>(p.w[1]) + j * p.ldw;
+    const int rows = static_cast<int>(p.m);
     float g[kM], u[kM];
 #pragma unroll
     for (int r = 0; r < kM; ++r) g[r] = u[r] = 0.f;
-    constexpr int kN = kVec ? Elem<T>::kVec : 1;
-    int64_t at = lane * kN;
-    if (kVec) {
-        constexpr int kU = 4;
-        // kU blocks of both weight rows are asked for before the first is used
-        for (; at + (kU - 1) * kLanes * kN + kN <= p.k; at += kU * kLanes * kN) {
-            uint4 a[kU], b[kU];
+    const int64_t units = p.k / kN;
+    for (int64_t at = lane; at < units; at += kU * kLanes) {
+        R a[kU], b[kU];
 #pragma unroll
-            for (int q = 0; q < kU; ++q) {
-                a[q] = ld_stream16(w0 + at + q * kLanes * kN);
-                b[q] = ld_stream16(w1 + at + q * kLanes * kN);
-            }
+        for (int q = 0; q < kU; ++q) {
+            if (at + q * kLanes >= units) break;
+            a[q] = load_weights<R>(w0 + (at + q * kLanes) * kN);
+            b[q] = load_weights<R>(w1 + (at + q * kLanes) * kN);
+        }
 #pragma unroll
-            for (int q = 0; q < kU; ++q) {
-                float wa[Elem<T>::kVec], wb[Elem<T>::kVec], xv[Elem<T>::kVec];
-                unpack16<T>(a[q], wa);
-                unpack16<T>(b[q], wb);
+        for (int q = 0; q < kU; ++q) {
+            if (at + q * kLanes >= units) break;
+            float wa[kN], wb[kN], xv[kN];
+            unpack<T>(a[q], wa);
+            unpack<T>(b[q], wb);
 #pragma unroll
-                for (int r = 0; r < kM; ++r) {
-                    if (i0 + r >= p.m) break;
-                    unpack16<T>(ld_cached16(x + r * p.ldx + at + q * kLanes * kN), xv);
+            for (int r = 0; r < kM; ++r) {
+                if (r >= rows) break;
+                unpack<T>(__ldg(reinterpret_cast<const R *>(x + r * p.ldx + (at + q * kLanes) * kN)), xv);
 #pragma unroll
-                    for (int e = 0; e < kN; ++e) {
-                        g[r] = fmaf(wa[e], xv[e], g[r]);
-                        u[r] = fmaf(wb[e], xv[e], u[r]);
-                    }
+                for (int e = 0; e < kN; ++e) {
+                    g[r] = fmaf(wa[e], xv[e], g[r]);
+                    u[r] = fmaf(wb[e], xv[e], u[r]);
                 }
             }
         }
     }
-    for (; at < p.k; at += kLanes * kN) {
+    // less than a unit is left at the end of a row
+    const int64_t e = units * kN + lane;
+    if (e < p.k) {
+        const float wa = Elem<T>::to_f(w0[e]), wb = Elem<T>::to_f(w1[e]);
 #pragma unroll
-        for (int e = 0; e < kN; ++e) {
-            if (at + e >= p.k) break;
-            const float wa = Elem<T>::to_f(w0[at + e]), wb = Elem<T>::to_f(w1[at + e]);
-#pragma unroll
-            for (int r = 0; r < kM; ++r) {
-                if (i0 + r >= p.m) break;
-                const float xv = Elem<T>::to_f(x[r * p.ldx + at + e]);
-                g[r] = fmaf(wa, xv, g[r]);
-                u[r] = fmaf(wb, xv, u[r]);
-            }
+        for (int r = 0; r < kM; ++r) {
+            if (r >= rows) break;
+            const float xv = Elem<T>::to_f(x[r * p.ldx + e]);
+            g[r] = fmaf(wa, xv, g[r]);
+            u[r] = fmaf(wb, xv, u[r]);
         }
     }
 #pragma unroll
@@ -110,36 +135,44 @@ __global__ void __launch_bounds__(32 * kDotWarps) gated_rowdot_kernel(const Gate
     }
 #pragma unroll
     for (int r = 0; r < kM; ++r) {
-        if (lane != r || i0 + r >= p.m) continue;
-        static_cast<T *>(p.h)[(i0 + r) * p.ldh + j] = Elem<T>::from_f(gate_act(p.act, g[r]) * u[r]);
+        if (lane != r || r >= rows) continue;
+        static_cast<T *>(p.h)[r * p.ldh + j] = Elem<T>::from_f(gate_act(p.act, g[r]) * u[r]);
         if (p.saved[0] != nullptr) {
-            static_cast<T *>(p.saved[0])[(i0 + r) * p.ld_saved + j] = Elem<T>::from_f(g[r]);
-            static_cast<T *>(p.saved[1])[(i0 + r) * p.ld_saved + j] = Elem<T>::from_f(u[r]);
+            static_cast<T *>(p.saved[0])[r * p.ld_saved + j] = Elem<T>::from_f(g[r]);
+            static_cast<T *>(p.saved[1])[r * p.ld_saved + j] = Elem<T>::from_f(u[r]);
         }
     }
 }
 
-template <typename T, int kM>
-cudaError_t rowdot_m(const GatedParams &p, bool vec, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>((p.n + kDotWarps - 1) / kDotWarps),
-                    static_cast<unsigned>((p.m + kM - 1) / kM));
-    if (vec) gated_rowdot_kernel<T, kM, true><<<grid, 32 * kDotWarps, 0, s>>>(p);
-    else gated_rowdot_kernel<T, kM, false><<<grid, 32 * kDotWarps, 0, s>>>(p);
-    return cudaGetLastError();
+bool rows_on(const void *p, int64_t ld_bytes, int unit) {
+    return reinterpret_cast<uintptr_t>(p) % unit == 0 && ld_bytes % unit == 0;
 }
+bool rows16(const void *p, int64_t ld, size_t size) { return rows_on(p, ld * static_cast<int64_t>(size), 16); }
 
-bool rows16(const void *p, int64_t ld, size_t size) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * static_cast<int64_t>(size) % 16 == 0;
+template <typename T, int kM>
+cudaError_t rowdot_m(const GatedParams &p, cudaStream_t s) {
+    constexpr int64_t size = sizeof(T);
+    int unit = 16;
+    while (unit > size && !(rows_on(p.x, p.ldx * size, unit) && rows_on(p.w[0], p.ldw * size, unit) &&
+                            rows_on(p.w[1], p.ldw * size, unit)))
+        unit /= 2;
+    const dim3 grid(static_cast<unsigned>((p.n + kDotWarps - 1) / kDotWarps)), block(32 * kDotWarps);
+    switch (unit) {
+    case 16: return launch_early(gated_rowdot_kernel<T, kM, 16>, grid, block, 0, s, p);
+    case 8: return launch_early(gated_rowdot_kernel<T, kM, 8>, grid, block, 0, s, p);
+    case 4: return launch_early(gated_rowdot_kernel<T, kM, 4>, grid, block, 0, s, p);
+    default:
+        if constexpr (sizeof(T) == 2) return launch_early(gated_rowdot_kernel<T, kM, 2>, grid, block, 0, s, p);
+        return cudaErrorInvalidValue;
+    }
 }
 
 template <typename T>
 cudaError_t rowdot_t(const GatedParams &p, cudaStream_t s) {
-    const bool vec = rows16(p.x, p.ldx, sizeof(T)) && rows16(p.w[0], p.ldw, sizeof(T)) &&
-                     rows16(p.w[1], p.ldw, sizeof(T));
-    if (p.m == 1) return rowdot_m<T, 1>(p, vec, s);
-    if (p.m == 2) return rowdot_m<T, 2>(p, vec, s);
-    if (p.m <= 4) return rowdot_m<T, 4>(p, vec, s);
-    return rowdot_m<T, 8>(p, vec, s);
+    if (p.m == 1) return rowdot_m<T, 1>(p, s);
+    if (p.m == 2) return rowdot_m<T, 2>(p, s);
+    if (p.m <= 4) return rowdot_m<T, 4>(p, s);
+    return p.m <= 8 ? rowdot_m<T, 8>(p, s) : cudaErrorInvalidValue;
 }
 
 // ---------------------------------------------------------------------------

@@ -13,159 +13,290 @@ bool rows_on(const void *p, int64_t ld_bytes, int unit) {
 
 // ---------------------------------------------------------------------------
 // quantisation: scale = max |x| * f32(1 / 127), code = the integer nearest to x / scale, ties to even
+//
+// A row is read once, into registers, by 32 or 256 threads (more for rows that these do not hold; a row longer than
+// 1024 threads hold is read again).  Bound by HBM, 3 bytes an element of 16 bits, so what each element costs
+// in instructions matters: fma(x, 1 / scale, 1.5 * 2^23) leaves the code in its low byte, and the distance to it tells
+// whether the quotient may lie on the other side of a middle; only then is the code worked out exactly.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// The integer nearest to x / s for |x| <= 127 s (1 + 2^-22), ties to even.  rint(x * inv) is that
+// The integer nearest to x / s for |x| <= 127 s (1 + 2^-22), ties to even.  rint(x / s) in f32 is that
 // integer or, next to the middle of two, its neighbour; the remainder x - n s is exact in one fma (it
 // is a multiple of the smaller of x's and s's last places and below s), and says which.
-__device__ __forceinline__ int nearest_code(float x, float s, float inv) {
-    float n = rintf(s < 1e-30f ? x / s : x * inv);
+__device__ __noinline__ int nearest_code(float x, float s) {
+    float n = rintf(x / s);
     const float r = fmaf(-n, s, x), twice = 2.f * fabsf(r);
     if (twice > s || (twice == s && (static_cast<int>(n) & 1))) n += r > 0.f ? 1.f : -1.f;
     return static_cast<int>(fminf(fmaxf(n, -127.f), 127.f));
 }
 
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(256) quantize_kernel(const QuantizeParams p) {
+// What a row's scale gives: inv = 1 / scale, 0 where codes are 0 (scale 0 or NaN), and `exact` where
+// 1 / scale is out of f32's normal range.
+struct RowScale {
+    float s, inv;
+    bool live, exact;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t most) {
+    RowScale r;
+    // infinities and NaN are above every finite value in the order of the absolute value's bits
+    const bool finite = most < 0x7f800000u;
+    r.s = finite ? __uint_as_float(most) * (1.f / 127.f) : __uint_as_float(0x7fc00000u);
+    r.live = finite && r.s > 0.f;
+    r.exact = r.live && r.s < 1e-30f;
+    r.inv = r.live && !r.exact ? 1.f / r.s : 0.f;
+    return r;
+}
+
+// Codes of four values, one a byte.  x * inv is off by 3 * 2^-24 of itself, below 2^-15: a quotient that is
+// further than 2^-12 from a middle is rounded to the side that it lies on.
+__device__ __forceinline__ uint32_t codes4(const float *v, const RowScale &r) {
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: what is added to it is rounded to an integer
+    uint32_t w[4];
+    float far = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float x = r.inv != 0.f ? v[e] : 0.f;  // no NaN or infinity from a row whose codes are 0
+        const float t = fmaf(x, r.inv, kMagic);
+        far = fmaxf(far, fabsf(fmaf(x, r.inv, -(t - kMagic))));
+        w[e] = __float_as_uint(t);
+    }
+    if (far > 0.5f - 0x1p-12f || r.exact) {
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) w[e] = static_cast<uint32_t>(nearest_code(v[e], r.s));
+    }
+    return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+}
+
+template <int kT>
+__device__ __forceinline__ uint32_t row_max(uint32_t most) {
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (kT > 32) {
+        __shared__ uint32_t warp_max[32];
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) warp_max[threadIdx.x >> 5] = most;
+        __syncthreads();
+        most = __reduce_max_sync(0xffffffffu, warp_max[lane % (kT / 32)]);
+    }
+    return most;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t piece_max(const uint4 &v) {
+    float f[Elem<T>::kVec];
+    unpack16<T>(v, f);
+    uint32_t most = 0;
+#pragma unroll
+    for (int e = 0; e < Elem<T>::kVec; ++e) most = max(most, abs_bits(f[e]));
+    return most;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_codes(const uint4 &v, const RowScale &r, int8_t *q) {
     constexpr int kN = Elem<T>::kVec;
-    __shared__ uint32_t warp_max[8];
+    float f[kN];
+    unpack16<T>(v, f);
+    if constexpr (kN == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(codes4(f, r), codes4(f + 4, r));
+    else *reinterpret_cast<uint32_t *>(q) = codes4(f, r);
+}
+
+// kT threads a row, kP pieces of 16 bytes a thread; kP == 0: any length, read twice
+template <typename T, int kT, int kP>
+__global__ void __launch_bounds__(kT < 256 ? 256 : kT) quantize_kernel(const QuantizeParams p) {
+    constexpr int kN = Elem<T>::kVec;
+    grid_dep_begin();
+    const int64_t i = kT < 256 ? static_cast<int64_t>(blockIdx.x) * (256 / kT) + threadIdx.x / kT : blockIdx.x;
+    if (kT == 32 && i >= p.m) return;
+    const int t = threadIdx.x % kT;
+    const T *x = static_cast<const T *>(p.x) + i * p.ldx;
+    int8_t *q = p.q + i * p.ldq;
+    const int64_t pieces = p.k / kN;
+    // the last, partial piece belongs to one thread
+    const int rest = static_cast<int>(p.k % kN);
+    const bool has_rest = rest != 0 && t == static_cast<int>(pieces % kT);
+    uint32_t most = 0;
+    if (has_rest)
+        for (int e = 0; e < rest; ++e) most = max(most, abs_bits(Elem<T>::to_f(x[pieces * kN + e])));
+    uint4 v[kP > 0 ? kP : 1];
+    if constexpr (kP > 0) {
+#pragma unroll
+        for (int c = 0; c < kP; ++c) {
+            const int64_t at = t + c * kT;
+            v[c] = at < pieces ? ld_stream16(x + at * kN) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int c = 0; c < kP; ++c) most = max(most, piece_max<T>(v[c]));
+    } else {
+#pragma unroll 4
+        for (int64_t at = t; at < pieces; at += kT) most = max(most, piece_max<T>(ld_cached16(x + at * kN)));
+    }
+    const RowScale r = row_scale(row_max<kT>(most));
+    if (t == 0) p.scale[i] = r.s;
+    if constexpr (kP > 0) {
+#pragma unroll
+        for (int c = 0; c < kP; ++c) {
+            const int64_t at = t + c * kT;
+            if (at < pieces) store_codes<T>(v[c], r, q + at * kN);
+        }
+    } else {
+#pragma unroll 4
+        for (int64_t at = t; at < pieces; at += kT) store_codes<T>(ld_cached16(x + at * kN), r, q + at * kN);
+    }
+    if (has_rest)
+        for (int e = 0; e < rest; ++e) {
+            const int64_t at = pieces * kN + e;
+            q[at] = static_cast<int8_t>(r.live ? nearest_code(Elem<T>::to_f(x[at]), r.s) : 0);
+        }
+}
+
+// rows that start anywhere: one element an access, four in flight
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_any_kernel(const QuantizeParams p) {
+    grid_dep_begin();
     const int64_t i = blockIdx.x;
     const T *x = static_cast<const T *>(p.x) + i * p.ldx;
     int8_t *q = p.q + i * p.ldq;
-    // infinities and NaN are above every finite value in the order of the absolute value's bits
     uint32_t most = 0;
-    int64_t at = threadIdx.x * kN;
-    if (kVec) {
-        for (; at + kN <= p.k; at += 256 * kN) {
-            float v[kN];
-            unpack16<T>(ld_cached16(x + at), v);
+#pragma unroll 8
+    for (int64_t c = threadIdx.x; c < p.k; c += 256) most = max(most, abs_bits(Elem<T>::to_f(x[c])));
+    const RowScale r = row_scale(row_max<256>(most));
+    if (threadIdx.x == 0) p.scale[i] = r.s;
+    for (int64_t c = threadIdx.x; c < p.k; c += 4 * 256) {
+        float v[4];
 #pragma unroll
-            for (int e = 0; e < kN; ++e) most = max(most, abs_bits(v[e]));
-        }
-        for (int e = 0; e < kN && at + e < p.k; ++e) most = max(most, abs_bits(Elem<T>::to_f(x[at + e])));
-    } else {
-        for (int64_t c = threadIdx.x; c < p.k; c += 256) most = max(most, abs_bits(Elem<T>::to_f(x[c])));
+        for (int e = 0; e < 4; ++e) v[e] = c + 256 * e < p.k ? Elem<T>::to_f(x[c + 256 * e]) : 0.f;
+        const uint32_t w = codes4(v, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + 256 * e < p.k) q[c + 256 * e] = static_cast<int8_t>(w >> (8 * e));
     }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = most;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) most = max(most, warp_max[w]);
-    const bool finite = most < 0x7f800000u;
-    const float s = finite ? __uint_as_float(most) * (1.f / 127.f) : __uint_as_float(0x7fc00000u);
-    if (threadIdx.x == 0) p.scale[i] = s;
-    const bool live = finite && s > 0.f;
-    const float inv = 1.f / s;
-    if (kVec) {
-        for (at = threadIdx.x * kN; at < p.k; at += 256 * kN) {
-            if (at + kN <= p.k) {
-                float v[kN];
-                unpack16<T>(ld_cached16(x + at), v);
-                uint32_t w[kN / 4];
-#pragma unroll
-                for (int g = 0; g < kN / 4; ++g) {
-                    w[g] = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[g] |= (static_cast<uint32_t>(live ? nearest_code(v[4 * g + e], s, inv) : 0) & 255u) << (8 * e);
-                }
-                if constexpr (kN == 8) *reinterpret_cast<uint2 *>(q + at) = make_uint2(w[0], w[1]);
-                else *reinterpret_cast<uint32_t *>(q + at) = w[0];
-            } else {
-                for (int e = 0; at + e < p.k; ++e)
-                    q[at + e] = static_cast<int8_t>(live ? nearest_code(Elem<T>::to_f(x[at + e]), s, inv) : 0);
-            }
-        }
-    } else {
-        for (int64_t c = threadIdx.x; c < p.k; c += 256)
-            q[c] = static_cast<int8_t>(live ? nearest_code(Elem<T>::to_f(x[c]), s, inv) : 0);
-    }
+}
+
+template <typename T, int kT, int kP>
+cudaError_t quantize_p(const QuantizeParams &p, cudaStream_t s) {
+    const int64_t blocks = kT < 256 ? (p.m + 256 / kT - 1) / (256 / kT) : p.m;
+    return launch_early(quantize_kernel<T, kT, kP>, dim3(static_cast<unsigned>(blocks)), dim3(kT < 256 ? 256 : kT), 0, s, p);
 }
 
 template <typename T>
 cudaError_t quantize_t(const QuantizeParams &p, cudaStream_t s) {
-    const bool vec = rows_on(p.x, p.ldx * static_cast<int64_t>(sizeof(T)), 16) && rows_on(p.q, p.ldq, Elem<T>::kVec);
-    if (vec) quantize_kernel<T, true><<<static_cast<unsigned>(p.m), 256, 0, s>>>(p);
-    else quantize_kernel<T, false><<<static_cast<unsigned>(p.m), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    if (!rows_on(p.x, p.ldx * static_cast<int64_t>(sizeof(T)), 16) || !rows_on(p.q, p.ldq, Elem<T>::kVec))
+        return launch_early(quantize_any_kernel<T>, dim3(static_cast<unsigned>(p.m)), dim3(256), 0, s, p);
+    const int64_t pieces = p.k / Elem<T>::kVec;
+    if (pieces <= 64) return quantize_p<T, 32, 2>(p, s);
+    if (pieces <= 256) return quantize_p<T, 256, 1>(p, s);
+    if (pieces <= 512) return quantize_p<T, 256, 2>(p, s);
+    if (pieces <= 1024) return quantize_p<T, 256, 4>(p, s);
+    if (pieces <= 1536) return quantize_p<T, 256, 6>(p, s);
+    if (pieces <= 2048) return quantize_p<T, 256, 8>(p, s);
+    if (pieces <= 8192) return quantize_p<T, 1024, 8>(p, s);
+    return quantize_p<T, 1024, 0>(p, s);
 }
 
 // ---------------------------------------------------------------------------
-// the product for few rows: a warp takes kR columns j and kM rows i, its lanes divide k
+// the product for few rows: a warp takes kR columns j and kM rows i, its lanes divide k.  Bound by reading b: a lane
+// asks for kU units of each of its columns before it uses the first.  A unit is 16 or 4 bytes where all rows allow that;
+// rows that start anywhere are read as the aligned words around each group of four, shifted into place.
 // ---------------------------------------------------------------------------
 
 constexpr int kDotWarps = 4;
 constexpr int kR = 2;
 
+// the four codes at row + 4 g; the row has k codes, and what lies past them counts as 0
+__device__ __forceinline__ uint32_t any4(const int8_t *row, int64_t g, int64_t k) {
+    const int8_t *at = row + 4 * g;
+    const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) & 3u);
+    const uint32_t *word = reinterpret_cast<const uint32_t *>(at - shift);
+    if (g > 0 && 4 * g + 8 <= k) return __funnelshift_r(__ldg(word), __ldg(word + 1), 8 * shift);
+    uint32_t v = 0;  // at a row's ends only its own bytes are read
+    for (int e = 0; e < 4; ++e)
+        if (4 * g + e < k) v |= static_cast<uint32_t>(static_cast<uint8_t>(at[e])) << (8 * e);
+    return v;
+}
+
+template <int kUnit> struct Codes;
+template <> struct Codes<16> {
+    uint4 v;
+    __device__ __forceinline__ int dot(const Codes &o, int s) const {
+        s = __dp4a(static_cast<int>(v.x), static_cast<int>(o.v.x), s);
+        s = __dp4a(static_cast<int>(v.y), static_cast<int>(o.v.y), s);
+        s = __dp4a(static_cast<int>(v.z), static_cast<int>(o.v.z), s);
+        return __dp4a(static_cast<int>(v.w), static_cast<int>(o.v.w), s);
+    }
+    static __device__ __forceinline__ Codes stream(const int8_t *row, int64_t u, int64_t) { return {ld_stream16(row + 16 * u)}; }
+    static __device__ __forceinline__ Codes cached(const int8_t *row, int64_t u, int64_t) { return {ld_cached16(row + 16 * u)}; }
+};
+template <> struct Codes<4> {
+    uint32_t v;
+    __device__ __forceinline__ int dot(const Codes &o, int s) const {
+        return __dp4a(static_cast<int>(v), static_cast<int>(o.v), s);
+    }
+    static __device__ __forceinline__ Codes stream(const int8_t *row, int64_t u, int64_t) { return cached(row, u, 0); }
+    static __device__ __forceinline__ Codes cached(const int8_t *row, int64_t u, int64_t) {
+        return {__ldg(reinterpret_cast<const uint32_t *>(row) + u)};
+    }
+};
+template <> struct Codes<1> {
+    uint32_t v;
+    __device__ __forceinline__ int dot(const Codes &o, int s) const {
+        return __dp4a(static_cast<int>(v), static_cast<int>(o.v), s);
+    }
+    static __device__ __forceinline__ Codes stream(const int8_t *row, int64_t u, int64_t k) { return {any4(row, u, k)}; }
+    static __device__ __forceinline__ Codes cached(const int8_t *row, int64_t u, int64_t k) { return {any4(row, u, k)}; }
+};
+
 template <typename T, int kM, int kUnit>
 __global__ void __launch_bounds__(32 * kDotWarps) gemm_i8_dot_kernel(const GemmI8Params p) {
+    constexpr int kU = 4;
+    constexpr int kStep = kUnit == 16 ? 16 : 4;  // codes in a unit
+    grid_dep_begin();
     const int lane = threadIdx.x & 31;
     const int64_t j0 = (static_cast<int64_t>(blockIdx.x) * kDotWarps + (threadIdx.x >> 5)) * kR;
     if (j0 >= p.n) return;
     const int8_t *b[kR];
 #pragma unroll
     for (int c = 0; c < kR; ++c) b[c] = p.b + min(j0 + c, p.n - 1) * p.ldb;
+    // units that are whole; rows that start anywhere have one more, whose missing codes are 0
+    const int64_t units = kUnit == 1 ? (p.k + 3) / 4 : p.k / kStep;
     for (int64_t i0 = static_cast<int64_t>(blockIdx.y) * kM; i0 < p.m; i0 += static_cast<int64_t>(gridDim.y) * kM) {
         const int8_t *a = p.a + i0 * p.lda;
+        const int rows = static_cast<int>(p.m - i0 < kM ? p.m - i0 : kM);
         int acc[kM][kR];
 #pragma unroll
         for (int r = 0; r < kM; ++r)
 #pragma unroll
             for (int c = 0; c < kR; ++c) acc[r][c] = 0;
-        int64_t at = lane * kUnit;
-        if (kUnit == 16) {
-            constexpr int kU = 4;
-            for (; at + (kU - 1) * 512 + 16 <= p.k; at += kU * 512) {
-                uint4 w[kU][kR];
+        for (int64_t at = lane; at < units; at += kU * 32) {
+            Codes<kUnit> w[kU][kR];
 #pragma unroll
-                for (int q = 0; q < kU; ++q)
+            for (int q = 0; q < kU; ++q) {
+                if (at + q * 32 >= units) break;
 #pragma unroll
-                    for (int c = 0; c < kR; ++c) w[q][c] = ld_stream16(b[c] + at + q * 512);
-#pragma unroll
-                for (int q = 0; q < kU; ++q)
-#pragma unroll
-                    for (int r = 0; r < kM; ++r) {
-                        if (i0 + r >= p.m) break;
-                        const uint4 v = ld_cached16(a + r * p.lda + at + q * 512);
-#pragma unroll
-                        for (int c = 0; c < kR; ++c) {
-                            acc[r][c] = __dp4a(static_cast<int>(w[q][c].x), static_cast<int>(v.x), acc[r][c]);
-                            acc[r][c] = __dp4a(static_cast<int>(w[q][c].y), static_cast<int>(v.y), acc[r][c]);
-                            acc[r][c] = __dp4a(static_cast<int>(w[q][c].z), static_cast<int>(v.z), acc[r][c]);
-                            acc[r][c] = __dp4a(static_cast<int>(w[q][c].w), static_cast<int>(v.w), acc[r][c]);
-                        }
-                    }
+                for (int c = 0; c < kR; ++c) w[q][c] = Codes<kUnit>::stream(b[c], at + q * 32, p.k);
             }
-        }
-        if (kUnit >= 4) {
-            for (; at + kUnit <= p.k; at += 32 * kUnit)
 #pragma unroll
-                for (int g = 0; g < kUnit; g += 4) {
-                    int w[kR];
-#pragma unroll
-                    for (int c = 0; c < kR; ++c) w[c] = *reinterpret_cast<const int *>(b[c] + at + g);
-#pragma unroll
-                    for (int r = 0; r < kM; ++r) {
-                        if (i0 + r >= p.m) break;
-                        const int v = *reinterpret_cast<const int *>(a + r * p.lda + at + g);
-#pragma unroll
-                        for (int c = 0; c < kR; ++c) acc[r][c] = __dp4a(w[c], v, acc[r][c]);
-                    }
-                }
-        }
-        // what is left of a row: less than a unit (one lane), or all of it where rows start anywhere
-        for (; at < p.k; at += 32 * kUnit)
-            for (int e = 0; e < kUnit && at + e < p.k; ++e) {
+            for (int q = 0; q < kU; ++q) {
+                if (at + q * 32 >= units) break;
 #pragma unroll
                 for (int r = 0; r < kM; ++r) {
-                    if (i0 + r >= p.m) break;
-                    const int v = a[r * p.lda + at + e];
+                    if (r >= rows) break;
+                    const Codes<kUnit> v = Codes<kUnit>::cached(a + r * p.lda, at + q * 32, p.k);
 #pragma unroll
-                    for (int c = 0; c < kR; ++c) acc[r][c] += v * static_cast<int>(b[c][at + e]);
+                    for (int c = 0; c < kR; ++c) acc[r][c] = w[q][c].dot(v, acc[r][c]);
                 }
             }
+        }
+        const int64_t e = units * kStep + lane;  // less than a unit is left at the end of a row
+        if (e < p.k) {
+#pragma unroll
+            for (int r = 0; r < kM; ++r) {
+                if (r >= rows) break;
+                const int v = a[r * p.lda + e];
+#pragma unroll
+                for (int c = 0; c < kR; ++c) acc[r][c] += v * static_cast<int>(b[c][e]);
+            }
+        }
 #pragma unroll
         for (int r = 0; r < kM; ++r)
 #pragma unroll
@@ -174,7 +305,7 @@ __global__ void __launch_bounds__(32 * kDotWarps) gemm_i8_dot_kernel(const GemmI
         for (int r = 0; r < kM; ++r)
 #pragma unroll
             for (int c = 0; c < kR; ++c) {
-                if (lane != r * kR + c || i0 + r >= p.m || j0 + c >= p.n) continue;
+                if (lane != r * kR + c || r >= rows || j0 + c >= p.n) continue;
                 const float sa = p.scale_a != nullptr ? p.scale_a[i0 + r] : 1.f;
                 const float sb = p.scale_b != nullptr ? p.scale_b[j0 + c] : 1.f;
                 static_cast<T *>(p.c)[(i0 + r) * p.ldc + j0 + c] =
@@ -187,13 +318,12 @@ template <typename T, int kM>
 cudaError_t dot_m(const GemmI8Params &p, cudaStream_t s) {
     const int64_t across = (p.n + kDotWarps * kR - 1) / (kDotWarps * kR), down = (p.m + kM - 1) / kM;
     const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(down < 65535 ? down : 65535));
+    const dim3 block(32 * kDotWarps);
     if (rows_on(p.a, p.lda, 16) && rows_on(p.b, p.ldb, 16))
-        gemm_i8_dot_kernel<T, kM, 16><<<grid, 32 * kDotWarps, 0, s>>>(p);
-    else if (rows_on(p.a, p.lda, 4) && rows_on(p.b, p.ldb, 4))
-        gemm_i8_dot_kernel<T, kM, 4><<<grid, 32 * kDotWarps, 0, s>>>(p);
-    else
-        gemm_i8_dot_kernel<T, kM, 1><<<grid, 32 * kDotWarps, 0, s>>>(p);
-    return cudaGetLastError();
+        return launch_early(gemm_i8_dot_kernel<T, kM, 16>, grid, block, 0, s, p);
+    if (rows_on(p.a, p.lda, 4) && rows_on(p.b, p.ldb, 4))
+        return launch_early(gemm_i8_dot_kernel<T, kM, 4>, grid, block, 0, s, p);
+    return launch_early(gemm_i8_dot_kernel<T, kM, 1>, grid, block, 0, s, p);
 }
 
 template <typename T>

@@ -225,7 +225,7 @@ struct PairTcParams {
     const float *scale_a, *scale_b;  // codes; null: 1
     int64_t ldc, ld_saved;
     int32_t m, n, k;                 // k: of one source
-    int32_t c_vec, saved_vec;        // rows allow 32-byte stores
+    int32_t c_vec, saved_vec;        // rows allow 32-byte (2) or 16-byte (1) stores
     int32_t act;
     int32_t tiles_m, tiles_n, num_tiles;  // set by the launcher
     uint32_t *err;

@@ -81,16 +81,22 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// 32 consecutive outputs of a row (32-byte stores where `vec`, else the first `left`)
+// 32 consecutive outputs of a row: 32- (vec 2) or 16-byte (vec 1) stores, or the first `left` one by one
 template <typename TC>
-__device__ __forceinline__ void store32(TC *dst, const float (&v)[32], bool vec, int64_t left) {
-    if (vec && left >= 32) {
+__device__ __forceinline__ void store32(TC *dst, const float (&v)[32], int vec, int64_t left) {
+    if (vec != 0 && left >= 32) {
         constexpr int kWords = 32 * sizeof(TC) / 4;
         uint32_t o[kWords];
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
             if constexpr (sizeof(TC) == 4) o[i] = __float_as_uint(v[i]);
             else o[i] = pack2<TC>(v[2 * i], v[2 * i + 1]);
+        }
+        if (vec == 1) {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4)
+                __stcs(reinterpret_cast<uint4 *>(dst) + i / 4, make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+            return;
         }
 #pragma unroll
         for (int i = 0; i < kWords; i += 8)
