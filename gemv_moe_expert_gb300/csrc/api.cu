@@ -516,6 +516,20 @@ bool encode_matrix16(CUtensorMap *map, int dt, const void *base, int64_t inner, 
                      uint32_t box_outer) {
     return encode_operand(map, dt, base, inner, outer, 1, ld, 0, true, box_outer);
 }
+bool encode_store32(CUtensorMap *map, int dt, const void *base, int64_t cols, int64_t rows, int64_t ld) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    const int64_t size = dtype_size(dt);
+    if (!fn || !aligned(base, 16) || ld * size % 16 != 0) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * size)};
+    const cuuint32_t box[2] = {32u, 32u}, estr[2] = {1u, 1u};
+    const CUtensorMapDataType ty = dt == kF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dt == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return fn(map, ty, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              dt == kF32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace gbmm
 
 extern "C" {

@@ -188,6 +188,22 @@ __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// 2-D tiled bulk tensor store shared -> global of this thread's bulk group; the shared memory may be
+// written again once bulk_store_read() has let it go.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(src),
+                 "r"(c0), "r"(c1)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// all but the newest kOpen groups have read their shared memory
+template <int kOpen>
+__device__ __forceinline__ void bulk_store_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOpen) : "memory");
+}
+// every group is complete
+__device__ __forceinline__ void bulk_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // Programmatic dependent launch: a kernel launched with programmatic stream
 // serialisation may start while the kernel before it in the stream still
 // runs; griddepcontrol.wait blocks until that kernel has completed and its

@@ -2,8 +2,6 @@
 // (gbmm_gated*) and of the 8-bit integer product (gbmm_quantize_i8,
 // gbmm_gemm_i8): argument checks, all of them before the first launch, then
 // the choice of kernels.
-#include <algorithm>
-
 #include "api_checks.h"
 #include "kernel_params.h"
 
@@ -38,11 +36,6 @@ Operand matrix(const char *label, const void *p, uint64_t bytes, int64_t cols, i
 bool rows16(const void *p, int64_t ld_bytes) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld_bytes % 16 == 0;
 }
-// widest stores that rows allow: 2: 32 bytes, 1: 16
-int32_t row_stores(const void *p, int64_t ld_bytes) {
-    return reinterpret_cast<uintptr_t>(p) % 32 == 0 && ld_bytes % 32 == 0 ? 2 : rows16(p, ld_bytes) ? 1 : 0;
-}
-
 // Few rows run as dot products, a warp for each column or two; more run as tiles.
 constexpr int64_t kDotRows = 8;
 
@@ -67,14 +60,14 @@ gbmm_status lay_again(const char *fn, Laid *l, int64_t rows, int64_t cols, int64
 }
 
 // what the tensor-core products share
-bool pair_params(PairTcParams *p, void *c, int64_t ldc, int size, int64_t m, int64_t n, int64_t k) {
+bool pair_params(PairTcParams *p, PairTcMaps *maps, int dt, void *c, int64_t ldc, int64_t m, int64_t n, int64_t k) {
     *p = PairTcParams{};
     p->c = c;
     p->ldc = ldc;
     p->m = static_cast<int32_t>(m);
     p->n = static_cast<int32_t>(n);
     p->k = static_cast<int32_t>(k);
-    p->c_vec = row_stores(c, ldc * size);
+    p->c_tma = encode_store32(&maps->out[0], dt, c, n, m, ldc);
     p->err = device_error_word();
     p->wait_limit_ns = kWaitLimitNs;
     return p->err != nullptr;
@@ -152,10 +145,10 @@ gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n,
         if (st == GBMM_OK) st = lay_again(fn, &lg, n, k, ldw, scratch, s);
         if (st == GBMM_OK) st = lay_again(fn, &lu, n, k, ldw, scratch, s);
         if (st != GBMM_OK) return st;
-        PairTcMaps maps;
+        PairTcMaps maps{};
         PairTcParams q;
         const uint32_t rows = static_cast<uint32_t>(pair_tc_rows());
-        if (!pair_params(&q, h, ldh, 2, m, n, k) || !encode_matrix16(&maps.a[0], dt, lx.p, k, m, lx.ld, rows) ||
+        if (!pair_params(&q, &maps, dt, h, ldh, m, n, k) || !encode_matrix16(&maps.a[0], dt, lx.p, k, m, lx.ld, rows) ||
             !encode_matrix16(&maps.b[0], dt, lg.p, k, n, lg.ld, rows) ||
             !encode_matrix16(&maps.b[1], dt, lu.p, k, n, lu.ld, rows))
             return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
@@ -163,7 +156,8 @@ gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n,
         q.saved[0] = gate;
         q.saved[1] = up;
         q.ld_saved = ld_saved;
-        q.saved_vec = std::min(row_stores(gate, ld_saved * 2), row_stores(up, ld_saved * 2));
+        q.saved_tma = gate != nullptr && encode_store32(&maps.out[1], dt, gate, n, m, ld_saved) &&
+                      encode_store32(&maps.out[2], dt, up, n, m, ld_saved);
         q.act = static_cast<int32_t>(activation);
         return finish_launch(launch_gated_tc(dt, maps, q, device_sm_count(), s), fn, s);
     }
@@ -291,9 +285,9 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     if (st == GBMM_OK) st = finish_launch(launch_gated_grad(dt, g, s), fn, s);
     if (st != GBMM_OK) return st;
     if (need_x && dt != GBMM_F32) {
-        PairTcMaps maps;
+        PairTcMaps maps{};
         PairTcParams q;
-        bool ok = pair_params(&q, d_x, ld_dx, 2, m, k, n);
+        bool ok = pair_params(&q, &maps, dt, d_x, ld_dx, m, k, n);
         for (int i = 0; i < 2 && ok; ++i)
             ok = encode_matrix16(&maps.a[i], dt, g.d[i], n, m, ldd, static_cast<uint32_t>(pair_tc_rows())) &&
                  encode_matrix16(&maps.b[i], dt, lw[i].p, k, n, lw[i].ld, static_cast<uint32_t>(pair_tc_block_k()));
@@ -391,10 +385,10 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
     const int64_t ld = round_up(k, 8);
     char *const base = Parts::base(scratch);
     const RepackParams ra{a, base + parts.add(m, ld, 2), m, k, lda, ld}, rb{b, base + parts.add(n, ld, 2), n, k, ldb, ld};
-    PairTcMaps maps;
+    PairTcMaps maps{};
     PairTcParams q;
     const uint32_t rows = static_cast<uint32_t>(pair_tc_rows());
-    if (!pair_params(&q, c, ldc, static_cast<int>(size), m, n, k) ||
+    if (!pair_params(&q, &maps, dt, c, ldc, m, n, k) ||
         !encode_matrix16(&maps.a[0], GBMM_F16, ra.dst, k, m, ld, rows) ||
         !encode_matrix16(&maps.b[0], GBMM_F16, rb.dst, k, n, ld, rows))
         return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);

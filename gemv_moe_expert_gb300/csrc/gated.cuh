@@ -24,6 +24,27 @@ __device__ __forceinline__ float gate_act(int act, float v) {
     }
 }
 
+// The same for results of 16 bits: errors of a few 2^-22 relative to v.  The exponential and the
+// quotient are the hardware's approximations; erf is 7.1.26 of Abramowitz and Stegun (off by 1.5e-7 at most):
+// erfc(z) = t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) e^(-z z), t = 1 / (1 + 0.3275911 z), z >= 0.
+__device__ __forceinline__ float sigmoid_16(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+__device__ __forceinline__ float half_erfc_16(float z) {  // erfc(|z|) / 2
+    const float y = fabsf(z), t = __fdividef(1.f, fmaf(0.3275911f, y, 1.f));
+    const float q = fmaf(fmaf(fmaf(fmaf(1.061405429f, t, -1.453152027f), t, 1.421413741f), t, -0.284496736f), t, 0.254829592f);
+    return 0.5f * q * t * __expf(-y * y);
+}
+__device__ __forceinline__ float gate_act_16(int act, float v) {
+    switch (act) {
+    case GBMM_GATE_SILU: return v * sigmoid_16(v);
+    case GBMM_GATE_GELU: {
+        const float c = half_erfc_16(0.70710678118654752f * v);
+        return v * (v > 0.f ? 1.f - c : c);
+    }
+    case GBMM_GATE_GELU_TANH: return v * sigmoid_16(gelu_tanh_arg(v));
+    default: return fmaxf(v, 0.f) + (v != v ? v : 0.f);
+    }
+}
+
 // act(v), and its derivative (relu: 0 at 0)
 __device__ __forceinline__ float gate_act_slope(int act, float v, float *slope) {
     switch (act) {

@@ -225,7 +225,7 @@ struct PairTcParams {
     const float *scale_a, *scale_b;  // codes; null: 1
     int64_t ldc, ld_saved;
     int32_t m, n, k;                 // k: of one source
-    int32_t c_vec, saved_vec;        // rows allow 32-byte (2) or 16-byte (1) stores
+    int32_t c_tma, saved_tma;        // the output's maps may be used (its rows start on multiples of 16 bytes)
     int32_t act;
     int32_t tiles_m, tiles_n, num_tiles;  // set by the launcher
     uint32_t *err;
@@ -233,6 +233,7 @@ struct PairTcParams {
 };
 struct PairTcMaps {
     CUtensorMap a[2], b[2];
+    CUtensorMap out[3];  // c and both saved projections, as 32 x 32 pieces
 };
 
 // ---- launchers (each returns the launch's cudaError_t) --------------------

@@ -37,7 +37,9 @@ constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr uint32_t kStageBytes = 2 * kABytes;
 constexpr uint32_t kMNBox = 64 * kBK * 2;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSmemBytes = kStages * kStageBytes + 256 + 1024;
+constexpr uint32_t kOutBytes = 4096;  // of each epilogue warp
+constexpr uint32_t kSmemBytes = kStages * kStageBytes + kEpiWarps * kOutBytes + 256 + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
 constexpr int kExactBlocks = 1024 / kBK;  // k-blocks whose sum of products of two codes stays within 2^24
 
 enum Mode { kGated, kSum, kCodes };
@@ -81,48 +83,69 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// 32 consecutive outputs of a row: 32- (vec 2) or 16-byte (vec 1) stores, or the first `left` one by one
+// A warp's way out for 32 x 32 outputs, one row a lane: through shared memory (swizzled, so that no two
+// lanes meet in a bank) and one TMA store, which writes whole row segments and leaves what is outside the matrix
+// alone; rows that TMA cannot write element by element.  Direct 32-byte stores, every lane its own row, held a warp for
+// about 700 cycles each.
 template <typename TC>
-__device__ __forceinline__ void store32(TC *dst, const float (&v)[32], int vec, int64_t left) {
-    if (vec != 0 && left >= 32) {
-        constexpr int kWords = 32 * sizeof(TC) / 4;
-        uint32_t o[kWords];
+struct Writer {
+    static constexpr int kBufs = sizeof(TC) == 4 ? 1 : 2;
+    uint32_t base;  // 4 KB of shared memory
+    int next = 0;
+
+    __device__ __forceinline__ void write(const float (&v)[32], const CUtensorMap *map, bool tma, TC *c, int64_t ld,
+                                          int64_t row0, int64_t col, int64_t m, int64_t n, int lane) {
+        if (row0 >= m || col >= n) return;
+        if (!tma) {
+            if (row0 + lane >= m) return;
+            TC *dst = c + (row0 + lane) * ld + col;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            if constexpr (sizeof(TC) == 4) o[i] = __float_as_uint(v[i]);
-            else o[i] = pack2<TC>(v[2 * i], v[2 * i + 1]);
-        }
-        if (vec == 1) {
-#pragma unroll
-            for (int i = 0; i < kWords; i += 4)
-                __stcs(reinterpret_cast<uint4 *>(dst) + i / 4, make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+            for (int i = 0; i < 32; ++i)
+                if (col + i < n) dst[i] = Elem<TC>::from_f(v[i]);
             return;
         }
+        const uint32_t buf = base + static_cast<uint32_t>(next) * (4096 / kBufs);
+        next = (next + 1) % kBufs;
+        if (lane == 0) bulk_store_read<kBufs - 1>();
+        __syncwarp();
+        constexpr int kPieces = 32 * sizeof(TC) / 16;
 #pragma unroll
-        for (int i = 0; i < kWords; i += 8)
-            asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                             reinterpret_cast<uint32_t *>(dst) + i),
-                         "r"(o[i]), "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]),
-                         "r"(o[i + 6]), "r"(o[i + 7])
+        for (int i = 0; i < kPieces; ++i) {
+            uint32_t w[4];
+            if constexpr (sizeof(TC) == 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[4 * i + e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = pack2<TC>(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
+            }
+            const uint32_t at = sizeof(TC) == 4 ? lane * 128 + ((i ^ (lane & 7)) << 4)
+                                                : lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                         "r"(w[3])
                          : "memory");
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < left) dst[i] = Elem<TC>::from_f(v[i]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(map, buf, static_cast<int32_t>(col), static_cast<int32_t>(row0));
+            bulk_commit();
+        }
     }
-}
+    __device__ __forceinline__ void finish(int lane) const {
+        if (lane == 0) bulk_store_done();
+    }
+};
 
 template <int kAct>
 __device__ __forceinline__ void gate32(const uint32_t (&g)[32], const uint32_t (&u)[32], float (&h)[32]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) h[i] = gate_act(kAct, __uint_as_float(g[i])) * __uint_as_float(u[i]);
+    for (int i = 0; i < 32; ++i) h[i] = gate_act_16(kAct, __uint_as_float(g[i])) * __uint_as_float(u[i]);
 }
 
 template <typename TC, uint32_t kFmt, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
-pair_tc_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ CUtensorMap map_a1,
-               const __grid_constant__ CUtensorMap map_b0, const __grid_constant__ CUtensorMap map_b1,
-               const PairTcParams p) {
+pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
     constexpr int kTileN = Shape<kMode>::kTileN;
     constexpr bool kBMN = kMode == kSum;  // B stored [k, n]
     extern __shared__ uint8_t smem_raw[];
@@ -130,7 +153,7 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
     uint8_t *smem = smem_raw + pad;
     const uint32_t s0 = raw_addr + pad;  // stage s: A at s0 + s * kStageBytes, B kABytes after it
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes + kEpiWarps * kOutBytes);
     const uint32_t bar0 = smem_addr(bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
@@ -160,10 +183,10 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&map_a0);
-        tma_prefetch_desc(&map_b0);
-        if (kMode != kCodes) tma_prefetch_desc(&map_b1);
-        if (kMode == kSum) tma_prefetch_desc(&map_a1);
+        tma_prefetch_desc(&maps.a[0]);
+        tma_prefetch_desc(&maps.b[0]);
+        if (kMode != kCodes) tma_prefetch_desc(&maps.b[1]);
+        if (kMode == kSum) tma_prefetch_desc(&maps.a[1]);
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_addr(tmem_slot), kTmemCols);
@@ -217,13 +240,13 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant
                     const uint32_t fb = mapa_shared(full_bar(stage), 0);
                     const bool second = kMode == kSum && kb >= blocks1;
                     const int k0 = (second ? kb - blocks1 : kb) * kBK;
-                    tma_load_3d_pair(sa, second ? &map_a1 : &map_a0, fb, k0, arow, 0);
+                    tma_load_3d_pair(sa, second ? &maps.a[1] : &maps.a[0], fb, k0, arow, 0);
                     if (kBMN) {
-                        const CUtensorMap *mb = second ? &map_b1 : &map_b0;
+                        const CUtensorMap *mb = second ? &maps.b[1] : &maps.b[0];
                         tma_load_3d_pair(sb, mb, fb, brow, k0, 0);
                         tma_load_3d_pair(sb + kMNBox, mb, fb, brow + 64, k0, 0);
                     } else {
-                        tma_load_3d_pair(sb, kMode == kGated && !leader ? &map_b1 : &map_b0, fb, k0, brow, 0);
+                        tma_load_3d_pair(sb, kMode == kGated && !leader ? &maps.b[1] : &maps.b[0], fb, k0, brow, 0);
                     }
                     if (++stage == kStages) {
                         stage = 0;
@@ -299,15 +322,24 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant
         uint32_t tphase[2] = {0u, 0u};
         int local = 0;
         bool ok = true;
+        Writer<TC> out;
+        out.base = s0 + kStages * kStageBytes + static_cast<uint32_t>(warp - 2) * kOutBytes;
         for (int u = cl; u < num_units && ok; u += ncl) {
             const Unit t = decode(u, split_from, kTileN, p);
             if (t.halves == 0) continue;
-            const int64_t row = static_cast<int64_t>(t.mb) * 2 * kBM + static_cast<int64_t>(rank) * kBM + quarter * 32 +
-                                lane;
+            const int64_t row0 = static_cast<int64_t>(t.mb) * 2 * kBM + static_cast<int64_t>(rank) * kBM + quarter * 32;
             const int width = t.halves * (kTileN / 2);  // outputs across this unit
             const int mine = width / 2;                 // and this warp's share of them
             const int64_t col0 = static_cast<int64_t>(t.nb) * kTileN + t.h * (kTileN / 2) + side * mine;
-            TC *crow = static_cast<TC *>(p.c) + row * p.ldc;
+            TC *const c = static_cast<TC *>(p.c);
+            // codes: scales of this lane's row and of column lane of each 32
+            float sa = 1.f, sb[kMode == kCodes ? 4 : 1];
+            if constexpr (kMode == kCodes) {
+                if (p.scale_a != nullptr && row0 + lane < p.m) sa = __ldg(p.scale_a + row0 + lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sb[i] = p.scale_b != nullptr && col0 + 32 * i + lane < p.n ? __ldg(p.scale_b + col0 + 32 * i + lane) : 1.f;
+            }
             int sum[kMode == kCodes ? kBN / 2 : 1];
             if constexpr (kMode == kCodes) {
 #pragma unroll
@@ -344,7 +376,6 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant
                         float v[32];
                         tmem_ld32(t_addr + i, r);
                         const int64_t col = col0 + i;
-                        const bool live = row < p.m && col < p.n;
                         if constexpr (kMode == kGated) {
                             uint32_t q[32];
                             tmem_ld32(t_addr + width + i, q);
@@ -355,21 +386,22 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant
                             case GBMM_GATE_GELU_TANH: gate32<GBMM_GATE_GELU_TANH>(r, q, v); break;
                             default: gate32<GBMM_GATE_RELU>(r, q, v);
                             }
-                            if (live) store32<TC>(crow + col, v, p.c_vec, p.n - col);
-                            if (p.saved[0] != nullptr && live) {
-                                const int64_t at = row * p.ld_saved + col;
+                            out.write(v, &maps.out[0], p.c_tma, c, p.ldc, row0, col, p.m, p.n, lane);
+                            if (p.saved[0] != nullptr) {
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
-                                store32<TC>(static_cast<TC *>(p.saved[0]) + at, v, p.saved_vec, p.n - col);
+                                out.write(v, &maps.out[1], p.saved_tma, static_cast<TC *>(p.saved[0]), p.ld_saved, row0,
+                                          col, p.m, p.n, lane);
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(q[e]);
-                                store32<TC>(static_cast<TC *>(p.saved[1]) + at, v, p.saved_vec, p.n - col);
+                                out.write(v, &maps.out[2], p.saved_tma, static_cast<TC *>(p.saved[1]), p.ld_saved, row0,
+                                          col, p.m, p.n, lane);
                             }
                         } else {
                             tmem_ld_wait();
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
-                            if (live) store32<TC>(crow + col, v, p.c_vec, p.n - col);
+                            out.write(v, &maps.out[0], p.c_tma, c, p.ldc, row0, col, p.m, p.n, lane);
                         }
                     }
                 }
@@ -380,23 +412,20 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant
                 tphase[a] ^= 1u;
             }
             if constexpr (kMode == kCodes) {
-                if (ok && row < p.m) {
-                    const float sa = p.scale_a != nullptr ? p.scale_a[row] : 1.f;
+                if (ok) {
 #pragma unroll
                     for (int i = 0; i < kBN / 2; i += 32) {
-                        const int64_t col = col0 + i;
-                        if (i >= mine || col >= p.n) break;
+                        if (i >= mine) break;
                         float v[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float sb = p.scale_b != nullptr ? __ldg(p.scale_b + min(col + e, p.n - int64_t{1})) : 1.f;
-                            v[e] = static_cast<float>(sum[i + e]) * sa * sb;
-                        }
-                        store32<TC>(crow + col, v, p.c_vec, p.n - col);
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = static_cast<float>(sum[i + e]) * sa * __shfl_sync(0xffffffffu, sb[i / 32], e);
+                        out.write(v, &maps.out[0], p.c_tma, c, p.ldc, row0, col0 + i, p.m, p.n, lane);
                     }
                 }
             }
         }
+        out.finish(lane);
     }
 
     tc_fence_before();
@@ -445,7 +474,7 @@ cudaError_t pair_t(const PairTcMaps &maps, PairTcParams p, int num_sms, cudaStre
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, pair_tc_kernel<TC, kFmt, kMode>, maps.a[0], maps.a[1], maps.b[0], maps.b[1], p);
+    return cudaLaunchKernelEx(&cfg, pair_tc_kernel<TC, kFmt, kMode>, maps, p);
 }
 
 }  // namespace
