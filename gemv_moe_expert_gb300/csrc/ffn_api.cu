@@ -272,8 +272,14 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     g.gate = gate;
     g.up = up;
     g.d_h = d_h;
-    g.d[0] = base + d_at[0];
-    g.d[1] = base + d_at[1];
+    // both gradients of the weights are one batch where one lies whole behind the other; the projections' gradients lie
+    // in the same order then
+    const intptr_t gap = reinterpret_cast<intptr_t>(d_w_up) - reinterpret_cast<intptr_t>(d_w_gate);
+    const bool batched = dt != GBMM_F32 && need_w && static_cast<uint64_t>(gap < 0 ? -gap : gap) >= dwb;
+    const int first = batched && gap < 0 ? 1 : 0;
+    const int64_t d_apart = static_cast<int64_t>(d_at[1] - d_at[0]) / static_cast<int64_t>(size);
+    g.d[first] = base + d_at[0];
+    g.d[!first] = base + d_at[1];
     g.m = m;
     g.n = n;
     g.ld_saved = ld_saved;
@@ -284,7 +290,13 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     for (int i = 0; i < 2 && st == GBMM_OK; ++i) st = lay_again(fn, &lw[i], n, k, ldw, scratch, s);
     if (st == GBMM_OK) st = finish_launch(launch_gated_grad(dt, g, s), fn, s);
     if (st != GBMM_OK) return st;
-    if (need_x && dt != GBMM_F32) {
+    void *const dw[2] = {d_w_gate, d_w_up};
+    if (dt == GBMM_F32) {
+        const SumGemmParams px{{g.d[0], g.d[1]}, {w_gate, w_up}, d_x, m, k, n, ldd, ldw, ld_dx};
+        const OuterGemmParams pw{x, {g.d[0], g.d[1]}, {dw[0], dw[1]}, m, n, k, ldx, ldd, ld_dw};
+        return finish_launch(launch_gated_products_simt(need_x ? &px : nullptr, need_w ? &pw : nullptr, s), fn, s);
+    }
+    if (need_x) {
         PairTcMaps maps{};
         PairTcParams q;
         bool ok = pair_params(&q, &maps, dt, d_x, ld_dx, m, k, n);
@@ -293,15 +305,15 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
                  encode_matrix16(&maps.b[i], dt, lw[i].p, k, n, lw[i].ld, static_cast<uint32_t>(pair_tc_block_k()));
         if (!ok) return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
         st = finish_launch(launch_sum_gemm_tc(dt, maps, q, device_sm_count(), s), fn, s);
-    } else if (need_x) {
-        const SumGemmParams q{{g.d[0], g.d[1]}, {w_gate, w_up}, d_x, m, k, n, ldd, ldw, ld_dx};
-        st = finish_launch(launch_sum_gemm_simt(dt, q, s), fn, s);
     }
-    if (need_w) {
-        void *const dw[2] = {d_w_gate, d_w_up};
-        for (int i = 0; i < 2 && st == GBMM_OK; ++i)
-            st = gbmm_gemm(dt, 1, n, k, m, 1, 0, g.d[i], 0, ldd, 0, lx.p, 0, lx.ld, 0, dw[i], 0, ld_dw, 0, stream);
+    if (st != GBMM_OK || !need_w) return st;
+    if (batched) {  // one product over both projections: more tiles in a launch
+        const int64_t apart = (reinterpret_cast<intptr_t>(dw[!first]) - reinterpret_cast<intptr_t>(dw[first])) / 2;
+        return gbmm_gemm(dt, 2, n, k, m, 1, 0, g.d[first], 0, ldd, d_apart, lx.p, 0, lx.ld, 0, dw[first], 0, ld_dw,
+                         apart, stream);
     }
+    for (int i = 0; i < 2 && st == GBMM_OK; ++i)
+        st = gbmm_gemm(dt, 1, n, k, m, 1, 0, g.d[i], 0, ldd, 0, lx.p, 0, lx.ld, 0, dw[i], 0, ld_dw, 0, stream);
     return st;
 }
 

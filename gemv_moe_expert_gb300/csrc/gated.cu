@@ -3,7 +3,11 @@
 //
 // Every kernel here takes any strides and alignment; the tensor-core forms are
 // chosen by the entry points (ffn_api.cu) where types and layouts allow.
+#include <cooperative_groups.h>
+
 #include "gated.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace gbmm {
 
@@ -176,12 +180,18 @@ cudaError_t rowdot_t(const GatedParams &p, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// FFMA tiles: two products in one pass.  kSum == false: c0 = a b0^T and c1 = a b1^T, b [n, k]
-// (the gated projection, two accumulators); kSum == true: c = a0 b0 + a1 b1, b [k, n] (the
-// gradient of x, one accumulator, the contraction over both sources).  16 kTM x 16 kTN tiles,
-// kTM x kTN outputs a thread and product, 16 deep, the next step's loads in registers while the
-// current one is multiplied.
+// FFMA tiles: two products in one pass.
+//   kGated  c0 = a b0^T, c1 = a b1^T    a [m, k], b [n, k]    the gated projection; two accumulators
+//   kSum    c = a0 b0 + a1 b1           a [m, k], b [k, n]    the gradient of x; one accumulator, the contraction
+//                                                             runs over the first source and then the second
+//   kOuter  c0 = b0^T a, c1 = b1^T a    a [k, m], b [k, n]    the weights' gradients; two accumulators, rows of c
+//                                                             along n
+// 16 kTM x 16 kTN tiles, kTM x kTN outputs a thread and product, 16 deep, the next step's loads in registers while the
+// current one is multiplied.  Two neighbouring outputs share an instruction (fma.rn.f32x2), which leaves issue slots
+// for the shared-memory reads.
 // ---------------------------------------------------------------------------
+
+enum TileMode { kGated, kSum, kOuter };
 
 struct TileArgs {
     const void *a[2], *b[2];
@@ -192,77 +202,58 @@ struct TileArgs {
 
 constexpr int kTK = 16;
 
-template <typename T, bool kSum, int kTM, int kTN>
+__device__ __forceinline__ uint64_t both(float v) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(v));
+    return d;
+}
+__device__ __forceinline__ void fma2(uint64_t &acc, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ float half_of(uint64_t v, int i) {
+    return __uint_as_float(static_cast<uint32_t>(i == 0 ? v : v >> 32));
+}
+
+template <typename T, int kMode, int kTM, int kTN>
 struct TileProduct {
-    static constexpr int kBM = 16 * kTM, kBN = 16 * kTN, kProducts = kSum ? 1 : 2;
+    static constexpr int kBM = 16 * kTM, kBN = 16 * kTN, kProducts = kMode == kSum ? 1 : 2;
+    // operands whose rows run along k are transposed on their way into shared memory
+    static constexpr bool kAK = kMode != kOuter, kBK = kMode == kGated;
     static constexpr int kAPieces = kBM * kTK / 4, kBPieces = kBN * kTK / 4;
     static constexpr int kA = (kAPieces + 255) / 256, kB = (kBPieces + 255) / 256;
     struct Smem {
         float a[2][kTK][kBM + 4];
         float b[2][kProducts][kTK][kBN + 4];
     };
-    float acc[kProducts][kTM][kTN];
+    uint64_t acc[kProducts][kTM][kTN / 2];
 
-    __device__ __forceinline__ void run(const TileArgs &t, int64_t m0, int64_t n0, Smem &sm) {
-        const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    __device__ __forceinline__ float at(int pr, int r, int c) const { return half_of(acc[pr][r][c / 2], c & 1); }
+
+    // first, count: which of the sources (kSum)
+    __device__ __forceinline__ void run(const TileArgs &t, int64_t m0, int64_t n0, Smem &sm, int first = 0,
+                                        int count = kMode == kSum ? 2 : 1) {
+        const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
         for (int q = 0; q < kProducts; ++q)
 #pragma unroll
             for (int r = 0; r < kTM; ++r)
 #pragma unroll
-                for (int c = 0; c < kTN; ++c) acc[q][r][c] = 0.f;
+                for (int c = 0; c < kTN / 2; ++c) acc[q][r][c] = 0;
         float ra[kA][4], rb[kProducts][kB][4];
-        const int64_t steps1 = (t.k + kTK - 1) / kTK, steps = kSum ? 2 * steps1 : steps1;
+        const int64_t steps1 = (t.k + kTK - 1) / kTK, steps = count * steps1;
         auto load = [&](int64_t step) {
-            const int src = kSum && step >= steps1 ? 1 : 0;
-            const int64_t k0 = (step - src * steps1) * kTK;
-            const T *A = static_cast<const T *>(t.a[src]);
-#pragma unroll
-            for (int e = 0; e < kA; ++e) {  // piece: row q / 4, k 4 (q % 4)
-                const int q = tid + 256 * e;
-                const int64_t i = m0 + q / 4, x = k0 + 4 * (q % 4);
-                const bool ok = (kAPieces % 256 == 0 || q < kAPieces) && i < t.m && x < t.k;
-                load_part(A + i * t.lda + x, ok, t.a_vec, t.k - x, ra[e]);
-            }
-#pragma unroll
-            for (int pr = 0; pr < kProducts; ++pr) {
-                const T *B = static_cast<const T *>(t.b[kSum ? src : pr]);
-#pragma unroll
-                for (int e = 0; e < kB; ++e) {
-                    const int q = tid + 256 * e;
-                    const bool in = kBPieces % 256 == 0 || q < kBPieces;
-                    if (kSum) {  // piece: k q / (kBN / 4), columns 4 (q % (kBN / 4))
-                        const int64_t y = k0 + q / (kBN / 4), j = n0 + 4 * (q % (kBN / 4));
-                        load_part(B + y * t.ldb + j, in && y < t.k && j < t.n, t.b_vec, t.n - j, rb[pr][e]);
-                    } else {     // piece: column q / 4, k 4 (q % 4)
-                        const int64_t j = n0 + q / 4, x = k0 + 4 * (q % 4);
-                        load_part(B + j * t.ldb + x, in && j < t.n && x < t.k, t.b_vec, t.k - x, rb[pr][e]);
-                    }
-                }
-            }
-        };
-        auto store = [&](int buf) {
-#pragma unroll
-            for (int e = 0; e < kA; ++e) {
-                const int q = tid + 256 * e;
-                if (kAPieces % 256 == 0 || q < kAPieces)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) sm.a[buf][4 * (q % 4) + c][q / 4] = ra[e][c];
-            }
+            const int64_t k0 = (step >= steps1 ? step - steps1 : step) * kTK;
+            const int src = kMode == kSum ? first + (step >= steps1 ? 1 : 0) : 0;
+            load_tile<kAK, kBM, kA>(static_cast<const T *>(src ? t.a[1] : t.a[0]), t.lda, m0, t.m, k0, t.k, t.a_vec, ra);
 #pragma unroll
             for (int pr = 0; pr < kProducts; ++pr)
+                load_tile<kBK, kBN, kB>(static_cast<const T *>((kMode == kSum ? src : pr) ? t.b[1] : t.b[0]), t.ldb, n0, t.n, k0, t.k,
+                                        t.b_vec, rb[pr]);
+        };
+        auto store = [&](int buf) {
+            store_tile<kAK, kBM, kA>(sm.a[buf], ra);
 #pragma unroll
-                for (int e = 0; e < kB; ++e) {
-                    const int q = tid + 256 * e;
-                    if (kBPieces % 256 != 0 && q >= kBPieces) continue;
-                    if (kSum) {
-                        *reinterpret_cast<float4 *>(&sm.b[buf][pr][q / (kBN / 4)][4 * (q % (kBN / 4))]) =
-                            make_float4(rb[pr][e][0], rb[pr][e][1], rb[pr][e][2], rb[pr][e][3]);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) sm.b[buf][pr][4 * (q % 4) + c][q / 4] = rb[pr][e][c];
-                    }
-                }
+            for (int pr = 0; pr < kProducts; ++pr) store_tile<kBK, kBN, kB>(sm.b[buf][pr], rb[pr]);
         };
         if (steps > 0) {
             load(0);
@@ -273,18 +264,21 @@ struct TileProduct {
         for (int64_t step = 0; step < steps; ++step) {
             const bool more = step + 1 < steps;
             if (more) load(step + 1);
+            // the next k's values are read while this one's are multiplied
+            float av[2][kTM];
+            uint64_t bv[2][kProducts][kTN / 2];
+            fetch(sm, cur, 0, ty, tx, av[0], bv[0]);
 #pragma unroll
             for (int kk = 0; kk < kTK; ++kk) {
-                float av[kTM], bv[kProducts][kTN];
-                fetch<kTM>(sm.a[cur][kk], ty, av);
+                if (kk + 1 < kTK) fetch(sm, cur, kk + 1, ty, tx, av[(kk + 1) & 1], bv[(kk + 1) & 1]);
 #pragma unroll
-                for (int pr = 0; pr < kProducts; ++pr) fetch<kTN>(sm.b[cur][pr][kk], tx, bv[pr]);
+                for (int r = 0; r < kTM; ++r) {
+                    const uint64_t a2 = both(av[kk & 1][r]);
 #pragma unroll
-                for (int pr = 0; pr < kProducts; ++pr)
+                    for (int pr = 0; pr < kProducts; ++pr)
 #pragma unroll
-                    for (int r = 0; r < kTM; ++r)
-#pragma unroll
-                        for (int c = 0; c < kTN; ++c) acc[pr][r][c] = fmaf(av[r], bv[pr][c], acc[pr][r][c]);
+                        for (int c = 0; c < kTN / 2; ++c) fma2(acc[pr][r][c], a2, bv[kk & 1][pr][c]);
+                }
             }
             if (more) store(cur ^ 1);
             __syncthreads();
@@ -292,21 +286,52 @@ struct TileProduct {
         }
     }
 
-    // thread t's outputs of a dimension: kN == 2: 2t..; 4: 4t..; 8: 4t.. and 64 + 4t..
-    template <int kN>
-    static __device__ __forceinline__ int place(int t, int i) {
-        return kN == 2 ? 2 * t + i : (i < 4 ? 4 * t + i : 60 + 4 * t + i);
-    }
-    template <int kN>
-    static __device__ __forceinline__ void fetch(const float *row, int t, float (&v)[kN]) {
-        if constexpr (kN == 2) {
-            const float2 f = *reinterpret_cast<const float2 *>(row + 2 * t);
-            v[0] = f.x, v[1] = f.y;
-        } else {
+    static __device__ __forceinline__ void fetch(const Smem &sm, int cur, int kk, int ty, int tx, float (&av)[kTM],
+                                                 uint64_t (&bv)[kProducts][kTN / 2]) {
 #pragma unroll
-            for (int h = 0; h < kN / 4; ++h) {
-                const float4 f = *reinterpret_cast<const float4 *>(row + 64 * h + 4 * t);
-                v[4 * h] = f.x, v[4 * h + 1] = f.y, v[4 * h + 2] = f.z, v[4 * h + 3] = f.w;
+        for (int h = 0; h < kTM / 4; ++h) {
+            const float4 f = *reinterpret_cast<const float4 *>(&sm.a[cur][kk][64 * h + 4 * ty]);
+            av[4 * h] = f.x, av[4 * h + 1] = f.y, av[4 * h + 2] = f.z, av[4 * h + 3] = f.w;
+        }
+#pragma unroll
+        for (int pr = 0; pr < kProducts; ++pr)
+#pragma unroll
+            for (int h = 0; h < kTN / 4; ++h) {
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(&sm.b[cur][pr][kk][64 * h + 4 * tx]);
+                bv[pr][2 * h] = f.x, bv[pr][2 * h + 1] = f.y;
+            }
+    }
+
+    // where output i of thread t lies in its dimension: 4 t .., and 64 + 4 t .. from the fifth on
+    static __device__ __forceinline__ int place(int t, int i) { return i < 4 ? 4 * t + i : 60 + 4 * t + i; }
+
+    // Pieces of four elements along the rows: K-major (rows of kLong along k) piece q is row q / 4, k 4 (q % 4); else
+    // k q / (kLong / 4), places 4 (q % (kLong / 4)).
+    template <bool kKMajor, int kLong, int kPieces>
+    static __device__ __forceinline__ void load_tile(const T *src, int64_t ld, int64_t o0, int64_t o_end, int64_t k0,
+                                                     int64_t k_end, bool vec, float (&v)[kPieces][4]) {
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e) {
+            const int q = threadIdx.x + 256 * e;
+            const bool in = kLong * kTK / 4 % 256 == 0 || q < kLong * kTK / 4;
+            const int64_t o = o0 + (kKMajor ? q / 4 : 4 * (q % (kLong / 4)));
+            const int64_t x = k0 + (kKMajor ? 4 * (q % 4) : q / (kLong / 4));
+            load_part(src + (kKMajor ? o * ld + x : x * ld + o), in && o < o_end && x < k_end, vec,
+                      kKMajor ? k_end - x : o_end - o, v[e]);
+        }
+    }
+    template <bool kKMajor, int kLong, int kPieces>
+    static __device__ __forceinline__ void store_tile(float (&dst)[kTK][kLong + 4], const float (&v)[kPieces][4]) {
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e) {
+            const int q = threadIdx.x + 256 * e;
+            if (kLong * kTK / 4 % 256 != 0 && q >= kLong * kTK / 4) continue;
+            if (kKMajor) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) dst[4 * (q % 4) + c][q / 4] = v[e][c];
+            } else {
+                *reinterpret_cast<float4 *>(&dst[q / (kLong / 4)][4 * (q % (kLong / 4))]) =
+                    make_float4(v[e][0], v[e][1], v[e][2], v[e][3]);
             }
         }
     }
@@ -332,7 +357,7 @@ struct TileProduct {
 
 template <typename T, int kTM, int kTN>
 __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const TileArgs t, const GatedParams p) {
-    using Tile = TileProduct<T, false, kTM, kTN>;
+    using Tile = TileProduct<T, kGated, kTM, kTN>;
     __shared__ __align__(16) typename Tile::Smem sm;
     Tile tile;
     const int64_t m0 = blockIdx.x / t.tiles_n * Tile::kBM, n0 = blockIdx.x % t.tiles_n * Tile::kBN;
@@ -340,13 +365,13 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const TileArgs t, co
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
     for (int r = 0; r < kTM; ++r) {
-        const int64_t i = m0 + Tile::template place<kTM>(ty, r);
+        const int64_t i = m0 + Tile::place(ty, r);
         if (i >= p.m) continue;
 #pragma unroll
         for (int c = 0; c < kTN; ++c) {
-            const int64_t j = n0 + Tile::template place<kTN>(tx, c);
+            const int64_t j = n0 + Tile::place(tx, c);
             if (j >= p.n) continue;
-            const float g = tile.acc[0][r][c], u = tile.acc[1][r][c];
+            const float g = tile.at(0, r, c), u = tile.at(1, r, c);
             static_cast<T *>(p.h)[i * p.ldh + j] = Elem<T>::from_f(gate_act(p.act, g) * u);
             if (p.saved[0] != nullptr) {
                 static_cast<T *>(p.saved[0])[i * p.ld_saved + j] = Elem<T>::from_f(g);
@@ -356,24 +381,118 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const TileArgs t, co
     }
 }
 
-template <typename T, int kTM, int kTN>
-__global__ void __launch_bounds__(256, 2) sum_gemm_simt_kernel(const TileArgs t, T *c_out, int64_t ldc) {
-    using Tile = TileProduct<T, true, kTM, kTN>;
-    __shared__ __align__(16) typename Tile::Smem sm;
+// One tile of the gradient of x.  kSplit: a cluster of two CTAs a tile, one source each; the odd one's sums go to the even
+// one through shared memory, two rows a thread at a time.
+template <int kTM, int kTN, bool kSplit>
+__device__ __forceinline__ void sum_tile(const TileArgs &t, float *out, int64_t ldc, int64_t block,
+                                         typename TileProduct<float, kSum, kTM, kTN>::Smem &sm) {
+    using Tile = TileProduct<float, kSum, kTM, kTN>;
     Tile tile;
-    const int64_t m0 = blockIdx.x / t.tiles_n * Tile::kBM, n0 = blockIdx.x % t.tiles_n * Tile::kBN;
-    tile.run(t, m0, n0, sm);
+    if (kSplit) block >>= 1;
+    const int64_t m0 = block / t.tiles_n * Tile::kBM, n0 = block % t.tiles_n * Tile::kBN;
+    if constexpr (kSplit) {
+        cg::cluster_group pair = cg::this_cluster();
+        const int rank = blockIdx.x & 1;
+        tile.run(t, m0, n0, sm, rank, 1);
+        uint64_t *mine = reinterpret_cast<uint64_t *>(&sm), *other = pair.map_shared_rank(mine, 1);
+        static_assert(256 * 2 * (kTN / 2) * sizeof(uint64_t) <= sizeof(sm), "two rows a thread");
+#pragma unroll
+        for (int r = 0; r < kTM; r += 2) {
+            if (rank == 1)
+#pragma unroll
+                for (int e = 0; e < kTN; ++e) mine[e * 256 + threadIdx.x] = tile.acc[0][r + e / (kTN / 2)][e % (kTN / 2)];
+            pair.sync();
+            if (rank == 0)
+#pragma unroll
+                for (int e = 0; e < kTN; ++e) {
+                    uint64_t &v = tile.acc[0][r + e / (kTN / 2)][e % (kTN / 2)];
+                    const uint64_t w = other[e * 256 + threadIdx.x];
+                    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
+                }
+            pair.sync();
+        }
+        if (rank == 1) return;
+    } else {
+        tile.run(t, m0, n0, sm);
+    }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
     for (int r = 0; r < kTM; ++r) {
-        const int64_t i = m0 + Tile::template place<kTM>(ty, r);
+        const int64_t i = m0 + Tile::place(ty, r);
         if (i >= t.m) continue;
 #pragma unroll
         for (int c = 0; c < kTN; ++c) {
-            const int64_t j = n0 + Tile::template place<kTN>(tx, c);
-            if (j < t.n) c_out[i * ldc + j] = Elem<T>::from_f(tile.acc[0][r][c]);
+            const int64_t j = n0 + Tile::place(tx, c);
+            if (j < t.n) out[i * ldc + j] = tile.at(0, r, c);
         }
     }
+}
+
+// One tile of the gradients of the weights; here t.m runs along the columns of the outputs and t.n along their rows.
+struct OuterOut {
+    float *c[2];
+    int64_t ldc;
+    int32_t vec;
+};
+template <int kTM, int kTN>
+__device__ __forceinline__ void outer_tile(const TileArgs &t, const OuterOut &o, int64_t block,
+                                           typename TileProduct<float, kOuter, kTM, kTN>::Smem &sm) {
+    using Tile = TileProduct<float, kOuter, kTM, kTN>;
+    Tile tile;
+    const int64_t m0 = block / t.tiles_n * Tile::kBM, n0 = block % t.tiles_n * Tile::kBN;
+    tile.run(t, m0, n0, sm);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+        for (int c = 0; c < kTN; ++c) {
+            const int64_t row = n0 + Tile::place(tx, c);
+            if (row >= t.n) continue;
+            float *dst = (pr == 0 ? o.c[0] : o.c[1]) + row * o.ldc;
+#pragma unroll
+            for (int h = 0; h < kTM; h += 4) {
+                const int64_t col = m0 + Tile::place(ty, h);
+                if (o.vec && col + 4 <= t.m) {
+                    *reinterpret_cast<float4 *>(dst + col) = make_float4(tile.at(pr, h, c), tile.at(pr, h + 1, c),
+                                                                         tile.at(pr, h + 2, c), tile.at(pr, h + 3, c));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < t.m) dst[col + e] = tile.at(pr, h + e, c);
+                }
+            }
+        }
+}
+
+template <int kTM, int kTN>
+__global__ void __launch_bounds__(256, 2) sum_gemm_simt_kernel(const TileArgs t, float *out, int64_t ldc) {
+    __shared__ __align__(16) typename TileProduct<float, kSum, kTM, kTN>::Smem sm;
+    sum_tile<kTM, kTN, false>(t, out, ldc, blockIdx.x, sm);
+}
+template <int kTM, int kTN>
+__global__ void __launch_bounds__(256, 2) outer_gemm_simt_kernel(const TileArgs t, const OuterOut o) {
+    __shared__ __align__(16) typename TileProduct<float, kOuter, kTM, kTN>::Smem sm;
+    outer_tile<kTM, kTN>(t, o, blockIdx.x, sm);
+}
+// Both gradients in one grid, so that the tiles of one fill the last round of the other's: clusters of two,
+// the first x_blocks of them the gradient of x (the longer tiles), a pair a tile.
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 2)
+both_gemm_simt_kernel(const TileArgs tx, float *out, int64_t ldc, unsigned x_blocks, const TileArgs tw, const OuterOut o,
+                      unsigned w_blocks) {
+    __shared__ __align__(16) union {
+        typename TileProduct<float, kSum, 8, 8>::Smem x;
+        typename TileProduct<float, kOuter, 8, 4>::Smem w;
+    } sm;
+    if (blockIdx.x < x_blocks) sum_tile<8, 8, true>(tx, out, ldc, blockIdx.x, sm.x);
+    else if (blockIdx.x - x_blocks < w_blocks) outer_tile<8, 4>(tw, o, blockIdx.x - x_blocks, sm.w);
+}
+
+// Not started early behind the kernel before it: blocks that take places as they come free gather on a few SMs, and a
+// grid of about one block an SM then takes twice as long (512 x 1408 x 2048 gradients: 412 against 300 us).
+template <typename... Params, typename... Args>
+cudaError_t launch_whole(void (*kernel)(Params...), unsigned blocks, cudaStream_t s, const Args &...args) {
+    kernel<<<blocks, 256, 0, s>>>(args...);
+    return cudaGetLastError();
 }
 
 bool groups_of_4(const void *p, int64_t ld, size_t size) {
@@ -387,36 +506,25 @@ unsigned tile_grid(int64_t m, int64_t n, int bm, int bn, TileArgs *t) {
     return blocks > INT32_MAX ? 0 : static_cast<unsigned>(blocks);
 }
 
+// Whether the larger of two tiles is taken.  A tile's time goes by its reads of shared memory, one cycle for each 4
+// bytes a thread reads: 16 a step of k for 128 x 64 outputs of two products or 128 x 128 of one (which is also
+// what their FMAs take), 12 for 64 x 64 of two and 8 for 64 x 64 of one, and a tenth more for storing them.  The
+// last round of blocks counts whole: 512 x 1408 x 2048 two products 88 / 176 blocks, 143 / 232 us.
+bool large_tiles(unsigned large, unsigned small, unsigned small_cost) {
+    const unsigned sms = static_cast<unsigned>(device_sm_count());
+    return large != 0 && (small == 0 || static_cast<uint64_t>((large + sms - 1) / sms) * 16 <=
+                                            static_cast<uint64_t>((small + sms - 1) / sms) * small_cost);
+}
+
 template <typename T>
 cudaError_t gated_simt_t(const GatedParams &p, cudaStream_t s) {
     TileArgs t{{p.x, p.x}, {p.w[0], p.w[1]}, p.m, p.n, p.k, p.ldx, p.ldw, 0, 0, 0};
     t.a_vec = groups_of_4(p.x, p.ldx, sizeof(T));
     t.b_vec = groups_of_4(p.w[0], p.ldw, sizeof(T)) && groups_of_4(p.w[1], p.ldw, sizeof(T));
-    unsigned blocks = tile_grid(p.m, p.n, 128, 64, &t);
-    if (blocks >= static_cast<unsigned>(device_sm_count())) {
-        gated_simt_kernel<T, 8, 4><<<blocks, 256, 0, s>>>(t, p);
-    } else {
-        blocks = tile_grid(p.m, p.n, 64, 32, &t);
-        if (blocks == 0) return cudaErrorInvalidConfiguration;
-        gated_simt_kernel<T, 4, 2><<<blocks, 256, 0, s>>>(t, p);
-    }
-    return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t sum_gemm_t(const SumGemmParams &p, cudaStream_t s) {
-    TileArgs t{{p.a[0], p.a[1]}, {p.b[0], p.b[1]}, p.m, p.n, p.k, p.lda, p.ldb, 0, 0, 0};
-    t.a_vec = groups_of_4(p.a[0], p.lda, sizeof(T)) && groups_of_4(p.a[1], p.lda, sizeof(T));
-    t.b_vec = groups_of_4(p.b[0], p.ldb, sizeof(T)) && groups_of_4(p.b[1], p.ldb, sizeof(T));
-    unsigned blocks = tile_grid(p.m, p.n, 128, 128, &t);
-    if (blocks >= static_cast<unsigned>(device_sm_count())) {
-        sum_gemm_simt_kernel<T, 8, 8><<<blocks, 256, 0, s>>>(t, static_cast<T *>(p.c), p.ldc);
-    } else {
-        blocks = tile_grid(p.m, p.n, 64, 64, &t);
-        if (blocks == 0) return cudaErrorInvalidConfiguration;
-        sum_gemm_simt_kernel<T, 4, 4><<<blocks, 256, 0, s>>>(t, static_cast<T *>(p.c), p.ldc);
-    }
-    return cudaGetLastError();
+    const unsigned small = tile_grid(p.m, p.n, 64, 64, &t), large = tile_grid(p.m, p.n, 128, 64, &t);
+    if (large == 0) return cudaErrorInvalidConfiguration;
+    if (large_tiles(large, small, 12)) return launch_whole(gated_simt_kernel<T, 8, 4>, large, s, t, p);
+    return launch_whole(gated_simt_kernel<T, 4, 4>, small, s, t, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -505,7 +613,49 @@ cudaError_t repack_t(const RepackParams &p, cudaStream_t s) {
 cudaError_t launch_gated_rowdot(int dt, const GatedParams &p, cudaStream_t s) { GBMM_BY_TYPE(dt, rowdot_t) }
 cudaError_t launch_gated_simt(int dt, const GatedParams &p, cudaStream_t s) { GBMM_BY_TYPE(dt, gated_simt_t) }
 cudaError_t launch_gated_grad(int dt, const GatedGradParams &p, cudaStream_t s) { GBMM_BY_TYPE(dt, gated_grad_t) }
-cudaError_t launch_sum_gemm_simt(int dt, const SumGemmParams &p, cudaStream_t s) { GBMM_BY_TYPE(dt, sum_gemm_t) }
+
+// The gradients of f32 blocks: x null or w null where one of them is not asked for.
+cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, cudaStream_t s) {
+    TileArgs tx{}, txs{}, tw{}, tws{};
+    unsigned x_small = 0, x_large = 0, w_small = 0, w_large = 0;
+    OuterOut o{};
+    if (x != nullptr) {
+        tx = TileArgs{{x->a[0], x->a[1]}, {x->b[0], x->b[1]}, x->m, x->n, x->k, x->lda, x->ldb, 0, 0, 0};
+        tx.a_vec = groups_of_4(x->a[0], x->lda, 4) && groups_of_4(x->a[1], x->lda, 4);
+        tx.b_vec = groups_of_4(x->b[0], x->ldb, 4) && groups_of_4(x->b[1], x->ldb, 4);
+        txs = tx;
+        x_small = tile_grid(x->m, x->n, 64, 64, &txs);
+        x_large = tile_grid(x->m, x->n, 128, 128, &tx);
+        if (x_large == 0) return cudaErrorInvalidConfiguration;
+    }
+    if (w != nullptr) {
+        tw = TileArgs{{w->x, w->x}, {w->d[0], w->d[1]}, w->k, w->n, w->m, w->ldx, w->ldd, 0, 0, 0};
+        tw.a_vec = groups_of_4(w->x, w->ldx, 4);
+        tw.b_vec = groups_of_4(w->d[0], w->ldd, 4) && groups_of_4(w->d[1], w->ldd, 4);
+        tws = tw;
+        w_small = tile_grid(tw.m, tw.n, 64, 64, &tws);
+        w_large = tile_grid(tw.m, tw.n, 128, 64, &tw);
+        if (w_large == 0) return cudaErrorInvalidConfiguration;
+        o = OuterOut{{static_cast<float *>(w->c[0]), static_cast<float *>(w->c[1])},
+                     w->ldc,
+                     groups_of_4(w->c[0], w->ldc, 4) && groups_of_4(w->c[1], w->ldc, 4)};
+    }
+    float *c = x != nullptr ? static_cast<float *>(x->c) : nullptr;
+    // one grid for both where it has a block for each SM
+    const uint64_t together = 2 * static_cast<uint64_t>(x_large) + w_large + (w_large & 1);
+    if (x != nullptr && w != nullptr && together >= static_cast<uint64_t>(device_sm_count()) && together <= INT32_MAX) {
+        both_gemm_simt_kernel<<<static_cast<unsigned>(together), 256, 0, s>>>(tx, c, x->ldc, 2 * x_large, tw, o, w_large);
+        return cudaGetLastError();
+    }
+    if (x != nullptr) {
+        const cudaError_t e = large_tiles(x_large, x_small, 8)
+                                  ? launch_whole(sum_gemm_simt_kernel<8, 8>, x_large, s, tx, c, x->ldc)
+                                  : launch_whole(sum_gemm_simt_kernel<4, 4>, x_small, s, txs, c, x->ldc);
+        if (e != cudaSuccess || w == nullptr) return e;
+    }
+    return large_tiles(w_large, w_small, 12) ? launch_whole(outer_gemm_simt_kernel<8, 4>, w_large, s, tw, o)
+                                             : launch_whole(outer_gemm_simt_kernel<4, 4>, w_small, s, tws, o);
+}
 cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s) { return repack_t<uint16_t>(p, s); }
 cudaError_t launch_codes_to_f16(const RepackParams &p, cudaStream_t s) { return repack_t<int8_t>(p, s); }
 

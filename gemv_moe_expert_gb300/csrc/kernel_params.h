@@ -196,6 +196,13 @@ struct SumGemmParams {
     int64_t m, n, k, lda, ldb, ldc;
 };
 
+// c[i] [n, k] = d[i]^T x, d [m, n] and x [m, k] (gated.cu).
+struct OuterGemmParams {
+    const void *x, *d[2];
+    void *c[2];
+    int64_t m, n, k, ldx, ldd, ldc;
+};
+
 // Rows laid out again: src [rows, cols] (16-bit values, or 8-bit codes that become f16) into
 // dst [rows, ldd] (gated.cu).
 struct RepackParams {
@@ -306,7 +313,8 @@ cudaError_t launch_q4_bf16(const Q4Params &p, cudaStream_t s);
 cudaError_t launch_gated_rowdot(int dt, const GatedParams &p, cudaStream_t s);
 cudaError_t launch_gated_simt(int dt, const GatedParams &p, cudaStream_t s);
 cudaError_t launch_gated_grad(int dt, const GatedGradParams &p, cudaStream_t s);
-cudaError_t launch_sum_gemm_simt(int dt, const SumGemmParams &p, cudaStream_t s);
+// f32
+cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, cudaStream_t s);
 cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s);
 cudaError_t launch_codes_to_f16(const RepackParams &p, cudaStream_t s);
 // on the tensor cores: gated a[0] = x, b = both weights, all K-contiguous in boxes of pair_tc_rows()
