@@ -171,7 +171,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
                  [i32, u32, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, u64,
                   vp]),
                 ("gbmm_quantize_i8", [i32, i64, i64, vp, i64, vp, i64, vp, vp]),
-                ("gbmm_gemm_i8_scratch_bytes", [i64, i64, i64, ctypes.POINTER(u64)]),
+                ("gbmm_gemm_i8_scratch_bytes", [i64, i64, i64, i32, ctypes.POINTER(u64)]),
                 ("gbmm_gemm_i8", [i32, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, u64, vp])):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = i32
@@ -387,10 +387,10 @@ def gbmm_quantize_i8(dtype, m, k, x, ldx, q, ldq, scale, stream=None) -> int:
     return load().gbmm_quantize_i8(_dt(dtype), m, k, _ptr(x), ldx, _ptr(q), ldq, _ptr(scale), _stream(stream))
 
 
-def gbmm_gemm_i8_scratch_bytes(m: int, n: int, k: int):
+def gbmm_gemm_i8_scratch_bytes(m: int, n: int, k: int, aligned: bool):
     """Returns (status, bytes)."""
     need = ctypes.c_uint64(0)
-    st = load().gbmm_gemm_i8_scratch_bytes(m, n, k, ctypes.byref(need))
+    st = load().gbmm_gemm_i8_scratch_bytes(m, n, k, int(bool(aligned)), ctypes.byref(need))
     return st, need.value
 
 

@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgbmm.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
-SOURCES = ["api.cu", "direct_tc.cu", "ffn_api.cu", "gated.cu", "gemv.cu", "gemv_tc.cu", "gemm_simt.cu", "gemm_tc.cu", "grouped_tc.cu", "i8.cu", "matmul_id.cu",
+SOURCES = ["api.cu", "direct_tc.cu", "few_tc.cu", "ffn_api.cu", "gated.cu", "gemv.cu", "gemv_tc.cu", "gemm_simt.cu", "gemm_tc.cu", "grouped_tc.cu", "i8.cu", "matmul_id.cu",
            "misc.cu", "moe_api.cu", "moe_route.cu", "moe_rows.cu", "moe_sort.cu", "pair_tc.cu", "q4_bf16.cu", "q4_f16.cu", "q4_f32.cu",
            "static_scratch.cu", "stream.cu"]
 HEADERS = ["api_checks.h", "api_internal.h", "device_common.cuh", "gated.cuh", "kernel_params.h", "q4.cuh"]

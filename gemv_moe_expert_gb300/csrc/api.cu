@@ -516,6 +516,16 @@ bool encode_matrix16(CUtensorMap *map, int dt, const void *base, int64_t inner, 
                      uint32_t box_outer) {
     return encode_operand(map, dt, base, inner, outer, 1, ld, 0, true, box_outer);
 }
+bool encode_matrix8(CUtensorMap *map, const void *base, int64_t inner, int64_t outer, int64_t ld, uint32_t box_outer) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer), 1u};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld), static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(outer)};
+    const cuuint32_t box[3] = {128u, box_outer, 1u}, estr[3] = {1u, 1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool encode_store32(CUtensorMap *map, int dt, const void *base, int64_t cols, int64_t rows, int64_t ld) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     const int64_t size = dtype_size(dt);

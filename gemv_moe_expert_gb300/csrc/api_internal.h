@@ -22,6 +22,8 @@ gbmm_status finish_launch(cudaError_t e, const char *name, cudaStream_t s);
 bool encode_matrix16(CUtensorMap *map, int dt, const void *base, int64_t inner, int64_t outer, int64_t ld,
                      uint32_t box_outer);
 
+// Tensor map of a matrix of bytes [outer][inner], boxes of box_outer x 128, 128-byte swizzle.
+bool encode_matrix8(CUtensorMap *map, const void *base, int64_t inner, int64_t outer, int64_t ld, uint32_t box_outer);
 // Tensor map for storing 32 x 32 pieces of a matrix [rows][cols] of type dt: rows of 64 bytes with 64-byte
 // swizzle (16-bit types), of 128 bytes with 128-byte swizzle (f32).  False where TMA cannot write it.
 bool encode_store32(CUtensorMap *map, int dt, const void *base, int64_t cols, int64_t rows, int64_t ld);

@@ -1,0 +1,427 @@
+// few_tc.cu -- products of the feed-forward block for some tens of tokens, on the tensor cores as
+// y^T = W x^T: the weights' rows are the MMA's M side (128 a tile), the tokens its N side (kN).
+//   gated   h = act(x Wg^T) * (x Wu^T): 64 rows of Wg and the same 64 of Wu share a tile, so an output's two
+//           projections lie 64 rows apart
+//   codes   c = (a b^T) scale_a scale_b for 8-bit codes: both operands' codes reach shared memory as bytes and four
+//           warps write them as f16 (exact) into the tiles that the MMAs read.  Each 1024 of k has an accumulator of
+//           its own: sums of products of two codes are exact up to there (2^24), and the accumulators are added as
+//           integers at the end.
+// Every weight byte is read once (per kN tokens), and the kernel is bound by that stream; two CTAs share an SM
+// where the ring allows, and the contraction is split over a thread-block cluster of up to eight CTAs where the tiles
+// are few.  Each CTA leaves its partial sums in its own (by then idle) ring, and after a cluster barrier every CTA adds
+// up its share of the tokens, in the order of the ranks, through distributed shared memory.
+//   warp 0      TMA
+//   warp 1      tensor memory, MMAs
+//   warps 2..5  codes: bytes to f16; then the epilogue
+// Every mbarrier wait is bounded; on a timeout the kernel records it in the device error word, waits (bounded) for
+// its own copies and MMAs, still takes part in the cluster barriers, releases its TMEM and returns.
+#include <cooperative_groups.h>
+
+#include <type_traits>
+
+#include "gated.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace gbmm {
+
+namespace {
+
+constexpr int kBM = 128;
+constexpr int kThreads = 192;
+constexpr int kMaxSplit = 8;
+constexpr uint32_t kWBytes = kBM * 128;  // 128 rows of 128 bytes: 64 16-bit values or 128 codes
+constexpr int kChunk = 8;                // code blocks (of 128) whose sums stay exact: 1024 of k
+
+template <bool kCodes, int kN>
+struct Ring {
+    static constexpr uint32_t kXBytes = kN * 128;
+    static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
+    // codes: stages of bytes, and slots of 64 k in f16 (a stage fills two)
+    static constexpr int kStages = kCodes ? (kN <= 16 ? 3 : kN == 128 ? 3 : 2) : (kN <= 16 ? 6 : kN == 32 ? 5 : kN == 64 ? 4 : 3);
+    static constexpr int kSlots = !kCodes ? 0 : (kN <= 32 ? 3 : kN == 64 ? 2 : 3);
+    static constexpr uint32_t kRingBytes = (kStages + kSlots) * kStageBytes;
+    static constexpr uint32_t kBarBytes = 256;
+    static constexpr uint32_t kSmemBytes = kRingBytes + kBarBytes + 1024;
+    static_assert(kStageBytes % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+    static_assert(kBM * kN * 4 <= kRingBytes, "the partial sums are parked in the ring");
+    static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
+    static_assert(8 * (2 * (kStages + kSlots) + 2) + 8 <= kBarBytes, "barriers");
+};
+
+// four codes as f16: a byte b behind 0x64 is the f16 1024 + b, and b is the code + 128 once its top bit is flipped
+__device__ __forceinline__ uint2 codes_to_half(uint32_t w) {
+    w ^= 0x80808080u;
+    const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), bias);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&hi), bias);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// Half h (64 codes) of each of kRows 128-byte rows at `raw`, as f16 at `dst`; both 128-byte swizzled.
+// Thread t of 128 takes row t % kRows, so that eight neighbours' 16-byte accesses fall into different banks.
+template <int kRows>
+__device__ __forceinline__ void convert(uint32_t raw, uint32_t dst, int h, int t) {
+#pragma unroll
+    for (int i = 0; i < (kRows * 4 + 127) / 128; ++i) {
+        const int id = t + 128 * i;
+        if (kRows * 4 % 128 != 0 && id >= kRows * 4) break;
+        const int row = id % kRows, c = id / kRows;
+        uint32_t v[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(raw + row * 128 + (((4 * h + c) ^ (row & 7)) << 4))
+                     : "memory");
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint2 a = codes_to_half(v[2 * e]), b = codes_to_half(v[2 * e + 1]);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * 128 + (((2 * c + e) ^ (row & 7)) << 4)),
+                         "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y)
+                         : "memory");
+        }
+    }
+}
+
+template <typename TC, uint32_t kFmt, bool kCodes, int kN>
+__global__ void __launch_bounds__(kThreads)
+few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
+              const __grid_constant__ CUtensorMap map_w1, const FewTcParams p) {
+    using R = Ring<kCodes, kN>;
+    constexpr int kStages = R::kStages, kSlots = R::kSlots;
+    constexpr int kRows = kCodes ? kBM : kBM / 2;  // outputs across a tile
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t s0 = raw_addr + pad;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + R::kRingBytes);
+    const uint32_t bar0 = smem_addr(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };                       // bytes of stage s have landed
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };          // ... are used up
+    auto slot_full = [&](int s) { return bar0 + 8u * (2 * kStages + s); };      // codes: slot s holds f16
+    auto slot_empty = [&](int s) { return bar0 + 8u * (2 * kStages + kSlots + s); };
+    const uint32_t tfull_bar = bar0 + 8u * (2 * (kStages + kSlots));
+    const uint32_t drain_bar = tfull_bar + 8u;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * (kStages + kSlots) + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ksplit = p.ksplit;
+    const int rank = static_cast<int>(blockIdx.x) % ksplit;  // == rank in the cluster
+    const int tile = static_cast<int>(blockIdx.x) / ksplit;
+    const int n0 = tile / p.token_blocks * kRows, t0 = tile % p.token_blocks * kN;
+    const uint64_t lim = p.wait_limit_ns;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), kCodes ? 4 : 1);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(slot_full(s), 4);
+            mbar_init(slot_empty(s), 1);
+        }
+        mbar_init(tfull_bar, 1);
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&map_x);
+        tma_prefetch_desc(&map_w0);
+        if (!kCodes) tma_prefetch_desc(&map_w1);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(tmem_slot), p.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    grid_dep_begin();
+    // this CTA's share of the k-blocks (128 bytes of a row each)
+    constexpr int kBlock = kCodes ? 128 : 64;
+    const int kb_total = (p.k + kBlock - 1) / kBlock;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(kb_total) * rank / ksplit);
+    const int kblocks = static_cast<int>(static_cast<int64_t>(kb_total) * (rank + 1) / ksplit) - kb0;
+    // the MMA warp's steps: a k-block, or half of one (64 codes)
+    const int steps = kCodes ? 2 * kblocks : kblocks;
+
+    auto fail = [&]() {
+        *abort_flag = 1;
+        report_device_error(p.err, kKidFewTc);
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer ----------------
+            const uint64_t pol = p.token_blocks == 1 ? policy_evict_first() : policy_evict_normal();
+            uint32_t issued = 0;
+            bool ok = true;
+            for (int kb = 0; kb < kblocks; ++kb) {
+                const int stage = kb % kStages;
+                const uint32_t use = static_cast<uint32_t>(kb / kStages);
+                if (use > 0 && !mbar_wait_bounded(empty_bar(stage), (use - 1u) & 1u, lim, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sw = s0 + stage * R::kStageBytes;
+                const int k0 = (kb0 + kb) * kBlock;
+                mbar_arrive_expect_tx(full_bar(stage), R::kStageBytes);
+                tma_load_3d_hint(sw, &map_w0, full_bar(stage), k0, n0, 0, pol);
+                if (!kCodes) tma_load_3d_hint(sw + kWBytes / 2, &map_w1, full_bar(stage), k0, n0, 0, pol);
+                tma_load_3d(sw + kWBytes, &map_x, full_bar(stage), k0, t0, 0);
+                ++issued;
+            }
+            if (!ok) {
+                fail();
+                // wait for this CTA's own copies still in flight
+                for (int s = 0; s < kStages; ++s) {
+                    const uint32_t n_s = issued / kStages + (static_cast<uint32_t>(s) < issued % kStages ? 1u : 0u);
+                    if (n_s > 0) mbar_wait_bounded(full_bar(s), (n_s - 1u) & 1u, lim, nullptr);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- MMA issuer ----------------
+            constexpr uint32_t kIdesc = idesc_f16(kFmt, kBM, kN);
+            constexpr int kDepth = kCodes ? kSlots : kStages;
+            bool ok = true;
+            for (int i = 0; i < steps; ++i) {
+                const int at = i % kDepth;
+                if (!mbar_wait_bounded(kCodes ? slot_full(at) : full_bar(at), static_cast<uint32_t>(i / kDepth) & 1u, lim,
+                                       abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sw = s0 + (kCodes ? kStages + at : at) * R::kStageBytes;
+                const int chunk = kCodes ? i / (2 * kChunk) : 0;
+                const uint32_t d = tmem_base + static_cast<uint32_t>(chunk * kN);
+                const bool fresh = kCodes ? i % (2 * kChunk) == 0 : i == 0;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_f16_ss(d, sdesc_kmajor_sw128(sw + kk * 32), sdesc_kmajor_sw128(sw + kWBytes + kk * 32), kIdesc,
+                                fresh && kk == 0 ? 0u : 1u);
+                umma_commit(kCodes ? slot_empty(at) : empty_bar(at));
+            }
+            if (ok) umma_commit(tfull_bar);
+            else fail();
+            // every MMA this thread issued has completed once this arrives
+            umma_commit(drain_bar);
+            mbar_wait_bounded(drain_bar, 0, lim, nullptr);
+        }
+    } else if constexpr (kCodes) {
+        // ---------------- codes to f16 ----------------
+        const int t = threadIdx.x - 64;
+        for (int i = 0; i < steps; ++i) {
+            const int kb = i >> 1, h = i & 1, stage = kb % kStages, slot = i % kSlots;
+            int ready = 1;
+            if (lane == 0) {
+                if (h == 0) ready = mbar_wait_bounded(full_bar(stage), static_cast<uint32_t>(kb / kStages) & 1u, lim, abort_flag);
+                const uint32_t use = static_cast<uint32_t>(i / kSlots);
+                if (ready && use > 0) ready = mbar_wait_bounded(slot_empty(slot), (use - 1u) & 1u, lim, abort_flag);
+            }
+            ready = __shfl_sync(0xffffffffu, ready, 0);
+            if (!ready) {
+                if (lane == 0) fail();
+                break;
+            }
+            // every lane orders the bytes that TMA wrote before its own reads
+            if (h == 0 && lane != 0) mbar_try_wait(full_bar(stage), static_cast<uint32_t>(kb / kStages) & 1u);
+            const uint32_t from = s0 + stage * R::kStageBytes, to = s0 + (kStages + slot) * R::kStageBytes;
+            convert<kBM>(from, to, h, t);
+            convert<kN>(from + kWBytes, to + kWBytes, h, t);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(slot_full(slot));
+                if (h == 1) mbar_arrive(empty_bar(stage));
+            }
+        }
+    }
+    __syncwarp();
+
+    // ---------------- epilogue (warps 2..5): partial sums to shared memory, [token][row] ----------------
+    using Sum = typename std::conditional<kCodes, int, float>::type;
+    Sum *part = reinterpret_cast<Sum *>(smem);
+    const int tokens = min(kN, p.m - t0);
+    if (warp >= 2) {
+        const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. + 31
+        int ready = 0;
+        if (lane == 0) ready = mbar_wait_bounded(tfull_bar, 0, lim, abort_flag);
+        ready = __shfl_sync(0xffffffffu, ready, 0);
+        __syncwarp();
+        if (!ready && lane == 0) fail();
+        if (ready) tc_fence_after();
+        const int chunks = !ready || kblocks == 0 ? 0 : kCodes ? (kblocks + kChunk - 1) / kChunk : 1;
+        const int row = quarter * 32 + lane;
+        for (int j = 0; j < tokens; j += 16) {
+            Sum v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = 0;
+            for (int c = 0; c < chunks; ++c) {
+                uint32_t r[16];
+                tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c * kN + j), r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if constexpr (kCodes) v[e] += __float2int_rn(__uint_as_float(r[e]));
+                    else v[e] = __uint_as_float(r[e]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part[(j + e) * kBM + row] = v[e];
+        }
+    }
+    cg::cluster_group cluster = cg::this_cluster();
+    // every thread of the cluster reaches both barriers, on every path
+    if (ksplit > 1) cluster.sync();
+    else __syncthreads();
+    if (warp >= 2) {
+        const int t = threadIdx.x - 64;
+        const int col = kCodes ? t : t & 63;
+        const int64_t j = static_cast<int64_t>(n0) + col;
+        const Sum *from[kMaxSplit];
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q)
+            from[q] = ksplit > 1 && q < ksplit ? cluster.map_shared_rank(part, q) : part;
+        if (j < p.n) {
+            const float sb = kCodes && p.scale_b != nullptr ? __ldg(p.scale_b + j) : 1.f;
+            const int step = kCodes ? ksplit : 2 * ksplit;
+#pragma unroll 2
+            for (int tk = kCodes ? rank : 2 * rank + (t >> 6); tk < tokens; tk += step) {
+                const int64_t i = t0 + tk;
+                TC *const out = static_cast<TC *>(p.c) + i * p.ldc + j;
+                if constexpr (kCodes) {
+                    int s = 0;
+#pragma unroll
+                    for (int q = 0; q < kMaxSplit; ++q)
+                        if (q < ksplit) s += from[q][tk * kBM + col];
+                    const float sa = p.scale_a != nullptr ? __ldg(p.scale_a + i) : 1.f;
+                    *out = Elem<TC>::from_f(static_cast<float>(s) * sa * sb);
+                } else {
+                    float g = 0.f, u = 0.f;
+#pragma unroll
+                    for (int q = 0; q < kMaxSplit; ++q)
+                        if (q < ksplit) {
+                            g += from[q][tk * kBM + col];
+                            u += from[q][tk * kBM + 64 + col];
+                        }
+                    *out = Elem<TC>::from_f(gate_act_16(p.act, g) * u);
+                    if (p.saved[0] != nullptr) {
+                        static_cast<TC *>(p.saved[0])[i * p.ld_saved + j] = Elem<TC>::from_f(g);
+                        static_cast<TC *>(p.saved[1])[i * p.ld_saved + j] = Elem<TC>::from_f(u);
+                    }
+                }
+            }
+        }
+    }
+    if (ksplit > 1) cluster.sync();  // every rank's shared memory lives until all have read it
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, p.tmem_cols);
+    }
+}
+
+template <typename TC, uint32_t kFmt, bool kCodes, int kN>
+cudaError_t few_n(const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
+    using R = Ring<kCodes, kN>;
+    static unsigned long long attr_set = 0;  // one bit per device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(attr_set & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(few_tc_kernel<TC, kFmt, kCodes, kN>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        attr_set |= bit;
+    }
+    const int rows = kCodes ? kBM : kBM / 2;
+    const int64_t blocks = (static_cast<int64_t>(p.n) + rows - 1) / rows * p.token_blocks * p.ksplit;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = R::kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.ksplit);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, few_tc_kernel<TC, kFmt, kCodes, kN>, maps.x, maps.w[0], maps.w[1], p);
+}
+
+template <typename TC, uint32_t kFmt, bool kCodes>
+cudaError_t few_t(int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
+    if (p.ksplit < 1 || p.ksplit > kMaxSplit) return cudaErrorInvalidValue;
+    switch (tokens) {
+    case 16: return few_n<TC, kFmt, kCodes, 16>(maps, p, s);
+    case 32: return few_n<TC, kFmt, kCodes, 32>(maps, p, s);
+    case 64: return few_n<TC, kFmt, kCodes, 64>(maps, p, s);
+    case 128: return few_n<TC, kFmt, kCodes, 128>(maps, p, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+int few_tc_rows(bool codes) { return codes ? kBM : kBM / 2; }
+
+namespace {
+int tile_tokens(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
+int ctas_per_sm(bool codes, int tokens) { return codes && tokens == 128 ? 1 : 2; }
+// code blocks that one CTA's accumulators take
+int64_t code_blocks(int tokens) { return (ctas_per_sm(true, tokens) == 1 ? 512 : 256) / tokens * kChunk; }
+}  // namespace
+
+bool few_tc_takes(bool codes, int64_t m, int64_t n, int64_t k) {
+    if (m > 128) return false;
+    return !codes || (k + 127) / 128 <= kMaxSplit * code_blocks(tile_tokens(m));
+}
+
+// The tokens of a tile; sets the CTAs that share its contraction and the columns of tensor memory.
+int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p) {
+    const int tokens = tile_tokens(m);
+    p->token_blocks = static_cast<int32_t>((m + tokens - 1) / tokens);
+    const int64_t rows = few_tc_rows(codes), tiles = (n + rows - 1) / rows * p->token_blocks;
+    const int64_t kb = codes ? (k + 127) / 128 : (k + 63) / 64;
+    int64_t split = 1;
+    // as many CTAs as the SMs hold at once, each with a few blocks of its own
+    while (split < kMaxSplit && tiles * (split + 1) <= static_cast<int64_t>(ctas_per_sm(codes, tokens)) * num_sms &&
+           kb >= (codes ? 2 : 4) * (split + 1))
+        ++split;
+    int64_t cols = tokens;
+    if (codes) {
+        while (split < kMaxSplit && (kb + split - 1) / split > code_blocks(tokens)) ++split;
+        cols = ((kb + split - 1) / split + kChunk - 1) / kChunk * tokens;
+    }
+    p->tmem_cols = 32;
+    while (p->tmem_cols < cols) p->tmem_cols *= 2;
+    p->ksplit = static_cast<int32_t>(split);
+    return tokens;
+}
+
+cudaError_t launch_gated_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
+    return dt == kF16 ? few_t<__half, 0, false>(tokens, maps, p, s) : few_t<__nv_bfloat16, 1, false>(tokens, maps, p, s);
+}
+cudaError_t launch_gemm_i8_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
+    switch (dt) {
+    case kF32: return few_t<float, 0, true>(tokens, maps, p, s);
+    case kF16: return few_t<__half, 0, true>(tokens, maps, p, s);
+    case kBF16: return few_t<__nv_bfloat16, 0, true>(tokens, maps, p, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace gbmm

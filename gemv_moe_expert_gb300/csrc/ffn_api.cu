@@ -73,6 +73,24 @@ bool pair_params(PairTcParams *p, PairTcMaps *maps, int dt, void *c, int64_t ldc
     return p->err != nullptr;
 }
 
+void few_params(FewTcParams *p, void *c, int64_t ldc, int64_t m, int64_t n, int64_t k) {
+    p->c = c;
+    p->ldc = ldc;
+    p->m = static_cast<int32_t>(m);
+    p->n = static_cast<int32_t>(n);
+    p->k = static_cast<int32_t>(k);
+    p->err = device_error_word();
+    p->wait_limit_ns = kWaitLimitNs;
+}
+
+// How an 8-bit product runs: dot products of bytes; bytes that become f16 inside the kernel (rows that TMA cannot
+// read are laid out again first); or both operands as f16 in the scratch.
+enum class I8Route { kDot, kFew, kTiles };
+I8Route i8_route(int64_t m, int64_t n, int64_t k) {
+    if (m <= kDotRows || n == 0 || k == 0) return I8Route::kDot;
+    return few_tc_takes(true, m, n, k) ? I8Route::kFew : I8Route::kTiles;
+}
+
 gbmm_status check_gated(const char *fn, gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n, int64_t k) {
     if (!known_dtype(dt))
         return fail(GBMM_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d is not f32, f16 or bf16", fn, (int)dt);
@@ -145,6 +163,22 @@ gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n,
         if (st == GBMM_OK) st = lay_again(fn, &lg, n, k, ldw, scratch, s);
         if (st == GBMM_OK) st = lay_again(fn, &lu, n, k, ldw, scratch, s);
         if (st != GBMM_OK) return st;
+        if (few_tc_takes(false, m, n, k)) {
+            FewTcMaps maps{};
+            FewTcParams q{};
+            few_params(&q, h, ldh, m, n, k);
+            const uint32_t tokens = static_cast<uint32_t>(few_tc_plan(false, m, n, k, device_sm_count(), &q));
+            const uint32_t rows = static_cast<uint32_t>(few_tc_rows(false));
+            if (q.err == nullptr || !encode_matrix16(&maps.x, dt, lx.p, k, m, lx.ld, tokens) ||
+                !encode_matrix16(&maps.w[0], dt, lg.p, k, n, lg.ld, rows) ||
+                !encode_matrix16(&maps.w[1], dt, lu.p, k, n, lu.ld, rows))
+                return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
+            q.saved[0] = gate;
+            q.saved[1] = up;
+            q.ld_saved = ld_saved;
+            q.act = static_cast<int32_t>(activation);
+            return finish_launch(launch_gated_few(dt, static_cast<int>(tokens), maps, q, s), fn, s);
+        }
         PairTcMaps maps{};
         PairTcParams q;
         const uint32_t rows = static_cast<uint32_t>(pair_tc_rows());
@@ -272,10 +306,17 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     g.gate = gate;
     g.up = up;
     g.d_h = d_h;
-    // both gradients of the weights are one batch where one lies whole behind the other; the projections' gradients lie
-    // in the same order then
+    // both gradients of the weights are one batch where one lies whole behind the other and neither operand of the
+    // product between them; the projections' gradients lie in the same order then
     const intptr_t gap = reinterpret_cast<intptr_t>(d_w_up) - reinterpret_cast<intptr_t>(d_w_gate);
-    const bool batched = dt != GBMM_F32 && need_w && static_cast<uint64_t>(gap < 0 ? -gap : gap) >= dwb;
+    const uintptr_t dw_lo = reinterpret_cast<uintptr_t>(gap < 0 ? d_w_up : d_w_gate);
+    const uintptr_t dw_hi = reinterpret_cast<uintptr_t>(gap < 0 ? d_w_gate : d_w_up) + dwb;
+    auto between = [&](const void *p, uint64_t bytes) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        return bytes > 0 && at < dw_hi && dw_lo < at + bytes;
+    };
+    const bool batched = dt != GBMM_F32 && need_w && static_cast<uint64_t>(gap < 0 ? -gap : gap) >= dwb &&
+                         !between(scratch, scratch_bytes) && !between(x, xb);
     const int first = batched && gap < 0 ? 1 : 0;
     const int64_t d_apart = static_cast<int64_t>(d_at[1] - d_at[0]) / static_cast<int64_t>(size);
     g.d[first] = base + d_at[0];
@@ -342,17 +383,19 @@ gbmm_status gbmm_quantize_i8(gbmm_dtype dt, int64_t m, int64_t k, const void *x,
     return finish_launch(launch_quantize_i8(dt, p, cuda_stream(stream)), fn, cuda_stream(stream));
 }
 
-gbmm_status gbmm_gemm_i8_scratch_bytes(int64_t m, int64_t n, int64_t k, uint64_t *bytes) {
+gbmm_status gbmm_gemm_i8_scratch_bytes(int64_t m, int64_t n, int64_t k, int aligned, uint64_t *bytes) {
     record_error(GBMM_OK, "");
     const char *fn = "gbmm_gemm_i8_scratch_bytes";
     if (!in_range(m) || !in_range(n) || k < 0 || k > GBMM_I8_MAX_K)
         return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: m and n must lie in [0, 2^31), k in [0, %d]", fn, GBMM_I8_MAX_K);
     if (bytes == nullptr) return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: bytes is null", fn);
     *bytes = 0;
-    if (m <= kDotRows || n == 0 || k == 0) return GBMM_OK;
+    const I8Route route = i8_route(m, n, k);
+    if (route == I8Route::kDot || (route == I8Route::kFew && aligned)) return GBMM_OK;
+    const int size = route == I8Route::kFew ? 1 : 2;
     Parts parts;
-    parts.add(m, round_up(k, 8), 2);
-    parts.add(n, round_up(k, 8), 2);
+    parts.add(m, round_up(k, 16 / size), size);
+    parts.add(n, round_up(k, 16 / size), size);
     *bytes = parts.bytes;
     return GBMM_OK;
 }
@@ -364,7 +407,6 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
     const char *fn = "gbmm_gemm_i8";
     if (!known_dtype(dt))
         return fail(GBMM_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d is not f32, f16 or bf16", fn, (int)dt);
-    uint64_t need;
     if (!in_range(m) || !in_range(n) || k < 0 || k > GBMM_I8_MAX_K)
         return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: m and n must lie in [0, 2^31), k in [0, %d]", fn, GBMM_I8_MAX_K);
     if (lda < k || ldb < k || ldc < n)
@@ -374,29 +416,50 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
     uint64_t ab, bb, cb;
     if (!span(m, k, lda, 1, &ab) || !span(n, k, ldb, 1, &bb) || !span(m, n, ldc, size, &cb))
         return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: operand extent overflows", fn);
-    gbmm_status st = gbmm_gemm_i8_scratch_bytes(m, n, k, &need);
-    if (st != GBMM_OK) return st;
+    const I8Route route = i8_route(m, n, k);
+    // both operands' rows laid out again in the scratch, as f16 or (where TMA cannot read them) as bytes
+    const int size2 = route == I8Route::kFew ? 1 : 2;
+    const int64_t ld = round_up(k, 16 / size2);
+    const bool again_a = route == I8Route::kTiles || (route == I8Route::kFew && !rows16(a, lda));
+    const bool again_b = route == I8Route::kTiles || (route == I8Route::kFew && !rows16(b, ldb));
+    Parts parts;
+    const uint64_t a_at = again_a ? parts.add(m, ld, size2) : 0, b_at = again_b ? parts.add(n, ld, size2) : 0;
+    const uint64_t need = again_a || again_b ? parts.bytes : 0;
     const Operand ops[] = {matrix("a", a, ab, k, lda, 1, false),
                            {"scale_a", scale_a, scale_a ? static_cast<uint64_t>(m) * 4 : 0, 4, false},
                            matrix("b", b, bb, k, ldb, 1, false),
                            {"scale_b", scale_b, scale_b ? static_cast<uint64_t>(n) * 4 : 0, 4, false},
                            matrix("c", c, cb, n, ldc, size, true),
                            {"scratch", scratch, scratch ? scratch_bytes : 0, 1, true}};
-    st = check_operands(fn, ops, 6);
+    gbmm_status st = check_operands(fn, ops, 6);
     if (st != GBMM_OK) return st;
     if (need > 0 && (scratch == nullptr || scratch_bytes < need))
         return fail(GBMM_ERR_SCRATCH, "%s: needs %llu bytes of scratch (got %llu)", fn, (unsigned long long)need,
                     (unsigned long long)(scratch ? scratch_bytes : 0));
     if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
     cudaStream_t s = cuda_stream(stream);
-    if (m <= kDotRows || k == 0) {
+    if (route == I8Route::kDot) {
         const GemmI8Params p{a, b, scale_a, scale_b, c, m, n, k, lda, ldb, ldc};
         return finish_launch(launch_gemm_i8_dot(dt, p, s), fn, s);
     }
-    Parts parts;
-    const int64_t ld = round_up(k, 8);
-    char *const base = Parts::base(scratch);
-    const RepackParams ra{a, base + parts.add(m, ld, 2), m, k, lda, ld}, rb{b, base + parts.add(n, ld, 2), n, k, ldb, ld};
+    const RepackParams ra{a, Parts::base(scratch) + a_at, m, k, lda, ld}, rb{b, Parts::base(scratch) + b_at, n, k, ldb, ld};
+    if (route == I8Route::kFew) {
+        FewTcMaps maps{};
+        FewTcParams q{};
+        few_params(&q, c, ldc, m, n, k);
+        q.scale_a = scale_a;
+        q.scale_b = scale_b;
+        const uint32_t tokens = static_cast<uint32_t>(few_tc_plan(true, m, n, k, device_sm_count(), &q));
+        if (q.err == nullptr || !encode_matrix8(&maps.x, again_a ? ra.dst : a, k, m, again_a ? ld : lda, tokens) ||
+            !encode_matrix8(&maps.w[0], again_b ? rb.dst : b, k, n, again_b ? ld : ldb,
+                            static_cast<uint32_t>(few_tc_rows(true))))
+            return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
+        maps.w[1] = maps.w[0];
+        if (again_a) st = finish_launch(launch_repack8(ra, s), fn, s);
+        if (st == GBMM_OK && again_b) st = finish_launch(launch_repack8(rb, s), fn, s);
+        if (st != GBMM_OK) return st;
+        return finish_launch(launch_gemm_i8_few(dt, static_cast<int>(tokens), maps, q, s), fn, s);
+    }
     PairTcMaps maps{};
     PairTcParams q;
     const uint32_t rows = static_cast<uint32_t>(pair_tc_rows());

@@ -198,6 +198,7 @@ struct TileArgs {
     int64_t m, n, k, lda, ldb;
     int32_t a_vec, b_vec;  // groups of four elements can be read in one access
     int64_t tiles_n;
+    uint32_t parts = 1;    // CTAs that share a tile
 };
 
 constexpr int kTK = 16;
@@ -229,9 +230,8 @@ struct TileProduct {
 
     __device__ __forceinline__ float at(int pr, int r, int c) const { return half_of(acc[pr][r][c / 2], c & 1); }
 
-    // first, count: which of the sources (kSum)
-    __device__ __forceinline__ void run(const TileArgs &t, int64_t m0, int64_t n0, Smem &sm, int first = 0,
-                                        int count = kMode == kSum ? 2 : 1) {
+    // part of parts: the share of the contraction (kSum: of both sources) that this block takes
+    __device__ __forceinline__ void run(const TileArgs &t, int64_t m0, int64_t n0, Smem &sm, int part = 0, int parts = 1) {
         const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
         for (int q = 0; q < kProducts; ++q)
@@ -240,10 +240,11 @@ struct TileProduct {
 #pragma unroll
                 for (int c = 0; c < kTN / 2; ++c) acc[q][r][c] = 0;
         float ra[kA][4], rb[kProducts][kB][4];
-        const int64_t steps1 = (t.k + kTK - 1) / kTK, steps = count * steps1;
+        const int64_t steps1 = (t.k + kTK - 1) / kTK, all = (kMode == kSum ? 2 : 1) * steps1;
+        const int64_t begin = all * part / parts, end = all * (part + 1) / parts;
         auto load = [&](int64_t step) {
-            const int64_t k0 = (step >= steps1 ? step - steps1 : step) * kTK;
-            const int src = kMode == kSum ? first + (step >= steps1 ? 1 : 0) : 0;
+            const int64_t k0 = (kMode == kSum && step >= steps1 ? step - steps1 : step) * kTK;
+            const int src = kMode == kSum && step >= steps1 ? 1 : 0;
             load_tile<kAK, kBM, kA>(static_cast<const T *>(src ? t.a[1] : t.a[0]), t.lda, m0, t.m, k0, t.k, t.a_vec, ra);
 #pragma unroll
             for (int pr = 0; pr < kProducts; ++pr)
@@ -255,14 +256,14 @@ struct TileProduct {
 #pragma unroll
             for (int pr = 0; pr < kProducts; ++pr) store_tile<kBK, kBN, kB>(sm.b[buf][pr], rb[pr]);
         };
-        if (steps > 0) {
-            load(0);
+        if (begin < end) {
+            load(begin);
             store(0);
         }
         __syncthreads();
         int cur = 0;
-        for (int64_t step = 0; step < steps; ++step) {
-            const bool more = step + 1 < steps;
+        for (int64_t step = begin; step < end; ++step) {
+            const bool more = step + 1 < end;
             if (more) load(step + 1);
             // the next k's values are read while this one's are multiplied
             float av[2][kTM];
@@ -284,6 +285,35 @@ struct TileProduct {
             __syncthreads();
             cur ^= 1;
         }
+    }
+
+    // The cluster's other CTAs hand their sums to the first one through shared memory, two rows a thread at a time;
+    // it adds them in the order of their ranks.
+    __device__ __forceinline__ void reduce_cluster(Smem &sm, int rank, int parts) {
+        cg::cluster_group cluster = cg::this_cluster();
+        uint64_t *mine = reinterpret_cast<uint64_t *>(&sm);
+        static_assert(256 * kTN * sizeof(uint64_t) <= sizeof(Smem), "two rows a thread");
+#pragma unroll
+        for (int pr = 0; pr < kProducts; ++pr)
+#pragma unroll
+            for (int r = 0; r < kTM; r += 2) {
+                if (rank != 0)
+#pragma unroll
+                    for (int e = 0; e < kTN; ++e)
+                        mine[e * 256 + threadIdx.x] = acc[pr][r + e / (kTN / 2)][e % (kTN / 2)];
+                cluster.sync();
+                if (rank == 0)
+                    for (int q = 1; q < parts; ++q) {
+                        const uint64_t *other = cluster.map_shared_rank(mine, q);
+#pragma unroll
+                        for (int e = 0; e < kTN; ++e) {
+                            uint64_t &v = acc[pr][r + e / (kTN / 2)][e % (kTN / 2)];
+                            const uint64_t w = other[e * 256 + threadIdx.x];
+                            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
+                        }
+                    }
+                cluster.sync();
+            }
     }
 
     static __device__ __forceinline__ void fetch(const Smem &sm, int cur, int kk, int ty, int tx, float (&av)[kTM],
@@ -355,13 +385,22 @@ struct TileProduct {
     }
 };
 
-template <typename T, int kTM, int kTN>
+// kSplit: a cluster of t.parts CTAs a tile, a share of the contraction each
+template <typename T, int kTM, int kTN, bool kSplit>
 __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const TileArgs t, const GatedParams p) {
     using Tile = TileProduct<T, kGated, kTM, kTN>;
     __shared__ __align__(16) typename Tile::Smem sm;
     Tile tile;
-    const int64_t m0 = blockIdx.x / t.tiles_n * Tile::kBM, n0 = blockIdx.x % t.tiles_n * Tile::kBN;
-    tile.run(t, m0, n0, sm);
+    const unsigned parts = kSplit ? t.parts : 1, block = blockIdx.x / parts;
+    const int64_t m0 = block / t.tiles_n * Tile::kBM, n0 = block % t.tiles_n * Tile::kBN;
+    if constexpr (kSplit) {
+        const int rank = static_cast<int>(blockIdx.x % parts);  // in the cluster, too
+        tile.run(t, m0, n0, sm, rank, static_cast<int>(parts));
+        tile.reduce_cluster(sm, rank, static_cast<int>(parts));
+        if (rank != 0) return;
+    } else {
+        tile.run(t, m0, n0, sm);
+    }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
     for (int r = 0; r < kTM; ++r) {
@@ -381,8 +420,7 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const TileArgs t, co
     }
 }
 
-// One tile of the gradient of x.  kSplit: a cluster of two CTAs a tile, one source each; the odd one's sums go to the even
-// one through shared memory, two rows a thread at a time.
+// One tile of the gradient of x.  kSplit: a cluster of two CTAs a tile, one source each.
 template <int kTM, int kTN, bool kSplit>
 __device__ __forceinline__ void sum_tile(const TileArgs &t, float *out, int64_t ldc, int64_t block,
                                          typename TileProduct<float, kSum, kTM, kTN>::Smem &sm) {
@@ -391,26 +429,9 @@ __device__ __forceinline__ void sum_tile(const TileArgs &t, float *out, int64_t 
     if (kSplit) block >>= 1;
     const int64_t m0 = block / t.tiles_n * Tile::kBM, n0 = block % t.tiles_n * Tile::kBN;
     if constexpr (kSplit) {
-        cg::cluster_group pair = cg::this_cluster();
         const int rank = blockIdx.x & 1;
-        tile.run(t, m0, n0, sm, rank, 1);
-        uint64_t *mine = reinterpret_cast<uint64_t *>(&sm), *other = pair.map_shared_rank(mine, 1);
-        static_assert(256 * 2 * (kTN / 2) * sizeof(uint64_t) <= sizeof(sm), "two rows a thread");
-#pragma unroll
-        for (int r = 0; r < kTM; r += 2) {
-            if (rank == 1)
-#pragma unroll
-                for (int e = 0; e < kTN; ++e) mine[e * 256 + threadIdx.x] = tile.acc[0][r + e / (kTN / 2)][e % (kTN / 2)];
-            pair.sync();
-            if (rank == 0)
-#pragma unroll
-                for (int e = 0; e < kTN; ++e) {
-                    uint64_t &v = tile.acc[0][r + e / (kTN / 2)][e % (kTN / 2)];
-                    const uint64_t w = other[e * 256 + threadIdx.x];
-                    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
-                }
-            pair.sync();
-        }
+        tile.run(t, m0, n0, sm, rank, 2);
+        tile.reduce_cluster(sm, rank, 2);
         if (rank == 1) return;
     } else {
         tile.run(t, m0, n0, sm);
@@ -523,8 +544,31 @@ cudaError_t gated_simt_t(const GatedParams &p, cudaStream_t s) {
     t.b_vec = groups_of_4(p.w[0], p.ldw, sizeof(T)) && groups_of_4(p.w[1], p.ldw, sizeof(T));
     const unsigned small = tile_grid(p.m, p.n, 64, 64, &t), large = tile_grid(p.m, p.n, 128, 64, &t);
     if (large == 0) return cudaErrorInvalidConfiguration;
-    if (large_tiles(large, small, 12)) return launch_whole(gated_simt_kernel<T, 8, 4>, large, s, t, p);
-    return launch_whole(gated_simt_kernel<T, 4, 4>, small, s, t, p);
+    const unsigned sms = static_cast<unsigned>(device_sm_count());
+    // At most one tile an SM: up to eight CTAs share a tile, as many as make the busiest SM's share smallest.
+    // 512 x 1408 x 2048, 88 tiles: 206 us whole, 195 by two, SPLIT3 by three.
+    if (large <= sms) {
+        const bool few = 4 * large <= sms;
+        const unsigned tiles = few ? small : large;
+        unsigned parts = 2;
+        for (unsigned q = 3; q <= 8 && p.k >= 256 * static_cast<int64_t>(q); ++q)
+            if (((tiles * q + sms - 1) / sms) * parts < ((tiles * parts + sms - 1) / sms) * q) parts = q;
+        t.parts = parts;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = parts;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(parts * tiles);
+        cfg.blockDim = dim3(256);
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return few ? cudaLaunchKernelEx(&cfg, gated_simt_kernel<T, 4, 4, true>, t, p)
+                   : cudaLaunchKernelEx(&cfg, gated_simt_kernel<T, 8, 4, true>, t, p);
+    }
+    if (large_tiles(large, small, 12)) return launch_whole(gated_simt_kernel<T, 8, 4, false>, large, s, t, p);
+    return launch_whole(gated_simt_kernel<T, 4, 4, false>, small, s, t, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -571,33 +615,37 @@ cudaError_t gated_grad_t(const GatedGradParams &p, cudaStream_t s) {
 // it can
 // ---------------------------------------------------------------------------
 
-struct alignas(16) Halves {
-    uint16_t v[8];
+template <typename D>
+struct alignas(16) Piece {
+    static constexpr int kN = 16 / sizeof(D);
+    D v[kN];
 };
 
-__device__ __forceinline__ uint16_t as_bits(uint16_t v) { return v; }
-__device__ __forceinline__ uint16_t as_bits(int8_t v) { return __half_as_ushort(__int2half_rn(v)); }
+__device__ __forceinline__ void put(uint16_t v, uint16_t *to) { *to = v; }
+__device__ __forceinline__ void put(int8_t v, int8_t *to) { *to = v; }
+__device__ __forceinline__ void put(int8_t v, uint16_t *to) { *to = __half_as_ushort(__int2half_rn(v)); }
 
-template <typename S>
+template <typename S, typename D>
 __global__ void __launch_bounds__(256) repack_kernel(const RepackParams p) {
+    constexpr int kN = Piece<D>::kN;
     grid_dep_begin();
-    const int64_t pieces = p.ldd / 8, total = pieces * p.rows;
+    const int64_t pieces = p.ldd / kN, total = pieces * p.rows;
     for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < total;
          at += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t i = at / pieces, j = (at - i * pieces) * 8;
+        const int64_t i = at / pieces, j = (at - i * pieces) * kN;
         const S *src = static_cast<const S *>(p.src) + i * p.lds + j;
-        Halves h;
+        Piece<D> h;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h.v[e] = j + e < p.cols ? as_bits(src[e]) : uint16_t{0};
-        *reinterpret_cast<Halves *>(static_cast<uint16_t *>(p.dst) + i * p.ldd + j) = h;
+        for (int e = 0; e < kN; ++e) put(j + e < p.cols ? src[e] : S{0}, &h.v[e]);
+        *reinterpret_cast<Piece<D> *>(static_cast<D *>(p.dst) + i * p.ldd + j) = h;
     }
 }
 
-template <typename S>
+template <typename S, typename D>
 cudaError_t repack_t(const RepackParams &p, cudaStream_t s) {
-    const int64_t blocks = (p.rows * (p.ldd / 8) + 255) / 256, most = 16LL * device_sm_count();
+    const int64_t blocks = (p.rows * (p.ldd / Piece<D>::kN) + 255) / 256, most = 16LL * device_sm_count();
     if (blocks == 0) return cudaSuccess;
-    return launch_early(repack_kernel<S>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, p);
+    return launch_early(repack_kernel<S, D>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, p);
 }
 
 }  // namespace
@@ -656,7 +704,8 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
     return large_tiles(w_large, w_small, 12) ? launch_whole(outer_gemm_simt_kernel<8, 4>, w_large, s, tw, o)
                                              : launch_whole(outer_gemm_simt_kernel<4, 4>, w_small, s, tws, o);
 }
-cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s) { return repack_t<uint16_t>(p, s); }
-cudaError_t launch_codes_to_f16(const RepackParams &p, cudaStream_t s) { return repack_t<int8_t>(p, s); }
+cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s) { return repack_t<uint16_t, uint16_t>(p, s); }
+cudaError_t launch_codes_to_f16(const RepackParams &p, cudaStream_t s) { return repack_t<int8_t, uint16_t>(p, s); }
+cudaError_t launch_repack8(const RepackParams &p, cudaStream_t s) { return repack_t<int8_t, int8_t>(p, s); }
 
 }  // namespace gbmm

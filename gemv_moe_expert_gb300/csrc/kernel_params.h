@@ -203,8 +203,8 @@ struct OuterGemmParams {
     int64_t m, n, k, ldx, ldd, ldc;
 };
 
-// Rows laid out again: src [rows, cols] (16-bit values, or 8-bit codes that become f16) into
-// dst [rows, ldd] (gated.cu).
+// Rows laid out again: src [rows, cols] (16-bit values, 8-bit codes, or codes that become f16) into
+// dst [rows, ldd], ldd a multiple of 16 bytes (gated.cu).
 struct RepackParams {
     const void *src;
     void *dst;
@@ -241,6 +241,23 @@ struct PairTcParams {
 struct PairTcMaps {
     CUtensorMap a[2], b[2];
     CUtensorMap out[3];  // c and both saved projections, as 32 x 32 pieces
+};
+
+// The same products for some tens of tokens (few_tc.cu).
+struct FewTcParams {
+    void *c;
+    void *saved[2];                  // gated: both projections, or null
+    const float *scale_a, *scale_b;  // codes; null: 1
+    int64_t ldc, ld_saved;
+    int32_t m, n, k;
+    int32_t act;
+    int32_t ksplit, token_blocks;    // these and tmem_cols: few_tc_plan()
+    uint32_t tmem_cols;
+    uint32_t *err;
+    uint64_t wait_limit_ns;
+};
+struct FewTcMaps {
+    CUtensorMap x, w[2];  // boxes of 128 bytes x tokens, and x few_tc_rows() rows
 };
 
 // ---- launchers (each returns the launch's cudaError_t) --------------------
@@ -316,6 +333,7 @@ cudaError_t launch_gated_grad(int dt, const GatedGradParams &p, cudaStream_t s);
 // f32
 cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, cudaStream_t s);
 cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s);
+cudaError_t launch_repack8(const RepackParams &p, cudaStream_t s);
 cudaError_t launch_codes_to_f16(const RepackParams &p, cudaStream_t s);
 // on the tensor cores: gated a[0] = x, b = both weights, all K-contiguous in boxes of pair_tc_rows()
 // rows; sum a and b as in SumGemmParams, b in 64 x 64 boxes; codes a[0] and b[0] (f16) as gated
@@ -324,6 +342,11 @@ cudaError_t launch_sum_gemm_tc(int dt, const PairTcMaps &maps, const PairTcParam
 cudaError_t launch_gemm_i8_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s);
 int pair_tc_rows();
 int pair_tc_block_k();
+int few_tc_rows(bool codes);
+bool few_tc_takes(bool codes, int64_t m, int64_t n, int64_t k);
+int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p);
+cudaError_t launch_gated_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s);
+cudaError_t launch_gemm_i8_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s);
 cudaError_t launch_quantize_i8(int dt, const QuantizeParams &p, cudaStream_t s);
 cudaError_t launch_gemm_i8_dot(int dt, const GemmI8Params &p, cudaStream_t s);
 

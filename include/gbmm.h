@@ -603,8 +603,10 @@ GBMM_API gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int
 GBMM_API gbmm_status gbmm_quantize_i8(gbmm_dtype dt, int64_t m, int64_t k, const void *x, int64_t ldx, int8_t *q,
                                       int64_t ldq, float *scale, gbmm_stream stream);
 
-/* gbmm_gemm_i8_scratch_bytes -- bytes of scratch that gbmm_gemm_i8 needs (0 is possible).  Host-only. */
-GBMM_API gbmm_status gbmm_gemm_i8_scratch_bytes(int64_t m, int64_t n, int64_t k, uint64_t *bytes);
+/* gbmm_gemm_i8_scratch_bytes -- bytes of scratch that gbmm_gemm_i8 needs (0 is possible).
+ * aligned: nonzero if a and b start on multiples of 16 bytes and lda and ldb are multiples of
+ * 16; 0 for any layout.  Host-only. */
+GBMM_API gbmm_status gbmm_gemm_i8_scratch_bytes(int64_t m, int64_t n, int64_t k, int aligned, uint64_t *bytes);
 
 /*
  * gbmm_gemm_i8 -- c[i,j] = (sum_x a[i,x] b[j,x]) * scale_a[i] * scale_b[j]

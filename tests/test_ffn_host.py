@@ -136,17 +136,22 @@ def test_scratch_sizes():
     over = dict(ldx=65, ldw=65)
     assert call(*CALLS["back"], dict(over, nbytes=need)) == PASSES
     assert call(*CALLS["back"], dict(over, nbytes=need - 1)) == SCRATCH
-    assert gb.gbmm_gemm_i8_scratch_bytes(1, 1, gb.I8_MAX_K + 1)[0] == BAD
-    assert gb.gbmm_gemm_i8_scratch_bytes(-1, 1, 1)[0] == BAD
-    assert gb.gbmm_gemm_i8_scratch_bytes(1 << 31, 1, 1)[0] == BAD
-    for m, n, k in ((4, 32, 64), (1000, 1001, 1003), (100000, 7, 131071)):
-        st, need = gb.gbmm_gemm_i8_scratch_bytes(m, n, k)
-        assert st == gb.GBMM_OK
-        far = dict(m=m, n=n, k=k, lda=k, ldb=k, ldc=n, a=BASE, b=BASE << 1, c=BASE << 2, scratch=BASE << 3, sa=0, sb=0)
-        assert call(*CALLS["gemm"], dict(far, nbytes=need)) == PASSES
-        if need:
-            assert call(*CALLS["gemm"], dict(far, nbytes=need - 1)) == SCRATCH
-            assert call(*CALLS["gemm"], dict(far, nbytes=need, scratch=0)) == SCRATCH
+    assert gb.gbmm_gemm_i8_scratch_bytes(1, 1, gb.I8_MAX_K + 1, True)[0] == BAD
+    assert gb.gbmm_gemm_i8_scratch_bytes(-1, 1, 1, True)[0] == BAD
+    assert gb.gbmm_gemm_i8_scratch_bytes(1 << 31, 1, 1, True)[0] == BAD
+    for m, n, k in ((4, 32, 64), (40, 32, 64), (40, 33, 1003), (100, 7, 131071), (1000, 1001, 1003), (100000, 7, 131071)):
+        sizes = []
+        for ld in (-(-k // 16) * 16, k | 1):
+            st, need = gb.gbmm_gemm_i8_scratch_bytes(m, n, k, ld % 16 == 0)
+            assert st == gb.GBMM_OK
+            far = dict(m=m, n=n, k=k, lda=ld, ldb=ld, ldc=n, a=BASE, b=BASE << 1, c=BASE << 2, scratch=BASE << 3, sa=0,
+                       sb=0)
+            assert call(*CALLS["gemm"], dict(far, nbytes=need)) == PASSES
+            if need:
+                assert call(*CALLS["gemm"], dict(far, nbytes=need - 1)) == SCRATCH
+                assert call(*CALLS["gemm"], dict(far, nbytes=need, scratch=0)) == SCRATCH
+            sizes.append(need)
+        assert sizes[0] <= sizes[1]
     st, need = gb.gbmm_gated_backward_scratch_bytes("bf16", 4, 32, 64, True)
     assert call(*CALLS["back"], dict(nbytes=need)) == PASSES
     assert call(*CALLS["back"], dict(nbytes=need - 1)) == SCRATCH

@@ -279,6 +279,36 @@ def test_gradient_against_differences(act):
         assert abs(got - ref) <= (2 * n + m + k + 100) * U * 1.2 * mag.sum() + 1e-9 * mag.sum(), (i, got, ref)
 
 
+@pytest.mark.parametrize("order", [("dwg", "dwu", "x", "scratch"), ("dwu", "dwg", "scratch", "x"),
+                                   ("dwg", "scratch", "dwu", "x"), ("dwu", "x", "dwg", "scratch"), "rows"])
+def test_backward_wherever_the_gradients_lie(order):
+    """Both weights' gradients next to each other, in either order, with an operand between them, and row by row."""
+    m, n, k = 80, 136, 200
+    b = Block("bf16", m, n, k)
+    ref = b.backward("silu")
+    need = gb.gbmm_gated_backward_scratch_bytes("bf16", m, n, k, True)[1]
+    size = {"dwg": n * k * 2, "dwu": n * k * 2, "x": m * k * 2, "scratch": need}
+    size = {name: -(-v // 256) * 256 for name, v in size.items()}
+    buf = torch.full((sum(size.values()) + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    base = -(-buf.data_ptr() // 256) * 256
+    at, ld = {}, k
+    for name in order if order != "rows" else ("x", "scratch", "dwg", "dwu"):
+        at[name] = base + sum(size[v] for v in at)
+    if order == "rows":
+        at["dwu"], ld = at["dwg"] + k * 2, 2 * k
+    off = at["x"] - buf.data_ptr()
+    buf[off:off + m * k * 2].copy_(torch.from_numpy(b.x.astype(np.float32)).bfloat16().cuda().reshape(-1).view(torch.uint8))
+    gb.check(gb.gbmm_gated_backward("bf16", CODE["silu"], m, n, k, at["x"], k, b.gp, b.up, b.ldk, b.saved[0][1],
+                                    b.saved[1][1], b.ldn, b.saved[2][1], b.ldn, None, k, at["dwg"], at["dwu"], ld,
+                                    at["scratch"], need))
+    torch.cuda.synchronize()
+    for name, want in (("dwg", ref[1]), ("dwu", ref[2])):
+        off = at[name] - buf.data_ptr()
+        got = buf[off:off + ((n - 1) * ld + k) * 2].view(torch.bfloat16)
+        got = got.as_strided((n, k), (ld, 1)).double().cpu().numpy()
+        assert np.array_equal(got, want), name
+
+
 def make(dtype, m, n, k, seed):
     g = torch.Generator(device="cuda").manual_seed(seed)
     dt = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dtype]

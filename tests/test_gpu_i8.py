@@ -119,7 +119,7 @@ class Product:
         m, n, k = self.m, self.n, self.k
         ldc = n + cpad
         cb, cp = empty(m, ldc, dtype, coff)
-        st, need = gb.gbmm_gemm_i8_scratch_bytes(m, n, k)
+        st, need = gb.gbmm_gemm_i8_scratch_bytes(m, n, k, False)
         gb.check(st)
         scratch = DevBuf(max(need, 1))
         gb.check(gb.gbmm_gemm_i8(dtype, m, n, k, self.ap, self.ld, self.sab and self.sab.ptr, self.bp, self.ld,
@@ -175,7 +175,7 @@ def test_product_of_extreme_codes_is_exact(m, k):
     b[2::4, ::2] = 127
     b[3::4] = codes(rng, len(b[3::4]), k, -128)
     a[1::3] = codes(rng, len(a[1::3]), k, -128)
-    st, need = gb.gbmm_gemm_i8_scratch_bytes(m, n, k)
+    st, need = gb.gbmm_gemm_i8_scratch_bytes(m, n, k, False)
     ad, bd = torch.from_numpy(a).cuda(), torch.from_numpy(b).cuda()
     c, scratch = torch.empty(m, n, device="cuda"), torch.empty(need + 1, dtype=torch.uint8, device="cuda")
     gb.check(gb.gbmm_gemm_i8("f32", m, n, k, ad, k, None, bd, k, None, c, n, scratch, need))
@@ -204,7 +204,7 @@ def layer(m, n, k, t, stream=None):
 
 def make(m, n, k, seed):
     g = torch.Generator(device="cuda").manual_seed(seed)
-    t = {"x": torch.randn(m, k, generator=g, device="cuda").bfloat16(), "need": gb.gbmm_gemm_i8_scratch_bytes(m, n, k)[1]}
+    t = {"x": torch.randn(m, k, generator=g, device="cuda").bfloat16(), "need": gb.gbmm_gemm_i8_scratch_bytes(m, n, k, False)[1]}
     w = torch.randn(n, k, generator=g, device="cuda").bfloat16()
     t |= {"q": torch.empty(m, k, dtype=torch.int8, device="cuda"), "s": torch.empty(m, device="cuda"),
           "w": torch.empty(n, k, dtype=torch.int8, device="cuda"), "ws": torch.empty(n, device="cuda"),
