@@ -2,17 +2,18 @@
 // y^T = W x^T: the weights' rows are the MMA's M side (128 a tile), the tokens its N side (kN).
 //   gated   h = act(x Wg^T) * (x Wu^T): 64 rows of Wg and the same 64 of Wu share a tile, so an output's two
 //           projections lie 64 rows apart
-//   codes   c = (a b^T) scale_a scale_b for 8-bit codes: both operands' codes reach shared memory as bytes and four
-//           warps write them as f16 (exact) into the tiles that the MMAs read.  Each 1024 of k has an accumulator of
-//           its own: sums of products of two codes are exact up to there (2^24), and the accumulators are added as
-//           integers at the end.
+//   codes   c = (a b^T) scale_a scale_b for 8-bit codes: the weights' codes reach shared memory as bytes and eight
+//           warps write them as f16 (exact) into the tiles that the MMAs read; so do the tokens' up to 32 of them, more
+//           come as f16 (they would cost as much as the weights).  Each 1024 of k has an accumulator of its own:
+//           sums of products of two codes are exact up to there (2^24), and the accumulators are added as integers
+//           at the end.
 // Every weight byte is read once (per kN tokens), and the kernel is bound by that stream; two CTAs share an SM
 // where the ring allows, and the contraction is split over a thread-block cluster of up to eight CTAs where the tiles
 // are few.  Each CTA leaves its partial sums in its own (by then idle) ring, and after a cluster barrier every CTA adds
 // up its share of the tokens, in the order of the ranks, through distributed shared memory.
 //   warp 0      TMA
 //   warp 1      tensor memory, MMAs
-//   warps 2..5  codes: bytes to f16; then the epilogue
+//   warps 2..5  (codes: 2..9, bytes to f16) the epilogue
 // Every mbarrier wait is bounded; on a timeout the kernel records it in the device error word, waits (bounded) for
 // its own copies and MMAs, still takes part in the cluster barriers, releases its TMEM and returns.
 #include <cooperative_groups.h>
@@ -28,22 +29,27 @@ namespace gbmm {
 namespace {
 
 constexpr int kBM = 128;
-constexpr int kThreads = 192;
 constexpr int kMaxSplit = 8;
+constexpr int64_t kFewCodeRows = 512;  // tokens of an 8-bit product that run here
 constexpr uint32_t kWBytes = kBM * 128;  // 128 rows of 128 bytes: 64 16-bit values or 128 codes
 constexpr int kChunk = 8;                // code blocks (of 128) whose sums stay exact: 1024 of k
 
 template <bool kCodes, int kN>
 struct Ring {
-    static constexpr uint32_t kXBytes = kN * 128;
-    static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
-    // codes: stages of bytes, and slots of 64 k in f16 (a stage fills two)
+    static constexpr int kWarps = kCodes ? 8 : 4;  // behind the TMA and MMA warps
+    static constexpr int kThreads = 64 + 32 * kWarps;
+    static constexpr bool kHalfX = kCodes && kN >= 64;  // the tokens' codes come as f16
+    static constexpr uint32_t kXBytes = kN * 128;       // 64 16-bit values or 128 codes of each token
+    // a stage: a k-block as TMA brings it; codes: a slot of 64 k in f16 (a stage fills two)
+    static constexpr uint32_t kStageBytes = kWBytes + (kHalfX ? 2 : 1) * kXBytes;
+    static constexpr uint32_t kSlotBytes = kWBytes + (kHalfX ? 0 : kXBytes);
     static constexpr int kStages = kCodes ? (kN <= 16 ? 3 : kN == 128 ? 3 : 2) : (kN <= 16 ? 6 : kN == 32 ? 5 : kN == 64 ? 4 : 3);
-    static constexpr int kSlots = !kCodes ? 0 : (kN <= 32 ? 3 : kN == 64 ? 2 : 3);
-    static constexpr uint32_t kRingBytes = (kStages + kSlots) * kStageBytes;
+    static constexpr int kSlots = !kCodes ? 0 : (kN <= 32 ? 3 : kN == 64 ? 2 : kN == 128 ? 4 : 3);
+    static constexpr uint32_t kSlot0 = kStages * kStageBytes;
+    static constexpr uint32_t kRingBytes = kSlot0 + kSlots * kSlotBytes;
     static constexpr uint32_t kBarBytes = 256;
     static constexpr uint32_t kSmemBytes = kRingBytes + kBarBytes + 1024;
-    static_assert(kStageBytes % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+    static_assert(kStageBytes % 1024 == 0 && kSlotBytes % 1024 == 0, "swizzled tiles need 1024-byte alignment");
     static_assert(kBM * kN * 4 <= kRingBytes, "the partial sums are parked in the ring");
     static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
     static_assert(8 * (2 * (kStages + kSlots) + 2) + 8 <= kBarBytes, "barriers");
@@ -60,22 +66,29 @@ __device__ __forceinline__ uint2 codes_to_half(uint32_t w) {
 }
 
 // Half h (64 codes) of each of kRows 128-byte rows at `raw`, as f16 at `dst`; both 128-byte swizzled.
-// Thread t of 128 takes row t % kRows, so that eight neighbours' 16-byte accesses fall into different banks.
+// Thread t of 256 takes row t % kRows, so that eight neighbours' 16-byte accesses fall into different banks.
 template <int kRows>
 __device__ __forceinline__ void convert(uint32_t raw, uint32_t dst, int h, int t) {
+    constexpr int kPieces = (kRows * 4 + 255) / 256;
+    uint32_t v[kPieces][4];
 #pragma unroll
-    for (int i = 0; i < (kRows * 4 + 127) / 128; ++i) {
-        const int id = t + 128 * i;
-        if (kRows * 4 % 128 != 0 && id >= kRows * 4) break;
+    for (int i = 0; i < kPieces; ++i) {
+        const int id = t + 256 * i;
+        if (kRows * 4 % 256 != 0 && id >= kRows * 4) break;
         const int row = id % kRows, c = id / kRows;
-        uint32_t v[4];
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
                      : "r"(raw + row * 128 + (((4 * h + c) ^ (row & 7)) << 4))
                      : "memory");
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        const int id = t + 256 * i;
+        if (kRows * 4 % 256 != 0 && id >= kRows * 4) break;
+        const int row = id % kRows, c = id / kRows;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const uint2 a = codes_to_half(v[2 * e]), b = codes_to_half(v[2 * e + 1]);
+            const uint2 a = codes_to_half(v[i][2 * e]), b = codes_to_half(v[i][2 * e + 1]);
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * 128 + (((2 * c + e) ^ (row & 7)) << 4)),
                          "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y)
                          : "memory");
@@ -84,11 +97,11 @@ __device__ __forceinline__ void convert(uint32_t raw, uint32_t dst, int h, int t
 }
 
 template <typename TC, uint32_t kFmt, bool kCodes, int kN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(Ring<kCodes, kN>::kThreads)
 few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
               const __grid_constant__ CUtensorMap map_w1, const FewTcParams p) {
     using R = Ring<kCodes, kN>;
-    constexpr int kStages = R::kStages, kSlots = R::kSlots;
+    constexpr int kStages = R::kStages, kSlots = R::kSlots, kWarps = R::kWarps;
     constexpr int kRows = kCodes ? kBM : kBM / 2;  // outputs across a tile
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
@@ -116,10 +129,10 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), kCodes ? 4 : 1);
+            mbar_init(empty_bar(s), kCodes && !R::kHalfX ? kWarps : 1);
         }
         for (int s = 0; s < kSlots; ++s) {
-            mbar_init(slot_full(s), 4);
+            mbar_init(slot_full(s), kWarps);
             mbar_init(slot_empty(s), 1);
         }
         mbar_init(tfull_bar, 1);
@@ -173,6 +186,7 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                 tma_load_3d_hint(sw, &map_w0, full_bar(stage), k0, n0, 0, pol);
                 if (!kCodes) tma_load_3d_hint(sw + kWBytes / 2, &map_w1, full_bar(stage), k0, n0, 0, pol);
                 tma_load_3d(sw + kWBytes, &map_x, full_bar(stage), k0, t0, 0);
+                if (R::kHalfX) tma_load_3d(sw + kWBytes + R::kXBytes, &map_x, full_bar(stage), k0 + 64, t0, 0);
                 ++issued;
             }
             if (!ok) {
@@ -192,21 +206,23 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             bool ok = true;
             for (int i = 0; i < steps; ++i) {
                 const int at = i % kDepth;
-                if (!mbar_wait_bounded(kCodes ? slot_full(at) : full_bar(at), static_cast<uint32_t>(i / kDepth) & 1u, lim,
-                                       abort_flag)) {
-                    ok = false;
-                    break;
-                }
+                const int stage = (kCodes ? i >> 1 : i) % kStages;
+                const uint32_t stage_phase = static_cast<uint32_t>((kCodes ? i >> 1 : i) / kStages) & 1u;
+                ok = !kCodes || mbar_wait_bounded(slot_full(at), static_cast<uint32_t>(i / kDepth) & 1u, lim, abort_flag);
+                if (ok && (!kCodes || R::kHalfX)) ok = mbar_wait_bounded(full_bar(stage), stage_phase, lim, abort_flag);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t sw = s0 + (kCodes ? kStages + at : at) * R::kStageBytes;
+                const uint32_t sw = kCodes ? s0 + R::kSlot0 + at * R::kSlotBytes : s0 + at * R::kStageBytes;
+                const uint32_t sx = R::kHalfX ? s0 + stage * R::kStageBytes + kWBytes + (i & 1) * R::kXBytes : sw + kWBytes;
                 const int chunk = kCodes ? i / (2 * kChunk) : 0;
                 const uint32_t d = tmem_base + static_cast<uint32_t>(chunk * kN);
                 const bool fresh = kCodes ? i % (2 * kChunk) == 0 : i == 0;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_f16_ss(d, sdesc_kmajor_sw128(sw + kk * 32), sdesc_kmajor_sw128(sw + kWBytes + kk * 32), kIdesc,
+                    umma_f16_ss(d, sdesc_kmajor_sw128(sw + kk * 32), sdesc_kmajor_sw128(sx + kk * 32), kIdesc,
                                 fresh && kk == 0 ? 0u : 1u);
                 umma_commit(kCodes ? slot_empty(at) : empty_bar(at));
+                if (R::kHalfX && (i & 1) == 1) umma_commit(empty_bar(stage));
             }
             if (ok) umma_commit(tfull_bar);
             else fail();
@@ -232,20 +248,20 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             }
             // every lane orders the bytes that TMA wrote before its own reads
             if (h == 0 && lane != 0) mbar_try_wait(full_bar(stage), static_cast<uint32_t>(kb / kStages) & 1u);
-            const uint32_t from = s0 + stage * R::kStageBytes, to = s0 + (kStages + slot) * R::kStageBytes;
+            const uint32_t from = s0 + stage * R::kStageBytes, to = s0 + R::kSlot0 + slot * R::kSlotBytes;
             convert<kBM>(from, to, h, t);
-            convert<kN>(from + kWBytes, to + kWBytes, h, t);
+            if constexpr (!R::kHalfX) convert<kN>(from + kWBytes, to + kWBytes, h, t);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(slot_full(slot));
-                if (h == 1) mbar_arrive(empty_bar(stage));
+                if (!R::kHalfX && h == 1) mbar_arrive(empty_bar(stage));
             }
         }
     }
     __syncwarp();
 
-    // ---------------- epilogue (warps 2..5): partial sums to shared memory, [token][row] ----------------
+    // ---------------- epilogue: partial sums to shared memory, [token][row] ----------------
     using Sum = typename std::conditional<kCodes, int, float>::type;
     Sum *part = reinterpret_cast<Sum *>(smem);
     const int tokens = min(kN, p.m - t0);
@@ -259,7 +275,8 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         if (ready) tc_fence_after();
         const int chunks = !ready || kblocks == 0 ? 0 : kCodes ? (kblocks + kChunk - 1) / kChunk : 1;
         const int row = quarter * 32 + lane;
-        for (int j = 0; j < tokens; j += 16) {
+        // two warps a quarter take every other 16 tokens
+        for (int j = 16 * ((warp - 2) >> 2); j < tokens; j += 4 * kWarps) {
             Sum v[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = 0;
@@ -283,7 +300,9 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     else __syncthreads();
     if (warp >= 2) {
         const int t = threadIdx.x - 64;
-        const int col = kCodes ? t : t & 63;
+        // a thread's column, and which of the tokens that run at once is its own
+        constexpr int kAcross = kRows, kDown = 32 * kWarps / kAcross;
+        const int col = t % kAcross, first = t / kAcross;
         const int64_t j = static_cast<int64_t>(n0) + col;
         const Sum *from[kMaxSplit];
 #pragma unroll
@@ -291,9 +310,8 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             from[q] = ksplit > 1 && q < ksplit ? cluster.map_shared_rank(part, q) : part;
         if (j < p.n) {
             const float sb = kCodes && p.scale_b != nullptr ? __ldg(p.scale_b + j) : 1.f;
-            const int step = kCodes ? ksplit : 2 * ksplit;
 #pragma unroll 2
-            for (int tk = kCodes ? rank : 2 * rank + (t >> 6); tk < tokens; tk += step) {
+            for (int tk = kDown * rank + first; tk < tokens; tk += kDown * ksplit) {
                 const int64_t i = t0 + tk;
                 TC *const out = static_cast<TC *>(p.c) + i * p.ldc + j;
                 if constexpr (kCodes) {
@@ -348,7 +366,7 @@ cudaError_t few_n(const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(R::kThreads);
     cfg.dynamicSmemBytes = R::kSmemBytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -370,6 +388,9 @@ cudaError_t few_t(int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaS
     case 32: return few_n<TC, kFmt, kCodes, 32>(maps, p, s);
     case 64: return few_n<TC, kFmt, kCodes, 64>(maps, p, s);
     case 128: return few_n<TC, kFmt, kCodes, 128>(maps, p, s);
+    case 256:
+        if constexpr (kCodes) return few_n<TC, kFmt, kCodes, 256>(maps, p, s);
+        return cudaErrorInvalidValue;
     default: return cudaErrorInvalidValue;
     }
 }
@@ -379,20 +400,24 @@ cudaError_t few_t(int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaS
 int few_tc_rows(bool codes) { return codes ? kBM : kBM / 2; }
 
 namespace {
-int tile_tokens(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
-int ctas_per_sm(bool codes, int tokens) { return codes && tokens == 128 ? 1 : 2; }
+int tile_tokens(bool codes, int64_t m) {
+    return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= 128 || !codes ? 128 : 256;
+}
+int ctas_per_sm(bool codes, int tokens) { return codes && tokens >= 128 ? 1 : 2; }
 // code blocks that one CTA's accumulators take
 int64_t code_blocks(int tokens) { return (ctas_per_sm(true, tokens) == 1 ? 512 : 256) / tokens * kChunk; }
 }  // namespace
 
 bool few_tc_takes(bool codes, int64_t m, int64_t n, int64_t k) {
-    if (m > 128) return false;
-    return !codes || (k + 127) / 128 <= kMaxSplit * code_blocks(tile_tokens(m));
+    if (m > (codes ? kFewCodeRows : 128)) return false;
+    return !codes || (k + 127) / 128 <= kMaxSplit * code_blocks(tile_tokens(true, m));
 }
+// whether the tokens' codes come as f16, in boxes of 64 k, rather than as bytes
+bool few_tc_half_tokens(int64_t m) { return tile_tokens(true, m) >= 64; }
 
 // The tokens of a tile; sets the CTAs that share its contraction and the columns of tensor memory.
 int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p) {
-    const int tokens = tile_tokens(m);
+    const int tokens = tile_tokens(codes, m);
     p->token_blocks = static_cast<int32_t>((m + tokens - 1) / tokens);
     const int64_t rows = few_tc_rows(codes), tiles = (n + rows - 1) / rows * p->token_blocks;
     const int64_t kb = codes ? (k + 127) / 128 : (k + 63) / 64;

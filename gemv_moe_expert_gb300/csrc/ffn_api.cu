@@ -83,12 +83,17 @@ void few_params(FewTcParams *p, void *c, int64_t ldc, int64_t m, int64_t n, int6
     p->wait_limit_ns = kWaitLimitNs;
 }
 
-// How an 8-bit product runs: dot products of bytes; bytes that become f16 inside the kernel (rows that TMA cannot
-// read are laid out again first); or both operands as f16 in the scratch.
-enum class I8Route { kDot, kFew, kTiles };
-I8Route i8_route(int64_t m, int64_t n, int64_t k) {
-    if (m <= kDotRows || n == 0 || k == 0) return I8Route::kDot;
-    return few_tc_takes(true, m, n, k) ? I8Route::kFew : I8Route::kTiles;
+// How an 8-bit product runs: dot products of bytes; bytes that become f16 inside the kernel, those of a as f16 from
+// the scratch once there are many tokens; or both operands as f16 in the scratch.  What is laid out again there: 0
+// nothing, 1 bytes (rows that TMA cannot read), 2 f16.
+struct I8Plan {
+    enum { kDot, kFew, kTiles } route;
+    int a_size, b_size;
+};
+I8Plan i8_plan(int64_t m, int64_t n, int64_t k, bool a_aligned, bool b_aligned) {
+    if (m <= kDotRows || n == 0 || k == 0) return {I8Plan::kDot, 0, 0};
+    if (!few_tc_takes(true, m, n, k)) return {I8Plan::kTiles, 2, 2};
+    return {I8Plan::kFew, few_tc_half_tokens(m) ? 2 : a_aligned ? 0 : 1, b_aligned ? 0 : 1};
 }
 
 gbmm_status check_gated(const char *fn, gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n, int64_t k) {
@@ -144,7 +149,9 @@ gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n,
                            {"scratch", scratch, scratch ? scratch_bytes : 0, 1, true}};
     st = check_operands(fn, ops, 7);
     if (st != GBMM_OK) return st;
-    const bool tiles16 = dt != GBMM_F32 && m > kDotRows && k > 0;
+    // 16-bit rows that TMA can read go to the tensor cores from two rows on
+    const bool aligned = dt != GBMM_F32 && rows16(x, ldx * 2) && rows16(w_gate, ldw * 2) && rows16(w_up, ldw * 2);
+    const bool tiles16 = dt != GBMM_F32 && m > (aligned ? 1 : kDotRows) && k > 0;
     Parts parts;
     Laid lx{}, lg{}, lu{};
     if (tiles16) {
@@ -390,12 +397,11 @@ gbmm_status gbmm_gemm_i8_scratch_bytes(int64_t m, int64_t n, int64_t k, int alig
         return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: m and n must lie in [0, 2^31), k in [0, %d]", fn, GBMM_I8_MAX_K);
     if (bytes == nullptr) return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: bytes is null", fn);
     *bytes = 0;
-    const I8Route route = i8_route(m, n, k);
-    if (route == I8Route::kDot || (route == I8Route::kFew && aligned)) return GBMM_OK;
-    const int size = route == I8Route::kFew ? 1 : 2;
+    const I8Plan plan = i8_plan(m, n, k, aligned != 0, aligned != 0);
+    if (plan.a_size == 0 && plan.b_size == 0) return GBMM_OK;
     Parts parts;
-    parts.add(m, round_up(k, 16 / size), size);
-    parts.add(n, round_up(k, 16 / size), size);
+    if (plan.a_size) parts.add(m, round_up(k, 16 / plan.a_size), plan.a_size);
+    if (plan.b_size) parts.add(n, round_up(k, 16 / plan.b_size), plan.b_size);
     *bytes = parts.bytes;
     return GBMM_OK;
 }
@@ -416,15 +422,11 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
     uint64_t ab, bb, cb;
     if (!span(m, k, lda, 1, &ab) || !span(n, k, ldb, 1, &bb) || !span(m, n, ldc, size, &cb))
         return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: operand extent overflows", fn);
-    const I8Route route = i8_route(m, n, k);
-    // both operands' rows laid out again in the scratch, as f16 or (where TMA cannot read them) as bytes
-    const int size2 = route == I8Route::kFew ? 1 : 2;
-    const int64_t ld = round_up(k, 16 / size2);
-    const bool again_a = route == I8Route::kTiles || (route == I8Route::kFew && !rows16(a, lda));
-    const bool again_b = route == I8Route::kTiles || (route == I8Route::kFew && !rows16(b, ldb));
+    const I8Plan plan = i8_plan(m, n, k, rows16(a, lda), rows16(b, ldb));
+    const int64_t lda2 = plan.a_size ? round_up(k, 16 / plan.a_size) : lda, ldb2 = plan.b_size ? round_up(k, 16 / plan.b_size) : ldb;
     Parts parts;
-    const uint64_t a_at = again_a ? parts.add(m, ld, size2) : 0, b_at = again_b ? parts.add(n, ld, size2) : 0;
-    const uint64_t need = again_a || again_b ? parts.bytes : 0;
+    const uint64_t a_at = plan.a_size ? parts.add(m, lda2, plan.a_size) : 0, b_at = plan.b_size ? parts.add(n, ldb2, plan.b_size) : 0;
+    const uint64_t need = plan.a_size || plan.b_size ? parts.bytes : 0;
     const Operand ops[] = {matrix("a", a, ab, k, lda, 1, false),
                            {"scale_a", scale_a, scale_a ? static_cast<uint64_t>(m) * 4 : 0, 4, false},
                            matrix("b", b, bb, k, ldb, 1, false),
@@ -438,43 +440,48 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
                     (unsigned long long)(scratch ? scratch_bytes : 0));
     if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
     cudaStream_t s = cuda_stream(stream);
-    if (route == I8Route::kDot) {
+    if (plan.route == I8Plan::kDot) {
         const GemmI8Params p{a, b, scale_a, scale_b, c, m, n, k, lda, ldb, ldc};
         return finish_launch(launch_gemm_i8_dot(dt, p, s), fn, s);
     }
-    const RepackParams ra{a, Parts::base(scratch) + a_at, m, k, lda, ld}, rb{b, Parts::base(scratch) + b_at, n, k, ldb, ld};
-    if (route == I8Route::kFew) {
-        FewTcMaps maps{};
-        FewTcParams q{};
-        few_params(&q, c, ldc, m, n, k);
+    const void *const a2 = plan.a_size ? Parts::base(scratch) + a_at : static_cast<const void *>(a);
+    const void *const b2 = plan.b_size ? Parts::base(scratch) + b_at : static_cast<const void *>(b);
+    auto lay_out = [&](const int8_t *from, const void *to, int64_t rows, int64_t ld, int64_t ld2, int to_size) {
+        if (to_size == 0) return GBMM_OK;
+        const RepackParams r{from, const_cast<void *>(to), rows, k, ld, ld2};
+        return finish_launch(to_size == 2 ? launch_codes_to_f16(r, s) : launch_repack8(r, s), fn, s);
+    };
+    FewTcMaps few{};
+    FewTcParams fp{};
+    PairTcMaps maps{};
+    PairTcParams q{};
+    uint32_t tokens = 0;
+    bool ok;
+    if (plan.route == I8Plan::kFew) {
+        few_params(&fp, c, ldc, m, n, k);
+        fp.scale_a = scale_a;
+        fp.scale_b = scale_b;
+        tokens = static_cast<uint32_t>(few_tc_plan(true, m, n, k, device_sm_count(), &fp));
+        ok = fp.err != nullptr && encode_matrix8(&few.w[0], b2, k, n, ldb2, static_cast<uint32_t>(few_tc_rows(true))) &&
+             (plan.a_size == 2 ? encode_matrix16(&few.x, GBMM_F16, a2, k, m, lda2, tokens)
+                               : encode_matrix8(&few.x, a2, k, m, lda2, tokens));
+        few.w[1] = few.w[0];
+    } else {
+        const uint32_t rows = static_cast<uint32_t>(pair_tc_rows());
+        ok = pair_params(&q, &maps, dt, c, ldc, m, n, k) && encode_matrix16(&maps.a[0], GBMM_F16, a2, k, m, lda2, rows) &&
+             encode_matrix16(&maps.b[0], GBMM_F16, b2, k, n, ldb2, rows);
+        maps.a[1] = maps.a[0];
+        maps.b[1] = maps.b[0];
         q.scale_a = scale_a;
         q.scale_b = scale_b;
-        const uint32_t tokens = static_cast<uint32_t>(few_tc_plan(true, m, n, k, device_sm_count(), &q));
-        if (q.err == nullptr || !encode_matrix8(&maps.x, again_a ? ra.dst : a, k, m, again_a ? ld : lda, tokens) ||
-            !encode_matrix8(&maps.w[0], again_b ? rb.dst : b, k, n, again_b ? ld : ldb,
-                            static_cast<uint32_t>(few_tc_rows(true))))
-            return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
-        maps.w[1] = maps.w[0];
-        if (again_a) st = finish_launch(launch_repack8(ra, s), fn, s);
-        if (st == GBMM_OK && again_b) st = finish_launch(launch_repack8(rb, s), fn, s);
-        if (st != GBMM_OK) return st;
-        return finish_launch(launch_gemm_i8_few(dt, static_cast<int>(tokens), maps, q, s), fn, s);
     }
-    PairTcMaps maps{};
-    PairTcParams q;
-    const uint32_t rows = static_cast<uint32_t>(pair_tc_rows());
-    if (!pair_params(&q, &maps, dt, c, ldc, m, n, k) ||
-        !encode_matrix16(&maps.a[0], GBMM_F16, ra.dst, k, m, ld, rows) ||
-        !encode_matrix16(&maps.b[0], GBMM_F16, rb.dst, k, n, ld, rows))
-        return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
-    maps.a[1] = maps.a[0];
-    maps.b[1] = maps.b[0];
-    q.scale_a = scale_a;
-    q.scale_b = scale_b;
-    st = finish_launch(launch_codes_to_f16(ra, s), fn, s);
-    if (st == GBMM_OK) st = finish_launch(launch_codes_to_f16(rb, s), fn, s);
+    if (!ok) return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
+    st = lay_out(a, a2, m, lda, lda2, plan.a_size);
+    if (st == GBMM_OK) st = lay_out(b, b2, n, ldb, ldb2, plan.b_size);
     if (st != GBMM_OK) return st;
-    return finish_launch(launch_gemm_i8_tc(dt, maps, q, device_sm_count(), s), fn, s);
+    return finish_launch(plan.route == I8Plan::kFew ? launch_gemm_i8_few(dt, static_cast<int>(tokens), few, fp, s)
+                                                    : launch_gemm_i8_tc(dt, maps, q, device_sm_count(), s),
+                         fn, s);
 }
 
 }  // extern "C"

@@ -344,6 +344,7 @@ int pair_tc_rows();
 int pair_tc_block_k();
 int few_tc_rows(bool codes);
 bool few_tc_takes(bool codes, int64_t m, int64_t n, int64_t k);
+bool few_tc_half_tokens(int64_t m);
 int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p);
 cudaError_t launch_gated_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s);
 cudaError_t launch_gemm_i8_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s);
