@@ -2,11 +2,11 @@
 // y^T = W x^T: the weights' rows are the MMA's M side (128 a tile), the tokens its N side (kN).
 //   gated   h = act(x Wg^T) * (x Wu^T): 64 rows of Wg and the same 64 of Wu share a tile, so an output's two
 //           projections lie 64 rows apart
-//   codes   c = (a b^T) scale_a scale_b for 8-bit codes: the weights' codes reach shared memory as bytes and eight
-//           warps write them as f16 (exact) into the tiles that the MMAs read; so do the tokens' up to 32 of them, more
-//           come as f16 (they would cost as much as the weights).  Each 1024 of k has an accumulator of its own:
-//           sums of products of two codes are exact up to there (2^24), and the accumulators are added as integers
-//           at the end.
+//   codes   c = (a b^T) scale_a scale_b for 8-bit codes: the weights' codes reach shared memory as bytes, and eight
+//           warps write them as f16 (exact) into tensor memory, from where the MMAs take their A operand; the
+//           tokens' codes become f16 in shared memory, or come as f16 from 64 tokens on.  Each 1024 of k has an
+//           accumulator of its own: sums of products of two codes are exact up to there (2^24), and the accumulators are
+//           added as integers at the end.
 // Every weight byte is read once (per kN tokens), and the kernel is bound by that stream; two CTAs share an SM
 // where the ring allows, and the contraction is split over a thread-block cluster of up to eight CTAs where the tiles
 // are few.  Each CTA leaves its partial sums in its own (by then idle) ring, and after a cluster barrier every CTA adds
@@ -40,15 +40,19 @@ struct Ring {
     static constexpr int kThreads = 64 + 32 * kWarps;
     static constexpr bool kHalfX = kCodes && kN >= 64;  // the tokens' codes come as f16
     static constexpr uint32_t kXBytes = kN * 128;       // 64 16-bit values or 128 codes of each token
-    // a stage: a k-block as TMA brings it; codes: a slot of 64 k in f16 (a stage fills two)
+    // a stage: a k-block as TMA brings it
     static constexpr uint32_t kStageBytes = kWBytes + (kHalfX ? 2 : 1) * kXBytes;
-    static constexpr uint32_t kSlotBytes = kWBytes + (kHalfX ? 0 : kXBytes);
-    static constexpr int kStages = kCodes ? (kN <= 16 ? 3 : kN == 128 ? 3 : 2) : (kN <= 16 ? 6 : kN == 32 ? 5 : kN == 64 ? 4 : 3);
-    static constexpr int kSlots = !kCodes ? 0 : (kN <= 32 ? 3 : kN == 64 ? 2 : kN == 128 ? 4 : 3);
+    static constexpr int kStages = kCodes ? (kN <= 16 ? 5 : kN <= 32 ? 4 : kN == 64 ? 3 : 4)
+                                          : (kN <= 16 ? 6 : kN == 32 ? 5 : kN == 64 ? 4 : 3);
+    // codes: slots for a k-block in f16, the weights' kSlotCols columns of tensor memory, the tokens' kSlotBytes
+    static constexpr int kSlots = kCodes ? 2 : 0;
+    static constexpr uint32_t kSlotCols = 64;
+    static constexpr uint32_t kSlotBytes = kHalfX ? 0 : 2 * kXBytes;
     static constexpr uint32_t kSlot0 = kStages * kStageBytes;
     static constexpr uint32_t kRingBytes = kSlot0 + kSlots * kSlotBytes;
     static constexpr uint32_t kBarBytes = 256;
     static constexpr uint32_t kSmemBytes = kRingBytes + kBarBytes + 1024;
+    static_assert(kSlots * kSlotCols == (kCodes ? 128 : 0), "few_tc_plan() counts them");
     static_assert(kStageBytes % 1024 == 0 && kSlotBytes % 1024 == 0, "swizzled tiles need 1024-byte alignment");
     static_assert(kBM * kN * 4 <= kRingBytes, "the partial sums are parked in the ring");
     static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
@@ -65,34 +69,29 @@ __device__ __forceinline__ uint2 codes_to_half(uint32_t w) {
     return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-// Half h (64 codes) of each of kRows 128-byte rows at `raw`, as f16 at `dst`; both 128-byte swizzled.
-// Thread t of 256 takes row t % kRows, so that eight neighbours' 16-byte accesses fall into different banks.
+__device__ __forceinline__ void load16(uint32_t at, uint32_t (&v)[4]) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
+}
+
+// The 128 codes of each of kRows tokens at `raw`, as f16 in two tiles of 64 at `dst`; all 128-byte swizzled.
+// Thread t of 256 takes rows t % kRows, so that eight neighbours' 16-byte accesses fall into different banks.
 template <int kRows>
-__device__ __forceinline__ void convert(uint32_t raw, uint32_t dst, int h, int t) {
-    constexpr int kPieces = (kRows * 4 + 255) / 256;
-    uint32_t v[kPieces][4];
+__device__ __forceinline__ void convert_tokens(uint32_t raw, uint32_t dst, int t) {
+    static_assert(kRows * 8 <= 256, "one piece a thread");
+    if (t >= kRows * 8) return;
+    const int row = t % kRows, c = t / kRows;
+    uint32_t v[4];
+    load16(raw + row * 128 + ((c ^ (row & 7)) << 4), v);
+    const uint32_t to = dst + (c >> 2) * (kRows * 128) + row * 128;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-        const int id = t + 256 * i;
-        if (kRows * 4 % 256 != 0 && id >= kRows * 4) break;
-        const int row = id % kRows, c = id / kRows;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
-                     : "r"(raw + row * 128 + (((4 * h + c) ^ (row & 7)) << 4))
+    for (int e = 0; e < 2; ++e) {
+        const uint2 a = codes_to_half(v[2 * e]), b = codes_to_half(v[2 * e + 1]);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((2 * (c & 3) + e) ^ (row & 7)) << 4)),
+                     "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y)
                      : "memory");
-    }
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-        const int id = t + 256 * i;
-        if (kRows * 4 % 256 != 0 && id >= kRows * 4) break;
-        const int row = id % kRows, c = id / kRows;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint2 a = codes_to_half(v[i][2 * e]), b = codes_to_half(v[i][2 * e + 1]);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * 128 + (((2 * c + e) ^ (row & 7)) << 4)),
-                         "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y)
-                         : "memory");
-        }
     }
 }
 
@@ -152,15 +151,13 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = *tmem_slot, acc_base = tmem_base + kSlots * R::kSlotCols;
     grid_dep_begin();
     // this CTA's share of the k-blocks (128 bytes of a row each)
     constexpr int kBlock = kCodes ? 128 : 64;
     const int kb_total = (p.k + kBlock - 1) / kBlock;
     const int kb0 = static_cast<int>(static_cast<int64_t>(kb_total) * rank / ksplit);
     const int kblocks = static_cast<int>(static_cast<int64_t>(kb_total) * (rank + 1) / ksplit) - kb0;
-    // the MMA warp's steps: a k-block, or half of one (64 codes)
-    const int steps = kCodes ? 2 * kblocks : kblocks;
 
     auto fail = [&]() {
         *abort_flag = 1;
@@ -202,27 +199,35 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         if (lane == 0) {
             // ---------------- MMA issuer ----------------
             constexpr uint32_t kIdesc = idesc_f16(kFmt, kBM, kN);
-            constexpr int kDepth = kCodes ? kSlots : kStages;
             bool ok = true;
-            for (int i = 0; i < steps; ++i) {
-                const int at = i % kDepth;
-                const int stage = (kCodes ? i >> 1 : i) % kStages;
-                const uint32_t stage_phase = static_cast<uint32_t>((kCodes ? i >> 1 : i) / kStages) & 1u;
-                ok = !kCodes || mbar_wait_bounded(slot_full(at), static_cast<uint32_t>(i / kDepth) & 1u, lim, abort_flag);
-                if (ok && (!kCodes || R::kHalfX)) ok = mbar_wait_bounded(full_bar(stage), stage_phase, lim, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t sw = kCodes ? s0 + R::kSlot0 + at * R::kSlotBytes : s0 + at * R::kStageBytes;
-                const uint32_t sx = R::kHalfX ? s0 + stage * R::kStageBytes + kWBytes + (i & 1) * R::kXBytes : sw + kWBytes;
-                const int chunk = kCodes ? i / (2 * kChunk) : 0;
-                const uint32_t d = tmem_base + static_cast<uint32_t>(chunk * kN);
-                const bool fresh = kCodes ? i % (2 * kChunk) == 0 : i == 0;
+            for (int kb = 0; kb < kblocks; ++kb) {
+                const int stage = kb % kStages;
+                const uint32_t stage_at = s0 + stage * R::kStageBytes;
+                if (!kCodes || R::kHalfX)
+                    ok = mbar_wait_bounded(full_bar(stage), static_cast<uint32_t>(kb / kStages) & 1u, lim, abort_flag);
+                if constexpr (kCodes) {
+                    const int slot = kb % kSlots;
+                    ok = ok && mbar_wait_bounded(slot_full(slot), static_cast<uint32_t>(kb / kSlots) & 1u, lim, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = acc_base + static_cast<uint32_t>(kb / kChunk * kN);
+                    const uint32_t sx = R::kHalfX ? stage_at + kWBytes : s0 + R::kSlot0 + slot * R::kSlotBytes;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    umma_f16_ss(d, sdesc_kmajor_sw128(sw + kk * 32), sdesc_kmajor_sw128(sx + kk * 32), kIdesc,
-                                fresh && kk == 0 ? 0u : 1u);
-                umma_commit(kCodes ? slot_empty(at) : empty_bar(at));
-                if (R::kHalfX && (i & 1) == 1) umma_commit(empty_bar(stage));
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_f16_ts(d, tmem_base + slot * R::kSlotCols + kk * 8,
+                                    sdesc_kmajor_sw128(sx + (kk >> 2) * R::kXBytes + (kk & 3) * 32), kIdesc,
+                                    kb % kChunk == 0 && kk == 0 ? 0u : 1u);
+                    umma_commit(slot_empty(slot));
+                    if (R::kHalfX) umma_commit(empty_bar(stage));
+                } else {
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16_ss(acc_base, sdesc_kmajor_sw128(stage_at + kk * 32),
+                                    sdesc_kmajor_sw128(stage_at + kWBytes + kk * 32), kIdesc, kb == 0 && kk == 0 ? 0u : 1u);
+                    umma_commit(empty_bar(stage));
+                }
             }
             if (ok) umma_commit(tfull_bar);
             else fail();
@@ -233,29 +238,46 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     } else if constexpr (kCodes) {
         // ---------------- codes to f16 ----------------
         const int t = threadIdx.x - 64;
-        for (int i = 0; i < steps; ++i) {
-            const int kb = i >> 1, h = i & 1, stage = kb % kStages, slot = i % kSlots;
+        const int quarter = warp & 3, half = (warp - 2) >> 2;  // this warp's lanes, and its 64 of the 128 codes
+        const int row = quarter * 32 + lane;
+        for (int kb = 0; kb < kblocks; ++kb) {
+            const int stage = kb % kStages, slot = kb % kSlots;
+            const uint32_t phase = static_cast<uint32_t>(kb / kStages) & 1u, use = static_cast<uint32_t>(kb / kSlots);
             int ready = 1;
-            if (lane == 0) {
-                if (h == 0) ready = mbar_wait_bounded(full_bar(stage), static_cast<uint32_t>(kb / kStages) & 1u, lim, abort_flag);
-                const uint32_t use = static_cast<uint32_t>(i / kSlots);
-                if (ready && use > 0) ready = mbar_wait_bounded(slot_empty(slot), (use - 1u) & 1u, lim, abort_flag);
+            if (lane == 0) ready = mbar_wait_bounded(full_bar(stage), phase, lim, abort_flag);
+            ready = __shfl_sync(0xffffffffu, ready, 0);
+            // every lane orders the bytes that TMA wrote before its own reads
+            if (ready && lane != 0) mbar_try_wait(full_bar(stage), phase);
+            uint32_t v[4][4], w[32];
+            if (ready) {
+                const uint32_t from = s0 + stage * R::kStageBytes + row * 128;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) load16(from + (((4 * half + c) ^ (row & 7)) << 4), v[c]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint2 h = codes_to_half(v[i >> 2][i & 3]);
+                    w[2 * i] = h.x;
+                    w[2 * i + 1] = h.y;
+                }
+                if (lane == 0 && use > 0) ready = mbar_wait_bounded(slot_empty(slot), (use - 1u) & 1u, lim, abort_flag);
             }
             ready = __shfl_sync(0xffffffffu, ready, 0);
             if (!ready) {
                 if (lane == 0) fail();
                 break;
             }
-            // every lane orders the bytes that TMA wrote before its own reads
-            if (h == 0 && lane != 0) mbar_try_wait(full_bar(stage), static_cast<uint32_t>(kb / kStages) & 1u);
-            const uint32_t from = s0 + stage * R::kStageBytes, to = s0 + R::kSlot0 + slot * R::kSlotBytes;
-            convert<kBM>(from, to, h, t);
-            if constexpr (!R::kHalfX) convert<kN>(from + kWBytes, to + kWBytes, h, t);
-            fence_async_smem();
+            tc_fence_after();
+            tmem_st32(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + slot * R::kSlotCols + half * 32, w);
+            if constexpr (!R::kHalfX) {
+                convert_tokens<kN>(s0 + stage * R::kStageBytes + kWBytes, s0 + R::kSlot0 + slot * R::kSlotBytes, t);
+                fence_async_smem();
+            }
+            tmem_st_wait();
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(slot_full(slot));
-                if (!R::kHalfX && h == 1) mbar_arrive(empty_bar(stage));
+                if (!R::kHalfX) mbar_arrive(empty_bar(stage));
             }
         }
     }
@@ -282,7 +304,7 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             for (int e = 0; e < 16; ++e) v[e] = 0;
             for (int c = 0; c < chunks; ++c) {
                 uint32_t r[16];
-                tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c * kN + j), r);
+                tmem_ld16(acc_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c * kN + j), r);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -304,35 +326,38 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         constexpr int kAcross = kRows, kDown = 32 * kWarps / kAcross;
         const int col = t % kAcross, first = t / kAcross;
         const int64_t j = static_cast<int64_t>(n0) + col;
-        const Sum *from[kMaxSplit];
-#pragma unroll
-        for (int q = 0; q < kMaxSplit; ++q)
-            from[q] = ksplit > 1 && q < ksplit ? cluster.map_shared_rank(part, q) : part;
         if (j < p.n) {
             const float sb = kCodes && p.scale_b != nullptr ? __ldg(p.scale_b + j) : 1.f;
-#pragma unroll 2
-            for (int tk = kDown * rank + first; tk < tokens; tk += kDown * ksplit) {
-                const int64_t i = t0 + tk;
-                TC *const out = static_cast<TC *>(p.c) + i * p.ldc + j;
-                if constexpr (kCodes) {
-                    int s = 0;
+            // eight tokens at a time, so that as many reads of another CTA's sums are under way
+            constexpr int kB = 8;
+            for (int tk0 = kDown * rank + first; tk0 < tokens; tk0 += kB * kDown * ksplit) {
+                Sum g[kB], u[kB];
 #pragma unroll
-                    for (int q = 0; q < kMaxSplit; ++q)
-                        if (q < ksplit) s += from[q][tk * kBM + col];
-                    const float sa = p.scale_a != nullptr ? __ldg(p.scale_a + i) : 1.f;
-                    *out = Elem<TC>::from_f(static_cast<float>(s) * sa * sb);
-                } else {
-                    float g = 0.f, u = 0.f;
+                for (int e = 0; e < kB; ++e) g[e] = u[e] = 0;
+                for (int q = 0; q < ksplit; ++q) {
+                    const Sum *from = (ksplit > 1 ? cluster.map_shared_rank(part, q) : part) + col;
 #pragma unroll
-                    for (int q = 0; q < kMaxSplit; ++q)
-                        if (q < ksplit) {
-                            g += from[q][tk * kBM + col];
-                            u += from[q][tk * kBM + 64 + col];
+                    for (int e = 0; e < kB; ++e) {
+                        const int tk = min(tk0 + e * kDown * ksplit, tokens - 1);
+                        g[e] += from[tk * kBM];
+                        if constexpr (!kCodes) u[e] += from[tk * kBM + 64];
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < kB; ++e) {
+                    const int tk = tk0 + e * kDown * ksplit;
+                    if (tk >= tokens) break;
+                    const int64_t i = t0 + tk;
+                    TC *const out = static_cast<TC *>(p.c) + i * p.ldc + j;
+                    if constexpr (kCodes) {
+                        const float sa = p.scale_a != nullptr ? __ldg(p.scale_a + i) : 1.f;
+                        *out = Elem<TC>::from_f(static_cast<float>(g[e]) * sa * sb);
+                    } else {
+                        *out = Elem<TC>::from_f(gate_act_16(p.act, g[e]) * u[e]);
+                        if (p.saved[0] != nullptr) {
+                            static_cast<TC *>(p.saved[0])[i * p.ld_saved + j] = Elem<TC>::from_f(g[e]);
+                            static_cast<TC *>(p.saved[1])[i * p.ld_saved + j] = Elem<TC>::from_f(u[e]);
                         }
-                    *out = Elem<TC>::from_f(gate_act_16(p.act, g) * u);
-                    if (p.saved[0] != nullptr) {
-                        static_cast<TC *>(p.saved[0])[i * p.ld_saved + j] = Elem<TC>::from_f(g);
-                        static_cast<TC *>(p.saved[1])[i * p.ld_saved + j] = Elem<TC>::from_f(u);
                     }
                 }
             }
@@ -388,9 +413,6 @@ cudaError_t few_t(int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaS
     case 32: return few_n<TC, kFmt, kCodes, 32>(maps, p, s);
     case 64: return few_n<TC, kFmt, kCodes, 64>(maps, p, s);
     case 128: return few_n<TC, kFmt, kCodes, 128>(maps, p, s);
-    case 256:
-        if constexpr (kCodes) return few_n<TC, kFmt, kCodes, 256>(maps, p, s);
-        return cudaErrorInvalidValue;
     default: return cudaErrorInvalidValue;
     }
 }
@@ -400,24 +422,23 @@ cudaError_t few_t(int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaS
 int few_tc_rows(bool codes) { return codes ? kBM : kBM / 2; }
 
 namespace {
-int tile_tokens(bool codes, int64_t m) {
-    return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= 128 || !codes ? 128 : 256;
-}
-int ctas_per_sm(bool codes, int tokens) { return codes && tokens >= 128 ? 1 : 2; }
+int tile_tokens(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
+int ctas_per_sm(bool codes, int tokens) { return codes && tokens == 128 ? 1 : 2; }
+constexpr int kCodeCols = 128;  // columns of tensor memory that hold weights
 // code blocks that one CTA's accumulators take
-int64_t code_blocks(int tokens) { return (ctas_per_sm(true, tokens) == 1 ? 512 : 256) / tokens * kChunk; }
+int64_t code_blocks(int tokens) { return ((ctas_per_sm(true, tokens) == 1 ? 512 : 256) - kCodeCols) / tokens * kChunk; }
 }  // namespace
 
 bool few_tc_takes(bool codes, int64_t m, int64_t n, int64_t k) {
     if (m > (codes ? kFewCodeRows : 128)) return false;
-    return !codes || (k + 127) / 128 <= kMaxSplit * code_blocks(tile_tokens(true, m));
+    return !codes || (k + 127) / 128 <= kMaxSplit * code_blocks(tile_tokens(m));
 }
 // whether the tokens' codes come as f16, in boxes of 64 k, rather than as bytes
-bool few_tc_half_tokens(int64_t m) { return tile_tokens(true, m) >= 64; }
+bool few_tc_half_tokens(int64_t m) { return tile_tokens(m) >= 64; }
 
 // The tokens of a tile; sets the CTAs that share its contraction and the columns of tensor memory.
 int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p) {
-    const int tokens = tile_tokens(codes, m);
+    const int tokens = tile_tokens(m);
     p->token_blocks = static_cast<int32_t>((m + tokens - 1) / tokens);
     const int64_t rows = few_tc_rows(codes), tiles = (n + rows - 1) / rows * p->token_blocks;
     const int64_t kb = codes ? (k + 127) / 128 : (k + 63) / 64;
@@ -429,7 +450,7 @@ int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcP
     int64_t cols = tokens;
     if (codes) {
         while (split < kMaxSplit && (kb + split - 1) / split > code_blocks(tokens)) ++split;
-        cols = ((kb + split - 1) / split + kChunk - 1) / kChunk * tokens;
+        cols = kCodeCols + ((kb + split - 1) / split + kChunk - 1) / kChunk * tokens;
     }
     p->tmem_cols = 32;
     while (p->tmem_cols < cols) p->tmem_cols *= 2;
