@@ -30,7 +30,13 @@ namespace {
 
 constexpr int kBM = 128;
 constexpr int kMaxSplit = 8;
-constexpr int64_t kFewCodeRows = 512;  // tokens of an 8-bit product that run here
+#ifndef V_FEW
+#define V_FEW 512
+#endif
+#ifndef V_TT
+#define V_TT 128
+#endif
+constexpr int64_t kFewCodeRows = V_FEW;  // tokens of an 8-bit product that run here
 constexpr uint32_t kWBytes = kBM * 128;  // 128 rows of 128 bytes: 64 16-bit values or 128 codes
 constexpr int kChunk = 8;                // code blocks (of 128) whose sums stay exact: 1024 of k
 
@@ -77,21 +83,23 @@ __device__ __forceinline__ void load16(uint32_t at, uint32_t (&v)[4]) {
 }
 
 // The 128 codes of each of kRows tokens at `raw`, as f16 in two tiles of 64 at `dst`; all 128-byte swizzled.
-// Thread t of 256 takes rows t % kRows, so that eight neighbours' 16-byte accesses fall into different banks.
+// Thread t of 128 takes rows t % kRows, so that eight neighbours' 16-byte accesses fall into different banks.
 template <int kRows>
 __device__ __forceinline__ void convert_tokens(uint32_t raw, uint32_t dst, int t) {
-    static_assert(kRows * 8 <= 256, "one piece a thread");
-    if (t >= kRows * 8) return;
-    const int row = t % kRows, c = t / kRows;
-    uint32_t v[4];
-    load16(raw + row * 128 + ((c ^ (row & 7)) << 4), v);
-    const uint32_t to = dst + (c >> 2) * (kRows * 128) + row * 128;
+    static_assert(kRows * 8 % 128 == 0, "whole turns");
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const uint2 a = codes_to_half(v[2 * e]), b = codes_to_half(v[2 * e + 1]);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((2 * (c & 3) + e) ^ (row & 7)) << 4)),
-                     "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y)
-                     : "memory");
+    for (int i = 0; i < kRows * 8 / 128; ++i) {
+        const int row = (t + 128 * i) % kRows, c = (t + 128 * i) / kRows;
+        uint32_t v[4];
+        load16(raw + row * 128 + ((c ^ (row & 7)) << 4), v);
+        const uint32_t to = dst + (c >> 2) * (kRows * 128) + row * 128;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint2 a = codes_to_half(v[2 * e]), b = codes_to_half(v[2 * e + 1]);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((2 * (c & 3) + e) ^ (row & 7)) << 4)),
+                         "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y)
+                         : "memory");
+        }
     }
 }
 
@@ -128,10 +136,10 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), kCodes && !R::kHalfX ? kWarps : 1);
+            mbar_init(empty_bar(s), kCodes && !R::kHalfX ? kWarps / 2 : 1);
         }
         for (int s = 0; s < kSlots; ++s) {
-            mbar_init(slot_full(s), kWarps);
+            mbar_init(slot_full(s), kWarps / 2);
             mbar_init(slot_empty(s), 1);
         }
         mbar_init(tfull_bar, 1);
@@ -237,28 +245,24 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         }
     } else if constexpr (kCodes) {
         // ---------------- codes to f16 ----------------
-        const int t = threadIdx.x - 64;
-        const int quarter = warp & 3, half = (warp - 2) >> 2;  // this warp's lanes, and its 64 of the 128 codes
-        const int row = quarter * 32 + lane;
-        for (int kb = 0; kb < kblocks; ++kb) {
-            const int stage = kb % kStages, slot = kb % kSlots;
+        // Two groups of four warps take every other k-block, each with a slot of its own: while one waits for its bytes or
+        // for its stores to tensor memory, the other converts.
+        const int group = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const int t = (threadIdx.x - 64) & 127;
+        for (int kb = group; kb < kblocks; kb += 2) {
+            const int stage = kb % kStages, slot = group;
             const uint32_t phase = static_cast<uint32_t>(kb / kStages) & 1u, use = static_cast<uint32_t>(kb / kSlots);
             int ready = 1;
             if (lane == 0) ready = mbar_wait_bounded(full_bar(stage), phase, lim, abort_flag);
             ready = __shfl_sync(0xffffffffu, ready, 0);
             // every lane orders the bytes that TMA wrote before its own reads
             if (ready && lane != 0) mbar_try_wait(full_bar(stage), phase);
-            uint32_t v[4][4], w[32];
+            const uint32_t from = s0 + stage * R::kStageBytes + row * 128;
+            const uint32_t to = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + slot * R::kSlotCols;
+            uint32_t v[8][4];
             if (ready) {
-                const uint32_t from = s0 + stage * R::kStageBytes + row * 128;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) load16(from + (((4 * half + c) ^ (row & 7)) << 4), v[c]);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint2 h = codes_to_half(v[i >> 2][i & 3]);
-                    w[2 * i] = h.x;
-                    w[2 * i + 1] = h.y;
-                }
+                for (int c = 0; c < 8; ++c) load16(from + ((c ^ (row & 7)) << 4), v[c]);
                 if (lane == 0 && use > 0) ready = mbar_wait_bounded(slot_empty(slot), (use - 1u) & 1u, lim, abort_flag);
             }
             ready = __shfl_sync(0xffffffffu, ready, 0);
@@ -267,7 +271,17 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                 break;
             }
             tc_fence_after();
-            tmem_st32(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + slot * R::kSlotCols + half * 32, w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint2 f = codes_to_half(v[4 * h + (i >> 2)][i & 3]);
+                    w[2 * i] = f.x;
+                    w[2 * i + 1] = f.y;
+                }
+                tmem_st32(to + h * 32, w);
+            }
             if constexpr (!R::kHalfX) {
                 convert_tokens<kN>(s0 + stage * R::kStageBytes + kWBytes, s0 + R::kSlot0 + slot * R::kSlotBytes, t);
                 fence_async_smem();
@@ -328,12 +342,13 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         const int64_t j = static_cast<int64_t>(n0) + col;
         if (j < p.n) {
             const float sb = kCodes && p.scale_b != nullptr ? __ldg(p.scale_b + j) : 1.f;
-            // eight tokens at a time, so that as many reads of another CTA's sums are under way
-            constexpr int kB = 8;
+            // several tokens at a time, so that as many reads of other CTAs' sums are under way
+            constexpr int kB = 4;
             for (int tk0 = kDown * rank + first; tk0 < tokens; tk0 += kB * kDown * ksplit) {
                 Sum g[kB], u[kB];
 #pragma unroll
                 for (int e = 0; e < kB; ++e) g[e] = u[e] = 0;
+#pragma unroll 4
                 for (int q = 0; q < ksplit; ++q) {
                     const Sum *from = (ksplit > 1 ? cluster.map_shared_rank(part, q) : part) + col;
 #pragma unroll
@@ -422,7 +437,7 @@ cudaError_t few_t(int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaS
 int few_tc_rows(bool codes) { return codes ? kBM : kBM / 2; }
 
 namespace {
-int tile_tokens(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
+int tile_tokens(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : V_TT; }
 int ctas_per_sm(bool codes, int tokens) { return codes && tokens == 128 ? 1 : 2; }
 constexpr int kCodeCols = 128;  // columns of tensor memory that hold weights
 // code blocks that one CTA's accumulators take

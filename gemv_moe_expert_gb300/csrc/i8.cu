@@ -7,6 +7,10 @@ namespace gbmm {
 
 namespace {
 
+template <typename T> struct Pair;
+template <> struct Pair<__half> { using type = __half2; };
+template <> struct Pair<__nv_bfloat16> { using type = __nv_bfloat162; };
+
 bool rows_on(const void *p, int64_t ld_bytes, int unit) {
     return reinterpret_cast<uintptr_t>(p) % unit == 0 && ld_bytes % unit == 0;
 }
@@ -15,9 +19,10 @@ bool rows_on(const void *p, int64_t ld_bytes, int unit) {
 // quantisation: scale = max |x| * f32(1 / 127), code = the integer nearest to x / scale, ties to even
 //
 // A row is read once, into registers, by 32 or 256 threads (more for rows that these do not hold; a row longer than
-// 1024 threads hold is read again).  Bound by HBM, 3 bytes an element of 16 bits, so what each element costs
+// 1024 threads hold is read again).  8192 x 11008 bf16: 45 us, 6.0 TB/s; 63 us while a value within 2^-12 of a
+// middle, one of 2000, sent its thread to work all of its codes out exactly.  Bound by HBM, 3 bytes an element of 16 bits, so what each element costs
 // in instructions matters: fma(x, 1 / scale, 1.5 * 2^23) leaves the code in its low byte, and the distance to it tells
-// whether the quotient may lie on the other side of a middle; only then is the code worked out exactly.
+// whether the quotient may lie on the other side of a middle; only such a thread works its codes out exactly.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
@@ -25,14 +30,14 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // The integer nearest to x / s for |x| <= 127 s (1 + 2^-22), ties to even.  rint(x / s) in f32 is that
 // integer or, next to the middle of two, its neighbour; the remainder x - n s is exact in one fma (it
 // is a multiple of the smaller of x's and s's last places and below s), and says which.
-__device__ __noinline__ int nearest_code(float x, float s) {
+__device__ __forceinline__ int nearest_code(float x, float s) {
     float n = rintf(x / s);
     const float r = fmaf(-n, s, x), twice = 2.f * fabsf(r);
     if (twice > s || (twice == s && (static_cast<int>(n) & 1))) n += r > 0.f ? 1.f : -1.f;
     return static_cast<int>(fminf(fmaxf(n, -127.f), 127.f));
 }
 
-// What a row's scale gives: inv = 1 / scale, 0 where codes are 0 (scale 0 or NaN), and `exact` where
+// What a row's scale gives: inv = 1 / scale; live: false where every code is 0 (scale 0 or NaN); exact: true where
 // 1 / scale is out of f32's normal range.
 struct RowScale {
     float s, inv;
@@ -49,22 +54,18 @@ __device__ __forceinline__ RowScale row_scale(uint32_t most) {
     return r;
 }
 
-// Codes of four values, one a byte.  x * inv is off by 3 * 2^-24 of itself, below 2^-15: a quotient that is
-// further than 2^-12 from a middle is rounded to the side that it lies on.
-__device__ __forceinline__ uint32_t codes4(const float *v, const RowScale &r) {
+// Codes of four values of a live row, one a byte.  x * inv is off by 3 * 2^-24 of itself, 2^-15.3 at most: a quotient
+// that is further than 2^-15 from a middle is rounded to the side that it lies on.  far: the largest distance from
+// a code so far; above kNear some code has to be worked out exactly (6 values in 100000).
+constexpr float kNear = 0.5f - 0x1p-15f;
+__device__ __forceinline__ uint32_t codes4(const float *v, float inv, float &far) {
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: what is added to it is rounded to an integer
     uint32_t w[4];
-    float far = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float x = r.inv != 0.f ? v[e] : 0.f;  // no NaN or infinity from a row whose codes are 0
-        const float t = fmaf(x, r.inv, kMagic);
-        far = fmaxf(far, fabsf(fmaf(x, r.inv, -(t - kMagic))));
+        const float t = fmaf(v[e], inv, kMagic);
+        far = fmaxf(far, fabsf(fmaf(v[e], inv, kMagic - t)));
         w[e] = __float_as_uint(t);
-    }
-    if (far > 0.5f - 0x1p-12f || r.exact) {
-#pragma unroll 1
-        for (int e = 0; e < 4; ++e) w[e] = static_cast<uint32_t>(nearest_code(v[e], r.s));
     }
     return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
 }
@@ -82,28 +83,39 @@ __device__ __forceinline__ uint32_t row_max(uint32_t most) {
     return most;
 }
 
+// the largest absolute value of a piece, as bits of an f32; a NaN gives a NaN
 template <typename T>
 __device__ __forceinline__ uint32_t piece_max(const uint4 &v) {
-    float f[Elem<T>::kVec];
-    unpack16<T>(v, f);
-    uint32_t most = 0;
-#pragma unroll
-    for (int e = 0; e < Elem<T>::kVec; ++e) most = max(most, abs_bits(f[e]));
-    return most;
+    if constexpr (sizeof(T) == 4) {
+        return max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+    } else {
+        using T2 = typename Pair<T>::type;
+        const T2 *h = reinterpret_cast<const T2 *>(&v);
+        const T2 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+        return max(abs_bits(Elem<T>::to_f(m.x)), abs_bits(Elem<T>::to_f(m.y)));
+    }
 }
 
+// writes the codes of a piece; true if some of them have to be worked out exactly
 template <typename T>
-__device__ __forceinline__ void store_codes(const uint4 &v, const RowScale &r, int8_t *q) {
+__device__ __forceinline__ bool store_codes(const uint4 &v, const RowScale &r, int8_t *q) {
     constexpr int kN = Elem<T>::kVec;
-    float f[kN];
+    float f[kN], far = 0.f;
     unpack16<T>(v, f);
-    if constexpr (kN == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(codes4(f, r), codes4(f + 4, r));
-    else *reinterpret_cast<uint32_t *>(q) = codes4(f, r);
+    if constexpr (kN == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(codes4(f, r.inv, far), codes4(f + 4, r.inv, far));
+    else *reinterpret_cast<uint32_t *>(q) = codes4(f, r.inv, far);
+    return far > kNear || r.exact;
+}
+
+// the codes of n values, worked out exactly
+template <typename T>
+__device__ __noinline__ void exact_codes(const T *x, int8_t *q, int n, float s) {
+    for (int e = 0; e < n; ++e) q[e] = static_cast<int8_t>(nearest_code(Elem<T>::to_f(x[e]), s));
 }
 
 // kT threads a row, kP pieces of 16 bytes a thread; kP == 0: any length, read twice
 template <typename T, int kT, int kP>
-__global__ void __launch_bounds__(kT < 256 ? 256 : kT) quantize_kernel(const QuantizeParams p) {
+__global__ void __launch_bounds__(kT < 256 ? 256 : kT, kT <= 256 && kP <= 6 ? 5 : kT == 512 ? 2 : 1) quantize_kernel(const QuantizeParams p) {
     constexpr int kN = Elem<T>::kVec;
     grid_dep_begin();
     const int64_t i = kT < 256 ? static_cast<int64_t>(blockIdx.x) * (256 / kT) + threadIdx.x / kT : blockIdx.x;
@@ -134,14 +146,22 @@ __global__ void __launch_bounds__(kT < 256 ? 256 : kT) quantize_kernel(const Qua
     const RowScale r = row_scale(row_max<kT>(most));
     if (t == 0) p.scale[i] = r.s;
     if constexpr (kP > 0) {
+        uint32_t redo = 0;
 #pragma unroll
         for (int c = 0; c < kP; ++c) {
             const int64_t at = t + c * kT;
-            if (at < pieces) store_codes<T>(v[c], r, q + at * kN);
+            if (!r.live) v[c] = make_uint4(0, 0, 0, 0);  // no NaN or infinity
+            if (at < pieces && store_codes<T>(v[c], r, q + at * kN)) redo |= 1u << c;
+        }
+        for (; redo != 0; redo &= redo - 1) {
+            const int64_t at = (t + (__ffs(redo) - 1) * kT) * kN;
+            exact_codes<T>(x + at, q + at, kN, r.s);
         }
     } else {
-#pragma unroll 4
-        for (int64_t at = t; at < pieces; at += kT) store_codes<T>(ld_cached16(x + at * kN), r, q + at * kN);
+        for (int64_t at = t; at < pieces; at += kT) {
+            const uint4 w = r.live ? ld_cached16(x + at * kN) : make_uint4(0, 0, 0, 0);
+            if (store_codes<T>(w, r, q + at * kN)) exact_codes<T>(x + at * kN, q + at * kN, kN, r.s);
+        }
     }
     if (has_rest)
         for (int e = 0; e < rest; ++e) {
@@ -150,7 +170,7 @@ __global__ void __launch_bounds__(kT < 256 ? 256 : kT) quantize_kernel(const Qua
         }
 }
 
-// rows that start anywhere: one element an access, four in flight
+// rows that start anywhere: one element an access, eight in flight
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_any_kernel(const QuantizeParams p) {
     grid_dep_begin();
@@ -162,14 +182,16 @@ __global__ void __launch_bounds__(256) quantize_any_kernel(const QuantizeParams 
     for (int64_t c = threadIdx.x; c < p.k; c += 256) most = max(most, abs_bits(Elem<T>::to_f(x[c])));
     const RowScale r = row_scale(row_max<256>(most));
     if (threadIdx.x == 0) p.scale[i] = r.s;
-    for (int64_t c = threadIdx.x; c < p.k; c += 4 * 256) {
-        float v[4];
+    for (int64_t c = threadIdx.x; c < p.k; c += 8 * 256) {
+        float v[8], far = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = c + 256 * e < p.k ? Elem<T>::to_f(x[c + 256 * e]) : 0.f;
-        const uint32_t w = codes4(v, r);
+        for (int e = 0; e < 8; ++e) v[e] = r.live && c + 256 * e < p.k ? Elem<T>::to_f(x[c + 256 * e]) : 0.f;
+        const uint32_t w[2] = {codes4(v, r.inv, far), codes4(v + 4, r.inv, far)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + 256 * e < p.k) q[c + 256 * e] = static_cast<int8_t>(w >> (8 * e));
+        for (int e = 0; e < 8; ++e)
+            if (c + 256 * e < p.k) q[c + 256 * e] = static_cast<int8_t>(w[e / 4] >> (8 * (e % 4)));
+        if (far > kNear || r.exact)
+            for (int64_t at = c; at < c + 8 * 256 && at < p.k; at += 256) exact_codes<T>(x + at, q + at, 1, r.s);
     }
 }
 
@@ -190,6 +212,8 @@ cudaError_t quantize_t(const QuantizeParams &p, cudaStream_t s) {
     if (pieces <= 1024) return quantize_p<T, 256, 4>(p, s);
     if (pieces <= 1536) return quantize_p<T, 256, 6>(p, s);
     if (pieces <= 2048) return quantize_p<T, 256, 8>(p, s);
+    if (pieces <= 3072) return quantize_p<T, 512, 6>(p, s);
+    if (pieces <= 4096) return quantize_p<T, 512, 8>(p, s);
     if (pieces <= 8192) return quantize_p<T, 1024, 8>(p, s);
     return quantize_p<T, 1024, 0>(p, s);
 }
@@ -201,7 +225,7 @@ cudaError_t quantize_t(const QuantizeParams &p, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 
 constexpr int kDotWarps = 4;
-constexpr int kR = 2;
+constexpr int kR = 1;
 
 // the four codes at row + 4 g; the row has k codes, and what lies past them counts as 0
 __device__ __forceinline__ uint32_t any4(const int8_t *row, int64_t g, int64_t k) {
@@ -246,13 +270,16 @@ template <> struct Codes<1> {
     static __device__ __forceinline__ Codes cached(const int8_t *row, int64_t u, int64_t k) { return {any4(row, u, k)}; }
 };
 
-template <typename T, int kM, int kUnit>
+// kShare: warps of a column (1, or all of a block where there are few columns)
+template <typename T, int kM, int kUnit, int kShare>
 __global__ void __launch_bounds__(32 * kDotWarps) gemm_i8_dot_kernel(const GemmI8Params p) {
-    constexpr int kU = 4;
+    constexpr int kU = kShare > 1 ? 2 : 4;
+    constexpr int kLanes = 32 * kShare;
     constexpr int kStep = kUnit == 16 ? 16 : 4;  // codes in a unit
     grid_dep_begin();
-    const int lane = threadIdx.x & 31;
-    const int64_t j0 = (static_cast<int64_t>(blockIdx.x) * kDotWarps + (threadIdx.x >> 5)) * kR;
+    const int lane = threadIdx.x & 31, share = kShare > 1 ? threadIdx.x >> 5 : 0;
+    const int64_t j0 = kShare > 1 ? static_cast<int64_t>(blockIdx.x) * kR
+                                  : (static_cast<int64_t>(blockIdx.x) * kDotWarps + (threadIdx.x >> 5)) * kR;
     if (j0 >= p.n) return;
     const int8_t *b[kR];
 #pragma unroll
@@ -267,28 +294,28 @@ __global__ void __launch_bounds__(32 * kDotWarps) gemm_i8_dot_kernel(const GemmI
         for (int r = 0; r < kM; ++r)
 #pragma unroll
             for (int c = 0; c < kR; ++c) acc[r][c] = 0;
-        for (int64_t at = lane; at < units; at += kU * 32) {
+        for (int64_t at = 32 * share + lane; at < units; at += kU * kLanes) {
             Codes<kUnit> w[kU][kR];
 #pragma unroll
             for (int q = 0; q < kU; ++q) {
-                if (at + q * 32 >= units) break;
+                if (at + q * kLanes >= units) break;
 #pragma unroll
-                for (int c = 0; c < kR; ++c) w[q][c] = Codes<kUnit>::stream(b[c], at + q * 32, p.k);
+                for (int c = 0; c < kR; ++c) w[q][c] = Codes<kUnit>::stream(b[c], at + q * kLanes, p.k);
             }
 #pragma unroll
             for (int q = 0; q < kU; ++q) {
-                if (at + q * 32 >= units) break;
+                if (at + q * kLanes >= units) break;
 #pragma unroll
                 for (int r = 0; r < kM; ++r) {
                     if (r >= rows) break;
-                    const Codes<kUnit> v = Codes<kUnit>::cached(a + r * p.lda, at + q * 32, p.k);
+                    const Codes<kUnit> v = Codes<kUnit>::cached(a + r * p.lda, at + q * kLanes, p.k);
 #pragma unroll
                     for (int c = 0; c < kR; ++c) acc[r][c] = w[q][c].dot(v, acc[r][c]);
                 }
             }
         }
         const int64_t e = units * kStep + lane;  // less than a unit is left at the end of a row
-        if (e < p.k) {
+        if (share == 0 && e < p.k) {
 #pragma unroll
             for (int r = 0; r < kM; ++r) {
                 if (r >= rows) break;
@@ -301,6 +328,24 @@ __global__ void __launch_bounds__(32 * kDotWarps) gemm_i8_dot_kernel(const GemmI
         for (int r = 0; r < kM; ++r)
 #pragma unroll
             for (int c = 0; c < kR; ++c) acc[r][c] = __reduce_add_sync(0xffffffffu, acc[r][c]);
+        if constexpr (kShare > 1) {
+            __shared__ int part[kShare][kM][kR];
+            __syncthreads();  // what an earlier turn left has been read
+            if (lane == 0) {
+#pragma unroll
+                for (int r = 0; r < kM; ++r)
+#pragma unroll
+                    for (int c = 0; c < kR; ++c) part[share][r][c] = acc[r][c];
+            }
+            __syncthreads();
+            if (share != 0) continue;
+#pragma unroll
+            for (int q = 1; q < kShare; ++q)
+#pragma unroll
+                for (int r = 0; r < kM; ++r)
+#pragma unroll
+                    for (int c = 0; c < kR; ++c) acc[r][c] += part[q][r][c];
+        }
 #pragma unroll
         for (int r = 0; r < kM; ++r)
 #pragma unroll
@@ -314,16 +359,25 @@ __global__ void __launch_bounds__(32 * kDotWarps) gemm_i8_dot_kernel(const GemmI
     }
 }
 
+template <typename T, int kM, int kUnit>
+cudaError_t dot_unit(const GemmI8Params &p, cudaStream_t s) {
+    const int64_t down = (p.m + kM - 1) / kM;
+    const dim3 block(32 * kDotWarps);
+    const unsigned y = static_cast<unsigned>(down < 65535 ? down : 65535);
+    const int64_t whole = (p.n + kR - 1) / kR, apart = (whole + kDotWarps - 1) / kDotWarps;
+    // A block's four warps share a column once each lane has four units of it (or of several rows' sums) to add up:
+    // 4096 columns of 11008 codes 9.2 against 10.2 us, 11008 of 4096 11.7 against 9.1.
+    const int64_t units = p.k / (kUnit == 16 ? 16 : 4);
+    if (units >= 16 * 32 || (p.m > 1 && units >= 4 * 32))
+        return launch_early(gemm_i8_dot_kernel<T, kM, kUnit, kDotWarps>, dim3(static_cast<unsigned>(whole), y), block, 0, s, p);
+    return launch_early(gemm_i8_dot_kernel<T, kM, kUnit, 1>, dim3(static_cast<unsigned>(apart), y), block, 0, s, p);
+}
+
 template <typename T, int kM>
 cudaError_t dot_m(const GemmI8Params &p, cudaStream_t s) {
-    const int64_t across = (p.n + kDotWarps * kR - 1) / (kDotWarps * kR), down = (p.m + kM - 1) / kM;
-    const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(down < 65535 ? down : 65535));
-    const dim3 block(32 * kDotWarps);
-    if (rows_on(p.a, p.lda, 16) && rows_on(p.b, p.ldb, 16))
-        return launch_early(gemm_i8_dot_kernel<T, kM, 16>, grid, block, 0, s, p);
-    if (rows_on(p.a, p.lda, 4) && rows_on(p.b, p.ldb, 4))
-        return launch_early(gemm_i8_dot_kernel<T, kM, 4>, grid, block, 0, s, p);
-    return launch_early(gemm_i8_dot_kernel<T, kM, 1>, grid, block, 0, s, p);
+    if (rows_on(p.a, p.lda, 16) && rows_on(p.b, p.ldb, 16)) return dot_unit<T, kM, 16>(p, s);
+    if (rows_on(p.a, p.lda, 4) && rows_on(p.b, p.ldb, 4)) return dot_unit<T, kM, 4>(p, s);
+    return dot_unit<T, kM, 1>(p, s);
 }
 
 template <typename T>
