@@ -67,6 +67,16 @@ __device__ __forceinline__ void unpack16<__nv_bfloat16>(const uint4 &v, float *o
     }
 }
 
+// Four 8-bit codes as f16: a byte b behind 0x64 is the f16 1024 + b, and b is the code + 128 once its top bit is flipped.
+__device__ __forceinline__ uint2 codes_to_half(uint32_t w) {
+    w ^= 0x80808080u;
+    const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), bias);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&hi), bias);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
 // 16-byte load that bypasses L1 allocation: for data streamed once from HBM.
 __device__ __forceinline__ uint4 ld_stream16(const void *p) {
     uint4 v;

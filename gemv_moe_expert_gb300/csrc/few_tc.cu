@@ -30,13 +30,6 @@ namespace {
 
 constexpr int kBM = 128;
 constexpr int kMaxSplit = 8;
-#ifndef V_FEW
-#define V_FEW 512
-#endif
-#ifndef V_TT
-#define V_TT 128
-#endif
-constexpr int64_t kFewCodeRows = V_FEW;  // tokens of an 8-bit product that run here
 constexpr uint32_t kWBytes = kBM * 128;  // 128 rows of 128 bytes: 64 16-bit values or 128 codes
 constexpr int kChunk = 8;                // code blocks (of 128) whose sums stay exact: 1024 of k
 
@@ -64,16 +57,6 @@ struct Ring {
     static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
     static_assert(8 * (2 * (kStages + kSlots) + 2) + 8 <= kBarBytes, "barriers");
 };
-
-// four codes as f16: a byte b behind 0x64 is the f16 1024 + b, and b is the code + 128 once its top bit is flipped
-__device__ __forceinline__ uint2 codes_to_half(uint32_t w) {
-    w ^= 0x80808080u;
-    const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
-    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-    const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), bias);
-    const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&hi), bias);
-    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-}
 
 __device__ __forceinline__ void load16(uint32_t at, uint32_t (&v)[4]) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -437,39 +420,60 @@ cudaError_t few_t(int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaS
 int few_tc_rows(bool codes) { return codes ? kBM : kBM / 2; }
 
 namespace {
-int tile_tokens(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : V_TT; }
 int ctas_per_sm(bool codes, int tokens) { return codes && tokens == 128 ? 1 : 2; }
 constexpr int kCodeCols = 128;  // columns of tensor memory that hold weights
 // code blocks that one CTA's accumulators take
 int64_t code_blocks(int tokens) { return ((ctas_per_sm(true, tokens) == 1 ? 512 : 256) - kCodeCols) / tokens * kChunk; }
+
+struct Split {
+    int64_t ctas, split;
+};
+Split split_for(bool codes, int tokens, int64_t m, int64_t n, int64_t k, int num_sms) {
+    const int64_t rows = few_tc_rows(codes), tiles = (n + rows - 1) / rows * ((m + tokens - 1) / tokens);
+    const int64_t kb = codes ? (k + 127) / 128 : (k + 63) / 64;
+    int64_t split = 1;
+    // as many CTAs as the SMs hold at once, each with a few blocks of its own (1408 x 2048 bf16, 16 tokens: 9.0, 7.1 and
+    // 8.5 us with at least 4, 8 and 16; 8-bit codes, 64 tokens: 8.3, 10.5 and 13.2 us with 2, 4 and 8)
+    while (split < kMaxSplit && tiles * (split + 1) <= static_cast<int64_t>(ctas_per_sm(codes, tokens)) * num_sms &&
+           kb >= (codes ? 2 : 8) * (split + 1))
+        ++split;
+    if (codes)
+        while (split < kMaxSplit && (kb + split - 1) / split > code_blocks(tokens)) ++split;
+    return {tiles * split, split};
+}
 }  // namespace
 
+// Up to 128 tokens; codes up to 256, and up to 512 where both operands' f16 form would fill few of the 256 x 256 tiles
+// (1408 x 2048, 512 tokens: 15 us here, 19 there; 11008 x 4096: 104 and 77).
 bool few_tc_takes(bool codes, int64_t m, int64_t n, int64_t k) {
-    if (m > (codes ? kFewCodeRows : 128)) return false;
-    return !codes || (k + 127) / 128 <= kMaxSplit * code_blocks(tile_tokens(m));
+    if (!codes) return m <= 128;
+    if (m > 256 && (m > 512 || m * n > (1 << 20))) return false;
+    return (k + 127) / 128 <= kMaxSplit * code_blocks(m <= 16 ? 16 : m <= 32 ? 32 : 128);
 }
 // whether the tokens' codes come as f16, in boxes of 64 k, rather than as bytes
-bool few_tc_half_tokens(int64_t m) { return tile_tokens(m) >= 64; }
+bool few_tc_half_tokens(int64_t m) { return m > 32; }
 
 // The tokens of a tile; sets the CTAs that share its contraction and the columns of tensor memory.
 int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p) {
-    const int tokens = tile_tokens(m);
-    p->token_blocks = static_cast<int32_t>((m + tokens - 1) / tokens);
-    const int64_t rows = few_tc_rows(codes), tiles = (n + rows - 1) / rows * p->token_blocks;
-    const int64_t kb = codes ? (k + 127) / 128 : (k + 63) / 64;
-    int64_t split = 1;
-    // as many CTAs as the SMs hold at once, each with a few blocks of its own
-    while (split < kMaxSplit && tiles * (split + 1) <= static_cast<int64_t>(ctas_per_sm(codes, tokens)) * num_sms &&
-           kb >= (codes ? 2 : 4) * (split + 1))
-        ++split;
-    int64_t cols = tokens;
-    if (codes) {
-        while (split < kMaxSplit && (kb + split - 1) / split > code_blocks(tokens)) ++split;
-        cols = kCodeCols + ((kb + split - 1) / split + kChunk - 1) / kChunk * tokens;
+    int tokens = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 || codes ? 64 : 128;
+    Split s = split_for(codes, tokens, m, n, k, num_sms);
+    if (codes && m > 64) {
+        // Tiles of 128 tokens read the weights once, but have an SM to themselves: taken where they fill the SMs
+        // (128 tokens: 4096 x 11008 26.5 us against 38 with 64 a tile, 11008 x 4096 42.7 against 37.7), or where 64 leave
+        // no room for the accumulators.
+        const Split wide = split_for(codes, 128, m, n, k, num_sms);
+        const int64_t kb = (k + 127) / 128;
+        if ((m <= 128 && 4 * wide.ctas >= 3LL * num_sms) || kb > s.split * code_blocks(64)) {
+            tokens = 128;
+            s = wide;
+        }
     }
+    p->token_blocks = static_cast<int32_t>((m + tokens - 1) / tokens);
+    p->ksplit = static_cast<int32_t>(s.split);
+    int64_t cols = tokens;
+    if (codes) cols = kCodeCols + (((k + 127) / 128 + s.split - 1) / s.split + kChunk - 1) / kChunk * tokens;
     p->tmem_cols = 32;
     while (p->tmem_cols < cols) p->tmem_cols *= 2;
-    p->ksplit = static_cast<int32_t>(split);
     return tokens;
 }
 

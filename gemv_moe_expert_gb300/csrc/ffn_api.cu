@@ -54,7 +54,7 @@ Laid lay(const void *p, int64_t rows, int64_t cols, int64_t ld, Parts *parts) {
 // launches what lay() put off; the matrix is read from its new place then
 gbmm_status lay_again(const char *fn, Laid *l, int64_t rows, int64_t cols, int64_t ld, void *scratch, cudaStream_t s) {
     if (!l->again) return GBMM_OK;
-    const RepackParams r{l->p, Parts::base(scratch) + l->at, rows, cols, ld, l->ld};
+    const RepackParams r{l->p, Parts::base(scratch) + l->at, rows, cols, ld, l->ld, 2};
     l->p = r.dst;
     return finish_launch(launch_repack16(r, s), fn, s);
 }
@@ -91,7 +91,10 @@ struct I8Plan {
     int a_size, b_size;
 };
 I8Plan i8_plan(int64_t m, int64_t n, int64_t k, bool a_aligned, bool b_aligned) {
-    if (m <= kDotRows || n == 0 || k == 0) return {I8Plan::kDot, 0, 0};
+    // Dot products cost 0.06 us for each row and MB of weights beyond the first row; the tensor cores' way about 5 us
+    // more than the weights' reading (11008 x 4096: 9.1, 12.1, 19 and 30 us for 1, 2, 4 and 8 rows against 15).
+    const bool dot = m <= kDotRows && (!a_aligned || !b_aligned || (m - 1) * n <= (85LL << 20) / (k > 0 ? k : 1));
+    if (dot || n == 0 || k == 0) return {I8Plan::kDot, 0, 0};
     if (!few_tc_takes(true, m, n, k)) return {I8Plan::kTiles, 2, 2};
     return {I8Plan::kFew, few_tc_half_tokens(m) ? 2 : a_aligned ? 0 : 1, b_aligned ? 0 : 1};
 }
@@ -149,9 +152,12 @@ gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n,
                            {"scratch", scratch, scratch ? scratch_bytes : 0, 1, true}};
     st = check_operands(fn, ops, 7);
     if (st != GBMM_OK) return st;
-    // 16-bit rows that TMA can read go to the tensor cores from two rows on
+    // 16-bit rows that TMA can read go to the tensor cores as soon as the dot products, 0.04 us for each row and MB of
+    // weights beyond the first row, cost more than that way's additional 5 us (11008 x 4096: 26.9 us for one row, 35, 48 and
+    // 81 for 2, 4 and 8 against 31 and 33; 1408 x 2048: 3 to 4.5 us against 6.5)
     const bool aligned = dt != GBMM_F32 && rows16(x, ldx * 2) && rows16(w_gate, ldw * 2) && rows16(w_up, ldw * 2);
-    const bool tiles16 = dt != GBMM_F32 && m > (aligned ? 1 : kDotRows) && k > 0;
+    const bool dot = m <= kDotRows && (!aligned || (m - 1) * n <= (32LL << 20) / (k > 0 ? k : 1));
+    const bool tiles16 = dt != GBMM_F32 && !dot && k > 0;
     Parts parts;
     Laid lx{}, lg{}, lu{};
     if (tiles16) {
@@ -446,11 +452,6 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
     }
     const void *const a2 = plan.a_size ? Parts::base(scratch) + a_at : static_cast<const void *>(a);
     const void *const b2 = plan.b_size ? Parts::base(scratch) + b_at : static_cast<const void *>(b);
-    auto lay_out = [&](const int8_t *from, const void *to, int64_t rows, int64_t ld, int64_t ld2, int to_size) {
-        if (to_size == 0) return GBMM_OK;
-        const RepackParams r{from, const_cast<void *>(to), rows, k, ld, ld2};
-        return finish_launch(to_size == 2 ? launch_codes_to_f16(r, s) : launch_repack8(r, s), fn, s);
-    };
     FewTcMaps few{};
     FewTcParams fp{};
     PairTcMaps maps{};
@@ -476,9 +477,12 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
         q.scale_b = scale_b;
     }
     if (!ok) return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
-    st = lay_out(a, a2, m, lda, lda2, plan.a_size);
-    if (st == GBMM_OK) st = lay_out(b, b2, n, ldb, ldb2, plan.b_size);
-    if (st != GBMM_OK) return st;
+    if (need > 0) {
+        const RepackParams ra{a, const_cast<void *>(a2), plan.a_size ? m : 0, k, lda, lda2, plan.a_size};
+        const RepackParams rb{b, const_cast<void *>(b2), plan.b_size ? n : 0, k, ldb, ldb2, plan.b_size};
+        st = finish_launch(launch_lay_out_codes(ra, rb, s), fn, s);
+        if (st != GBMM_OK) return st;
+    }
     return finish_launch(plan.route == I8Plan::kFew ? launch_gemm_i8_few(dt, static_cast<int>(tokens), few, fp, s)
                                                     : launch_gemm_i8_tc(dt, maps, q, device_sm_count(), s),
                          fn, s);

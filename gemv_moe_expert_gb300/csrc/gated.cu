@@ -600,28 +600,43 @@ cudaError_t gated_simt_t(const GatedParams &p, cudaStream_t s) {
 // d_gate = d_h * up * act'(gate), d_up = d_h * act(gate): one pass, 16 bytes an access
 // ---------------------------------------------------------------------------
 
-template <typename T>
+template <typename T, int kAct>
+__device__ __forceinline__ void grad_piece(const GatedGradParams &p, int vec, int64_t i, int64_t j) {
+    constexpr int kN = Elem<T>::kVec;
+    const int64_t left = p.n - j;
+    const bool whole = vec && left >= kN;
+    float g[kN], u[kN], d[kN], dg[kN], du[kN];
+    load_f<T, kN>(static_cast<const T *>(p.gate) + i * p.ld_saved + j, whole, left, g);
+    load_f<T, kN>(static_cast<const T *>(p.up) + i * p.ld_saved + j, whole, left, u);
+    load_f<T, kN>(static_cast<const T *>(p.d_h) + i * p.ld_dh + j, whole, left, d);
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+        float slope;
+        const float a = sizeof(T) == 2 ? gate_act_slope_16(kAct, g[e], &slope) : gate_act_slope(kAct, g[e], &slope);
+        dg[e] = d[e] * u[e] * slope;
+        du[e] = d[e] * a;
+    }
+    store_f<T, kN>(static_cast<T *>(p.d[0]) + i * p.ldd + j, left >= kN, left, dg);
+    store_f<T, kN>(static_cast<T *>(p.d[1]) + i * p.ldd + j, left >= kN, left, du);
+}
+
+// blocks walk over the pieces; the row and the place in it advance without a division
+template <typename T, int kAct>
 __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p, int vec) {
     constexpr int kN = Elem<T>::kVec;
     grid_dep_begin();
-    const int64_t pieces = (p.n + kN - 1) / kN, total = pieces * p.m;
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < total;
-         at += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t i = at / pieces, j = (at - i * pieces) * kN, left = p.n - j;
-        const bool whole = vec && left >= kN;
-        float g[kN], u[kN], d[kN], dg[kN], du[kN];
-        load_f<T, kN>(static_cast<const T *>(p.gate) + i * p.ld_saved + j, whole, left, g);
-        load_f<T, kN>(static_cast<const T *>(p.up) + i * p.ld_saved + j, whole, left, u);
-        load_f<T, kN>(static_cast<const T *>(p.d_h) + i * p.ld_dh + j, whole, left, d);
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-            float slope;
-            const float a = gate_act_slope(p.act, g[e], &slope);
-            dg[e] = d[e] * u[e] * slope;
-            du[e] = d[e] * a;
+    const int64_t pieces = (p.n + kN - 1) / kN, stride = static_cast<int64_t>(gridDim.x) * 256;
+    const int64_t down = stride / pieces, across = stride - down * pieces;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    int64_t i = at / pieces, j = at - i * pieces;
+    while (i < p.m) {
+        grad_piece<T, kAct>(p, vec, i, j * kN);
+        i += down;
+        j += across;
+        if (j >= pieces) {
+            j -= pieces;
+            ++i;
         }
-        store_f<T, kN>(static_cast<T *>(p.d[0]) + i * p.ldd + j, left >= kN, left, dg);
-        store_f<T, kN>(static_cast<T *>(p.d[1]) + i * p.ldd + j, left >= kN, left, du);
     }
 }
 
@@ -631,46 +646,35 @@ cudaError_t gated_grad_t(const GatedGradParams &p, cudaStream_t s) {
                     rows16(p.d_h, p.ld_dh, sizeof(T));
     const int64_t blocks = (p.m * ((p.n + Elem<T>::kVec - 1) / Elem<T>::kVec) + 255) / 256;
     const int64_t most = 16LL * device_sm_count();
-    return launch_early(gated_grad_kernel<T>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s,
-                        p, vec);
-}
-
-// ---------------------------------------------------------------------------
-// rows that TMA cannot read (or that hold 8-bit codes), written 16 bytes at a time into rows that
-// it can
-// ---------------------------------------------------------------------------
-
-template <typename D>
-struct alignas(16) Piece {
-    static constexpr int kN = 16 / sizeof(D);
-    D v[kN];
-};
-
-__device__ __forceinline__ void put(uint16_t v, uint16_t *to) { *to = v; }
-__device__ __forceinline__ void put(int8_t v, int8_t *to) { *to = v; }
-__device__ __forceinline__ void put(int8_t v, uint16_t *to) { *to = __half_as_ushort(__int2half_rn(v)); }
-
-template <typename S, typename D>
-__global__ void __launch_bounds__(256) repack_kernel(const RepackParams p) {
-    constexpr int kN = Piece<D>::kN;
-    grid_dep_begin();
-    const int64_t pieces = p.ldd / kN, total = pieces * p.rows;
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < total;
-         at += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t i = at / pieces, j = (at - i * pieces) * kN;
-        const S *src = static_cast<const S *>(p.src) + i * p.lds + j;
-        Piece<D> h;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) put(j + e < p.cols ? src[e] : S{0}, &h.v[e]);
-        *reinterpret_cast<Piece<D> *>(static_cast<D *>(p.dst) + i * p.ldd + j) = h;
+    const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most)), block(256);
+    switch (p.act) {
+    case GBMM_GATE_SILU: return launch_early(gated_grad_kernel<T, GBMM_GATE_SILU>, grid, block, 0, s, p, vec);
+    case GBMM_GATE_GELU: return launch_early(gated_grad_kernel<T, GBMM_GATE_GELU>, grid, block, 0, s, p, vec);
+    case GBMM_GATE_GELU_TANH: return launch_early(gated_grad_kernel<T, GBMM_GATE_GELU_TANH>, grid, block, 0, s, p, vec);
+    default: return launch_early(gated_grad_kernel<T, GBMM_GATE_RELU>, grid, block, 0, s, p, vec);
     }
 }
 
-template <typename S, typename D>
-cudaError_t repack_t(const RepackParams &p, cudaStream_t s) {
-    const int64_t blocks = (p.rows * (p.ldd / Piece<D>::kN) + 255) / 256, most = 16LL * device_sm_count();
-    if (blocks == 0) return cudaSuccess;
-    return launch_early(repack_kernel<S, D>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, p);
+// ---------------------------------------------------------------------------
+// 16-bit rows that TMA cannot read, written 16 bytes at a time into rows that it can
+// ---------------------------------------------------------------------------
+
+struct alignas(16) Halves {
+    uint16_t v[8];
+};
+
+__global__ void __launch_bounds__(256) repack16_kernel(const RepackParams p) {
+    grid_dep_begin();
+    const int64_t pieces = p.ldd / 8, total = pieces * p.rows;
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < total;
+         at += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t i = at / pieces, j = (at - i * pieces) * 8;
+        const uint16_t *src = static_cast<const uint16_t *>(p.src) + i * p.lds + j;
+        Halves h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h.v[e] = j + e < p.cols ? __ldg(src + e) : uint16_t{0};
+        *reinterpret_cast<Halves *>(static_cast<uint16_t *>(p.dst) + i * p.ldd + j) = h;
+    }
 }
 
 }  // namespace
@@ -729,8 +733,10 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
     return large_tiles(w_large, w_small, 12) ? launch_whole(outer_gemm_simt_kernel<8, 4>, w_large, s, tw, o)
                                              : launch_whole(outer_gemm_simt_kernel<4, 4>, w_small, s, tws, o);
 }
-cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s) { return repack_t<uint16_t, uint16_t>(p, s); }
-cudaError_t launch_codes_to_f16(const RepackParams &p, cudaStream_t s) { return repack_t<int8_t, uint16_t>(p, s); }
-cudaError_t launch_repack8(const RepackParams &p, cudaStream_t s) { return repack_t<int8_t, int8_t>(p, s); }
+cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s) {
+    const int64_t blocks = (p.rows * (p.ldd / 8) + 255) / 256, most = 16LL * device_sm_count();
+    if (blocks == 0) return cudaSuccess;
+    return launch_early(repack16_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, p);
+}
 
 }  // namespace gbmm

@@ -71,4 +71,27 @@ __device__ __forceinline__ float gate_act_slope(int act, float v, float *slope) 
     }
 }
 
+// the same for results of 16 bits
+__device__ __forceinline__ float gate_act_slope_16(int act, float v, float *slope) {
+    switch (act) {
+    case GBMM_GATE_SILU: {
+        const float s = sigmoid_16(v);
+        *slope = s * fmaf(v, 1.f - s, 1.f);
+        return v * s;
+    }
+    case GBMM_GATE_GELU: {
+        const float h = half_erfc_16(0.70710678118654752f * v), c = v > 0.f ? 1.f - h : h;
+        *slope = fmaf(v, 0.3989422804014327f * __expf(-0.5f * v * v), c);
+        return v * c;
+    }
+    case GBMM_GATE_GELU_TANH: {
+        const float s = sigmoid_16(gelu_tanh_arg(v)), t = s * (1.f - s);
+        const float d = t == 0.f ? 0.f : v * t * 1.5957691216057308f * fmaf(3.f * 0.044715f, v * v, 1.f);
+        *slope = s + d;
+        return v * s;
+    }
+    default: return gate_act_slope(act, v, slope);
+    }
+}
+
 }  // namespace gbmm

@@ -229,6 +229,7 @@ constexpr int kR = 1;
 
 // the four codes at row + 4 g; the row has k codes, and what lies past them counts as 0
 __device__ __forceinline__ uint32_t any4(const int8_t *row, int64_t g, int64_t k) {
+    if (4 * g >= k) return 0;
     const int8_t *at = row + 4 * g;
     const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) & 3u);
     const uint32_t *word = reinterpret_cast<const uint32_t *>(at - shift);
@@ -388,7 +389,54 @@ cudaError_t dot_t(const GemmI8Params &p, cudaStream_t s) {
     return dot_m<T, 8>(p, s);
 }
 
+// ---------------------------------------------------------------------------
+// codes laid out again, as bytes or as f16, 16 at a time; both operands of a product in one launch
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void lay_out_piece(const RepackParams &p, int aligned, int64_t i, int64_t j) {
+    const int8_t *row = static_cast<const int8_t *>(p.src) + i * p.lds;
+    uint4 v;
+    if (aligned && j + 16 <= p.cols) {
+        v = ld_stream16(row + j);
+    } else {
+        v = make_uint4(any4(row, j / 4, p.cols), any4(row, j / 4 + 1, p.cols), any4(row, j / 4 + 2, p.cols),
+                       any4(row, j / 4 + 3, p.cols));
+    }
+    if (p.to_size == 1) {
+        *reinterpret_cast<uint4 *>(static_cast<int8_t *>(p.dst) + i * p.ldd + j) = v;
+        return;
+    }
+    const uint2 a = codes_to_half(v.x), b = codes_to_half(v.y), c = codes_to_half(v.z), d = codes_to_half(v.w);
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dst) + i * p.ldd + j);
+    dst[0] = make_uint4(a.x, a.y, b.x, b.y);
+    if (j + 8 < p.ldd) dst[1] = make_uint4(c.x, c.y, d.x, d.y);
+}
+
+__global__ void __launch_bounds__(256) lay_out_codes_kernel(const RepackParams a, const RepackParams b, int a_aligned,
+                                                            int b_aligned) {
+    grid_dep_begin();
+    const int64_t pa = (a.ldd + 15) / 16, pb = (b.ldd + 15) / 16, na = pa * a.rows, total = na + pb * b.rows;
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < total;
+         at += static_cast<int64_t>(gridDim.x) * 256) {
+        if (at < na) {
+            const int64_t i = at / pa;
+            lay_out_piece(a, a_aligned, i, (at - i * pa) * 16);
+        } else {
+            const int64_t i = (at - na) / pb;
+            lay_out_piece(b, b_aligned, i, (at - na - i * pb) * 16);
+        }
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_lay_out_codes(const RepackParams &a, const RepackParams &b, cudaStream_t s) {
+    const int64_t total = (a.ldd + 15) / 16 * a.rows + (b.ldd + 15) / 16 * b.rows;
+    const int64_t blocks = (total + 255) / 256, most = 16LL * device_sm_count();
+    if (blocks == 0) return cudaSuccess;
+    return launch_early(lay_out_codes_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, a,
+                        b, static_cast<int>(rows_on(a.src, a.lds, 16)), static_cast<int>(rows_on(b.src, b.lds, 16)));
+}
 
 cudaError_t launch_quantize_i8(int dt, const QuantizeParams &p, cudaStream_t s) {
     switch (dt) {

@@ -203,12 +203,13 @@ struct OuterGemmParams {
     int64_t m, n, k, ldx, ldd, ldc;
 };
 
-// Rows laid out again: src [rows, cols] (16-bit values, 8-bit codes, or codes that become f16) into
-// dst [rows, ldd], ldd a multiple of 16 bytes (gated.cu).
+// Rows laid out again: src [rows, cols] into dst [rows, ldd], ldd a multiple of 16 bytes.  16-bit values (gated.cu);
+// 8-bit codes (i8.cu), to_size bytes each at dst: 1, or 2 for f16.
 struct RepackParams {
     const void *src;
     void *dst;
     int64_t rows, cols, lds, ldd;
+    int32_t to_size;
 };
 
 // Rows to 8-bit codes with a scale each, and the product of such codes (i8.cu).
@@ -333,8 +334,7 @@ cudaError_t launch_gated_grad(int dt, const GatedGradParams &p, cudaStream_t s);
 // f32
 cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, cudaStream_t s);
 cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s);
-cudaError_t launch_repack8(const RepackParams &p, cudaStream_t s);
-cudaError_t launch_codes_to_f16(const RepackParams &p, cudaStream_t s);
+cudaError_t launch_lay_out_codes(const RepackParams &a, const RepackParams &b, cudaStream_t s);  // rows 0: nothing to do
 // on the tensor cores: gated a[0] = x, b = both weights, all K-contiguous in boxes of pair_tc_rows()
 // rows; sum a and b as in SumGemmParams, b in 64 x 64 boxes; codes a[0] and b[0] (f16) as gated
 cudaError_t launch_gated_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s);
