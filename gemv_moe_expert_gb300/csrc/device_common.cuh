@@ -77,6 +77,44 @@ __device__ __forceinline__ uint2 codes_to_half(uint32_t w) {
     return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
+// Words o, o + 32, .. (kU of them; o = o0 + lane) of a row of `bytes` that may start anywhere: the four bytes at row + 4 o,
+// from the aligned words around them, shifted into place, a word's other part from the next lane.  At a row's ends only
+// its own elements are read (kSize bytes each); what lies past them is 0.  Every lane of the warp calls it.
+template <int kSize, int kU>
+__device__ __forceinline__ void shifted_words(const uint8_t *row, int64_t o0, int64_t bytes, int lane, uint32_t (&v)[kU]) {
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 3u);
+    const uint32_t *words = reinterpret_cast<const uint32_t *>(row - shift) + o0;
+    const int64_t first = 4 * o0 - shift;
+    uint32_t lo[kU + 1];  // the last: lane 0's is the word behind all others
+    if (first >= 0 && first + 4 * (32 * kU + 1) <= bytes) {
+#pragma unroll
+        for (int q = 0; q < kU; ++q) lo[q] = __ldg(words + 32 * q + lane);
+        lo[kU] = lane == 0 ? __ldg(words + 32 * kU) : 0u;
+    } else {
+        auto word = [&](int64_t at) {  // bytes at .. at + 3 of the row
+            if (at >= 0 && at + 4 <= bytes) return __ldg(reinterpret_cast<const uint32_t *>(row + at));
+            uint32_t w = 0;
+#pragma unroll
+            for (int e = 0; e < 4; e += kSize)
+                if (at + e >= 0 && at + e + kSize <= bytes)
+                    w |= static_cast<uint32_t>(kSize == 2 ? __ldg(reinterpret_cast<const uint16_t *>(row + at + e))
+                                                          : static_cast<uint16_t>(__ldg(row + at + e)))
+                         << (8 * e);
+            return w;
+        };
+#pragma unroll
+        for (int q = 0; q < kU; ++q) lo[q] = word(first + 4 * (32 * q + lane));
+        lo[kU] = lane == 0 && shift != 0 ? word(first + 4 * 32 * kU) : 0u;
+    }
+#pragma unroll
+    for (int q = 0; q < kU; ++q) {
+        // lane l's other part is lane l + 1's word, lane 31's the next group's first
+        const uint32_t give = lane == 0 ? lo[q + 1] : lo[q];
+        const uint32_t hi = __shfl_sync(0xffffffffu, give, (lane + 1) & 31);
+        v[q] = __funnelshift_r(lo[q], hi, 8 * shift);
+    }
+}
+
 // 16-byte load that bypasses L1 allocation: for data streamed once from HBM.
 __device__ __forceinline__ uint4 ld_stream16(const void *p) {
     uint4 v;

@@ -432,9 +432,10 @@ Split split_for(bool codes, int tokens, int64_t m, int64_t n, int64_t k, int num
     const int64_t rows = few_tc_rows(codes), tiles = (n + rows - 1) / rows * ((m + tokens - 1) / tokens);
     const int64_t kb = codes ? (k + 127) / 128 : (k + 63) / 64;
     int64_t split = 1;
-    // as many CTAs as the SMs hold at once, each with a few blocks of its own (1408 x 2048 bf16, 16 tokens: 9.0, 7.1 and
+    // as many CTAs as the SMs hold at once (a cluster lies within a group of 16 to 20 SMs, so that an eighth of
+    // the places may not be used), each with a few blocks of its own (1408 x 2048 bf16, 16 tokens: 9.0, 7.1 and
     // 8.5 us with at least 4, 8 and 16; 8-bit codes, 64 tokens: 8.3, 10.5 and 13.2 us with 2, 4 and 8)
-    while (split < kMaxSplit && tiles * (split + 1) <= static_cast<int64_t>(ctas_per_sm(codes, tokens)) * num_sms &&
+    while (split < kMaxSplit && 8 * tiles * (split + 1) <= 7LL * ctas_per_sm(codes, tokens) * num_sms &&
            kb >= (codes ? 2 : 8) * (split + 1))
         ++split;
     if (codes)

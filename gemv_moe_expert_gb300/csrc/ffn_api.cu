@@ -19,15 +19,21 @@ bool in_range(int64_t v) { return v >= 0 && v <= INT32_MAX; }
 // kAlign bytes from a base that is rounded up to one.
 struct Parts {
     uint64_t bytes = kAlign;
+    bool ok = true;  // false: more bytes than an int64 counts
     uint64_t add(int64_t rows, int64_t ld, int size) {
         const uint64_t at = bytes;
-        bytes += static_cast<uint64_t>(round_up(rows * ld * size, kAlign));
+        const unsigned __int128 more = static_cast<unsigned __int128>(rows) * static_cast<uint64_t>(ld) * size;
+        ok = ok && more < (1ull << 62) && bytes < (1ull << 62);
+        if (ok) bytes += static_cast<uint64_t>(round_up(static_cast<int64_t>(more), kAlign));
         return at;
     }
+    uint64_t needed() const { return bytes > kAlign ? bytes : 0; }
     static char *base(void *scratch) {
         return reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(scratch) + kAlign - 1) / kAlign * kAlign) - kAlign;
     }
 };
+
+gbmm_status too_large(const char *fn) { return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: scratch extent overflows", fn); }
 
 Operand matrix(const char *label, const void *p, uint64_t bytes, int64_t cols, int64_t ld, uint32_t size, bool output) {
     return {label, p, bytes, size, output, static_cast<uint64_t>(cols) * size, static_cast<uint64_t>(ld) * size};
@@ -39,23 +45,23 @@ bool rows16(const void *p, int64_t ld_bytes) {
 // Few rows run as dot products, a warp for each column or two; more run as tiles.
 constexpr int64_t kDotRows = 8;
 
-// A 16-bit matrix as TMA reads it: in place, or laid out again in a part of the scratch.
+// A 16-bit matrix as TMA reads it: in place (to null), or laid out again in a part of the scratch.
 struct Laid {
-    const void *p;
-    int64_t ld;
-    uint64_t at;
-    bool again;
+    const void *from;
+    void *to;
+    int64_t rows, cols, from_ld, ld;
+    const void *p() const { return to != nullptr ? to : from; }
 };
-Laid lay(const void *p, int64_t rows, int64_t cols, int64_t ld, Parts *parts) {
-    if (rows16(p, ld * 2)) return {p, ld, 0, false};
-    const int64_t to = round_up(cols, 8);
-    return {p, to, parts->add(rows, to, 2), true};
+Laid lay(const void *p, int64_t rows, int64_t cols, int64_t ld, void *scratch, Parts *parts) {
+    Laid l{p, nullptr, rows, cols, ld, ld};
+    if (rows16(p, ld * 2)) return l;
+    l.ld = round_up(cols, 8);
+    l.to = Parts::base(scratch) + parts->add(rows, l.ld, 2);
+    return l;
 }
-// launches what lay() put off; the matrix is read from its new place then
-gbmm_status lay_again(const char *fn, Laid *l, int64_t rows, int64_t cols, int64_t ld, void *scratch, cudaStream_t s) {
-    if (!l->again) return GBMM_OK;
-    const RepackParams r{l->p, Parts::base(scratch) + l->at, rows, cols, ld, l->ld, 2};
-    l->p = r.dst;
+gbmm_status lay_again(const char *fn, const Laid &l, cudaStream_t s) {
+    if (l.to == nullptr) return GBMM_OK;
+    const RepackParams r{l.from, l.to, l.rows, l.cols, l.from_ld, l.ld, 2};
     return finish_launch(launch_repack16(r, s), fn, s);
 }
 
@@ -71,6 +77,19 @@ bool pair_params(PairTcParams *p, PairTcMaps *maps, int dt, void *c, int64_t ldc
     p->err = device_error_word();
     p->wait_limit_ns = kWaitLimitNs;
     return p->err != nullptr;
+}
+
+// whether m rows run as dot products: at most kDotRows, and rows beyond the first times weights up to `most`
+bool few_rows(int64_t m, int64_t n, int64_t k, int64_t most) {
+    return m <= kDotRows && (k == 0 || (m - 1) * n <= most / k);
+}
+
+// 16-bit rows go to the tensor cores as soon as the dot products, 0.04 us for each row and MB of weights beyond the first
+// row, cost more than that way's additional 5 us (11008 x 4096: 26.9 us for one row, 35, 48 and 81 for 2, 4 and 8 against
+// 31 to 32; 1408 x 2048: 3 to 4.5 us against 6.5); rows that start anywhere once they pay for being laid out again, too
+// (4096 x 4096: 18, 24, 49 and 111 us for 1, 2, 4 and 8 rows against 37).
+bool gated_dot(int64_t m, int64_t n, int64_t k, bool aligned) {
+    return few_rows(m, n, k, aligned ? 32LL << 20 : 48LL << 20);
 }
 
 void few_params(FewTcParams *p, void *c, int64_t ldc, int64_t m, int64_t n, int64_t k) {
@@ -91,9 +110,10 @@ struct I8Plan {
     int a_size, b_size;
 };
 I8Plan i8_plan(int64_t m, int64_t n, int64_t k, bool a_aligned, bool b_aligned) {
-    // Dot products cost 0.06 us for each row and MB of weights beyond the first row; the tensor cores' way about 5 us
-    // more than the weights' reading (11008 x 4096: 9.1, 12.1, 19 and 30 us for 1, 2, 4 and 8 rows against 15).
-    const bool dot = m <= kDotRows && (!a_aligned || !b_aligned || (m - 1) * n <= (85LL << 20) / (k > 0 ? k : 1));
+    // Dot products cost 0.06 us for each row and MB of weights beyond the first row (0.3 where rows start anywhere), the
+    // tensor cores' way about 5 us more than reading the weights (and writing and reading them again): 11008 x 4096
+    // 9.1, 12.8, 19 and 30 us for 1, 2, 4 and 8 rows against 15; 4096 x 4096 in odd rows 6.7 and 43 for 1 and 8 against 15.
+    const bool dot = few_rows(m, n, k, a_aligned && b_aligned ? 85LL << 20 : 24LL << 20);
     if (dot || n == 0 || k == 0) return {I8Plan::kDot, 0, 0};
     if (!few_tc_takes(true, m, n, k)) return {I8Plan::kTiles, 2, 2};
     return {I8Plan::kFew, few_tc_half_tokens(m) ? 2 : a_aligned ? 0 : 1, b_aligned ? 0 : 1};
@@ -120,12 +140,13 @@ gbmm_status gbmm_gated_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t n, int64_
     if (st != GBMM_OK) return st;
     if (bytes == nullptr) return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: bytes is null", fn);
     *bytes = 0;
-    if (dt == GBMM_F32 || aligned || m <= kDotRows || n == 0 || k == 0) return GBMM_OK;
+    if (dt == GBMM_F32 || aligned || gated_dot(m, n, k, false) || m == 0 || n == 0 || k == 0) return GBMM_OK;
     Parts parts;
     parts.add(m, round_up(k, 8), 2);
     parts.add(n, round_up(k, 8), 2);
     parts.add(n, round_up(k, 8), 2);
-    *bytes = parts.bytes;
+    if (!parts.ok) return too_large(fn);
+    *bytes = parts.needed();
     return GBMM_OK;
 }
 
@@ -152,61 +173,62 @@ gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n,
                            {"scratch", scratch, scratch ? scratch_bytes : 0, 1, true}};
     st = check_operands(fn, ops, 7);
     if (st != GBMM_OK) return st;
-    // 16-bit rows that TMA can read go to the tensor cores as soon as the dot products, 0.04 us for each row and MB of
-    // weights beyond the first row, cost more than that way's additional 5 us (11008 x 4096: 26.9 us for one row, 35, 48 and
-    // 81 for 2, 4 and 8 against 31 and 33; 1408 x 2048: 3 to 4.5 us against 6.5)
-    const bool aligned = dt != GBMM_F32 && rows16(x, ldx * 2) && rows16(w_gate, ldw * 2) && rows16(w_up, ldw * 2);
-    const bool dot = m <= kDotRows && (!aligned || (m - 1) * n <= (32LL << 20) / (k > 0 ? k : 1));
+    const bool aligned = rows16(x, ldx * 2) && rows16(w_gate, ldw * 2) && rows16(w_up, ldw * 2);
+    const bool dot = gated_dot(m, n, k, aligned) || (m <= kDotRows && !aligned && scratch == nullptr);
     const bool tiles16 = dt != GBMM_F32 && !dot && k > 0;
     Parts parts;
-    Laid lx{}, lg{}, lu{};
+    Laid lx{}, lw[2] = {};
     if (tiles16) {
-        lx = lay(x, m, k, ldx, &parts);
-        lg = lay(w_gate, n, k, ldw, &parts);
-        lu = lay(w_up, n, k, ldw, &parts);
+        lx = lay(x, m, k, ldx, scratch, &parts);
+        lw[0] = lay(w_gate, n, k, ldw, scratch, &parts);
+        lw[1] = lay(w_up, n, k, ldw, scratch, &parts);
     }
-    const bool again = lx.again || lg.again || lu.again;
-    if (again && scratch != nullptr && scratch_bytes < parts.bytes)
+    const uint64_t need = parts.needed();
+    if (!parts.ok) return too_large(fn);
+    if (need > 0 && scratch != nullptr && scratch_bytes < need)
         return fail(GBMM_ERR_SCRATCH, "%s: needs %llu bytes of scratch for this layout (got %llu)", fn,
-                    (unsigned long long)parts.bytes, (unsigned long long)scratch_bytes);
+                    (unsigned long long)need, (unsigned long long)scratch_bytes);
     if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
     cudaStream_t s = cuda_stream(stream);
-    if (tiles16 && (!again || scratch != nullptr)) {
-        st = lay_again(fn, &lx, m, k, ldx, scratch, s);
-        if (st == GBMM_OK) st = lay_again(fn, &lg, n, k, ldw, scratch, s);
-        if (st == GBMM_OK) st = lay_again(fn, &lu, n, k, ldw, scratch, s);
-        if (st != GBMM_OK) return st;
-        if (few_tc_takes(false, m, n, k)) {
-            FewTcMaps maps{};
-            FewTcParams q{};
-            few_params(&q, h, ldh, m, n, k);
-            const uint32_t tokens = static_cast<uint32_t>(few_tc_plan(false, m, n, k, device_sm_count(), &q));
+    if (tiles16 && (need == 0 || scratch != nullptr)) {
+        const bool few = few_tc_takes(false, m, n, k);
+        FewTcMaps few_maps{};
+        FewTcParams fp{};
+        PairTcMaps maps{};
+        PairTcParams q{};
+        uint32_t tokens = 0;
+        bool ok;
+        if (few) {
+            few_params(&fp, h, ldh, m, n, k);
+            tokens = static_cast<uint32_t>(few_tc_plan(false, m, n, k, device_sm_count(), &fp));
             const uint32_t rows = static_cast<uint32_t>(few_tc_rows(false));
-            if (q.err == nullptr || !encode_matrix16(&maps.x, dt, lx.p, k, m, lx.ld, tokens) ||
-                !encode_matrix16(&maps.w[0], dt, lg.p, k, n, lg.ld, rows) ||
-                !encode_matrix16(&maps.w[1], dt, lu.p, k, n, lu.ld, rows))
-                return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
+            ok = fp.err != nullptr && encode_matrix16(&few_maps.x, dt, lx.p(), k, m, lx.ld, tokens) &&
+                 encode_matrix16(&few_maps.w[0], dt, lw[0].p(), k, n, lw[0].ld, rows) &&
+                 encode_matrix16(&few_maps.w[1], dt, lw[1].p(), k, n, lw[1].ld, rows);
+            fp.saved[0] = gate;
+            fp.saved[1] = up;
+            fp.ld_saved = ld_saved;
+            fp.act = static_cast<int32_t>(activation);
+        } else {
+            const uint32_t rows = static_cast<uint32_t>(pair_tc_rows());
+            ok = pair_params(&q, &maps, dt, h, ldh, m, n, k) && encode_matrix16(&maps.a[0], dt, lx.p(), k, m, lx.ld, rows) &&
+                 encode_matrix16(&maps.b[0], dt, lw[0].p(), k, n, lw[0].ld, rows) &&
+                 encode_matrix16(&maps.b[1], dt, lw[1].p(), k, n, lw[1].ld, rows);
+            maps.a[1] = maps.a[0];
             q.saved[0] = gate;
             q.saved[1] = up;
             q.ld_saved = ld_saved;
+            q.saved_tma = gate != nullptr && encode_store32(&maps.out[1], dt, gate, n, m, ld_saved) &&
+                          encode_store32(&maps.out[2], dt, up, n, m, ld_saved);
             q.act = static_cast<int32_t>(activation);
-            return finish_launch(launch_gated_few(dt, static_cast<int>(tokens), maps, q, s), fn, s);
         }
-        PairTcMaps maps{};
-        PairTcParams q;
-        const uint32_t rows = static_cast<uint32_t>(pair_tc_rows());
-        if (!pair_params(&q, &maps, dt, h, ldh, m, n, k) || !encode_matrix16(&maps.a[0], dt, lx.p, k, m, lx.ld, rows) ||
-            !encode_matrix16(&maps.b[0], dt, lg.p, k, n, lg.ld, rows) ||
-            !encode_matrix16(&maps.b[1], dt, lu.p, k, n, lu.ld, rows))
-            return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
-        maps.a[1] = maps.a[0];
-        q.saved[0] = gate;
-        q.saved[1] = up;
-        q.ld_saved = ld_saved;
-        q.saved_tma = gate != nullptr && encode_store32(&maps.out[1], dt, gate, n, m, ld_saved) &&
-                      encode_store32(&maps.out[2], dt, up, n, m, ld_saved);
-        q.act = static_cast<int32_t>(activation);
-        return finish_launch(launch_gated_tc(dt, maps, q, device_sm_count(), s), fn, s);
+        if (!ok) return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
+        st = lay_again(fn, lx, s);
+        for (int i = 0; i < 2 && st == GBMM_OK; ++i) st = lay_again(fn, lw[i], s);
+        if (st != GBMM_OK) return st;
+        return finish_launch(few ? launch_gated_few(dt, static_cast<int>(tokens), few_maps, fp, s)
+                                 : launch_gated_tc(dt, maps, q, device_sm_count(), s),
+                             fn, s);
     }
     GatedParams p{};
     p.x = x;
@@ -242,7 +264,8 @@ gbmm_status gbmm_gated_backward_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t 
         parts.add(n, round_up(k, 8), 2);
         parts.add(n, round_up(k, 8), 2);
     }
-    *bytes = parts.bytes;
+    if (!parts.ok) return too_large(fn);
+    *bytes = parts.needed();
     return GBMM_OK;
 }
 
@@ -275,14 +298,15 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     Parts parts;
     const int64_t ldd = round_up(n, 16 / static_cast<int>(size));
     const uint64_t d_at[2] = {parts.add(m, ldd, static_cast<int>(size)), parts.add(m, ldd, static_cast<int>(size))};
-    Laid lx{x, ldx, 0, false}, lw[2] = {{w_gate, ldw, 0, false}, {w_up, ldw, 0, false}};
+    Laid lx{x, nullptr, m, k, ldx, ldx}, lw[2] = {{w_gate, nullptr, n, k, ldw, ldw}, {w_up, nullptr, n, k, ldw, ldw}};
     if (dt != GBMM_F32 && !empty) {
-        if (need_w) lx = lay(x, m, k, ldx, &parts);
+        if (need_w) lx = lay(x, m, k, ldx, scratch, &parts);
         if (need_x) {
-            lw[0] = lay(w_gate, n, k, ldw, &parts);
-            lw[1] = lay(w_up, n, k, ldw, &parts);
+            lw[0] = lay(w_gate, n, k, ldw, scratch, &parts);
+            lw[1] = lay(w_up, n, k, ldw, scratch, &parts);
         }
     }
+    if (!parts.ok) return too_large(fn);
     const Operand ops[] = {matrix("x", x, xb, k, ldx, size, false),
                            matrix("w_gate", w_gate, wb, k, ldw, size, false),
                            matrix("w_up", w_up, wb, k, ldw, size, false),
@@ -340,34 +364,37 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     g.ld_dh = ld_dh;
     g.ldd = ldd;
     g.act = static_cast<int32_t>(activation);
-    st = lay_again(fn, &lx, m, k, ldx, scratch, s);
-    for (int i = 0; i < 2 && st == GBMM_OK; ++i) st = lay_again(fn, &lw[i], n, k, ldw, scratch, s);
+    PairTcMaps maps{};
+    PairTcParams q{};
+    if (need_x && dt != GBMM_F32) {
+        bool ok = pair_params(&q, &maps, dt, d_x, ld_dx, m, k, n);
+        for (int i = 0; i < 2 && ok; ++i)
+            ok = encode_matrix16(&maps.a[i], dt, g.d[i], n, m, ldd, static_cast<uint32_t>(pair_tc_rows())) &&
+                 encode_matrix16(&maps.b[i], dt, lw[i].p(), k, n, lw[i].ld, static_cast<uint32_t>(pair_tc_block_k()));
+        if (!ok) return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
+    }
+    st = lay_again(fn, lx, s);
+    for (int i = 0; i < 2 && st == GBMM_OK; ++i) st = lay_again(fn, lw[i], s);
     if (st == GBMM_OK) st = finish_launch(launch_gated_grad(dt, g, s), fn, s);
     if (st != GBMM_OK) return st;
     void *const dw[2] = {d_w_gate, d_w_up};
     if (dt == GBMM_F32) {
         const SumGemmParams px{{g.d[0], g.d[1]}, {w_gate, w_up}, d_x, m, k, n, ldd, ldw, ld_dx};
         const OuterGemmParams pw{x, {g.d[0], g.d[1]}, {dw[0], dw[1]}, m, n, k, ldx, ldd, ld_dw};
-        return finish_launch(launch_gated_products_simt(need_x ? &px : nullptr, need_w ? &pw : nullptr, s), fn, s);
+        int launches = 0;
+        st = finish_launch(launch_gated_products_simt(need_x ? &px : nullptr, need_w ? &pw : nullptr, &launches, s), fn, s);
+        for (; st == GBMM_OK && launches > 1; --launches) st = finish_launch(cudaSuccess, fn, s);
+        return st;
     }
-    if (need_x) {
-        PairTcMaps maps{};
-        PairTcParams q;
-        bool ok = pair_params(&q, &maps, dt, d_x, ld_dx, m, k, n);
-        for (int i = 0; i < 2 && ok; ++i)
-            ok = encode_matrix16(&maps.a[i], dt, g.d[i], n, m, ldd, static_cast<uint32_t>(pair_tc_rows())) &&
-                 encode_matrix16(&maps.b[i], dt, lw[i].p, k, n, lw[i].ld, static_cast<uint32_t>(pair_tc_block_k()));
-        if (!ok) return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
-        st = finish_launch(launch_sum_gemm_tc(dt, maps, q, device_sm_count(), s), fn, s);
-    }
+    if (need_x) st = finish_launch(launch_sum_gemm_tc(dt, maps, q, device_sm_count(), s), fn, s);
     if (st != GBMM_OK || !need_w) return st;
     if (batched) {  // one product over both projections: more tiles in a launch
         const int64_t apart = (reinterpret_cast<intptr_t>(dw[!first]) - reinterpret_cast<intptr_t>(dw[first])) / 2;
-        return gbmm_gemm(dt, 2, n, k, m, 1, 0, g.d[first], 0, ldd, d_apart, lx.p, 0, lx.ld, 0, dw[first], 0, ld_dw,
+        return gbmm_gemm(dt, 2, n, k, m, 1, 0, g.d[first], 0, ldd, d_apart, lx.p(), 0, lx.ld, 0, dw[first], 0, ld_dw,
                          apart, stream);
     }
     for (int i = 0; i < 2 && st == GBMM_OK; ++i)
-        st = gbmm_gemm(dt, 1, n, k, m, 1, 0, g.d[i], 0, ldd, 0, lx.p, 0, lx.ld, 0, dw[i], 0, ld_dw, 0, stream);
+        st = gbmm_gemm(dt, 1, n, k, m, 1, 0, g.d[i], 0, ldd, 0, lx.p(), 0, lx.ld, 0, dw[i], 0, ld_dw, 0, stream);
     return st;
 }
 
@@ -408,7 +435,8 @@ gbmm_status gbmm_gemm_i8_scratch_bytes(int64_t m, int64_t n, int64_t k, int alig
     Parts parts;
     if (plan.a_size) parts.add(m, round_up(k, 16 / plan.a_size), plan.a_size);
     if (plan.b_size) parts.add(n, round_up(k, 16 / plan.b_size), plan.b_size);
-    *bytes = parts.bytes;
+    if (!parts.ok) return too_large(fn);
+    *bytes = parts.needed();
     return GBMM_OK;
 }
 
@@ -432,7 +460,8 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
     const int64_t lda2 = plan.a_size ? round_up(k, 16 / plan.a_size) : lda, ldb2 = plan.b_size ? round_up(k, 16 / plan.b_size) : ldb;
     Parts parts;
     const uint64_t a_at = plan.a_size ? parts.add(m, lda2, plan.a_size) : 0, b_at = plan.b_size ? parts.add(n, ldb2, plan.b_size) : 0;
-    const uint64_t need = plan.a_size || plan.b_size ? parts.bytes : 0;
+    const uint64_t need = parts.needed();
+    if (!parts.ok) return too_large(fn);
     const Operand ops[] = {matrix("a", a, ab, k, lda, 1, false),
                            {"scale_a", scale_a, scale_a ? static_cast<uint64_t>(m) * 4 : 0, 4, false},
                            matrix("b", b, bb, k, ldb, 1, false),

@@ -77,7 +77,25 @@ __device__ __forceinline__ R load_weights(const void *p) {
     else return __ldg(static_cast<const R *>(p));
 }
 
-// kShare: warps of a column (1, or all of a block where there are few columns)
+// Sums of N values over a warp: lanes trade halves of what they hold, so that N + log2(32 / N) exchanges do in place of
+// 5 N.  v[0] of lane l is then the sum of value l / (32 / N).
+template <int N>
+__device__ __forceinline__ void reduce_scatter(float (&v)[N], int lane) {
+    int bit = kLanes / 2;
+#pragma unroll
+    for (int half = N / 2; half >= 1; half /= 2, bit /= 2) {
+        const bool high = (lane & bit) != 0;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float keep = high ? v[half + i] : v[i], send = high ? v[i] : v[half + i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+        }
+    }
+#pragma unroll
+    for (; bit >= 1; bit /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+}
+
+// kShare: warps of a column (1, or all of a block)
 template <typename T, int kM, int kBytes, int kShare>
 __global__ void __launch_bounds__(32 * kDotWarps) gated_rowdot_kernel(const GatedParams p) {
     using R = typename Raw<kBytes>::type;
@@ -134,31 +152,32 @@ __global__ void __launch_bounds__(32 * kDotWarps) gated_rowdot_kernel(const Gate
             u[r] = fmaf(wb, xv, u[r]);
         }
     }
+    float v[2 * kM];
 #pragma unroll
-    for (int r = 0; r < kM; ++r) {
-        g[r] = warp_sum(g[r]);
-        u[r] = warp_sum(u[r]);
-    }
+    for (int r = 0; r < kM; ++r) v[r] = g[r], v[kM + r] = u[r];
+    // value `which` of the warp's sums lies in v[0]; the gate's kM values come before the up projection's
+    reduce_scatter<2 * kM>(v, lane);
+    constexpr int kCopies = kLanes / (2 * kM);  // lanes that hold the same value
+    const int which = lane / kCopies;
+    float sum = v[0];
     if constexpr (kShare > 1) {
-        __shared__ float part[kShare][2][kM];
-        if (lane == 0) {
-#pragma unroll
-            for (int r = 0; r < kM; ++r) part[share][0][r] = g[r], part[share][1][r] = u[r];
-        }
+        __shared__ float part[kShare][2 * kM];
+        if (lane % kCopies == 0) part[share][which] = sum;
         __syncthreads();
         if (share != 0) return;
+        sum = 0.f;
 #pragma unroll
-        for (int q = 1; q < kShare; ++q)
-#pragma unroll
-            for (int r = 0; r < kM; ++r) g[r] += part[q][0][r], u[r] += part[q][1][r];
+        for (int q = 0; q < kShare; ++q) sum += part[q][which];
     }
-#pragma unroll
-    for (int r = 0; r < kM; ++r) {
-        if (lane != r || r >= rows) continue;
-        static_cast<T *>(p.h)[r * p.ldh + j] = Elem<T>::from_f(gate_act(p.act, g[r]) * u[r]);
-        if (p.saved[0] != nullptr) {
-            static_cast<T *>(p.saved[0])[r * p.ld_saved + j] = Elem<T>::from_f(g[r]);
-            static_cast<T *>(p.saved[1])[r * p.ld_saved + j] = Elem<T>::from_f(u[r]);
+    const float other = __shfl_down_sync(0xffffffffu, sum, kM * kCopies);  // the up projection's value
+    if (lane % kCopies == 0 && which < rows) {
+        const int64_t r = which;
+        if (which < kM) {
+            static_cast<T *>(p.h)[r * p.ldh + j] = Elem<T>::from_f(gate_act(p.act, sum) * other);
+            if (p.saved[0] != nullptr) {
+                static_cast<T *>(p.saved[0])[r * p.ld_saved + j] = Elem<T>::from_f(sum);
+                static_cast<T *>(p.saved[1])[r * p.ld_saved + j] = Elem<T>::from_f(other);
+            }
         }
     }
 }
@@ -656,24 +675,24 @@ cudaError_t gated_grad_t(const GatedGradParams &p, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// 16-bit rows that TMA cannot read, written 16 bytes at a time into rows that it can
+// 16-bit rows that TMA cannot read, written again into rows that it can
 // ---------------------------------------------------------------------------
 
-struct alignas(16) Halves {
-    uint16_t v[8];
-};
-
-__global__ void __launch_bounds__(256) repack16_kernel(const RepackParams p) {
+// a warp takes 512 values of a row at a time
+__global__ void __launch_bounds__(256) repack16_kernel(const RepackParams p, int64_t parts) {
+    constexpr int kU = 8;
     grid_dep_begin();
-    const int64_t pieces = p.ldd / 8, total = pieces * p.rows;
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < total;
-         at += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t i = at / pieces, j = (at - i * pieces) * 8;
-        const uint16_t *src = static_cast<const uint16_t *>(p.src) + i * p.lds + j;
-        Halves h;
+    const int lane = threadIdx.x & 31;
+    const int64_t items = p.rows * parts, warps = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; at < items; at += warps) {
+        const int64_t i = at / parts, o0 = (at - i * parts) * (32 * kU);  // words of two values
+        const uint8_t *src = static_cast<const uint8_t *>(p.src) + 2 * i * p.lds;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.dst) + i * p.ldd);
+        uint32_t v[kU];
+        shifted_words<2, kU>(src, o0, 2 * p.cols, lane, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h.v[e] = j + e < p.cols ? __ldg(src + e) : uint16_t{0};
-        *reinterpret_cast<Halves *>(static_cast<uint16_t *>(p.dst) + i * p.ldd + j) = h;
+        for (int q = 0; q < kU; ++q)
+            if (2 * (o0 + 32 * q + lane) < p.ldd) dst[o0 + 32 * q + lane] = v[q];
     }
 }
 
@@ -692,7 +711,7 @@ cudaError_t launch_gated_simt(int dt, const GatedParams &p, cudaStream_t s) { GB
 cudaError_t launch_gated_grad(int dt, const GatedGradParams &p, cudaStream_t s) { GBMM_BY_TYPE(dt, gated_grad_t) }
 
 // The gradients of f32 blocks: x null or w null where one of them is not asked for.
-cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, cudaStream_t s) {
+cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, int *launches, cudaStream_t s) {
     TileArgs tx{}, txs{}, tw{}, tws{};
     unsigned x_small = 0, x_large = 0, w_small = 0, w_large = 0;
     OuterOut o{};
@@ -720,6 +739,7 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
     float *c = x != nullptr ? static_cast<float *>(x->c) : nullptr;
     // one grid for both where it has a block for each SM
     const uint64_t together = 2 * static_cast<uint64_t>(x_large) + w_large + (w_large & 1);
+    *launches = 1;
     if (x != nullptr && w != nullptr && together >= static_cast<uint64_t>(device_sm_count()) && together <= INT32_MAX) {
         both_gemm_simt_kernel<<<static_cast<unsigned>(together), 256, 0, s>>>(tx, c, x->ldc, 2 * x_large, tw, o, w_large);
         return cudaGetLastError();
@@ -729,14 +749,15 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
                                   ? launch_whole(sum_gemm_simt_kernel<8, 8>, x_large, s, tx, c, x->ldc)
                                   : launch_whole(sum_gemm_simt_kernel<4, 4>, x_small, s, txs, c, x->ldc);
         if (e != cudaSuccess || w == nullptr) return e;
+        *launches = 2;
     }
     return large_tiles(w_large, w_small, 12) ? launch_whole(outer_gemm_simt_kernel<8, 4>, w_large, s, tw, o)
                                              : launch_whole(outer_gemm_simt_kernel<4, 4>, w_small, s, tws, o);
 }
 cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s) {
-    const int64_t blocks = (p.rows * (p.ldd / 8) + 255) / 256, most = 16LL * device_sm_count();
+    const int64_t parts = (p.ldd + 511) / 512, blocks = (p.rows * parts + 7) / 8, most = 32LL * device_sm_count();
     if (blocks == 0) return cudaSuccess;
-    return launch_early(repack16_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, p);
+    return launch_early(repack16_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, p, parts);
 }
 
 }  // namespace gbmm

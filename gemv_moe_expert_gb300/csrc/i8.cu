@@ -390,52 +390,73 @@ cudaError_t dot_t(const GemmI8Params &p, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// codes laid out again, as bytes or as f16, 16 at a time; both operands of a product in one launch
+// codes laid out again, as bytes or as f16; both operands of a product in one launch
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void lay_out_piece(const RepackParams &p, int aligned, int64_t i, int64_t j) {
+// The codes of a row from column j0 on, 2048 for a warp: 16 a lane and access where rows allow it, else 4.
+__device__ __forceinline__ void lay_out_part(const RepackParams &p, bool aligned, int64_t i, int64_t j0, int lane) {
     const int8_t *row = static_cast<const int8_t *>(p.src) + i * p.lds;
-    uint4 v;
-    if (aligned && j + 16 <= p.cols) {
-        v = ld_stream16(row + j);
-    } else {
-        v = make_uint4(any4(row, j / 4, p.cols), any4(row, j / 4 + 1, p.cols), any4(row, j / 4 + 2, p.cols),
-                       any4(row, j / 4 + 3, p.cols));
-    }
-    if (p.to_size == 1) {
-        *reinterpret_cast<uint4 *>(static_cast<int8_t *>(p.dst) + i * p.ldd + j) = v;
+    if (aligned) {
+        constexpr int kU = 4;
+        uint4 v[kU];
+#pragma unroll
+        for (int q = 0; q < kU; ++q) {
+            const int64_t j = j0 + 16 * (lane + 32 * q);
+            if (j + 16 <= p.cols) v[q] = ld_stream16(row + j);
+            else v[q] = make_uint4(any4(row, j / 4, p.cols), any4(row, j / 4 + 1, p.cols), any4(row, j / 4 + 2, p.cols),
+                                   any4(row, j / 4 + 3, p.cols));
+        }
+#pragma unroll
+        for (int q = 0; q < kU; ++q) {
+            const int64_t j = j0 + 16 * (lane + 32 * q);
+            if (j >= p.ldd) break;
+            if (p.to_size == 1) {
+                *reinterpret_cast<uint4 *>(static_cast<int8_t *>(p.dst) + i * p.ldd + j) = v[q];
+                continue;
+            }
+            const uint2 w0 = codes_to_half(v[q].x), w1 = codes_to_half(v[q].y), w2 = codes_to_half(v[q].z),
+                        w3 = codes_to_half(v[q].w);
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dst) + i * p.ldd + j);
+            dst[0] = make_uint4(w0.x, w0.y, w1.x, w1.y);
+            if (j + 8 < p.ldd) dst[1] = make_uint4(w2.x, w2.y, w3.x, w3.y);
+        }
         return;
     }
-    const uint2 a = codes_to_half(v.x), b = codes_to_half(v.y), c = codes_to_half(v.z), d = codes_to_half(v.w);
-    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dst) + i * p.ldd + j);
-    dst[0] = make_uint4(a.x, a.y, b.x, b.y);
-    if (j + 8 < p.ldd) dst[1] = make_uint4(c.x, c.y, d.x, d.y);
+    constexpr int kU = 8;
+#pragma unroll 1
+    for (int64_t j1 = j0; j1 < j0 + 2048 && j1 < p.ldd; j1 += 128 * kU) {
+        uint32_t v[kU];
+        shifted_words<1, kU>(reinterpret_cast<const uint8_t *>(row), j1 / 4, p.cols, lane, v);
+#pragma unroll
+        for (int q = 0; q < kU; ++q) {
+            const int64_t j = j1 + 4 * (lane + 32 * q);
+            if (j >= p.ldd) break;
+            if (p.to_size == 1) *reinterpret_cast<uint32_t *>(static_cast<int8_t *>(p.dst) + i * p.ldd + j) = v[q];
+            else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.dst) + i * p.ldd + j) = codes_to_half(v[q]);
+        }
+    }
 }
 
 __global__ void __launch_bounds__(256) lay_out_codes_kernel(const RepackParams a, const RepackParams b, int a_aligned,
-                                                            int b_aligned) {
+                                                            int b_aligned, int64_t parts) {
     grid_dep_begin();
-    const int64_t pa = (a.ldd + 15) / 16, pb = (b.ldd + 15) / 16, na = pa * a.rows, total = na + pb * b.rows;
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < total;
-         at += static_cast<int64_t>(gridDim.x) * 256) {
-        if (at < na) {
-            const int64_t i = at / pa;
-            lay_out_piece(a, a_aligned, i, (at - i * pa) * 16);
-        } else {
-            const int64_t i = (at - na) / pb;
-            lay_out_piece(b, b_aligned, i, (at - na - i * pb) * 16);
-        }
+    const int lane = threadIdx.x & 31;
+    const int64_t items = (a.rows + b.rows) * parts, warps = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; at < items; at += warps) {
+        const int64_t i = at / parts, j0 = (at - i * parts) * 2048;
+        if (i < a.rows) lay_out_part(a, a_aligned, i, j0, lane);
+        else lay_out_part(b, b_aligned, i - a.rows, j0, lane);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_lay_out_codes(const RepackParams &a, const RepackParams &b, cudaStream_t s) {
-    const int64_t total = (a.ldd + 15) / 16 * a.rows + (b.ldd + 15) / 16 * b.rows;
-    const int64_t blocks = (total + 255) / 256, most = 16LL * device_sm_count();
+    const int64_t widest = a.ldd > b.ldd ? a.ldd : b.ldd, parts = (widest + 2047) / 2048;
+    const int64_t blocks = ((a.rows + b.rows) * parts + 7) / 8, most = 16LL * device_sm_count();
     if (blocks == 0) return cudaSuccess;
     return launch_early(lay_out_codes_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, a,
-                        b, static_cast<int>(rows_on(a.src, a.lds, 16)), static_cast<int>(rows_on(b.src, b.lds, 16)));
+                        b, static_cast<int>(rows_on(a.src, a.lds, 16)), static_cast<int>(rows_on(b.src, b.lds, 16)), parts);
 }
 
 cudaError_t launch_quantize_i8(int dt, const QuantizeParams &p, cudaStream_t s) {

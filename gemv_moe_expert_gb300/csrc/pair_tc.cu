@@ -85,30 +85,27 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
 
 // A warp's way out for 32 x 32 outputs, one row a lane: through shared memory (swizzled, so that no two
 // lanes meet in a bank) and one TMA store, which writes whole row segments and leaves what is outside the matrix
-// alone; rows that TMA cannot write element by element.  Direct 32-byte stores, every lane its own row, held a warp for
-// about 700 cycles each.
+// alone; where TMA cannot write the rows, a row at a time.  Direct 32-byte stores, every lane its own row, held a warp
+// for about 700 cycles each.
 template <typename TC>
 struct Writer {
     static constexpr int kBufs = sizeof(TC) == 4 ? 1 : 2;
     uint32_t base;  // 4 KB of shared memory
     int next = 0;
 
+    // where 16-byte piece i of row r lies
+    static __device__ __forceinline__ uint32_t piece(int r, int i) {
+        return sizeof(TC) == 4 ? r * 128 + ((i ^ (r & 7)) << 4) : r * 64 + ((i ^ ((r >> 1) & 3)) << 4);
+    }
+
     __device__ __forceinline__ void write(const float (&v)[32], const CUtensorMap *map, bool tma, TC *c, int64_t ld,
                                           int64_t row0, int64_t col, int64_t m, int64_t n, int lane) {
         if (row0 >= m || col >= n) return;
-        if (!tma) {
-            if (row0 + lane >= m) return;
-            TC *dst = c + (row0 + lane) * ld + col;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (col + i < n) dst[i] = Elem<TC>::from_f(v[i]);
-            return;
-        }
         const uint32_t buf = base + static_cast<uint32_t>(next) * (4096 / kBufs);
         next = (next + 1) % kBufs;
         if (lane == 0) bulk_store_read<kBufs - 1>();
         __syncwarp();
-        constexpr int kPieces = 32 * sizeof(TC) / 16;
+        constexpr int kPieces = 32 * sizeof(TC) / 16, kPer = 16 / sizeof(TC);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             uint32_t w[4];
@@ -119,18 +116,38 @@ struct Writer {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = pack2<TC>(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
             }
-            const uint32_t at = sizeof(TC) == 4 ? lane * 128 + ((i ^ (lane & 7)) << 4)
-                                                : lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                         "r"(w[3])
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + piece(lane, i)), "r"(w[0]), "r"(w[1]),
+                         "r"(w[2]), "r"(w[3])
                          : "memory");
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(map, buf, static_cast<int32_t>(col), static_cast<int32_t>(row0));
-            bulk_commit();
+        if (tma) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(map, buf, static_cast<int32_t>(col), static_cast<int32_t>(row0));
+                bulk_commit();
+            }
+            return;
         }
+        // rows that TMA cannot write: a row an access, a lane a column
+        __syncwarp();
+        const int rows = static_cast<int>(m - row0 < 32 ? m - row0 : 32);
+        TC *dst = c + row0 * ld + col + lane;
+        const bool live = col + lane < n;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r, dst += ld) {
+            const uint32_t at = buf + piece(r, lane / kPer) + lane % kPer * sizeof(TC);
+            if constexpr (sizeof(TC) == 4) {
+                uint32_t e;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(e) : "r"(at) : "memory");
+                if (live) *reinterpret_cast<uint32_t *>(dst) = e;
+            } else {
+                uint16_t e;
+                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(e) : "r"(at) : "memory");
+                if (live) *reinterpret_cast<uint16_t *>(dst) = e;
+            }
+        }
+        __syncwarp();
     }
     __device__ __forceinline__ void finish(int lane) const {
         if (lane == 0) bulk_store_done();

@@ -121,11 +121,17 @@ def test_scratch_sizes():
         assert fn(5, 4, 4, 4, True)[0] == DTYPE
         assert fn("bf16", -1, 4, 4, True)[0] == BAD
         assert fn("bf16", 4, 1 << 31, 4, True)[0] == BAD
+        assert fn("bf16", (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1, False)[0] == BAD
         for aligned in (False, True):
             sizes = [fn("bf16", m, 1000, 1000, aligned) for m in (0, 1, 1000, 100000)]
             assert all(st == gb.GBMM_OK for st, _ in sizes) and [v for _, v in sizes] == sorted(v for _, v in sizes)
         assert fn("bf16", 1000, 1000, 1000, True)[1] < fn("bf16", 1000, 1000, 1000, False)[1]
         assert fn("f32", 1000, 1000, 1000, True)[1] == fn("f32", 1000, 1000, 1000, False)[1]
+    # few rows times few weights need none, many do
+    assert gb.gbmm_gated_scratch_bytes("f16", 8, 1000, 1000, False) == (gb.GBMM_OK, 0)
+    assert gb.gbmm_gated_scratch_bytes("f16", 8, 10000, 10000, False)[1] > 2 * 2 * 10000 * 10000
+    assert gb.gbmm_gemm_i8_scratch_bytes(8, 1000, 1000, False) == (gb.GBMM_OK, 0)
+    assert gb.gbmm_gemm_i8_scratch_bytes(8, 10000, 10000, False)[1] > 10000 * 10000
     # rows that do not start on multiples of 16 bytes
     need = gb.gbmm_gated_scratch_bytes("bf16", 40, 32, 64, False)[1]
     over = dict(m=40, ldx=65, ldw=65)

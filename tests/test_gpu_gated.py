@@ -135,6 +135,17 @@ def test_forward_layouts(dtype, m, pad, off):
     b.check_forward("silu", b.forward("silu", save=True))
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k,pad,off", [(2, 4100, 8200, 0, 0), (5, 4096, 2104, 0, 0), (5, 4100, 2104, 8, 8),
+                                           (8, 4099, 1801, 3, 1), (4, 4099, 4097, 0, 0), (3, 300, 40000, 0, 0)])
+def test_forward_few_rows_of_large_weights(dtype, m, n, k, pad, off):
+    """Weights for which few rows go to the tensor cores, and rows that are laid out again for them."""
+    b = Block(dtype, m, n, k, pad=pad, off=off)
+    b.check_forward("silu", b.forward("silu", save=True))
+    if pad or k % 8:
+        b.check_forward("silu", b.forward("silu", scratch=False))
+
+
 @pytest.mark.parametrize("m", [12, 300])
 def test_forward_rows_that_start_anywhere_without_scratch(m):
     b = Block("bf16", m, 70, 130, pad=1, off=1)

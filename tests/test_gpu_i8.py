@@ -156,6 +156,15 @@ def test_product_layouts(m, pad, off):
     p.check("f16", p.run("f16", pad, off))
 
 
+@pytest.mark.parametrize("m,n,k,pad,off", [(8, 4096, 3001, 0, 0), (4, 8200, 4096, 0, 0), (3, 4099, 11000, 0, 0),
+                                           (5, 4100, 2003, 1, 1), (40, 70, 20000, 0, 0), (100, 70, 20001, 0, 0),
+                                           (12, 40, 66000, 0, 0), (250, 600, 9000, 0, 0), (300, 130, 4100, 16, 16)])
+def test_product_of_large_weights_and_long_sums(m, n, k, pad, off):
+    """Few rows on the tensor cores, and sums over several accumulators."""
+    p = Product(m, n, k, pad, off)
+    p.check("f32", p.run("f32"))
+
+
 @pytest.mark.parametrize("m,n,k", [(512, 2000, 576), (1000, 1300, 2100), (700, 5504, 64), (2049, 264, 1031)])
 def test_product_many_tiles(m, n, k):
     p = Product(m, n, k)
