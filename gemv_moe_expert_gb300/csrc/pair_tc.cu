@@ -120,7 +120,8 @@ struct Writer {
                          "r"(w[2]), "r"(w[3])
                          : "memory");
         }
-        if (tma) {
+        // a TMA store writes whole groups of 16 bytes, past the last column where that does not end one
+        if (tma && (col + 32 <= n || n * sizeof(TC) % 16 == 0)) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {

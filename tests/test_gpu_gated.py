@@ -136,6 +136,15 @@ def test_forward_layouts(dtype, m, pad, off):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k,pad", [(30, 133, 261, 3), (300, 133, 261, 3), (300, 1030, 1030, 2), (600, 1025, 513, 7)])
+def test_columns_that_end_inside_16_bytes_of_aligned_rows(dtype, m, n, k, pad):
+    """What lies behind the last column of each row of every output stays as it was."""
+    b = Block(dtype, m, n, k, pad=pad)
+    b.check_forward("silu", b.forward("silu", save=True))
+    b.check_backward("gelu", b.backward("gelu"))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("m,n,k,pad,off", [(2, 4100, 8200, 0, 0), (5, 4096, 2104, 0, 0), (5, 4100, 2104, 8, 8),
                                            (8, 4099, 1801, 3, 1), (4, 4099, 4097, 0, 0), (3, 300, 40000, 0, 0)])
 def test_forward_few_rows_of_large_weights(dtype, m, n, k, pad, off):
@@ -204,6 +213,33 @@ def test_projections_side_by_side(m):
     gb.check(gb.gbmm_gated("f16", 0, m, n, k, x, k, w, w[n:], k, h, n, both, both[:, n:], 2 * n, None, 0))
     gb.check(gb.gbmm_gated("f16", 0, m, n, k, x, k, w, w[n:].clone(), k, h2, n, *apart, n, None, 0))
     assert torch.equal(h, h2) and torch.equal(both, torch.cat(apart, dim=1))
+
+
+@pytest.mark.parametrize("m", [2, 20, 200])
+def test_offsets_past_32_bits(m):
+    """Weights and gradients with rows 2^30 elements apart (both weights side by side), outputs 2^24 apart."""
+    n, k, ldw, ldh = 6, 72, 1 << 30, 1 << 24
+    g = torch.Generator(device="cuda").manual_seed(m)
+    x, w = torch.randn(m, k, generator=g, device="cuda").half(), torch.randn(n, 2 * k, generator=g, device="cuda").half()
+    wide = torch.empty((n - 1) * ldw + 2 * k, dtype=torch.float16, device="cuda").as_strided((n, 2 * k), (ldw, 1))
+    wide.copy_(w)
+    outs = torch.empty((m - 1) * ldh + 3 * n, dtype=torch.float16, device="cuda").as_strided((m, 3 * n), (ldh, 1))
+    gb.check(gb.gbmm_gated("f16", 0, m, n, k, x, k, wide, wide[:, k:], ldw, outs, ldh, outs[:, n:], outs[:, 2 * n:], ldh,
+                           None, 0))
+    tight = torch.empty(3, m, n, device="cuda").half()
+    halves = [w[:, :k].contiguous(), w[:, k:].contiguous()]
+    gb.check(gb.gbmm_gated("f16", 0, m, n, k, x, k, *halves, k, tight[0], n, tight[1], tight[2], n, None, 0))
+    assert torch.equal(outs.reshape(m, 3, n).transpose(0, 1), tight)
+    d_h = torch.randn(m, n, generator=g, device="cuda").half()
+    need = gb.gbmm_gated_backward_scratch_bytes("f16", m, n, k, False)[1]
+    scratch = torch.empty(need, dtype=torch.uint8, device="cuda")
+    dw = torch.empty((n - 1) * ldw + 2 * k, dtype=torch.float16, device="cuda").as_strided((n, 2 * k), (ldw, 1))
+    dx, dx2, dw2 = torch.empty_like(x), torch.empty_like(x), torch.empty(2, n, k, device="cuda").half()
+    gb.check(gb.gbmm_gated_backward("f16", 0, m, n, k, x, k, wide, wide[:, k:], ldw, tight[1], tight[2], n, d_h, n, dx, k,
+                                    dw, dw[:, k:], ldw, scratch, need))
+    gb.check(gb.gbmm_gated_backward("f16", 0, m, n, k, x, k, *halves, k, tight[1], tight[2], n, d_h, n, dx2, k, dw2[0],
+                                    dw2[1], k, scratch, need))
+    assert torch.equal(dx, dx2) and torch.equal(dw[:, :k], dw2[0]) and torch.equal(dw[:, k:], dw2[1])
 
 
 BACK_SIZES = [(1, 1, 1), (1, 64, 128), (3, 5, 7), (7, 40, 264), (16, 64, 64), (33, 129, 65), (64, 128, 256),

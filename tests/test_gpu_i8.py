@@ -156,6 +156,14 @@ def test_product_layouts(m, pad, off):
     p.check("f16", p.run("f16", pad, off))
 
 
+@pytest.mark.parametrize("m", [40, 300, 700])
+@pytest.mark.parametrize("n,cpad", [(133, 3), (1030, 2), (33, 3), (35, 1)])
+def test_product_columns_that_end_inside_16_bytes_of_aligned_rows(m, n, cpad):
+    p = Product(m, n, 272)
+    for dtype in ("f32", "f16", "bf16"):
+        p.check(dtype, p.run(dtype, cpad))
+
+
 @pytest.mark.parametrize("m,n,k,pad,off", [(8, 4096, 3001, 0, 0), (4, 8200, 4096, 0, 0), (3, 4099, 11000, 0, 0),
                                            (5, 4100, 2003, 1, 1), (40, 70, 20000, 0, 0), (100, 70, 20001, 0, 0),
                                            (12, 40, 66000, 0, 0), (250, 600, 9000, 0, 0), (300, 130, 4100, 16, 16)])
@@ -201,6 +209,30 @@ def test_product_of_nothing_and_scales_that_are_not_finite(m):
                                                       .view(np.uint8).copy()))
     bad = np.isnan(p.run("f32"))
     assert bad[m // 2].all() and bad.sum() == 40
+
+
+@pytest.mark.parametrize("m", [2, 20, 200, 600])
+def test_offsets_past_32_bits(m):
+    """Codes with rows 2^30 bytes apart, values and outputs 2^24 elements apart."""
+    n, k, ldb, ldc = 6, 144, 1 << 30, 1 << 24
+    g = torch.Generator(device="cuda").manual_seed(m)
+    wide = torch.empty((m - 1) * ldc + k, dtype=torch.bfloat16, device="cuda").as_strided((m, k), (ldc, 1))
+    x = torch.randn(m, k, generator=g, device="cuda").bfloat16()
+    wide.copy_(x)
+    q = [torch.empty(m, k, dtype=torch.int8, device="cuda"),
+         torch.empty((m - 1) * ldc + k, dtype=torch.int8, device="cuda").as_strided((m, k), (ldc, 1))]
+    s = torch.empty(2, m, device="cuda")
+    gb.check(gb.gbmm_quantize_i8("bf16", m, k, x, k, q[0], k, s[0]))
+    gb.check(gb.gbmm_quantize_i8("bf16", m, k, wide, ldc, q[1], ldc, s[1]))
+    assert torch.equal(q[0], q[1]) and torch.equal(s[0], s[1])
+    b = torch.randint(-128, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    far = torch.empty((n - 1) * ldb + k, dtype=torch.int8, device="cuda").as_strided((n, k), (ldb, 1))
+    far.copy_(b)
+    y = torch.empty((m - 1) * ldc + n, device="cuda").as_strided((m, n), (ldc, 1))
+    need = gb.gbmm_gemm_i8_scratch_bytes(m, n, k, False)[1]
+    scratch = torch.empty(need + 1, dtype=torch.uint8, device="cuda")
+    gb.check(gb.gbmm_gemm_i8("f32", m, n, k, q[1], ldc, None, far, ldb, None, y, ldc, scratch, need))
+    assert torch.equal(y, (q[0].double() @ b.double().T).float())
 
 
 def layer(m, n, k, t, stream=None):
