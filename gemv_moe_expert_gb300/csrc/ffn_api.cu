@@ -433,8 +433,8 @@ gbmm_status gbmm_gemm_i8_scratch_bytes(int64_t m, int64_t n, int64_t k, int alig
     const I8Plan plan = i8_plan(m, n, k, aligned != 0, aligned != 0);
     if (plan.a_size == 0 && plan.b_size == 0) return GBMM_OK;
     Parts parts;
-    if (plan.a_size) parts.add(m, round_up(k, 16 / plan.a_size), plan.a_size);
-    if (plan.b_size) parts.add(n, round_up(k, 16 / plan.b_size), plan.b_size);
+    if (plan.a_size) parts.add(m, round_up(k, 16), plan.a_size);
+    if (plan.b_size) parts.add(n, round_up(k, 16), plan.b_size);
     if (!parts.ok) return too_large(fn);
     *bytes = parts.needed();
     return GBMM_OK;
@@ -457,7 +457,7 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
     if (!span(m, k, lda, 1, &ab) || !span(n, k, ldb, 1, &bb) || !span(m, n, ldc, size, &cb))
         return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: operand extent overflows", fn);
     const I8Plan plan = i8_plan(m, n, k, rows16(a, lda), rows16(b, ldb));
-    const int64_t lda2 = plan.a_size ? round_up(k, 16 / plan.a_size) : lda, ldb2 = plan.b_size ? round_up(k, 16 / plan.b_size) : ldb;
+    const int64_t lda2 = plan.a_size ? round_up(k, 16) : lda, ldb2 = plan.b_size ? round_up(k, 16) : ldb;
     Parts parts;
     const uint64_t a_at = plan.a_size ? parts.add(m, lda2, plan.a_size) : 0, b_at = plan.b_size ? parts.add(n, ldb2, plan.b_size) : 0;
     const uint64_t need = parts.needed();

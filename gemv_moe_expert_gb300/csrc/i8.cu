@@ -416,9 +416,11 @@ __device__ __forceinline__ void lay_out_part(const RepackParams &p, bool aligned
             }
             const uint2 w0 = codes_to_half(v[q].x), w1 = codes_to_half(v[q].y), w2 = codes_to_half(v[q].z),
                         w3 = codes_to_half(v[q].w);
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dst) + i * p.ldd + j);
-            dst[0] = make_uint4(w0.x, w0.y, w1.x, w1.y);
-            if (j + 8 < p.ldd) dst[1] = make_uint4(w2.x, w2.y, w3.x, w3.y);
+            // one store of a whole sector: two of 16 bytes each wrote half of every sector twice
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             static_cast<uint16_t *>(p.dst) + i * p.ldd + j),
+                         "r"(w0.x), "r"(w0.y), "r"(w1.x), "r"(w1.y), "r"(w2.x), "r"(w2.y), "r"(w3.x), "r"(w3.y)
+                         : "memory");
         }
         return;
     }

@@ -203,8 +203,8 @@ struct OuterGemmParams {
     int64_t m, n, k, ldx, ldd, ldc;
 };
 
-// Rows laid out again: src [rows, cols] into dst [rows, ldd], ldd a multiple of 16 bytes.  16-bit values (gated.cu);
-// 8-bit codes (i8.cu), to_size bytes each at dst: 1, or 2 for f16.
+// Rows laid out again: src [rows, cols] into dst [rows, ldd].  16-bit values, ldd a multiple of 8 (gated.cu); 8-bit
+// codes, ldd a multiple of 16, to_size bytes each at dst: 1, or 2 for f16 (i8.cu).
 struct RepackParams {
     const void *src;
     void *dst;
