@@ -590,7 +590,7 @@ cudaError_t gated_simt_t(const GatedParams &p, cudaStream_t s) {
     if (large == 0) return cudaErrorInvalidConfiguration;
     const unsigned sms = static_cast<unsigned>(device_sm_count());
     // At most one tile an SM: up to eight CTAs share a tile, as many as make the busiest SM's share smallest.
-    // 512 x 1408 x 2048, 88 tiles: 206 us whole, 195 by two, SPLIT3 by three.
+    // 512 x 1408 x 2048, 88 tiles: 206 us whole, 195 by two, 177 by three.
     if (large <= sms) {
         const bool few = 4 * large <= sms;
         const unsigned tiles = few ? small : large;
