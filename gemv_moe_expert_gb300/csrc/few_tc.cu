@@ -459,12 +459,12 @@ int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcP
     int tokens = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 || codes ? 64 : 128;
     Split s = split_for(codes, tokens, m, n, k, num_sms);
     if (codes && m > 64) {
-        // Tiles of 128 tokens read the weights once, but have an SM to themselves: taken where they fill the SMs
+        // Tiles of 128 tokens read the weights once, but have an SM to themselves: taken where they fill the SMs once
         // (128 tokens: 4096 x 11008 26.5 us against 38 with 64 a tile, 11008 x 4096 42.7 against 37.7), or where 64 leave
         // no room for the accumulators.
         const Split wide = split_for(codes, 128, m, n, k, num_sms);
         const int64_t kb = (k + 127) / 128;
-        if ((m <= 128 && 4 * wide.ctas >= 3LL * num_sms) || kb > s.split * code_blocks(64)) {
+        if ((m <= 128 && wide.ctas <= num_sms && 4 * wide.ctas >= 3LL * num_sms) || kb > s.split * code_blocks(64)) {
             tokens = 128;
             s = wide;
         }

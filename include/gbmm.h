@@ -26,7 +26,7 @@
  *     the captured buffers hold.  GroupedPrefill's grouped kernel is launched
  *     with programmatic stream serialisation behind the map kernel and waits
  *     for it before touching global memory, which a capture keeps; the kernels
- *     of gbmm_moe_* are behind whatever precedes them.  Not with
+ *     of gbmm_moe_*, gbmm_gated* and *_i8 are behind whatever precedes them.  Not with
  *     GBMM_DEBUG_SYNC=1 (it synchronises the stream).
  *   - Debugging: with the environment variable GBMM_DEBUG_SYNC=1 (read once
  *     per process) every launch is followed by a stream synchronisation, so a
@@ -528,8 +528,8 @@ GBMM_API gbmm_status gbmm_matmul_id_q4(gbmm_dtype dt, uint32_t m, int64_t n, int
  * [n, k], h, gate, up and d_h [m, n], rows ld* elements apart (both weights with the
  * same ldw, both saved projections with the same ld_saved, both weights' gradients
  * with the same ld_dw; two of them may lie side by side in rows of that pitch).
- * m, n and k below 2^31.  Sums are f32 in a fixed order, and each output is rounded
- * once.  Pointers must be aligned to their elements, and outputs must not overlap
+ * m, n and k below 2^31.  Sums are f32 in a fixed order, activations are off by at most
+ * 2^-20 of their argument, and each output is rounded once.  Pointers must be aligned to their elements, and outputs must not overlap
  * inputs, scratch or each other (GBMM_ERR_OVERLAP).
  */
 enum {
