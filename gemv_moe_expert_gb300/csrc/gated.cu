@@ -243,9 +243,15 @@ struct TileArgs {
     int32_t a_vec, b_vec;  // groups of four elements can be read in one access
     int64_t tiles_n;
     uint32_t parts = 1;    // CTAs that share a tile
+    int32_t fold = 0;      // a long contraction: the sums of kFold steps each are added up in shared memory
 };
 
 constexpr int kTK = 16;
+
+// Steps of the contraction whose sums stay in one register.  Normal products summed one after the other end 4e-7 of the
+// sum's own size off (rms) after 512, 1.2e-6 after 4096 and 3.3e-6 after 32768, the rounding of each addition growing with
+// the sum so far; in runs of 512 whose sums are then added, 32768 stay at 5e-7.
+constexpr int64_t kFold = 32;
 
 __device__ __forceinline__ uint64_t both(float v) {
     uint64_t d;
@@ -272,10 +278,36 @@ struct TileProduct {
     };
     uint64_t acc[kProducts][kTM][kTN / 2];
 
+    static constexpr uint32_t kFoldBytes = kProducts * kTM * kTN * 256 * sizeof(float);
+
     __device__ __forceinline__ float at(int pr, int r, int c) const { return half_of(acc[pr][r][c / 2], c & 1); }
+
+    // adds what is stored to the sums (unless they are the first) and stores them again (unless they are the last); each
+    // thread its own
+    __device__ __forceinline__ void fold(uint64_t *sums, bool first, bool last) {
+        int i = threadIdx.x;
+#pragma unroll
+        for (int pr = 0; pr < kProducts; ++pr)
+#pragma unroll
+            for (int r = 0; r < kTM; ++r)
+#pragma unroll
+                for (int c = 0; c < kTN / 2; ++c, i += 256) {
+                    uint64_t &v = acc[pr][r][c];
+                    if (!first) {
+                        const uint64_t w = sums[i];
+                        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
+                    }
+                    if (!last) {
+                        sums[i] = v;
+                        v = 0;
+                    }
+                }
+    }
 
     // part of parts: the share of the contraction (kSum: of both sources) that this block takes
     __device__ __forceinline__ void run(const TileArgs &t, int64_t m0, int64_t n0, Smem &sm, int part = 0, int parts = 1) {
+        extern __shared__ __align__(16) uint64_t sums[];
+        bool folded = false;
         const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
         for (int q = 0; q < kProducts; ++q)
@@ -326,9 +358,14 @@ struct TileProduct {
                 }
             }
             if (more) store(cur ^ 1);
+            if (t.fold && more && (step - begin + 1) % kFold == 0) {
+                fold(sums, !folded, false);
+                folded = true;
+            }
             __syncthreads();
             cur ^= 1;
         }
+        if (folded) fold(sums, false, true);
     }
 
     // The cluster's other CTAs hand their sums to the first one through shared memory, two rows a thread at a time;
@@ -541,7 +578,7 @@ __global__ void __launch_bounds__(256, 2) outer_gemm_simt_kernel(const TileArgs 
 }
 // Both gradients in one grid, so that the tiles of one fill the last round of the other's: clusters of two,
 // the first x_blocks of them the gradient of x (the longer tiles), a pair a tile.
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(256, 2)
 both_gemm_simt_kernel(const TileArgs tx, float *out, int64_t ldc, unsigned x_blocks, const TileArgs tw, const OuterOut o,
                       unsigned w_blocks) {
     __shared__ __align__(16) union {
@@ -554,10 +591,32 @@ both_gemm_simt_kernel(const TileArgs tx, float *out, int64_t ldc, unsigned x_blo
 
 // Not started early behind the kernel before it: blocks that take places as they come free gather on a few SMs, and a
 // grid of about one block an SM then takes twice as long (512 x 1408 x 2048 gradients: 412 against 300 us).
+// cluster: CTAs of a cluster; fold_bytes: the shared memory of sums of sums, 0 for short contractions.
 template <typename... Params, typename... Args>
-cudaError_t launch_whole(void (*kernel)(Params...), unsigned blocks, cudaStream_t s, const Args &...args) {
-    kernel<<<blocks, 256, 0, s>>>(args...);
-    return cudaGetLastError();
+cudaError_t launch_whole(void (*kernel)(Params...), unsigned blocks, unsigned cluster, uint32_t fold_bytes, cudaStream_t s,
+                         const Args &...args) {
+    if (fold_bytes > 0) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(fold_bytes));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = fold_bytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// whether a contraction of k (of `sources`, divided over `parts`) is long: from one and a half runs
+int32_t folds(int64_t k, int sources, int64_t parts) {
+    return (k + kTK - 1) / kTK * sources / parts > kFold * 3 / 2;
 }
 
 bool groups_of_4(const void *p, int64_t ld, size_t size) {
@@ -598,21 +657,18 @@ cudaError_t gated_simt_t(const GatedParams &p, cudaStream_t s) {
         for (unsigned q = 3; q <= 8 && p.k >= 256 * static_cast<int64_t>(q); ++q)
             if (((tiles * q + sms - 1) / sms) * parts < ((tiles * parts + sms - 1) / sms) * q) parts = q;
         t.parts = parts;
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = parts;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.gridDim = dim3(parts * tiles);
-        cfg.blockDim = dim3(256);
-        cfg.stream = s;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return few ? cudaLaunchKernelEx(&cfg, gated_simt_kernel<T, 4, 4, true>, t, p)
-                   : cudaLaunchKernelEx(&cfg, gated_simt_kernel<T, 8, 4, true>, t, p);
+        t.fold = folds(p.k, 1, parts);
+        return few ? launch_whole(gated_simt_kernel<T, 4, 4, true>, parts * tiles, parts,
+                                  t.fold ? TileProduct<T, kGated, 4, 4>::kFoldBytes : 0, s, t, p)
+                   : launch_whole(gated_simt_kernel<T, 8, 4, true>, parts * tiles, parts,
+                                  t.fold ? TileProduct<T, kGated, 8, 4>::kFoldBytes : 0, s, t, p);
     }
-    if (large_tiles(large, small, 12)) return launch_whole(gated_simt_kernel<T, 8, 4, false>, large, s, t, p);
-    return launch_whole(gated_simt_kernel<T, 4, 4, false>, small, s, t, p);
+    t.fold = folds(p.k, 1, 1);
+    if (large_tiles(large, small, 12))
+        return launch_whole(gated_simt_kernel<T, 8, 4, false>, large, 1, t.fold ? TileProduct<T, kGated, 8, 4>::kFoldBytes : 0,
+                            s, t, p);
+    return launch_whole(gated_simt_kernel<T, 4, 4, false>, small, 1, t.fold ? TileProduct<T, kGated, 4, 4>::kFoldBytes : 0, s,
+                        t, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -720,6 +776,7 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
         tx.a_vec = groups_of_4(x->a[0], x->lda, 4) && groups_of_4(x->a[1], x->lda, 4);
         tx.b_vec = groups_of_4(x->b[0], x->ldb, 4) && groups_of_4(x->b[1], x->ldb, 4);
         txs = tx;
+        txs.fold = folds(x->k, 2, 1);
         x_small = tile_grid(x->m, x->n, 64, 64, &txs);
         x_large = tile_grid(x->m, x->n, 128, 128, &tx);
         if (x_large == 0) return cudaErrorInvalidConfiguration;
@@ -728,6 +785,7 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
         tw = TileArgs{{w->x, w->x}, {w->d[0], w->d[1]}, w->k, w->n, w->m, w->ldx, w->ldd, 0, 0, 0};
         tw.a_vec = groups_of_4(w->x, w->ldx, 4);
         tw.b_vec = groups_of_4(w->d[0], w->ldd, 4) && groups_of_4(w->d[1], w->ldd, 4);
+        tw.fold = folds(w->m, 1, 1);
         tws = tw;
         w_small = tile_grid(tw.m, tw.n, 64, 64, &tws);
         w_large = tile_grid(tw.m, tw.n, 128, 64, &tw);
@@ -741,19 +799,30 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
     const uint64_t together = 2 * static_cast<uint64_t>(x_large) + w_large + (w_large & 1);
     *launches = 1;
     if (x != nullptr && w != nullptr && together >= static_cast<uint64_t>(device_sm_count()) && together <= INT32_MAX) {
-        both_gemm_simt_kernel<<<static_cast<unsigned>(together), 256, 0, s>>>(tx, c, x->ldc, 2 * x_large, tw, o, w_large);
-        return cudaGetLastError();
+        tx.fold = folds(x->k, 2, 2);
+        const uint32_t bytes = tx.fold || tw.fold ? TileProduct<float, kSum, 8, 8>::kFoldBytes : 0;
+        static_assert(TileProduct<float, kSum, 8, 8>::kFoldBytes == TileProduct<float, kOuter, 8, 4>::kFoldBytes, "both");
+        return launch_whole(both_gemm_simt_kernel, static_cast<unsigned>(together), 2, bytes, s, tx, c, x->ldc, 2 * x_large,
+                            tw, o, w_large);
     }
     if (x != nullptr) {
-        const cudaError_t e = large_tiles(x_large, x_small, 8)
-                                  ? launch_whole(sum_gemm_simt_kernel<8, 8>, x_large, s, tx, c, x->ldc)
-                                  : launch_whole(sum_gemm_simt_kernel<4, 4>, x_small, s, txs, c, x->ldc);
+        tx.fold = txs.fold;
+        const cudaError_t e =
+            large_tiles(x_large, x_small, 8)
+                ? launch_whole(sum_gemm_simt_kernel<8, 8>, x_large, 1, tx.fold ? TileProduct<float, kSum, 8, 8>::kFoldBytes : 0,
+                               s, tx, c, x->ldc)
+                : launch_whole(sum_gemm_simt_kernel<4, 4>, x_small, 1, tx.fold ? TileProduct<float, kSum, 4, 4>::kFoldBytes : 0,
+                               s, txs, c, x->ldc);
         if (e != cudaSuccess || w == nullptr) return e;
         *launches = 2;
     }
-    return large_tiles(w_large, w_small, 12) ? launch_whole(outer_gemm_simt_kernel<8, 4>, w_large, s, tw, o)
-                                             : launch_whole(outer_gemm_simt_kernel<4, 4>, w_small, s, tws, o);
+    return large_tiles(w_large, w_small, 12)
+               ? launch_whole(outer_gemm_simt_kernel<8, 4>, w_large, 1, tw.fold ? TileProduct<float, kOuter, 8, 4>::kFoldBytes : 0,
+                              s, tw, o)
+               : launch_whole(outer_gemm_simt_kernel<4, 4>, w_small, 1, tw.fold ? TileProduct<float, kOuter, 4, 4>::kFoldBytes : 0,
+                              s, tws, o);
 }
+
 cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s) {
     const int64_t parts = (p.ldd + 511) / 512, blocks = (p.rows * parts + 7) / 8, most = 32LL * device_sm_count();
     if (blocks == 0) return cudaSuccess;

@@ -283,6 +283,44 @@ def test_backward_many_tiles(dtype, m, n, k):
     b.check_backward("silu", b.backward("silu"))
 
 
+# A product just under half a step of f32 beyond 1: added one after the other, every one that is added to 8192 or more
+# is rounded down, and 16384 of them end 2e-4 too low.
+LOST = float(np.float32(1 + 2.0 ** -11 - 2.0 ** -22))
+
+
+@pytest.mark.parametrize("m", [1, 20, 70, 300])
+def test_long_sums_in_f32(m):
+    """A projection's sum is made of runs of at most 512 products, and of at most k / 512 + 16 sums of runs:
+    (512 + k / 512 + 16) u of the magnitudes, 4e-5 at k = 32768 and not 2e-3."""
+    n, k = 70, 32768
+    x, w = torch.full((m, k), LOST, device="cuda"), torch.ones(n, k, device="cuda")
+    st, need = gb.gbmm_gated_scratch_bytes("f32", m, n, k, False)
+    gb.check(st)
+    scratch, out = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.empty(3, m, n, device="cuda")
+    gb.check(gb.gbmm_gated("f32", CODE["relu"], m, n, k, x, k, w, w, k, out[0], n, out[1], out[2], n, scratch, need))
+    r = (512 + k / 512 + 16) * U
+    assert (out[1:].double() / (k * LOST) - 1).abs().max() <= r
+    assert (out[0].double() / (k * LOST) ** 2 - 1).abs().max() <= 2 * r + r * r + 16 * U
+
+
+@pytest.mark.parametrize("d_x,d_w", [(True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("m,n,k", [(16384, 40, 72), (16384, 300, 1100), (40, 16384, 72), (300, 16384, 1100)])
+def test_long_sums_of_gradients_in_f32(m, n, k, d_x, d_w):
+    """As above, over 2 n products for x and over m for the weights."""
+    x, w = torch.ones(m, k, device="cuda"), torch.ones(n, k, device="cuda")
+    one, d_h = torch.ones(m, n, device="cuda"), torch.full((m, n), LOST, device="cuda")
+    dx, dw = torch.empty(m, k, device="cuda"), torch.empty(2, n, k, device="cuda")
+    st, need = gb.gbmm_gated_backward_scratch_bytes("f32", m, n, k, True)
+    gb.check(st)
+    scratch = torch.empty(need, dtype=torch.uint8, device="cuda")
+    gb.check(gb.gbmm_gated_backward("f32", CODE["relu"], m, n, k, x if d_w else None, k, w if d_x else None,
+                                    w if d_x else None, k, one, one, n, d_h, n, dx if d_x else None, k,
+                                    dw[0] if d_w else None, dw[1] if d_w else None, k, scratch, need))
+    for on, out, length in ((d_x, dx, 2 * n), (d_w, dw, m)):
+        if on:
+            assert (out.double() / (length * LOST) - 1).abs().max() <= (512 + length / 512 + 16) * U
+
+
 def test_backward_of_nothing_writes_zeros():
     t = torch.full((3, 8, 16), 7.0, device="cuda")
     gb.check(gb.gbmm_gated_backward("f32", 0, 0, 8, 16, None, 16, t, t, 16, None, None, 8, None, 8, None, 16, t[0],
