@@ -146,7 +146,7 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     grid_dep_begin();
     // this CTA's share of the k-blocks (128 bytes of a row each)
     constexpr int kBlock = kCodes ? 128 : 64;
-    const int kb_total = (p.k + kBlock - 1) / kBlock;
+    const int kb_total = p.k / kBlock + (p.k % kBlock != 0);
     const int kb0 = static_cast<int>(static_cast<int64_t>(kb_total) * rank / ksplit);
     const int kblocks = static_cast<int>(static_cast<int64_t>(kb_total) * (rank + 1) / ksplit) - kb0;
 

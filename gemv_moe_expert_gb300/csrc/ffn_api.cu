@@ -322,12 +322,8 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     if (!empty && (scratch == nullptr || scratch_bytes < parts.bytes))
         return fail(GBMM_ERR_SCRATCH, "%s: needs %llu bytes of scratch (got %llu)", fn, (unsigned long long)parts.bytes,
                     (unsigned long long)(scratch ? scratch_bytes : 0));
-    // the products' kernels are asked for before the first launch, so that nothing runs where one is missing
-    static const char *const kProducts[] = {"gbmm_fill_zero",     "gbmm_gemm_tc", "gbmm_gemm_simt", "gbmm_gemv_rowdot",
-                                            "gbmm_gemv_coldot", "gbmm_gemv_tc"};
-    if (!resolve_kernel(fn)) return GBMM_ERR_KERNEL_UNAVAILABLE;
-    for (const char *name : kProducts)
-        if (!resolve_kernel(name)) return GBMM_ERR_KERNEL_UNAVAILABLE;
+    // the kernels are asked for before the first launch, so that nothing runs where one is missing
+    if (!resolve_kernel(fn) || !resolve_kernel("gbmm_fill_zero")) return GBMM_ERR_KERNEL_UNAVAILABLE;
     cudaStream_t s = cuda_stream(stream);
     if (empty) {
         if (m == 0) {
@@ -343,41 +339,40 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     g.gate = gate;
     g.up = up;
     g.d_h = d_h;
-    // both gradients of the weights are one batch where one lies whole behind the other and neither operand of the
-    // product between them; the projections' gradients lie in the same order then
-    const intptr_t gap = reinterpret_cast<intptr_t>(d_w_up) - reinterpret_cast<intptr_t>(d_w_gate);
-    const uintptr_t dw_lo = reinterpret_cast<uintptr_t>(gap < 0 ? d_w_up : d_w_gate);
-    const uintptr_t dw_hi = reinterpret_cast<uintptr_t>(gap < 0 ? d_w_gate : d_w_up) + dwb;
-    auto between = [&](const void *p, uint64_t bytes) {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-        return bytes > 0 && at < dw_hi && dw_lo < at + bytes;
-    };
-    const bool batched = dt != GBMM_F32 && need_w && static_cast<uint64_t>(gap < 0 ? -gap : gap) >= dwb &&
-                         !between(scratch, scratch_bytes) && !between(x, xb);
-    const int first = batched && gap < 0 ? 1 : 0;
-    const int64_t d_apart = static_cast<int64_t>(d_at[1] - d_at[0]) / static_cast<int64_t>(size);
-    g.d[first] = base + d_at[0];
-    g.d[!first] = base + d_at[1];
+    for (int i = 0; i < 2; ++i) g.d[i] = base + d_at[i];
     g.m = m;
     g.n = n;
     g.ld_saved = ld_saved;
     g.ld_dh = ld_dh;
     g.ldd = ldd;
     g.act = static_cast<int32_t>(activation);
+    void *const dw[2] = {d_w_gate, d_w_up};
     PairTcMaps maps{};
     PairTcParams q{};
-    if (need_x && dt != GBMM_F32) {
+    if (dt != GBMM_F32) {
+        const uint32_t rows = static_cast<uint32_t>(pair_tc_rows()), box = static_cast<uint32_t>(pair_tc_block_k());
         bool ok = pair_params(&q, &maps, dt, d_x, ld_dx, m, k, n);
-        for (int i = 0; i < 2 && ok; ++i)
-            ok = encode_matrix16(&maps.a[i], dt, g.d[i], n, m, ldd, static_cast<uint32_t>(pair_tc_rows())) &&
-                 encode_matrix16(&maps.b[i], dt, lw[i].p(), k, n, lw[i].ld, static_cast<uint32_t>(pair_tc_block_k()));
+        q.need_c = need_x;
+        q.need_dw = need_w;
+        q.ld_dw = ld_dw;
+        q.dw_tma = 1;
+        for (int i = 0; i < 2 && ok; ++i) {
+            if (need_x)
+                ok = encode_matrix16(&maps.a[i], dt, g.d[i], n, m, ldd, rows) &&
+                     encode_matrix16(&maps.b[i], dt, lw[i].p(), k, n, lw[i].ld, box);
+            if (need_w && ok) {
+                ok = encode_matrix16(&maps.dw_a[i], dt, g.d[i], n, m, ldd, box) &&
+                     encode_matrix16(&maps.dw_b, dt, lx.p(), k, m, lx.ld, box);
+                q.dw[i] = dw[i];
+                if (!encode_store32(&maps.out[1 + i], dt, dw[i], k, n, ld_dw)) q.dw_tma = 0;
+            }
+        }
         if (!ok) return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
     }
     st = lay_again(fn, lx, s);
     for (int i = 0; i < 2 && st == GBMM_OK; ++i) st = lay_again(fn, lw[i], s);
     if (st == GBMM_OK) st = finish_launch(launch_gated_grad(dt, g, s), fn, s);
     if (st != GBMM_OK) return st;
-    void *const dw[2] = {d_w_gate, d_w_up};
     if (dt == GBMM_F32) {
         const SumGemmParams px{{g.d[0], g.d[1]}, {w_gate, w_up}, d_x, m, k, n, ldd, ldw, ld_dx};
         const OuterGemmParams pw{x, {g.d[0], g.d[1]}, {dw[0], dw[1]}, m, n, k, ldx, ldd, ld_dw};
@@ -386,16 +381,7 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
         for (; st == GBMM_OK && launches > 1; --launches) st = finish_launch(cudaSuccess, fn, s);
         return st;
     }
-    if (need_x) st = finish_launch(launch_sum_gemm_tc(dt, maps, q, device_sm_count(), s), fn, s);
-    if (st != GBMM_OK || !need_w) return st;
-    if (batched) {  // one product over both projections: more tiles in a launch
-        const int64_t apart = (reinterpret_cast<intptr_t>(dw[!first]) - reinterpret_cast<intptr_t>(dw[first])) / 2;
-        return gbmm_gemm(dt, 2, n, k, m, 1, 0, g.d[first], 0, ldd, d_apart, lx.p(), 0, lx.ld, 0, dw[first], 0, ld_dw,
-                         apart, stream);
-    }
-    for (int i = 0; i < 2 && st == GBMM_OK; ++i)
-        st = gbmm_gemm(dt, 1, n, k, m, 1, 0, g.d[i], 0, ldd, 0, lx.p(), 0, lx.ld, 0, dw[i], 0, ld_dw, 0, stream);
-    return st;
+    return finish_launch(launch_gated_products_tc(dt, maps, q, device_sm_count(), s), fn, s);
 }
 
 gbmm_status gbmm_quantize_i8(gbmm_dtype dt, int64_t m, int64_t k, const void *x, int64_t ldx, int8_t *q, int64_t ldq,

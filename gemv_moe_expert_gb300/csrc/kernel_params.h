@@ -238,10 +238,17 @@ struct PairTcParams {
     int32_t tiles_m, tiles_n, num_tiles;  // set by the launcher
     uint32_t *err;
     uint64_t wait_limit_ns;
+    // gradients: c [m, n] over both sources of k, and dw[i] [k, n] over m; either may be left out
+    void *dw[2];
+    int64_t ld_dw;
+    int32_t need_c, need_dw, dw_tma;
+    int32_t pairs;                              // these and the next are set by the launcher
+    int32_t dw_tiles_m, c_units, c_split, dw_units, dw_split, early, behind;
 };
 struct PairTcMaps {
     CUtensorMap a[2], b[2];
-    CUtensorMap out[3];  // c and both saved projections, as 32 x 32 pieces
+    CUtensorMap out[3];  // c, and both saved projections or both weights' gradients, as 32 x 32 pieces
+    CUtensorMap dw_a[2], dw_b;  // gradients: the sources' columns and x, in 64 x 64 boxes
 };
 
 // The same products for some tens of tokens (few_tc.cu).
@@ -336,9 +343,9 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
 cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s);
 cudaError_t launch_lay_out_codes(const RepackParams &a, const RepackParams &b, cudaStream_t s);  // rows 0: nothing to do
 // on the tensor cores: gated a[0] = x, b = both weights, all K-contiguous in boxes of pair_tc_rows()
-// rows; sum a and b as in SumGemmParams, b in 64 x 64 boxes; codes a[0] and b[0] (f16) as gated
+// rows; gradients a and b as in SumGemmParams, b in 64 x 64 boxes; codes a[0] and b[0] (f16) as gated
 cudaError_t launch_gated_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s);
-cudaError_t launch_sum_gemm_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_gated_products_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_gemm_i8_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s);
 int pair_tc_rows();
 int pair_tc_block_k();

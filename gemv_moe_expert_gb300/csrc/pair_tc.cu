@@ -3,8 +3,10 @@
 //   kGated  h = act(x Wg^T) * (x Wu^T): the pair's even CTA loads 128 rows of Wg, its odd CTA
 //           the same 128 rows of Wu, so columns 0..127 of each CTA's accumulator hold the gate
 //           and 128..255 the up projection of the same outputs; one thread has both
-//   kSum    c = a0 b0 + a1 b1 (the gradient of x from those of both projections): one
-//           accumulator, the contraction runs over the first source and then the second
+//   kGrads  the gradients of x and of both weights from those of both projections, in one grid:
+//           c = a0 b0 + a1 b1, the contraction running over the first source and then the
+//           second, and dw_i = a_i^T x.  The tiles of c are the long ones; they come first, and
+//           those of dw level the pairs out (Walk)
 //   kCodes  c = (a b^T) scale_a scale_b for 8-bit codes held as f16: a product of two codes, and
 //           any sum of them below 2^24, is exact in the f32 accumulator; after each 1024 of k (at
 //           most 2^24) the epilogue adds the accumulator to 32-bit integers in registers
@@ -20,6 +22,8 @@
 //   warp 1      tensor memory; in the even CTA one thread issues the pair's MMAs
 //   warps 2..9  epilogue (both CTAs)
 // Every wait is bounded; a timeout raises both CTAs' abort flags and the device error word.
+#include <algorithm>
+
 #include "gated.cuh"
 
 namespace gbmm {
@@ -42,26 +46,33 @@ constexpr uint32_t kSmemBytes = kStages * kStageBytes + kEpiWarps * kOutBytes + 
 static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
 constexpr int kExactBlocks = 1024 / kBK;  // k-blocks whose sum of products of two codes stays within 2^24
 
-enum Mode { kGated, kSum, kCodes };
+enum Mode { kGated, kGrads, kCodes };
 
 template <int kMode>
 struct Shape {
     static constexpr int kTileN = kMode == kGated ? kBN / 2 : kBN;  // outputs across a tile
 };
 
+__host__ __device__ constexpr int blocks_for(int k) { return k / kBK + (k % kBK != 0); }
+
 struct Unit {
     int mb, nb;
     int h;       // half of the tile's columns that a half unit computes
     int halves;  // 2: whole tile, 1: half unit h, 0: nothing (half past n)
+    int dw;      // -1: c; 0, 1: that weight's gradient
 };
 
 // Units [0, split_from) are whole tiles; every tile from there on is two half units.
-__device__ __forceinline__ Unit decode(int u, int split_from, int tile_n, const PairTcParams &p) {
+__host__ __device__ __forceinline__ Unit decode(int u, int split_from, int tile_n, int tiles_m, const PairTcParams &p) {
     Unit t;
     const bool half = u >= split_from;
-    const int tile = half ? split_from + (u - split_from) / 2 : u;
+    int tile = half ? split_from + (u - split_from) / 2 : u;
+    const int weight = tiles_m * p.tiles_n;
+    const int which = tile >= weight ? 1 : 0;  // c has no tiles beyond these
+    tile -= which * weight;
+    t.dw = which;
     const int first_m = tile / (kGroupM * p.tiles_n) * kGroupM;
-    const int gm = min(kGroupM, p.tiles_m - first_m);
+    const int gm = kGroupM < tiles_m - first_m ? kGroupM : tiles_m - first_m;
     const int local = tile % (kGroupM * p.tiles_n);
     t.mb = first_m + local % gm;
     t.nb = local / gm;
@@ -69,6 +80,49 @@ __device__ __forceinline__ Unit decode(int u, int split_from, int tile_n, const 
     t.halves = !half ? 2 : (static_cast<int64_t>(t.nb) * tile_n + t.h * (tile_n / 2) < p.n ? 1 : 0);
     return t;
 }
+
+// The units of one pair, the same for all its warps.  Units of c (of the only output, where there is one) go round
+// the pairs; where the last round leaves some pairs without, those first take `early` units of the weights'
+// gradients each, and what is left of these goes round all pairs again, beginning with pair `behind`.
+template <int kMode>
+struct Walk {
+    const PairTcParams &p;
+    const int pair;
+    int i = 0;
+    __host__ __device__ __forceinline__ Walk(const PairTcParams &params, int own) : p(params), pair(own) {}
+    __host__ __device__ __forceinline__ bool next(Unit *t) {
+        for (;;) {
+            if (!any(t)) return false;
+            if (t->halves != 0) return true;
+        }
+    }
+
+  private:
+    __host__ __device__ __forceinline__ bool any(Unit *t) {
+        int j = i++;
+        const int u = pair + j * p.pairs;
+        if (u < p.c_units) {
+            *t = decode(u, p.c_split, Shape<kMode>::kTileN, p.tiles_m, p);
+            t->dw = -1;
+            return true;
+        }
+        if constexpr (kMode != kGrads) return false;
+        j -= p.c_units > pair ? (p.c_units - pair + p.pairs - 1) / p.pairs : 0;
+        const int over = p.c_units % p.pairs, without = p.pairs - over;
+        const int taken = p.early * without < p.dw_units ? p.early * without : p.dw_units;
+        int w;
+        if (pair >= over && j < p.early) {
+            w = pair - over + j * without;
+            if (w >= taken) return false;  // all are taken
+        } else {
+            if (pair >= over) j -= p.early;
+            w = taken + (pair - p.behind + p.pairs) % p.pairs + j * p.pairs;
+            if (w >= p.dw_units) return false;
+        }
+        *t = decode(w, p.dw_split, Shape<kMode>::kTileN, p.dw_tiles_m, p);
+        return true;
+    }
+};
 
 template <typename TC>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
@@ -165,7 +219,7 @@ template <typename TC, uint32_t kFmt, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
     constexpr int kTileN = Shape<kMode>::kTileN;
-    constexpr bool kBMN = kMode == kSum;  // B stored [k, n]
+    constexpr bool kBMN = kMode == kGrads;  // B stored [k, n]
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
@@ -204,7 +258,7 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
         tma_prefetch_desc(&maps.a[0]);
         tma_prefetch_desc(&maps.b[0]);
         if (kMode != kCodes) tma_prefetch_desc(&maps.b[1]);
-        if (kMode == kSum) tma_prefetch_desc(&maps.a[1]);
+        if (kMode == kGrads) tma_prefetch_desc(&maps.a[1]);
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_addr(tmem_slot), kTmemCols);
@@ -217,15 +271,12 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     grid_dep_begin();
-    const int blocks1 = (p.k + kBK - 1) / kBK;  // k-blocks of a source
-    const int kblocks = kMode == kSum ? 2 * blocks1 : blocks1;
-    const int chunk = kMode == kCodes ? kExactBlocks : kblocks;  // k-blocks that go into one accumulator
-    const int cl = static_cast<int>(blockIdx.x) >> 1;
-    const int ncl = static_cast<int>(gridDim.x) >> 1;
-    int tail = p.num_tiles > ncl ? p.num_tiles % ncl : (2 * p.num_tiles <= ncl ? p.num_tiles : 0);
-    if (2 * tail > ncl) tail = 0;
-    const int split_from = p.num_tiles - tail;
-    const int num_units = split_from + 2 * tail;
+    const int blocks1 = blocks_for(p.k);  // k-blocks of a source
+    // k-blocks of a unit, and how many go into one accumulator
+    auto blocks_of = [&](const Unit &t) {
+        return kMode != kGrads ? blocks1 : t.dw < 0 ? 2 * blocks1 : blocks_for(p.m);
+    };
+    const int pair = static_cast<int>(blockIdx.x) >> 1;
     // a timeout stops both CTAs of the pair
     const uint32_t peer_abort = mapa_shared(smem_addr(const_cast<int *>(abort_flag)), rank ^ 1u);
     auto raise_abort = [&]() {
@@ -240,9 +291,9 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int u = cl; u < num_units && ok; u += ncl) {
-                const Unit t = decode(u, split_from, kTileN, p);
-                if (t.halves == 0) continue;
+            Walk<kMode> walk(p, pair);
+            for (Unit t; ok && walk.next(&t);) {
+                const int kblocks = blocks_of(t);
                 const int arow = t.mb * 2 * kBM + static_cast<int>(rank) * kBM;
                 // a half unit uses the first 64 of the 128 B rows that each CTA loads
                 const int brow = kMode == kGated ? t.nb * kTileN + t.h * (kTileN / 2)
@@ -256,11 +307,18 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
                     if (leader) mbar_arrive_expect_tx(full_bar(stage), 2 * kStageBytes);
                     const uint32_t sa = s0 + stage * kStageBytes, sb = sa + kABytes;
                     const uint32_t fb = mapa_shared(full_bar(stage), 0);
-                    const bool second = kMode == kSum && kb >= blocks1;
+                    const bool outer = kMode == kGrads && t.dw >= 0;
+                    const bool second = kMode == kGrads && !outer && kb >= blocks1;
                     const int k0 = (second ? kb - blocks1 : kb) * kBK;
-                    tma_load_3d_pair(sa, second ? &maps.a[1] : &maps.a[0], fb, k0, arow, 0);
+                    if (outer) {
+                        const CUtensorMap *ma = t.dw == 1 ? &maps.dw_a[1] : &maps.dw_a[0];
+                        tma_load_3d_pair(sa, ma, fb, arow, k0, 0);
+                        tma_load_3d_pair(sa + kMNBox, ma, fb, arow + 64, k0, 0);
+                    } else {
+                        tma_load_3d_pair(sa, second ? &maps.a[1] : &maps.a[0], fb, k0, arow, 0);
+                    }
                     if (kBMN) {
-                        const CUtensorMap *mb = second ? &maps.b[1] : &maps.b[0];
+                        const CUtensorMap *mb = outer ? &maps.dw_b : second ? &maps.b[1] : &maps.b[0];
                         tma_load_3d_pair(sb, mb, fb, brow, k0, 0);
                         tma_load_3d_pair(sb + kMNBox, mb, fb, brow + 64, k0, 0);
                     } else {
@@ -285,15 +343,17 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
             // ---------------- pair MMA issuer (even CTA) ----------------
             constexpr uint32_t kIdesc = idesc_f16(kFmt, 2 * kBM, kBN, 0u, kBMN ? 1u : 0u);
             constexpr uint32_t kIdescHalf = idesc_f16(kFmt, 2 * kBM, kBN / 2, 0u, kBMN ? 1u : 0u);
+            constexpr uint32_t kAColumns = idesc_f16(kFmt, 2 * kBM, kBN, 1u) & ~idesc_f16(kFmt, 2 * kBM, kBN);  // A stored [k, m]
             int stage = 0;
             uint32_t phase = 0;
             uint32_t acc_phase[2] = {0u, 0u};
             bool ok = true;
             int local = 0;
-            for (int u = cl; u < num_units && ok; u += ncl) {
-                const Unit t = decode(u, split_from, kTileN, p);
-                if (t.halves == 0) continue;
-                const uint32_t idesc = t.halves == 2 ? kIdesc : kIdescHalf;
+            Walk<kMode> walk(p, pair);
+            for (Unit t; ok && walk.next(&t);) {
+                const int kblocks = blocks_of(t), chunk = kMode == kCodes ? kExactBlocks : kblocks;
+                const bool outer = kMode == kGrads && t.dw >= 0;
+                const uint32_t idesc = (t.halves == 2 ? kIdesc : kIdescHalf) | (outer ? kAColumns : 0u);
                 for (int c0 = 0; c0 < kblocks && ok; c0 += chunk) {
                     const int a = local++ & 1;
                     // both CTAs' epilogues have read what this accumulator held
@@ -313,7 +373,8 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
                         const uint32_t sa = s0 + stage * kStageBytes, sb = sa + kABytes;
 #pragma unroll
                         for (int kk = 0; kk < kBK / 16; ++kk) {
-                            const uint64_t da = sdesc_kmajor_sw128(sa + kk * 32);
+                            const uint64_t da = outer ? sdesc_mnmajor_sw128(sa + kk * 2048, kMNBox)
+                                                      : sdesc_kmajor_sw128(sa + kk * 32);
                             const uint64_t db = kBMN ? sdesc_mnmajor_sw128(sb + kk * 2048, kMNBox)
                                                      : sdesc_kmajor_sw128(sb + kk * 32);
                             umma_f16_ss_pair(d_tmem, da, db, idesc, kb != c0 || kk != 0 ? 1u : 0u);
@@ -342,9 +403,9 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
         bool ok = true;
         Writer<TC> out;
         out.base = s0 + kStages * kStageBytes + static_cast<uint32_t>(warp - 2) * kOutBytes;
-        for (int u = cl; u < num_units && ok; u += ncl) {
-            const Unit t = decode(u, split_from, kTileN, p);
-            if (t.halves == 0) continue;
+        Walk<kMode> walk(p, pair);
+        for (Unit t; ok && walk.next(&t);) {
+            const int kblocks = blocks_of(t), chunk = kMode == kCodes ? kExactBlocks : kblocks;
             const int64_t row0 = static_cast<int64_t>(t.mb) * 2 * kBM + static_cast<int64_t>(rank) * kBM + quarter * 32;
             const int width = t.halves * (kTileN / 2);  // outputs across this unit
             const int mine = width / 2;                 // and this warp's share of them
@@ -419,7 +480,12 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
                             tmem_ld_wait();
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
-                            out.write(v, &maps.out[0], p.c_tma, c, p.ldc, row0, col, p.m, p.n, lane);
+                            if (kMode == kGrads && t.dw >= 0)
+                                out.write(v, t.dw == 0 ? &maps.out[1] : &maps.out[2], p.dw_tma,
+                                          static_cast<TC *>(t.dw == 0 ? p.dw[0] : p.dw[1]), p.ld_dw, row0, col, p.k, p.n,
+                                          lane);
+                            else
+                                out.write(v, &maps.out[0], p.c_tma, c, p.ldc, row0, col, p.m, p.n, lane);
                         }
                     }
                 }
@@ -457,6 +523,70 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
     }
 }
 
+// Tiles of the last round become half units where that round would leave half of the pairs idle: of `tiles` on
+// `pairs`, as many as this.
+int last_tiles(int tiles, int pairs) {
+    const int last = tiles > pairs ? tiles % pairs : (2 * tiles <= pairs ? tiles : 0);
+    return 2 * last <= pairs ? last : 0;
+}
+
+// Sets the units and how Walk deals them out.  With both outputs: the division, of the few that there are, whose
+// busiest pair has the least to do, in k-blocks of `c_cost` and `dw_cost` a tile.
+void plan_units(PairTcParams *p, int c_tiles, int dw_tiles, int c_cost, int dw_cost) {
+    const int pairs = p->pairs;
+    auto units = [](int tiles, int halved, int32_t *count, int32_t *split) {
+        *split = tiles - halved;
+        *count = tiles + halved;
+    };
+    p->early = p->behind = 0;
+    units(c_tiles, dw_tiles == 0 ? last_tiles(c_tiles, pairs) : 0, &p->c_units, &p->c_split);
+    units(dw_tiles, c_tiles == 0 ? last_tiles(dw_tiles, pairs) : 0, &p->dw_units, &p->dw_split);
+    if (c_tiles == 0 || dw_tiles == 0) return;
+    constexpr double kHalf = 0.6;  // of a tile's time for half of it: A is read as often
+    double best = -1;
+    const PairTcParams whole = *p;
+    for (int halve = 0; halve < (last_tiles(c_tiles, pairs) > 0 ? 2 : 1); ++halve) {
+        PairTcParams q = whole;
+        units(c_tiles, halve ? last_tiles(c_tiles, pairs) : 0, &q.c_units, &q.c_split);
+        const int over = q.c_units % pairs, without = pairs - over, rounds = q.c_units / pairs;
+        const double last = halve ? kHalf * c_cost : c_cost;  // what the pairs before `over` have more
+        // whole rounds of c (halved tiles begin a round or are all there is)
+        const double base = halve && q.c_split == 0 && rounds > 0 ? kHalf * c_cost * rounds : 1.0 * c_cost * rounds;
+        for (int up = 0; up < (over > 0 ? 2 : 1); ++up) {
+            q.early = over > 0 ? static_cast<int>(last / dw_cost) + up : 0;
+            if (q.early > dw_tiles) q.early = dw_tiles;
+            const int taken = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(q.early) * without, dw_tiles));
+            const int rest = dw_tiles - taken;
+            const bool first_without = over > 0 && q.early * dw_cost < last;  // whose turn it is then
+            q.behind = first_without ? over : 0;
+            for (int h = 0; h < 2; ++h) {
+                const int halved = h ? last_tiles(rest, pairs) : 0;
+                if (h && halved == 0) break;
+                units(dw_tiles, halved, &q.dw_units, &q.dw_split);
+                const int left = rest + halved, every = left / pairs, more = left % pairs;
+                // units of the last round weigh `unit` each
+                const double unit = halved ? kHalf * dw_cost : dw_cost;
+                double most = 0;
+                for (int c = 0; c < pairs; ++c) {
+                    const bool without_one = c >= over;
+                    double load = base + (without_one ? 0 : last);
+                    if (without_one && q.early > 0) {
+                        const int own = c - over < taken ? (taken - 1 - (c - over)) / without + 1 : 0;
+                        load += static_cast<double>(own) * dw_cost;
+                    }
+                    load += static_cast<double>(every) * (halved && rest < pairs ? unit : dw_cost);
+                    if ((c - q.behind + pairs) % pairs < more) load += unit;
+                    most = std::max(most, load);
+                }
+                if (best < 0 || most < best) {
+                    best = most;
+                    *p = q;
+                }
+            }
+        }
+    }
+}
+
 template <typename TC, uint32_t kFmt, int kMode>
 cudaError_t pair_t(const PairTcMaps &maps, PairTcParams p, int num_sms, cudaStream_t s) {
     constexpr int kTileN = Shape<kMode>::kTileN;
@@ -470,14 +600,22 @@ cudaError_t pair_t(const PairTcMaps &maps, PairTcParams p, int num_sms, cudaStre
         if (e != cudaSuccess) return e;
         attr_set |= bit;
     }
-    const int64_t tm = (static_cast<int64_t>(p.m) + 2 * kBM - 1) / (2 * kBM), tn = (p.n + kTileN - 1) / kTileN;
-    if (tm * tn > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
-    p.tiles_m = static_cast<int32_t>(tm);
-    p.tiles_n = static_cast<int32_t>(tn);
-    p.num_tiles = static_cast<int32_t>(tm * tn);
     const int pairs = num_sms / 2;
-    const int clusters = 2 * p.num_tiles <= pairs ? 2 * p.num_tiles : (p.num_tiles < pairs ? p.num_tiles : pairs);
-    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    const int64_t tn = (static_cast<int64_t>(p.n) + kTileN - 1) / kTileN, tm = (static_cast<int64_t>(p.m) + 2 * kBM - 1) / (2 * kBM);
+    const int64_t wm = (static_cast<int64_t>(p.k) + 2 * kBM - 1) / (2 * kBM);
+    const int64_t c_tiles = kMode == kGrads && !p.need_c ? 0 : tm * tn;
+    const int64_t dw_tiles = kMode == kGrads && p.need_dw ? 2 * wm * tn : 0;
+    if (pairs < 1 || c_tiles + dw_tiles < 1 || c_tiles > INT32_MAX / 4 || dw_tiles > INT32_MAX / 4)
+        return cudaErrorInvalidConfiguration;
+    p.tiles_m = static_cast<int32_t>(tm);
+    p.dw_tiles_m = static_cast<int32_t>(wm);
+    p.tiles_n = static_cast<int32_t>(tn);
+    p.pairs = pairs;
+    plan_units(&p, static_cast<int>(c_tiles), static_cast<int>(dw_tiles), 2 * blocks_for(p.k),
+               blocks_for(p.m));
+    const int units = p.c_units + p.dw_units;
+    // the first pairs have all units where there are fewer of them than pairs
+    const int clusters = units < pairs && (p.c_units == 0 || p.dw_units == 0 || p.early > 0) ? units : pairs;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
@@ -501,8 +639,9 @@ cudaError_t launch_gated_tc(int dt, const PairTcMaps &maps, const PairTcParams &
     return dt == kF16 ? pair_t<__half, 0, kGated>(maps, p, num_sms, s)
                       : pair_t<__nv_bfloat16, 1, kGated>(maps, p, num_sms, s);
 }
-cudaError_t launch_sum_gemm_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s) {
-    return dt == kF16 ? pair_t<__half, 0, kSum>(maps, p, num_sms, s) : pair_t<__nv_bfloat16, 1, kSum>(maps, p, num_sms, s);
+cudaError_t launch_gated_products_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s) {
+    return dt == kF16 ? pair_t<__half, 0, kGrads>(maps, p, num_sms, s)
+                      : pair_t<__nv_bfloat16, 1, kGrads>(maps, p, num_sms, s);
 }
 cudaError_t launch_gemm_i8_tc(int dt, const PairTcMaps &maps, const PairTcParams &p, int num_sms, cudaStream_t s) {
     switch (dt) {
