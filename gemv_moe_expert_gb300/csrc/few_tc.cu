@@ -7,6 +7,8 @@
 //           tokens' codes become f16 in shared memory, or come as f16 from 64 tokens on.  Each 1024 of k has an
 //           accumulator of its own: sums of products of two codes are exact up to there (2^24), and the accumulators are
 //           added as integers at the end.
+//   sum     d_x = d_gate Wg + d_up Wu, the gradient of x: the weights' columns are the M side (128 a tile, in boxes of 64 x
+//           64), the contraction runs over the rows of Wg and then of Wu
 // Every weight byte is read once (per kN tokens), and the kernel is bound by that stream; two CTAs share an SM
 // where the ring allows, and the contraction is split over a thread-block cluster of up to eight CTAs where the tiles
 // are few.  Each CTA leaves its partial sums in its own (by then idle) ring, and after a cluster barrier every CTA adds
@@ -33,8 +35,11 @@ constexpr int kMaxSplit = 8;
 constexpr uint32_t kWBytes = kBM * 128;  // 128 rows of 128 bytes: 64 16-bit values or 128 codes
 constexpr int kChunk = 8;                // code blocks (of 128) whose sums stay exact: 1024 of k
 
-template <bool kCodes, int kN>
+enum Kind { kGated, kCodes8, kSum };
+
+template <int kKind, int kN>
 struct Ring {
+    static constexpr bool kCodes = kKind == kCodes8;
     static constexpr int kWarps = kCodes ? 8 : 4;  // behind the TMA and MMA warps
     static constexpr int kThreads = 64 + 32 * kWarps;
     static constexpr bool kHalfX = kCodes && kN >= 64;  // the tokens' codes come as f16
@@ -86,13 +91,13 @@ __device__ __forceinline__ void convert_tokens(uint32_t raw, uint32_t dst, int t
     }
 }
 
-template <typename TC, uint32_t kFmt, bool kCodes, int kN>
-__global__ void __launch_bounds__(Ring<kCodes, kN>::kThreads)
-few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
-              const __grid_constant__ CUtensorMap map_w1, const FewTcParams p) {
-    using R = Ring<kCodes, kN>;
+template <typename TC, uint32_t kFmt, int kKind, int kN>
+__global__ void __launch_bounds__(Ring<kKind, kN>::kThreads)
+few_tc_kernel(const __grid_constant__ FewTcMaps maps, const FewTcParams p) {
+    using R = Ring<kKind, kN>;
+    constexpr bool kCodes = R::kCodes;
     constexpr int kStages = R::kStages, kSlots = R::kSlots, kWarps = R::kWarps;
-    constexpr int kRows = kCodes ? kBM : kBM / 2;  // outputs across a tile
+    constexpr int kRows = kKind == kGated ? kBM / 2 : kBM;  // outputs across a tile
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
@@ -131,9 +136,10 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&map_x);
-        tma_prefetch_desc(&map_w0);
-        if (!kCodes) tma_prefetch_desc(&map_w1);
+        tma_prefetch_desc(&maps.x[0]);
+        tma_prefetch_desc(&maps.w[0]);
+        if (!kCodes) tma_prefetch_desc(&maps.w[1]);
+        if (kKind == kSum) tma_prefetch_desc(&maps.x[1]);
     }
     if (warp == 1) {
         tmem_alloc(smem_addr(tmem_slot), p.tmem_cols);
@@ -146,7 +152,8 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     grid_dep_begin();
     // this CTA's share of the k-blocks (128 bytes of a row each)
     constexpr int kBlock = kCodes ? 128 : 64;
-    const int kb_total = p.k / kBlock + (p.k % kBlock != 0);
+    const int blocks1 = p.k / kBlock + (p.k % kBlock != 0);  // of a source
+    const int kb_total = kKind == kSum ? 2 * blocks1 : blocks1;
     const int kb0 = static_cast<int>(static_cast<int64_t>(kb_total) * rank / ksplit);
     const int kblocks = static_cast<int>(static_cast<int64_t>(kb_total) * (rank + 1) / ksplit) - kb0;
 
@@ -169,12 +176,20 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     break;
                 }
                 const uint32_t sw = s0 + stage * R::kStageBytes;
-                const int k0 = (kb0 + kb) * kBlock;
+                const bool second = kKind == kSum && kb0 + kb >= blocks1;
+                const int k0 = (second ? kb0 + kb - blocks1 : kb0 + kb) * kBlock;
+                const CUtensorMap *const x = second ? &maps.x[1] : &maps.x[0];
                 mbar_arrive_expect_tx(full_bar(stage), R::kStageBytes);
-                tma_load_3d_hint(sw, &map_w0, full_bar(stage), k0, n0, 0, pol);
-                if (!kCodes) tma_load_3d_hint(sw + kWBytes / 2, &map_w1, full_bar(stage), k0, n0, 0, pol);
-                tma_load_3d(sw + kWBytes, &map_x, full_bar(stage), k0, t0, 0);
-                if (R::kHalfX) tma_load_3d(sw + kWBytes + R::kXBytes, &map_x, full_bar(stage), k0 + 64, t0, 0);
+                if constexpr (kKind == kSum) {
+                    const CUtensorMap *const w = second ? &maps.w[1] : &maps.w[0];
+                    tma_load_3d_hint(sw, w, full_bar(stage), n0, k0, 0, pol);
+                    tma_load_3d_hint(sw + kWBytes / 2, w, full_bar(stage), n0 + 64, k0, 0, pol);
+                } else {
+                    tma_load_3d_hint(sw, &maps.w[0], full_bar(stage), k0, n0, 0, pol);
+                    if (!kCodes) tma_load_3d_hint(sw + kWBytes / 2, &maps.w[1], full_bar(stage), k0, n0, 0, pol);
+                }
+                tma_load_3d(sw + kWBytes, x, full_bar(stage), k0, t0, 0);
+                if (R::kHalfX) tma_load_3d(sw + kWBytes + R::kXBytes, x, full_bar(stage), k0 + 64, t0, 0);
                 ++issued;
             }
             if (!ok) {
@@ -189,7 +204,7 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     } else if (warp == 1) {
         if (lane == 0) {
             // ---------------- MMA issuer ----------------
-            constexpr uint32_t kIdesc = idesc_f16(kFmt, kBM, kN);
+            constexpr uint32_t kIdesc = idesc_f16(kFmt, kBM, kN, kKind == kSum ? 1u : 0u);
             bool ok = true;
             for (int kb = 0; kb < kblocks; ++kb) {
                 const int stage = kb % kStages;
@@ -215,7 +230,9 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_f16_ss(acc_base, sdesc_kmajor_sw128(stage_at + kk * 32),
+                        umma_f16_ss(acc_base,
+                                    kKind == kSum ? sdesc_mnmajor_sw128(stage_at + kk * 2048, kWBytes / 2)
+                                                  : sdesc_kmajor_sw128(stage_at + kk * 32),
                                     sdesc_kmajor_sw128(stage_at + kWBytes + kk * 32), kIdesc, kb == 0 && kk == 0 ? 0u : 1u);
                     umma_commit(empty_bar(stage));
                 }
@@ -338,7 +355,7 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     for (int e = 0; e < kB; ++e) {
                         const int tk = min(tk0 + e * kDown * ksplit, tokens - 1);
                         g[e] += from[tk * kBM];
-                        if constexpr (!kCodes) u[e] += from[tk * kBM + 64];
+                        if constexpr (kKind == kGated) u[e] += from[tk * kBM + 64];
                     }
                 }
 #pragma unroll
@@ -350,6 +367,8 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     if constexpr (kCodes) {
                         const float sa = p.scale_a != nullptr ? __ldg(p.scale_a + i) : 1.f;
                         *out = Elem<TC>::from_f(static_cast<float>(g[e]) * sa * sb);
+                    } else if constexpr (kKind == kSum) {
+                        *out = Elem<TC>::from_f(g[e]);
                     } else {
                         *out = Elem<TC>::from_f(gate_act_16(p.act, g[e]) * u[e]);
                         if (p.saved[0] != nullptr) {
@@ -371,20 +390,20 @@ few_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     }
 }
 
-template <typename TC, uint32_t kFmt, bool kCodes, int kN>
+template <typename TC, uint32_t kFmt, int kKind, int kN>
 cudaError_t few_n(const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
-    using R = Ring<kCodes, kN>;
+    using R = Ring<kKind, kN>;
     static unsigned long long attr_set = 0;  // one bit per device
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(attr_set & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(few_tc_kernel<TC, kFmt, kCodes, kN>,
+        const cudaError_t e = cudaFuncSetAttribute(few_tc_kernel<TC, kFmt, kKind, kN>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmemBytes);
         if (e != cudaSuccess) return e;
         attr_set |= bit;
     }
-    const int rows = kCodes ? kBM : kBM / 2;
+    const int rows = kKind == kGated ? kBM / 2 : kBM;
     const int64_t blocks = (static_cast<int64_t>(p.n) + rows - 1) / rows * p.token_blocks * p.ksplit;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
@@ -400,17 +419,17 @@ cudaError_t few_n(const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, few_tc_kernel<TC, kFmt, kCodes, kN>, maps.x, maps.w[0], maps.w[1], p);
+    return cudaLaunchKernelEx(&cfg, few_tc_kernel<TC, kFmt, kKind, kN>, maps, p);
 }
 
-template <typename TC, uint32_t kFmt, bool kCodes>
+template <typename TC, uint32_t kFmt, int kKind>
 cudaError_t few_t(int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
     if (p.ksplit < 1 || p.ksplit > kMaxSplit) return cudaErrorInvalidValue;
     switch (tokens) {
-    case 16: return few_n<TC, kFmt, kCodes, 16>(maps, p, s);
-    case 32: return few_n<TC, kFmt, kCodes, 32>(maps, p, s);
-    case 64: return few_n<TC, kFmt, kCodes, 64>(maps, p, s);
-    case 128: return few_n<TC, kFmt, kCodes, 128>(maps, p, s);
+    case 16: return few_n<TC, kFmt, kKind, 16>(maps, p, s);
+    case 32: return few_n<TC, kFmt, kKind, 32>(maps, p, s);
+    case 64: return few_n<TC, kFmt, kKind, 64>(maps, p, s);
+    case 128: return few_n<TC, kFmt, kKind, 128>(maps, p, s);
     default: return cudaErrorInvalidValue;
     }
 }
@@ -418,6 +437,7 @@ cudaError_t few_t(int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaS
 }  // namespace
 
 int few_tc_rows(bool codes) { return codes ? kBM : kBM / 2; }
+int few_tc_block_k() { return 64; }
 
 namespace {
 int ctas_per_sm(bool codes, int tokens) { return codes && tokens == 128 ? 1 : 2; }
@@ -428,9 +448,10 @@ int64_t code_blocks(int tokens) { return ((ctas_per_sm(true, tokens) == 1 ? 512 
 struct Split {
     int64_t ctas, split;
 };
-Split split_for(bool codes, int tokens, int64_t m, int64_t n, int64_t k, int num_sms) {
-    const int64_t rows = few_tc_rows(codes), tiles = (n + rows - 1) / rows * ((m + tokens - 1) / tokens);
-    const int64_t kb = codes ? (k + 127) / 128 : (k + 63) / 64;
+Split split_for(int kind, int tokens, int64_t m, int64_t n, int64_t k, int num_sms) {
+    const bool codes = kind == kCodes8;
+    const int64_t rows = few_tc_rows(kind != kGated), tiles = (n + rows - 1) / rows * ((m + tokens - 1) / tokens);
+    const int64_t kb = codes ? (k + 127) / 128 : (k + 63) / 64 * (kind == kSum ? 2 : 1);
     int64_t split = 1;
     // as many CTAs as the SMs hold at once (a cluster lies within a group of 16 to 20 SMs, so that an eighth of
     // the places may not be used), each with a few blocks of its own (1408 x 2048 bf16, 16 tokens: 9.0, 7.1 and
@@ -457,12 +478,12 @@ bool few_tc_half_tokens(int64_t m) { return m > 32; }
 // The tokens of a tile; sets the CTAs that share its contraction and the columns of tensor memory.
 int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p) {
     int tokens = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 || codes ? 64 : 128;
-    Split s = split_for(codes, tokens, m, n, k, num_sms);
+    Split s = split_for(codes ? kCodes8 : kGated, tokens, m, n, k, num_sms);
     if (codes && m > 64) {
         // Tiles of 128 tokens read the weights once, but have an SM to themselves: taken where they fill the SMs once
         // (128 tokens: 4096 x 11008 26.5 us against 38 with 64 a tile, 11008 x 4096 42.7 against 37.7), or where 64 leave
         // no room for the accumulators.
-        const Split wide = split_for(codes, 128, m, n, k, num_sms);
+        const Split wide = split_for(kCodes8, 128, m, n, k, num_sms);
         const int64_t kb = (k + 127) / 128;
         if ((m <= 128 && wide.ctas <= num_sms && 4 * wide.ctas >= 3LL * num_sms) || kb > s.split * code_blocks(64)) {
             tokens = 128;
@@ -478,14 +499,38 @@ int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcP
     return tokens;
 }
 
+// The gradient of x, m tokens of k columns from n rows of both weights, in a launch of its own.  In the other way,
+// 256 x 256 tiles among those of the weights' gradients (pair_tc.cu), one tile runs through the whole contraction: taken
+// here where that chain of k-blocks (0.6 of them for half tiles) is by half longer than all work over all pairs, and long
+// enough to be worth a launch.  bf16, here and there: 1 token, 5504 x 2048 31 and 66 us; 16, 1408 x 2048 17 and 19; 256,
+// 5504 x 2048 48 and 59; 1024, 11008 x 704 90 and 124; but 16, 704 x 512 13 and 12, 128, 1408 x 2048 24 and 19.
+bool few_tc_takes_sum(int64_t m, int64_t n, int64_t k, bool need_w, int num_sms) {
+    const int64_t chain = 2 * ((n + 63) / 64), across = (k + 255) / 256, tiles = (m + 255) / 256 * across;
+    const int64_t pairs = num_sms / 2;
+    if (chain < (m <= 64 ? 40 : 100)) return false;
+    const int64_t work = tiles * chain + (need_w ? 2 * ((n + 255) / 256) * across * ((m + 63) / 64) : 0);
+    return (2 * tiles <= pairs ? 0.6 : 1.0) * static_cast<double>(chain) * static_cast<double>(pairs) >=
+           1.5 * static_cast<double>(work);
+}
+int few_tc_plan_sum(int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p) {
+    const int tokens = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+    p->token_blocks = static_cast<int32_t>((m + tokens - 1) / tokens);
+    p->ksplit = static_cast<int32_t>(split_for(kSum, tokens, m, k, n, num_sms).split);
+    p->tmem_cols = tokens < 32 ? 32 : tokens;
+    return tokens;
+}
+
 cudaError_t launch_gated_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
-    return dt == kF16 ? few_t<__half, 0, false>(tokens, maps, p, s) : few_t<__nv_bfloat16, 1, false>(tokens, maps, p, s);
+    return dt == kF16 ? few_t<__half, 0, kGated>(tokens, maps, p, s) : few_t<__nv_bfloat16, 1, kGated>(tokens, maps, p, s);
+}
+cudaError_t launch_sum_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
+    return dt == kF16 ? few_t<__half, 0, kSum>(tokens, maps, p, s) : few_t<__nv_bfloat16, 1, kSum>(tokens, maps, p, s);
 }
 cudaError_t launch_gemm_i8_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
     switch (dt) {
-    case kF32: return few_t<float, 0, true>(tokens, maps, p, s);
-    case kF16: return few_t<__half, 0, true>(tokens, maps, p, s);
-    case kBF16: return few_t<__nv_bfloat16, 0, true>(tokens, maps, p, s);
+    case kF32: return few_t<float, 0, kCodes8>(tokens, maps, p, s);
+    case kF16: return few_t<__half, 0, kCodes8>(tokens, maps, p, s);
+    case kBF16: return few_t<__nv_bfloat16, 0, kCodes8>(tokens, maps, p, s);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -202,7 +202,7 @@ gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n,
             few_params(&fp, h, ldh, m, n, k);
             tokens = static_cast<uint32_t>(few_tc_plan(false, m, n, k, device_sm_count(), &fp));
             const uint32_t rows = static_cast<uint32_t>(few_tc_rows(false));
-            ok = fp.err != nullptr && encode_matrix16(&few_maps.x, dt, lx.p(), k, m, lx.ld, tokens) &&
+            ok = fp.err != nullptr && encode_matrix16(&few_maps.x[0], dt, lx.p(), k, m, lx.ld, tokens) &&
                  encode_matrix16(&few_maps.w[0], dt, lw[0].p(), k, n, lw[0].ld, rows) &&
                  encode_matrix16(&few_maps.w[1], dt, lw[1].p(), k, n, lw[1].ld, rows);
             fp.saved[0] = gate;
@@ -349,15 +349,26 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     void *const dw[2] = {d_w_gate, d_w_up};
     PairTcMaps maps{};
     PairTcParams q{};
+    FewTcMaps few_maps{};
+    FewTcParams fp{};
+    const bool few = dt != GBMM_F32 && need_x && few_tc_takes_sum(m, n, k, need_w, device_sm_count());
+    int tokens = 0;
     if (dt != GBMM_F32) {
         const uint32_t rows = static_cast<uint32_t>(pair_tc_rows()), box = static_cast<uint32_t>(pair_tc_block_k());
         bool ok = pair_params(&q, &maps, dt, d_x, ld_dx, m, k, n);
-        q.need_c = need_x;
+        if (few) {
+            few_params(&fp, d_x, ld_dx, m, k, n);
+            tokens = few_tc_plan_sum(m, n, k, device_sm_count(), &fp);
+        }
+        q.need_c = need_x && !few;
         q.need_dw = need_w;
         q.ld_dw = ld_dw;
         q.dw_tma = 1;
         for (int i = 0; i < 2 && ok; ++i) {
-            if (need_x)
+            if (few)
+                ok = encode_matrix16(&few_maps.x[i], dt, g.d[i], n, m, ldd, static_cast<uint32_t>(tokens)) &&
+                     encode_matrix16(&few_maps.w[i], dt, lw[i].p(), k, n, lw[i].ld, static_cast<uint32_t>(few_tc_block_k()));
+            else if (need_x)
                 ok = encode_matrix16(&maps.a[i], dt, g.d[i], n, m, ldd, rows) &&
                      encode_matrix16(&maps.b[i], dt, lw[i].p(), k, n, lw[i].ld, box);
             if (need_w && ok) {
@@ -381,6 +392,8 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
         for (; st == GBMM_OK && launches > 1; --launches) st = finish_launch(cudaSuccess, fn, s);
         return st;
     }
+    if (few) st = finish_launch(launch_sum_few(dt, tokens, few_maps, fp, s), fn, s);
+    if (st != GBMM_OK || (few && !need_w)) return st;
     return finish_launch(launch_gated_products_tc(dt, maps, q, device_sm_count(), s), fn, s);
 }
 
@@ -479,8 +492,8 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
         fp.scale_b = scale_b;
         tokens = static_cast<uint32_t>(few_tc_plan(true, m, n, k, device_sm_count(), &fp));
         ok = fp.err != nullptr && encode_matrix8(&few.w[0], b2, k, n, ldb2, static_cast<uint32_t>(few_tc_rows(true))) &&
-             (plan.a_size == 2 ? encode_matrix16(&few.x, GBMM_F16, a2, k, m, lda2, tokens)
-                               : encode_matrix8(&few.x, a2, k, m, lda2, tokens));
+             (plan.a_size == 2 ? encode_matrix16(&few.x[0], GBMM_F16, a2, k, m, lda2, tokens)
+                               : encode_matrix8(&few.x[0], a2, k, m, lda2, tokens));
         few.w[1] = few.w[0];
     } else {
         const uint32_t rows = static_cast<uint32_t>(pair_tc_rows());

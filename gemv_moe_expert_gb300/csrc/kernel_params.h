@@ -265,7 +265,7 @@ struct FewTcParams {
     uint64_t wait_limit_ns;
 };
 struct FewTcMaps {
-    CUtensorMap x, w[2];  // boxes of 128 bytes x tokens, and x few_tc_rows() rows
+    CUtensorMap x[2], w[2];  // boxes of 128 bytes x tokens, and x few_tc_rows() (sum: 64) rows; x[1]: only sum
 };
 
 // ---- launchers (each returns the launch's cudaError_t) --------------------
@@ -353,6 +353,10 @@ int few_tc_rows(bool codes);
 bool few_tc_takes(bool codes, int64_t m, int64_t n, int64_t k);
 bool few_tc_half_tokens(int64_t m);
 int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p);
+int few_tc_block_k();
+bool few_tc_takes_sum(int64_t m, int64_t n, int64_t k, bool need_w, int num_sms);
+int few_tc_plan_sum(int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p);
+cudaError_t launch_sum_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s);
 cudaError_t launch_gated_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s);
 cudaError_t launch_gemm_i8_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s);
 cudaError_t launch_quantize_i8(int dt, const QuantizeParams &p, cudaStream_t s);

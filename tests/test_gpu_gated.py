@@ -283,6 +283,23 @@ def test_backward_many_tiles(dtype, m, n, k):
     b.check_backward("silu", b.backward("silu"))
 
 
+@pytest.mark.parametrize("d_w", [True, False])
+@pytest.mark.parametrize("m,n,k,pad", [(1, 1290, 72, 0), (16, 1300, 264, 3), (20, 1285, 128, 3), (64, 1290, 70, 2),
+                                       (70, 3205, 133, 3), (130, 3300, 136, 0), (300, 3208, 640, 8)])
+def test_backward_over_many_rows_of_weights(m, n, k, pad, d_w):
+    """Few tokens and columns, a long contraction for d_x."""
+    b = Block("bf16" if m % 4 else "f16", m, n, k, pad=pad)
+    b.check_backward("gelu", b.backward("gelu", True, d_w))
+
+
+@pytest.mark.parametrize("d_x,d_w", [(True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("m,n,k", [(2570, 300, 2100), (520, 2600, 1300), (1300, 1290, 1290)])
+def test_backward_tiles_of_both_products(m, n, k, d_x, d_w):
+    """More tiles than pairs of CTAs, and rounds that end between."""
+    b = Block("bf16", m, n, k)
+    b.check_backward("relu", b.backward("relu", d_x, d_w))
+
+
 # A product just under half a step of f32 beyond 1: added one after the other, every one that is added to 8192 or more
 # is rounded down, and 16384 of them end 2e-4 too low.
 LOST = float(np.float32(1 + 2.0 ** -11 - 2.0 ** -22))
