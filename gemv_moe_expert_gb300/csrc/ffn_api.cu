@@ -59,10 +59,18 @@ Laid lay(const void *p, int64_t rows, int64_t cols, int64_t ld, void *scratch, P
     l.to = Parts::base(scratch) + parts->add(rows, l.ld, 2);
     return l;
 }
-gbmm_status lay_again(const char *fn, const Laid &l, cudaStream_t s) {
-    if (l.to == nullptr) return GBMM_OK;
-    const RepackParams r{l.from, l.to, l.rows, l.cols, l.from_ld, l.ld, 2};
-    return finish_launch(launch_repack16(r, s), fn, s);
+// x and both weights, of the same columns, in one launch.
+gbmm_status lay_again(const char *fn, const Laid &x, const Laid (&w)[2], cudaStream_t s) {
+    const Laid *const all[3] = {&x, &w[0], &w[1]};
+    RepackParams r[3];
+    bool any = false;
+    for (int i = 0; i < 3; ++i) {
+        const Laid &l = *all[i];
+        const bool laid = l.to != nullptr;
+        r[i] = {l.from, l.to, laid ? l.rows : 0, l.cols, l.from_ld, round_up(l.cols, 8), 2};
+        any = any || (laid && l.rows > 0);
+    }
+    return any ? finish_launch(launch_repack16(r, s), fn, s) : GBMM_OK;
 }
 
 // what the tensor-core products share
@@ -223,8 +231,7 @@ gbmm_status gbmm_gated(gbmm_dtype dt, uint32_t activation, int64_t m, int64_t n,
             q.act = static_cast<int32_t>(activation);
         }
         if (!ok) return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
-        st = lay_again(fn, lx, s);
-        for (int i = 0; i < 2 && st == GBMM_OK; ++i) st = lay_again(fn, lw[i], s);
+        st = lay_again(fn, lx, lw, s);
         if (st != GBMM_OK) return st;
         return finish_launch(few ? launch_gated_few(dt, static_cast<int>(tokens), few_maps, fp, s)
                                  : launch_gated_tc(dt, maps, q, device_sm_count(), s),
@@ -380,8 +387,7 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
         }
         if (!ok) return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
     }
-    st = lay_again(fn, lx, s);
-    for (int i = 0; i < 2 && st == GBMM_OK; ++i) st = lay_again(fn, lw[i], s);
+    st = lay_again(fn, lx, lw, s);
     if (st == GBMM_OK) st = finish_launch(launch_gated_grad(dt, g, s), fn, s);
     if (st != GBMM_OK) return st;
     if (dt == GBMM_F32) {

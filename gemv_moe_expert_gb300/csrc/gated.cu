@@ -734,14 +734,18 @@ cudaError_t gated_grad_t(const GatedGradParams &p, cudaStream_t s) {
 // 16-bit rows that TMA cannot read, written again into rows that it can
 // ---------------------------------------------------------------------------
 
-// a warp takes 512 values of a row at a time
-__global__ void __launch_bounds__(256) repack16_kernel(const RepackParams p, int64_t parts) {
+// a warp takes 512 values of a row at a time, of up to three matrices of as many columns
+__global__ void __launch_bounds__(256)
+repack16_kernel(const RepackParams first, const RepackParams second, const RepackParams third, int64_t parts) {
     constexpr int kU = 8;
     grid_dep_begin();
     const int lane = threadIdx.x & 31;
-    const int64_t items = p.rows * parts, warps = static_cast<int64_t>(gridDim.x) * 8;
+    const int64_t items = (first.rows + second.rows + third.rows) * parts, warps = static_cast<int64_t>(gridDim.x) * 8;
     for (int64_t at = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; at < items; at += warps) {
-        const int64_t i = at / parts, o0 = (at - i * parts) * (32 * kU);  // words of two values
+        const int64_t row = at / parts, o0 = (at - row * parts) * (32 * kU);  // words of two values
+        const bool in_first = row < first.rows, in_second = row < first.rows + second.rows;
+        const RepackParams &p = in_first ? first : in_second ? second : third;
+        const int64_t i = in_first ? row : in_second ? row - first.rows : row - first.rows - second.rows;
         const uint8_t *src = static_cast<const uint8_t *>(p.src) + 2 * i * p.lds;
         uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.dst) + i * p.ldd);
         uint32_t v[kU];
@@ -823,10 +827,13 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
                               s, tws, o);
 }
 
-cudaError_t launch_repack16(const RepackParams &p, cudaStream_t s) {
-    const int64_t parts = (p.ldd + 511) / 512, blocks = (p.rows * parts + 7) / 8, most = 32LL * device_sm_count();
+// ldd and cols the same in all three; rows 0: nothing to do
+cudaError_t launch_repack16(const RepackParams (&p)[3], cudaStream_t s) {
+    const int64_t parts = (p[0].ldd + 511) / 512, most = 32LL * device_sm_count();
+    const int64_t blocks = ((p[0].rows + p[1].rows + p[2].rows) * parts + 7) / 8;
     if (blocks == 0) return cudaSuccess;
-    return launch_early(repack16_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, p, parts);
+    return launch_early(repack16_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, p[0],
+                        p[1], p[2], parts);
 }
 
 }  // namespace gbmm
