@@ -243,7 +243,7 @@ struct TileArgs {
     int32_t a_vec, b_vec;  // groups of four elements can be read in one access
     int64_t tiles_n;
     uint32_t parts = 1;    // CTAs that share a tile
-    int32_t fold = 0;      // a long contraction: the sums of kFold steps each are added up in shared memory
+    int32_t fold = 0;      // 1: a long contraction, the sums of kFold steps each are added up in shared memory
 };
 
 constexpr int kTK = 16;
@@ -614,7 +614,7 @@ cudaError_t launch_whole(void (*kernel)(Params...), unsigned blocks, unsigned cl
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// whether a contraction of k (of `sources`, divided over `parts`) is long: from one and a half runs
+// 1 where a contraction of k (of `sources`, divided over `parts`) is long: from one and a half runs
 int32_t folds(int64_t k, int sources, int64_t parts) {
     return (k + kTK - 1) / kTK * sources / parts > kFold * 3 / 2;
 }
@@ -648,6 +648,7 @@ cudaError_t gated_simt_t(const GatedParams &p, cudaStream_t s) {
     const unsigned small = tile_grid(p.m, p.n, 64, 64, &t), large = tile_grid(p.m, p.n, 128, 64, &t);
     if (large == 0) return cudaErrorInvalidConfiguration;
     const unsigned sms = static_cast<unsigned>(device_sm_count());
+    constexpr uint32_t kSmall = TileProduct<T, kGated, 4, 4>::kFoldBytes, kLarge = TileProduct<T, kGated, 8, 4>::kFoldBytes;
     // At most one tile an SM: up to eight CTAs share a tile, as many as make the busiest SM's share smallest.
     // 512 x 1408 x 2048, 88 tiles: 206 us whole, 195 by two, 177 by three.
     if (large <= sms) {
@@ -658,17 +659,13 @@ cudaError_t gated_simt_t(const GatedParams &p, cudaStream_t s) {
             if (((tiles * q + sms - 1) / sms) * parts < ((tiles * parts + sms - 1) / sms) * q) parts = q;
         t.parts = parts;
         t.fold = folds(p.k, 1, parts);
-        return few ? launch_whole(gated_simt_kernel<T, 4, 4, true>, parts * tiles, parts,
-                                  t.fold ? TileProduct<T, kGated, 4, 4>::kFoldBytes : 0, s, t, p)
-                   : launch_whole(gated_simt_kernel<T, 8, 4, true>, parts * tiles, parts,
-                                  t.fold ? TileProduct<T, kGated, 8, 4>::kFoldBytes : 0, s, t, p);
+        return few ? launch_whole(gated_simt_kernel<T, 4, 4, true>, parts * tiles, parts, t.fold * kSmall, s, t, p)
+                   : launch_whole(gated_simt_kernel<T, 8, 4, true>, parts * tiles, parts, t.fold * kLarge, s, t, p);
     }
     t.fold = folds(p.k, 1, 1);
     if (large_tiles(large, small, 12))
-        return launch_whole(gated_simt_kernel<T, 8, 4, false>, large, 1, t.fold ? TileProduct<T, kGated, 8, 4>::kFoldBytes : 0,
-                            s, t, p);
-    return launch_whole(gated_simt_kernel<T, 4, 4, false>, small, 1, t.fold ? TileProduct<T, kGated, 4, 4>::kFoldBytes : 0, s,
-                        t, p);
+        return launch_whole(gated_simt_kernel<T, 8, 4, false>, large, 1, t.fold * kLarge, s, t, p);
+    return launch_whole(gated_simt_kernel<T, 4, 4, false>, small, 1, t.fold * kSmall, s, t, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -772,6 +769,10 @@ cudaError_t launch_gated_grad(int dt, const GatedGradParams &p, cudaStream_t s) 
 
 // The gradients of f32 blocks: x null or w null where one of them is not asked for.
 cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, int *launches, cudaStream_t s) {
+    constexpr uint32_t kLargeX = TileProduct<float, kSum, 8, 8>::kFoldBytes;
+    constexpr uint32_t kSmallX = TileProduct<float, kSum, 4, 4>::kFoldBytes;
+    constexpr uint32_t kLargeW = TileProduct<float, kOuter, 8, 4>::kFoldBytes;
+    constexpr uint32_t kSmallW = TileProduct<float, kOuter, 4, 4>::kFoldBytes;
     TileArgs tx{}, txs{}, tw{}, tws{};
     unsigned x_small = 0, x_large = 0, w_small = 0, w_large = 0;
     OuterOut o{};
@@ -804,27 +805,22 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
     *launches = 1;
     if (x != nullptr && w != nullptr && together >= static_cast<uint64_t>(device_sm_count()) && together <= INT32_MAX) {
         tx.fold = folds(x->k, 2, 2);
-        const uint32_t bytes = tx.fold || tw.fold ? TileProduct<float, kSum, 8, 8>::kFoldBytes : 0;
-        static_assert(TileProduct<float, kSum, 8, 8>::kFoldBytes == TileProduct<float, kOuter, 8, 4>::kFoldBytes, "both");
-        return launch_whole(both_gemm_simt_kernel, static_cast<unsigned>(together), 2, bytes, s, tx, c, x->ldc, 2 * x_large,
-                            tw, o, w_large);
+        static_assert(kLargeX == kLargeW, "one launch for both");
+        return launch_whole(both_gemm_simt_kernel, static_cast<unsigned>(together), 2, (tx.fold | tw.fold) * kLargeX, s, tx, c,
+                            x->ldc, 2 * x_large, tw, o, w_large);
     }
     if (x != nullptr) {
         tx.fold = txs.fold;
         const cudaError_t e =
             large_tiles(x_large, x_small, 8)
-                ? launch_whole(sum_gemm_simt_kernel<8, 8>, x_large, 1, tx.fold ? TileProduct<float, kSum, 8, 8>::kFoldBytes : 0,
-                               s, tx, c, x->ldc)
-                : launch_whole(sum_gemm_simt_kernel<4, 4>, x_small, 1, tx.fold ? TileProduct<float, kSum, 4, 4>::kFoldBytes : 0,
-                               s, txs, c, x->ldc);
+                ? launch_whole(sum_gemm_simt_kernel<8, 8>, x_large, 1, tx.fold * kLargeX, s, tx, c, x->ldc)
+                : launch_whole(sum_gemm_simt_kernel<4, 4>, x_small, 1, tx.fold * kSmallX, s, txs, c, x->ldc);
         if (e != cudaSuccess || w == nullptr) return e;
         *launches = 2;
     }
     return large_tiles(w_large, w_small, 12)
-               ? launch_whole(outer_gemm_simt_kernel<8, 4>, w_large, 1, tw.fold ? TileProduct<float, kOuter, 8, 4>::kFoldBytes : 0,
-                              s, tw, o)
-               : launch_whole(outer_gemm_simt_kernel<4, 4>, w_small, 1, tw.fold ? TileProduct<float, kOuter, 4, 4>::kFoldBytes : 0,
-                              s, tws, o);
+               ? launch_whole(outer_gemm_simt_kernel<8, 4>, w_large, 1, tw.fold * kLargeW, s, tw, o)
+               : launch_whole(outer_gemm_simt_kernel<4, 4>, w_small, 1, tw.fold * kSmallW, s, tws, o);
 }
 
 // ldd and cols the same in all three; rows 0: nothing to do

@@ -212,7 +212,7 @@ cudaError_t quantize_t(const QuantizeParams &p, cudaStream_t s) {
     if (pieces <= 1024) return quantize_p<T, 256, 4>(p, s);
     if (pieces <= 1536) return quantize_p<T, 256, 6>(p, s);
     if (pieces <= 2048) return quantize_p<T, 256, 8>(p, s);
-    if (pieces <= 3072) return quantize_p<T, 512, 6>(p, s);
+    if (pieces <= 3584) return quantize_p<T, 512, 7>(p, s);
     if (pieces <= 4096) return quantize_p<T, 512, 8>(p, s);
     if (pieces <= 8192) return quantize_p<T, 1024, 8>(p, s);
     return quantize_p<T, 1024, 0>(p, s);
