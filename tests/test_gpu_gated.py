@@ -433,7 +433,7 @@ def step(dtype, m, n, k, t, stream=None):
 
 
 STEPS = [("f32", 20, 72, 136), ("f16", 12, 264, 520), ("bf16", 100, 200, 320), ("bf16", 600, 1032, 520),
-         ("f16", 130, 77, 33)]
+         ("f16", 130, 77, 33), ("bf16", 40, 1400, 264), ("f16", 7, 3001, 133), ("f32", 2000, 72, 136)]
 
 
 @pytest.mark.parametrize("dtype,m,n,k", STEPS)
@@ -465,7 +465,7 @@ def test_steps_replay_from_a_graph(dtype, m, n, k):
 
 
 def test_two_streams_at_once():
-    cases = [("bf16", 600, 1032, 520), ("f16", 12, 264, 520)]
+    cases = [("bf16", 600, 1032, 520), ("f16", 12, 264, 520), ("bf16", 40, 1400, 264), ("f32", 2000, 72, 136)]
     sets = [make(*c, seed) for seed, c in enumerate(cases)]
     want = [step(*c, t) for c, t in zip(cases, sets)]
     torch.cuda.synchronize()
