@@ -503,11 +503,12 @@ int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcP
 // 256 x 256 tiles among those of the weights' gradients (pair_tc.cu), one tile runs through the whole contraction: taken
 // here where that chain of k-blocks (0.6 of them for half tiles) is by half longer than all work over all pairs, and long
 // enough to be worth a launch.  bf16, here and there: 1 token, 5504 x 2048 31 and 66 us; 16, 1408 x 2048 17 and 19; 256,
-// 5504 x 2048 48 and 59; 1024, 11008 x 704 90 and 124; but 16, 704 x 512 13 and 12, 128, 1408 x 2048 24 and 19.
+// 5504 x 2048 48 and 59; 1024, 11008 x 704 90 and 124; but 16, 704 x 512 13 and 12, 128, 1408 x 2048 24 and 19.  Where the
+// weights' gradients are not in that grid any chain will do (4 tokens, 704 x 512 9.0 and 12.7; 1, 200 x 200 6.6 and 8.1).
 bool few_tc_takes_sum(int64_t m, int64_t n, int64_t k, bool need_w, int num_sms) {
     const int64_t chain = 2 * ((n + 63) / 64), across = (k + 255) / 256, tiles = (m + 255) / 256 * across;
     const int64_t pairs = num_sms / 2;
-    if (chain < (m <= 64 ? 40 : 100)) return false;
+    if (chain < (m > 64 ? 100 : need_w ? 40 : 0)) return false;
     const int64_t work = tiles * chain + (need_w ? 2 * ((n + 255) / 256) * across * ((m + 63) / 64) : 0);
     return (2 * tiles <= pairs ? 0.6 : 1.0) * static_cast<double>(chain) * static_cast<double>(pairs) >=
            1.5 * static_cast<double>(work);

@@ -300,6 +300,8 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
         (need_w && !span(n, k, ld_dw, size, &dwb)))
         return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: operand extent overflows", fn);
     const bool empty = m == 0 || n == 0;  // what is left to do is writing zeros
+    // the weights' gradients of few tokens take no tiles (gated.cu)
+    const bool outer_few = dt != GBMM_F32 && need_w && m <= gated_few_tokens();
     if (empty || !need_w) xb = 0;
     if (empty || !need_x) wb = 0;
     Parts parts;
@@ -307,7 +309,7 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     const uint64_t d_at[2] = {parts.add(m, ldd, static_cast<int>(size)), parts.add(m, ldd, static_cast<int>(size))};
     Laid lx{x, nullptr, m, k, ldx, ldx}, lw[2] = {{w_gate, nullptr, n, k, ldw, ldw}, {w_up, nullptr, n, k, ldw, ldw}};
     if (dt != GBMM_F32 && !empty) {
-        if (need_w) lx = lay(x, m, k, ldx, scratch, &parts);
+        if (need_w && !outer_few) lx = lay(x, m, k, ldx, scratch, &parts);
         if (need_x) {
             lw[0] = lay(w_gate, n, k, ldw, scratch, &parts);
             lw[1] = lay(w_up, n, k, ldw, scratch, &parts);
@@ -358,7 +360,7 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     PairTcParams q{};
     FewTcMaps few_maps{};
     FewTcParams fp{};
-    const bool few = dt != GBMM_F32 && need_x && few_tc_takes_sum(m, n, k, need_w, device_sm_count());
+    const bool few = dt != GBMM_F32 && need_x && few_tc_takes_sum(m, n, k, need_w && !outer_few, device_sm_count());
     int tokens = 0;
     if (dt != GBMM_F32) {
         const uint32_t rows = static_cast<uint32_t>(pair_tc_rows()), box = static_cast<uint32_t>(pair_tc_block_k());
@@ -368,7 +370,7 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
             tokens = few_tc_plan_sum(m, n, k, device_sm_count(), &fp);
         }
         q.need_c = need_x && !few;
-        q.need_dw = need_w;
+        q.need_dw = need_w && !outer_few;
         q.ld_dw = ld_dw;
         q.dw_tma = 1;
         for (int i = 0; i < 2 && ok; ++i) {
@@ -378,7 +380,7 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
             else if (need_x)
                 ok = encode_matrix16(&maps.a[i], dt, g.d[i], n, m, ldd, rows) &&
                      encode_matrix16(&maps.b[i], dt, lw[i].p(), k, n, lw[i].ld, box);
-            if (need_w && ok) {
+            if (q.need_dw && ok) {
                 ok = encode_matrix16(&maps.dw_a[i], dt, g.d[i], n, m, ldd, box) &&
                      encode_matrix16(&maps.dw_b, dt, lx.p(), k, m, lx.ld, box);
                 q.dw[i] = dw[i];
@@ -388,7 +390,14 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
         if (!ok) return fail(GBMM_ERR_CUDA, "%s: tensor maps or the device error word are unavailable", fn);
     }
     st = lay_again(fn, lx, lw, s);
-    if (st == GBMM_OK) st = finish_launch(launch_gated_grad(dt, g, s), fn, s);
+    if (st != GBMM_OK) return st;
+    if (outer_few) {
+        if (!need_x) g.d[0] = g.d[1] = nullptr;
+        const OuterGemmParams pw{x, {nullptr, nullptr}, {dw[0], dw[1]}, m, n, k, ldx, ldd, ld_dw};
+        st = finish_launch(launch_gated_outer_few(dt, g, pw, s), fn, s);
+    } else {
+        st = finish_launch(launch_gated_grad(dt, g, s), fn, s);
+    }
     if (st != GBMM_OK) return st;
     if (dt == GBMM_F32) {
         const SumGemmParams px{{g.d[0], g.d[1]}, {w_gate, w_up}, d_x, m, k, n, ldd, ldw, ld_dx};
@@ -399,7 +408,7 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
         return st;
     }
     if (few) st = finish_launch(launch_sum_few(dt, tokens, few_maps, fp, s), fn, s);
-    if (st != GBMM_OK || (few && !need_w)) return st;
+    if (st != GBMM_OK || !(q.need_c || q.need_dw)) return st;
     return finish_launch(launch_gated_products_tc(dt, maps, q, device_sm_count(), s), fn, s);
 }
 

@@ -669,7 +669,9 @@ cudaError_t gated_simt_t(const GatedParams &p, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// d_gate = d_h * up * act'(gate), d_up = d_h * act(gate): one pass, 16 bytes an access
+// d_gate = d_h * up * act'(gate), d_up = d_h * act(gate): one pass, 16 bytes an access; bound by HBM (4096 x 5504 bf16:
+// 225 MB in 40 us).  Both are rounded to the tensors' type, which is what the tensor cores multiply: half a step
+// between the inputs and a gradient, beside the half step of the gradient itself.
 // ---------------------------------------------------------------------------
 
 template <typename T, int kAct>
@@ -728,6 +730,112 @@ cudaError_t gated_grad_t(const GatedGradParams &p, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
+// the weights' gradients of up to four tokens: d_w[i, :] = sum over the tokens of d[token, i] x[token, :], bound by writing
+// them.  A block takes 32 rows of both weights and 256 columns: it evaluates d_gate and d_up of its rows into shared memory
+// (f32, nothing is rounded on the way into the sums), then a warp takes every eighth row and a lane eight columns of it,
+// whose values of x it holds in registers.  Blocks of the first columns also write d_gate and d_up, rounded, for d_x.
+// Against tiles of the tensor cores, with d_x: 4 tokens 5504 x 2048 21.6 us and 31.6, 1408 x 2048 11.4 and 16.4; with 8
+// tokens, whose values of x take 64 registers, 35.9 and 32.0.
+// ---------------------------------------------------------------------------
+
+constexpr int kFewRows = 32, kFewCols = 256, kFewTokens = 4;
+
+// kVec: a lane's eight columns lie together and are one access; else every 32nd
+template <typename T, int kAct, bool kVec>
+__global__ void __launch_bounds__(256) outer_few_kernel(const GatedGradParams p, const OuterGemmParams w) {
+    __shared__ __align__(16) float sd[2][kFewRows][kFewTokens];
+    grid_dep_begin();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t chunks = (w.k + kFewCols - 1) / kFewCols;
+    const int64_t i0 = blockIdx.x / chunks * kFewRows, j0 = blockIdx.x % chunks * kFewCols;
+    const int tokens = static_cast<int>(p.m);
+    if (warp < kFewTokens) {
+        const int64_t i = i0 + lane;  // this thread's row; its token is `warp`
+        float dg = 0.f, du = 0.f;
+        if (warp < tokens && i < p.n) {
+            const float g = Elem<T>::to_f(static_cast<const T *>(p.gate)[warp * p.ld_saved + i]);
+            const float u = Elem<T>::to_f(static_cast<const T *>(p.up)[warp * p.ld_saved + i]);
+            const float d = Elem<T>::to_f(static_cast<const T *>(p.d_h)[warp * p.ld_dh + i]);
+            float slope;
+            const float a = gate_act_slope_16(kAct, g, &slope);
+            dg = d * u * slope;
+            du = d * a;
+            if (j0 == 0 && p.d[0] != nullptr) {
+                static_cast<T *>(p.d[0])[warp * p.ldd + i] = Elem<T>::from_f(dg);
+                static_cast<T *>(p.d[1])[warp * p.ldd + i] = Elem<T>::from_f(du);
+            }
+        }
+        sd[0][lane][warp] = dg;
+        sd[1][lane][warp] = du;
+    }
+    auto column = [&](int e) { return kVec ? j0 + 8 * lane + e : j0 + lane + 32 * e; };
+    const int64_t left = w.k - column(0);
+    float x[kFewTokens][8];
+#pragma unroll
+    for (int t = 0; t < kFewTokens; ++t) {
+        const T *from = static_cast<const T *>(w.x) + t * w.ldx;
+        if (kVec) {
+            if (t < tokens && left > 0) {
+                load_f<T, 8>(from + column(0), left >= 8, left, x[t]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[t][e] = 0.f;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[t][e] = t < tokens && column(e) < w.k ? Elem<T>::to_f(from[column(e)]) : 0.f;
+        }
+    }
+    __syncthreads();
+    for (int r = warp; r < kFewRows && i0 + r < p.n; r += 8) {
+#pragma unroll
+        for (int pr = 0; pr < 2; ++pr) {
+            float d[kFewTokens], v[8];
+#pragma unroll
+            for (int q = 0; q < kFewTokens / 4; ++q) {
+                const float4 f = *reinterpret_cast<const float4 *>(&sd[pr][r][4 * q]);
+                d[4 * q] = f.x, d[4 * q + 1] = f.y, d[4 * q + 2] = f.z, d[4 * q + 3] = f.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll
+            for (int t = 0; t < kFewTokens; ++t) {
+                if (t >= tokens) break;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = fmaf(d[t], x[t][e], v[e]);
+            }
+            T *to = static_cast<T *>(pr == 0 ? w.c[0] : w.c[1]) + (i0 + r) * w.ldc;
+            if (kVec) {
+                if (left > 0) store_f<T, 8>(to + column(0), left >= 8, left, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (column(e) < w.k) to[column(e)] = Elem<T>::from_f(v[e]);
+            }
+        }
+    }
+}
+
+template <typename T, bool kVec>
+cudaError_t outer_few_v(const GatedGradParams &p, const OuterGemmParams &w, cudaStream_t s) {
+    const int64_t blocks = (p.n + kFewRows - 1) / kFewRows * ((w.k + kFewCols - 1) / kFewCols);
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+    switch (p.act) {
+    case GBMM_GATE_SILU: return launch_early(outer_few_kernel<T, GBMM_GATE_SILU, kVec>, grid, block, 0, s, p, w);
+    case GBMM_GATE_GELU: return launch_early(outer_few_kernel<T, GBMM_GATE_GELU, kVec>, grid, block, 0, s, p, w);
+    case GBMM_GATE_GELU_TANH: return launch_early(outer_few_kernel<T, GBMM_GATE_GELU_TANH, kVec>, grid, block, 0, s, p, w);
+    default: return launch_early(outer_few_kernel<T, GBMM_GATE_RELU, kVec>, grid, block, 0, s, p, w);
+    }
+}
+template <typename T>
+cudaError_t outer_few_t(const GatedGradParams &p, const OuterGemmParams &w, cudaStream_t s) {
+    auto rows16 = [](const void *ptr, int64_t ld) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % 8 == 0; };
+    return rows16(w.x, w.ldx) && rows16(w.c[0], w.ldc) && rows16(w.c[1], w.ldc) ? outer_few_v<T, true>(p, w, s)
+                                                                                 : outer_few_v<T, false>(p, w, s);
+}
+
+// ---------------------------------------------------------------------------
 // 16-bit rows that TMA cannot read, written again into rows that it can
 // ---------------------------------------------------------------------------
 
@@ -766,6 +874,12 @@ repack16_kernel(const RepackParams first, const RepackParams second, const Repac
 cudaError_t launch_gated_rowdot(int dt, const GatedParams &p, cudaStream_t s) { GBMM_BY_TYPE(dt, rowdot_t) }
 cudaError_t launch_gated_simt(int dt, const GatedParams &p, cudaStream_t s) { GBMM_BY_TYPE(dt, gated_simt_t) }
 cudaError_t launch_gated_grad(int dt, const GatedGradParams &p, cudaStream_t s) { GBMM_BY_TYPE(dt, gated_grad_t) }
+
+// The weights' gradients of at most gated_few_tokens() tokens, 16-bit types; p.d null: d_gate and d_up are not written.
+int gated_few_tokens() { return kFewTokens; }
+cudaError_t launch_gated_outer_few(int dt, const GatedGradParams &p, const OuterGemmParams &w, cudaStream_t s) {
+    return dt == kF16 ? outer_few_t<__half>(p, w, s) : outer_few_t<__nv_bfloat16>(p, w, s);
+}
 
 // The gradients of f32 blocks: x null or w null where one of them is not asked for.
 cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, int *launches, cudaStream_t s) {

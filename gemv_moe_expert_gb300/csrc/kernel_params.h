@@ -340,6 +340,8 @@ cudaError_t launch_gated_simt(int dt, const GatedParams &p, cudaStream_t s);
 cudaError_t launch_gated_grad(int dt, const GatedGradParams &p, cudaStream_t s);
 // f32
 cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, int *launches, cudaStream_t s);
+int gated_few_tokens();
+cudaError_t launch_gated_outer_few(int dt, const GatedGradParams &p, const OuterGemmParams &w, cudaStream_t s);
 cudaError_t launch_repack16(const RepackParams (&p)[3], cudaStream_t s);
 cudaError_t launch_lay_out_codes(const RepackParams &a, const RepackParams &b, cudaStream_t s);  // rows 0: nothing to do
 // on the tensor cores: gated a[0] = x, b = both weights, all K-contiguous in boxes of pair_tc_rows()

@@ -570,7 +570,8 @@ GBMM_API gbmm_status gbmm_gated_backward_scratch_bytes(gbmm_dtype dt, int64_t m,
 
 /*
  * gbmm_gated_backward -- from d_h, x, the weights and the saved projections:
- *   d_gate = d_h * up * act'(gate)      d_up = d_h * act(gate)     (rounded to dt)
+ *   d_gate = d_h * up * act'(gate)      d_up = d_h * act(gate)     (rounded to dt; not for
+ *                                       the weights' gradients of up to four tokens)
  *   d_x [m, k] = d_gate w_gate + d_up w_up
  *   d_w_gate [n, k] = d_gate^T x        d_w_up [n, k] = d_up^T x
  * d_x may be NULL (the weights are not read then), and d_w_gate and d_w_up may both be (x is

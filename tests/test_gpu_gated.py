@@ -292,6 +292,24 @@ def test_backward_over_many_rows_of_weights(m, n, k, pad, d_w):
     b.check_backward("gelu", b.backward("gelu", True, d_w))
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k,pad,off", [(1, 1, 1, 0, 0), (1, 200, 200, 0, 0), (2, 128, 1032, 3, 0), (3, 33, 255, 0, 1),
+                                           (4, 95, 264, 8, 8), (4, 700, 512, 0, 0), (3, 1025, 2049, 0, 0),
+                                           (4, 65, 257, 4, 4)])
+def test_weights_gradients_of_few_tokens_round_once(dtype, m, n, k, pad, off):
+    """Up to four tokens: d_gate and d_up enter the weights' gradients in f32, off by 16 u |d_h up| and 16 u |d_h gate|."""
+    b = Block(dtype, m, n, k, pad=pad, off=off)
+    for d_x in (True, False):
+        got = b.backward("silu", d_x, True)
+        b.check_backward("silu", got)
+        _, dwg, dwu, dg, du = ffn_ref.backward("silu", b.x, b.wg, b.wu, b.g, b.u, b.d_h)
+        x = np.abs(b.x)
+        for out, ref, d, other in ((got[1], dwg, dg, b.u), (got[2], dwu, du, b.g)):
+            e = 16 * U * np.abs(b.d_h * other)
+            tol = e.T @ x + (m + 16) * U * ((np.abs(d) + e).T @ x)
+            near(out, ref, tol * (1 + UO[dtype]) + UO[dtype] * np.abs(ref) + TINY[dtype], "d_w")
+
+
 @pytest.mark.parametrize("d_x,d_w", [(True, True), (True, False), (False, True)])
 @pytest.mark.parametrize("m,n,k", [(2570, 300, 2100), (520, 2600, 1300), (1300, 1290, 1290)])
 def test_backward_tiles_of_both_products(m, n, k, d_x, d_w):
@@ -433,7 +451,7 @@ def step(dtype, m, n, k, t, stream=None):
 
 
 STEPS = [("f32", 20, 72, 136), ("f16", 12, 264, 520), ("bf16", 100, 200, 320), ("bf16", 600, 1032, 520),
-         ("f16", 130, 77, 33), ("bf16", 40, 1400, 264), ("f16", 7, 3001, 133), ("f32", 2000, 72, 136)]
+         ("f16", 130, 77, 33), ("f16", 3, 264, 520), ("bf16", 40, 1400, 264), ("f16", 7, 3001, 133), ("f32", 2000, 72, 136)]
 
 
 @pytest.mark.parametrize("dtype,m,n,k", STEPS)
