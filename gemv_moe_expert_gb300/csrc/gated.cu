@@ -5,6 +5,8 @@
 // chosen by the entry points (ffn_api.cu) where types and layouts allow.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "gated.cuh"
 
 namespace cg = cooperative_groups;
@@ -501,19 +503,17 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const TileArgs t, co
     }
 }
 
-// One tile of the gradient of x.  kSplit: a cluster of two CTAs a tile, one source each.
+// One tile of the gradient of x.  kSplit: a cluster of `parts` CTAs a tile (two: one source each).
 template <int kTM, int kTN, bool kSplit>
-__device__ __forceinline__ void sum_tile(const TileArgs &t, float *out, int64_t ldc, int64_t block,
+__device__ __forceinline__ void sum_tile(const TileArgs &t, float *out, int64_t ldc, int64_t block, int rank, int parts,
                                          typename TileProduct<float, kSum, kTM, kTN>::Smem &sm) {
     using Tile = TileProduct<float, kSum, kTM, kTN>;
     Tile tile;
-    if (kSplit) block >>= 1;
     const int64_t m0 = block / t.tiles_n * Tile::kBM, n0 = block % t.tiles_n * Tile::kBN;
     if constexpr (kSplit) {
-        const int rank = blockIdx.x & 1;
-        tile.run(t, m0, n0, sm, rank, 2);
-        tile.reduce_cluster(sm, rank, 2);
-        if (rank == 1) return;
+        tile.run(t, m0, n0, sm, rank, parts);
+        tile.reduce_cluster(sm, rank, parts);
+        if (rank != 0) return;
     } else {
         tile.run(t, m0, n0, sm);
     }
@@ -536,13 +536,19 @@ struct OuterOut {
     int64_t ldc;
     int32_t vec;
 };
-template <int kTM, int kTN>
-__device__ __forceinline__ void outer_tile(const TileArgs &t, const OuterOut &o, int64_t block,
+template <int kTM, int kTN, bool kSplit>
+__device__ __forceinline__ void outer_tile(const TileArgs &t, const OuterOut &o, int64_t block, int rank, int parts,
                                            typename TileProduct<float, kOuter, kTM, kTN>::Smem &sm) {
     using Tile = TileProduct<float, kOuter, kTM, kTN>;
     Tile tile;
     const int64_t m0 = block / t.tiles_n * Tile::kBM, n0 = block % t.tiles_n * Tile::kBN;
-    tile.run(t, m0, n0, sm);
+    if constexpr (kSplit) {
+        tile.run(t, m0, n0, sm, rank, parts);
+        tile.reduce_cluster(sm, rank, parts);
+        if (rank != 0) return;
+    } else {
+        tile.run(t, m0, n0, sm);
+    }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
     for (int pr = 0; pr < 2; ++pr)
@@ -569,12 +575,12 @@ __device__ __forceinline__ void outer_tile(const TileArgs &t, const OuterOut &o,
 template <int kTM, int kTN>
 __global__ void __launch_bounds__(256, 2) sum_gemm_simt_kernel(const TileArgs t, float *out, int64_t ldc) {
     __shared__ __align__(16) typename TileProduct<float, kSum, kTM, kTN>::Smem sm;
-    sum_tile<kTM, kTN, false>(t, out, ldc, blockIdx.x, sm);
+    sum_tile<kTM, kTN, false>(t, out, ldc, blockIdx.x, 0, 1, sm);
 }
 template <int kTM, int kTN>
 __global__ void __launch_bounds__(256, 2) outer_gemm_simt_kernel(const TileArgs t, const OuterOut o) {
     __shared__ __align__(16) typename TileProduct<float, kOuter, kTM, kTN>::Smem sm;
-    outer_tile<kTM, kTN>(t, o, blockIdx.x, sm);
+    outer_tile<kTM, kTN, false>(t, o, blockIdx.x, 0, 1, sm);
 }
 // Both gradients in one grid, so that the tiles of one fill the last round of the other's: clusters of two,
 // the first x_blocks of them the gradient of x (the longer tiles), a pair a tile.
@@ -585,8 +591,35 @@ both_gemm_simt_kernel(const TileArgs tx, float *out, int64_t ldc, unsigned x_blo
         typename TileProduct<float, kSum, 8, 8>::Smem x;
         typename TileProduct<float, kOuter, 8, 4>::Smem w;
     } sm;
-    if (blockIdx.x < x_blocks) sum_tile<8, 8, true>(tx, out, ldc, blockIdx.x, sm.x);
-    else if (blockIdx.x - x_blocks < w_blocks) outer_tile<8, 4>(tw, o, blockIdx.x - x_blocks, sm.w);
+    if (blockIdx.x < x_blocks) sum_tile<8, 8, true>(tx, out, ldc, blockIdx.x >> 1, blockIdx.x & 1, 2, sm.x);
+    else if (blockIdx.x - x_blocks < w_blocks) outer_tile<8, 4, false>(tw, o, blockIdx.x - x_blocks, 0, 1, sm.w);
+}
+// The same where the tiles would not fill the SMs: small ones, in clusters of `parts` that divide the contraction of one
+// tile (x_split, w_split) or take a tile each; the side with the longer chains first.
+struct SmallGrid {
+    unsigned x_tiles, w_tiles, parts, x_blocks, w_blocks;
+    int32_t x_split, w_split, w_first;
+};
+__global__ void __launch_bounds__(256, 2)
+both_small_simt_kernel(const TileArgs tx, float *out, int64_t ldc, const TileArgs tw, const OuterOut o, const SmallGrid g) {
+    __shared__ __align__(16) union {
+        typename TileProduct<float, kSum, 4, 4>::Smem x;
+        typename TileProduct<float, kOuter, 4, 4>::Smem w;
+    } sm;
+    const unsigned first = g.w_first ? g.w_blocks : g.x_blocks;
+    const bool is_x = (blockIdx.x < first) != (g.w_first != 0);
+    const unsigned block = blockIdx.x < first ? blockIdx.x : blockIdx.x - first;
+    const bool split = is_x ? g.x_split : g.w_split;
+    const unsigned tile = split ? block / g.parts : block;
+    const int rank = split ? static_cast<int>(block % g.parts) : 0, parts = static_cast<int>(g.parts);
+    if (tile >= (is_x ? g.x_tiles : g.w_tiles)) return;
+    if (is_x) {
+        if (split) sum_tile<4, 4, true>(tx, out, ldc, tile, rank, parts, sm.x);
+        else sum_tile<4, 4, false>(tx, out, ldc, tile, 0, 1, sm.x);
+    } else {
+        if (split) outer_tile<4, 4, true>(tw, o, tile, rank, parts, sm.w);
+        else outer_tile<4, 4, false>(tw, o, tile, 0, 1, sm.w);
+    }
 }
 
 // Not started early behind the kernel before it: blocks that take places as they come free gather on a few SMs, and a
@@ -638,6 +671,36 @@ bool large_tiles(unsigned large, unsigned small, unsigned small_cost) {
     const unsigned sms = static_cast<unsigned>(device_sm_count());
     return large != 0 && (small == 0 || static_cast<uint64_t>((large + sms - 1) / sms) * 16 <=
                                             static_cast<uint64_t>((small + sms - 1) / sms) * small_cost);
+}
+
+// How few tiles are divided: what counts is the longest chain of steps (0.3 us each) of any block, the exchange in a
+// cluster as kJoin steps.  Blocks beyond two an SM (an eighth fewer in large clusters, which lie within groups of 16 to 20
+// SMs) wait for a place, as long as an average one.  m x n x k 21 x 640 x 64: 13.9 us, and 57 undivided; 4000 x 128 x 256:
+// 47 and 267; 256 x 512 x 512: 25 and 63.
+SmallGrid small_grid(unsigned x_tiles, unsigned w_tiles, int64_t x_steps, int64_t w_steps) {
+    constexpr int64_t kJoin = 8;
+    SmallGrid best{};
+    int64_t least = -1;
+    for (unsigned parts = 1; parts <= 8; ++parts) {
+        const int64_t places = (parts > 4 ? 14 : 16) * static_cast<int64_t>(device_sm_count()) / 8;
+        for (int split = parts > 1 ? 1 : 0; split < (parts > 1 ? 4 : 1); ++split) {
+            const int xs = split & 1, ws = split >> 1;
+            if ((xs && x_tiles == 0) || (ws && w_tiles == 0)) continue;
+            auto blocks = [&](unsigned tiles, int divided) {
+                return divided ? tiles * parts : (tiles + parts - 1) / parts * parts;
+            };
+            const int64_t xc = x_tiles ? (xs ? (x_steps + parts - 1) / parts + kJoin : x_steps) : 0;
+            const int64_t wc = w_tiles ? (ws ? (w_steps + parts - 1) / parts + kJoin : w_steps) : 0;
+            SmallGrid g{x_tiles, w_tiles, parts, blocks(x_tiles, xs), blocks(w_tiles, ws), xs, ws, wc > xc};
+            const int64_t count = static_cast<int64_t>(g.x_blocks) + g.w_blocks, all = g.x_blocks * xc + g.w_blocks * wc;
+            const int64_t time = std::max(xc, wc) + (count > places ? all / count * ((count - 1) / places) : 0);
+            if (least < 0 || time < least) {
+                least = time;
+                best = g;
+            }
+        }
+    }
+    return best;
 }
 
 template <typename T>
@@ -922,6 +985,15 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
         static_assert(kLargeX == kLargeW, "one launch for both");
         return launch_whole(both_gemm_simt_kernel, static_cast<unsigned>(together), 2, (tx.fold | tw.fold) * kLargeX, s, tx, c,
                             x->ldc, 2 * x_large, tw, o, w_large);
+    }
+    if (together < static_cast<uint64_t>(device_sm_count()) && (x == nullptr || x_small > 0) && (w == nullptr || w_small > 0)) {
+        const SmallGrid g = small_grid(x_small, w_small, x != nullptr ? 2 * ((x->k + kTK - 1) / kTK) : 0,
+                                       w != nullptr ? (w->m + kTK - 1) / kTK : 0);
+        if (x != nullptr) txs.fold = folds(x->k, 2, g.x_split ? g.parts : 1);
+        if (w != nullptr) tws.fold = folds(w->m, 1, g.w_split ? g.parts : 1);
+        static_assert(kSmallX <= kSmallW, "one launch for both");
+        return launch_whole(both_small_simt_kernel, g.x_blocks + g.w_blocks, g.parts, (txs.fold | tws.fold) * kSmallW, s, txs,
+                            c, x != nullptr ? x->ldc : int64_t{0}, tws, o, g);
     }
     if (x != nullptr) {
         tx.fold = txs.fold;

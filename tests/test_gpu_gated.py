@@ -356,6 +356,15 @@ def test_long_sums_of_gradients_in_f32(m, n, k, d_x, d_w):
             assert (out.double() / (length * LOST) - 1).abs().max() <= (512 + length / 512 + 16) * U
 
 
+@pytest.mark.parametrize("d_x,d_w", [(True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("m,n,k,pad", [(21, 640, 64, 8), (1000, 64, 70, 1), (1300, 128, 256, 0), (16, 1409, 513, 0),
+                                       (256, 512, 512, 0), (3, 1500, 100, 3), (1, 1, 300, 0)])
+def test_backward_of_few_tiles_in_f32(m, n, k, pad, d_x, d_w):
+    """Contractions divided over clusters: of one product, of both, of neither."""
+    b = Block("f32", m, n, k, pad=pad)
+    b.check_backward("silu", b.backward("silu", d_x, d_w))
+
+
 def test_backward_of_nothing_writes_zeros():
     t = torch.full((3, 8, 16), 7.0, device="cuda")
     gb.check(gb.gbmm_gated_backward("f32", 0, 0, 8, 16, None, 16, t, t, 16, None, None, 8, None, 8, None, 16, t[0],
@@ -451,7 +460,8 @@ def step(dtype, m, n, k, t, stream=None):
 
 
 STEPS = [("f32", 20, 72, 136), ("f16", 12, 264, 520), ("bf16", 100, 200, 320), ("bf16", 600, 1032, 520),
-         ("f16", 130, 77, 33), ("f16", 3, 264, 520), ("bf16", 40, 1400, 264), ("f16", 7, 3001, 133), ("f32", 2000, 72, 136)]
+         ("f16", 130, 77, 33), ("f16", 3, 264, 520), ("bf16", 40, 1400, 264), ("f16", 7, 3001, 133),
+         ("f32", 2000, 72, 136), ("f32", 90, 1300, 500)]
 
 
 @pytest.mark.parametrize("dtype,m,n,k", STEPS)
