@@ -267,7 +267,7 @@ gbmm_status gbmm_gated_backward_scratch_bytes(gbmm_dtype dt, int64_t m, int64_t 
     parts.add(m, round_up(n, 16 / size), size);
     parts.add(m, round_up(n, 16 / size), size);
     if (dt != GBMM_F32 && !aligned) {
-        parts.add(m, round_up(k, 8), 2);
+        if (m > gated_few_tokens()) parts.add(m, round_up(k, 8), 2);  // few tokens' x is read as it lies
         parts.add(n, round_up(k, 8), 2);
         parts.add(n, round_up(k, 8), 2);
     }
