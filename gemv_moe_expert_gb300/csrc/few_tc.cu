@@ -37,6 +37,11 @@ constexpr int kChunk = 8;                // code blocks (of 128) whose sums stay
 
 enum Kind { kGated, kCodes8, kSum };
 
+// CTAs that an SM holds at once.  Together they never ask for more than its kTmemCols columns of tensor memory: a CTA
+// that waited for columns would wait without a limit, and for one that may itself be waiting in a cluster barrier.
+constexpr int ctas_per_sm(bool codes, int tokens) { return codes && tokens == 128 ? 1 : 2; }
+constexpr uint32_t kTmemCols = 512;
+
 template <int kKind, int kN>
 struct Ring {
     static constexpr bool kCodes = kKind == kCodes8;
@@ -60,6 +65,7 @@ struct Ring {
     static_assert(kStageBytes % 1024 == 0 && kSlotBytes % 1024 == 0, "swizzled tiles need 1024-byte alignment");
     static_assert(kBM * kN * 4 <= kRingBytes, "the partial sums are parked in the ring");
     static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
+    static_assert(228 * 1024 / (kSmemBytes + 1024) == ctas_per_sm(kCodes, kN), "CTAs that shared memory lets an SM hold");
     static_assert(8 * (2 * (kStages + kSlots) + 2) + 8 <= kBarBytes, "barriers");
 };
 
@@ -424,7 +430,8 @@ cudaError_t few_n(const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
 
 template <typename TC, uint32_t kFmt, int kKind>
 cudaError_t few_t(int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
-    if (p.ksplit < 1 || p.ksplit > kMaxSplit) return cudaErrorInvalidValue;
+    if (p.ksplit < 1 || p.ksplit > kMaxSplit || ctas_per_sm(kKind == kCodes8, tokens) * p.tmem_cols > kTmemCols)
+        return cudaErrorInvalidValue;
     switch (tokens) {
     case 16: return few_n<TC, kFmt, kKind, 16>(maps, p, s);
     case 32: return few_n<TC, kFmt, kKind, 32>(maps, p, s);
@@ -438,12 +445,14 @@ cudaError_t few_t(int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaS
 
 int few_tc_rows(bool codes) { return codes ? kBM : kBM / 2; }
 int few_tc_block_k() { return 64; }
+int few_tc_ctas_per_sm(bool codes, int tokens) { return ctas_per_sm(codes, tokens); }
 
 namespace {
-int ctas_per_sm(bool codes, int tokens) { return codes && tokens == 128 ? 1 : 2; }
 constexpr int kCodeCols = 128;  // columns of tensor memory that hold weights
 // code blocks that one CTA's accumulators take
-int64_t code_blocks(int tokens) { return ((ctas_per_sm(true, tokens) == 1 ? 512 : 256) - kCodeCols) / tokens * kChunk; }
+int64_t code_blocks(int tokens) {
+    return (static_cast<int>(kTmemCols) / ctas_per_sm(true, tokens) - kCodeCols) / tokens * kChunk;
+}
 
 struct Split {
     int64_t ctas, split;
@@ -479,13 +488,14 @@ bool few_tc_half_tokens(int64_t m) { return m > 32; }
 int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p) {
     int tokens = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 || codes ? 64 : 128;
     Split s = split_for(codes ? kCodes8 : kGated, tokens, m, n, k, num_sms);
-    if (codes && m > 64) {
+    if (codes && m > 32) {
         // Tiles of 128 tokens read the weights once, but have an SM to themselves: taken where they fill the SMs once
         // (128 tokens: 4096 x 11008 26.5 us against 38 with 64 a tile, 11008 x 4096 42.7 against 37.7), or where 64 leave
-        // no room for the accumulators.
+        // no room for the accumulators of so long a sum.
         const Split wide = split_for(kCodes8, 128, m, n, k, num_sms);
         const int64_t kb = (k + 127) / 128;
-        if ((m <= 128 && wide.ctas <= num_sms && 4 * wide.ctas >= 3LL * num_sms) || kb > s.split * code_blocks(64)) {
+        const bool fills = m > 64 && m <= 128 && wide.ctas <= num_sms && 4 * wide.ctas >= 3LL * num_sms;
+        if (fills || kb > s.split * code_blocks(64)) {
             tokens = 128;
             s = wide;
         }

@@ -531,4 +531,23 @@ gbmm_status gbmm_gemm_i8(gbmm_dtype dt, int64_t m, int64_t n, int64_t k, const i
                          fn, s);
 }
 
+gbmm_status gbmm_test_few_plan(int form, int64_t m, int64_t n, int64_t k, int32_t sms, int32_t plan[4]) {
+    record_error(GBMM_OK, "");
+    const char *fn = "gbmm_test_few_plan";
+    if (form < 0 || form > 2 || m < 1 || n < 1 || k < 1 || !in_range(m) || !in_range(n) || !in_range(k) || sms < 1 ||
+        plan == nullptr)
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "%s: unknown form, size out of range, or plan is null", fn);
+    for (int i = 0; i < 4; ++i) plan[i] = 0;
+    const bool codes = form == 1;
+    if (codes ? k > GBMM_I8_MAX_K || i8_plan(m, n, k, true, true).route != I8Plan::kFew
+              : form == 0 && (gated_dot(m, n, k, true) || !few_tc_takes(false, m, n, k)))
+        return GBMM_OK;
+    FewTcParams p{};
+    plan[0] = form == 2 ? few_tc_plan_sum(m, n, k, sms, &p) : few_tc_plan(codes, m, n, k, sms, &p);
+    plan[1] = p.ksplit;
+    plan[2] = static_cast<int32_t>(p.tmem_cols);
+    plan[3] = few_tc_ctas_per_sm(codes, plan[0]);
+    return GBMM_OK;
+}
+
 }  // extern "C"

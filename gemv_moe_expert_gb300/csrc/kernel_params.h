@@ -356,6 +356,7 @@ bool few_tc_takes(bool codes, int64_t m, int64_t n, int64_t k);
 bool few_tc_half_tokens(int64_t m);
 int few_tc_plan(bool codes, int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p);
 int few_tc_block_k();
+int few_tc_ctas_per_sm(bool codes, int tokens);
 bool few_tc_takes_sum(int64_t m, int64_t n, int64_t k, bool need_w, int num_sms);
 int few_tc_plan_sum(int64_t m, int64_t n, int64_t k, int num_sms, FewTcParams *p);
 cudaError_t launch_sum_few(int dt, int tokens, const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s);

@@ -696,6 +696,15 @@ GBMM_API gbmm_status gbmm_test_bounded_wait(uint64_t limit_ns, gbmm_stream strea
  */
 GBMM_API gbmm_status gbmm_test_static_scratch_copy(void *dst, uint64_t bytes, gbmm_stream stream);
 
+/*
+ * gbmm_test_few_plan -- how a product of some tens of tokens would be divided on a GPU of `sms`
+ * SMs; nothing is launched.  form: 0 gbmm_gated, 1 gbmm_gemm_i8 (both 16-byte-aligned), 2 the d_x
+ * of gbmm_gated_backward.  plan: tokens of a tile, CTAs that share a tile, columns of tensor memory
+ * that each of them allocates, and CTAs that an SM holds at once; zeros where such a call takes
+ * another way.
+ */
+GBMM_API gbmm_status gbmm_test_few_plan(int form, int64_t m, int64_t n, int64_t k, int32_t sms, int32_t plan[4]);
+
 #ifdef __cplusplus
 }
 #endif

@@ -168,3 +168,50 @@ def test_backward_asks_for_its_kernels_first(kernel):
     gb.gbmm_test_inject_kernel_failure(kernel)
     assert call(*CALLS["back"], {}) == PASSES and kernel in gb.gbmm_last_error()
     gb.gbmm_test_inject_kernel_failure("*")
+
+
+GATED_FORM, CODES_FORM, SUM_FORM = 0, 1, 2
+
+
+def needed_columns(form, tokens, cluster, k):
+    """Tensor-memory columns of one CTA: one f32 accumulator of `tokens` columns; for codes one for each 1024 of its
+    share of k, in whole blocks of 128, beside 128 columns of weights."""
+    if form != CODES_FORM:
+        return tokens
+    share = -(-(-(-k // 128)) // cluster)
+    return 128 + -(-share // 8) * tokens
+
+
+@pytest.mark.parametrize("sms", [152, 148, 16, 2, 1])
+@pytest.mark.parametrize("form", [GATED_FORM, CODES_FORM, SUM_FORM])
+def test_ctas_of_an_sm_share_its_tensor_memory(form, sms):
+    """A CTA that waits for columns waits without a limit: the CTAs that an SM holds never ask for more than 512."""
+    edges = [e + d for e in (1, 8, 16, 32, 64, 128, 256, 512, 600) for d in (-1, 0, 1) if e + d > 0]
+    lengths = [1, 64, 127, 128, 129, 1000, 1024, 1025, 2048, 4096, 11008]
+    lengths += [1024 * e + d for e in (8, 12, 16, 20, 24, 32, 48, 64, 96, 120) for d in (-1, 0, 1)]
+    lengths += [18944, 20000, 131071]
+    seen = 0
+    for m in edges:
+        for n in (1, 70, 128, 1000, 2048, 3584, 4096, 8192, 11008, 100000):
+            for k in lengths:
+                st, (tokens, cluster, columns, held) = gb.gbmm_test_few_plan(form, m, n, k, sms)
+                assert st == gb.GBMM_OK
+                if tokens == 0:
+                    continue
+                seen += 1
+                size = (m, n, k)
+                assert tokens in (16, 32, 64, 128) and 1 <= cluster <= 8 and held in (1, 2), size
+                assert needed_columns(form, tokens, cluster, k) <= columns, size
+                assert columns >= 32 and columns & (columns - 1) == 0 and columns * held <= 512, size
+    assert seen > 500
+
+
+def test_the_long_sums_of_some_tens_of_tokens_take_wide_tiles():
+    """33 to 64 tokens over more than 16384 codes: three accumulators of 64 tokens would fill an SM's tensor memory
+    twice over, so that such tiles are 128 tokens wide and have their SM to themselves."""
+    for m in (33, 40, 48, 64):
+        for k in (16385, 18944, 20000, 24576):
+            assert gb.gbmm_test_few_plan(CODES_FORM, m, 3584, k, 152)[1][0] == 128
+        assert gb.gbmm_test_few_plan(CODES_FORM, m, 3584, 16384, 152)[1][0] == 64
+        assert gb.gbmm_test_few_plan(CODES_FORM, m, 3584, 24577, 152)[1][0] == 0
+    assert gb.gbmm_test_few_plan(3, 1, 1, 1, 152)[0] == BAD and gb.gbmm_test_few_plan(0, 0, 1, 1, 152)[0] == BAD
