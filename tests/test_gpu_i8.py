@@ -307,11 +307,11 @@ def test_two_streams_at_once():
         assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
-@pytest.mark.parametrize("m,n,k", [(40, 2560, 18944), (64, 2500, 24576), (33, 2600, 16385), (64, 2600, 16384)])
+@pytest.mark.parametrize("m,n,k", [(40, 3584, 18944), (64, 2500, 24576), (33, 3584, 16385), (64, 2600, 16384)])
 def test_long_sums_of_some_tens_of_tokens_in_more_ctas_than_sms(m, n, k):
-    """Tiles of 64 and of 128 tokens on both sides of the limit of 64's tensor memory, clusters of eight over all SMs."""
+    """Tiles of 64 and of 128 tokens on both sides of the limit of 64's tensor memory, clusters of six to eight over all SMs."""
     st, (tokens, cluster, _, _) = gb.gbmm_test_few_plan(1, m, n, k, 152)
     gb.check(st)
-    assert cluster == 8 and -(-n // 128) * cluster > 152 and tokens == (64 if k <= 16384 else 128)
+    assert cluster >= 6 and -(-n // 128) * cluster > 152 and tokens == (64 if k <= 16384 else 128)
     p = Product(m, n, k)
     p.check("f32", p.run("f32"))
