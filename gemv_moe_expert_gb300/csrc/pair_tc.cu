@@ -141,6 +141,8 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
 // lanes meet in a bank) and one TMA store, which writes whole row segments and leaves what is outside the matrix
 // alone; where TMA cannot write the rows, a row at a time.  Direct 32-byte stores, every lane its own row, held a warp
 // for about 700 cycles each.
+// Every write commits one bulk group, an empty one where it needs no TMA store: the groups count the writes, so that
+// the newest one may be open when the other buffer is written again.
 template <typename TC>
 struct Writer {
     static constexpr int kBufs = sizeof(TC) == 4 ? 1 : 2;
@@ -202,6 +204,7 @@ struct Writer {
                 if (live) *reinterpret_cast<uint16_t *>(dst) = e;
             }
         }
+        if (lane == 0) bulk_commit();
         __syncwarp();
     }
     __device__ __forceinline__ void finish(int lane) const {

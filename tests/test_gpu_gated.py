@@ -505,3 +505,24 @@ def test_two_streams_at_once():
                 got.append(step(*c, t, s))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(300, 264, 328), (2049, 2003, 64), (1000, 4101, 136)])
+@pytest.mark.parametrize("pad_h,pad_saved", [(0, 1), (1, 0), (0, 0)])
+def test_outputs_whose_rows_tma_can_and_cannot_write(dtype, m, n, k, pad_h, pad_saved):
+    """h or the saved projections in rows on multiples of 16 bytes and the others not, and last columns that end inside
+    16 bytes of aligned rows: pieces that leave by TMA and by plain stores alternate.  The same values whatever the rows."""
+    b = Block(dtype, m, n, k)
+    outs = {}
+    for ld_h, ld_saved in ((n | 1, n | 1), (-(-n // 8) * 8 + pad_h, -(-n // 8) * 8 + pad_saved)):
+        for turn in range(4):
+            bufs = [empty(m, ld, dtype, 0) for ld in (ld_h, ld_saved, ld_saved)]
+            gb.check(gb.gbmm_gated(dtype, CODE["silu"], m, n, k, b.xp, b.ldk, b.gp, b.up, b.ldk, bufs[0][1], ld_h,
+                                   bufs[1][1], bufs[2][1], ld_saved, None, 0))
+            got = [fetch(o[0], m, n, ld, dtype, 0) for o, ld in zip(bufs, (ld_h, ld_saved, ld_saved))]
+            if not outs:
+                b.check_forward("silu", got)
+                outs["first"] = got
+            assert all(np.array_equal(a, c) for a, c in zip(outs["first"], got))
+    assert gb.gbmm_device_error()[0] == gb.GBMM_OK
