@@ -16,8 +16,9 @@
 //   warp 0      TMA
 //   warp 1      tensor memory, MMAs
 //   warps 2..5  (codes: 2..9, bytes to f16) the epilogue
-// Every mbarrier wait is bounded; on a timeout the kernel records it in the device error word, waits (bounded) for
-// its own copies and MMAs, still takes part in the cluster barriers, releases its TMEM and returns.
+// Every mbarrier wait is bounded; on a timeout the kernel records it in the device error word.  Whatever role gave up,
+// the CTA waits (bounded) for its own copies and MMAs, still takes part in the cluster barriers, releases its TMEM and
+// returns.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -198,13 +199,12 @@ few_tc_kernel(const __grid_constant__ FewTcMaps maps, const FewTcParams p) {
                 if (R::kHalfX) tma_load_3d(sw + kWBytes + R::kXBytes, x, full_bar(stage), k0 + 64, t0, 0);
                 ++issued;
             }
-            if (!ok) {
-                fail();
-                // wait for this CTA's own copies still in flight
-                for (int s = 0; s < kStages; ++s) {
-                    const uint32_t n_s = issued / kStages + (static_cast<uint32_t>(s) < issued % kStages ? 1u : 0u);
-                    if (n_s > 0) mbar_wait_bounded(full_bar(s), (n_s - 1u) & 1u, lim, nullptr);
-                }
+            if (!ok) fail();
+            // This CTA's copies have landed before it goes on to use the ring for something else, also where another role
+            // gave up after the last of them was issued.
+            for (int s = 0; s < kStages; ++s) {
+                const uint32_t n_s = issued / kStages + (static_cast<uint32_t>(s) < issued % kStages ? 1u : 0u);
+                if (n_s > 0 && !mbar_wait_bounded(full_bar(s), (n_s - 1u) & 1u, lim, nullptr)) fail();
             }
         }
     } else if (warp == 1) {
@@ -301,7 +301,9 @@ few_tc_kernel(const __grid_constant__ FewTcMaps maps, const FewTcParams p) {
             }
         }
     }
+    // the ring is idle from here on: copies have landed, conversions and MMAs are done or given up
     __syncwarp();
+    __syncthreads();
 
     // ---------------- epilogue: partial sums to shared memory, [token][row] ----------------
     using Sum = typename std::conditional<kCodes, int, float>::type;
