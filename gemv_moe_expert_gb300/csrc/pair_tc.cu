@@ -333,6 +333,15 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
                     }
                 }
             }
+            // Every stage has been used up before this CTA goes on to its end; a role that gave up after the last copies were
+            // issued shows here.
+            for (int s = 0; ok && s < kStages; ++s) {
+                ok = mbar_wait_bounded_cluster(empty_bar(stage), phase ^ 1u, lim, abort_flag);
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
             if (!ok) {
                 raise_abort();
                 // copies still in flight land within microseconds; give them 200 us
