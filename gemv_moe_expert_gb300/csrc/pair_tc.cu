@@ -258,10 +258,18 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&maps.a[0]);
-        tma_prefetch_desc(&maps.b[0]);
-        if (kMode != kCodes) tma_prefetch_desc(&maps.b[1]);
-        if (kMode == kGrads) tma_prefetch_desc(&maps.a[1]);
+        // only maps that the call has encoded
+        if (kMode != kGrads || p.need_c) {
+            tma_prefetch_desc(&maps.a[0]);
+            tma_prefetch_desc(&maps.b[0]);
+            if (kMode != kCodes) tma_prefetch_desc(&maps.b[1]);
+            if (kMode == kGrads) tma_prefetch_desc(&maps.a[1]);
+        }
+        if (kMode == kGrads && p.need_dw) {
+            tma_prefetch_desc(&maps.dw_a[0]);
+            tma_prefetch_desc(&maps.dw_a[1]);
+            tma_prefetch_desc(&maps.dw_b);
+        }
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_addr(tmem_slot), kTmemCols);
