@@ -60,12 +60,11 @@ bool resolve(const char *name) {
 }
 
 bool debug_sync() {
-    static int v = -1;
-    if (v < 0) {
+    static const bool v = [] {
         const char *e = getenv("GBMM_DEBUG_SYNC");
-        v = (e && e[0] == '1') ? 1 : 0;
-    }
-    return v == 1;
+        return e && e[0] == '1';
+    }();
+    return v;
 }
 
 gbmm_status after_launch(cudaError_t e, const char *name, cudaStream_t s) {

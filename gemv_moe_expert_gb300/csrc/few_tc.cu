@@ -401,7 +401,7 @@ few_tc_kernel(const __grid_constant__ FewTcMaps maps, const FewTcParams p) {
 template <typename TC, uint32_t kFmt, int kKind, int kN>
 cudaError_t few_n(const FewTcMaps &maps, const FewTcParams &p, cudaStream_t s) {
     using R = Ring<kKind, kN>;
-    static unsigned long long attr_set = 0;  // one bit per device
+    static DeviceBits attr_set{0};
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);

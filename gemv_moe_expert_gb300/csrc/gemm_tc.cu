@@ -624,7 +624,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 template <typename TC, uint32_t kFmt, bool kAMN, bool kBMN>
 cudaError_t tc_pair_t(const CUtensorMap &ma, const CUtensorMap &mb, const GemmTcParams &p, int num_sms,
                       cudaStream_t s) {
-    static unsigned long long attr_set = 0;  // one bit per device
+    static DeviceBits attr_set{0};
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);
@@ -664,7 +664,7 @@ cudaError_t tc_pair_major(const CUtensorMap &ma, const CUtensorMap &mb, const Ge
 template <typename TC, uint32_t kFmt, bool kAMN, bool kBMN>
 cudaError_t tc_t(const CUtensorMap &ma, const CUtensorMap &mb, const GemmTcParams &p, int num_sms,
                  cudaStream_t s) {
-    static unsigned long long attr_set = 0;  // one bit per device
+    static DeviceBits attr_set{0};
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);

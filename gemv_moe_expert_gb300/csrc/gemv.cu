@@ -379,7 +379,7 @@ __global__ void fill_zero_kernel(T *c, int64_t batch, int64_t m, int64_t n, int6
 }
 
 int num_sms() {
-    static int cached[64] = {0};
+    static std::atomic<int> cached[64];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) dev = 0;
@@ -446,7 +446,7 @@ cudaError_t coldot_stream_t(const CUtensorMap &map, const GemvParams &p, cudaStr
     // keeping at least four k-blocks per CTA
     int ksplit = 1;
     while (ksplit < 8 && tiles * bgrid * ksplit < 2LL * num_sms() && kbt >= 4LL * ksplit * 2) ksplit *= 2;
-    static unsigned long long attr_set = 0;  // one bit per device
+    static DeviceBits attr_set{0};
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);

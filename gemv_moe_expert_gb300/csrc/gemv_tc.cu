@@ -243,7 +243,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 
 template <typename TC, uint32_t kFmt>
 cudaError_t gemv_tc_t(const CUtensorMap &mw, const CUtensorMap &mx, const GemvTcParams &p, cudaStream_t s) {
-    static unsigned long long attr_set = 0;  // one bit per device
+    static DeviceBits attr_set{0};
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);

@@ -894,7 +894,7 @@ namespace {
 template <bool kSplit, bool kF16>
 cudaError_t grouped_tc_t(const CUtensorMap &map_w, const MatmulIdParams &p, int out_vec_ok, int num_sms,
                          cudaStream_t s) {
-    static unsigned long long attr_set = 0;
+    static DeviceBits attr_set{0};
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace gbmm {
 
 enum DType : int { kF32 = 0, kF16 = 1, kBF16 = 2 };
@@ -29,6 +31,9 @@ enum KernelId : uint32_t {
     kKidPairTc = 8,
     kKidFewTc = 9,
 };
+
+// What a launcher has done on a device, a bit each; host threads may launch at the same time.
+using DeviceBits = std::atomic<unsigned long long>;
 
 // default limit of a bounded device wait (1 s)
 constexpr uint64_t kWaitLimitNs = 1000000000ull;

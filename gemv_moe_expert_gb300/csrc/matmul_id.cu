@@ -716,7 +716,7 @@ cudaError_t launch_matmul_id_direct(int wdt, const MatmulIdParams &p, cudaStream
 
 cudaError_t launch_matmul_id_map(const MatmulIdParams &p, cudaStream_t s) {
     const size_t smem = (static_cast<size_t>(kMapWarps) + 1) * static_cast<size_t>(p.n_experts) * 4;
-    static unsigned long long attr_set = 0;
+    static DeviceBits attr_set{0};
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);

@@ -26,7 +26,7 @@ __global__ void bounded_wait_test_kernel(uint32_t *err, uint64_t limit_ns) {
 }  // namespace
 
 uint32_t *device_error_word() {
-    static uint32_t *cached[64] = {nullptr};
+    static std::atomic<uint32_t *> cached[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
     if (cached[dev] == nullptr) {
@@ -38,7 +38,7 @@ uint32_t *device_error_word() {
 }
 
 int device_sm_count() {
-    static int cached[64] = {0};
+    static std::atomic<int> cached[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
     if (cached[dev] == 0) {

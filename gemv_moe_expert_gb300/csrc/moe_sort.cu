@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_sort_place_kernel(MoeSortPara
 // once for each device: the kernel may use the shared memory of kMaxKeys keys, and
 // clusters of more than 8 CTAs
 template <typename K>
-cudaError_t allow(K *kernel, bool cluster, unsigned long long *done) {
+cudaError_t allow(K *kernel, bool cluster, DeviceBits *done) {
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);
@@ -276,7 +276,7 @@ uint64_t moe_sort_scratch_words(uint64_t rows, uint32_t n_experts) {
 int moe_sort_launches(uint64_t rows) { return tiles_of(rows, kClusterP) <= kClusterTiles ? 1 : 3; }
 
 cudaError_t prepare_moe_sort(uint64_t rows) {
-    static unsigned long long cluster_done = 0, place_done = 0;
+    static DeviceBits cluster_done{0}, place_done{0};
     if (moe_sort_launches(rows) == 1) return allow(moe_sort_cluster_kernel, true, &cluster_done);
     return allow(moe_sort_place_kernel, false, &place_done);
 }

@@ -610,7 +610,7 @@ void plan_units(PairTcParams *p, int c_tiles, int dw_tiles, int c_cost, int dw_c
 template <typename TC, uint32_t kFmt, int kMode>
 cudaError_t pair_t(const PairTcMaps &maps, PairTcParams p, int num_sms, cudaStream_t s) {
     constexpr int kTileN = Shape<kMode>::kTileN;
-    static unsigned long long attr_set = 0;  // one bit per device
+    static DeviceBits attr_set{0};
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);

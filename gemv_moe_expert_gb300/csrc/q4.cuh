@@ -841,7 +841,7 @@ cudaError_t launch_nt(const Q4Params &p, int num_sms, cudaStream_t s) {
     const int64_t wr = kWarps / wk;
     const int bytes = kZeroBytes + lines * kPitchPad + cfg.slab * per_block;
 
-    static unsigned long long done = 0;  // devices on which the kernel may use its shared memory
+    static DeviceBits done{0};  // devices on which the kernel may use its shared memory
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__((kGemvWarps + 1) * 32, 1) gemv_stream_kernel(G
 // one attribute call per (kernel, device): `done` is the caller's own flag
 // set, one per kernel (kernels of the same signature share a K)
 template <typename K>
-cudaError_t set_smem_once(K kernel, uint32_t bytes, unsigned long long &done) {
+cudaError_t set_smem_once(K kernel, uint32_t bytes, DeviceBits &done) {
     int dev = 0;
     cudaGetDevice(&dev);
     const unsigned long long bit = 1ull << (dev & 63);
@@ -325,7 +325,7 @@ cudaError_t gemv_stream_t(const GemvParams &p, int num_sms, cudaStream_t s) {
     const int rp = static_cast<int>(kSlotBytes / row_bytes);
     const int64_t pieces = (p.rows + rp - 1) / rp;
     const int64_t grid = pieces < num_sms ? pieces : num_sms;
-    static unsigned long long done = 0;
+    static DeviceBits done{0};
     cudaError_t e = set_smem_once(gemv_stream_kernel<T>, kStreamSmem, done);
     if (e != cudaSuccess) return e;
     gemv_stream_kernel<T><<<static_cast<unsigned>(grid), (kGemvWarps + 1) * 32, kStreamSmem, s>>>(p, rp);

@@ -75,6 +75,36 @@ def test_serve_replays_from_a_graph(example):
     assert torch.equal(y, want)
 
 
+def test_host_threads_at_once(example):
+    """Four host threads, a stream each, whose first calls of every kernel of the block meet."""
+    import threading
+    sizes = [(9, 256, 320), (70, 256, 320), (300, 520, 264), (1, 512, 264)]
+    blocks = [example.FeedForward(h, i, torch.float16) for _, h, i in sizes]
+    xs = [torch.randn(m, h, device="cuda").half() for m, h, _ in sizes]
+    torch.cuda.synchronize()
+    gate, got, failed = threading.Barrier(len(sizes)), [None] * len(sizes), []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                gate.wait(30)
+                y, kept = blocks[i].forward(xs[i])
+                got[i] = (y, *blocks[i].backward(kept, xs[i]), blocks[i].serve(xs[i]))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sizes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for block, x, out in zip(blocks, xs, got):
+        y, kept = block.forward(x)
+        assert all(torch.equal(a, b) for a, b in zip(out, (y, *block.backward(kept, x), block.serve(x))))
+
+
 def test_example_runs(example, capsys):
     example.main()
     assert "replayed from a graph" in capsys.readouterr().out
