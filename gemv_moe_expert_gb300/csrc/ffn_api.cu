@@ -402,10 +402,7 @@ gbmm_status gbmm_gated_backward(gbmm_dtype dt, uint32_t activation, int64_t m, i
     if (dt == GBMM_F32) {
         const SumGemmParams px{{g.d[0], g.d[1]}, {w_gate, w_up}, d_x, m, k, n, ldd, ldw, ld_dx};
         const OuterGemmParams pw{x, {g.d[0], g.d[1]}, {dw[0], dw[1]}, m, n, k, ldx, ldd, ld_dw};
-        int launches = 0;
-        st = finish_launch(launch_gated_products_simt(need_x ? &px : nullptr, need_w ? &pw : nullptr, &launches, s), fn, s);
-        for (; st == GBMM_OK && launches > 1; --launches) st = finish_launch(cudaSuccess, fn, s);
-        return st;
+        return finish_launch(launch_gated_products_simt(need_x ? &px : nullptr, need_w ? &pw : nullptr, s), fn, s);
     }
     if (few) st = finish_launch(launch_sum_few(dt, tokens, few_maps, fp, s), fn, s);
     if (st != GBMM_OK || !(q.need_c || q.need_dw)) return st;
@@ -547,6 +544,16 @@ gbmm_status gbmm_test_few_plan(int form, int64_t m, int64_t n, int64_t k, int32_
     plan[1] = p.ksplit;
     plan[2] = static_cast<int32_t>(p.tmem_cols);
     plan[3] = few_tc_ctas_per_sm(codes, plan[0]);
+    return GBMM_OK;
+}
+
+gbmm_status gbmm_test_gradient_plan(int64_t m, int64_t n, int64_t k, int need_x, int need_w, int32_t sms,
+                                    int32_t plan[4]) {
+    record_error(GBMM_OK, "");
+    if (m < 1 || n < 1 || k < 1 || !in_range(m) || !in_range(n) || !in_range(k) || (!need_x && !need_w) || sms < 1 ||
+        plan == nullptr)
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "gbmm_test_gradient_plan: nothing asked for, size out of range, or plan is null");
+    gated_products_simt_plan(m, n, k, need_x != 0, need_w != 0, sms, plan);
     return GBMM_OK;
 }
 

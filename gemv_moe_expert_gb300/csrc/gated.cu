@@ -572,39 +572,18 @@ __device__ __forceinline__ void outer_tile(const TileArgs &t, const OuterOut &o,
         }
 }
 
-template <int kTM, int kTN>
-__global__ void __launch_bounds__(256, 2) sum_gemm_simt_kernel(const TileArgs t, float *out, int64_t ldc) {
-    __shared__ __align__(16) typename TileProduct<float, kSum, kTM, kTN>::Smem sm;
-    sum_tile<kTM, kTN, false>(t, out, ldc, blockIdx.x, 0, 1, sm);
-}
-template <int kTM, int kTN>
-__global__ void __launch_bounds__(256, 2) outer_gemm_simt_kernel(const TileArgs t, const OuterOut o) {
-    __shared__ __align__(16) typename TileProduct<float, kOuter, kTM, kTN>::Smem sm;
-    outer_tile<kTM, kTN, false>(t, o, blockIdx.x, 0, 1, sm);
-}
-// Both gradients in one grid, so that the tiles of one fill the last round of the other's: clusters of two,
-// the first x_blocks of them the gradient of x (the longer tiles), a pair a tile.
-__global__ void __launch_bounds__(256, 2)
-both_gemm_simt_kernel(const TileArgs tx, float *out, int64_t ldc, unsigned x_blocks, const TileArgs tw, const OuterOut o,
-                      unsigned w_blocks) {
-    __shared__ __align__(16) union {
-        typename TileProduct<float, kSum, 8, 8>::Smem x;
-        typename TileProduct<float, kOuter, 8, 4>::Smem w;
-    } sm;
-    if (blockIdx.x < x_blocks) sum_tile<8, 8, true>(tx, out, ldc, blockIdx.x >> 1, blockIdx.x & 1, 2, sm.x);
-    else if (blockIdx.x - x_blocks < w_blocks) outer_tile<8, 4, false>(tw, o, blockIdx.x - x_blocks, 0, 1, sm.w);
-}
-// The same where the tiles would not fill the SMs: small ones, in clusters of `parts` that divide the contraction of one
-// tile (x_split, w_split) or take a tile each; the side with the longer chains first.
-struct SmallGrid {
+// Both gradients in one grid, so that the tiles of one fill the places that the other's leave.  Clusters of `parts` divide
+// the contraction of one tile (x_split, w_split) or take a tile each; the side with the longer chains comes first.
+struct GradGrid {
     unsigned x_tiles, w_tiles, parts, x_blocks, w_blocks;
     int32_t x_split, w_split, w_first;
 };
+template <int kXM, int kXN, int kWM, int kWN>
 __global__ void __launch_bounds__(256, 2)
-both_small_simt_kernel(const TileArgs tx, float *out, int64_t ldc, const TileArgs tw, const OuterOut o, const SmallGrid g) {
+gradients_simt_kernel(const TileArgs tx, float *out, int64_t ldc, const TileArgs tw, const OuterOut o, const GradGrid g) {
     __shared__ __align__(16) union {
-        typename TileProduct<float, kSum, 4, 4>::Smem x;
-        typename TileProduct<float, kOuter, 4, 4>::Smem w;
+        typename TileProduct<float, kSum, kXM, kXN>::Smem x;
+        typename TileProduct<float, kOuter, kWM, kWN>::Smem w;
     } sm;
     const unsigned first = g.w_first ? g.w_blocks : g.x_blocks;
     const bool is_x = (blockIdx.x < first) != (g.w_first != 0);
@@ -614,11 +593,11 @@ both_small_simt_kernel(const TileArgs tx, float *out, int64_t ldc, const TileArg
     const int rank = split ? static_cast<int>(block % g.parts) : 0, parts = static_cast<int>(g.parts);
     if (tile >= (is_x ? g.x_tiles : g.w_tiles)) return;
     if (is_x) {
-        if (split) sum_tile<4, 4, true>(tx, out, ldc, tile, rank, parts, sm.x);
-        else sum_tile<4, 4, false>(tx, out, ldc, tile, 0, 1, sm.x);
+        if (split) sum_tile<kXM, kXN, true>(tx, out, ldc, tile, rank, parts, sm.x);
+        else sum_tile<kXM, kXN, false>(tx, out, ldc, tile, 0, 1, sm.x);
     } else {
-        if (split) outer_tile<4, 4, true>(tw, o, tile, rank, parts, sm.w);
-        else outer_tile<4, 4, false>(tw, o, tile, 0, 1, sm.w);
+        if (split) outer_tile<kWM, kWN, true>(tw, o, tile, rank, parts, sm.w);
+        else outer_tile<kWM, kWN, false>(tw, o, tile, 0, 1, sm.w);
     }
 }
 
@@ -673,35 +652,121 @@ bool large_tiles(unsigned large, unsigned small, unsigned small_cost) {
                                             static_cast<uint64_t>((small + sms - 1) / sms) * small_cost);
 }
 
-// How few tiles are divided: what counts is the longest chain of steps (0.3 us each) of any block, the exchange in a
-// cluster as kJoin steps.  Blocks beyond two an SM (an eighth fewer in large clusters, which lie within groups of 16 to 20
-// SMs) wait for a place, as long as an average one.  m x n x k 21 x 640 x 64: 13.9 us, and 57 undivided; 4000 x 128 x 256:
-// 47 and 267; 256 x 512 x 512: 25 and 63.
-SmallGrid small_grid(unsigned x_tiles, unsigned w_tiles, int64_t x_steps, int64_t w_steps) {
-    constexpr int64_t kJoin = 8;
-    SmallGrid best{};
-    int64_t least = -1;
-    for (unsigned parts = 1; parts <= 8; ++parts) {
-        const int64_t places = (parts > 4 ? 14 : 16) * static_cast<int64_t>(device_sm_count()) / 8;
+// The ways to divide the tiles of both gradients: clusters of one to eight CTAs, either or both kinds divided.  Calls
+// time(grid, steps of a block of x, of w) for each, and returns the grid of the least.
+template <typename Time>
+GradGrid least_grid(unsigned x_tiles, unsigned w_tiles, int64_t x_steps, int64_t w_steps, int64_t x_join, int64_t w_join,
+                    int64_t *least, Time time) {
+    GradGrid best{};
+    *least = -1;
+    for (unsigned parts = 1; parts <= 8; ++parts)
         for (int split = parts > 1 ? 1 : 0; split < (parts > 1 ? 4 : 1); ++split) {
             const int xs = split & 1, ws = split >> 1;
             if ((xs && x_tiles == 0) || (ws && w_tiles == 0)) continue;
             auto blocks = [&](unsigned tiles, int divided) {
-                return divided ? tiles * parts : (tiles + parts - 1) / parts * parts;
+                return divided ? static_cast<int64_t>(tiles) * parts
+                               : (static_cast<int64_t>(tiles) + parts - 1) / parts * parts;
             };
-            const int64_t xc = x_tiles ? (xs ? (x_steps + parts - 1) / parts + kJoin : x_steps) : 0;
-            const int64_t wc = w_tiles ? (ws ? (w_steps + parts - 1) / parts + kJoin : w_steps) : 0;
-            SmallGrid g{x_tiles, w_tiles, parts, blocks(x_tiles, xs), blocks(w_tiles, ws), xs, ws, wc > xc};
-            const int64_t count = static_cast<int64_t>(g.x_blocks) + g.w_blocks, all = g.x_blocks * xc + g.w_blocks * wc;
-            const int64_t time = std::max(xc, wc) + (count > places ? all / count * ((count - 1) / places) : 0);
-            if (least < 0 || time < least) {
-                least = time;
+            const int64_t xb = blocks(x_tiles, xs), wb = blocks(w_tiles, ws);
+            if (xb + wb > INT32_MAX) continue;
+            GradGrid g{x_tiles, w_tiles, parts, static_cast<unsigned>(xb), static_cast<unsigned>(wb), xs, ws, 0};
+            const int64_t t = time(g, x_tiles == 0 ? 0 : xs ? (x_steps + parts - 1) / parts + x_join : x_steps,
+                                   w_tiles == 0 ? 0 : ws ? (w_steps + parts - 1) / parts + w_join : w_steps);
+            if (*least < 0 || t < *least) {
+                *least = t;
                 best = g;
             }
         }
-    }
     return best;
 }
+
+// Few tiles: what counts is the longest chain of steps (0.3 us each) of any block, the exchange in a cluster as kJoin
+// steps.  Blocks beyond two an SM (an eighth fewer in large clusters, which lie within groups of 16 to 20 SMs) wait for a
+// place, as long as an average one.  m x n x k 21 x 640 x 64: 13.9 us, and 57 undivided; 4000 x 128 x 256: 47 and 267;
+// 256 x 512 x 512: 25 and 63.
+GradGrid few_tiles_grid(unsigned x_tiles, unsigned w_tiles, int64_t x_steps, int64_t w_steps, int64_t sms) {
+    constexpr int64_t kJoin = 8;
+    int64_t least;
+    return least_grid(x_tiles, w_tiles, x_steps, w_steps, kJoin, kJoin, &least, [&](GradGrid &g, int64_t xc, int64_t wc) {
+        const int64_t places = (g.parts > 4 ? 14 : 16) * sms / 8;
+        const int64_t count = static_cast<int64_t>(g.x_blocks) + g.w_blocks, all = g.x_blocks * xc + g.w_blocks * wc;
+        g.w_first = wc > xc;
+        return std::max(xc, wc) + (count > places ? all / count * ((count - 1) / places) : 0);
+    });
+}
+
+// What a tile's step of the contraction takes of an SM in ns (8 to 16 tiles of one kind an SM), and the exchange in a
+// cluster in such steps.
+struct StepCost {
+    int64_t x, w, x_join, w_join;
+};
+constexpr StepCost kLargeSteps{1577, 1394, 3, 4}, kSmallSteps{554, 819, 3, 5};
+
+// Many tiles: the longer chains begin, one after the other on each SM (two at once take twice as long), and the others go
+// wherever an SM is done first.  m x n x k, against pairs on the gradient of x and the weights' undivided behind it: 26 x
+// 9664 x 384 107 us and 1008; 6605 x 192 x 320 105 and 699; 2346 x 892 x 686 307 and 522; 7297 x 256 x 2944 825 and 1762;
+// 512 x 1408 x 2048, where the two are the same, 238.
+GradGrid many_tiles_grid(unsigned x_tiles, unsigned w_tiles, int64_t x_steps, int64_t w_steps, const StepCost &cost,
+                         int64_t sms, int64_t *least) {
+    return least_grid(x_tiles, w_tiles, x_steps, w_steps, cost.x_join, cost.w_join, least,
+                      [&](GradGrid &g, int64_t x_chain, int64_t w_chain) {
+        // a block's time, with a step for its beginning and end
+        const int64_t xc = x_tiles ? cost.x * (x_chain + 1) : 0, wc = w_tiles ? cost.w * (w_chain + 1) : 0;
+        g.w_first = wc > xc;
+        const int64_t count = static_cast<int64_t>(g.x_blocks) + g.w_blocks, n1 = g.w_first ? g.w_blocks : g.x_blocks;
+        const int64_t n2 = count - n1, c1 = std::max(xc, wc), c2 = std::min(xc, wc);
+        const int64_t over = n1 % sms, low = n1 / sms * c1, high = low + (over > 0 ? c1 : 0);
+        int64_t t = high;
+        if (n2 > 0) {
+            auto ended = [&](int64_t at) {
+                return (sms - over) * ((at - low) / c2) + over * (at > high ? (at - high) / c2 : 0);
+            };
+            t = std::max(t, low + c2);
+            while (ended(t) < n2) t += std::max(c2 / 2, (n2 - ended(t)) / sms * c2);
+        }
+        // One CTA alone does not use an SM up, and clusters of more than four lie two to an SM.  Where the grid is more
+        // than the SMs hold, clusters wait for as many places at once: the odd sizes the longest.
+        t = std::max(t, c1 * (g.parts > 4 ? 17 : 12) / 10);
+        if (4 * count > 7 * sms) t = t * (g.parts <= 2 ? 100 : g.parts == 4 || g.parts == 8 ? 105 : 112) / 100;
+        return t;
+    });
+}
+
+// The launch of the gradients' products by tiles of one size; x null or w null where one of them is not asked for.
+template <int kXM, int kXN, int kWM, int kWN>
+struct GradTiles {
+    TileArgs tx, tw;
+    unsigned x_tiles = 0, w_tiles = 0;
+    int64_t x_steps = 0, w_steps = 0;
+    bool fits = true;
+    GradGrid grid{};
+    GradTiles(const SumGemmParams *x, const OuterGemmParams *w, const TileArgs &x_args, const TileArgs &w_args)
+        : tx(x_args), tw(w_args) {
+        if (x != nullptr) {
+            x_tiles = tile_grid(x->m, x->n, 16 * kXM, 16 * kXN, &tx);
+            x_steps = 2 * ((x->k + kTK - 1) / kTK);
+        }
+        if (w != nullptr) {
+            w_tiles = tile_grid(tw.m, tw.n, 16 * kWM, 16 * kWN, &tw);
+            w_steps = (w->m + kTK - 1) / kTK;
+        }
+        fits = (x == nullptr || x_tiles > 0) && (w == nullptr || w_tiles > 0);
+    }
+    // sets the grid; its time, or -1 where the tiles are too many
+    int64_t plan(const StepCost &cost, int64_t sms) {
+        int64_t time = -1;
+        if (fits) grid = many_tiles_grid(x_tiles, w_tiles, x_steps, w_steps, cost, sms, &time);
+        return time;
+    }
+    cudaError_t launch(float *c, int64_t ldc, const OuterOut &o, cudaStream_t s) {
+        constexpr uint32_t kX = TileProduct<float, kSum, kXM, kXN>::kFoldBytes;
+        constexpr uint32_t kW = TileProduct<float, kOuter, kWM, kWN>::kFoldBytes;
+        if (x_tiles) tx.fold = folds(tx.k, 2, grid.x_split ? grid.parts : 1);
+        if (w_tiles) tw.fold = folds(tw.k, 1, grid.w_split ? grid.parts : 1);
+        return launch_whole(gradients_simt_kernel<kXM, kXN, kWM, kWN>, grid.x_blocks + grid.w_blocks, grid.parts,
+                            (tx.fold | tw.fold) * std::max(kX, kW), s, tx, c, ldc, tw, o, grid);
+    }
+};
 
 template <typename T>
 cudaError_t gated_simt_t(const GatedParams &p, cudaStream_t s) {
@@ -944,69 +1009,68 @@ cudaError_t launch_gated_outer_few(int dt, const GatedGradParams &p, const Outer
     return dt == kF16 ? outer_few_t<__half>(p, w, s) : outer_few_t<__nv_bfloat16>(p, w, s);
 }
 
+namespace {
+
 // The gradients of f32 blocks: x null or w null where one of them is not asked for.
-cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, int *launches, cudaStream_t s) {
-    constexpr uint32_t kLargeX = TileProduct<float, kSum, 8, 8>::kFoldBytes;
-    constexpr uint32_t kSmallX = TileProduct<float, kSum, 4, 4>::kFoldBytes;
-    constexpr uint32_t kLargeW = TileProduct<float, kOuter, 8, 4>::kFoldBytes;
-    constexpr uint32_t kSmallW = TileProduct<float, kOuter, 4, 4>::kFoldBytes;
-    TileArgs tx{}, txs{}, tw{}, tws{};
-    unsigned x_small = 0, x_large = 0, w_small = 0, w_large = 0;
-    OuterOut o{};
-    if (x != nullptr) {
-        tx = TileArgs{{x->a[0], x->a[1]}, {x->b[0], x->b[1]}, x->m, x->n, x->k, x->lda, x->ldb, 0, 0, 0};
-        tx.a_vec = groups_of_4(x->a[0], x->lda, 4) && groups_of_4(x->a[1], x->lda, 4);
-        tx.b_vec = groups_of_4(x->b[0], x->ldb, 4) && groups_of_4(x->b[1], x->ldb, 4);
-        txs = tx;
-        txs.fold = folds(x->k, 2, 1);
-        x_small = tile_grid(x->m, x->n, 64, 64, &txs);
-        x_large = tile_grid(x->m, x->n, 128, 128, &tx);
-        if (x_large == 0) return cudaErrorInvalidConfiguration;
+struct GradPlan {
+    GradTiles<8, 8, 8, 4> large;
+    GradTiles<4, 4, 4, 4> small;
+    bool take_small = false;
+    GradPlan(const SumGemmParams *x, const OuterGemmParams *w, const TileArgs &tx, const TileArgs &tw, int64_t sms)
+        : large(x, w, tx, tw), small(x, w, tx, tw) {
+        // fewer large tiles, those of x in pairs, than SMs
+        if (large.fits && small.fits && 2 * static_cast<int64_t>(large.x_tiles) + large.w_tiles < sms) {
+            small.grid = few_tiles_grid(small.x_tiles, small.w_tiles, small.x_steps, small.w_steps, sms);
+            take_small = true;
+        } else {
+            const int64_t time_large = large.plan(kLargeSteps, sms), time_small = small.plan(kSmallSteps, sms);
+            take_small = time_small >= 0 && time_small < time_large;
+            large.fits = time_large >= 0;
+        }
     }
-    if (w != nullptr) {
-        tw = TileArgs{{w->x, w->x}, {w->d[0], w->d[1]}, w->k, w->n, w->m, w->ldx, w->ldd, 0, 0, 0};
-        tw.a_vec = groups_of_4(w->x, w->ldx, 4);
-        tw.b_vec = groups_of_4(w->d[0], w->ldd, 4) && groups_of_4(w->d[1], w->ldd, 4);
-        tw.fold = folds(w->m, 1, 1);
-        tws = tw;
-        w_small = tile_grid(tw.m, tw.n, 64, 64, &tws);
-        w_large = tile_grid(tw.m, tw.n, 128, 64, &tw);
-        if (w_large == 0) return cudaErrorInvalidConfiguration;
+};
+TileArgs x_args(const SumGemmParams &x) {
+    TileArgs t{{x.a[0], x.a[1]}, {x.b[0], x.b[1]}, x.m, x.n, x.k, x.lda, x.ldb, 0, 0, 0};
+    t.a_vec = groups_of_4(x.a[0], x.lda, 4) && groups_of_4(x.a[1], x.lda, 4);
+    t.b_vec = groups_of_4(x.b[0], x.ldb, 4) && groups_of_4(x.b[1], x.ldb, 4);
+    return t;
+}
+TileArgs w_args(const OuterGemmParams &w) {
+    TileArgs t{{w.x, w.x}, {w.d[0], w.d[1]}, w.k, w.n, w.m, w.ldx, w.ldd, 0, 0, 0};
+    t.a_vec = groups_of_4(w.x, w.ldx, 4);
+    t.b_vec = groups_of_4(w.d[0], w.ldd, 4) && groups_of_4(w.d[1], w.ldd, 4);
+    return t;
+}
+
+}  // namespace
+
+cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, cudaStream_t s) {
+    GradPlan plan(x, w, x != nullptr ? x_args(*x) : TileArgs{}, w != nullptr ? w_args(*w) : TileArgs{}, device_sm_count());
+    if (!plan.large.fits) return cudaErrorInvalidConfiguration;
+    OuterOut o{};
+    if (w != nullptr)
         o = OuterOut{{static_cast<float *>(w->c[0]), static_cast<float *>(w->c[1])},
                      w->ldc,
                      groups_of_4(w->c[0], w->ldc, 4) && groups_of_4(w->c[1], w->ldc, 4)};
-    }
-    float *c = x != nullptr ? static_cast<float *>(x->c) : nullptr;
-    // one grid for both where it has a block for each SM
-    const uint64_t together = 2 * static_cast<uint64_t>(x_large) + w_large + (w_large & 1);
-    *launches = 1;
-    if (x != nullptr && w != nullptr && together >= static_cast<uint64_t>(device_sm_count()) && together <= INT32_MAX) {
-        tx.fold = folds(x->k, 2, 2);
-        static_assert(kLargeX == kLargeW, "one launch for both");
-        return launch_whole(both_gemm_simt_kernel, static_cast<unsigned>(together), 2, (tx.fold | tw.fold) * kLargeX, s, tx, c,
-                            x->ldc, 2 * x_large, tw, o, w_large);
-    }
-    if (together < static_cast<uint64_t>(device_sm_count()) && (x == nullptr || x_small > 0) && (w == nullptr || w_small > 0)) {
-        const SmallGrid g = small_grid(x_small, w_small, x != nullptr ? 2 * ((x->k + kTK - 1) / kTK) : 0,
-                                       w != nullptr ? (w->m + kTK - 1) / kTK : 0);
-        if (x != nullptr) txs.fold = folds(x->k, 2, g.x_split ? g.parts : 1);
-        if (w != nullptr) tws.fold = folds(w->m, 1, g.w_split ? g.parts : 1);
-        static_assert(kSmallX <= kSmallW, "one launch for both");
-        return launch_whole(both_small_simt_kernel, g.x_blocks + g.w_blocks, g.parts, (txs.fold | tws.fold) * kSmallW, s, txs,
-                            c, x != nullptr ? x->ldc : int64_t{0}, tws, o, g);
-    }
-    if (x != nullptr) {
-        tx.fold = txs.fold;
-        const cudaError_t e =
-            large_tiles(x_large, x_small, 8)
-                ? launch_whole(sum_gemm_simt_kernel<8, 8>, x_large, 1, tx.fold * kLargeX, s, tx, c, x->ldc)
-                : launch_whole(sum_gemm_simt_kernel<4, 4>, x_small, 1, tx.fold * kSmallX, s, txs, c, x->ldc);
-        if (e != cudaSuccess || w == nullptr) return e;
-        *launches = 2;
-    }
-    return large_tiles(w_large, w_small, 12)
-               ? launch_whole(outer_gemm_simt_kernel<8, 4>, w_large, 1, tw.fold * kLargeW, s, tw, o)
-               : launch_whole(outer_gemm_simt_kernel<4, 4>, w_small, 1, tw.fold * kSmallW, s, tws, o);
+    float *const c = x != nullptr ? static_cast<float *>(x->c) : nullptr;
+    const int64_t ldc = x != nullptr ? x->ldc : 0;
+    return plan.take_small ? plan.small.launch(c, ldc, o, s) : plan.large.launch(c, ldc, o, s);
+}
+
+// tile: the edge of a tile of x (weights: as many columns, and 64 rows); grid: CTAs that divide a tile of x, of the weights
+// (1: undivided), whether the weights' come first
+void gated_products_simt_plan(int64_t m, int64_t n, int64_t k, bool need_x, bool need_w, int64_t sms, int32_t plan[4]) {
+    SumGemmParams x{};
+    OuterGemmParams w{};
+    x.m = w.m = m;
+    x.n = w.k = k;
+    x.k = w.n = n;
+    const GradPlan p(need_x ? &x : nullptr, need_w ? &w : nullptr, x_args(x), w_args(w), sms);
+    const GradGrid &g = p.take_small ? p.small.grid : p.large.grid;
+    plan[0] = p.take_small ? 64 : 128;
+    plan[1] = g.x_split ? static_cast<int32_t>(g.parts) : 1;
+    plan[2] = g.w_split ? static_cast<int32_t>(g.parts) : 1;
+    plan[3] = g.w_first;
 }
 
 // ldd and cols the same in all three; rows 0: nothing to do

@@ -705,6 +705,16 @@ GBMM_API gbmm_status gbmm_test_static_scratch_copy(void *dst, uint64_t bytes, gb
  */
 GBMM_API gbmm_status gbmm_test_few_plan(int form, int64_t m, int64_t n, int64_t k, int32_t sms, int32_t plan[4]);
 
+/*
+ * gbmm_test_gradient_plan -- how the products of an f32 gbmm_gated_backward would be divided on a
+ * GPU of `sms` SMs; nothing is launched.  need_x, need_w: which gradients are asked for.  plan: edge
+ * of a tile of d_x (128 or 64; the weights' tiles are as wide, and 64 rows high, of both weights),
+ * CTAs that divide the contraction of one tile of d_x, the same of the weights', and whether the
+ * weights' tiles come first.
+ */
+GBMM_API gbmm_status gbmm_test_gradient_plan(int64_t m, int64_t n, int64_t k, int need_x, int need_w, int32_t sms,
+                                             int32_t plan[4]);
+
 #ifdef __cplusplus
 }
 #endif

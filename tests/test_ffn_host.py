@@ -215,3 +215,29 @@ def test_the_long_sums_of_some_tens_of_tokens_take_wide_tiles():
         assert gb.gbmm_test_few_plan(CODES_FORM, m, 3584, 16384, 152)[1][0] == 64
         assert gb.gbmm_test_few_plan(CODES_FORM, m, 3584, 24577, 152)[1][0] == 0
     assert gb.gbmm_test_few_plan(3, 1, 1, 1, 152)[0] == BAD and gb.gbmm_test_few_plan(0, 0, 1, 1, 152)[0] == BAD
+
+
+@pytest.mark.parametrize("need_x,need_w", [(True, True), (True, False), (False, True)])
+def test_no_chain_of_an_f32_gradient_outlasts_an_equal_share(need_x, need_w):
+    """A block's work, in products of a step, against an SM's share of all: at most twice that (two blocks lie on an
+    SM), or a contraction divided by eight, or, where there is little to do, 64 steps of a small tile.
+    Where blocks wait for a place, chains that are much longer come first."""
+    sms = 152
+    for m in (1, 5, 26, 49, 130, 500, 1000, 2346, 4000, 8192):
+        for n in (64, 192, 512, 892, 1408, 3136, 5504, 9664, 11008):
+            for k in (64, 320, 384, 686, 960, 2048, 4096, 11008):
+                st, (edge, x_parts, w_parts, w_first) = gb.gbmm_test_gradient_plan(m, n, k, need_x, need_w, sms)
+                assert st == gb.GBMM_OK and edge in (64, 128) and 1 <= x_parts <= 8 and 1 <= w_parts <= 8
+                x_tiles = -(-m // edge) * -(-k // edge) * need_x
+                w_tiles = -(-n // 64) * -(-k // edge) * need_w
+                x_steps, w_steps = 2 * -(-n // 16), -(-m // 16)
+                x_cost, w_cost = edge * edge, 2 * 64 * edge  # of a step
+                share = (x_tiles * x_steps * x_cost + w_tiles * w_steps * w_cost) / sms
+                x_chain, w_chain = -(-x_steps // x_parts) * x_cost * need_x, -(-w_steps // w_parts) * w_cost * need_w
+                for chain, parts, cost in ((x_chain, x_parts, x_cost), (w_chain, w_parts, w_cost)):
+                    assert chain <= 2 * share or parts == 8 or chain <= 64 * 64 * 64, (m, n, k, edge, x_parts, w_parts)
+                blocks = x_tiles * x_parts + w_tiles * w_parts
+                if need_x and need_w and blocks > 2 * sms and max(x_chain, w_chain) > 2.5 * min(x_chain, w_chain):
+                    assert w_first == (w_chain > x_chain), (m, n, k)
+    assert gb.gbmm_test_gradient_plan(1, 1, 1, False, False, sms)[0] == BAD
+    assert gb.gbmm_test_gradient_plan(0, 1, 1, True, True, sms)[0] == BAD

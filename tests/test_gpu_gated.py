@@ -526,3 +526,21 @@ def test_outputs_whose_rows_tma_can_and_cannot_write(dtype, m, n, k, pad_h, pad_
                 outs["first"] = got
             assert all(np.array_equal(a, c) for a, c in zip(outs["first"], got))
     assert gb.gbmm_device_error()[0] == gb.GBMM_OK
+
+
+F32_PLANS = [(26, 9664, 64), (2346, 892, 300), (3000, 64, 1400), (1000, 1100, 515), (132, 3000, 420), (2444, 192, 1100),
+             (6605, 70, 200), (700, 1546, 1200), (5, 700, 5003)]
+
+
+@pytest.mark.parametrize("m,n,k", F32_PLANS)
+@pytest.mark.parametrize("d_x,d_w,pad", [(True, True, 0), (True, True, 3), (True, False, 0), (False, True, 0)])
+def test_f32_gradients_however_they_are_divided(m, n, k, d_x, d_w, pad):
+    b = Block("f32", m, n, k, pad=pad)
+    b.check_backward("silu", b.backward("silu", d_x, d_w))
+
+
+def test_f32_gradients_are_divided_in_different_ways():
+    plans = {gb.gbmm_test_gradient_plan(*s, True, True, torch.cuda.get_device_properties(0).multi_processor_count)[1]
+             for s in F32_PLANS}
+    assert len({p[0] for p in plans}) == 2 and len({p[1] for p in plans}) > 2 and len({p[2] for p in plans}) > 2
+    assert len({p[3] for p in plans}) == 2
