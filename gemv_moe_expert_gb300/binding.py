@@ -53,7 +53,7 @@ EXPORTS = (
     "gbmm_moe_combine_backward", "gbmm_gemv_q4", "gbmm_matmul_id_q4",
     "gbmm_gated", "gbmm_gated_scratch_bytes", "gbmm_gated_backward", "gbmm_gated_backward_scratch_bytes",
     "gbmm_quantize_i8", "gbmm_gemm_i8", "gbmm_gemm_i8_scratch_bytes",
-    "gbmm_test_few_plan", "gbmm_test_gradient_plan",
+    "gbmm_test_few_plan", "gbmm_test_gradient_plan", "gbmm_test_gated_plan",
 )
 
 # n_experts * m * 4 bytes of routed rows fit the fixed scratch of
@@ -174,6 +174,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
                 ("gbmm_quantize_i8", [i32, i64, i64, vp, i64, vp, i64, vp, vp]),
                 ("gbmm_gemm_i8_scratch_bytes", [i64, i64, i64, i32, ctypes.POINTER(u64)]),
                 ("gbmm_test_few_plan", [i32, i64, i64, i64, i32, ctypes.POINTER(i32)]),
+                ("gbmm_test_gated_plan", [i64, i64, i64, i32, ctypes.POINTER(i32)]),
                 ("gbmm_test_gradient_plan", [i64, i64, i64, i32, i32, i32, ctypes.POINTER(i32)]),
                 ("gbmm_gemm_i8", [i32, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, u64, vp])):
             getattr(lib, name).argtypes = args
@@ -461,6 +462,13 @@ def gbmm_test_gradient_plan(m: int, n: int, k: int, need_x: bool, need_w: bool, 
     """Returns (status, (edge of a tile of d_x, CTAs that divide it, CTAs that divide one of the weights', weights first))."""
     plan = (ctypes.c_int32 * 4)()
     st = load().gbmm_test_gradient_plan(m, n, k, int(bool(need_x)), int(bool(need_w)), sms, plan)
+    return st, tuple(plan)
+
+
+def gbmm_test_gated_plan(m: int, n: int, k: int, sms: int):
+    """Returns (status, (height of a tile, CTAs that divide it))."""
+    plan = (ctypes.c_int32 * 2)()
+    st = load().gbmm_test_gated_plan(m, n, k, sms, plan)
     return st, tuple(plan)
 
 

@@ -557,4 +557,12 @@ gbmm_status gbmm_test_gradient_plan(int64_t m, int64_t n, int64_t k, int need_x,
     return GBMM_OK;
 }
 
+gbmm_status gbmm_test_gated_plan(int64_t m, int64_t n, int64_t k, int32_t sms, int32_t plan[2]) {
+    record_error(GBMM_OK, "");
+    if (m <= kDotRows || n < 1 || k < 0 || !in_range(m) || !in_range(n) || !in_range(k) || sms < 1 || plan == nullptr)
+        return fail(GBMM_ERR_INVALID_ARGUMENT, "gbmm_test_gated_plan: size out of range, or plan is null");
+    gated_simt_plan(m, n, k, sms, plan);
+    return GBMM_OK;
+}
+
 }  // extern "C"

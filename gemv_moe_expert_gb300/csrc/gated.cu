@@ -642,16 +642,6 @@ unsigned tile_grid(int64_t m, int64_t n, int bm, int bn, TileArgs *t) {
     return blocks > INT32_MAX ? 0 : static_cast<unsigned>(blocks);
 }
 
-// Whether the larger of two tiles is taken.  A tile's time goes by its reads of shared memory, one cycle for each 4
-// bytes a thread reads: 16 a step of k for 128 x 64 outputs of two products or 128 x 128 of one (which is also
-// what their FMAs take), 12 for 64 x 64 of two and 8 for 64 x 64 of one, and a tenth more for storing them.  The
-// last round of blocks counts whole: 512 x 1408 x 2048 two products 88 / 176 blocks, 143 / 232 us.
-bool large_tiles(unsigned large, unsigned small, unsigned small_cost) {
-    const unsigned sms = static_cast<unsigned>(device_sm_count());
-    return large != 0 && (small == 0 || static_cast<uint64_t>((large + sms - 1) / sms) * 16 <=
-                                            static_cast<uint64_t>((small + sms - 1) / sms) * small_cost);
-}
-
 // The ways to divide the tiles of both gradients: clusters of one to eight CTAs, either or both kinds divided.  Calls
 // time(grid, steps of a block of x, of w) for each, and returns the grid of the least.
 template <typename Time>
@@ -768,32 +758,78 @@ struct GradTiles {
     }
 };
 
+// Clusters lie within groups of SMs: CTAs in clusters of 1 to 8 that run at once, of two and of one for each SM, in
+// percent (cudaOccupancyMaxActiveClusters).
+constexpr int kPairPlaces[9] = {0, 100, 100, 95, 97, 95, 90, 87, 94}, kSinglePlaces[9] = {0, 100, 100, 90, 94, 92, 90, 69, 78};
+
+// How many CTAs share a tile of a gated projection, and the time that comes to in ns.  step: what a step of the contraction
+// takes of an SM; join: steps of the exchange in a cluster, beside half a step for each CTA.
+struct GatedGrid {
+    int64_t time = -1;
+    unsigned parts = 1;
+};
+GatedGrid gated_grid(unsigned tiles, int64_t steps, int64_t step, int64_t join, int64_t sms) {
+    GatedGrid best;
+    for (unsigned parts = 1; parts <= 8 && tiles > 0; ++parts) {
+        const int64_t count = static_cast<int64_t>(tiles) * parts;
+        if (count > INT32_MAX) break;
+        const int64_t pairs = 2 * sms * kPairPlaces[parts] / 100, singles = sms * kSinglePlaces[parts] / 100;
+        // where CTAs wait for a place, half of an exchange runs under another tile
+        const int64_t exchange = parts > 1 ? (2 * join + parts) / (count > pairs ? 4 : 2) : 0;
+        const int64_t chain = step * (1 + (steps + parts - 1) / parts + exchange);
+        // in fifths of a chain: one CTA alone does not use an SM up, two beside each other take twice as long
+        auto round = [&](int64_t blocks) { return blocks <= singles ? 6 : 10; };
+        int64_t t;
+        if (count <= pairs) {
+            t = chain * round(count) / 5;
+        } else if (count <= 3 * sms) {
+            t = chain * (10 + round(count - pairs)) / 5;
+        } else {
+            // after four rounds the SMs are apart enough for half of the last one to be filled
+            t = chain * ((count + sms - 1) / sms);
+            if (count > 4 * sms) t = std::min(t, chain * count / sms + chain / 2);
+            if (parts == 3 || (parts > 4 && parts < 8)) t = t * 112 / 100;  // which find as many places at once rarely
+        }
+        if (best.time < 0 || t < best.time) best = GatedGrid{t, parts};
+    }
+    return best;
+}
+
+// Tiles 128 rows high or 64, and the CTAs that share one; blocks: 0 where there are too many.  m x n x k, against tiles
+// that were divided only where they were at most one an SM: 10 x 5795 x 2512 198 -> 100 us, 512 x 1408 x 2048 178 -> 137,
+// 512 x 2816 x 2048 367 -> 253, 6469 x 231 x 7616 1383 -> 1070, 454 x 145 x 25 9.5 -> 6.5.
+struct GatedPlan {
+    bool high = true;
+    unsigned parts = 1, blocks = 0;
+    GatedPlan(int64_t m, int64_t n, int64_t k, int64_t sms) {
+        TileArgs t{};
+        const unsigned large = tile_grid(m, n, 128, 64, &t), small = tile_grid(m, n, 64, 64, &t);
+        const int64_t steps = (k + kTK - 1) / kTK;
+        const GatedGrid by_large = gated_grid(large, steps, 1394, 4, sms), by_small = gated_grid(small, steps, 819, 2, sms);
+        if (by_large.time < 0) return;
+        high = by_small.time < 0 || by_large.time <= by_small.time;
+        parts = high ? by_large.parts : by_small.parts;
+        blocks = parts * (high ? large : small);
+    }
+};
+
 template <typename T>
 cudaError_t gated_simt_t(const GatedParams &p, cudaStream_t s) {
     TileArgs t{{p.x, p.x}, {p.w[0], p.w[1]}, p.m, p.n, p.k, p.ldx, p.ldw, 0, 0, 0};
     t.a_vec = groups_of_4(p.x, p.ldx, sizeof(T));
     t.b_vec = groups_of_4(p.w[0], p.ldw, sizeof(T)) && groups_of_4(p.w[1], p.ldw, sizeof(T));
-    const unsigned small = tile_grid(p.m, p.n, 64, 64, &t), large = tile_grid(p.m, p.n, 128, 64, &t);
-    if (large == 0) return cudaErrorInvalidConfiguration;
-    const unsigned sms = static_cast<unsigned>(device_sm_count());
-    constexpr uint32_t kSmall = TileProduct<T, kGated, 4, 4>::kFoldBytes, kLarge = TileProduct<T, kGated, 8, 4>::kFoldBytes;
-    // At most one tile an SM: up to eight CTAs share a tile, as many as make the busiest SM's share smallest.
-    // 512 x 1408 x 2048, 88 tiles: 206 us whole, 195 by two, 177 by three.
-    if (large <= sms) {
-        const bool few = 4 * large <= sms;
-        const unsigned tiles = few ? small : large;
-        unsigned parts = 2;
-        for (unsigned q = 3; q <= 8 && p.k >= 256 * static_cast<int64_t>(q); ++q)
-            if (((tiles * q + sms - 1) / sms) * parts < ((tiles * parts + sms - 1) / sms) * q) parts = q;
-        t.parts = parts;
-        t.fold = folds(p.k, 1, parts);
-        return few ? launch_whole(gated_simt_kernel<T, 4, 4, true>, parts * tiles, parts, t.fold * kSmall, s, t, p)
-                   : launch_whole(gated_simt_kernel<T, 8, 4, true>, parts * tiles, parts, t.fold * kLarge, s, t, p);
-    }
-    t.fold = folds(p.k, 1, 1);
-    if (large_tiles(large, small, 12))
-        return launch_whole(gated_simt_kernel<T, 8, 4, false>, large, 1, t.fold * kLarge, s, t, p);
-    return launch_whole(gated_simt_kernel<T, 4, 4, false>, small, 1, t.fold * kSmall, s, t, p);
+    t.tiles_n = (p.n + 63) / 64;
+    const GatedPlan plan(p.m, p.n, p.k, device_sm_count());
+    if (plan.blocks == 0) return cudaErrorInvalidConfiguration;
+    t.parts = plan.parts;
+    t.fold = folds(p.k, 1, t.parts);
+    const uint32_t bytes =
+        t.fold * (plan.high ? TileProduct<T, kGated, 8, 4>::kFoldBytes : TileProduct<T, kGated, 4, 4>::kFoldBytes);
+    if (t.parts > 1)
+        return plan.high ? launch_whole(gated_simt_kernel<T, 8, 4, true>, plan.blocks, t.parts, bytes, s, t, p)
+                         : launch_whole(gated_simt_kernel<T, 4, 4, true>, plan.blocks, t.parts, bytes, s, t, p);
+    return plan.high ? launch_whole(gated_simt_kernel<T, 8, 4, false>, plan.blocks, 1, bytes, s, t, p)
+                     : launch_whole(gated_simt_kernel<T, 4, 4, false>, plan.blocks, 1, bytes, s, t, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -1057,6 +1093,12 @@ cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmPa
     return plan.take_small ? plan.small.launch(c, ldc, o, s) : plan.large.launch(c, ldc, o, s);
 }
 
+// the height of a tile of a gated projection on the FFMA pipe and the CTAs that share one; zeros where there are too many
+void gated_simt_plan(int64_t m, int64_t n, int64_t k, int64_t sms, int32_t plan[2]) {
+    const GatedPlan p(m, n, k, sms);
+    plan[0] = p.blocks == 0 ? 0 : p.high ? 128 : 64;
+    plan[1] = p.blocks == 0 ? 0 : static_cast<int32_t>(p.parts);
+}
 // tile: the edge of a tile of x (weights: as many columns, and 64 rows); grid: CTAs that divide a tile of x, of the weights
 // (1: undivided), whether the weights' come first
 void gated_products_simt_plan(int64_t m, int64_t n, int64_t k, bool need_x, bool need_w, int64_t sms, int32_t plan[4]) {

@@ -345,6 +345,7 @@ cudaError_t launch_gated_simt(int dt, const GatedParams &p, cudaStream_t s);
 cudaError_t launch_gated_grad(int dt, const GatedGradParams &p, cudaStream_t s);
 // f32
 cudaError_t launch_gated_products_simt(const SumGemmParams *x, const OuterGemmParams *w, cudaStream_t s);
+void gated_simt_plan(int64_t m, int64_t n, int64_t k, int64_t sms, int32_t plan[2]);
 void gated_products_simt_plan(int64_t m, int64_t n, int64_t k, bool need_x, bool need_w, int64_t sms, int32_t plan[4]);
 int gated_few_tokens();
 cudaError_t launch_gated_outer_few(int dt, const GatedGradParams &p, const OuterGemmParams &w, cudaStream_t s);

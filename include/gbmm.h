@@ -705,6 +705,11 @@ GBMM_API gbmm_status gbmm_test_static_scratch_copy(void *dst, uint64_t bytes, gb
  */
 GBMM_API gbmm_status gbmm_test_few_plan(int form, int64_t m, int64_t n, int64_t k, int32_t sms, int32_t plan[4]);
 
+/* gbmm_test_gated_plan -- the same for gbmm_gated on the FFMA pipe (f32, more than 8 rows): height of
+ * a tile (64 columns of both projections wide) and CTAs that divide its contraction; zeros where
+ * there would be too many. */
+GBMM_API gbmm_status gbmm_test_gated_plan(int64_t m, int64_t n, int64_t k, int32_t sms, int32_t plan[2]);
+
 /*
  * gbmm_test_gradient_plan -- how the products of an f32 gbmm_gated_backward would be divided on a
  * GPU of `sms` SMs; nothing is launched.  need_x, need_w: which gradients are asked for.  plan: edge

@@ -241,3 +241,23 @@ def test_no_chain_of_an_f32_gradient_outlasts_an_equal_share(need_x, need_w):
                     assert w_first == (w_chain > x_chain), (m, n, k)
     assert gb.gbmm_test_gradient_plan(1, 1, 1, False, False, sms)[0] == BAD
     assert gb.gbmm_test_gradient_plan(0, 1, 1, True, True, sms)[0] == BAD
+
+
+def test_f32_projections_are_divided_about_evenly():
+    """Tiles of 128 or 64 rows (1394 and 819 ns a step), divided over one to eight CTAs (the exchange as six steps): the
+    rounds of the plan taken come to at most 1.4 times the least of all of them, and two steps."""
+    sms = 152
+
+    def time(m, n, k, height, parts):
+        tiles = -(-m // height) * -(-n // 64)
+        steps = -(--(-k // 16) // parts) + (6 if parts > 1 else 0)
+        return -(-tiles * parts // sms) * steps * (1394 if height == 128 else 819)
+
+    for m in (9, 10, 44, 66, 143, 272, 512, 890, 2512, 4356, 6469):
+        for n in (64, 203, 231, 704, 1408, 2816, 4217, 7374, 10169):
+            for k in (25, 64, 512, 1408, 2048, 2512, 4928, 7616):
+                st, (height, parts) = gb.gbmm_test_gated_plan(m, n, k, sms)
+                assert st == gb.GBMM_OK and height in (64, 128) and 1 <= parts <= 8
+                least = min(time(m, n, k, h, p) for h in (64, 128) for p in range(1, 9))
+                assert time(m, n, k, height, parts) <= 1.4 * least + 2 * 1394, (m, n, k, height, parts)
+    assert gb.gbmm_test_gated_plan(8, 1, 1, sms)[0] == BAD

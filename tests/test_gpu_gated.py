@@ -544,3 +544,20 @@ def test_f32_gradients_are_divided_in_different_ways():
              for s in F32_PLANS}
     assert len({p[0] for p in plans}) == 2 and len({p[1] for p in plans}) > 2 and len({p[2] for p in plans}) > 2
     assert len({p[3] for p in plans}) == 2
+
+
+F32_TILES = [(10, 2795, 512), (44, 3169, 300), (707, 216, 656), (512, 1408, 2048), (512, 2816, 1024), (6469, 131, 61),
+             (454, 145, 25), (12, 40, 5000), (1300, 1668, 259)]
+
+
+@pytest.mark.parametrize("m,n,k", F32_TILES)
+@pytest.mark.parametrize("pad", [0, 3])
+def test_f32_projections_however_they_are_divided(m, n, k, pad):
+    b = Block("f32", m, n, k, pad=pad)
+    b.check_forward("gelu", b.forward("gelu", save=True))
+
+
+def test_f32_projections_are_divided_in_different_ways():
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    plans = {gb.gbmm_test_gated_plan(*s, sms)[1] for s in F32_TILES}
+    assert {p[0] for p in plans} == {64, 128} and len({p[1] for p in plans}) > 3
