@@ -529,7 +529,8 @@ GBMM_API gbmm_status gbmm_matmul_id_q4(gbmm_dtype dt, uint32_t m, int64_t n, int
  * same ldw, both saved projections with the same ld_saved, both weights' gradients
  * with the same ld_dw; two of them may lie side by side in rows of that pitch).
  * m, n and k below 2^31.  Sums are f32 in a fixed order, activations are off by at most
- * 2^-20 of their argument, and each output is rounded once.  Pointers must be aligned to
+ * 2^-20 of their argument (and 2^-14 of themselves down to f32's smallest normal values),
+ * and each output is rounded once.  Pointers must be aligned to
  * their elements, and outputs must not overlap inputs, scratch or each other
  * (GBMM_ERR_OVERLAP).
  */

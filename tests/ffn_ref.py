@@ -6,6 +6,7 @@ import math
 import numpy as np
 
 _erf = np.vectorize(math.erf, otypes=[np.float64])
+erfc = np.vectorize(math.erfc, otypes=[np.float64])
 C = math.sqrt(2 / math.pi)
 ACTS = ("silu", "gelu", "gelu_tanh", "relu")
 

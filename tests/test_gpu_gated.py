@@ -561,3 +561,80 @@ def test_f32_projections_are_divided_in_different_ways():
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     plans = {gb.gbmm_test_gated_plan(*s, sms)[1] for s in F32_TILES}
     assert {p[0] for p in plans} == {64, 128} and len({p[1] for p in plans}) > 3
+
+
+def exact_gates(dtype, act):
+    """Gates of the type's own values over the range in which the activation's far ends are normal numbers in f32."""
+    most = {"gelu_tanh": 9.0, "relu": 100.0}.get(act, 12.0)
+    v = np.concatenate([np.linspace(-most, most, 997), np.linspace(-1, 1, 203)])
+    return strided(v[None, :], v.size, dtype)[2][0]
+
+
+def activation_bound(act, v):
+    """What evaluating the activation may be off by, relative to v times its sigmoid (or normal distribution): 2^-18, and
+    the rounding of the exponent in front of the exponential, four steps of its own size (gelu v^2 / 2; silu v; the tanh
+    form its argument)."""
+    exponent = {"gelu": v * v / 2, "silu": np.abs(v), "gelu_tanh": 2 * ffn_ref.C * np.abs(v + 0.044715 * v ** 3),
+                "relu": 0 * v}[act]
+    return 2.0 ** -18 + 8 * U * exponent
+
+
+@pytest.mark.parametrize("act", ffn_ref.ACTS)
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,pad", [(3, 0), (40, 0), (300, 0), (300, 1)])
+def test_far_ends_of_activations(m, pad, dtype, act):
+    """Rows of x pick single columns of w_gate, and w_up is 1, so that h is the activation of exact gates: off by half a
+    step and activation_bound() relative to h itself, whichever way the number of rows takes."""
+    v = exact_gates(dtype, act)
+    n, k = v.size // 8, 8
+    b = Block(dtype, m, n, k, pad=pad)
+    x = np.zeros((m, k))
+    x[np.arange(m), np.arange(m) % k] = 1
+    xb, xp, _ = strided(x, b.ldk, dtype, fill=0.0)
+    gate = v.reshape(k, n)
+    gb_, gp, _ = strided(gate.T, b.ldk, dtype, fill=0.0)
+    ub, up, _ = strided(np.ones((n, k)), b.ldk, dtype, fill=0.0)
+    h = empty(m, n, dtype, 0)
+    sb, need = scratch_for(gb.gbmm_gated_scratch_bytes, dtype, m, n, k)
+    gb.check(gb.gbmm_gated(dtype, CODE[act], m, n, k, xp, b.ldk, gp, up, b.ldk, h[1], n, None, None, 0, sb.ptr, need))
+    g = gate[np.arange(m) % k]
+    want = ffn_ref.act(act, g) if act != "gelu" else 0.5 * g * ffn_ref.erfc(-g / 2 ** 0.5)
+    if act == "gelu_tanh":
+        want = g * ffn_ref._sigmoid(2 * ffn_ref.C * (g + 0.044715 * g ** 3))
+    tol = np.abs(want) * (UO[dtype] + activation_bound(act, g) * (1 + UO[dtype])) + TINY[dtype]
+    near(fetch(h[0], m, n, n, dtype, 0), want, tol, "h")
+
+
+@pytest.mark.parametrize("act", ffn_ref.ACTS)
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m", [4, 40, 300])
+def test_far_ends_of_slopes(m, dtype, act):
+    """d_h and up of 1 and rows of x that pick single columns: the weights' gradients are the slopes and the activations
+    of exact gates, rounded to the type (twice above four rows: once more where they are stored)."""
+    v = exact_gates(dtype, act)
+    n, k = v.size // 4, 4
+    gate = np.zeros((m, n))
+    gate[:4] = v[:4 * n].reshape(4, n)
+    x = np.zeros((m, k))
+    x[np.arange(4), np.arange(4)] = 1
+    (xb, xp, _), (sb_, sp, _) = strided(x, k, dtype), strided(gate, n, dtype)
+    (ub, up, _), (hb, hp, _) = (strided(np.ones((m, n)), n, dtype) for _ in range(2))
+    dg, du = empty(n, k, dtype, 0), empty(n, k, dtype, 0)
+    sb, need = scratch_for(gb.gbmm_gated_backward_scratch_bytes, dtype, m, n, k)
+    gb.check(gb.gbmm_gated_backward(dtype, CODE[act], m, n, k, xp, k, None, None, k, sp, up, n, hp, n, None, k, dg[1],
+                                    du[1], k, sb.ptr, need))
+    g = gate[:4]
+    bound = activation_bound(act, g)
+    if act == "gelu":
+        share, far, lever = 0.5 * ffn_ref.erfc(-g / 2 ** 0.5), g * np.exp(-0.5 * g * g) / (2 * np.pi) ** 0.5, g
+    elif act == "relu":
+        share, far, lever = (g > 0).astype(float), 0 * g, g
+    else:
+        a = g if act == "silu" else 2 * ffn_ref.C * (g + 0.044715 * g ** 3)
+        share = ffn_ref._sigmoid(a)
+        lever = g if act == "silu" else 2 * ffn_ref.C * (g + 3 * 0.044715 * g ** 3)
+        far = share * ffn_ref._sigmoid(-a) * lever
+    for out, want, size in ((dg, share + far, np.abs(share) + np.abs(far)), (du, g * share, np.abs(g * share))):
+        # 1 - sigmoid is off by a step of the sigmoid, times what it is multiplied with in the slope
+        tol = 2 * UO[dtype] * np.abs(want) + bound * size + 4 * U * np.abs(lever) * share + 2 * TINY[dtype]
+        near(fetch(out[0], n, k, k, dtype, 0).T, want, tol, "slope")
