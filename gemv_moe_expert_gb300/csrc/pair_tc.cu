@@ -44,6 +44,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOutBytes = 4096;  // of each epilogue warp
 constexpr uint32_t kSmemBytes = kStages * kStageBytes + kEpiWarps * kOutBytes + 256 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
+constexpr uint64_t kBlockLimitNs = 4000;  // what a k-block may add to a wait for all of a unit's
 constexpr int kExactBlocks = 1024 / kBK;  // k-blocks whose sum of products of two codes stays within 2^24
 
 enum Mode { kGated, kGrads, kCodes };
@@ -447,7 +448,9 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
             for (int c0 = 0; c0 < kblocks; c0 += chunk) {
                 const int a = local++ & 1;
                 int ready = 0;
-                if (lane == 0) ready = mbar_wait_bounded_cluster(tfull_bar(a), tphase[a], lim, abort_flag);
+                // a whole chain of k-blocks (0.33 us each) lies between two arrivals: more than `lim` where m is 2^28
+                const uint64_t chain = static_cast<uint64_t>(min(chunk, kblocks - c0)) * kBlockLimitNs;
+                if (lane == 0) ready = mbar_wait_bounded_cluster(tfull_bar(a), tphase[a], lim + chain, abort_flag);
                 ready = __shfl_sync(0xffffffffu, ready, 0);
                 if (!ready) {
                     if (lane == 0) raise_abort();

@@ -638,3 +638,22 @@ def test_far_ends_of_slopes(m, dtype, act):
         # 1 - sigmoid is off by a step of the sigmoid, times what it is multiplied with in the slope
         tol = 2 * UO[dtype] * np.abs(want) + bound * size + 4 * U * np.abs(lever) * share + 2 * TINY[dtype]
         near(fetch(out[0], n, k, k, dtype, 0).T, want, tol, "slope")
+
+
+def test_weights_gradients_of_268_million_tokens():
+    """One tile whose contraction takes longer than any single wait may: every 2^20th row and the last hold ones, which
+    the gradients count."""
+    m, n = 1 << 28, 8
+    rows = torch.zeros(m, n, dtype=torch.float16, device="cuda")
+    rows[7::1 << 20] = 1
+    rows[-1] = 1
+    st, need = gb.gbmm_gated_backward_scratch_bytes("f16", m, n, n, True)
+    gb.check(st)
+    scratch = torch.empty(need, dtype=torch.uint8, device="cuda")
+    d_w = torch.empty(2, n, n, dtype=torch.float16, device="cuda")
+    gb.check(gb.gbmm_gated_backward("f16", gb.GATE_RELU, m, n, n, rows, n, None, None, n, rows, rows, n, rows, n, None, n,
+                                    d_w[0], d_w[1], n, scratch, need))
+    assert gb.gbmm_device_error()[0] == gb.GBMM_OK
+    assert (d_w == m // (1 << 20) + 1).all()
+    del rows, scratch
+    torch.cuda.empty_cache()
