@@ -39,9 +39,7 @@ Operand matrix(const char *label, const void *p, uint64_t bytes, int64_t cols, i
     return {label, p, bytes, size, output, static_cast<uint64_t>(cols) * size, static_cast<uint64_t>(ld) * size};
 }
 
-bool rows16(const void *p, int64_t ld_bytes) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld_bytes % 16 == 0;
-}
+bool rows16(const void *p, int64_t ld_bytes) { return rows_on(p, ld_bytes, 16); }
 // Few rows run as dot products, a warp for each column or two; more run as tiles.
 constexpr int64_t kDotRows = 8;
 

@@ -184,9 +184,6 @@ __global__ void __launch_bounds__(32 * kDotWarps) gated_rowdot_kernel(const Gate
     }
 }
 
-bool rows_on(const void *p, int64_t ld_bytes, int unit) {
-    return reinterpret_cast<uintptr_t>(p) % unit == 0 && ld_bytes % unit == 0;
-}
 bool rows16(const void *p, int64_t ld, size_t size) { return rows_on(p, ld * static_cast<int64_t>(size), 16); }
 
 template <typename T, int kM, int kBytes>
@@ -994,9 +991,8 @@ cudaError_t outer_few_v(const GatedGradParams &p, const OuterGemmParams &w, cuda
 }
 template <typename T>
 cudaError_t outer_few_t(const GatedGradParams &p, const OuterGemmParams &w, cudaStream_t s) {
-    auto rows16 = [](const void *ptr, int64_t ld) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % 8 == 0; };
-    return rows16(w.x, w.ldx) && rows16(w.c[0], w.ldc) && rows16(w.c[1], w.ldc) ? outer_few_v<T, true>(p, w, s)
-                                                                                 : outer_few_v<T, false>(p, w, s);
+    const bool vec = rows16(w.x, w.ldx, 2) && rows16(w.c[0], w.ldc, 2) && rows16(w.c[1], w.ldc, 2);
+    return vec ? outer_few_v<T, true>(p, w, s) : outer_few_v<T, false>(p, w, s);
 }
 
 // ---------------------------------------------------------------------------

@@ -11,10 +11,6 @@ template <typename T> struct Pair;
 template <> struct Pair<__half> { using type = __half2; };
 template <> struct Pair<__nv_bfloat16> { using type = __nv_bfloat162; };
 
-bool rows_on(const void *p, int64_t ld_bytes, int unit) {
-    return reinterpret_cast<uintptr_t>(p) % unit == 0 && ld_bytes % unit == 0;
-}
-
 // ---------------------------------------------------------------------------
 // quantisation: scale = max |x| * f32(1 / 127), code = the integer nearest to x / scale, ties to even
 //
@@ -37,8 +33,8 @@ __device__ __forceinline__ int nearest_code(float x, float s) {
     return static_cast<int>(fminf(fmaxf(n, -127.f), 127.f));
 }
 
-// What a row's scale gives: inv = 1 / scale; live: false where every code is 0 (scale 0 or NaN); exact: true where
-// 1 / scale is out of f32's normal range.
+// What a row's scale gives: inv = 1 / scale; live: false where every code is 0 (scale 0 or NaN); exact: true for scales
+// below 1e-30, far above the 3e-39 below which 1 / scale leaves f32's range: no inv there, every code is worked out exactly.
 struct RowScale {
     float s, inv;
     bool live, exact;
@@ -219,13 +215,12 @@ cudaError_t quantize_t(const QuantizeParams &p, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// the product for few rows: a warp takes kR columns j and kM rows i, its lanes divide k.  Bound by reading b: a lane
-// asks for kU units of each of its columns before it uses the first.  A unit is 16 or 4 bytes where all rows allow that;
+// the product for few rows: a warp takes a column j and kM rows i, its lanes divide k.  Bound by reading b: a lane
+// asks for kU units of its column before it uses the first.  A unit is 16 or 4 bytes where all rows allow that;
 // rows that start anywhere are read as the aligned words around each group of four, shifted into place.
 // ---------------------------------------------------------------------------
 
 constexpr int kDotWarps = 4;
-constexpr int kR = 1;
 
 // the four codes at row + 4 g; the row has k codes, and what lies past them counts as 0
 __device__ __forceinline__ uint32_t any4(const int8_t *row, int64_t g, int64_t k) {
@@ -279,29 +274,23 @@ __global__ void __launch_bounds__(32 * kDotWarps) gemm_i8_dot_kernel(const GemmI
     constexpr int kStep = kUnit == 16 ? 16 : 4;  // codes in a unit
     grid_dep_begin();
     const int lane = threadIdx.x & 31, share = kShare > 1 ? threadIdx.x >> 5 : 0;
-    const int64_t j0 = kShare > 1 ? static_cast<int64_t>(blockIdx.x) * kR
-                                  : (static_cast<int64_t>(blockIdx.x) * kDotWarps + (threadIdx.x >> 5)) * kR;
-    if (j0 >= p.n) return;
-    const int8_t *b[kR];
-#pragma unroll
-    for (int c = 0; c < kR; ++c) b[c] = p.b + min(j0 + c, p.n - 1) * p.ldb;
+    const int64_t j = kShare > 1 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kDotWarps + (threadIdx.x >> 5);
+    if (j >= p.n) return;
+    const int8_t *b = p.b + j * p.ldb;
     // units that are whole; rows that start anywhere have one more, whose missing codes are 0
     const int64_t units = kUnit == 1 ? (p.k + 3) / 4 : p.k / kStep;
     for (int64_t i0 = static_cast<int64_t>(blockIdx.y) * kM; i0 < p.m; i0 += static_cast<int64_t>(gridDim.y) * kM) {
         const int8_t *a = p.a + i0 * p.lda;
         const int rows = static_cast<int>(p.m - i0 < kM ? p.m - i0 : kM);
-        int acc[kM][kR];
+        int acc[kM];
 #pragma unroll
-        for (int r = 0; r < kM; ++r)
-#pragma unroll
-            for (int c = 0; c < kR; ++c) acc[r][c] = 0;
+        for (int r = 0; r < kM; ++r) acc[r] = 0;
         for (int64_t at = 32 * share + lane; at < units; at += kU * kLanes) {
-            Codes<kUnit> w[kU][kR];
+            Codes<kUnit> w[kU];
 #pragma unroll
             for (int q = 0; q < kU; ++q) {
                 if (at + q * kLanes >= units) break;
-#pragma unroll
-                for (int c = 0; c < kR; ++c) w[q][c] = Codes<kUnit>::stream(b[c], at + q * kLanes, p.k);
+                w[q] = Codes<kUnit>::stream(b, at + q * kLanes, p.k);
             }
 #pragma unroll
             for (int q = 0; q < kU; ++q) {
@@ -309,9 +298,7 @@ __global__ void __launch_bounds__(32 * kDotWarps) gemm_i8_dot_kernel(const GemmI
 #pragma unroll
                 for (int r = 0; r < kM; ++r) {
                     if (r >= rows) break;
-                    const Codes<kUnit> v = Codes<kUnit>::cached(a + r * p.lda, at + q * kLanes, p.k);
-#pragma unroll
-                    for (int c = 0; c < kR; ++c) acc[r][c] = w[q][c].dot(v, acc[r][c]);
+                    acc[r] = w[q].dot(Codes<kUnit>::cached(a + r * p.lda, at + q * kLanes, p.k), acc[r]);
                 }
             }
         }
@@ -320,43 +307,32 @@ __global__ void __launch_bounds__(32 * kDotWarps) gemm_i8_dot_kernel(const GemmI
 #pragma unroll
             for (int r = 0; r < kM; ++r) {
                 if (r >= rows) break;
-                const int v = a[r * p.lda + e];
-#pragma unroll
-                for (int c = 0; c < kR; ++c) acc[r][c] += v * static_cast<int>(b[c][e]);
+                acc[r] += static_cast<int>(a[r * p.lda + e]) * static_cast<int>(b[e]);
             }
         }
 #pragma unroll
-        for (int r = 0; r < kM; ++r)
-#pragma unroll
-            for (int c = 0; c < kR; ++c) acc[r][c] = __reduce_add_sync(0xffffffffu, acc[r][c]);
+        for (int r = 0; r < kM; ++r) acc[r] = __reduce_add_sync(0xffffffffu, acc[r]);
         if constexpr (kShare > 1) {
-            __shared__ int part[kShare][kM][kR];
+            __shared__ int part[kShare][kM];
             __syncthreads();  // what an earlier turn left has been read
             if (lane == 0) {
 #pragma unroll
-                for (int r = 0; r < kM; ++r)
-#pragma unroll
-                    for (int c = 0; c < kR; ++c) part[share][r][c] = acc[r][c];
+                for (int r = 0; r < kM; ++r) part[share][r] = acc[r];
             }
             __syncthreads();
             if (share != 0) continue;
 #pragma unroll
             for (int q = 1; q < kShare; ++q)
 #pragma unroll
-                for (int r = 0; r < kM; ++r)
-#pragma unroll
-                    for (int c = 0; c < kR; ++c) acc[r][c] += part[q][r][c];
+                for (int r = 0; r < kM; ++r) acc[r] += part[q][r];
         }
 #pragma unroll
-        for (int r = 0; r < kM; ++r)
-#pragma unroll
-            for (int c = 0; c < kR; ++c) {
-                if (lane != r * kR + c || r >= rows || j0 + c >= p.n) continue;
-                const float sa = p.scale_a != nullptr ? p.scale_a[i0 + r] : 1.f;
-                const float sb = p.scale_b != nullptr ? p.scale_b[j0 + c] : 1.f;
-                static_cast<T *>(p.c)[(i0 + r) * p.ldc + j0 + c] =
-                    Elem<T>::from_f(static_cast<float>(acc[r][c]) * sa * sb);
-            }
+        for (int r = 0; r < kM; ++r) {
+            if (lane != r || r >= rows) continue;
+            const float sa = p.scale_a != nullptr ? p.scale_a[i0 + r] : 1.f;
+            const float sb = p.scale_b != nullptr ? p.scale_b[j] : 1.f;
+            static_cast<T *>(p.c)[(i0 + r) * p.ldc + j] = Elem<T>::from_f(static_cast<float>(acc[r]) * sa * sb);
+        }
     }
 }
 
@@ -365,12 +341,12 @@ cudaError_t dot_unit(const GemmI8Params &p, cudaStream_t s) {
     const int64_t down = (p.m + kM - 1) / kM;
     const dim3 block(32 * kDotWarps);
     const unsigned y = static_cast<unsigned>(down < 65535 ? down : 65535);
-    const int64_t whole = (p.n + kR - 1) / kR, apart = (whole + kDotWarps - 1) / kDotWarps;
+    const int64_t apart = (p.n + kDotWarps - 1) / kDotWarps;
     // A block's four warps share a column once each lane has four units of it (or of several rows' sums) to add up:
     // 4096 columns of 11008 codes 9.2 against 10.2 us, 11008 of 4096 11.7 against 9.1.
     const int64_t units = p.k / (kUnit == 16 ? 16 : 4);
     if (units >= 16 * 32 || (p.m > 1 && units >= 4 * 32))
-        return launch_early(gemm_i8_dot_kernel<T, kM, kUnit, kDotWarps>, dim3(static_cast<unsigned>(whole), y), block, 0, s, p);
+        return launch_early(gemm_i8_dot_kernel<T, kM, kUnit, kDotWarps>, dim3(static_cast<unsigned>(p.n), y), block, 0, s, p);
     return launch_early(gemm_i8_dot_kernel<T, kM, kUnit, 1>, dim3(static_cast<unsigned>(apart), y), block, 0, s, p);
 }
 

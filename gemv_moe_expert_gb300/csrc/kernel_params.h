@@ -15,6 +15,11 @@ enum DType : int { kF32 = 0, kF16 = 1, kBF16 = 2 };
 
 inline int dtype_size(int dt) { return dt == kF32 ? 4 : 2; }
 
+// whether rows ld_bytes apart all start on multiples of `unit` bytes
+inline bool rows_on(const void *p, int64_t ld_bytes, int unit) {
+    return reinterpret_cast<uintptr_t>(p) % unit == 0 && ld_bytes % unit == 0;
+}
+
 // device error word bits
 constexpr uint32_t kErrWaitTimeout = 1u;
 
@@ -240,7 +245,7 @@ struct PairTcParams {
     int32_t m, n, k;                 // k: of one source
     int32_t c_tma, saved_tma;        // the output's maps may be used (its rows start on multiples of 16 bytes)
     int32_t act;
-    int32_t tiles_m, tiles_n, num_tiles;  // set by the launcher
+    int32_t tiles_m, tiles_n;  // set by the launcher
     uint32_t *err;
     uint64_t wait_limit_ns;
     // gradients: c [m, n] over both sources of k, and dw[i] [k, n] over m; either may be left out

@@ -448,7 +448,7 @@ pair_tc_kernel(const __grid_constant__ PairTcMaps maps, const PairTcParams p) {
             for (int c0 = 0; c0 < kblocks; c0 += chunk) {
                 const int a = local++ & 1;
                 int ready = 0;
-                // a whole chain of k-blocks (0.33 us each) lies between two arrivals: more than `lim` where m is 2^28
+                // a whole chain of k-blocks (0.28 us each) lies between two arrivals: more than `lim` where m is 2^28
                 const uint64_t chain = static_cast<uint64_t>(min(chunk, kblocks - c0)) * kBlockLimitNs;
                 if (lane == 0) ready = mbar_wait_bounded_cluster(tfull_bar(a), tphase[a], lim + chain, abort_flag);
                 ready = __shfl_sync(0xffffffffu, ready, 0);
