@@ -802,7 +802,9 @@ struct GatedPlan {
         TileArgs t{};
         const unsigned large = tile_grid(m, n, 128, 64, &t), small = tile_grid(m, n, 64, 64, &t);
         const int64_t steps = (k + kTK - 1) / kTK;
-        const GatedGrid by_large = gated_grid(large, steps, 1394, 4, sms), by_small = gated_grid(small, steps, 819, 2, sms);
+        // two products of 128 x 64 or 64 x 64 outputs, like the weights' gradients
+        const GatedGrid by_large = gated_grid(large, steps, kLargeSteps.w, 4, sms);
+        const GatedGrid by_small = gated_grid(small, steps, kSmallSteps.w, 2, sms);
         if (by_large.time < 0) return;
         high = by_small.time < 0 || by_large.time <= by_small.time;
         parts = high ? by_large.parts : by_small.parts;
